@@ -1,7 +1,7 @@
 /*
  * mtp.h -- C ABI of the GB300 MTP speculative-decoding hot path.
  *
- * Five operations, all asynchronous on a caller-supplied CUDA stream:
+ * Eight operations, all asynchronous on a caller-supplied CUDA stream:
  *
  *   mtp_draft_block    N chained draft steps of an MTP assistant head that
  *                      cross-attends into the target's KV cache, in ONE
@@ -15,6 +15,13 @@
  *   mtp_nextn_draft    the dense NextN self-speculation drafter: its own
  *                      block and its own KV, the catch-up on the accepted
  *                      rows, then N chained draft steps, in ONE launch.
+ *   mtp_kv_append      the target's new key and value rows into its paged KV
+ *                      cache (fp32, bf16, or e4m3 with a scale per page and
+ *                      KV head), key norm and RoPE on the way.
+ *   mtp_paged_attention  the target's 1..64 new rows per sequence (a verify
+ *                      step, or plain decoding) attend that cache.
+ *   mtp_token_logprobs log probability, entropy and top alternatives of given
+ *                      tokens from rows of logits.
  *
  * Definitions are those of the pages this library implements:
  *   [G4] "Gemma 4 MTP -- Multi-Token Prediction speculative decoding":
@@ -68,7 +75,8 @@ enum {
     MTP_ERR_CAPACITY = -6      /* (device status) a sampling candidate set overflowed */
 };
 
-enum { MTP_DTYPE_F32 = 0, MTP_DTYPE_BF16 = 1 };
+enum { MTP_DTYPE_F32 = 0, MTP_DTYPE_BF16 = 1,
+       MTP_DTYPE_E4M3 = 2 };       /* only as mtp_kv_cache.kv_dtype */
 /* projection weight formats (mtp_config.wquant) */
 enum { MTP_WQ_NONE = 0, MTP_WQ_Q8_0 = 1, MTP_WQ_Q4_0 = 2 };
 
@@ -78,6 +86,11 @@ enum { MTP_WQ_NONE = 0, MTP_WQ_Q8_0 = 1, MTP_WQ_Q4_0 = 2 };
 #define MTP_MAX_VERIFY_BATCH 65536  /* sequences of one verify or draw call */
 #define MTP_MAX_CENTROIDS 8192      /* centroids of a centroid-routed LM head */
 #define MTP_MAX_CATCHUP 16          /* catch-up rows per sequence of one mtp_nextn_draft call */
+#define MTP_MAX_PAGED_BATCH 1024    /* sequences of one mtp_kv_append or mtp_paged_attention call */
+#define MTP_MAX_APPEND_ROWS 65536   /* rows per sequence of one mtp_kv_append call */
+#define MTP_MAX_ATTN_ROWS 64        /* rows per sequence of one mtp_paged_attention call */
+#define MTP_MAX_PAGE_SIZE 256       /* slots of a page */
+#define MTP_MAX_TOP 32              /* alternatives per row of mtp_token_logprobs */
 
 /* Sizes and scalars of the assistant head ([G4] sec. 3-4).
  *   d_t        backbone (target) width: token embedding, h_prev, LM head input
@@ -188,6 +201,40 @@ typedef struct mtp_sample_params {
     float temp, top_p, min_p, rep_penalty, presence_penalty;
     int32_t top_k;
 } mtp_sample_params;
+
+/* The paged KV cache of one target layer.  Position t of sequence b lives in
+ * slot t % page_size of page page_table[b * max_pages + t / page_size]; element
+ * (page, kv head g, slot s, d) of k and of v at page*stride_p + g*stride_h +
+ * s*stride_t + d (elements of kv_dtype, d contiguous).  Consecutive pages of
+ * one sequence with stride_p == page_size * stride_t are a mtp_kv_view of the
+ * same memory (window 0), which the drafters read.
+ *   kv_dtype   MTP_DTYPE_F32, MTP_DTYPE_BF16, or MTP_DTYPE_E4M3: 8-bit codes,
+ *              the value is code * k_scale[page * n_kv_heads + g] (v_scale
+ *              for v), fp32 [n_pages, n_kv_heads], powers of two within
+ *              [2^-40, 2^40] (what mtp_kv_append writes)
+ *   head_dim   32, 64, 128, 256 or 512 (strides: multiples of 16 bytes, k and
+ *              v 16-byte aligned)
+ *   page_size  16, 32, 64, 128 or 256
+ *   window, sink  window W > 0: a row at position p attends the last W
+ *              positions (p - W, p] and the attention sink, positions
+ *              [0, min(sink, p + 1 - W)), as in mtp_kv_view; window 0 (sink 0)
+ *              attends [0, p].  Pages outside what is attended are not read
+ *              and may be absent.
+ *   rope_theta > 0: RoPE base, NeoX pairs (i, i + head_dim/2), of the keys on
+ *              their way in and of the queries; 0: neither is rotated
+ * An entry of page_table is a page in [0, n_pages); any other value means
+ * that the page is absent. */
+typedef struct mtp_kv_cache {
+    void *k, *v;
+    float *k_scale, *v_scale;      /* MTP_DTYPE_E4M3 only (NULL otherwise) */
+    const int32_t *page_table;     /* [B, max_pages] */
+    int64_t stride_p, stride_h, stride_t;
+    int32_t n_pages, page_size, max_pages;
+    int32_t n_kv_heads, head_dim, kv_dtype;
+    int32_t window, sink;
+    float rope_theta;
+    int32_t pad_;
+} mtp_kv_cache;
 
 /* Q8_0 quantisation of a row-major fp32 matrix [rows, cols] on the host
  * ("opus-mtp-turbo: Track 1 report", item 3, ggml's Q8_0 rule): per block of
@@ -379,6 +426,86 @@ int mtp_sample_drafts(const void *dft_logits, int ldtype, int B, int N, int V,
                       const int32_t *hist, int H, const mtp_sample_params *sp,
                       uint64_t seed, uint64_t offset, int32_t *out_drafts,
                       void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/* Workspace bytes of mtp_kv_append and mtp_paged_attention on this cache for at
+ * most B sequences of at most M rows each (beyond MTP_MAX_ATTN_ROWS only
+ * appended) and n_q_heads query heads.  Returns 0 for invalid sizes. */
+size_t mtp_kv_workspace_size(const mtp_kv_cache *c, int B, int M, int n_q_heads);
+
+/* Append rows to the cache: row j < n_new[b] of sequence b goes to position
+ * kv_len[b] + j as key = rope(rmsnorm(k_j; k_norm)), value = v_j (per KV head;
+ * the norm only where k_norm is given, the rotation where rope_theta > 0), each
+ * rounded once to kv_dtype, nearest even.
+ *   k, v       rows in in_dtype (F32 or BF16): row (b, j, kv head g) at
+ *              b*in_stride_b + j*in_stride_m + g*in_stride_h (elements; 16-byte
+ *              multiples, 16-byte aligned), head_dim contiguous -- slices of a
+ *              fused projection's output, for example
+ *   kv_len [B] int32 >= 0: positions already cached;  n_new [B] int32 in
+ *              [0, M] (NULL: all M);  kv_len + n_new <= max_pages * page_size
+ *   k_norm     fp32 [head_dim] or NULL;  rms_eps its epsilon
+ * MTP_DTYPE_E4M3: the scale of a (page, KV head) is the smallest power of two s
+ * with max |x| <= 448 s over this call's finite values in it, at least 2^-40
+ * and at most 2^40 (larger values saturate), and at least the scale it has if
+ * the page already holds positions of the sequence (slot kv_len % page_size >
+ * 0): its older codes are then re-rounded to the larger scale.  A page whose
+ * first slot is written starts anew.  NaN and infinities are stored as NaN.
+ * Slots behind the last row keep their bytes.  The pages that one call writes
+ * must be distinct between sequences.
+ * A sequence whose kv_len or n_new is out of range is left out, rows whose
+ * page is absent are dropped, and both set the status word to MTP_ERR_ARG.
+ * 1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= M <= MTP_MAX_APPEND_ROWS.  One launch. */
+int mtp_kv_append(const mtp_kv_cache *c, int B, int M, const int32_t *kv_len, const int32_t *n_new,
+                  const void *k, const void *v, int in_dtype,
+                  int64_t in_stride_b, int64_t in_stride_m, int64_t in_stride_h,
+                  const float *k_norm, float rms_eps, void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/* Attention of the appended rows over the cache: row j < n_new[b] of sequence
+ * b, at position p = kv_len[b] + j, query head h (KV head h / (n_q_heads /
+ * n_kv_heads)):
+ *   q' = rope(rmsnorm(q; q_norm), p)   (norm and rotation as for the keys)
+ *   out = sum_t softmax_t(attn_scale q' . k_t) v_t  over the positions t that
+ *         p attends (see mtp_kv_cache); kv_len is the length BEFORE the rows,
+ *         whose keys and values are in the cache already (mtp_kv_append)
+ *   q          rows in dtype (F32 or BF16): row (b, j, head h) at b*q_stride_b
+ *              + j*q_stride_m + h*q_stride_h (elements; 16-byte multiples,
+ *              16-byte aligned)
+ *   q_norm     fp32 [head_dim] or NULL;  rms_eps its epsilon
+ *   attn_scale 0 = the default 1/sqrt(head_dim)
+ *   out [B, M, n_q_heads, head_dim] in dtype; rows j >= n_new[b] keep their
+ *              bytes
+ * fp32 queries are computed in fp32 throughout.  bf16 queries against a bf16
+ * or e4m3 cache with head_dim 64, 128, 256 or 512 run on the tensor cores: the
+ * probabilities are then rounded to bf16 precision (sums and maxima fp32).
+ * Slots that hold no attended position are never used, whatever they contain.
+ * A row that attends nothing (all its pages absent) gives zeros.  A sequence
+ * whose kv_len or n_new is out of range is left out, positions on absent pages
+ * are masked, and both set the status word to MTP_ERR_ARG.
+ * 1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= M <= MTP_MAX_ATTN_ROWS, at most 16
+ * query heads per KV head.  Two launches. */
+int mtp_paged_attention(const mtp_kv_cache *c, int B, int M, int n_q_heads, const int32_t *kv_len,
+                        const int32_t *n_new, const void *q, int dtype,
+                        int64_t q_stride_b, int64_t q_stride_m, int64_t q_stride_h,
+                        const float *q_norm, float rms_eps, float attn_scale, void *out,
+                        void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/* Log probabilities of given tokens: for row r of logits [rows, V] in ldtype
+ * (rows row_stride elements apart), with lse = log sum_v exp z_v,
+ *   out_logprob[r]  = z_t - lse, t = tokens[r]
+ *   out_entropy[r]  = -sum_v p_v log p_v (natural), p = exp(z - lse)
+ *   out_top_ids / out_top_logprobs [rows, top_k]: the largest logits with
+ *                     their z - lse, by value descending, lowest index first
+ *                     on ties; -1 and -inf behind the last one
+ * NaN logits are left out as if they were -inf; -inf is never an alternative.
+ * A row with a +inf logit, or with nothing above -inf, gives NaN log
+ * probabilities and entropy.  A row whose token is outside
+ * [0, V) (the -1 padding of a verify's out_tokens) is not read and its
+ * outputs keep their values; tokens NULL: every row, out_logprob not written.
+ * Each output may be NULL (top_k 0: both alternatives' arrays unused).
+ * 1 <= rows <= 17 * MTP_MAX_VERIFY_BATCH, 0 <= top_k <= MTP_MAX_TOP, V >= 1,
+ * row_stride >= V.  One launch, no workspace. */
+int mtp_token_logprobs(const void *logits, int ldtype, int64_t rows, int V, int64_t row_stride,
+                       const int32_t *tokens, int top_k, float *out_logprob, float *out_entropy,
+                       int32_t *out_top_ids, float *out_top_logprobs, mtp_stream_t stream);
 
 /* Greedy verify without a workspace.  The pages have no counterpart of this
  * call; it exists for callers that may not allocate device memory at all --

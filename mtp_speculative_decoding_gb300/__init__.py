@@ -24,6 +24,7 @@ MTP_ERR_TIMEOUT = -5
 MTP_ERR_CAPACITY = -6
 MTP_DTYPE_F32 = 0
 MTP_DTYPE_BF16 = 1
+MTP_DTYPE_E4M3 = 2
 MTP_WQ_NONE = 0
 MTP_WQ_Q8_0 = 1
 MTP_WQ_Q4_0 = 2
@@ -32,11 +33,17 @@ MTP_MAX_VIEWS = 4
 MTP_MAX_BATCH = 64
 MTP_MAX_VERIFY_BATCH = 65536
 MTP_MAX_CATCHUP = 16
+MTP_MAX_PAGED_BATCH = 1024
+MTP_MAX_APPEND_ROWS = 65536
+MTP_MAX_ATTN_ROWS = 64
+MTP_MAX_PAGE_SIZE = 256
+MTP_MAX_TOP = 32
 
 # every entry point include/mtp.h declares
 EXPORTS = ("mtp_workspace_size", "mtp_draft_block", "mtp_verify_greedy", "mtp_verify_sample",
            "mtp_sample_drafts", "mtp_quantize_q8_0", "mtp_last_error", "mtp_strerror", "mtp_debug_barrier_timeout",
-           "mtp_verify_greedy_noalloc", "mtp_nextn_draft", "mtp_quantize_q4_0")
+           "mtp_verify_greedy_noalloc", "mtp_nextn_draft", "mtp_quantize_q4_0",
+           "mtp_kv_workspace_size", "mtp_kv_append", "mtp_paged_attention", "mtp_token_logprobs")
 
 
 class MTPError(RuntimeError):
@@ -73,6 +80,14 @@ class KVView(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("stride_b", C.c_int64), ("stride_h", C.c_int64),
                 ("stride_t", C.c_int64), ("cap", C.c_int32), ("window", C.c_int32), ("rope_theta", C.c_float),
                 ("sink", C.c_int32)]
+
+
+class KVCache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("page_table", C.c_void_p), ("stride_p", C.c_int64), ("stride_h", C.c_int64), ("stride_t", C.c_int64),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("max_pages", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("kv_dtype", C.c_int32),
+                ("window", C.c_int32), ("sink", C.c_int32), ("rope_theta", C.c_float), ("pad_", C.c_int32)]
 
 
 class SampleParams(C.Structure):
@@ -119,6 +134,15 @@ def lib():
             L.mtp_quantize_q4_0.argtypes = [P, C.c_int64, C.c_int64, P, P]
             L.mtp_quantize_q4_0.restype = I
             L.mtp_quantize_q8_0.restype = I
+            L64, F = C.c_int64, C.c_float
+            L.mtp_kv_workspace_size.argtypes = [P, I, I, I]
+            L.mtp_kv_workspace_size.restype = Z
+            L.mtp_kv_append.argtypes = [P, I, I, P, P, P, P, I, L64, L64, L64, P, F, P, Z, P]
+            L.mtp_kv_append.restype = I
+            L.mtp_paged_attention.argtypes = [P, I, I, I, P, P, P, I, L64, L64, L64, P, F, F, P, P, Z, P]
+            L.mtp_paged_attention.restype = I
+            L.mtp_token_logprobs.argtypes = [P, I, L64, I, L64, P, I, P, P, P, P, P]
+            L.mtp_token_logprobs.restype = I
             _lib = L
     return _lib
 
@@ -384,6 +408,144 @@ def sample_drafts(dft_logits, hist, params, seed: int, offset: int, out_drafts, 
     rc = lib().mtp_sample_drafts(_ptr(dft_logits), _dtype_code(dft_logits), B, N, V, _ptr(hist), H, C.byref(sp),
                                  seed, offset, _ptr(out_drafts), _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "mtp_sample_drafts")
+
+
+# ----------------------------------------------------------------------------
+# the target's paged KV cache and its rows; log probabilities
+# ----------------------------------------------------------------------------
+
+def make_kv_cache(k, v, page_table, k_scale=None, v_scale=None, window: int = 0, sink: int = 0,
+                  rope_theta: float = 0.0) -> KVCache:
+    """k, v: [n_pages, n_kv_heads, page_size, head_dim] device tensors of one
+    layout (any strides, head_dim contiguous: a pool stored as [n_pages,
+    page_size, n_kv_heads, head_dim] is passed as its permuted view) in fp32,
+    bf16 or float8_e4m3fn; page_table [B, max_pages] int32; k_scale, v_scale
+    [n_pages, n_kv_heads] fp32 for an e4m3 cache.  rope_theta 0: keys and
+    queries are not rotated (see mtp_kv_cache)."""
+    import torch
+    _require_current(k, v, page_table, k_scale, v_scale)
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(-1) != 1:
+        raise ValueError("k and v: two [n_pages, n_kv_heads, page_size, head_dim] tensors of one dtype and layout, head_dim contiguous")
+    if k.dtype == torch.float8_e4m3fn:
+        dt = MTP_DTYPE_E4M3
+        for s in (k_scale, v_scale):
+            if s is None or s.dtype != torch.float32 or s.shape != k.shape[:2] or not s.is_contiguous():
+                raise ValueError("an e4m3 cache needs contiguous fp32 k_scale and v_scale [n_pages, n_kv_heads]")
+    else:
+        dt = _dtype_code(k)
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales are for an e4m3 cache only")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+        raise ValueError("page_table: contiguous int32 [B, max_pages]")
+    sp, sh, st, _ = k.stride()
+    n, hkv, ps, hd = k.shape
+    cache = KVCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+                    v_scale.data_ptr() if v_scale is not None else None, page_table.data_ptr(), sp, sh, st, n, ps,
+                    page_table.shape[1], hkv, hd, dt, window, sink, rope_theta, 0)
+    cache.table_rows = page_table.shape[0]   # for the calls' check of their batch
+    return cache
+
+
+def kv_workspace_size(cache: KVCache, B: int, M: int, n_q_heads: int) -> int:
+    """Workspace bytes of kv_append and paged_attention for B sequences of at most M rows."""
+    n = lib().mtp_kv_workspace_size(C.byref(cache), B, M, n_q_heads)
+    if n == 0:
+        raise MTPError(MTP_ERR_ARG, "mtp_kv_workspace_size")
+    return int(n)
+
+
+def _require_current(*tensors):
+    """The calls launch on the current device: tensors of another one are refused."""
+    import torch
+    _require_cuda(*tensors)
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor lives on {t.device}, the current device is cuda:{dev}")
+
+
+def _require_lengths(cache, B, *tensors):
+    import torch
+    if B > getattr(cache, "table_rows", B):
+        raise ValueError("more sequences than page_table has rows")
+    for t in tensors:
+        if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous()):
+            raise ValueError("kv_len and n_new: contiguous int32 [B]")
+
+
+def _require_gain(hd, gain):
+    import torch
+    if gain is not None and (gain.dtype != torch.float32 or gain.shape != (hd,) or not gain.is_contiguous()):
+        raise ValueError("the norm's gain: contiguous fp32 [head_dim]")
+
+
+def kv_append(cache: KVCache, k_new, v_new, kv_len, ws, n_new=None, k_norm=None, rms_eps: float = 1e-6,
+              stream=None) -> None:
+    """Launch mtp_kv_append on the current stream: rows k_new, v_new [B, M,
+    n_kv_heads, head_dim] (fp32 or bf16, one layout, head_dim contiguous) to
+    positions kv_len[b] + j, j < n_new[b] (all M without n_new)."""
+    _require_current(k_new, v_new, kv_len, ws, n_new, k_norm)
+    B, M, hkv, hd = k_new.shape
+    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype or v_new.stride() != k_new.stride() or k_new.stride(3) != 1:
+        raise ValueError("k_new and v_new: two [B, M, n_kv_heads, head_dim] tensors of one dtype and layout, head_dim contiguous")
+    if hkv != cache.n_kv_heads or hd != cache.head_dim:
+        raise ValueError("the rows' heads are not the cache's")
+    _require_lengths(cache, B, kv_len, n_new)
+    _require_gain(hd, k_norm)
+    sb, sm, sh, _ = k_new.stride()
+    rc = lib().mtp_kv_append(C.byref(cache), B, M, _ptr(kv_len), _ptr(n_new), _ptr(k_new), _ptr(v_new),
+                             _dtype_code(k_new), sb, sm, sh, _ptr(k_norm), rms_eps, _ptr(ws), ws.numel(), _stream(stream))
+    _check(rc, "mtp_kv_append")
+
+
+def paged_attention(cache: KVCache, q, kv_len, out, ws, n_new=None, q_norm=None, rms_eps: float = 1e-6,
+                    attn_scale: float | None = None, stream=None) -> None:
+    """Launch mtp_paged_attention on the current stream: rows q [B, M,
+    n_q_heads, head_dim] (fp32 or bf16, head_dim contiguous) at positions
+    kv_len[b] + j attend the cache, which holds their keys and values already;
+    out [B, M, n_q_heads, head_dim] contiguous in q's dtype."""
+    _require_current(q, kv_len, out, ws, n_new, q_norm)
+    B, M, hq, hd = q.shape
+    if hd != cache.head_dim or q.stride(3) != 1:
+        raise ValueError("q: [B, M, n_q_heads, head_dim] with the cache's head_dim, contiguous")
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out: contiguous, of q's shape and dtype")
+    _require_lengths(cache, B, kv_len, n_new)
+    _require_gain(hd, q_norm)
+    sb, sm, sh, _ = q.stride()
+    rc = lib().mtp_paged_attention(C.byref(cache), B, M, hq, _ptr(kv_len), _ptr(n_new), _ptr(q), _dtype_code(q), sb, sm, sh,
+                                   _ptr(q_norm), rms_eps, 0.0 if attn_scale is None else attn_scale, _ptr(out), _ptr(ws),
+                                   ws.numel(), _stream(stream))
+    _check(rc, "mtp_paged_attention")
+
+
+def token_logprobs(logits, tokens, out_logprob, out_entropy=None, out_top_ids=None, out_top_logprobs=None,
+                   stream=None) -> None:
+    """Launch mtp_token_logprobs on the current stream.  logits [..., V] (fp32
+    or bf16, rows at one stride), tokens int32 with the rows' shape (a verify's
+    out_tokens: rows of token -1 are skipped) or None; out_logprob and
+    out_entropy fp32 with the rows' shape, out_top_ids int32 and
+    out_top_logprobs fp32 with the rows' shape and one more axis of top_k."""
+    import torch
+    _require_current(logits, tokens, out_logprob, out_entropy, out_top_ids, out_top_logprobs)
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    if logits.stride(-1) != 1 and V > 1:
+        raise ValueError("logits: the vocabulary axis must be contiguous")
+    z = logits if logits.dim() == 2 else logits.view(-1, V)   # raises where the rows have no single stride
+    rows = z.shape[0]
+    for t, dt in ((tokens, torch.int32), (out_logprob, torch.float32), (out_entropy, torch.float32)):
+        if t is not None and (t.dtype != dt or t.shape != lead or not t.is_contiguous()):
+            raise ValueError("tokens (int32), out_logprob and out_entropy (fp32): contiguous, of the rows' shape")
+    top = 0
+    for t, dt in ((out_top_ids, torch.int32), (out_top_logprobs, torch.float32)):
+        if t is not None:
+            if t.dtype != dt or t.shape[:-1] != lead or not t.is_contiguous() or (top and t.shape[-1] != top):
+                raise ValueError("out_top_ids (int32) and out_top_logprobs (fp32): contiguous, the rows' shape and top_k")
+            top = t.shape[-1]
+    rc = lib().mtp_token_logprobs(_ptr(z), _dtype_code(z), rows, V, z.stride(0) if rows > 1 else V, _ptr(tokens), top,
+                                  _ptr(out_logprob), _ptr(out_entropy), _ptr(out_top_ids), _ptr(out_top_logprobs),
+                                  _stream(stream))
+    _check(rc, "mtp_token_logprobs")
 
 
 def last_error(ws, stream=None) -> int:

@@ -21,7 +21,8 @@ LIB = os.path.join(BUILD, "libmtp.so")
 # (object name, source, extra defines): the draft kernel's variants are one
 # source compiled once per (weight type, head dimension, tensor-core paths)
 UNITS = [("api", "api.cu", []), ("verify", "verify.cu", []), ("noalloc", "noalloc.cu", []),
-         ("draft_dispatch", "draft_dispatch.cu", [])]
+         ("draft_dispatch", "draft_dispatch.cu", []), ("paged_api", "paged_api.cu", []),
+         ("kv_append", "kv_append.cu", []), ("paged_attn", "paged_attn.cu", []), ("logprobs", "logprobs.cu", [])]
 for _hd in (32, 64, 128, 256, 512):
     for _name, _bf, _tc in (("f32", 0, 0), ("bf16_cc", 1, 0), ("bf16_tc", 1, 1)):
         UNITS.append((f"draft_{_name}_{_hd}", "draft_inst.cu",

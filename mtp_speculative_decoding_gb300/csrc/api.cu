@@ -14,18 +14,13 @@
 
 #include "common.cuh"
 #include "draft.cuh"
+#include "host.cuh"
 #include "mtp.h"
 #include "verify.cuh"
 
 using namespace mtp;
 
-namespace {
-
-constexpr unsigned long long kBarrierLimitNs = 1000000000ull;  // 1 s per barrier wait
-
-size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+namespace mtp {
 
 int num_sms() {
     int dev = 0;
@@ -37,6 +32,31 @@ int num_sms() {
     if (dev >= 0 && dev < 64) cache[dev] = n;
     return n;
 }
+
+// cuTensorMapEncodeTiled from the driver, resolved once
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+}  // namespace mtp
+
+namespace {
+
+constexpr unsigned long long kBarrierLimitNs = 1000000000ull;  // 1 s per barrier wait
+
+size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // LM head on tensor cores: the dense head, bf16 weights and a batch of at
 // least kTcMinBatch
@@ -159,21 +179,6 @@ DraftLayout draft_layout(const mtp_config* c, int B, int N) {
     L.ACT = off;     off = al256(off + (size_t)B * L.kmax * f);
     L.end = off;
     return L;
-}
-
-// cuTensorMapEncodeTiled from the driver, resolved once
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
 }
 
 // 2-D bf16 tensor map over a row-major [rows, cols] matrix: box of 64

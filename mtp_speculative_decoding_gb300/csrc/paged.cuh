@@ -1,0 +1,274 @@
+// paged.cuh -- argument blocks, launchers and row helpers of the paged KV
+// cache's append and attention kernels (internal).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace mtp {
+
+// The paged cache as the kernels take it (see mtp_kv_cache).
+struct PagedKV {
+    void *k, *v;
+    float *ks, *vs;            // e4m3: scale of (page, KV head)
+    const int32_t* table;      // [B, max_pages]
+    long long sp, sh, st;      // strides of page, KV head, slot (elements)
+    int n_pages, ps_log2, max_pages, Hkv;
+    int window, sink;
+};
+
+// Turns (angle / 2 pi) per position of the rotation pair i, as a sum of two
+// floats (48 bits): theta^(-2 i / hd) / (2 pi).  Rounded to one float, a
+// position of 10^5 would already be 10^-2 radians off.
+struct RopeTab {
+    float hi[256], lo[256];
+    int on;
+};
+
+// ---------------------------------------------------------------------------
+// a row in units: thread c of a row's hd/16 threads holds the dimensions
+// [8c, 8c + 8) in a and [hd/2 + 8c, hd/2 + 8c + 8) in b -- the rotation's
+// pairs (i, i + hd/2) meet in one thread, and each half is a 16-byte load of
+// bf16
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    const uint4 u = ld_stream16(p), w = ld_stream16(p + 4);
+    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    x[4] = __uint_as_float(w.x); x[5] = __uint_as_float(w.y); x[6] = __uint_as_float(w.z); x[7] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+    const uint4 u = ld_stream16(p);
+    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
+    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+}
+// two floats rounded to bf16 (nearest even), lo in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// RMSNorm of a row spread over U = hd/16 consecutive lanes (a power of two;
+// every lane of the warp takes part)
+__device__ __forceinline__ void unit_norm(float (&a)[8], float (&b)[8], const float* gain, int c, int hd, float eps) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
+    for (int o = hd >> 5; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float r = 1.0f / sqrtf(s / (float)hd + eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        a[i] = a[i] * r * __ldg(gain + 8 * c + i);
+        b[i] = b[i] * r * __ldg(gain + (hd >> 1) + 8 * c + i);
+    }
+}
+
+// cos and sin of the unit's 8 pairs at position pos.  pos = 4096 ph + pl; each
+// product with the table's high part is split exactly by an fma, whole turns
+// are dropped, and what the remaining fp32 sum cannot hold turns the result
+// by a first-order correction -- the angle keeps about 2^-45 of its size plus
+// 2^-40 turns, so only the rounding of cos and sin themselves is left.
+__device__ __forceinline__ void unit_angles(long long pos, const RopeTab& tab, int c, float (&cs)[8], float (&sn)[8]) {
+    const float pl = (float)(int)(pos & 4095), ph = (float)(int)(pos >> 12) * 4096.f, pf = ph + pl;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float h = tab.hi[8 * c + i], l = tab.lo[8 * c + i];
+        float x = __fmul_rn(pl, h), y = __fmul_rn(ph, h);   // (no contraction: the products' own roundings are wanted)
+        float e = fmaf(pl, h, -x) + fmaf(ph, h, -y);
+        x -= rintf(x);
+        y -= rintf(y);
+        float s = x + y;
+        const float z = s - x;
+        e += (x - (s - z)) + (y - z);      // the rounding of x + y
+        s -= rintf(s);
+        e = fmaf(pf, l, e);                // up to 2^-7 turns at positions of 2^19: most of it joins s
+        const float t0 = s + e;
+        e -= t0 - s;
+        s = t0;
+        float sv, cv;
+        sincospif(2.f * s, &sv, &cv);
+        const float d = 6.2831853f * e;
+        cs[i] = fmaf(-sv, d, cv);
+        sn[i] = fmaf(cv, d, sv);
+    }
+}
+__device__ __forceinline__ void unit_rotate(float (&a)[8], float (&b)[8], const float (&cs)[8], const float (&sn)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = a[i], y = b[i];
+        a[i] = fmaf(x, cs[i], -y * sn[i]);
+        b[i] = fmaf(y, cs[i], x * sn[i]);
+    }
+}
+
+// A sequence's lengths are usable: 0 <= len, 0 <= n <= M, len + n <= the
+// positions its table row can map.
+__device__ __forceinline__ bool seq_ok(int len, int n, int M, const PagedKV& c) {
+    return len >= 0 && n >= 0 && n <= M && (long long)len + n <= (long long)c.max_pages << c.ps_log2;
+}
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+struct AppendArgs {
+    PagedKV c;
+    int hd, B, M;
+    const int32_t *kv_len, *n_new;
+    const void *k, *v;
+    long long sb, sm, sh;      // input strides (elements)
+    const float* k_norm;
+    float eps;
+    WsHeader* hdr;
+    RopeTab rope;
+    int hpt;                   // KV heads per thread (fp32 / bf16 caches; set by the launcher)
+};
+cudaError_t launch_kv_append(const AppendArgs& a, int in_dtype, int kv_dtype, int sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// attention
+// ---------------------------------------------------------------------------
+// An item is (sequence, KV head, row tile): RT of the sequence's n * G
+// rows (row r: new row r / G, query head r % G of the group) against its
+// attended positions in tiles of `tile` positions.  The items' tiles lie end
+// to end, sequence-major, T in all; CTA c takes tiles [T c / grid, T (c + 1) /
+// grid), so ragged lengths cost the same on every CTA.  A segment is the part
+// of one item inside one CTA's range.  A whole item is written out directly;
+// a part is left as (o, m, l) in slot 2c if it begins inside the item (at most
+// the CTA's first) and in 2c + 1 if it only ends there (at most its last), and
+// a second kernel merges the parts.
+struct PagedAttnArgs {
+    PagedKV c;
+    int hd, B, M, Hq, G;
+    const int32_t *kv_len, *n_new;
+    const void* q;
+    long long sb, sm, sh;
+    const float* q_norm;
+    float eps, scale;          // scale: attn_scale * log2(e) (scores are in bits)
+    void* out;
+    WsHeader* hdr;
+    int* cta_status;           // [grid]: MTP_OK or an error, written by every CTA
+    long long* pre;            // [B + 1]: tiles before a sequence, written by CTA 0 for the merge
+    float* part;               // [2 grid] slots of RT * (hd + 2) floats
+    int RT, tile, grid;
+    unsigned long long timeout_ns;
+    RopeTab rope;
+};
+
+// attended tiles of a sequence: tiles [0, st) (the sink) and [lt, et)
+struct TileMap { int st, lt, n; };
+__device__ __forceinline__ TileMap tile_map(const PagedAttnArgs& a, int len, int n) {
+    TileMap m = {0, 0, 0};
+    if (n <= 0 || !seq_ok(len, n, a.M, a.c)) return m;
+    const int et = (int)(((long long)len + n + a.tile - 1) / a.tile);
+    if (a.c.window > 0) {
+        const int lo = len + 1 > a.c.window ? len + 1 - a.c.window : 0;             // the first row's window
+        const int hi = len + n > a.c.window ? len + n - a.c.window : 0;             // the last row's
+        m.lt = lo / a.tile;
+        m.st = ((a.c.sink < hi ? a.c.sink : hi) + a.tile - 1) / a.tile;
+        if (m.st > m.lt) m.st = m.lt;
+    }
+    m.n = m.st + et - m.lt;
+    return m;
+}
+__device__ __forceinline__ int tile_at(const TileMap& m, int k) { return k < m.st ? k : m.lt + (k - m.st); }
+// position t is attended by the row at position p
+__device__ __forceinline__ bool attends(const PagedKV& c, int t, int p) {
+    return t <= p && (c.window == 0 || t > p - c.window || t < c.sink);
+}
+
+// row tiles that hold rows of a sequence with n new ones
+__device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int n) { return (n * a.G + a.RT - 1) / a.RT; }
+
+// pre[0..B] for the whole CTA (pre: shared, B + 1; tmp: shared, 33)
+template <int THREADS>
+__device__ __forceinline__ void schedule(const PagedAttnArgs& a, long long* pre, long long* tmp) {
+    const int per = (a.B + THREADS - 1) / THREADS, b0 = (int)threadIdx.x * per;
+    const int b1 = b0 + per < a.B ? b0 + per : a.B;
+    auto tiles = [&](int b) {
+        const int n = a.n_new ? a.n_new[b] : a.M;
+        return (long long)tile_map(a, a.kv_len[b], n).n * a.c.Hkv * row_tiles(a, n);
+    };
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += tiles(b);
+    long long inc = sum;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) tmp[warp] = inc;
+    __syncthreads();
+    long long base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += tmp[w];
+    for (int b = b0; b < b1; ++b) {
+        pre[b] = base;
+        base += tiles(b);
+        if (b == a.B - 1) pre[a.B] = base;
+    }
+    __syncthreads();
+}
+// first tile of CTA c's share, and the CTA whose share holds tile x.  With
+// fewer tiles than CTAs the first T CTAs take one each (no share between two
+// others is empty, so the merge reads written slots only).
+__device__ __forceinline__ long long share_lo(long long T, int c, int grid) {
+    return T < grid ? (c < T ? c : T) : T * c / grid;
+}
+__device__ __forceinline__ int share_of(long long T, long long x, int grid) {
+    return (int)(T < grid ? x : ((x + 1) * grid - 1) / T);
+}
+
+struct Segment {
+    int b, g, rt;              // sequence, KV head, row tile
+    int t0, n;                 // the item's tiles [t0, t0 + n)
+    int len, rows, slot;       // kv_len, rows of this tile, partial slot (-1: whole item)
+    TileMap map;
+};
+// CTA c's segment at x of its range [.., xe)
+__device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const long long* pre, long long x, long long xe, int c) {
+    Segment s;
+    int b = 0;
+    for (int hi = a.B - 1; b < hi;) {   // the last b with pre[b] <= x
+        const int mid = (b + hi + 1) >> 1;
+        if (pre[mid] <= x) b = mid;
+        else hi = mid - 1;
+    }
+    const int n = a.n_new ? a.n_new[b] : a.M;
+    s.b = b;
+    s.len = a.kv_len[b];
+    s.map = tile_map(a, s.len, n);
+    const long long rel = x - pre[b];
+    const int item = (int)(rel / s.map.n);
+    const int nrt = row_tiles(a, n);
+    s.g = item / nrt;
+    s.rt = item % nrt;
+    s.t0 = (int)(rel % s.map.n);
+    const long long left = xe - x;
+    s.n = s.map.n - s.t0 < left ? s.map.n - s.t0 : (int)left;
+    const int R = n * a.G - s.rt * a.RT;
+    s.rows = R < a.RT ? R : a.RT;
+    s.slot = s.t0 > 0 ? 2 * c : (s.n < s.map.n ? 2 * c + 1 : -1);
+    return s;
+}
+
+// floats of one partial slot
+__host__ __device__ constexpr long long part_floats(int RT, int hd) { return (long long)RT * (hd + 2); }
+
+constexpr int kCcTile = 32, kCcRows = 16;   // positions and rows of a tile on the CUDA cores
+
+cudaError_t launch_paged_attn_cc(const PagedAttnArgs& a, int dtype, int kv_dtype, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t s);
+
+}  // namespace mtp

@@ -1,0 +1,325 @@
+// paged_attn.cu -- attention over the paged cache on the CUDA cores, and the
+// merge of split items.
+//
+// Every score, maximum, sum and output is fp32; this path serves fp32 queries
+// or caches and the head dimension 32 (the bf16 and e4m3 caches of bf16
+// queries run on the tensor cores).
+#include "paged.cuh"
+
+namespace mtp {
+
+__device__ __forceinline__ void kv8(const float* p, float, float (&x)[8]) { load8(p, x); }
+__device__ __forceinline__ void kv8(const uint16_t* p, float, float (&x)[8]) { load8(p, x); }
+__device__ __forceinline__ void kv8(const uint8_t* p, float s, float (&x)[8]) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 y = __half22float2(__half2(h));
+        x[2 * i] = y.x * s;
+        x[2 * i + 1] = y.y * s;
+    }
+}
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(uint16_t* p, float x) { *p = (uint16_t)pack_bf16(x, 0.f); }
+
+constexpr int kCcThreads = 128;
+
+// One CTA: 16 rows x 32 positions a tile, K and then V staged as fp32 in
+// shared memory.  Warp w scores rows 4w..4w+3 with lane = position; thread d
+// owns output dimensions d, d + 128, .. of all 16 rows.
+template <typename QT, typename KT>
+__global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_constant__ PagedAttnArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    const int hd = a.hd, pitch = hd + 4, U = hd >> 4;
+    float* sq = sm;                               // [16][hd]
+    float* skv = sq + kCcRows * hd;               // [32][pitch]
+    float* sp = skv + kCcTile * pitch;            // [16][32]
+    float* sf = sp + kCcRows * kCcTile;           // [16] rescale factors
+    long long* pre = reinterpret_cast<long long*>(sf + kCcRows);
+    __shared__ long long tmp[33];
+    __shared__ const KT *skp[kCcTile], *svp[kCcTile];   // a position's K and V rows (null: absent)
+    __shared__ float sks[kCcTile], svs[kCcTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    schedule<kCcThreads>(a, pre, tmp);
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= a.B; b += kCcThreads) a.pre[b] = pre[b];
+    bool bad = false;
+    if (blockIdx.x == 0)
+        for (int b = tid; b < a.B; b += kCcThreads) bad = bad || !seq_ok(a.kv_len[b], a.n_new ? a.n_new[b] : a.M, a.M, a.c);
+    const long long T = pre[a.B];
+    long long x = share_lo(T, blockIdx.x, a.grid);
+    const long long xe = share_lo(T, blockIdx.x + 1, a.grid);
+    const QT* q = reinterpret_cast<const QT*>(a.q);
+    while (x < xe) {
+        const Segment s = segment_at(a, pre, x, xe, blockIdx.x);
+        const int r0 = s.rt * a.RT;
+        // queries: norm, rotation, scale
+        for (int i0 = 0; i0 < kCcRows * U; i0 += kCcThreads) {
+            const int i = i0 + tid, r = i / U, c = i % U;
+            const bool in = r < s.rows;
+            const int j = in ? (r0 + r) / a.G : 0, h = in ? (r0 + r) % a.G : 0;
+            float p[8], w[8];
+            const QT* src = q + s.b * a.sb + j * a.sm + (s.g * a.G + h) * a.sh + 8 * c;
+            load8(src, p);
+            load8(src + (hd >> 1), w);
+            if (a.q_norm) unit_norm(p, w, a.q_norm, c, hd, a.eps);
+            if (a.rope.on) {
+                float cs[8], sn[8];
+                unit_angles((long long)s.len + j, a.rope, c, cs, sn);
+                unit_rotate(p, w, cs, sn);
+            }
+            if (r < kCcRows)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sq[r * hd + 8 * c + e] = in ? p[e] * a.scale : 0.f;
+                    sq[r * hd + (hd >> 1) + 8 * c + e] = in ? w[e] * a.scale : 0.f;
+                }
+        }
+        float acc[kCcRows][4], m[4], l[4];
+#pragma unroll
+        for (int r = 0; r < kCcRows; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = -1e30f;
+            l[i] = 0.f;
+        }
+        const int p_last = s.len + (r0 + s.rows - 1) / a.G;   // position of the tile's last row
+        for (int k = 0; k < s.n; ++k) {
+            const int t0 = tile_at(s.map, s.t0 + k) * kCcTile;
+            __syncthreads();
+            if (tid < kCcTile) {
+                const int t = t0 + tid;
+                const KT *kp = nullptr, *vp = nullptr;
+                float ks = 1.f, vs = 1.f;
+                if (s.rows > 0 && t <= p_last) {
+                    const int pg = a.c.table[(long long)s.b * a.c.max_pages + (t >> a.c.ps_log2)];
+                    if ((unsigned)pg < (unsigned)a.c.n_pages) {
+                        const long long o = pg * a.c.sp + s.g * a.c.sh + (t & ((1 << a.c.ps_log2) - 1)) * a.c.st;
+                        kp = reinterpret_cast<const KT*>(a.c.k) + o;
+                        vp = reinterpret_cast<const KT*>(a.c.v) + o;
+                        if (a.c.ks) {
+                            ks = a.c.ks[(long long)pg * a.c.Hkv + s.g];
+                            vs = a.c.vs[(long long)pg * a.c.Hkv + s.g];
+                        }
+                    } else {
+                        // absent: an error only where a row attends it
+                        for (int r = 0; r < s.rows; r += a.G) bad = bad || attends(a.c, t, s.len + (r0 + r) / a.G);
+                        bad = bad || attends(a.c, t, p_last);
+                    }
+                }
+                skp[tid] = kp;
+                svp[tid] = vp;
+                sks[tid] = ks;
+                svs[tid] = vs;
+            }
+            __syncthreads();
+            auto stage = [&](const KT* const* rows, const float* sc) {
+                const int per = hd >> 3;
+                for (int i = tid; i < kCcTile * per; i += kCcThreads) {
+                    const int t = i / per, c = i % per;
+                    float v[8];
+                    if (rows[t]) kv8(rows[t] + 8 * c, sc[t], v);
+                    else
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+                    store8(skv + t * pitch + 8 * c, v);
+                }
+            };
+            stage(skp, sks);
+            __syncthreads();
+            float z[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int d = 0; d < hd; d += 4) {
+                const float4 kk = *reinterpret_cast<const float4*>(skv + lane * pitch + d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 qq = *reinterpret_cast<const float4*>(sq + (4 * warp + i) * hd + d);
+                    z[i] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, z[i]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * warp + i;
+                const bool see = r < s.rows && skp[lane] && attends(a.c, t0 + lane, s.len + (r0 + r) / a.G);
+                const float v = see ? z[i] : -__int_as_float(0x7F800000);
+                const float mn = fmaxf(m[i], warp_max(v));
+                const float p = exp2f(v - mn);
+                const float f = exp2f(m[i] - mn);
+                l[i] = l[i] * f + warp_sum(see ? p : 0.f);
+                m[i] = mn;
+                sp[r * kCcTile + lane] = see ? p : -1.f;   // -1: masked, whatever the value row holds
+                if (lane == 0) sf[r] = f;
+            }
+            __syncthreads();
+            stage(svp, svs);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = tid + kCcThreads * i;
+                if (d >= hd) break;
+#pragma unroll
+                for (int r = 0; r < kCcRows; ++r) acc[r][i] *= sf[r];
+                for (int t = 0; t < kCcTile; ++t) {
+                    const float v = skv[t * pitch + d];
+#pragma unroll
+                    for (int r = 0; r < kCcRows; ++r) {
+                        const float p = sp[r * kCcTile + t];
+                        if (!(p < 0.f)) acc[r][i] = fmaf(p, v, acc[r][i]);
+                    }
+                }
+            }
+        }
+        // l of every row to all threads
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane == 0) {
+                sf[4 * warp + i] = l[i];
+                sp[4 * warp + i] = m[i];
+            }
+        __syncthreads();
+        float* part = s.slot >= 0 ? a.part + s.slot * part_floats(a.RT, hd) : nullptr;
+#pragma unroll
+        for (int r = 0; r < kCcRows; ++r) {
+            if (r >= s.rows) break;
+            const int j = (r0 + r) / a.G, h = s.g * a.G + (r0 + r) % a.G;
+            QT* o = reinterpret_cast<QT*>(a.out) + (((long long)s.b * a.M + j) * a.Hq + h) * hd;
+            const float inv = sf[r] == 0.f ? 0.f : 1.f / sf[r];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = tid + kCcThreads * i;
+                if (d >= hd) break;
+                if (part) part[r * hd + d] = acc[r][i];
+                else put(o + d, acc[r][i] * inv);
+            }
+            if (part && tid == 0) {
+                part[a.RT * hd + r] = sp[r];
+                part[a.RT * (hd + 1) + r] = sf[r];
+            }
+        }
+        x += s.n;
+    }
+    const int any = __syncthreads_or(bad);
+    if (tid == 0) a.cta_status[blockIdx.x] = any ? MTP_ERR_ARG : MTP_OK;
+}
+
+// ---------------------------------------------------------------------------
+// merge: a warp takes one row of one item; an item that one CTA held whole is
+// written already.  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+// ---------------------------------------------------------------------------
+constexpr int kMergeThreads = 128;
+
+template <typename QT>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedAttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (blockIdx.x == gridDim.x - 1) {   // the call's status from the CTAs'
+        int bad = 0;
+        for (int c = tid; c < a.grid; c += kMergeThreads) {
+            const int st = a.cta_status[c];
+            if (st == MTP_ERR_TIMEOUT) bad |= 2;
+            else if (st != MTP_OK) bad |= 1;
+        }
+        const int any1 = __syncthreads_or(bad & 1), any2 = __syncthreads_or(bad & 2);
+        if (tid == 0) {
+            a.hdr->status = any2 ? MTP_ERR_TIMEOUT : (any1 ? MTP_ERR_ARG : MTP_OK);
+            a.hdr->barrier = 0;
+            a.hdr->done = 0;
+        }
+        return;
+    }
+    const int R = a.M * a.G;
+    const long long w = (long long)blockIdx.x * (kMergeThreads / 32) + (tid >> 5);
+    if (w >= (long long)a.B * a.c.Hkv * R) return;
+    const int rr = (int)(w % R), g = (int)(w / R % a.c.Hkv), b = (int)(w / R / a.c.Hkv);
+    const int n = a.n_new ? a.n_new[b] : a.M;
+    const long long T = a.pre[a.B], p0 = a.pre[b], span = a.pre[b + 1] - p0;
+    if (span == 0 || rr >= n * a.G) return;
+    const int nrt = row_tiles(a, n);
+    const long long per = span / (a.c.Hkv * nrt);
+    const int rt = rr / a.RT, r = rr % a.RT, hd = a.hd;
+    const long long x0 = p0 + per * (g * nrt + rt);
+    const int c0 = share_of(T, x0, a.grid), c1 = share_of(T, x0 + per - 1, a.grid);
+    if (c0 == c1) return;
+    const long long psz = part_floats(a.RT, hd);
+    float M = -1e30f;
+    auto slot = [&](int c) { return a.part + (c == c0 ? 2 * c + 1 : 2 * c) * psz; };
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot(c)[a.RT * hd + r]);
+    M = warp_max(M);
+    float l = 0.f;
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    for (int cb = c0; cb <= c1; cb += 32) {
+        const int c = cb + lane;
+        float wt = 0.f;
+        if (c <= c1) {
+            wt = exp2f(slot(c)[a.RT * hd + r] - M);
+            l = fmaf(wt, slot(c)[a.RT * (hd + 1) + r], l);
+        }
+        const int cnt = c1 - cb + 1 < 32 ? c1 - cb + 1 : 32;
+#pragma unroll 4
+        for (int k = 0; k < cnt; ++k) {
+            const float f = __shfl_sync(0xffffffffu, wt, k);
+            const float* o = slot(cb + k) + r * hd;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int d = lane + 32 * i;
+                if (d < hd) acc[i] = fmaf(f, o[d], acc[i]);
+            }
+        }
+    }
+    l = warp_sum(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    QT* o = reinterpret_cast<QT*>(a.out) + (((long long)b * a.M + rr / a.G) * a.Hq + g * a.G + rr % a.G) * hd;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int d = lane + 32 * i;
+        if (d < hd) put(o + d, acc[i] * inv);
+    }
+}
+
+namespace {
+size_t cc_smem(const PagedAttnArgs& a) {
+    return ((size_t)kCcRows * a.hd + (size_t)kCcTile * (a.hd + 4) + kCcRows * kCcTile + kCcRows) * sizeof(float) +
+           ((size_t)a.B + 1) * sizeof(long long);
+}
+template <typename QT, typename KT>
+cudaError_t cc(const PagedAttnArgs& a, cudaStream_t s) {
+    const size_t smem = cc_smem(a);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_attn_cc_kernel<QT, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    paged_attn_cc_kernel<QT, KT><<<a.grid, kCcThreads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+template <typename QT>
+cudaError_t cc_kv(const PagedAttnArgs& a, int kv_dtype, cudaStream_t s) {
+    return kv_dtype == MTP_DTYPE_F32 ? cc<QT, float>(a, s) : kv_dtype == MTP_DTYPE_BF16 ? cc<QT, uint16_t>(a, s) : cc<QT, uint8_t>(a, s);
+}
+}  // namespace
+
+cudaError_t launch_paged_attn_cc(const PagedAttnArgs& a, int dtype, int kv_dtype, cudaStream_t s) {
+    return dtype == MTP_DTYPE_F32 ? cc_kv<float>(a, kv_dtype, s) : cc_kv<uint16_t>(a, kv_dtype, s);
+}
+
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t s) {
+    const long long warps = (long long)a.B * a.c.Hkv * a.M * a.G;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32)) + 1);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its CTAs come in while the attention ends
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return dtype == MTP_DTYPE_F32 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<float>, a)
+                                  : cudaLaunchKernelEx(&cfg, paged_merge_kernel<uint16_t>, a);
+}
+
+}  // namespace mtp
