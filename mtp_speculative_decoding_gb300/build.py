@@ -22,7 +22,8 @@ LIB = os.path.join(BUILD, "libmtp.so")
 # source compiled once per (weight type, head dimension, tensor-core paths)
 UNITS = [("api", "api.cu", []), ("verify", "verify.cu", []), ("noalloc", "noalloc.cu", []),
          ("draft_dispatch", "draft_dispatch.cu", []), ("paged_api", "paged_api.cu", []),
-         ("kv_append", "kv_append.cu", []), ("paged_attn", "paged_attn.cu", []), ("logprobs", "logprobs.cu", [])]
+         ("kv_append", "kv_append.cu", []), ("paged_attn", "paged_attn.cu", []), ("logprobs", "logprobs.cu", []),
+         ("paged_attn_tc_bf16", "paged_attn_tc.cu", []), ("paged_attn_tc_e4m3", "paged_attn_tc.cu", ["-DMTP_PAGED_E4M3"])]
 for _hd in (32, 64, 128, 256, 512):
     for _name, _bf, _tc in (("f32", 0, 0), ("bf16_cc", 1, 0), ("bf16_tc", 1, 1)):
         UNITS.append((f"draft_{_name}_{_hd}", "draft_inst.cu",

@@ -11,6 +11,7 @@
 #include "logprobs.cuh"
 #include "mtp.h"
 #include "paged.cuh"
+#include "paged_attn_tc.cuh"
 
 using namespace mtp;
 
@@ -29,10 +30,10 @@ int check_cache(const mtp_kv_cache* c, bool pointers) {
     const int hd = c->head_dim;
     if (hd != 32 && hd != 64 && hd != 128 && hd != 256 && hd != 512) return MTP_ERR_UNSUPPORTED;
     if (c->page_size < 16 || c->page_size > MTP_MAX_PAGE_SIZE || (c->page_size & (c->page_size - 1))) return MTP_ERR_UNSUPPORTED;
-    if (c->n_kv_heads > 65535) return MTP_ERR_UNSUPPORTED;
+    if (c->n_kv_heads > 1024) return MTP_ERR_UNSUPPORTED;
     if (c->window < 0 || c->sink < 0 || (c->window == 0 && c->sink != 0)) return MTP_ERR_ARG;
     if (!(c->rope_theta >= 0.f) || isinf(c->rope_theta)) return MTP_ERR_ARG;
-    if ((long long)c->max_pages * c->page_size > 0x7FFFFFFFll) return MTP_ERR_UNSUPPORTED;   // positions are 31-bit
+    if ((long long)c->max_pages * c->page_size > 0x7FFFFF00ll) return MTP_ERR_UNSUPPORTED;   // positions are 31-bit
     const int esz = elem_size(c->kv_dtype);
     if (c->stride_t < hd || c->stride_h < 0 || c->stride_p < 0) return MTP_ERR_ARG;
     if ((c->stride_t * esz) % 16 || (c->stride_h * esz) % 16 || (c->stride_p * esz) % 16) return MTP_ERR_ARG;
@@ -82,7 +83,29 @@ void fill_rope(RopeTab* t, float theta, int hd) {
 
 // Tensor cores: bf16 queries, bf16 or e4m3 cache, head dimensions with a
 // 64-element multiple
-bool tc_path(const mtp_kv_cache* c, int dtype) { return false; }
+bool tc_path(const mtp_kv_cache* c, int dtype) {
+    return dtype == MTP_DTYPE_BF16 && c->kv_dtype != MTP_DTYPE_F32 && c->head_dim >= 64;
+}
+
+// (dimension, slot, KV head, page) map of k or v: boxes of one 128-byte (64 for
+// rows of 64 bytes) swizzled column by min(page_size, 128) slots
+bool encode_pages(CUtensorMap* m, const void* base, const mtp_kv_cache* c) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int esz = elem_size(c->kv_dtype);
+    const uint64_t row = (uint64_t)c->head_dim * esz;
+    const int box_bytes = row < 128 ? (int)row : 128;
+    const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->page_size, (cuuint64_t)c->n_kv_heads, (cuuint64_t)c->n_pages};
+    // a stride that no index uses may be anything: give it a legal value
+    const cuuint64_t strides[3] = {(cuuint64_t)c->stride_t * esz, c->n_kv_heads > 1 ? (cuuint64_t)c->stride_h * esz : row,
+                                   c->n_pages > 1 ? (cuuint64_t)c->stride_p * esz : row};
+    const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / esz), (cuuint32_t)(c->page_size < kTcTile ? c->page_size : kTcTile), 1, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return enc(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+               strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 struct AttnPlan {
     bool tc;
@@ -92,9 +115,9 @@ struct AttnPlan {
 AttnPlan attn_plan(const mtp_kv_cache* c, int B, int M, int n_q_heads, bool tc, int sms) {
     AttnPlan p;
     p.tc = tc;
-    p.RT = kCcRows;
-    p.tile = kCcTile;
-    p.grid = 2 * sms;
+    p.RT = tc ? tc_rows(M * (n_q_heads / c->n_kv_heads), c->head_dim) : kCcRows;
+    p.tile = tc ? kTcTile : kCcTile;
+    p.grid = tc ? sms : 2 * sms;
     size_t off = sizeof(WsHeader);
     p.status = off; off = al256(off + (size_t)p.grid * sizeof(int));
     p.pre = off;    off = al256(off + ((size_t)B + 1) * sizeof(long long));
@@ -169,7 +192,8 @@ int mtp_paged_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, cons
     const AttnPlan p = attn_plan(c, B, M, n_q_heads, tc_path(c, dtype), sms);
     if (!ws || misaligned(ws, 256) || ws_bytes < p.end) return MTP_ERR_WORKSPACE;
     char* base = static_cast<char*>(ws);
-    PagedAttnArgs a;
+    PagedTcArgs t;
+    PagedAttnArgs& a = t.a;
     a.c = device_cache(c);
     a.hd = c->head_dim; a.B = B; a.M = M; a.Hq = n_q_heads; a.G = n_q_heads / c->n_kv_heads;
     a.kv_len = kv_len; a.n_new = n_new;
@@ -185,7 +209,17 @@ int mtp_paged_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, cons
     a.timeout_ns = kWaitLimitNs;
     fill_rope(&a.rope, c->rope_theta, c->head_dim);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (launch_paged_attn_cc(a, dtype, c->kv_dtype, s) != cudaSuccess) return MTP_ERR_CUDA;
+    cudaError_t e;
+    if (p.tc) {
+        const bool e4m3 = c->kv_dtype == MTP_DTYPE_E4M3;
+        t.slots = tc_slots(e4m3, c->head_dim, p.RT, B);
+        if (t.slots < (c->head_dim + 127) / 128) return MTP_ERR_UNSUPPORTED;   // a value tile must fit the ring
+        if (!encode_pages(&t.tk, c->k, c) || !encode_pages(&t.tv, c->v, c)) return MTP_ERR_UNSUPPORTED;   // a stride beyond 2^40 bytes
+        e = e4m3 ? launch_paged_attn_tc_e4m3(t, s) : launch_paged_attn_tc_bf16(t, s);
+    } else {
+        e = launch_paged_attn_cc(a, dtype, c->kv_dtype, s);
+    }
+    if (e != cudaSuccess) return MTP_ERR_CUDA;
     return launch_paged_merge(a, dtype, s) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
 

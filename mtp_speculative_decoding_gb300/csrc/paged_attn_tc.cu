@@ -1,0 +1,773 @@
+// paged_attn_tc.cu -- attention of a verify step's rows over the paged cache
+// on tcgen05 tensor cores.
+//
+// The rows of one KV head (new rows x query heads of the group, 1 to a few
+// hundred) are few against the positions, so the positions take the MMA's M
+// side: S^T [128 positions, RT rows] = K Q^T with K's tile as it lies in the
+// page (K-major), and O^T [128 dimensions, RT rows] += V^T P^T with V's tile as
+// it lies in the page (its dimensions contiguous: the M-major operand).  K and
+// V go from the pages to the tensor core by TMA alone; an e4m3 cache is
+// multiplied as e4m3, exactly, so its bytes are the only traffic.  What would
+// lose bits is split instead: a query row into two bf16 parts (against bf16) or
+// three e4m3 parts under a power of two of its own (2^-12), a probability is
+// bf16 (against bf16), or three e5m2 parts (2^-9; e5m2 for its range: a weight
+// 2^-28 below the largest still counts).  The sum over the parts is the MMA's
+// own accumulation.
+//
+// Softmax: a thread is one position of the tile and holds its RT scores.  The
+// reference m of a row (the running maximum) moves only when a score exceeds
+// it by more than 2^kSlack, so most tiles need no reduction at all: one vote,
+// then exponentials.  A page's value scale is a power of two and joins the
+// score's exponent; the sum l takes it out again.
+//
+// Warps 0-3: softmax, epilogue; warp 4: TMA producer; warp 5: MMA issue.
+#include "paged_attn_tc.cuh"
+
+namespace mtp {
+
+namespace {
+
+// ---- tensor-core helpers of this kernel ----
+__device__ __forceinline__ void umma_f8(unsigned int d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(unsigned int taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, unsigned long long* bar,
+                                            unsigned long long pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+        "%4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)), "l"(pol)
+        : "memory");
+}
+// shared-memory matrix descriptor: 128- or 64-byte swizzled rows of ROWB
+// bytes, 8-row groups following one another; lead: bytes between the ROWB-wide
+// blocks of an M-major operand (0: the same block again, for rows of 64
+// dimensions under an M of 128 -- the upper half of the accumulator repeats
+// the lower and is not read)
+template <int ROWB>
+__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lead >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((8 * ROWB) >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(ROWB == 128 ? 2 : 4) << 61;
+    return d;
+}
+// fp32 accumulator, M x N; types 0 / 1: e4m3 / e5m2 (kind f8f6f4), 1: bf16 (kind f16)
+__host__ __device__ constexpr uint32_t instr(int ta, int tb, bool a_mn, int M, int N) {
+    return (1u << 4) | ((uint32_t)ta << 7) | ((uint32_t)tb << 10) | (a_mn ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+// 16-byte chunk `ch` of row r under the swizzle
+template <int ROWB>
+__device__ __forceinline__ int swz(int r, int ch) {
+    return r * ROWB + ((ROWB == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ bool vote_or(bool p) {   // over the 128 softmax threads
+    unsigned int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((unsigned)p)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float fexp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool E4M3, int HD, int RT>
+struct Shape {
+    static constexpr int ESZ = E4M3 ? 1 : 2;
+    static constexpr int ROWB = HD * ESZ < 128 ? HD * ESZ : 128;   // bytes of a box row
+    static constexpr int DB = HD < 128 ? HD : 128;                 // dimensions of a ring slot
+    static constexpr int D = HD / DB;                              // slots of a K or V tile
+    static constexpr int NBOX = DB * ESZ / ROWB;                   // boxes side by side in a slot
+    static constexpr int BOXB = kTcTile * ROWB;
+    static constexpr int SLOTB = NBOX * BOXB;
+    static constexpr int NQ = E4M3 ? 3 : 2;                        // parts of Q
+    static constexpr int QBOX = HD * ESZ / ROWB;                   // boxes of a Q row
+    static constexpr int QB = NQ * QBOX * RT * ROWB;
+    static constexpr int NP = E4M3 ? 3 : 1;                        // parts of P
+    static constexpr int PB = E4M3 ? 3 * RT * 128 : 2 * RT * 128;
+    static constexpr int COLS0 = (2 + D) * RT;
+    static constexpr int COLS = COLS0 <= 32 ? 32 : COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
+    // a score's exponent relative to its row's reference: at most kSlack; P
+    // against e4m3 lies in e5m2's range [2^-16, 2^15] with it and 2^kBias
+    static constexpr float kSlack = E4M3 ? 4.f : 8.f, kBias = E4M3 ? 11.f : 0.f;
+};
+
+constexpr int kTcThreads = 192;
+
+template <bool E4M3, int HD, int RT>
+__global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __grid_constant__ PagedTcArgs pa) {
+    using S = Shape<E4M3, HD, RT>;
+    const PagedAttnArgs& a = pa.a;
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int NS = pa.slots;
+    unsigned char* ring = base;
+    unsigned char* sQ = ring + (size_t)NS * S::SLOTB;
+    unsigned char* sP = sQ + S::QB;
+    unsigned long long* bars = reinterpret_cast<unsigned long long*>(sP + 2 * S::PB);
+    unsigned long long *full = bars, *empty = full + kTcSlotsMax, *meta_full = empty + kTcSlotsMax, *s_full = meta_full + kTcMeta,
+                       *s_free = s_full + 2, *p_full = s_free + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *end_bar = q_full + 1;
+    long long* tmp = reinterpret_cast<long long*>(end_bar + 1);
+    long long* pre = tmp + 33;
+    float* m_ks = reinterpret_cast<float*>(pre + a.B + 1);   // [kTcMeta][8] key scale (0: page not loaded)
+    float* m_vs = m_ks + kTcMeta * 8;                         // [kTcMeta][8] exponent of the value scale
+    float* s_m = m_vs + kTcMeta * 8;                          // [RT] reference
+    float* s_f = s_m + RT;                                    // [RT] rescale factor
+    float* s_c = s_f + RT;                                    // [RT] scale of the query row
+    float* s_red = s_c + RT;                                  // [4][RT]
+    int* s_pos = reinterpret_cast<int*>(s_red + 4 * RT);      // [RT] position of the row
+    int* s_row = s_pos + RT;                                  // [RT] output row
+    int* s_fix = s_row + RT;                                  // [kTcFix]
+    int* m_all = s_fix + kTcFix;                              // [kTcMeta] every page of the tile is loaded
+    __shared__ unsigned int s_tmem;
+    __shared__ int s_nfix, s_bad;
+    __shared__ volatile int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < kTcMeta; ++i) mbar_init(meta_full + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(s_free + i, 4);
+            mbar_init(p_full + i, 128);
+            mbar_init(pv_done + i, 1);
+        }
+        mbar_init(q_full, 128);
+        mbar_init(end_bar, 1);
+        mbar_fence_init();
+        s_nfix = 0;
+        s_bad = 0;
+        s_abort = 0;
+    }
+    if (warp == 5) {
+        tmem_alloc(&s_tmem, S::COLS);
+        tmem_relinquish();
+    }
+    schedule<kTcThreads>(a, pre, tmp);   // ends with a CTA barrier
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= a.B; b += kTcThreads) {
+            a.pre[b] = pre[b];
+            if (b < a.B && !seq_ok(a.kv_len[b], a.n_new ? a.n_new[b] : a.M, a.M, a.c)) s_bad = 1;
+        }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long T = pre[a.B];
+    const long long x0 = share_lo(T, blockIdx.x, a.grid), xe = share_lo(T, blockIdx.x + 1, a.grid);
+    // bounded wait; after one gave up every other does too
+    auto wait = [&](unsigned long long* bar, unsigned int parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(bar, parity)) {
+            if (s_abort) return false;
+            if (global_ns() - t0 > a.timeout_ns) {
+                s_abort = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+    const int ps = 1 << a.c.ps_log2, box_rows = ps < kTcTile ? ps : kTcTile, np = kTcTile / box_rows;
+
+    if (warp == 4) {
+        // ------------------------------------------------------------------
+        // producer: K tile k, then V tile k - 1, in the order the MMAs take
+        // them; lane i of a batch of 32 / np tiles holds page i % np of tile
+        // i / np
+        // ------------------------------------------------------------------
+        const unsigned long long pol = l2_evict_first();
+        unsigned int slot = 0, phase = 0, ti = 0;
+        bool ok = true, bad = false;
+        const int per_batch = 32 / np;
+        long long x = x0;
+        while (x < xe && ok) {
+            const Segment s = segment_at(a, pre, x, xe, blockIdx.x);
+            const int n_new = a.n_new ? a.n_new[s.b] : a.M, end = s.len + n_new;
+            const int lo = a.c.window > 0 && s.len + 1 > a.c.window ? s.len + 1 - a.c.window : 0;
+            const int hi = a.c.window > 0 && end > a.c.window ? end - a.c.window : 0;
+            const int sink = a.c.sink < hi ? a.c.sink : hi;
+            const int* tab = a.c.table + (long long)s.b * a.c.max_pages;
+            auto entry = [&](int k, int& y) -> int {   // page of this lane for tile s.t0 + k; -1: not loaded
+                y = 0;
+                if (k >= s.n) return -2;
+                const int p0 = tile_at(s.map, s.t0 + k) * kTcTile + (lane % np) * box_rows;
+                y = p0 & (ps - 1);
+                if (p0 >= end || (p0 + box_rows <= lo && p0 >= sink)) return -2;   // attended by no row
+                const int pg = tab[p0 >> a.c.ps_log2];
+                if ((unsigned)pg < (unsigned)a.c.n_pages) return pg;
+                bad = true;
+                return -1;
+            };
+            // tiles of V lag one behind K: keep the batch's and the previous tile's pages
+            int pg = -2, y = 0, pv_pg = -2, pv_y = 0, npg = -2, ny = 0;
+            npg = entry(lane / np, ny);
+            for (int k = 0; k <= s.n && ok; ++k) {
+                const int in = k % per_batch;
+                int kp = -2, ky = 0;
+                if (k < s.n) {
+                    if (in == 0) {
+                        pg = npg;
+                        y = ny;
+                        npg = entry(k + per_batch + lane / np, ny);
+                    }
+                    kp = __shfl_sync(0xffffffffu, pg, in * np + lane % np);
+                    ky = __shfl_sync(0xffffffffu, y, in * np + lane % np);
+                    if (lane < np) {
+                        float ks = kp >= 0 ? 1.f : 0.f, vs = 0.f;
+                        if (E4M3 && kp >= 0) {
+                            const long long o = (long long)kp * a.c.Hkv + s.g;
+                            ks = a.c.ks[o];
+                            vs = (float)((int)((__float_as_uint(a.c.vs[o]) >> 23) & 0xFF) - 127);
+                        }
+                        m_ks[(ti % kTcMeta) * 8 + lane] = ks;
+                        m_vs[(ti % kTcMeta) * 8 + lane] = vs;
+                    }
+                    const bool all = __all_sync(0xffffffffu, lane >= np || kp >= 0);
+                    if (lane == 0) m_all[ti % kTcMeta] = all;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(meta_full + ti % kTcMeta);
+                    ++ti;
+                }
+#pragma unroll 1
+                for (int which = 0; which < 2 && ok; ++which) {
+                    const bool key = which == 0;
+                    if (key ? k == s.n : k == 0) continue;
+                    const int p = key ? kp : pv_pg, yy = key ? ky : pv_y;
+                    const unsigned cnt = __popc(__ballot_sync(0xffffffffu, lane < np && p >= 0));
+                    for (int d = 0; d < S::D && ok; ++d) {
+                        ok = wait(empty + slot, phase ^ 1);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(full + slot, cnt * (unsigned)(box_rows * S::ROWB * S::NBOX));
+                        __syncwarp();
+                        if (lane < np && p >= 0) {
+                            unsigned char* dst = ring + (size_t)slot * S::SLOTB + lane * box_rows * S::ROWB;
+#pragma unroll
+                            for (int nb = 0; nb < S::NBOX; ++nb)
+                                tma_load_4d(dst + nb * S::BOXB, key ? &pa.tk : &pa.tv, d * S::DB + nb * (S::ROWB / S::ESZ), yy, s.g, p,
+                                            full + slot, pol);
+                        }
+                        if (++slot == (unsigned)NS) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+                pv_pg = kp;
+                pv_y = ky;
+            }
+            x += s.n;
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
+        if (!ok) {   // gave up: this warp's copies in flight end before the CTA does
+            const unsigned long long t0 = global_ns();
+            for (int i = 0; i < NS; ++i) {
+                // slot i's last fill has phase `phase` below the cursor, the phase before from it on
+                const unsigned int ph = i < (int)slot ? phase : phase ^ 1;
+                while (!mbar_try_wait(full + i, ph) && global_ns() - t0 < a.timeout_ns) {}
+            }
+        }
+    } else if (warp == 5) {
+        // ------------------------------------------------------------------
+        // MMA issue
+        // ------------------------------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t idS = E4M3 ? instr(0, 0, false, 128, RT) : instr(1, 1, false, 128, RT);
+            constexpr uint32_t idO = E4M3 ? instr(0, 1, true, 128, RT) : instr(1, 1, true, 128, RT);
+            const uint32_t q0 = smem_addr(sQ), p0 = smem_addr(sP), r0 = smem_addr(ring);
+            unsigned int slot = 0, phase = 0, ti = 0, seg = 0;
+            bool ok = true;
+            auto next = [&] {
+                if (++slot == (unsigned)NS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            long long x = x0;
+            while (x < xe && ok) {
+                const Segment s = segment_at(a, pre, x, xe, blockIdx.x);
+                ok = wait(q_full, seg & 1);
+                ++seg;
+                for (int k = 0; k <= s.n && ok; ++k) {
+                    if (k < s.n) {   // S^T of tile k
+                        const unsigned int t = ti + k, buf = t & 1;
+                        ok = wait(s_free + buf, ((t >> 1) & 1) ^ 1);
+                        for (int d = 0; d < S::D && ok; ++d) {
+                            ok = wait(full + slot, phase);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int nb = 0; nb < S::NBOX; ++nb)
+#pragma unroll
+                                for (int ks = 0; ks < S::ROWB / 32; ++ks)
+#pragma unroll
+                                    for (int part = 0; part < S::NQ; ++part) {
+                                        const uint64_t ad = desc<S::ROWB>(r0 + slot * S::SLOTB + nb * S::BOXB + ks * 32, 16);
+                                        const uint64_t bd = desc<S::ROWB>(
+                                            q0 + ((part * S::QBOX + d * S::NBOX + nb) * RT) * S::ROWB + ks * 32, 16);
+                                        const uint32_t acc = d > 0 || nb > 0 || ks > 0 || part > 0;
+                                        if (E4M3) umma_f8(tmem + buf * RT, ad, bd, idS, acc);
+                                        else umma_bf16(tmem + buf * RT, ad, bd, idS, acc);
+                                    }
+                            umma_commit(empty + slot);
+                            next();
+                        }
+                        if (ok) umma_commit(s_full + buf);
+                    }
+                    if (k > 0 && ok) {   // O^T of tile k - 1
+                        const unsigned int t = ti + k - 1, buf = t & 1;
+                        ok = wait(p_full + buf, (t >> 1) & 1);
+                        tc_fence_after();
+                        for (int d = 0; d < S::D && ok; ++d) {
+                            ok = wait(full + slot, phase);
+                            if (!ok) break;
+                            tc_fence_after();
+                            constexpr int KT = E4M3 ? 32 : 16;   // positions of an MMA
+#pragma unroll
+                            for (int ks = 0; ks < kTcTile / KT; ++ks)
+#pragma unroll
+                                for (int part = 0; part < S::NP; ++part) {
+                                    const uint64_t ad = desc<S::ROWB>(r0 + slot * S::SLOTB + ks * KT * S::ROWB, S::NBOX == 2 ? S::BOXB : 0);
+                                    // P: rows of 128 bytes (128 positions of e5m2, 64 of bf16)
+                                    const uint64_t bd = desc<128>(
+                                        p0 + buf * S::PB + (E4M3 ? part * RT * 128 + ks * 32 : (ks / 4) * RT * 128 + (ks % 4) * 32), 16);
+                                    const uint32_t acc = k > 1 || ks > 0 || part > 0;
+                                    if (E4M3) umma_f8(tmem + (2 + d) * RT, ad, bd, idO, acc);
+                                    else umma_bf16(tmem + (2 + d) * RT, ad, bd, idO, acc);
+                                }
+                            umma_commit(empty + slot);
+                            next();
+                        }
+                        if (ok) umma_commit(pv_done + buf);
+                    }
+                }
+                ti += s.n;
+                x += s.n;
+            }
+            umma_commit(end_bar);   // whatever was issued has ended before the CTA frees its memory
+            const unsigned long long t0 = global_ns();
+            while (!mbar_try_wait(end_bar, 0) && global_ns() - t0 < a.timeout_ns) {}
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------
+        // softmax and epilogue: thread = position of the tile, then dimension.
+        // A wait that gave up ends the other warps' work; these go on to the
+        // end with whatever is there, because they meet in barriers.
+        // ------------------------------------------------------------------
+        const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
+        unsigned int ti = 0, g0 = 0;   // tiles and ring slots before this segment
+        long long x = x0;
+        while (x < xe) {
+            const Segment s = segment_at(a, pre, x, xe, blockIdx.x);
+            const int r0 = s.rt * RT;
+            // ---- queries: norm, rotation, scale, parts ----
+            {
+                constexpr int U = HD / 16, RP = 128 / U;
+                const int c = tid % U;
+#pragma unroll 1
+                for (int rb = 0; rb < RT; rb += RP) {
+                    const int r = rb + tid / U;
+                    if (RP > RT && r >= RT) break;
+                    const bool in = r < s.rows;
+                    const int j = in ? (r0 + r) / a.G : 0, h = in ? (r0 + r) % a.G : 0;
+                    float p[8], q[8];
+                    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + s.b * a.sb + j * a.sm + (s.g * a.G + h) * a.sh + 8 * c;
+                    load8(src, p);
+                    load8(src + HD / 2, q);
+                    if (a.q_norm) unit_norm(p, q, a.q_norm, c, HD, a.eps);
+                    if (a.rope.on) {
+                        float cs[8], sn[8];
+                        unit_angles((long long)s.len + j, a.rope, c, cs, sn);
+                        unit_rotate(p, q, cs, sn);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        p[e] = in ? p[e] * a.scale : 0.f;
+                        q[e] = in ? q[e] * a.scale : 0.f;
+                    }
+                    if (E4M3) {
+                        float m = 0.f;
+                        bool fin = true;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            m = fmaxf(m, fmaxf(fabsf(p[e]), fabsf(q[e])));
+                            fin = fin && p[e] - p[e] == 0.f && q[e] - q[e] == 0.f;
+                        }
+                        for (int o = U / 2; o > 0; o >>= 1) {
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                            fin = __shfl_xor_sync(0xffffffffu, (int)fin, o) && fin;
+                        }
+                        int k = (int)(__float_as_uint(m) >> 23) - 127 - 7;   // m / 2^k in [128, 256)
+                        if (m == 0.f || k < -100) k = -100;
+                        if (k > 100) k = 100;
+                        const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
+                        if (c == 0) s_c[r] = fin ? __uint_as_float((uint32_t)(127 + k) << 23) : __uint_as_float(0x7FC00000u);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            p[e] *= inv;
+                            q[e] *= inv;
+                        }
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float* v = i < 2 ? p + 4 * i : q + 4 * (i - 2);
+                                uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+                                uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+                                w[i] = lo | (hi << 16);
+                                const float2 a0 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)lo, __NV_E4M3)));
+                                const float2 a1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+                                v[0] -= a0.x;
+                                v[1] -= a0.y;
+                                v[2] -= a1.x;
+                                v[3] -= a1.y;
+                            }
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int byte = half * (HD / 2) + 8 * c, box = byte / S::ROWB, in_row = byte % S::ROWB;
+                                unsigned char* d = sQ + ((part * S::QBOX + box) * RT) * S::ROWB + swz<S::ROWB>(r, in_row >> 4) + (in_row & 8);
+                                *reinterpret_cast<uint2*>(d) = make_uint2(w[2 * half], w[2 * half + 1]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                float* v = i < 4 ? p + 2 * i : q + 2 * (i - 4);
+                                w[i] = pack_bf16(v[0], v[1]);
+                                v[0] -= bf16_lo(w[i]);
+                                v[1] -= bf16_hi(w[i]);
+                            }
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int byte = half * HD + 16 * c, box = byte / S::ROWB;
+                                *reinterpret_cast<uint4*>(sQ + ((part * S::QBOX + box) * RT) * S::ROWB +
+                                                          swz<S::ROWB>(r, (byte % S::ROWB) >> 4)) =
+                                    make_uint4(w[4 * half], w[4 * half + 1], w[4 * half + 2], w[4 * half + 3]);
+                            }
+                        }
+                    }
+                }
+            }
+            const int p_first = s.len + r0 / a.G, p_last = s.len + (r0 + s.rows - 1) / a.G;
+            if (tid < RT) {
+                const int r = tid < s.rows ? tid : s.rows - 1;
+                s_pos[tid] = s.len + (r0 + r) / a.G;
+                s_row[tid] = (s.b * a.M + (r0 + r) / a.G) * a.Hq + s.g * a.G + (r0 + r) % a.G;
+                s_m[tid] = -1e30f;
+            }
+            if (tid == 0) s_nfix = 0;
+            fence_proxy_async_smem();
+            mbar_arrive(q_full);
+            softmax_sync();
+            float l[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) l[r] = 0.f;
+
+            for (int k = 0; k < s.n; ++k) {
+                const unsigned int t = ti + k, buf = t & 1, par = (t >> 1) & 1;
+                wait(meta_full + t % kTcMeta, (t / kTcMeta) & 1);
+                const int t0 = tile_at(s.map, s.t0 + k) * kTcTile, pos = t0 + tid;
+                const float ks = m_ks[(t % kTcMeta) * 8 + tid / box_rows];
+                const float ev = E4M3 ? m_vs[(t % kTcMeta) * 8 + tid / box_rows] : 0.f;
+                // every row attends every position of the tile
+                const bool whole = m_all[t % kTcMeta] && t0 + kTcTile - 1 <= p_first &&
+                                   (a.c.window == 0 || t0 > p_last - a.c.window || t0 + kTcTile <= a.c.sink);
+                wait(s_full + buf, par);
+                tc_fence_after();
+                float z[RT];
+#pragma unroll
+                for (int c = 0; c < RT; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(my + buf * RT + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[c + i] = __uint_as_float(v[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free + buf);
+                if (E4M3) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) z[r] = fmaf(z[r], ks * s_c[r], ev);
+                }
+                bool any = true, each = true;   // some row, every row attends this position
+                if (!whole) {
+                    const bool here = ks != 0.f;
+                    any = false;
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const bool see = here && attends(a.c, pos, s_pos[r]);
+                        any = any || see;
+                        each = each && see;
+                        z[r] = see ? z[r] : -__int_as_float(0x7F800000);
+                    }
+                }
+                bool over = false;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) over = over || z[r] > s_m[r] + S::kSlack;
+                if (vote_or(over)) {
+                    // move the references: the column maxima of this tile
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const float mx = redux_max(z[r]);
+                        if (lane == 0) s_red[warp * RT + r] = mx;
+                    }
+                    softmax_sync();
+                    if (tid < RT) {
+                        const float mo = s_m[tid];
+                        const float mn = fmaxf(fmaxf(fmaxf(s_red[tid], s_red[RT + tid]), fmaxf(s_red[2 * RT + tid], s_red[3 * RT + tid])), mo);
+                        s_m[tid] = mn;
+                        s_f[tid] = fexp2(mo - mn);
+                    }
+                    softmax_sync();
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) l[r] *= s_f[r];
+                    if (k > 0) {   // the accumulator, between two tiles' MMAs
+                        wait(pv_done + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < S::D * RT; c += 16) {
+                            uint32_t v[16];
+                            tmem_ld16(my + 2 * RT + c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * s_f[c % RT + i]);
+                            tmem_st16(my + 2 * RT + c, v);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                    }
+                }
+                // P of tile t - 2 is read
+                if (t >= 2) wait(pv_done + buf, par ^ 1);
+                unsigned char* P = sP + buf * S::PB;
+                if (E4M3) {
+                    const float unscale = fexp2(-ev);
+                    unsigned char* w = P + (tid & 15);
+                    const int ch = tid >> 4;
+#pragma unroll
+                    for (int r = 0; r < RT; r += 2) {
+                        const float e0 = fexp2(z[r] - s_m[r] + S::kBias), e1 = fexp2(z[r + 1] - s_m[r + 1] + S::kBias);
+                        l[r] = fmaf(e0, unscale, l[r]);
+                        l[r + 1] = fmaf(e1, unscale, l[r + 1]);
+                        __half2 h = __floats2half2_rn(e0, e1);
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) {
+                            const uint32_t b = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)h, __NV_SATFINITE, __NV_E5M2);
+                            w[part * RT * 128 + swz<128>(r, ch)] = (unsigned char)b;
+                            w[part * RT * 128 + swz<128>(r + 1, ch)] = (unsigned char)(b >> 8);
+                            if (part < 2) {
+                                const uint32_t back = __byte_perm(b, 0, 0x1404);   // e5m2 is fp16's upper byte
+                                h = __hsub2(h, *reinterpret_cast<const __half2*>(&back));
+                            }
+                        }
+                    }
+                } else {
+                    unsigned char* w = P + (tid >> 6) * RT * 128 + 2 * (tid & 7);
+                    const int ch = (tid & 63) >> 3;
+#pragma unroll
+                    for (int r = 0; r < RT; r += 2) {
+                        const float e0 = fexp2(z[r] - s_m[r]), e1 = fexp2(z[r + 1] - s_m[r + 1]);
+                        l[r] += e0;
+                        l[r + 1] += e1;
+                        const uint32_t b = pack_bf16(e0, e1);
+                        *reinterpret_cast<uint16_t*>(w + swz<128>(r, ch)) = (uint16_t)b;
+                        *reinterpret_cast<uint16_t*>(w + swz<128>(r + 1, ch)) = (uint16_t)(b >> 16);
+                    }
+                }
+                if (!whole && !each) {
+                    // a value row that not every row attends: zero it where it would
+                    // turn a zero weight into a NaN (all of it where nobody attends
+                    // it: the slot may hold anything; else only what is not finite,
+                    // which the epilogue adds to the rows that do attend it)
+                    const unsigned int v0 = g0 + (k == s.n - 1 ? (2 * s.n - 1) * S::D : (2 * k + 2) * S::D);
+                    bool listed = false;
+                    for (int d = 0; d < S::D; ++d) {
+                        const unsigned int g = v0 + d, sl = g % (unsigned)NS;
+                        wait(full + sl, (g / (unsigned)NS) & 1);
+                        unsigned char* row = ring + (size_t)sl * S::SLOTB;
+#pragma unroll 1
+                        for (int i = 0; i < S::NBOX * S::ROWB / 16; ++i) {
+                            uint4* e = reinterpret_cast<uint4*>(row + (i / (S::ROWB / 16)) * S::BOXB + swz<S::ROWB>(tid, i % (S::ROWB / 16)));
+                            if (!any) {
+                                *e = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            uint4 v = *e;
+                            uint32_t* q = reinterpret_cast<uint32_t*>(&v);
+                            bool hit = false;
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                if (E4M3) {
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y)
+                                        if (((q[n] >> (8 * y)) & 0x7Fu) == 0x7Fu) {
+                                            q[n] &= ~(0xFFu << (8 * y));
+                                            hit = true;
+                                        }
+                                } else {
+#pragma unroll
+                                    for (int y = 0; y < 2; ++y)
+                                        if (((q[n] >> (16 * y)) & 0x7F80u) == 0x7F80u) {
+                                            q[n] &= ~(0xFFFFu << (16 * y));
+                                            hit = true;
+                                        }
+                                }
+                            }
+                            if (hit) {
+                                *e = v;
+                                listed = true;
+                            }
+                        }
+                    }
+                    if (listed) {
+                        const int i = atomicAdd(&s_nfix, 1);
+                        if (i < kTcFix) s_fix[i] = pos;
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(p_full + buf);
+            }
+            // ---- epilogue: the row sums, then the accumulator ----
+            const unsigned int last = ti + s.n - 1;
+            wait(pv_done + (last & 1), (last >> 1) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const float v = warp_sum(l[r]);
+                if (lane == 0) s_red[warp * RT + r] = v;
+            }
+            softmax_sync();
+            if (tid < RT) {
+                const float v = s_red[tid] + s_red[RT + tid] + s_red[2 * RT + tid] + s_red[3 * RT + tid];
+                if (s.slot >= 0) {
+                    float* part = a.part + s.slot * part_floats(RT, HD);
+                    part[RT * HD + tid] = s_m[tid];
+                    part[RT * (HD + 1) + tid] = v;
+                    s_f[tid] = 1.f;
+                } else {
+                    s_f[tid] = v == 0.f ? 0.f : 1.f / v;
+                }
+            }
+            softmax_sync();
+            const int nfix = s_nfix < kTcFix ? s_nfix : kTcFix;
+#pragma unroll 1
+            for (int c = 0; c < S::D * RT; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(my + 2 * RT + c, v);
+                tmem_ld_wait();
+                const int d = (c / RT) * 128 + tid, rb = c % RT;
+                if (HD < 128 && tid >= HD) continue;
+                for (int f = 0; f < nfix; ++f) {   // values that are not finite, to the rows that attend them
+                    const int t = s_fix[f];
+                    const int pg = a.c.table[(long long)s.b * a.c.max_pages + (t >> a.c.ps_log2)];
+                    const long long o = pg * a.c.sp + s.g * a.c.sh + (t & (ps - 1)) * a.c.st + d;
+                    float val;
+                    if (E4M3) val = (reinterpret_cast<const uint8_t*>(a.c.v)[o] & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f;
+                    else val = bf16_to_f32(reinterpret_cast<const uint16_t*>(a.c.v)[o]);
+                    if (val - val == 0.f) continue;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (attends(a.c, t, s_pos[rb + i])) v[i] = __float_as_uint(__uint_as_float(v[i]) + val);
+                }
+                if (s.slot >= 0) {
+                    float* part = a.part + s.slot * part_floats(RT, HD);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (rb + i < s.rows) part[(rb + i) * HD + d] = __uint_as_float(v[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (rb + i < s.rows)
+                            reinterpret_cast<uint16_t*>(a.out)[(long long)s_row[rb + i] * HD + d] =
+                                (uint16_t)pack_bf16(__uint_as_float(v[i]) * s_f[rb + i], 0.f);
+                }
+            }
+            tc_fence_before();
+            softmax_sync();   // the row tables are rewritten next
+            ti += s.n;
+            g0 += 2 * s.n * S::D;
+            x += s.n;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) a.cta_status[blockIdx.x] = s_abort ? MTP_ERR_TIMEOUT : s_bad ? MTP_ERR_ARG : MTP_OK;
+    if (warp == 5) tmem_dealloc(tmem, S::COLS);
+}
+
+template <bool E4M3, int HD, int RT>
+cudaError_t go(const PagedTcArgs& p, cudaStream_t s) {
+    const int smem = p.slots * tc_slot_bytes(E4M3, HD) + tc_other(E4M3, HD, RT, p.a.B);
+    const cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<E4M3, HD, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    paged_attn_tc_kernel<E4M3, HD, RT><<<p.a.grid, kTcThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+template <bool E4M3, int HD>
+cudaError_t rows(const PagedTcArgs& p, cudaStream_t s) {
+    if (p.a.RT == 16) return go<E4M3, HD, 16>(p, s);
+    if (p.a.RT == 32) return go<E4M3, HD, 32>(p, s);
+    if constexpr (HD < 512) return go<E4M3, HD, 64>(p, s);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+#ifdef MTP_PAGED_E4M3
+cudaError_t launch_paged_attn_tc_e4m3(const PagedTcArgs& p, cudaStream_t s) {
+    constexpr bool E = true;
+#else
+cudaError_t launch_paged_attn_tc_bf16(const PagedTcArgs& p, cudaStream_t s) {
+    constexpr bool E = false;
+#endif
+    switch (p.a.hd) {
+    case 64: return rows<E, 64>(p, s);
+    case 128: return rows<E, 128>(p, s);
+    case 256: return rows<E, 256>(p, s);
+    case 512: return rows<E, 512>(p, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace mtp

@@ -1,0 +1,48 @@
+// paged_attn_tc.cuh -- attention over the paged cache on the tensor cores:
+// sizes shared by the kernel and the host's plan (internal).
+#pragma once
+
+#include <cuda.h>
+
+#include "paged.cuh"
+
+namespace mtp {
+
+constexpr int kTcTile = 128;          // positions of a tile: the MMA's M side
+constexpr int kTcSlotsMax = 24;       // ring slots of a CTA at most
+constexpr int kTcMeta = 16;           // tiles of page scales the producer may be ahead
+constexpr int kTcFix = 256;           // positions listed as not finite
+constexpr int kTcSmemLimit = 227 * 1024;
+
+struct PagedTcArgs {
+    CUtensorMap tk, tv;               // (dimension, slot, KV head, page) of k and v
+    PagedAttnArgs a;
+    int slots;                        // ring slots
+};
+
+// bytes of shared memory besides the ring
+__host__ __device__ constexpr int tc_other(bool e4m3, int hd, int RT, int B) {
+    return (e4m3 ? 3 : 2 * 2) * RT * hd                          // Q, in parts
+           + 2 * (e4m3 ? 3 * RT * 128 : 2 * RT * 128)            // P, two tiles
+           + kTcMeta * 8 * 2 * 4 + kTcMeta * 4                   // page scales
+           + RT * 4 * (4 + 3 + 2) + kTcFix * 4                   // row tables, list
+           + (2 * kTcSlotsMax + kTcMeta + 16) * 8 + 33 * 8 + 64 + (B + 1) * 8 + 1024;
+}
+__host__ __device__ constexpr int tc_slot_bytes(bool e4m3, int hd) { return kTcTile * (hd < 128 ? hd : 128) * (e4m3 ? 1 : 2); }
+__host__ __device__ constexpr int tc_slots(bool e4m3, int hd, int RT, int B) {
+    int n = (kTcSmemLimit - tc_other(e4m3, hd, RT, B)) / tc_slot_bytes(e4m3, hd);
+    const int d = hd < 128 ? 1 : hd / 128;
+    if (n > kTcSlotsMax) n = kTcSlotsMax;
+    if (n > 24 * d) n = 24 * d;
+    return n;
+}
+
+// rows of a row tile: the smallest of 16, 32, 64 that holds all rows (64, or
+// 32 at head dimension 512, where the queries of more rows leave no ring)
+inline int tc_rows(int rows, int hd) { return rows <= 16 ? 16 : rows <= 32 || hd == 512 ? 32 : 64; }
+
+// one translation unit each (paged_attn_tc.cu)
+cudaError_t launch_paged_attn_tc_bf16(const PagedTcArgs& p, cudaStream_t s);
+cudaError_t launch_paged_attn_tc_e4m3(const PagedTcArgs& p, cudaStream_t s);
+
+}  // namespace mtp
