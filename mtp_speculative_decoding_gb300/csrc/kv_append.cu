@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant_
     if (!__any_sync(0xffffffffu, dst != nullptr)) return;
     float cs[8], sn[8];
     const bool rot = key && a.rope.on;
-    if (rot) unit_angles(live ? pos : 0, a.rope, c, cs, sn);
+    if (rot) unit_angles<false>(live ? pos : 0, a.rope.hi + 8 * c, a.rope.lo + 8 * c, cs, sn);
 #pragma unroll 4
     for (int h = 0; h < a.hpt; ++h) {
         float p[8], q[8];
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(512) append_e4m3_kernel(const __grid_constant_
             if (key && a.k_norm) unit_norm(p[i], q[i], a.k_norm, c, a.hd, a.eps);
             if (key && a.rope.on) {
                 float cs[8], sn[8];
-                unit_angles((long long)len + j0 + (x < units ? x >> ulog : 0), a.rope, c, cs, sn);
+                unit_angles<false>((long long)len + j0 + (x < units ? x >> ulog : 0), a.rope.hi + 8 * c, a.rope.lo + 8 * c, cs, sn);
                 unit_rotate(p[i], q[i], cs, sn);
             }
         }

@@ -80,11 +80,14 @@ __device__ __forceinline__ void unit_norm(float (&a)[8], float (&b)[8], const fl
 // are dropped, and what the remaining fp32 sum cannot hold turns the result
 // by a first-order correction -- the angle keeps about 2^-45 of its size plus
 // 2^-40 turns, so only the rounding of cos and sin themselves is left.
-__device__ __forceinline__ void unit_angles(long long pos, const RopeTab& tab, int c, float (&cs)[8], float (&sn)[8]) {
+// FAST: the sine and cosine instructions (2^-20), for rows that round to 16
+// bits or fewer right after.  hi, lo: the table's 8 entries of this unit.
+template <bool FAST>
+__device__ __forceinline__ void unit_angles(long long pos, const float* hi, const float* lo, float (&cs)[8], float (&sn)[8]) {
     const float pl = (float)(int)(pos & 4095), ph = (float)(int)(pos >> 12) * 4096.f, pf = ph + pl;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float h = tab.hi[8 * c + i], l = tab.lo[8 * c + i];
+        const float h = hi[i], l = lo[i];
         float x = __fmul_rn(pl, h), y = __fmul_rn(ph, h);   // (no contraction: the products' own roundings are wanted)
         float e = fmaf(pl, h, -x) + fmaf(ph, h, -y);
         x -= rintf(x);
@@ -98,8 +101,15 @@ __device__ __forceinline__ void unit_angles(long long pos, const RopeTab& tab, i
         e -= t0 - s;
         s = t0;
         float sv, cv;
-        sincospif(2.f * s, &sv, &cv);
         const float d = 6.2831853f * e;
+        if (FAST) {
+            s -= rintf(s);
+            const float r = 6.2831853f * s;
+            asm("sin.approx.f32 %0, %1;" : "=f"(sn[i]) : "f"(r));
+            asm("cos.approx.f32 %0, %1;" : "=f"(cs[i]) : "f"(r));
+            continue;
+        }
+        sincospif(2.f * s, &sv, &cv);
         cs[i] = fmaf(-sv, d, cv);
         sn[i] = fmaf(cv, d, sv);
     }
@@ -161,7 +171,7 @@ struct PagedAttnArgs {
     int* cta_status;           // [grid]: MTP_OK or an error, written by every CTA
     long long* pre;            // [B + 1]: tiles before a sequence, written by CTA 0 for the merge
     float* part;               // [2 grid] slots of RT * (hd + 2) floats
-    int RT, tile, grid;
+    int RT, tile_log2, grid;
     unsigned long long timeout_ns;
     RopeTab rope;
 };
@@ -170,13 +180,14 @@ struct PagedAttnArgs {
 struct TileMap { int st, lt, n; };
 __device__ __forceinline__ TileMap tile_map(const PagedAttnArgs& a, int len, int n) {
     TileMap m = {0, 0, 0};
-    if (n <= 0 || !seq_ok(len, n, a.M, a.c)) return m;
-    const int et = (int)(((long long)len + n + a.tile - 1) / a.tile);
+    if (n <= 0) return m;
+    const int et = (len + n - 1 >> a.tile_log2) + 1;
     if (a.c.window > 0) {
         const int lo = len + 1 > a.c.window ? len + 1 - a.c.window : 0;             // the first row's window
         const int hi = len + n > a.c.window ? len + n - a.c.window : 0;             // the last row's
-        m.lt = lo / a.tile;
-        m.st = ((a.c.sink < hi ? a.c.sink : hi) + a.tile - 1) / a.tile;
+        m.lt = lo >> a.tile_log2;
+        const int sk = a.c.sink < hi ? a.c.sink : hi;
+        m.st = sk > 0 ? (sk - 1 >> a.tile_log2) + 1 : 0;
         if (m.st > m.lt) m.st = m.lt;
     }
     m.n = m.st + et - m.lt;
@@ -191,17 +202,35 @@ __device__ __forceinline__ bool attends(const PagedKV& c, int t, int p) {
 // row tiles that hold rows of a sequence with n new ones
 __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int n) { return (n * a.G + a.RT - 1) / a.RT; }
 
-// pre[0..B] for the whole CTA (pre: shared, B + 1; tmp: shared, 33)
+// What a CTA keeps of the call's sequences in shared memory.
+struct Plan {
+    long long* pre;            // [B + 1] tiles before a sequence
+    int2* len;                 // [B] kv_len, n_new
+};
+__host__ __device__ constexpr int plan_bytes(int B) { return (2 * B + 1) * 8; }
+
+// Fills the plan (tmp: shared, 33); false for this thread if it saw lengths
+// that are out of range.
 template <int THREADS>
-__device__ __forceinline__ void schedule(const PagedAttnArgs& a, long long* pre, long long* tmp) {
+__device__ __forceinline__ bool schedule(const PagedAttnArgs& a, const Plan& plan, long long* tmp) {
     const int per = (a.B + THREADS - 1) / THREADS, b0 = (int)threadIdx.x * per;
     const int b1 = b0 + per < a.B ? b0 + per : a.B;
+    long long* pre = plan.pre;
     auto tiles = [&](int b) {
-        const int n = a.n_new ? a.n_new[b] : a.M;
-        return (long long)tile_map(a, a.kv_len[b], n).n * a.c.Hkv * row_tiles(a, n);
+        const int2 l = plan.len[b];
+        return (long long)tile_map(a, l.x, l.y).n * row_tiles(a, l.y) * a.c.Hkv;
     };
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += tiles(b);
+    bool good = true;
+    for (int b = b0; b < b1; ++b) {
+        int2 l = make_int2(a.kv_len[b], a.n_new ? a.n_new[b] : a.M);
+        if (!seq_ok(l.x, l.y, a.M, a.c)) {
+            l = make_int2(0, 0);   // left out
+            good = false;
+        }
+        plan.len[b] = l;
+        sum += tiles(b);
+    }
     long long inc = sum;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -219,45 +248,52 @@ __device__ __forceinline__ void schedule(const PagedAttnArgs& a, long long* pre,
         if (b == a.B - 1) pre[a.B] = base;
     }
     __syncthreads();
+    return good;
 }
 // first tile of CTA c's share, and the CTA whose share holds tile x.  With
 // fewer tiles than CTAs the first T CTAs take one each (no share between two
 // others is empty, so the merge reads written slots only).
 __device__ __forceinline__ long long share_lo(long long T, int c, int grid) {
-    return T < grid ? (c < T ? c : T) : T * c / grid;
+    if (T < grid) return c < T ? c : T;
+    if (T < (1ll << 31) / (grid + 1)) return (unsigned)((unsigned)T * (unsigned)c) / (unsigned)grid;   // (a 64-bit division is slow)
+    return T * c / grid;
 }
 __device__ __forceinline__ int share_of(long long T, long long x, int grid) {
-    return (int)(T < grid ? x : ((x + 1) * grid - 1) / T);
+    if (T < grid) return (int)x;
+    if (T < (1ll << 31) / (grid + 1)) return (int)(((unsigned)(x + 1) * (unsigned)grid - 1u) / (unsigned)T);
+    return (int)(((x + 1) * grid - 1) / T);
 }
 
 struct Segment {
     int b, g, rt;              // sequence, KV head, row tile
     int t0, n;                 // the item's tiles [t0, t0 + n)
-    int len, rows, slot;       // kv_len, rows of this tile, partial slot (-1: whole item)
+    int len, n_new;            // of the sequence
+    int rows, slot;            // rows of this tile, partial slot (-1: whole item)
     TileMap map;
 };
 // CTA c's segment at x of its range [.., xe)
-__device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const long long* pre, long long x, long long xe, int c) {
+__device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const Plan& plan, long long x, long long xe, int c) {
     Segment s;
     int b = 0;
     for (int hi = a.B - 1; b < hi;) {   // the last b with pre[b] <= x
         const int mid = (b + hi + 1) >> 1;
-        if (pre[mid] <= x) b = mid;
+        if (plan.pre[mid] <= x) b = mid;
         else hi = mid - 1;
     }
-    const int n = a.n_new ? a.n_new[b] : a.M;
+    const int2 l = plan.len[b];
     s.b = b;
-    s.len = a.kv_len[b];
-    s.map = tile_map(a, s.len, n);
-    const long long rel = x - pre[b];
-    const int item = (int)(rel / s.map.n);
-    const int nrt = row_tiles(a, n);
-    s.g = item / nrt;
-    s.rt = item % nrt;
-    s.t0 = (int)(rel % s.map.n);
+    s.len = l.x;
+    s.n_new = l.y;
+    s.map = tile_map(a, l.x, l.y);
+    const long long rel = x - plan.pre[b];
+    const unsigned item = rel < (1ll << 31) ? (unsigned)rel / (unsigned)s.map.n : (unsigned)(rel / s.map.n);
+    s.t0 = (int)(rel - (long long)item * s.map.n);
+    const unsigned nrt = (unsigned)row_tiles(a, l.y);
+    s.g = (int)(item / nrt);
+    s.rt = (int)(item - s.g * nrt);
     const long long left = xe - x;
     s.n = s.map.n - s.t0 < left ? s.map.n - s.t0 : (int)left;
-    const int R = n * a.G - s.rt * a.RT;
+    const int R = l.y * a.G - s.rt * a.RT;
     s.rows = R < a.RT ? R : a.RT;
     s.slot = s.t0 > 0 ? 2 * c : (s.n < s.map.n ? 2 * c + 1 : -1);
     return s;
@@ -266,7 +302,7 @@ __device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const long
 // floats of one partial slot
 __host__ __device__ constexpr long long part_floats(int RT, int hd) { return (long long)RT * (hd + 2); }
 
-constexpr int kCcTile = 32, kCcRows = 16;   // positions and rows of a tile on the CUDA cores
+constexpr int kCcTileLog2 = 5, kCcTile = 1 << kCcTileLog2, kCcRows = 16;   // positions and rows of a tile on the CUDA cores
 
 cudaError_t launch_paged_attn_cc(const PagedAttnArgs& a, int dtype, int kv_dtype, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t s);

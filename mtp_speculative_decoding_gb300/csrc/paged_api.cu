@@ -109,14 +109,14 @@ bool encode_pages(CUtensorMap* m, const void* base, const mtp_kv_cache* c) {
 
 struct AttnPlan {
     bool tc;
-    int RT, tile, grid;
+    int RT, tile_log2, grid;
     size_t status, pre, part, end;
 };
 AttnPlan attn_plan(const mtp_kv_cache* c, int B, int M, int n_q_heads, bool tc, int sms) {
     AttnPlan p;
     p.tc = tc;
     p.RT = tc ? tc_rows(M * (n_q_heads / c->n_kv_heads), c->head_dim) : kCcRows;
-    p.tile = tc ? kTcTile : kCcTile;
+    p.tile_log2 = tc ? kTcTileLog2 : kCcTileLog2;
     p.grid = tc ? sms : 2 * sms;
     size_t off = sizeof(WsHeader);
     p.status = off; off = al256(off + (size_t)p.grid * sizeof(int));
@@ -205,7 +205,7 @@ int mtp_paged_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, cons
     a.cta_status = reinterpret_cast<int*>(base + p.status);
     a.pre = reinterpret_cast<long long*>(base + p.pre);
     a.part = reinterpret_cast<float*>(base + p.part);
-    a.RT = p.RT; a.tile = p.tile; a.grid = p.grid;
+    a.RT = p.RT; a.tile_log2 = p.tile_log2; a.grid = p.grid;
     a.timeout_ns = kWaitLimitNs;
     fill_rope(&a.rope, c->rope_theta, c->head_dim);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -37,23 +37,22 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
     float* skv = sq + kCcRows * hd;               // [32][pitch]
     float* sp = skv + kCcTile * pitch;            // [16][32]
     float* sf = sp + kCcRows * kCcTile;           // [16] rescale factors
-    long long* pre = reinterpret_cast<long long*>(sf + kCcRows);
+    Plan plan;
+    plan.pre = reinterpret_cast<long long*>(sf + kCcRows);
+    plan.len = reinterpret_cast<int2*>(plan.pre + a.B + 1);
     __shared__ long long tmp[33];
     __shared__ const KT *skp[kCcTile], *svp[kCcTile];   // a position's K and V rows (null: absent)
     __shared__ float sks[kCcTile], svs[kCcTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    schedule<kCcThreads>(a, pre, tmp);
+    bool bad = !schedule<kCcThreads>(a, plan, tmp) && blockIdx.x == 0;
     if (blockIdx.x == 0)
-        for (int b = tid; b <= a.B; b += kCcThreads) a.pre[b] = pre[b];
-    bool bad = false;
-    if (blockIdx.x == 0)
-        for (int b = tid; b < a.B; b += kCcThreads) bad = bad || !seq_ok(a.kv_len[b], a.n_new ? a.n_new[b] : a.M, a.M, a.c);
-    const long long T = pre[a.B];
+        for (int b = tid; b <= a.B; b += kCcThreads) a.pre[b] = plan.pre[b];
+    const long long T = plan.pre[a.B];
     long long x = share_lo(T, blockIdx.x, a.grid);
     const long long xe = share_lo(T, blockIdx.x + 1, a.grid);
     const QT* q = reinterpret_cast<const QT*>(a.q);
     while (x < xe) {
-        const Segment s = segment_at(a, pre, x, xe, blockIdx.x);
+        const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
         const int r0 = s.rt * a.RT;
         // queries: norm, rotation, scale
         for (int i0 = 0; i0 < kCcRows * U; i0 += kCcThreads) {
@@ -67,7 +66,7 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
             if (a.q_norm) unit_norm(p, w, a.q_norm, c, hd, a.eps);
             if (a.rope.on) {
                 float cs[8], sn[8];
-                unit_angles((long long)s.len + j, a.rope, c, cs, sn);
+                unit_angles<false>((long long)s.len + j, a.rope.hi + 8 * c, a.rope.lo + 8 * c, cs, sn);
                 unit_rotate(p, w, cs, sn);
             }
             if (r < kCcRows)
@@ -207,15 +206,28 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------------------
-// merge: a warp takes one row of one item; an item that one CTA held whole is
-// written already.  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+// merge: a CTA takes one row of one item; an item that one CTA held whole is
+// written already.  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  The
+// parts are spread over the CTA's thread groups (hd / 4 threads each, four
+// dimensions a thread) so that their loads are in flight together: it is bound
+// by the latency of three dependent loads (the schedule, the maxima, the
+// parts).
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 128, kMergeParts = 512;   // parts whose weights are staged at a time
+
+__device__ __forceinline__ void put4(float* p, const float4& x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void put4(uint16_t* p, const float4& x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+}
 
 template <typename QT>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedAttnArgs a) {
+    __shared__ float s_w[kMergeParts];
+    __shared__ float4 s_o[kMergeThreads];
+    __shared__ float s_x[kMergeThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int R = a.M * a.G, rr = (int)(blockIdx.x % (unsigned)R), bg = (int)(blockIdx.x / (unsigned)R), g = bg % a.c.Hkv, b = bg / a.c.Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31;
     if (blockIdx.x == gridDim.x - 1) {   // the call's status from the CTAs'
         int bad = 0;
         for (int c = tid; c < a.grid; c += kMergeThreads) {
@@ -231,10 +243,6 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         }
         return;
     }
-    const int R = a.M * a.G;
-    const long long w = (long long)blockIdx.x * (kMergeThreads / 32) + (tid >> 5);
-    if (w >= (long long)a.B * a.c.Hkv * R) return;
-    const int rr = (int)(w % R), g = (int)(w / R % a.c.Hkv), b = (int)(w / R / a.c.Hkv);
     const int n = a.n_new ? a.n_new[b] : a.M;
     const long long T = a.pre[a.B], p0 = a.pre[b], span = a.pre[b + 1] - p0;
     if (span == 0 || rr >= n * a.G) return;
@@ -245,47 +253,67 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     const int c0 = share_of(T, x0, a.grid), c1 = share_of(T, x0 + per - 1, a.grid);
     if (c0 == c1) return;
     const long long psz = part_floats(a.RT, hd);
-    float M = -1e30f;
     auto slot = [&](int c) { return a.part + (c == c0 ? 2 * c + 1 : 2 * c) * psz; };
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot(c)[a.RT * hd + r]);
+    float M = -1e30f;
+    for (int c = c0 + tid; c <= c1; c += kMergeThreads) M = fmaxf(M, slot(c)[a.RT * hd + r]);
     M = warp_max(M);
+    if (lane == 0) s_x[warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(s_x[0], s_x[1]), fmaxf(s_x[2], s_x[3]));
+    const int gt = hd >> 2, groups = kMergeThreads / gt > 0 ? kMergeThreads / gt : 1;   // threads of a group, groups
+    const int my = tid / gt, d = 4 * (tid % gt);
     float l = 0.f;
-    float acc[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    for (int cb = c0; cb <= c1; cb += 32) {
-        const int c = cb + lane;
-        float wt = 0.f;
-        if (c <= c1) {
-            wt = exp2f(slot(c)[a.RT * hd + r] - M);
-            l = fmaf(wt, slot(c)[a.RT * (hd + 1) + r], l);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int cb = c0; cb <= c1; cb += kMergeParts) {
+        const int cnt = c1 - cb + 1 < kMergeParts ? c1 - cb + 1 : kMergeParts;
+        __syncthreads();
+        for (int k = tid; k < cnt; k += kMergeThreads) {
+            const float* p = slot(cb + k) + a.RT * hd + r;
+            const float w = exp2f(p[0] - M);
+            s_w[k] = w;
+            l = fmaf(w, p[a.RT], l);
         }
-        const int cnt = c1 - cb + 1 < 32 ? c1 - cb + 1 : 32;
-#pragma unroll 4
-        for (int k = 0; k < cnt; ++k) {
-            const float f = __shfl_sync(0xffffffffu, wt, k);
-            const float* o = slot(cb + k) + r * hd;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int d = lane + 32 * i;
-                if (d < hd) acc[i] = fmaf(f, o[d], acc[i]);
+        __syncthreads();
+        if (my < groups) {
+#pragma unroll 8
+            for (int k = my; k < cnt; k += groups) {
+                const float w = s_w[k];
+                const float4 o = *reinterpret_cast<const float4*>(slot(cb + k) + r * hd + d);
+                acc.x = fmaf(w, o.x, acc.x);
+                acc.y = fmaf(w, o.y, acc.y);
+                acc.z = fmaf(w, o.z, acc.z);
+                acc.w = fmaf(w, o.w, acc.w);
             }
         }
     }
     l = warp_sum(l);
+    __syncthreads();
+    if (lane == 0) s_x[warp] = l;
+    s_o[tid] = acc;
+    __syncthreads();
+    l = s_x[0] + s_x[1] + s_x[2] + s_x[3];
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    QT* o = reinterpret_cast<QT*>(a.out) + (((long long)b * a.M + rr / a.G) * a.Hq + g * a.G + rr % a.G) * hd;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int d = lane + 32 * i;
-        if (d < hd) put(o + d, acc[i] * inv);
+    if (tid < gt) {
+        for (int k = 1; k < groups; ++k) {
+            const float4 o = s_o[tid + k * gt];
+            acc.x += o.x;
+            acc.y += o.y;
+            acc.z += o.z;
+            acc.w += o.w;
+        }
+        acc.x *= inv;
+        acc.y *= inv;
+        acc.z *= inv;
+        acc.w *= inv;
+        QT* o = reinterpret_cast<QT*>(a.out) + (((long long)b * a.M + rr / a.G) * a.Hq + g * a.G + rr % a.G) * hd;
+        put4(o + d, acc);
     }
 }
 
 namespace {
 size_t cc_smem(const PagedAttnArgs& a) {
     return ((size_t)kCcRows * a.hd + (size_t)kCcTile * (a.hd + 4) + kCcRows * kCcTile + kCcRows) * sizeof(float) +
-           ((size_t)a.B + 1) * sizeof(long long);
+           (size_t)plan_bytes(a.B);
 }
 template <typename QT, typename KT>
 cudaError_t cc(const PagedAttnArgs& a, cudaStream_t s) {
@@ -308,9 +336,8 @@ cudaError_t launch_paged_attn_cc(const PagedAttnArgs& a, int dtype, int kv_dtype
 }
 
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t s) {
-    const long long warps = (long long)a.B * a.c.Hkv * a.M * a.G;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32)) + 1);
+    cfg.gridDim = dim3((unsigned)a.B * a.c.Hkv * a.M * a.G + 1);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];

@@ -20,7 +20,8 @@
 // then exponentials.  A page's value scale is a power of two and joins the
 // score's exponent; the sum l takes it out again.
 //
-// Warps 0-3: softmax, epilogue; warp 4: TMA producer; warp 5: MMA issue.
+// Warps 0-7: softmax and epilogue, half of the rows for each of two
+// warpgroups; warp 8: TMA producer; warp 9: MMA issue.
 #include "paged_attn_tc.cuh"
 
 namespace mtp {
@@ -36,13 +37,24 @@ __device__ __forceinline__ void umma_f8(unsigned int d, uint64_t ad, uint64_t bd
         "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(unsigned int taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld8(unsigned int taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(unsigned int taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    unsigned int p;
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-        : "memory");
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, unsigned long long* bar,
@@ -68,9 +80,21 @@ __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead) {
     d |= (uint64_t)(ROWB == 128 ? 2 : 4) << 61;
     return d;
 }
+// P: its rows (N) are contiguous, 16 bytes of them a position, no swizzle; 8
+// positions are a 128-byte core, positions follow densely, 16-byte row blocks
+// are 2048 bytes apart
+__device__ __forceinline__ uint64_t desc_p(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(128 >> 4) << 16;
+    d |= (uint64_t)(2048 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    return d;
+}
 // fp32 accumulator, M x N; types 0 / 1: e4m3 / e5m2 (kind f8f6f4), 1: bf16 (kind f16)
-__host__ __device__ constexpr uint32_t instr(int ta, int tb, bool a_mn, int M, int N) {
-    return (1u << 4) | ((uint32_t)ta << 7) | ((uint32_t)tb << 10) | (a_mn ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) |
+// (mn: both operands M- / N-major)
+__host__ __device__ constexpr uint32_t instr(int ta, int tb, bool mn, int M, int N) {
+    return (1u << 4) | ((uint32_t)ta << 7) | ((uint32_t)tb << 10) | (mn ? 3u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
 // 16-byte chunk `ch` of row r under the swizzle
@@ -78,19 +102,21 @@ template <int ROWB>
 __device__ __forceinline__ int swz(int r, int ch) {
     return r * ROWB + ((ROWB == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4);
 }
-__device__ __forceinline__ bool vote_or(bool p) {   // over the 128 softmax threads
+// barriers of a softmax warpgroup (id 1 + wg) and of both (id 3)
+__device__ __forceinline__ bool vote_or(int wg, bool p) {
     unsigned int r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.aligned.pred q, 1, 128, p;\n\t"
+        "setp.ne.b32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %1, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((unsigned)p)
+        : "r"(1 + wg), "r"((unsigned)p)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void wg_sync(int wg) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + wg) : "memory"); }
+__device__ __forceinline__ void both_sync() { asm volatile("barrier.cta.sync.aligned 3, 256;" ::: "memory"); }
 __device__ __forceinline__ float redux_max(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -115,19 +141,28 @@ struct Shape {
     static constexpr int QBOX = HD * ESZ / ROWB;                   // boxes of a Q row
     static constexpr int QB = NQ * QBOX * RT * ROWB;
     static constexpr int NP = E4M3 ? 3 : 1;                        // parts of P
-    static constexpr int PB = E4M3 ? 3 * RT * 128 : 2 * RT * 128;
-    static constexpr int COLS0 = (2 + D) * RT;
+    static constexpr int PB = NP * RT * ESZ * kTcTile;
+    // The parts of an operand lie side by side in N where tensor memory has the
+    // columns (one MMA instead of NQ or NP: an MMA takes about 40 ns here
+    // whatever its N), and are summed when they are read; else they accumulate.
+    static constexpr int SCOLS = NQ * RT;                          // scores, two tiles
+    static constexpr bool ON = 2 * SCOLS + D * NP * RT <= 512;     // outputs side by side too
+    static constexpr int NO = ON ? NP : 1;
+    static constexpr int O0 = 2 * SCOLS, COLS0 = O0 + D * NO * RT;
     static constexpr int COLS = COLS0 <= 32 ? 32 : COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
+    static_assert(COLS0 <= 512, "tensor memory");
+    static constexpr int RW = RT / 2;                              // rows of a softmax warpgroup
     // a score's exponent relative to its row's reference: at most kSlack; P
     // against e4m3 lies in e5m2's range [2^-16, 2^15] with it and 2^kBias
     static constexpr float kSlack = E4M3 ? 4.f : 8.f, kBias = E4M3 ? 11.f : 0.f;
 };
 
-constexpr int kTcThreads = 192;
+constexpr int kTcThreads = 320;
 
 template <bool E4M3, int HD, int RT>
 __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __grid_constant__ PagedTcArgs pa) {
     using S = Shape<E4M3, HD, RT>;
+    constexpr int RW = S::RW;
     const PagedAttnArgs& a = pa.a;
     extern __shared__ unsigned char raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -135,25 +170,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     unsigned char* ring = base;
     unsigned char* sQ = ring + (size_t)NS * S::SLOTB;
     unsigned char* sP = sQ + S::QB;
-    unsigned long long* bars = reinterpret_cast<unsigned long long*>(sP + 2 * S::PB);
+    float* s_hi = reinterpret_cast<float*>(sP + 2 * S::PB);   // [HD/2], [HD/2]: rotation table
+    float* s_lo = s_hi + HD / 2;
+    float* m_ks = s_lo + HD / 2;                               // [kTcMeta][8] key scale (0: page not loaded)
+    float* m_vs = m_ks + kTcMeta * 8;                          // [kTcMeta][8] exponent of the value scale
+    float* s_m = m_vs + kTcMeta * 8;                           // [RT] reference
+    float* s_f = s_m + RT;                                     // [RT] rescale factor
+    float* s_c = s_f + RT;                                     // [RT] scale of the query row
+    float* s_red = s_c + RT;                                   // [4][RT]
+    int* s_pos = reinterpret_cast<int*>(s_red + 4 * RT);       // [RT] position of the row
+    int* s_row = s_pos + RT;                                   // [RT] output row
+    int* s_fix = s_row + RT;                                   // [kTcFix]
+    int* m_all = s_fix + kTcFix;                               // [kTcMeta] every page of the tile is loaded
+    unsigned long long* bars = reinterpret_cast<unsigned long long*>(m_all + kTcMeta);
     unsigned long long *full = bars, *empty = full + kTcSlotsMax, *meta_full = empty + kTcSlotsMax, *s_full = meta_full + kTcMeta,
                        *s_free = s_full + 2, *p_full = s_free + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *end_bar = q_full + 1;
     long long* tmp = reinterpret_cast<long long*>(end_bar + 1);
-    long long* pre = tmp + 33;
-    float* m_ks = reinterpret_cast<float*>(pre + a.B + 1);   // [kTcMeta][8] key scale (0: page not loaded)
-    float* m_vs = m_ks + kTcMeta * 8;                         // [kTcMeta][8] exponent of the value scale
-    float* s_m = m_vs + kTcMeta * 8;                          // [RT] reference
-    float* s_f = s_m + RT;                                    // [RT] rescale factor
-    float* s_c = s_f + RT;                                    // [RT] scale of the query row
-    float* s_red = s_c + RT;                                  // [4][RT]
-    int* s_pos = reinterpret_cast<int*>(s_red + 4 * RT);      // [RT] position of the row
-    int* s_row = s_pos + RT;                                  // [RT] output row
-    int* s_fix = s_row + RT;                                  // [kTcFix]
-    int* m_all = s_fix + kTcFix;                              // [kTcMeta] every page of the tile is loaded
+    Plan plan;
+    plan.pre = tmp + 33;
+    plan.len = reinterpret_cast<int2*>(plan.pre + a.B + 1);
     __shared__ unsigned int s_tmem;
     __shared__ int s_nfix, s_bad;
     __shared__ volatile int s_abort;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(full + i, 1);
@@ -162,33 +201,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         for (int i = 0; i < kTcMeta; ++i) mbar_init(meta_full + i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(s_free + i, 4);
-            mbar_init(p_full + i, 128);
+            mbar_init(s_free + i, 8);
+            mbar_init(p_full + i, 256);
             mbar_init(pv_done + i, 1);
         }
-        mbar_init(q_full, 128);
+        mbar_init(q_full, 256);
         mbar_init(end_bar, 1);
         mbar_fence_init();
         s_nfix = 0;
         s_bad = 0;
         s_abort = 0;
     }
-    if (warp == 5) {
+    if (warp == 9) {
         tmem_alloc(&s_tmem, S::COLS);
         tmem_relinquish();
     }
-    schedule<kTcThreads>(a, pre, tmp);   // ends with a CTA barrier
+    if (a.rope.on)
+        for (int i = tid; i < HD / 2; i += kTcThreads) {
+            s_hi[i] = a.rope.hi[i];
+            s_lo[i] = a.rope.lo[i];
+        }
+    const bool good = schedule<kTcThreads>(a, plan, tmp);   // meets in CTA barriers
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
-    if (blockIdx.x == 0)
-        for (int b = tid; b <= a.B; b += kTcThreads) {
-            a.pre[b] = pre[b];
-            if (b < a.B && !seq_ok(a.kv_len[b], a.n_new ? a.n_new[b] : a.M, a.M, a.c)) s_bad = 1;
-        }
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+    if (blockIdx.x == 0) {
+        for (int b = tid; b <= a.B; b += kTcThreads) a.pre[b] = plan.pre[b];
+        if (!good) s_bad = 1;
+    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long T = pre[a.B];
+    const long long T = plan.pre[a.B];
     const long long x0 = share_lo(T, blockIdx.x, a.grid), xe = share_lo(T, blockIdx.x + 1, a.grid);
     // bounded wait; after one gave up every other does too
     auto wait = [&](unsigned long long* bar, unsigned int parity) -> bool {
@@ -203,9 +246,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         }
         return true;
     };
-    const int ps = 1 << a.c.ps_log2, box_rows = ps < kTcTile ? ps : kTcTile, np = kTcTile / box_rows;
+    const int ps = 1 << a.c.ps_log2, box_log2 = a.c.ps_log2 < kTcTileLog2 ? a.c.ps_log2 : kTcTileLog2, box_rows = 1 << box_log2,
+              np = kTcTile >> box_log2, np_log2 = kTcTileLog2 - box_log2;
 
-    if (warp == 4) {
+    if (warp == 8) {
         // ------------------------------------------------------------------
         // producer: K tile k, then V tile k - 1, in the order the MMAs take
         // them; lane i of a batch of 32 / np tiles holds page i % np of tile
@@ -214,19 +258,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         const unsigned long long pol = l2_evict_first();
         unsigned int slot = 0, phase = 0, ti = 0;
         bool ok = true, bad = false;
-        const int per_batch = 32 / np;
+        const int per_batch = 32 >> np_log2;
         long long x = x0;
         while (x < xe && ok) {
-            const Segment s = segment_at(a, pre, x, xe, blockIdx.x);
-            const int n_new = a.n_new ? a.n_new[s.b] : a.M, end = s.len + n_new;
+            const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
+            const int end = s.len + s.n_new;
             const int lo = a.c.window > 0 && s.len + 1 > a.c.window ? s.len + 1 - a.c.window : 0;
             const int hi = a.c.window > 0 && end > a.c.window ? end - a.c.window : 0;
             const int sink = a.c.sink < hi ? a.c.sink : hi;
             const int* tab = a.c.table + (long long)s.b * a.c.max_pages;
-            auto entry = [&](int k, int& y) -> int {   // page of this lane for tile s.t0 + k; -1: not loaded
+            auto entry = [&](int k, int& y) -> int {   // page of this lane for tile s.t0 + k; below 0: not loaded
                 y = 0;
                 if (k >= s.n) return -2;
-                const int p0 = tile_at(s.map, s.t0 + k) * kTcTile + (lane % np) * box_rows;
+                const int p0 = tile_at(s.map, s.t0 + k) * kTcTile + ((lane & (np - 1)) << box_log2);
                 y = p0 & (ps - 1);
                 if (p0 >= end || (p0 + box_rows <= lo && p0 >= sink)) return -2;   // attended by no row
                 const int pg = tab[p0 >> a.c.ps_log2];
@@ -234,35 +278,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 bad = true;
                 return -1;
             };
-            // tiles of V lag one behind K: keep the batch's and the previous tile's pages
-            int pg = -2, y = 0, pv_pg = -2, pv_y = 0, npg = -2, ny = 0;
-            npg = entry(lane / np, ny);
+            int pg = -2, y = 0, pv_pg = -2, pv_y = 0, ny = 0;
+            int npg = entry(lane >> np_log2, ny);
             for (int k = 0; k <= s.n && ok; ++k) {
-                const int in = k % per_batch;
                 int kp = -2, ky = 0;
                 if (k < s.n) {
-                    if (in == 0) {
+                    const int in = k & (per_batch - 1);
+                    if (in == 0) {   // this batch's pages; the next one's are on their way meanwhile
                         pg = npg;
                         y = ny;
-                        npg = entry(k + per_batch + lane / np, ny);
+                        npg = entry(k + per_batch + (lane >> np_log2), ny);
                     }
-                    kp = __shfl_sync(0xffffffffu, pg, in * np + lane % np);
-                    ky = __shfl_sync(0xffffffffu, y, in * np + lane % np);
-                    if (lane < np) {
-                        float ks = kp >= 0 ? 1.f : 0.f, vs = 0.f;
-                        if (E4M3 && kp >= 0) {
-                            const long long o = (long long)kp * a.c.Hkv + s.g;
-                            ks = a.c.ks[o];
-                            vs = (float)((int)((__float_as_uint(a.c.vs[o]) >> 23) & 0xFF) - 127);
-                        }
-                        m_ks[(ti % kTcMeta) * 8 + lane] = ks;
-                        m_vs[(ti % kTcMeta) * 8 + lane] = vs;
-                    }
-                    const bool all = __all_sync(0xffffffffu, lane >= np || kp >= 0);
-                    if (lane == 0) m_all[ti % kTcMeta] = all;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(meta_full + ti % kTcMeta);
-                    ++ti;
+                    kp = __shfl_sync(0xffffffffu, pg, (in << np_log2) + (lane & (np - 1)));
+                    ky = __shfl_sync(0xffffffffu, y, (in << np_log2) + (lane & (np - 1)));
                 }
 #pragma unroll 1
                 for (int which = 0; which < 2 && ok; ++which) {
@@ -288,6 +316,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                             phase ^= 1;
                         }
                     }
+                    if (key) {   // the tile's scales, while its keys are on their way
+                        if (lane < np) {
+                            float ks = kp >= 0 ? 1.f : 0.f, vs = 0.f;
+                            if (E4M3 && kp >= 0) {
+                                const long long o = (long long)kp * a.c.Hkv + s.g;
+                                ks = a.c.ks[o];
+                                vs = (float)((int)((__float_as_uint(a.c.vs[o]) >> 23) & 0xFF) - 127);
+                            }
+                            m_ks[(ti % kTcMeta) * 8 + lane] = ks;
+                            m_vs[(ti % kTcMeta) * 8 + lane] = vs;
+                        }
+                        const bool all = __all_sync(0xffffffffu, lane >= np || kp >= 0);
+                        if (lane == 0) m_all[ti % kTcMeta] = all;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(meta_full + ti % kTcMeta);
+                        ++ti;
+                    }
                 }
                 pv_pg = kp;
                 pv_y = ky;
@@ -298,144 +343,146 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         if (!ok) {   // gave up: this warp's copies in flight end before the CTA does
             const unsigned long long t0 = global_ns();
             for (int i = 0; i < NS; ++i) {
-                // slot i's last fill has phase `phase` below the cursor, the phase before from it on
+                // slot i's last fill: of this lap below the cursor, of the lap before from it on
                 const unsigned int ph = i < (int)slot ? phase : phase ^ 1;
                 while (!mbar_try_wait(full + i, ph) && global_ns() - t0 < a.timeout_ns) {}
             }
         }
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         // ------------------------------------------------------------------
-        // MMA issue
+        // MMA issue: the whole warp walks (descriptors stay in uniform
+        // registers), one elected lane issues
         // ------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t idS = E4M3 ? instr(0, 0, false, 128, RT) : instr(1, 1, false, 128, RT);
-            constexpr uint32_t idO = E4M3 ? instr(0, 1, true, 128, RT) : instr(1, 1, true, 128, RT);
-            const uint32_t q0 = smem_addr(sQ), p0 = smem_addr(sP), r0 = smem_addr(ring);
-            unsigned int slot = 0, phase = 0, ti = 0, seg = 0;
-            bool ok = true;
-            auto next = [&] {
-                if (++slot == (unsigned)NS) {
-                    slot = 0;
-                    phase ^= 1;
-                }
-            };
-            long long x = x0;
-            while (x < xe && ok) {
-                const Segment s = segment_at(a, pre, x, xe, blockIdx.x);
-                ok = wait(q_full, seg & 1);
-                ++seg;
-                for (int k = 0; k <= s.n && ok; ++k) {
-                    if (k < s.n) {   // S^T of tile k
-                        const unsigned int t = ti + k, buf = t & 1;
-                        ok = wait(s_free + buf, ((t >> 1) & 1) ^ 1);
-                        for (int d = 0; d < S::D && ok; ++d) {
-                            ok = wait(full + slot, phase);
-                            if (!ok) break;
-                            tc_fence_after();
+        constexpr uint32_t idS = E4M3 ? instr(0, 0, false, 128, S::SCOLS) : instr(1, 1, false, 128, S::SCOLS);
+        constexpr uint32_t idO = E4M3 ? instr(0, 1, true, 128, S::NO * RT) : instr(1, 1, true, 128, S::NO * RT);
+        const uint32_t q0 = smem_addr(sQ), p0 = smem_addr(sP), r0 = smem_addr(ring);
+        const bool leader = elect_one();
+        unsigned int slot = 0, phase = 0, ti = 0, seg = 0;
+        bool ok = true;
+        auto next = [&] {
+            if (++slot == (unsigned)NS) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        auto hold = [&](unsigned long long* bar, unsigned int parity) {
+            ok = __all_sync(0xffffffffu, wait(bar, parity));
+            tc_fence_after();
+        };
+        long long x = x0;
+        while (x < xe && ok) {
+            const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
+            hold(q_full, seg & 1);
+            ++seg;
+            for (int k = 0; k <= s.n && ok; ++k) {
+                if (k < s.n) {   // S^T of tile k
+                    const unsigned int t = ti + k, buf = t & 1;
+                    hold(s_free + buf, ((t >> 1) & 1) ^ 1);
+                    for (int d = 0; d < S::D && ok; ++d) {
+                        hold(full + slot, phase);
+                        if (!ok) break;
+                        if (leader) {
 #pragma unroll
                             for (int nb = 0; nb < S::NBOX; ++nb)
 #pragma unroll
-                                for (int ks = 0; ks < S::ROWB / 32; ++ks)
-#pragma unroll
-                                    for (int part = 0; part < S::NQ; ++part) {
-                                        const uint64_t ad = desc<S::ROWB>(r0 + slot * S::SLOTB + nb * S::BOXB + ks * 32, 16);
-                                        const uint64_t bd = desc<S::ROWB>(
-                                            q0 + ((part * S::QBOX + d * S::NBOX + nb) * RT) * S::ROWB + ks * 32, 16);
-                                        const uint32_t acc = d > 0 || nb > 0 || ks > 0 || part > 0;
-                                        if (E4M3) umma_f8(tmem + buf * RT, ad, bd, idS, acc);
-                                        else umma_bf16(tmem + buf * RT, ad, bd, idS, acc);
-                                    }
+                                for (int ks = 0; ks < S::ROWB / 32; ++ks) {
+                                    const uint64_t ad = desc<S::ROWB>(r0 + slot * S::SLOTB + nb * S::BOXB + ks * 32, 16);
+                                    const uint64_t bd = desc<S::ROWB>(q0 + (d * S::NBOX + nb) * S::NQ * RT * S::ROWB + ks * 32, 16);
+                                    const uint32_t acc = d > 0 || nb > 0 || ks > 0;
+                                    if (E4M3) umma_f8(tmem + buf * S::SCOLS, ad, bd, idS, acc);
+                                    else umma_bf16(tmem + buf * S::SCOLS, ad, bd, idS, acc);
+                                }
                             umma_commit(empty + slot);
-                            next();
                         }
-                        if (ok) umma_commit(s_full + buf);
+                        next();
                     }
-                    if (k > 0 && ok) {   // O^T of tile k - 1
-                        const unsigned int t = ti + k - 1, buf = t & 1;
-                        ok = wait(p_full + buf, (t >> 1) & 1);
-                        tc_fence_after();
-                        for (int d = 0; d < S::D && ok; ++d) {
-                            ok = wait(full + slot, phase);
-                            if (!ok) break;
-                            tc_fence_after();
+                    if (ok && leader) umma_commit(s_full + buf);
+                }
+                if (k > 0 && ok) {   // O^T of tile k - 1
+                    const unsigned int t = ti + k - 1, buf = t & 1;
+                    hold(p_full + buf, (t >> 1) & 1);
+                    for (int d = 0; d < S::D && ok; ++d) {
+                        hold(full + slot, phase);
+                        if (!ok) break;
+                        if (leader) {
                             constexpr int KT = E4M3 ? 32 : 16;   // positions of an MMA
 #pragma unroll
                             for (int ks = 0; ks < kTcTile / KT; ++ks)
 #pragma unroll
-                                for (int part = 0; part < S::NP; ++part) {
+                                for (int part = 0; part < S::NP / S::NO; ++part) {
                                     const uint64_t ad = desc<S::ROWB>(r0 + slot * S::SLOTB + ks * KT * S::ROWB, S::NBOX == 2 ? S::BOXB : 0);
-                                    // P: rows of 128 bytes (128 positions of e5m2, 64 of bf16)
-                                    const uint64_t bd = desc<128>(
-                                        p0 + buf * S::PB + (E4M3 ? part * RT * 128 + ks * 32 : (ks / 4) * RT * 128 + (ks % 4) * 32), 16);
+                                    const uint64_t bd = desc_p(p0 + buf * S::PB + part * (RT * S::ESZ / 16) * 2048 + ks * KT * 16);
                                     const uint32_t acc = k > 1 || ks > 0 || part > 0;
-                                    if (E4M3) umma_f8(tmem + (2 + d) * RT, ad, bd, idO, acc);
-                                    else umma_bf16(tmem + (2 + d) * RT, ad, bd, idO, acc);
+                                    if (E4M3) umma_f8(tmem + S::O0 + d * S::NO * RT, ad, bd, idO, acc);
+                                    else umma_bf16(tmem + S::O0 + d * S::NO * RT, ad, bd, idO, acc);
                                 }
                             umma_commit(empty + slot);
-                            next();
                         }
-                        if (ok) umma_commit(pv_done + buf);
+                        next();
                     }
+                    if (ok && leader) umma_commit(pv_done + buf);
                 }
-                ti += s.n;
-                x += s.n;
             }
-            umma_commit(end_bar);   // whatever was issued has ended before the CTA frees its memory
-            const unsigned long long t0 = global_ns();
-            while (!mbar_try_wait(end_bar, 0) && global_ns() - t0 < a.timeout_ns) {}
+            ti += s.n;
+            x += s.n;
         }
+        if (leader) umma_commit(end_bar);   // whatever was issued has ended before the CTA frees its memory
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(end_bar, 0) && global_ns() - t0 < a.timeout_ns) {}
         __syncwarp();
     } else {
         // ------------------------------------------------------------------
-        // softmax and epilogue: thread = position of the tile, then dimension.
+        // softmax and epilogue: thread = position of the tile, then dimension;
+        // warpgroup wg has the rows [wg RW, wg RW + RW).
         // A wait that gave up ends the other warps' work; these go on to the
         // end with whatever is there, because they meet in barriers.
         // ------------------------------------------------------------------
-        const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
+        const int wg = warp >> 2, tok = tid & 127, w4 = warp & 3, rw = wg * RW;
+        const uint32_t my = tmem + ((uint32_t)(w4 * 32) << 16);
         unsigned int ti = 0, g0 = 0;   // tiles and ring slots before this segment
         long long x = x0;
         while (x < xe) {
-            const Segment s = segment_at(a, pre, x, xe, blockIdx.x);
+            const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
             const int r0 = s.rt * RT;
             // ---- queries: norm, rotation, scale, parts ----
             {
-                constexpr int U = HD / 16, RP = 128 / U;
+                constexpr int U = HD / 16, RP = 256 / U;
                 const int c = tid % U;
 #pragma unroll 1
                 for (int rb = 0; rb < RT; rb += RP) {
                     const int r = rb + tid / U;
-                    if (RP > RT && r >= RT) break;
+                    if (RP > RT && r >= RT) break;   // whole warps
                     const bool in = r < s.rows;
-                    const int j = in ? (r0 + r) / a.G : 0, h = in ? (r0 + r) % a.G : 0;
                     float p[8], q[8];
-                    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + s.b * a.sb + j * a.sm + (s.g * a.G + h) * a.sh + 8 * c;
-                    load8(src, p);
-                    load8(src + HD / 2, q);
-                    if (a.q_norm) unit_norm(p, q, a.q_norm, c, HD, a.eps);
-                    if (a.rope.on) {
+                    bool fin = true;
+                    float amax = 0.f;
+                    if (__any_sync(0xffffffffu, in)) {
+                        const int j = in ? (r0 + r) / a.G : 0, h = in ? (r0 + r) - j * a.G : 0;
+                        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + s.b * a.sb + j * a.sm + (s.g * a.G + h) * a.sh + 8 * c;
+                        load8(src, p);
+                        load8(src + HD / 2, q);
                         float cs[8], sn[8];
-                        unit_angles((long long)s.len + j, a.rope, c, cs, sn);
-                        unit_rotate(p, q, cs, sn);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        p[e] = in ? p[e] * a.scale : 0.f;
-                        q[e] = in ? q[e] * a.scale : 0.f;
-                    }
-                    if (E4M3) {
-                        float m = 0.f;
-                        bool fin = true;
+                        if (a.rope.on) unit_angles<true>((long long)s.len + j, s_hi + 8 * c, s_lo + 8 * c, cs, sn);
+                        if (a.q_norm) unit_norm(p, q, a.q_norm, c, HD, a.eps);
+                        if (a.rope.on) unit_rotate(p, q, cs, sn);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            m = fmaxf(m, fmaxf(fabsf(p[e]), fabsf(q[e])));
+                            p[e] = in ? p[e] * a.scale : 0.f;
+                            q[e] = in ? q[e] * a.scale : 0.f;
+                            amax = fmaxf(amax, fmaxf(fabsf(p[e]), fabsf(q[e])));
                             fin = fin && p[e] - p[e] == 0.f && q[e] - q[e] == 0.f;
                         }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
+                    }
+                    if (E4M3) {
                         for (int o = U / 2; o > 0; o >>= 1) {
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                             fin = __shfl_xor_sync(0xffffffffu, (int)fin, o) && fin;
                         }
-                        int k = (int)(__float_as_uint(m) >> 23) - 127 - 7;   // m / 2^k in [128, 256)
-                        if (m == 0.f || k < -100) k = -100;
+                        int k = (int)(__float_as_uint(amax) >> 23) - 127 - 7;   // the largest over 2^k in [128, 256)
+                        if (amax == 0.f || k < -100) k = -100;
                         if (k > 100) k = 100;
                         const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
                         if (c == 0) s_c[r] = fin ? __uint_as_float((uint32_t)(127 + k) << 23) : __uint_as_float(0x7FC00000u);
@@ -463,7 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
                                 const int byte = half * (HD / 2) + 8 * c, box = byte / S::ROWB, in_row = byte % S::ROWB;
-                                unsigned char* d = sQ + ((part * S::QBOX + box) * RT) * S::ROWB + swz<S::ROWB>(r, in_row >> 4) + (in_row & 8);
+                                unsigned char* d = sQ + (box * S::NQ + part) * RT * S::ROWB + swz<S::ROWB>(r, in_row >> 4) + (in_row & 8);
                                 *reinterpret_cast<uint2*>(d) = make_uint2(w[2 * half], w[2 * half + 1]);
                             }
                         }
@@ -481,7 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
                                 const int byte = half * HD + 16 * c, box = byte / S::ROWB;
-                                *reinterpret_cast<uint4*>(sQ + ((part * S::QBOX + box) * RT) * S::ROWB +
+                                *reinterpret_cast<uint4*>(sQ + (box * S::NQ + part) * RT * S::ROWB +
                                                           swz<S::ROWB>(r, (byte % S::ROWB) >> 4)) =
                                     make_uint4(w[4 * half], w[4 * half + 1], w[4 * half + 2], w[4 * half + 3]);
                             }
@@ -489,147 +536,167 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     }
                 }
             }
+            fence_proxy_async_smem();
+            mbar_arrive(q_full);
             const int p_first = s.len + r0 / a.G, p_last = s.len + (r0 + s.rows - 1) / a.G;
             if (tid < RT) {
                 const int r = tid < s.rows ? tid : s.rows - 1;
                 s_pos[tid] = s.len + (r0 + r) / a.G;
                 s_row[tid] = (s.b * a.M + (r0 + r) / a.G) * a.Hq + s.g * a.G + (r0 + r) % a.G;
-                s_m[tid] = -1e30f;
             }
             if (tid == 0) s_nfix = 0;
-            fence_proxy_async_smem();
-            mbar_arrive(q_full);
-            softmax_sync();
-            float l[RT];
+            both_sync();
+            float l[RW], m[RW], c[RW];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) l[r] = 0.f;
+            for (int r = 0; r < RW; ++r) {
+                l[r] = 0.f;
+                m[r] = -1e30f;
+                c[r] = E4M3 ? s_c[rw + r] : 1.f;
+            }
 
             for (int k = 0; k < s.n; ++k) {
                 const unsigned int t = ti + k, buf = t & 1, par = (t >> 1) & 1;
                 wait(meta_full + t % kTcMeta, (t / kTcMeta) & 1);
-                const int t0 = tile_at(s.map, s.t0 + k) * kTcTile, pos = t0 + tid;
-                const float ks = m_ks[(t % kTcMeta) * 8 + tid / box_rows];
-                const float ev = E4M3 ? m_vs[(t % kTcMeta) * 8 + tid / box_rows] : 0.f;
+                const int t0 = tile_at(s.map, s.t0 + k) * kTcTile, pos = t0 + tok;
+                const float ks = m_ks[(t % kTcMeta) * 8 + (tok >> box_log2)];
+                const float ev = E4M3 ? m_vs[(t % kTcMeta) * 8 + (tok >> box_log2)] : 0.f;
                 // every row attends every position of the tile
                 const bool whole = m_all[t % kTcMeta] && t0 + kTcTile - 1 <= p_first &&
                                    (a.c.window == 0 || t0 > p_last - a.c.window || t0 + kTcTile <= a.c.sink);
                 wait(s_full + buf, par);
                 tc_fence_after();
-                float z[RT];
+                float z[RW];
+                {
+                    uint32_t v[S::NQ][RW];
 #pragma unroll
-                for (int c = 0; c < RT; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(my + buf * RT + c, v);
+                    for (int part = 0; part < S::NQ; ++part)
+#pragma unroll
+                        for (int i = 0; i < RW; i += 8) tmem_ld8(my + buf * S::SCOLS + part * RT + rw + i, v[part] + i);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[c + i] = __uint_as_float(v[i]);
+                    for (int r = 0; r < RW; ++r) {
+                        z[r] = __uint_as_float(v[0][r]) + __uint_as_float(v[1][r]);
+                        if (S::NQ == 3) z[r] += __uint_as_float(v[S::NQ - 1][r]);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free + buf);
                 if (E4M3) {
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) z[r] = fmaf(z[r], ks * s_c[r], ev);
+                    for (int r = 0; r < RW; ++r) z[r] = fmaf(z[r], ks * c[r], ev);
                 }
-                bool any = true, each = true;   // some row, every row attends this position
                 if (!whole) {
                     const bool here = ks != 0.f;
-                    any = false;
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const bool see = here && attends(a.c, pos, s_pos[r]);
-                        any = any || see;
-                        each = each && see;
-                        z[r] = see ? z[r] : -__int_as_float(0x7F800000);
-                    }
+                    for (int r = 0; r < RW; ++r)
+                        if (!(here && attends(a.c, pos, s_pos[rw + r]))) z[r] = -__int_as_float(0x7F800000);
                 }
                 bool over = false;
 #pragma unroll
-                for (int r = 0; r < RT; ++r) over = over || z[r] > s_m[r] + S::kSlack;
-                if (vote_or(over)) {
+                for (int r = 0; r < RW; ++r) over = over || z[r] > m[r] + S::kSlack;
+                if (vote_or(wg, over)) {
                     // move the references: the column maxima of this tile
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
+                    for (int r = 0; r < RW; ++r) {
                         const float mx = redux_max(z[r]);
-                        if (lane == 0) s_red[warp * RT + r] = mx;
+                        if (lane == 0) s_red[w4 * RT + rw + r] = mx;
                     }
-                    softmax_sync();
-                    if (tid < RT) {
-                        const float mo = s_m[tid];
-                        const float mn = fmaxf(fmaxf(fmaxf(s_red[tid], s_red[RT + tid]), fmaxf(s_red[2 * RT + tid], s_red[3 * RT + tid])), mo);
-                        s_m[tid] = mn;
-                        s_f[tid] = fexp2(mo - mn);
-                    }
-                    softmax_sync();
+                    wg_sync(wg);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) l[r] *= s_f[r];
+                    for (int r = 0; r < RW; ++r) {
+                        const float* q = s_red + rw + r;
+                        const float mn = fmaxf(fmaxf(fmaxf(q[0], q[RT]), fmaxf(q[2 * RT], q[3 * RT])), m[r]);
+                        const float f = fexp2(m[r] - mn);
+                        l[r] *= f;
+                        m[r] = mn;
+                        if (tok == r) s_f[rw + r] = f;
+                    }
                     if (k > 0) {   // the accumulator, between two tiles' MMAs
                         wait(pv_done + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+                        wg_sync(wg);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < S::D * RT; c += 16) {
-                            uint32_t v[16];
-                            tmem_ld16(my + 2 * RT + c, v);
-                            tmem_ld_wait();
+                        for (int b = 0; b < S::D * S::NO; ++b)
+#pragma unroll 1
+                            for (int i = 0; i < RW; i += 8) {
+                                uint32_t v[8];
+                                const uint32_t at = my + S::O0 + b * RT + rw + i;
+                                tmem_ld8(at, v);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * s_f[c % RT + i]);
-                            tmem_st16(my + 2 * RT + c, v);
-                        }
+                                for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * s_f[rw + i + e]);
+                                tmem_st8(at, v);
+                            }
                         tmem_st_wait();
                         tc_fence_before();
                     }
                 }
                 // P of tile t - 2 is read
                 if (t >= 2) wait(pv_done + buf, par ^ 1);
-                unsigned char* P = sP + buf * S::PB;
+                unsigned char* P = sP + buf * S::PB + tok * 16;
                 if (E4M3) {
                     const float unscale = fexp2(-ev);
-                    unsigned char* w = P + (tid & 15);
-                    const int ch = tid >> 4;
+                    uint32_t w[3][RW / 4];   // four rows a word
 #pragma unroll
-                    for (int r = 0; r < RT; r += 2) {
-                        const float e0 = fexp2(z[r] - s_m[r] + S::kBias), e1 = fexp2(z[r + 1] - s_m[r + 1] + S::kBias);
+                    for (int r = 0; r < RW; r += 2) {
+                        const float e0 = fexp2(z[r] - m[r] + S::kBias), e1 = fexp2(z[r + 1] - m[r + 1] + S::kBias);
                         l[r] = fmaf(e0, unscale, l[r]);
                         l[r + 1] = fmaf(e1, unscale, l[r + 1]);
                         __half2 h = __floats2half2_rn(e0, e1);
 #pragma unroll
                         for (int part = 0; part < 3; ++part) {
                             const uint32_t b = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)h, __NV_SATFINITE, __NV_E5M2);
-                            w[part * RT * 128 + swz<128>(r, ch)] = (unsigned char)b;
-                            w[part * RT * 128 + swz<128>(r + 1, ch)] = (unsigned char)(b >> 8);
+                            w[part][r >> 2] = r & 2 ? w[part][r >> 2] | (b << 16) : b;
                             if (part < 2) {
                                 const uint32_t back = __byte_perm(b, 0, 0x1404);   // e5m2 is fp16's upper byte
                                 h = __hsub2(h, *reinterpret_cast<const __half2*>(&back));
                             }
                         }
                     }
-                } else {
-                    unsigned char* w = P + (tid >> 6) * RT * 128 + 2 * (tid & 7);
-                    const int ch = (tid & 63) >> 3;
 #pragma unroll
-                    for (int r = 0; r < RT; r += 2) {
-                        const float e0 = fexp2(z[r] - s_m[r]), e1 = fexp2(z[r + 1] - s_m[r + 1]);
-                        l[r] += e0;
-                        l[r + 1] += e1;
-                        const uint32_t b = pack_bf16(e0, e1);
-                        *reinterpret_cast<uint16_t*>(w + swz<128>(r, ch)) = (uint16_t)b;
-                        *reinterpret_cast<uint16_t*>(w + swz<128>(r + 1, ch)) = (uint16_t)(b >> 16);
+                    for (int part = 0; part < 3; ++part) {
+                        unsigned char* d = P + (part * RT + rw) / 16 * 2048 + rw % 16;
+                        if (RW == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[part][0], w[part][1]);
+                        else
+#pragma unroll
+                            for (int i = 0; i < RW / 16; ++i)
+                                *reinterpret_cast<uint4*>(d + i * 2048) =
+                                    make_uint4(w[part][4 * i], w[part][4 * i + 1], w[part][4 * i + 2], w[part][4 * i + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RW / 8; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 8 * i + 2 * e;
+                            const float e0 = fexp2(z[r] - m[r]), e1 = fexp2(z[r + 1] - m[r + 1]);
+                            l[r] += e0;
+                            l[r + 1] += e1;
+                            w[e] = pack_bf16(e0, e1);
+                        }
+                        *reinterpret_cast<uint4*>(P + (rw / 8 + i) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                if (!whole && !each) {
+                if (!whole) {
                     // a value row that not every row attends: zero it where it would
                     // turn a zero weight into a NaN (all of it where nobody attends
                     // it: the slot may hold anything; else only what is not finite,
                     // which the epilogue adds to the rows that do attend it)
+                    const bool here = ks != 0.f;
+                    const bool any = here && pos <= p_last && (a.c.window == 0 || pos > p_first - a.c.window || pos < a.c.sink);
+                    const bool each = here && pos <= p_first && (a.c.window == 0 || pos > p_last - a.c.window || pos < a.c.sink);
                     const unsigned int v0 = g0 + (k == s.n - 1 ? (2 * s.n - 1) * S::D : (2 * k + 2) * S::D);
                     bool listed = false;
                     for (int d = 0; d < S::D; ++d) {
                         const unsigned int g = v0 + d, sl = g % (unsigned)NS;
                         wait(full + sl, (g / (unsigned)NS) & 1);
+                        if (each) continue;
                         unsigned char* row = ring + (size_t)sl * S::SLOTB;
 #pragma unroll 1
-                        for (int i = 0; i < S::NBOX * S::ROWB / 16; ++i) {
-                            uint4* e = reinterpret_cast<uint4*>(row + (i / (S::ROWB / 16)) * S::BOXB + swz<S::ROWB>(tid, i % (S::ROWB / 16)));
+                        for (int i = wg; i < S::NBOX * S::ROWB / 16; i += 2) {   // the warpgroups take turns
+                            uint4* e = reinterpret_cast<uint4*>(row + (i / (S::ROWB / 16)) * S::BOXB + swz<S::ROWB>(tok, i % (S::ROWB / 16)));
                             if (!any) {
                                 *e = make_uint4(0, 0, 0, 0);
                                 continue;
@@ -661,7 +728,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                             }
                         }
                     }
-                    if (listed) {
+                    if (listed) {   // (both warpgroups may list it: an infinity or NaN added twice is the same)
                         const int i = atomicAdd(&s_nfix, 1);
                         if (i < kTcFix) s_fix[i] = pos;
                     }
@@ -671,61 +738,64 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             }
             // ---- epilogue: the row sums, then the accumulator ----
             const unsigned int last = ti + s.n - 1;
-            wait(pv_done + (last & 1), (last >> 1) & 1);
-            tc_fence_after();
+            wg_sync(wg);   // the last tile's column maxima are read
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int r = 0; r < RW; ++r) {
                 const float v = warp_sum(l[r]);
-                if (lane == 0) s_red[warp * RT + r] = v;
+                if (lane == 0) s_red[w4 * RT + rw + r] = v;
             }
-            softmax_sync();
-            if (tid < RT) {
-                const float v = s_red[tid] + s_red[RT + tid] + s_red[2 * RT + tid] + s_red[3 * RT + tid];
-                if (s.slot >= 0) {
-                    float* part = a.part + s.slot * part_floats(RT, HD);
-                    part[RT * HD + tid] = s_m[tid];
-                    part[RT * (HD + 1) + tid] = v;
-                    s_f[tid] = 1.f;
-                } else {
-                    s_f[tid] = v == 0.f ? 0.f : 1.f / v;
+            both_sync();
+            float* part = s.slot >= 0 ? a.part + s.slot * part_floats(RT, HD) : nullptr;
+#pragma unroll
+            for (int r = 0; r < RW; ++r) {
+                const float* q = s_red + rw + r;
+                const float v = (q[0] + q[RT]) + (q[2 * RT] + q[3 * RT]);
+                l[r] = part ? 1.f : v == 0.f ? 0.f : 1.f / v;
+                if (part && tok == r) {
+                    part[RT * HD + rw + r] = m[r];
+                    part[RT * (HD + 1) + rw + r] = v;
                 }
             }
-            softmax_sync();
             const int nfix = s_nfix < kTcFix ? s_nfix : kTcFix;
+            wait(pv_done + (last & 1), (last >> 1) & 1);
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < S::D * RT; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(my + 2 * RT + c, v);
+            for (int d0 = 0; d0 < S::D; ++d0) {
+                uint32_t v[S::NO][RW];
+#pragma unroll
+                for (int o = 0; o < S::NO; ++o)
+#pragma unroll
+                    for (int i = 0; i < RW; i += 8) tmem_ld8(my + S::O0 + (d0 * S::NO + o) * RT + rw + i, v[o] + i);
                 tmem_ld_wait();
-                const int d = (c / RT) * 128 + tid, rb = c % RT;
-                if (HD < 128 && tid >= HD) continue;
+                const int d = d0 * 128 + tok;
+                if (HD < 128 && tok >= HD) continue;   // whole warps
+                float o[RW];
+#pragma unroll
+                for (int r = 0; r < RW; ++r) {
+                    o[r] = __uint_as_float(v[0][r]);
+                    if (S::NO == 3) o[r] += __uint_as_float(v[1 % S::NO][r]) + __uint_as_float(v[2 % S::NO][r]);
+                }
                 for (int f = 0; f < nfix; ++f) {   // values that are not finite, to the rows that attend them
                     const int t = s_fix[f];
                     const int pg = a.c.table[(long long)s.b * a.c.max_pages + (t >> a.c.ps_log2)];
-                    const long long o = pg * a.c.sp + s.g * a.c.sh + (t & (ps - 1)) * a.c.st + d;
+                    const long long at = pg * a.c.sp + s.g * a.c.sh + (t & (ps - 1)) * a.c.st + d;
                     float val;
-                    if (E4M3) val = (reinterpret_cast<const uint8_t*>(a.c.v)[o] & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f;
-                    else val = bf16_to_f32(reinterpret_cast<const uint16_t*>(a.c.v)[o]);
+                    if (E4M3) val = (reinterpret_cast<const uint8_t*>(a.c.v)[at] & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f;
+                    else val = bf16_to_f32(reinterpret_cast<const uint16_t*>(a.c.v)[at]);
                     if (val - val == 0.f) continue;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (attends(a.c, t, s_pos[rb + i])) v[i] = __float_as_uint(__uint_as_float(v[i]) + val);
+                    for (int r = 0; r < RW; ++r)
+                        if (attends(a.c, t, s_pos[rw + r])) o[r] += val;
                 }
-                if (s.slot >= 0) {
-                    float* part = a.part + s.slot * part_floats(RT, HD);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (rb + i < s.rows) part[(rb + i) * HD + d] = __uint_as_float(v[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (rb + i < s.rows)
-                            reinterpret_cast<uint16_t*>(a.out)[(long long)s_row[rb + i] * HD + d] =
-                                (uint16_t)pack_bf16(__uint_as_float(v[i]) * s_f[rb + i], 0.f);
+                for (int r = 0; r < RW; ++r) {
+                    if (rw + r >= s.rows) break;
+                    if (part) part[(rw + r) * HD + d] = o[r];
+                    else reinterpret_cast<uint16_t*>(a.out)[(long long)s_row[rw + r] * HD + d] = (uint16_t)pack_bf16(o[r] * l[r], 0.f);
                 }
             }
             tc_fence_before();
-            softmax_sync();   // the row tables are rewritten next
+            both_sync();   // the row tables are rewritten next
             ti += s.n;
             g0 += 2 * s.n * S::D;
             x += s.n;
@@ -733,14 +803,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     }
     __syncthreads();
     if (tid == 0) a.cta_status[blockIdx.x] = s_abort ? MTP_ERR_TIMEOUT : s_bad ? MTP_ERR_ARG : MTP_OK;
-    if (warp == 5) tmem_dealloc(tmem, S::COLS);
+    if (warp == 9) tmem_dealloc(tmem, S::COLS);
 }
 
 template <bool E4M3, int HD, int RT>
 cudaError_t go(const PagedTcArgs& p, cudaStream_t s) {
+    static int ready[64] = {0};   // the attribute is set, per device
     const int smem = p.slots * tc_slot_bytes(E4M3, HD) + tc_other(E4M3, HD, RT, p.a.B);
-    const cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<E4M3, HD, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || ready[dev] == 0) {
+        e = cudaFuncSetAttribute(paged_attn_tc_kernel<E4M3, HD, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemLimit);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) ready[dev] = 1;
+    }
     paged_attn_tc_kernel<E4M3, HD, RT><<<p.a.grid, kTcThreads, smem, s>>>(p);
     return cudaGetLastError();
 }

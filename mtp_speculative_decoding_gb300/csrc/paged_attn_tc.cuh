@@ -8,11 +8,11 @@
 
 namespace mtp {
 
-constexpr int kTcTile = 128;          // positions of a tile: the MMA's M side
+constexpr int kTcTileLog2 = 7, kTcTile = 1 << kTcTileLog2;          // positions of a tile: the MMA's M side
 constexpr int kTcSlotsMax = 24;       // ring slots of a CTA at most
 constexpr int kTcMeta = 16;           // tiles of page scales the producer may be ahead
 constexpr int kTcFix = 256;           // positions listed as not finite
-constexpr int kTcSmemLimit = 227 * 1024;
+constexpr int kTcSmemLimit = 227 * 1024 - 64;   // beside the static words
 
 struct PagedTcArgs {
     CUtensorMap tk, tv;               // (dimension, slot, KV head, page) of k and v
@@ -25,8 +25,8 @@ __host__ __device__ constexpr int tc_other(bool e4m3, int hd, int RT, int B) {
     return (e4m3 ? 3 : 2 * 2) * RT * hd                          // Q, in parts
            + 2 * (e4m3 ? 3 * RT * 128 : 2 * RT * 128)            // P, two tiles
            + kTcMeta * 8 * 2 * 4 + kTcMeta * 4                   // page scales
-           + RT * 4 * (4 + 3 + 2) + kTcFix * 4                   // row tables, list
-           + (2 * kTcSlotsMax + kTcMeta + 16) * 8 + 33 * 8 + 64 + (B + 1) * 8 + 1024;
+           + RT * 4 * (4 + 3 + 2) + kTcFix * 4 + hd * 4          // row tables, list, rotation table
+           + (2 * kTcSlotsMax + kTcMeta + 16) * 8 + 33 * 8 + 64 + plan_bytes(B) + 1024;
 }
 __host__ __device__ constexpr int tc_slot_bytes(bool e4m3, int hd) { return kTcTile * (hd < 128 ? hd : 128) * (e4m3 ? 1 : 2); }
 __host__ __device__ constexpr int tc_slots(bool e4m3, int hd, int RT, int B) {
