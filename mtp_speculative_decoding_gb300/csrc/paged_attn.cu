@@ -209,11 +209,10 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
 // merge: a CTA takes one row of one item; an item that one CTA held whole is
 // written already.  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  The
 // parts are spread over the CTA's thread groups (hd / 4 threads each, four
-// dimensions a thread) so that their loads are in flight together: it is bound
-// by the latency of three dependent loads (the schedule, the maxima, the
-// parts).
+// dimensions a thread), eight a turn with all their loads in flight, so it is
+// bound by the latency of two dependent loads: the schedule, then the parts.
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 128, kMergeParts = 512;   // parts whose weights are staged at a time
+constexpr int kMergeThreads = 128, kMergeBatch = 8;
 
 __device__ __forceinline__ void put4(float* p, const float4& x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void put4(uint16_t* p, const float4& x) {
@@ -222,11 +221,11 @@ __device__ __forceinline__ void put4(uint16_t* p, const float4& x) {
 
 template <typename QT>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedAttnArgs a) {
-    __shared__ float s_w[kMergeParts];
     __shared__ float4 s_o[kMergeThreads];
-    __shared__ float s_x[kMergeThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float2 s_ml[kMergeThreads];
+    const int tid = threadIdx.x;
     const int R = a.M * a.G, rr = (int)(blockIdx.x % (unsigned)R), bg = (int)(blockIdx.x / (unsigned)R), g = bg % a.c.Hkv, b = bg / a.c.Hkv;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == gridDim.x - 1) {   // the call's status from the CTAs'
         int bad = 0;
@@ -247,67 +246,77 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     const long long T = a.pre[a.B], p0 = a.pre[b], span = a.pre[b + 1] - p0;
     if (span == 0 || rr >= n * a.G) return;
     const int nrt = row_tiles(a, n);
-    const long long per = span / (a.c.Hkv * nrt);
-    const int rt = rr / a.RT, r = rr % a.RT, hd = a.hd;
+    const unsigned items = (unsigned)a.c.Hkv * nrt;
+    const long long per = span < (1ll << 31) ? (unsigned)span / items : span / items;
+    const int rt = rr / a.RT, r = rr - rt * a.RT, hd = a.hd;
     const long long x0 = p0 + per * (g * nrt + rt);
     const int c0 = share_of(T, x0, a.grid), c1 = share_of(T, x0 + per - 1, a.grid);
     if (c0 == c1) return;
     const long long psz = part_floats(a.RT, hd);
     auto slot = [&](int c) { return a.part + (c == c0 ? 2 * c + 1 : 2 * c) * psz; };
-    float M = -1e30f;
-    for (int c = c0 + tid; c <= c1; c += kMergeThreads) M = fmaxf(M, slot(c)[a.RT * hd + r]);
-    M = warp_max(M);
-    if (lane == 0) s_x[warp] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(s_x[0], s_x[1]), fmaxf(s_x[2], s_x[3]));
-    const int gt = hd >> 2, groups = kMergeThreads / gt > 0 ? kMergeThreads / gt : 1;   // threads of a group, groups
-    const int my = tid / gt, d = 4 * (tid % gt);
-    float l = 0.f;
+    const int gt = hd >> 2, groups = kMergeThreads / gt;   // threads of a group, groups
+    const int my = tid / gt, d = 4 * (tid - my * gt);
+    float M = -1e30f, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int cb = c0; cb <= c1; cb += kMergeParts) {
-        const int cnt = c1 - cb + 1 < kMergeParts ? c1 - cb + 1 : kMergeParts;
-        __syncthreads();
-        for (int k = tid; k < cnt; k += kMergeThreads) {
-            const float* p = slot(cb + k) + a.RT * hd + r;
-            const float w = exp2f(p[0] - M);
-            s_w[k] = w;
-            l = fmaf(w, p[a.RT], l);
+    for (int cb = c0 + my; cb <= c1; cb += kMergeBatch * groups) {
+        float m[kMergeBatch], ls[kMergeBatch];
+        float4 o[kMergeBatch];
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+            const int c = cb + k * groups;
+            m[k] = -1e30f;
+            ls[k] = 0.f;
+            o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c > c1) continue;
+            const float* p = slot(c);
+            m[k] = p[a.RT * hd + r];
+            ls[k] = p[a.RT * (hd + 1) + r];
+            o[k] = *reinterpret_cast<const float4*>(p + r * hd + d);
         }
-        __syncthreads();
-        if (my < groups) {
-#pragma unroll 8
-            for (int k = my; k < cnt; k += groups) {
-                const float w = s_w[k];
-                const float4 o = *reinterpret_cast<const float4*>(slot(cb + k) + r * hd + d);
-                acc.x = fmaf(w, o.x, acc.x);
-                acc.y = fmaf(w, o.y, acc.y);
-                acc.z = fmaf(w, o.z, acc.z);
-                acc.w = fmaf(w, o.w, acc.w);
-            }
+        float nm = M;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) nm = fmaxf(nm, m[k]);
+        const float f = exp2f(M - nm);
+        acc.x *= f;
+        acc.y *= f;
+        acc.z *= f;
+        acc.w *= f;
+        l *= f;
+        M = nm;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+            const float w = exp2f(m[k] - nm);
+            acc.x = fmaf(w, o[k].x, acc.x);
+            acc.y = fmaf(w, o[k].y, acc.y);
+            acc.z = fmaf(w, o[k].z, acc.z);
+            acc.w = fmaf(w, o[k].w, acc.w);
+            l = fmaf(w, ls[k], l);
         }
     }
-    l = warp_sum(l);
-    __syncthreads();
-    if (lane == 0) s_x[warp] = l;
     s_o[tid] = acc;
+    s_ml[tid] = make_float2(M, l);
     __syncthreads();
-    l = s_x[0] + s_x[1] + s_x[2] + s_x[3];
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (tid < gt) {
-        for (int k = 1; k < groups; ++k) {
-            const float4 o = s_o[tid + k * gt];
-            acc.x += o.x;
-            acc.y += o.y;
-            acc.z += o.z;
-            acc.w += o.w;
-        }
-        acc.x *= inv;
-        acc.y *= inv;
-        acc.z *= inv;
-        acc.w *= inv;
-        QT* o = reinterpret_cast<QT*>(a.out) + (((long long)b * a.M + rr / a.G) * a.Hq + g * a.G + rr % a.G) * hd;
-        put4(o + d, acc);
+    if (tid >= gt) return;
+    for (int k = 0; k < groups; ++k) M = fmaxf(M, s_ml[tid + k * gt].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
+    for (int k = 0; k < groups; ++k) {
+        const float2 ml = s_ml[tid + k * gt];
+        const float4 o = s_o[tid + k * gt];
+        const float w = exp2f(ml.x - M);
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+        l = fmaf(w, ml.y, l);
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    acc.x *= inv;
+    acc.y *= inv;
+    acc.z *= inv;
+    acc.w *= inv;
+    QT* o = reinterpret_cast<QT*>(a.out) + (((long long)b * a.M + rr / a.G) * a.Hq + g * a.G + rr % a.G) * hd;
+    put4(o + d, acc);
 }
 
 namespace {

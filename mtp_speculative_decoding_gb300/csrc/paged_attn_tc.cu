@@ -178,10 +178,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     float* s_f = s_m + RT;                                     // [RT] rescale factor
     float* s_c = s_f + RT;                                     // [RT] scale of the query row
     float* s_red = s_c + RT;                                   // [4][RT]
-    int* s_pos = reinterpret_cast<int*>(s_red + 4 * RT);       // [RT] position of the row
-    int* s_row = s_pos + RT;                                   // [RT] output row
-    int* s_fix = s_row + RT;                                   // [kTcFix]
-    int* m_all = s_fix + kTcFix;                               // [kTcMeta] every page of the tile is loaded
+    int* s_pos2 = reinterpret_cast<int*>(s_red + 4 * RT);      // [2][RT] position of the row
+    int* s_row2 = s_pos2 + 2 * RT;                             // [2][RT] output row
+    int* s_fix2 = s_row2 + 2 * RT;                             // [2][kTcFix]
+    int* m_all = s_fix2 + 2 * kTcFix;                          // [kTcMeta] every page of the tile is loaded
     unsigned long long* bars = reinterpret_cast<unsigned long long*>(m_all + kTcMeta);
     unsigned long long *full = bars, *empty = full + kTcSlotsMax, *meta_full = empty + kTcSlotsMax, *s_full = meta_full + kTcMeta,
                        *s_free = s_full + 2, *p_full = s_free + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *end_bar = q_full + 1;
@@ -190,25 +190,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     plan.pre = tmp + 33;
     plan.len = reinterpret_cast<int2*>(plan.pre + a.B + 1);
     __shared__ unsigned int s_tmem;
-    __shared__ int s_nfix, s_bad;
+    __shared__ int s_nfix[2], s_bad;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    // one thread each: the ring's, the scales', and the ten others' counts
+    if (tid < 2 * kTcSlotsMax + kTcMeta) mbar_init(bars + tid, 1);
+    else if (tid < 2 * kTcSlotsMax + kTcMeta + 10) {
+        const int i = tid - (2 * kTcSlotsMax + kTcMeta);   // s_full, s_free, p_full, pv_done (two each), q_full, end_bar
+        mbar_init(bars + tid, i == 2 || i == 3 ? 8 : i == 4 || i == 5 || i == 8 ? 256 : 1);
+    }
+    mbar_fence_init();
     if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
-        }
-        for (int i = 0; i < kTcMeta; ++i) mbar_init(meta_full + i, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full + i, 1);
-            mbar_init(s_free + i, 8);
-            mbar_init(p_full + i, 256);
-            mbar_init(pv_done + i, 1);
-        }
-        mbar_init(q_full, 256);
-        mbar_init(end_bar, 1);
-        mbar_fence_init();
-        s_nfix = 0;
+        s_nfix[0] = s_nfix[1] = 0;
         s_bad = 0;
         s_abort = 0;
     }
@@ -221,6 +214,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             s_hi[i] = a.rope.hi[i];
             s_lo[i] = a.rope.lo[i];
         }
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // what ran before has written its rows
     const bool good = schedule<kTcThreads>(a, plan, tmp);   // meets in CTA barriers
     tc_fence_before();
     __syncthreads();
@@ -440,113 +434,189 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         const int wg = warp >> 2, tok = tid & 127, w4 = warp & 3, rw = wg * RW;
         const uint32_t my = tmem + ((uint32_t)(w4 * 32) << 16);
         unsigned int ti = 0, g0 = 0;   // tiles and ring slots before this segment
+        int par0 = 1;                  // row tables of this segment
         long long x = x0;
-        while (x < xe) {
-            const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
-            const int r0 = s.rt * RT;
-            // ---- queries: norm, rotation, scale, parts ----
-            {
-                constexpr int U = HD / 16, RP = 256 / U;
-                const int c = tid % U;
-#pragma unroll 1
-                for (int rb = 0; rb < RT; rb += RP) {
-                    const int r = rb + tid / U;
-                    if (RP > RT && r >= RT) break;   // whole warps
-                    const bool in = r < s.rows;
-                    float p[8], q[8];
-                    bool fin = true;
-                    float amax = 0.f;
-                    if (__any_sync(0xffffffffu, in)) {
-                        const int j = in ? (r0 + r) / a.G : 0, h = in ? (r0 + r) - j * a.G : 0;
-                        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + s.b * a.sb + j * a.sm + (s.g * a.G + h) * a.sh + 8 * c;
-                        load8(src, p);
-                        load8(src + HD / 2, q);
-                        float cs[8], sn[8];
-                        if (a.rope.on) unit_angles<true>((long long)s.len + j, s_hi + 8 * c, s_lo + 8 * c, cs, sn);
-                        if (a.q_norm) unit_norm(p, q, a.q_norm, c, HD, a.eps);
-                        if (a.rope.on) unit_rotate(p, q, cs, sn);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            p[e] = in ? p[e] * a.scale : 0.f;
-                            q[e] = in ? q[e] * a.scale : 0.f;
-                            amax = fmaxf(amax, fmaxf(fabsf(p[e]), fabsf(q[e])));
-                            fin = fin && p[e] - p[e] == 0.f && q[e] - q[e] == 0.f;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
-                    }
-                    if (E4M3) {
-                        for (int o = U / 2; o > 0; o >>= 1) {
-                            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                            fin = __shfl_xor_sync(0xffffffffu, (int)fin, o) && fin;
-                        }
-                        int k = (int)(__float_as_uint(amax) >> 23) - 127 - 7;   // the largest over 2^k in [128, 256)
-                        if (amax == 0.f || k < -100) k = -100;
-                        if (k > 100) k = 100;
-                        const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
-                        if (c == 0) s_c[r] = fin ? __uint_as_float((uint32_t)(127 + k) << 23) : __uint_as_float(0x7FC00000u);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            p[e] *= inv;
-                            q[e] *= inv;
-                        }
-#pragma unroll
-                        for (int part = 0; part < 3; ++part) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float* v = i < 2 ? p + 4 * i : q + 4 * (i - 2);
-                                uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
-                                uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
-                                w[i] = lo | (hi << 16);
-                                const float2 a0 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)lo, __NV_E4M3)));
-                                const float2 a1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
-                                v[0] -= a0.x;
-                                v[1] -= a0.y;
-                                v[2] -= a1.x;
-                                v[3] -= a1.y;
+        Segment s = {}, nx = {};
+        bool have = false;
+        float l[RW], m[RW], c[RW];
+        // A turn prepares the next segment's queries (its scores' MMAs start
+        // on them), writes this segment's output, and goes through the next
+        // one's tiles.
+        for (;;) {
+            const bool more = x < xe;
+            if (more) {
+                nx = segment_at(a, plan, x, xe, blockIdx.x);
+                const int pn = par0 ^ 1;
+                const int r0 = nx.rt * RT;
+                // ---- queries: norm, rotation, scale, parts ----
+                {
+                    constexpr int U = HD / 16, RP = 256 / U;
+                    const int c = tid % U;
+    #pragma unroll 1
+                    for (int rb = 0; rb < RT; rb += RP) {
+                        const int r = rb + tid / U;
+                        if (RP > RT && r >= RT) break;   // whole warps
+                        const bool in = r < nx.rows;
+                        float p[8], q[8];
+                        bool fin = true;
+                        float amax = 0.f;
+                        if (__any_sync(0xffffffffu, in)) {
+                            const int j = in ? (r0 + r) / a.G : 0, h = in ? (r0 + r) - j * a.G : 0;
+                            const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + nx.b * a.sb + j * a.sm + (nx.g * a.G + h) * a.sh + 8 * c;
+                            load8(src, p);
+                            load8(src + HD / 2, q);
+                            float cs[8], sn[8];
+                            if (a.rope.on) unit_angles<true>((long long)nx.len + j, s_hi + 8 * c, s_lo + 8 * c, cs, sn);
+                            if (a.q_norm) unit_norm(p, q, a.q_norm, c, HD, a.eps);
+                            if (a.rope.on) unit_rotate(p, q, cs, sn);
+    #pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                p[e] = in ? p[e] * a.scale : 0.f;
+                                q[e] = in ? q[e] * a.scale : 0.f;
+                                amax = fmaxf(amax, fmaxf(fabsf(p[e]), fabsf(q[e])));
+                                fin = fin && p[e] - p[e] == 0.f && q[e] - q[e] == 0.f;
                             }
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const int byte = half * (HD / 2) + 8 * c, box = byte / S::ROWB, in_row = byte % S::ROWB;
-                                unsigned char* d = sQ + (box * S::NQ + part) * RT * S::ROWB + swz<S::ROWB>(r, in_row >> 4) + (in_row & 8);
-                                *reinterpret_cast<uint2*>(d) = make_uint2(w[2 * half], w[2 * half + 1]);
-                            }
+                        } else {
+    #pragma unroll
+                            for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
                         }
-                    } else {
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float* v = i < 4 ? p + 2 * i : q + 2 * (i - 4);
-                                w[i] = pack_bf16(v[0], v[1]);
-                                v[0] -= bf16_lo(w[i]);
-                                v[1] -= bf16_hi(w[i]);
+                        if (E4M3) {
+                            for (int o = U / 2; o > 0; o >>= 1) {
+                                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                                fin = __shfl_xor_sync(0xffffffffu, (int)fin, o) && fin;
                             }
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const int byte = half * HD + 16 * c, box = byte / S::ROWB;
-                                *reinterpret_cast<uint4*>(sQ + (box * S::NQ + part) * RT * S::ROWB +
-                                                          swz<S::ROWB>(r, (byte % S::ROWB) >> 4)) =
-                                    make_uint4(w[4 * half], w[4 * half + 1], w[4 * half + 2], w[4 * half + 3]);
+                            int k = (int)(__float_as_uint(amax) >> 23) - 127 - 7;   // the largest over 2^k in [128, 256)
+                            if (amax == 0.f || k < -100) k = -100;
+                            if (k > 100) k = 100;
+                            const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
+                            if (c == 0) s_c[r] = fin ? __uint_as_float((uint32_t)(127 + k) << 23) : __uint_as_float(0x7FC00000u);
+    #pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                p[e] *= inv;
+                                q[e] *= inv;
+                            }
+    #pragma unroll
+                            for (int part = 0; part < 3; ++part) {
+                                uint32_t w[4];
+    #pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    float* v = i < 2 ? p + 4 * i : q + 4 * (i - 2);
+                                    uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+                                    uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+                                    w[i] = lo | (hi << 16);
+                                    const float2 a0 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)lo, __NV_E4M3)));
+                                    const float2 a1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+                                    v[0] -= a0.x;
+                                    v[1] -= a0.y;
+                                    v[2] -= a1.x;
+                                    v[3] -= a1.y;
+                                }
+    #pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    const int byte = half * (HD / 2) + 8 * c, box = byte / S::ROWB, in_row = byte % S::ROWB;
+                                    unsigned char* d = sQ + (box * S::NQ + part) * RT * S::ROWB + swz<S::ROWB>(r, in_row >> 4) + (in_row & 8);
+                                    *reinterpret_cast<uint2*>(d) = make_uint2(w[2 * half], w[2 * half + 1]);
+                                }
+                            }
+                        } else {
+    #pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                uint32_t w[8];
+    #pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    float* v = i < 4 ? p + 2 * i : q + 2 * (i - 4);
+                                    w[i] = pack_bf16(v[0], v[1]);
+                                    v[0] -= bf16_lo(w[i]);
+                                    v[1] -= bf16_hi(w[i]);
+                                }
+    #pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    const int byte = half * HD + 16 * c, box = byte / S::ROWB;
+                                    *reinterpret_cast<uint4*>(sQ + (box * S::NQ + part) * RT * S::ROWB +
+                                                              swz<S::ROWB>(r, (byte % S::ROWB) >> 4)) =
+                                        make_uint4(w[4 * half], w[4 * half + 1], w[4 * half + 2], w[4 * half + 3]);
+                                }
                             }
                         }
                     }
                 }
+                fence_proxy_async_smem();
+                mbar_arrive(q_full);
+                if (tid < RT) {
+                    const int r = tid < nx.rows ? tid : nx.rows - 1;
+                    s_pos2[pn * RT + tid] = nx.len + (r0 + r) / a.G;
+                    s_row2[pn * RT + tid] = (nx.b * a.M + (r0 + r) / a.G) * a.Hq + nx.g * a.G + (r0 + r) % a.G;
+                }
+                if (tid == 0) s_nfix[pn] = 0;
             }
-            fence_proxy_async_smem();
-            mbar_arrive(q_full);
-            const int p_first = s.len + r0 / a.G, p_last = s.len + (r0 + s.rows - 1) / a.G;
-            if (tid < RT) {
-                const int r = tid < s.rows ? tid : s.rows - 1;
-                s_pos[tid] = s.len + (r0 + r) / a.G;
-                s_row[tid] = (s.b * a.M + (r0 + r) / a.G) * a.Hq + s.g * a.G + (r0 + r) % a.G;
+            if (have) {
+                // ---- epilogue: the row sums, then the accumulator ----
+                const unsigned int last = ti - 1;
+                const int pe = par0;
+                wg_sync(wg);   // the last tile's column maxima are read
+#pragma unroll
+                for (int r = 0; r < RW; ++r) {
+                    const float v = warp_sum(l[r]);
+                    if (lane == 0) s_red[w4 * RT + rw + r] = v;
+                }
+                both_sync();
+                float* part = s.slot >= 0 ? a.part + s.slot * part_floats(RT, HD) : nullptr;
+#pragma unroll
+                for (int r = 0; r < RW; ++r) {
+                    const float* q = s_red + rw + r;
+                    const float v = (q[0] + q[RT]) + (q[2 * RT] + q[3 * RT]);
+                    l[r] = part ? 1.f : v == 0.f ? 0.f : 1.f / v;
+                    if (part && tok == r) {
+                        part[RT * HD + rw + r] = m[r];
+                        part[RT * (HD + 1) + rw + r] = v;
+                    }
+                }
+                const int nfix = s_nfix[pe] < kTcFix ? s_nfix[pe] : kTcFix;
+                wait(pv_done + (last & 1), (last >> 1) & 1);
+                tc_fence_after();
+#pragma unroll 1
+                for (int d0 = 0; d0 < S::D; ++d0) {
+                    uint32_t v[S::NO][RW];
+#pragma unroll
+                    for (int o = 0; o < S::NO; ++o)
+#pragma unroll
+                        for (int i = 0; i < RW; i += 8) tmem_ld8(my + S::O0 + (d0 * S::NO + o) * RT + rw + i, v[o] + i);
+                    tmem_ld_wait();
+                    const int d = d0 * 128 + tok;
+                    if (HD < 128 && tok >= HD) continue;   // whole warps
+                    float o[RW];
+#pragma unroll
+                    for (int r = 0; r < RW; ++r) {
+                        o[r] = __uint_as_float(v[0][r]);
+                        if (S::NO == 3) o[r] += __uint_as_float(v[1 % S::NO][r]) + __uint_as_float(v[2 % S::NO][r]);
+                    }
+                    for (int f = 0; f < nfix; ++f) {   // values that are not finite, to the rows that attend them
+                        const int t = s_fix2[pe * kTcFix + f];
+                        const int pg = a.c.table[(long long)s.b * a.c.max_pages + (t >> a.c.ps_log2)];
+                        const long long at = pg * a.c.sp + s.g * a.c.sh + (t & (ps - 1)) * a.c.st + d;
+                        float val;
+                        if (E4M3) val = (reinterpret_cast<const uint8_t*>(a.c.v)[at] & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f;
+                        else val = bf16_to_f32(reinterpret_cast<const uint16_t*>(a.c.v)[at]);
+                        if (val - val == 0.f) continue;
+#pragma unroll
+                        for (int r = 0; r < RW; ++r)
+                            if (attends(a.c, t, s_pos2[pe * RT + rw + r])) o[r] += val;
+                    }
+#pragma unroll
+                    for (int r = 0; r < RW; ++r) {
+                        if (rw + r >= s.rows) break;
+                        if (part) part[(rw + r) * HD + d] = o[r];
+                        else reinterpret_cast<uint16_t*>(a.out)[(long long)s_row2[pe * RT + rw + r] * HD + d] = (uint16_t)pack_bf16(o[r] * l[r], 0.f);
+                    }
+                }
+                tc_fence_before();
             }
-            if (tid == 0) s_nfix = 0;
-            both_sync();
-            float l[RW], m[RW], c[RW];
+            both_sync();   // the next segment's row tables stand; this one's are read
+            if (!more) break;
+            s = nx;
+            have = true;
+            par0 ^= 1;
+            const int p_first = s.len + s.rt * RT / a.G, p_last = s.len + (s.rt * RT + s.rows - 1) / a.G;
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
                 l[r] = 0.f;
@@ -590,7 +660,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     const bool here = ks != 0.f;
 #pragma unroll
                     for (int r = 0; r < RW; ++r)
-                        if (!(here && attends(a.c, pos, s_pos[rw + r]))) z[r] = -__int_as_float(0x7F800000);
+                        if (!(here && attends(a.c, pos, s_pos2[par0 * RT + rw + r]))) z[r] = -__int_as_float(0x7F800000);
                 }
                 bool over = false;
 #pragma unroll
@@ -694,13 +764,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                         wait(full + sl, (g / (unsigned)NS) & 1);
                         if (each) continue;
                         unsigned char* row = ring + (size_t)sl * S::SLOTB;
-#pragma unroll 1
-                        for (int i = wg; i < S::NBOX * S::ROWB / 16; i += 2) {   // the warpgroups take turns
-                            uint4* e = reinterpret_cast<uint4*>(row + (i / (S::ROWB / 16)) * S::BOXB + swz<S::ROWB>(tok, i % (S::ROWB / 16)));
-                            if (!any) {
-                                *e = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
+                        constexpr int CH = S::NBOX * S::ROWB / 16;   // 16-byte chunks of a row: the warpgroups take turns
+                        auto chunk = [&](int i) {
+                            return reinterpret_cast<uint4*>(row + (i / (S::ROWB / 16)) * S::BOXB + swz<S::ROWB>(tok, i % (S::ROWB / 16)));
+                        };
+                        if (!any) {
+#pragma unroll
+                            for (int i = 0; i < CH; i += 2) *chunk(i + wg) = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+#pragma unroll 2
+                        for (int i = wg; i < CH; i += 2) {
+                            uint4* e = chunk(i);
                             uint4 v = *e;
                             uint32_t* q = reinterpret_cast<uint32_t*>(&v);
                             bool hit = false;
@@ -729,73 +804,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                         }
                     }
                     if (listed) {   // (both warpgroups may list it: an infinity or NaN added twice is the same)
-                        const int i = atomicAdd(&s_nfix, 1);
-                        if (i < kTcFix) s_fix[i] = pos;
+                        const int i = atomicAdd(&s_nfix[par0], 1);
+                        if (i < kTcFix) s_fix2[par0 * kTcFix + i] = pos;
                     }
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(p_full + buf);
             }
-            // ---- epilogue: the row sums, then the accumulator ----
-            const unsigned int last = ti + s.n - 1;
-            wg_sync(wg);   // the last tile's column maxima are read
-#pragma unroll
-            for (int r = 0; r < RW; ++r) {
-                const float v = warp_sum(l[r]);
-                if (lane == 0) s_red[w4 * RT + rw + r] = v;
-            }
-            both_sync();
-            float* part = s.slot >= 0 ? a.part + s.slot * part_floats(RT, HD) : nullptr;
-#pragma unroll
-            for (int r = 0; r < RW; ++r) {
-                const float* q = s_red + rw + r;
-                const float v = (q[0] + q[RT]) + (q[2 * RT] + q[3 * RT]);
-                l[r] = part ? 1.f : v == 0.f ? 0.f : 1.f / v;
-                if (part && tok == r) {
-                    part[RT * HD + rw + r] = m[r];
-                    part[RT * (HD + 1) + rw + r] = v;
-                }
-            }
-            const int nfix = s_nfix < kTcFix ? s_nfix : kTcFix;
-            wait(pv_done + (last & 1), (last >> 1) & 1);
-            tc_fence_after();
-#pragma unroll 1
-            for (int d0 = 0; d0 < S::D; ++d0) {
-                uint32_t v[S::NO][RW];
-#pragma unroll
-                for (int o = 0; o < S::NO; ++o)
-#pragma unroll
-                    for (int i = 0; i < RW; i += 8) tmem_ld8(my + S::O0 + (d0 * S::NO + o) * RT + rw + i, v[o] + i);
-                tmem_ld_wait();
-                const int d = d0 * 128 + tok;
-                if (HD < 128 && tok >= HD) continue;   // whole warps
-                float o[RW];
-#pragma unroll
-                for (int r = 0; r < RW; ++r) {
-                    o[r] = __uint_as_float(v[0][r]);
-                    if (S::NO == 3) o[r] += __uint_as_float(v[1 % S::NO][r]) + __uint_as_float(v[2 % S::NO][r]);
-                }
-                for (int f = 0; f < nfix; ++f) {   // values that are not finite, to the rows that attend them
-                    const int t = s_fix[f];
-                    const int pg = a.c.table[(long long)s.b * a.c.max_pages + (t >> a.c.ps_log2)];
-                    const long long at = pg * a.c.sp + s.g * a.c.sh + (t & (ps - 1)) * a.c.st + d;
-                    float val;
-                    if (E4M3) val = (reinterpret_cast<const uint8_t*>(a.c.v)[at] & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f;
-                    else val = bf16_to_f32(reinterpret_cast<const uint16_t*>(a.c.v)[at]);
-                    if (val - val == 0.f) continue;
-#pragma unroll
-                    for (int r = 0; r < RW; ++r)
-                        if (attends(a.c, t, s_pos[rw + r])) o[r] += val;
-                }
-#pragma unroll
-                for (int r = 0; r < RW; ++r) {
-                    if (rw + r >= s.rows) break;
-                    if (part) part[(rw + r) * HD + d] = o[r];
-                    else reinterpret_cast<uint16_t*>(a.out)[(long long)s_row[rw + r] * HD + d] = (uint16_t)pack_bf16(o[r] * l[r], 0.f);
-                }
-            }
-            tc_fence_before();
-            both_sync();   // the row tables are rewritten next
             ti += s.n;
             g0 += 2 * s.n * S::D;
             x += s.n;
@@ -818,8 +833,17 @@ cudaError_t go(const PagedTcArgs& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev] = 1;
     }
-    paged_attn_tc_kernel<E4M3, HD, RT><<<p.a.grid, kTcThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.a.grid);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up while the kernel before it ends
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<E4M3, HD, RT>, p);
 }
 template <bool E4M3, int HD>
 cudaError_t rows(const PagedTcArgs& p, cudaStream_t s) {

@@ -25,7 +25,7 @@ __host__ __device__ constexpr int tc_other(bool e4m3, int hd, int RT, int B) {
     return (e4m3 ? 3 : 2 * 2) * RT * hd                          // Q, in parts
            + 2 * (e4m3 ? 3 * RT * 128 : 2 * RT * 128)            // P, two tiles
            + kTcMeta * 8 * 2 * 4 + kTcMeta * 4                   // page scales
-           + RT * 4 * (4 + 3 + 2) + kTcFix * 4 + hd * 4          // row tables, list, rotation table
+           + RT * 4 * (4 + 3 + 4) + 2 * kTcFix * 4 + hd * 4          // row tables, list, rotation table
            + (2 * kTcSlotsMax + kTcMeta + 16) * 8 + 33 * 8 + 64 + plan_bytes(B) + 1024;
 }
 __host__ __device__ constexpr int tc_slot_bytes(bool e4m3, int hd) { return kTcTile * (hd < 128 ? hd : 128) * (e4m3 ? 1 : 2); }
