@@ -423,7 +423,7 @@ def make_kv_cache(k, v, page_table, k_scale=None, v_scale=None, window: int = 0,
     [n_pages, n_kv_heads] fp32 for an e4m3 cache.  rope_theta 0: keys and
     queries are not rotated (see mtp_kv_cache)."""
     import torch
-    _require_current(k, v, page_table, k_scale, v_scale)
+    _require_cuda(k, v, page_table, k_scale, v_scale)
     if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(-1) != 1:
         raise ValueError("k and v: two [n_pages, n_kv_heads, page_size, head_dim] tensors of one dtype and layout, head_dim contiguous")
     if k.dtype == torch.float8_e4m3fn:
@@ -454,29 +454,52 @@ def kv_workspace_size(cache: KVCache, B: int, M: int, n_q_heads: int) -> int:
     return int(n)
 
 
-def _require_current(*tensors):
-    """The calls launch on the current device: tensors of another one are refused."""
-    import torch
-    _require_cuda(*tensors)
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"a tensor lives on {t.device}, the current device is cuda:{dev}")
+# The three calls below cost the host a few microseconds each, next to kernels
+# that take about as long: what they look up once is kept here.
+class _Runtime:
+    def __init__(self):
+        import torch
+        self.lib = lib()
+        self.device = torch.cuda.current_device if torch.cuda.is_available() else lambda: -2   # (no tensor is on it)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        self.code = {torch.float32: MTP_DTYPE_F32, torch.bfloat16: MTP_DTYPE_BF16}
+        self.f32, self.i32 = torch.float32, torch.int32
 
 
-def _require_lengths(cache, B, *tensors):
-    import torch
-    if B > getattr(cache, "table_rows", B):
-        raise ValueError("more sequences than page_table has rows")
-    for t in tensors:
-        if t is not None and (t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous()):
-            raise ValueError("kv_len and n_new: contiguous int32 [B]")
+_runtime: _Runtime | None = None
 
 
-def _require_gain(hd, gain):
-    import torch
-    if gain is not None and (gain.dtype != torch.float32 or gain.shape != (hd,) or not gain.is_contiguous()):
-        raise ValueError("the norm's gain: contiguous fp32 [head_dim]")
+def _rt() -> _Runtime:
+    global _runtime
+    if _runtime is None:
+        _runtime = _Runtime()
+    return _runtime
+
+
+def _on(dev: int, t, what: str):
+    """The address of t (0 for None), which must live on the current device: the calls launch there."""
+    if t is None:
+        return 0
+    if t.get_device() != dev:
+        raise ValueError(f"{what} lives on {t.device}, the current device is cuda:{dev}" if t.is_cuda else
+                         "every tensor argument must live on the CUDA device")
+    return t.data_ptr()
+
+
+def _plain(dev: int, t, dtype, shape, what: str):
+    """_on() for a contiguous tensor of this dtype and shape (None passes)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} {list(shape)}")
+    return _on(dev, t, what)
+
+
+def _code(rt: _Runtime, t, what: str) -> int:
+    c = rt.code.get(t.dtype)
+    if c is None:
+        raise ValueError(f"{what}: unsupported dtype {t.dtype}")
+    return c
 
 
 def kv_append(cache: KVCache, k_new, v_new, kv_len, ws, n_new=None, k_norm=None, rms_eps: float = 1e-6,
@@ -484,18 +507,23 @@ def kv_append(cache: KVCache, k_new, v_new, kv_len, ws, n_new=None, k_norm=None,
     """Launch mtp_kv_append on the current stream: rows k_new, v_new [B, M,
     n_kv_heads, head_dim] (fp32 or bf16, one layout, head_dim contiguous) to
     positions kv_len[b] + j, j < n_new[b] (all M without n_new)."""
-    _require_current(k_new, v_new, kv_len, ws, n_new, k_norm)
-    B, M, hkv, hd = k_new.shape
-    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype or v_new.stride() != k_new.stride() or k_new.stride(3) != 1:
+    rt = _runtime or _rt()
+    dev = rt.device()
+    shape, strides = k_new.shape, k_new.stride()
+    if len(shape) != 4 or v_new.shape != shape or v_new.dtype != k_new.dtype or v_new.stride() != strides or strides[3] != 1:
         raise ValueError("k_new and v_new: two [B, M, n_kv_heads, head_dim] tensors of one dtype and layout, head_dim contiguous")
+    B, M, hkv, hd = shape
     if hkv != cache.n_kv_heads or hd != cache.head_dim:
         raise ValueError("the rows' heads are not the cache's")
-    _require_lengths(cache, B, kv_len, n_new)
-    _require_gain(hd, k_norm)
-    sb, sm, sh, _ = k_new.stride()
-    rc = lib().mtp_kv_append(C.byref(cache), B, M, _ptr(kv_len), _ptr(n_new), _ptr(k_new), _ptr(v_new),
-                             _dtype_code(k_new), sb, sm, sh, _ptr(k_norm), rms_eps, _ptr(ws), ws.numel(), _stream(stream))
-    _check(rc, "mtp_kv_append")
+    if B > getattr(cache, "table_rows", B):
+        raise ValueError("more sequences than page_table has rows")
+    rc = rt.lib.mtp_kv_append(C.byref(cache), B, M, _plain(dev, kv_len, rt.i32, (B,), "kv_len"),
+                              _plain(dev, n_new, rt.i32, (B,), "n_new"), _on(dev, k_new, "k_new"), _on(dev, v_new, "v_new"),
+                              _code(rt, k_new, "k_new"), strides[0], strides[1], strides[2],
+                              _plain(dev, k_norm, rt.f32, (hd,), "k_norm"), rms_eps, _on(dev, ws, "ws"), ws.numel(),
+                              rt.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise MTPError(rc, "mtp_kv_append")
 
 
 def paged_attention(cache: KVCache, q, kv_len, out, ws, n_new=None, q_norm=None, rms_eps: float = 1e-6,
@@ -504,19 +532,21 @@ def paged_attention(cache: KVCache, q, kv_len, out, ws, n_new=None, q_norm=None,
     n_q_heads, head_dim] (fp32 or bf16, head_dim contiguous) at positions
     kv_len[b] + j attend the cache, which holds their keys and values already;
     out [B, M, n_q_heads, head_dim] contiguous in q's dtype."""
-    _require_current(q, kv_len, out, ws, n_new, q_norm)
-    B, M, hq, hd = q.shape
-    if hd != cache.head_dim or q.stride(3) != 1:
+    rt = _runtime or _rt()
+    dev = rt.device()
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 4 or shape[3] != cache.head_dim or strides[3] != 1:
         raise ValueError("q: [B, M, n_q_heads, head_dim] with the cache's head_dim, contiguous")
-    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("out: contiguous, of q's shape and dtype")
-    _require_lengths(cache, B, kv_len, n_new)
-    _require_gain(hd, q_norm)
-    sb, sm, sh, _ = q.stride()
-    rc = lib().mtp_paged_attention(C.byref(cache), B, M, hq, _ptr(kv_len), _ptr(n_new), _ptr(q), _dtype_code(q), sb, sm, sh,
-                                   _ptr(q_norm), rms_eps, 0.0 if attn_scale is None else attn_scale, _ptr(out), _ptr(ws),
-                                   ws.numel(), _stream(stream))
-    _check(rc, "mtp_paged_attention")
+    B, M, hq, hd = shape
+    if B > getattr(cache, "table_rows", B):
+        raise ValueError("more sequences than page_table has rows")
+    rc = rt.lib.mtp_paged_attention(C.byref(cache), B, M, hq, _plain(dev, kv_len, rt.i32, (B,), "kv_len"),
+                                    _plain(dev, n_new, rt.i32, (B,), "n_new"), _on(dev, q, "q"), _code(rt, q, "q"),
+                                    strides[0], strides[1], strides[2], _plain(dev, q_norm, rt.f32, (hd,), "q_norm"), rms_eps,
+                                    0.0 if attn_scale is None else attn_scale, _plain(dev, out, q.dtype, shape, "out"),
+                                    _on(dev, ws, "ws"), ws.numel(), rt.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise MTPError(rc, "mtp_paged_attention")
 
 
 def token_logprobs(logits, tokens, out_logprob, out_entropy=None, out_top_ids=None, out_top_logprobs=None,
@@ -526,26 +556,25 @@ def token_logprobs(logits, tokens, out_logprob, out_entropy=None, out_top_ids=No
     out_tokens: rows of token -1 are skipped) or None; out_logprob and
     out_entropy fp32 with the rows' shape, out_top_ids int32 and
     out_top_logprobs fp32 with the rows' shape and one more axis of top_k."""
-    import torch
-    _require_current(logits, tokens, out_logprob, out_entropy, out_top_ids, out_top_logprobs)
+    rt = _runtime or _rt()
+    dev = rt.device()
     lead, V = logits.shape[:-1], logits.shape[-1]
     if logits.stride(-1) != 1 and V > 1:
         raise ValueError("logits: the vocabulary axis must be contiguous")
     z = logits if logits.dim() == 2 else logits.view(-1, V)   # raises where the rows have no single stride
     rows = z.shape[0]
-    for t, dt in ((tokens, torch.int32), (out_logprob, torch.float32), (out_entropy, torch.float32)):
-        if t is not None and (t.dtype != dt or t.shape != lead or not t.is_contiguous()):
-            raise ValueError("tokens (int32), out_logprob and out_entropy (fp32): contiguous, of the rows' shape")
-    top = 0
-    for t, dt in ((out_top_ids, torch.int32), (out_top_logprobs, torch.float32)):
-        if t is not None:
-            if t.dtype != dt or t.shape[:-1] != lead or not t.is_contiguous() or (top and t.shape[-1] != top):
-                raise ValueError("out_top_ids (int32) and out_top_logprobs (fp32): contiguous, the rows' shape and top_k")
-            top = t.shape[-1]
-    rc = lib().mtp_token_logprobs(_ptr(z), _dtype_code(z), rows, V, z.stride(0) if rows > 1 else V, _ptr(tokens), top,
-                                  _ptr(out_logprob), _ptr(out_entropy), _ptr(out_top_ids), _ptr(out_top_logprobs),
-                                  _stream(stream))
-    _check(rc, "mtp_token_logprobs")
+    top = out_top_ids if out_top_ids is not None else out_top_logprobs
+    K = 0 if top is None else top.shape[-1]
+    rc = rt.lib.mtp_token_logprobs(_on(dev, z, "logits"), _code(rt, z, "logits"), rows, V, z.stride(0) if rows > 1 else V,
+                                   _plain(dev, tokens, rt.i32, lead, "tokens"), K,
+                                   _plain(dev, out_logprob, rt.f32, lead, "out_logprob"),
+                                   _plain(dev, out_entropy, rt.f32, lead, "out_entropy"),
+                                   out_top_ids is not None and _plain(dev, out_top_ids, rt.i32, (*lead, K), "out_top_ids") or 0,
+                                   out_top_logprobs is not None and _plain(dev, out_top_logprobs, rt.f32, (*lead, K),
+                                                                           "out_top_logprobs") or 0,
+                                   rt.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise MTPError(rc, "mtp_token_logprobs")
 
 
 def last_error(ws, stream=None) -> int:

@@ -169,9 +169,10 @@ struct PagedAttnArgs {
     void* out;
     WsHeader* hdr;
     int* cta_status;           // [grid]: MTP_OK or an error, written by every CTA
-    long long* pre;            // [B + 1]: tiles before a sequence, written by CTA 0 for the merge
+    int4* split;               // [grid]: the item that begins in CTA c's share and ends in another's, written by every
+                               // CTA for the merge: sequence, KV head, first row | rows << 16, last CTA (-1: none)
     float* part;               // [2 grid] slots of RT * (hd + 2) floats
-    int RT, tile_log2, grid;
+    int RT, rt_log2, tile_log2, grid;
     unsigned long long timeout_ns;
     RopeTab rope;
 };
@@ -200,7 +201,7 @@ __device__ __forceinline__ bool attends(const PagedKV& c, int t, int p) {
 }
 
 // row tiles that hold rows of a sequence with n new ones
-__device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int n) { return (n * a.G + a.RT - 1) / a.RT; }
+__device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int n) { return (n * a.G + a.RT - 1) >> a.rt_log2; }
 
 // What a CTA keeps of the call's sequences in shared memory.
 struct Plan {
@@ -253,14 +254,23 @@ __device__ __forceinline__ bool schedule(const PagedAttnArgs& a, const Plan& pla
 // first tile of CTA c's share, and the CTA whose share holds tile x.  With
 // fewer tiles than CTAs the first T CTAs take one each (no share between two
 // others is empty, so the merge reads written slots only).
+// a / b; small numbers by one approximate division and a correction (an
+// integer division is some 20 dependent instructions)
+__device__ __forceinline__ unsigned udiv(unsigned a, unsigned b) {
+    if (a >= 1u << 20) return a / b;
+    unsigned q = (unsigned)__fdividef((float)a, (float)b);   // off by one at most
+    const int r = (int)(a - q * b);
+    q += r < 0 ? -1 : r >= (int)b ? 1 : 0;
+    return q;
+}
 __device__ __forceinline__ long long share_lo(long long T, int c, int grid) {
     if (T < grid) return c < T ? c : T;
-    if (T < (1ll << 31) / (grid + 1)) return (unsigned)((unsigned)T * (unsigned)c) / (unsigned)grid;   // (a 64-bit division is slow)
+    if (T < (1ll << 31) / (grid + 1)) return udiv((unsigned)T * (unsigned)c, (unsigned)grid);   // (a 64-bit division is slower still)
     return T * c / grid;
 }
 __device__ __forceinline__ int share_of(long long T, long long x, int grid) {
     if (T < grid) return (int)x;
-    if (T < (1ll << 31) / (grid + 1)) return (int)(((unsigned)(x + 1) * (unsigned)grid - 1u) / (unsigned)T);
+    if (T < (1ll << 31) / (grid + 1)) return (int)udiv((unsigned)(x + 1) * (unsigned)grid - 1u, (unsigned)T);
     return (int)(((x + 1) * grid - 1) / T);
 }
 
@@ -286,10 +296,10 @@ __device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const Plan
     s.n_new = l.y;
     s.map = tile_map(a, l.x, l.y);
     const long long rel = x - plan.pre[b];
-    const unsigned item = rel < (1ll << 31) ? (unsigned)rel / (unsigned)s.map.n : (unsigned)(rel / s.map.n);
+    const unsigned item = rel < (1ll << 31) ? udiv((unsigned)rel, (unsigned)s.map.n) : (unsigned)(rel / s.map.n);
     s.t0 = (int)(rel - (long long)item * s.map.n);
     const unsigned nrt = (unsigned)row_tiles(a, l.y);
-    s.g = (int)(item / nrt);
+    s.g = (int)udiv(item, nrt);
     s.rt = (int)(item - s.g * nrt);
     const long long left = xe - x;
     s.n = s.map.n - s.t0 < left ? s.map.n - s.t0 : (int)left;
@@ -297,6 +307,11 @@ __device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const Plan
     s.rows = R < a.RT ? R : a.RT;
     s.slot = s.t0 > 0 ? 2 * c : (s.n < s.map.n ? 2 * c + 1 : -1);
     return s;
+}
+
+// what CTA c leaves in a.split for an item that begins in its share at tile x
+__device__ __forceinline__ int4 split_record(const PagedAttnArgs& a, const Segment& s, long long T, long long x) {
+    return make_int4(s.b, s.g, s.rt * a.RT | s.rows << 16, share_of(T, x + s.map.n - 1, a.grid));
 }
 
 // floats of one partial slot

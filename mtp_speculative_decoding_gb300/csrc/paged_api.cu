@@ -110,9 +110,9 @@ bool encode_pages(CUtensorMap* m, const void* base, const mtp_kv_cache* c) {
 struct AttnPlan {
     bool tc;
     int RT, tile_log2, grid;
-    size_t status, pre, part, end;
+    size_t status, split, part, end;
 };
-AttnPlan attn_plan(const mtp_kv_cache* c, int B, int M, int n_q_heads, bool tc, int sms) {
+AttnPlan attn_plan(const mtp_kv_cache* c, int M, int n_q_heads, bool tc, int sms) {
     AttnPlan p;
     p.tc = tc;
     p.RT = tc ? tc_rows(M * (n_q_heads / c->n_kv_heads), c->head_dim) : kCcRows;
@@ -120,7 +120,7 @@ AttnPlan attn_plan(const mtp_kv_cache* c, int B, int M, int n_q_heads, bool tc, 
     p.grid = tc ? sms : 2 * sms;
     size_t off = sizeof(WsHeader);
     p.status = off; off = al256(off + (size_t)p.grid * sizeof(int));
-    p.pre = off;    off = al256(off + ((size_t)B + 1) * sizeof(long long));
+    p.split = off;  off = al256(off + (size_t)p.grid * sizeof(int4));
     p.part = off;   off = al256(off + 2 * (size_t)p.grid * part_floats(p.RT, c->head_dim) * sizeof(float));
     p.end = off;
     return p;
@@ -142,7 +142,7 @@ size_t mtp_kv_workspace_size(const mtp_kv_cache* c, int B, int M, int n_q_heads)
     int sms = num_sms();
     if (sms <= 0) sms = 152;   // no device (a host-side size query)
     if (M > MTP_MAX_ATTN_ROWS) M = MTP_MAX_ATTN_ROWS;
-    const size_t cc = attn_plan(c, B, M, n_q_heads, false, sms).end, tc = attn_plan(c, B, M, n_q_heads, true, sms).end;
+    const size_t cc = attn_plan(c, M, n_q_heads, false, sms).end, tc = attn_plan(c, M, n_q_heads, true, sms).end;
     return cc > tc ? cc : tc;
 }
 
@@ -189,7 +189,7 @@ int mtp_paged_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, cons
     if (!out || misaligned(out, 16)) return MTP_ERR_ARG;
     const int sms = num_sms();
     if (sms <= 0) return MTP_ERR_CUDA;
-    const AttnPlan p = attn_plan(c, B, M, n_q_heads, tc_path(c, dtype), sms);
+    const AttnPlan p = attn_plan(c, M, n_q_heads, tc_path(c, dtype), sms);
     if (!ws || misaligned(ws, 256) || ws_bytes < p.end) return MTP_ERR_WORKSPACE;
     char* base = static_cast<char*>(ws);
     PagedTcArgs t;
@@ -203,9 +203,11 @@ int mtp_paged_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, cons
     a.out = out;
     a.hdr = static_cast<WsHeader*>(ws);
     a.cta_status = reinterpret_cast<int*>(base + p.status);
-    a.pre = reinterpret_cast<long long*>(base + p.pre);
+    a.split = reinterpret_cast<int4*>(base + p.split);
     a.part = reinterpret_cast<float*>(base + p.part);
-    a.RT = p.RT; a.tile_log2 = p.tile_log2; a.grid = p.grid;
+    a.RT = p.RT; a.rt_log2 = 0;
+    while ((1 << a.rt_log2) < p.RT) ++a.rt_log2;
+    a.tile_log2 = p.tile_log2; a.grid = p.grid;
     a.timeout_ns = kWaitLimitNs;
     fill_rope(&a.rope, c->rope_theta, c->head_dim);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

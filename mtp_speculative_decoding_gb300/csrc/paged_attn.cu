@@ -45,8 +45,7 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
     __shared__ float sks[kCcTile], svs[kCcTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     bool bad = !schedule<kCcThreads>(a, plan, tmp) && blockIdx.x == 0;
-    if (blockIdx.x == 0)
-        for (int b = tid; b <= a.B; b += kCcThreads) a.pre[b] = plan.pre[b];
+    int4 split = make_int4(0, 0, 0, -1);
     const long long T = plan.pre[a.B];
     long long x = share_lo(T, blockIdx.x, a.grid);
     const long long xe = share_lo(T, blockIdx.x + 1, a.grid);
@@ -54,6 +53,7 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
     while (x < xe) {
         const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
         const int r0 = s.rt * a.RT;
+        if (s.slot >= 0 && s.t0 == 0) split = split_record(a, s, T, x);
         // queries: norm, rotation, scale
         for (int i0 = 0; i0 < kCcRows * U; i0 += kCcThreads) {
             const int i = i0 + tid, r = i / U, c = i % U;
@@ -202,15 +202,19 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
         x += s.n;
     }
     const int any = __syncthreads_or(bad);
-    if (tid == 0) a.cta_status[blockIdx.x] = any ? MTP_ERR_ARG : MTP_OK;
+    if (tid == 0) {
+        a.cta_status[blockIdx.x] = any ? MTP_ERR_ARG : MTP_OK;
+        a.split[blockIdx.x] = split;
+    }
 }
 
 // ---------------------------------------------------------------------------
-// merge: a CTA takes one row of one item; an item that one CTA held whole is
-// written already.  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  The
+// merge: a CTA takes one row of an item that begins in CTA c0's share of the
+// attention and ends in another's (an item that one CTA held whole is written
+// already).  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  The
 // parts are spread over the CTA's thread groups (hd / 4 threads each, four
 // dimensions a thread), eight a turn with all their loads in flight, so it is
-// bound by the latency of two dependent loads: the schedule, then the parts.
+// bound by the latency of two dependent loads: the item, then its parts.
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 128, kMergeBatch = 8;
 
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     __shared__ float4 s_o[kMergeThreads];
     __shared__ float2 s_ml[kMergeThreads];
     const int tid = threadIdx.x;
-    const int R = a.M * a.G, rr = (int)(blockIdx.x % (unsigned)R), bg = (int)(blockIdx.x / (unsigned)R), g = bg % a.c.Hkv, b = bg / a.c.Hkv;
+    const int c0 = (int)blockIdx.x >> a.rt_log2, r = (int)blockIdx.x & (a.RT - 1), hd = a.hd;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == gridDim.x - 1) {   // the call's status from the CTAs'
@@ -242,16 +246,9 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         }
         return;
     }
-    const int n = a.n_new ? a.n_new[b] : a.M;
-    const long long T = a.pre[a.B], p0 = a.pre[b], span = a.pre[b + 1] - p0;
-    if (span == 0 || rr >= n * a.G) return;
-    const int nrt = row_tiles(a, n);
-    const unsigned items = (unsigned)a.c.Hkv * nrt;
-    const long long per = span < (1ll << 31) ? (unsigned)span / items : span / items;
-    const int rt = rr / a.RT, r = rr - rt * a.RT, hd = a.hd;
-    const long long x0 = p0 + per * (g * nrt + rt);
-    const int c0 = share_of(T, x0, a.grid), c1 = share_of(T, x0 + per - 1, a.grid);
-    if (c0 == c1) return;
+    const int4 it = a.split[c0];
+    const int c1 = it.w;
+    if (c1 < 0 || r >= it.z >> 16) return;
     const long long psz = part_floats(a.RT, hd);
     auto slot = [&](int c) { return a.part + (c == c0 ? 2 * c + 1 : 2 * c) * psz; };
     const int gt = hd >> 2, groups = kMergeThreads / gt;   // threads of a group, groups
@@ -315,7 +312,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     acc.y *= inv;
     acc.z *= inv;
     acc.w *= inv;
-    QT* o = reinterpret_cast<QT*>(a.out) + (((long long)b * a.M + rr / a.G) * a.Hq + g * a.G + rr % a.G) * hd;
+    const int rr = (it.z & 0xFFFF) + r, j = (int)udiv((unsigned)rr, (unsigned)a.G);
+    QT* o = reinterpret_cast<QT*>(a.out) + (((long long)it.x * a.M + j) * a.Hq + it.y * a.G + rr - j * a.G) * hd;
     put4(o + d, acc);
 }
 
@@ -346,7 +344,7 @@ cudaError_t launch_paged_attn_cc(const PagedAttnArgs& a, int dtype, int kv_dtype
 
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.B * a.c.Hkv * a.M * a.G + 1);
+    cfg.gridDim = dim3((unsigned)a.grid * a.RT + 1);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];

@@ -220,10 +220,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-    if (blockIdx.x == 0) {
-        for (int b = tid; b <= a.B; b += kTcThreads) a.pre[b] = plan.pre[b];
-        if (!good) s_bad = 1;
-    }
+    if (blockIdx.x == 0 && !good) s_bad = 1;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long T = plan.pre[a.B];
     const long long x0 = share_lo(T, blockIdx.x, a.grid), xe = share_lo(T, blockIdx.x + 1, a.grid);
@@ -438,6 +435,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         long long x = x0;
         Segment s = {}, nx = {};
         bool have = false;
+        int4 split = make_int4(0, 0, 0, -1);
         float l[RW], m[RW], c[RW];
         // A turn prepares the next segment's queries (its scores' MMAs start
         // on them), writes this segment's output, and goes through the next
@@ -446,6 +444,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             const bool more = x < xe;
             if (more) {
                 nx = segment_at(a, plan, x, xe, blockIdx.x);
+                if (nx.slot >= 0 && nx.t0 == 0) split = split_record(a, nx, T, x);
                 const int pn = par0 ^ 1;
                 const int r0 = nx.rt * RT;
                 // ---- queries: norm, rotation, scale, parts ----
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                         bool fin = true;
                         float amax = 0.f;
                         if (__any_sync(0xffffffffu, in)) {
-                            const int j = in ? (r0 + r) / a.G : 0, h = in ? (r0 + r) - j * a.G : 0;
+                            const int j = in ? (int)udiv((unsigned)(r0 + r), (unsigned)a.G) : 0, h = in ? (r0 + r) - j * a.G : 0;
                             const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + nx.b * a.sb + j * a.sm + (nx.g * a.G + h) * a.sh + 8 * c;
                             load8(src, p);
                             load8(src + HD / 2, q);
@@ -544,8 +543,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 mbar_arrive(q_full);
                 if (tid < RT) {
                     const int r = tid < nx.rows ? tid : nx.rows - 1;
-                    s_pos2[pn * RT + tid] = nx.len + (r0 + r) / a.G;
-                    s_row2[pn * RT + tid] = (nx.b * a.M + (r0 + r) / a.G) * a.Hq + nx.g * a.G + (r0 + r) % a.G;
+                    const int j = (int)udiv((unsigned)(r0 + r), (unsigned)a.G);
+                    s_pos2[pn * RT + tid] = nx.len + j;
+                    s_row2[pn * RT + tid] = (nx.b * a.M + j) * a.Hq + nx.g * a.G + r0 + r - j * a.G;
                 }
                 if (tid == 0) s_nfix[pn] = 0;
             }
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             s = nx;
             have = true;
             par0 ^= 1;
-            const int p_first = s.len + s.rt * RT / a.G, p_last = s.len + (s.rt * RT + s.rows - 1) / a.G;
+            const int p_first = s_pos2[par0 * RT], p_last = s_pos2[par0 * RT + RT - 1];
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
                 l[r] = 0.f;
@@ -815,6 +815,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             g0 += 2 * s.n * S::D;
             x += s.n;
         }
+        if (tid == 0) a.split[blockIdx.x] = split;
     }
     __syncthreads();
     if (tid == 0) a.cta_status[blockIdx.x] = s_abort ? MTP_ERR_TIMEOUT : s_bad ? MTP_ERR_ARG : MTP_OK;
