@@ -42,9 +42,20 @@ __device__ void append_status(const AppendArgs& a) {
 // ---------------------------------------------------------------------------
 template <typename IT, typename CT>
 __global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+    __shared__ __align__(16) float s_hi[256], s_lo[256], s_gain[512];
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y == 0) append_status(a);
         return;
+    }
+    if (blockIdx.y == 0) {   // keys: lanes read the tables at different places, which parameters serve one by one
+        if (a.rope.on)
+            for (int i = threadIdx.x; i < a.hd >> 1; i += blockDim.x) {
+                s_hi[i] = a.rope.hi[i];
+                s_lo[i] = a.rope.lo[i];
+            }
+        if (a.k_norm)
+            for (int i = threadIdx.x; i < a.hd; i += blockDim.x) s_gain[i] = a.k_norm[i];
+        __syncthreads();
     }
     const int U = a.hd >> 4, groups = a.c.Hkv / a.hpt;
     const long long total = (long long)a.B * a.M * groups * U;
@@ -69,13 +80,13 @@ __global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant_
     if (!__any_sync(0xffffffffu, dst != nullptr)) return;
     float cs[8], sn[8];
     const bool rot = key && a.rope.on;
-    if (rot) unit_angles<false>(live ? pos : 0, a.rope.hi + 8 * c, a.rope.lo + 8 * c, cs, sn);
+    if (rot) unit_angles<false>(live ? pos : 0, s_hi + 8 * c, s_lo + 8 * c, cs, sn);
 #pragma unroll 4
     for (int h = 0; h < a.hpt; ++h) {
         float p[8], q[8];
         load8(src + h * a.sh, p);
         load8(src + h * a.sh + (a.hd >> 1), q);
-        if (key && a.k_norm) unit_norm(p, q, a.k_norm, c, a.hd, a.eps);
+        if (key && a.k_norm) unit_norm_staged(p, q, s_gain, c, a.hd, a.eps);
         if (rot) unit_rotate(p, q, cs, sn);
         if (dst) {
             store8(dst + h * a.c.sh, p);
@@ -113,104 +124,251 @@ __device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8], float inv) {
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// UPT: units of a thread that stay in registers between the maximum and the
-// rounding; a page whose new rows need more is read twice (the second time
-// from L2)
-template <typename IT, int UPT>
-__global__ void __launch_bounds__(512) append_e4m3_kernel(const __grid_constant__ AppendArgs a) {
+// The page's older codes, re-rounded to a scale that grew by 1/f.
+__device__ __forceinline__ void reround(uint8_t* dst, long long st, int off, int ulog, float f) {
+    for (int x = threadIdx.x; x < off << ulog; x += blockDim.x) {
+        uint4* d = reinterpret_cast<uint4*>(dst + (x >> ulog) * st + 16 * (x & ((1 << ulog) - 1)));
+        uint4 w = *d;
+        uint32_t* ws = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t r = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(ws[i] >> (16 * h)), __NV_E4M3);
+                float2 y = __half22float2(__half2(v));
+                y.x *= f;
+                y.y *= f;
+                r |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * h);
+            }
+            ws[i] = r;
+        }
+        *d = w;
+    }
+}
+
+// Where the new rows of a (sequence, touched page) lie; false: nothing to do.
+struct PageRows {
+    int b, len, j0, j1, page, off;   // rows [j0, j1), slots [0, off) are the sequence's already
+    long long first;                 // position of the page's slot 0
+};
+__device__ __forceinline__ bool page_rows(const AppendArgs& a, int nt, PageRows& r) {
+    const int ps = 1 << a.c.ps_log2, it = blockIdx.x % nt;
+    r.b = blockIdx.x / nt;
+    r.len = a.kv_len[r.b];
+    const int n = a.n_new ? a.n_new[r.b] : a.M;
+    if (!seq_ok(r.len, n, a.M, a.c)) return false;
+    const int pi = (r.len >> a.c.ps_log2) + it;
+    r.first = (long long)pi << a.c.ps_log2;
+    r.j0 = it == 0 ? 0 : (int)(r.first - r.len);
+    r.j1 = r.first + ps - r.len < n ? (int)(r.first + ps - r.len) : n;
+    if (r.j0 >= r.j1) return false;
+    r.page = a.c.table[(long long)r.b * a.c.max_pages + pi];
+    r.off = (int)(r.len + r.j0 - r.first);
+    return (unsigned)r.page < (unsigned)a.c.n_pages;
+}
+
+// Few rows a page (decoding): a CTA takes one KV head; every thread's one unit
+// stays in registers between the maximum and the rounding.
+template <typename IT>
+__global__ void __launch_bounds__(256) append_e4m3_kernel(const __grid_constant__ AppendArgs a) {
     const int ps = 1 << a.c.ps_log2, nt = (a.M + ps - 2) / ps + 1;
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y == 0 && blockIdx.z == 0) append_status(a);
         return;
     }
-    __shared__ float red[16];
-    const int b = blockIdx.x / nt, it = blockIdx.x % nt, g = blockIdx.y;
+    __shared__ float red[8];
+    PageRows w;
+    if (!page_rows(a, nt, w)) return;
+    const int g = blockIdx.y;
     const bool key = blockIdx.z == 0;
-    const int len = a.kv_len[b], n = a.n_new ? a.n_new[b] : a.M;
-    if (!seq_ok(len, n, a.M, a.c)) return;
-    const int pi = (len >> a.c.ps_log2) + it;
-    const long long first = (long long)pi << a.c.ps_log2;                     // position of the page's slot 0
-    const int j0 = it == 0 ? 0 : (int)(first - len);
-    const int j1 = first + ps - len < n ? (int)(first + ps - len) : n;
-    if (j0 >= j1) return;
-    const int page = a.c.table[(long long)b * a.c.max_pages + pi];
-    if ((unsigned)page >= (unsigned)a.c.n_pages) return;
-    const int off = (int)(len + j0 - first);                                   // slots the page holds already
-    float* sc = (key ? a.c.ks : a.c.vs) + (long long)page * a.c.Hkv + g;
-    const float had = off > 0 ? *sc : 0.f;
-    const int U = a.hd >> 4, ulog = 31 - __clz(U), units = (j1 - j0) << ulog;
-    const int step = (int)blockDim.x * UPT;
-    const IT* src = reinterpret_cast<const IT*>(key ? a.k : a.v) + b * a.sb + g * a.sh;
-    uint8_t* dst = reinterpret_cast<uint8_t*>(key ? a.c.k : a.c.v) + page * a.c.sp + g * a.c.sh;
-    float p[UPT][8], q[UPT][8];
-    auto fetch = [&](int base) {
+    float* sc = (key ? a.c.ks : a.c.vs) + (long long)w.page * a.c.Hkv + g;
+    const float had = w.off > 0 ? *sc : 0.f;
+    const int U = a.hd >> 4, ulog = 31 - __clz(U), units = (w.j1 - w.j0) << ulog;
+    const IT* src = reinterpret_cast<const IT*>(key ? a.k : a.v) + w.b * a.sb + g * a.sh;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(key ? a.c.k : a.c.v) + w.page * a.c.sp + g * a.c.sh;
+    const int x = threadIdx.x, c = x & (U - 1), j = w.j0 + (x < units ? x >> ulog : 0);
+    float p[8], q[8];
+    load8(src + j * a.sm + 8 * c, p);
+    load8(src + j * a.sm + 8 * c + (a.hd >> 1), q);
+    if (key && a.rope.on) {
+        float cs[8], sn[8];
+        unit_angles<false>((long long)w.len + j, a.rope.hi + 8 * c, a.rope.lo + 8 * c, cs, sn);
+        if (a.k_norm) unit_norm(p, q, a.k_norm, c, a.hd, a.eps);
+        unit_rotate(p, q, cs, sn);
+    } else if (key && a.k_norm) {
+        unit_norm(p, q, a.k_norm, c, a.hd, a.eps);
+    }
+    float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-            const int x = base + i * (int)blockDim.x + (int)threadIdx.x, c = x & (U - 1);
-            const int j = j0 + (x < units ? x >> ulog : 0);
-            load8(src + j * a.sm + 8 * c, p[i]);
-            load8(src + j * a.sm + 8 * c + (a.hd >> 1), q[i]);
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(p[e]), finite_abs(q[e])));
+    m = warp_max(m);   // (threads without a unit hold the first row's again)
+    if ((x & 31) == 0) red[x >> 5] = m;
+    __syncthreads();
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) m = fmaxf(m, red[i]);
+    const float now = fmaxf(pow2i(e4m3_exponent(m)), had), inv = 1.f / now;   // powers of two: exact
+    if (x == 0) *sc = now;
+    if (x < units) {
+        uint8_t* d = dst + (w.off + (x >> ulog)) * a.c.st + 8 * c;
+        *reinterpret_cast<uint2*>(d) = pack_e4m3(p, inv);
+        *reinterpret_cast<uint2*>(d + (a.hd >> 1)) = pack_e4m3(q, inv);
+    }
+    if (had > 0.f && had != now) reround(dst, a.c.st, w.off, ulog, had * inv);
+}
+
+// Many rows a page (prompts): a CTA of 512 threads takes the keys or the
+// values of a page for `hpt` KV heads after one another; the next head's rows
+// are on their way while this one's are rounded, and the angles are computed
+// once for all heads, slot s of the page as the product of the rotations by its
+// 16-slot base and by s % 16 (20 sines a pair for a page of 64 instead of 64;
+// the product costs the angle 3 u).  ONE: a head's rows fit two units a thread
+// and stay in registers between the maximum and the rounding; larger pages are
+// read twice, the second time from L2.
+constexpr int kPageThreads = 512;
+
+template <typename IT> struct Raw { uint4 v[4 * sizeof(IT) / 4]; };   // a unit as loaded
+__device__ __forceinline__ void raw_load(const uint16_t* p, int half, Raw<uint16_t>& r) {
+    r.v[0] = ld_stream16(p);
+    r.v[1] = ld_stream16(p + half);
+}
+__device__ __forceinline__ void raw_load(const float* p, int half, Raw<float>& r) {
+    r.v[0] = ld_stream16(p);
+    r.v[1] = ld_stream16(p + 4);
+    r.v[2] = ld_stream16(p + half);
+    r.v[3] = ld_stream16(p + half + 4);
+}
+__device__ __forceinline__ void raw_open(const Raw<uint16_t>& r, float (&p)[8], float (&q)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint4 u = r.v[h];
+        float* x = h ? q : p;
+        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
+        x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+    }
+}
+__device__ __forceinline__ void raw_open(const Raw<float>& r, float (&p)[8], float (&q)[8]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const uint4 u = r.v[h];
+        float* x = (h < 2 ? p : q) + 4 * (h & 1);
+        x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    }
+}
+
+template <typename IT, bool ONE>
+__global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(const __grid_constant__ AppendArgs a) {
+    extern __shared__ __align__(16) float2 s_rot[];   // [ps / 16][hd / 2] bases, [16][hd / 2] steps
+    __shared__ __align__(16) float s_gain[512];
+    __shared__ float red[2][kPageThreads / 32];
+    const int ps = 1 << a.c.ps_log2, nt = (a.M + ps - 2) / ps + 1;
+    if (blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y == 0 && blockIdx.z == 0) append_status(a);
+        return;
+    }
+    PageRows w;
+    if (!page_rows(a, nt, w)) return;
+    constexpr int UPT = 2;
+    const bool key = blockIdx.z == 0, rot = key && a.rope.on, nrm = key && a.k_norm;
+    const int tid = threadIdx.x, U = a.hd >> 4, ulog = 31 - __clz(U), units = (w.j1 - w.j0) << ulog, half = a.hd >> 1;
+    const int g0 = blockIdx.y * a.hpt, step = kPageThreads * UPT;
+    const int c = tid & (U - 1);   // the same for all of a thread's units
+    const IT* src = reinterpret_cast<const IT*>(key ? a.k : a.v) + w.b * a.sb + g0 * a.sh + 8 * c;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(key ? a.c.k : a.c.v) + w.page * a.c.sp + g0 * a.c.sh;
+    float* scale = (key ? a.c.ks : a.c.vs) + (long long)w.page * a.c.Hkv + g0;
+    auto row = [&](int base, int i) {
+        const int x = base + i * kPageThreads + tid;
+        return x < units ? x >> ulog : 0;
+    };
+    Raw<IT> raw[UPT];
+#pragma unroll
+    for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(0, i)) * a.sm, half, raw[i]);
+    if (nrm)
+        for (int i = tid; i < a.hd; i += kPageThreads) s_gain[i] = a.k_norm[i];
+    const int nb = ps >> 4;
+    if (rot) {
+        const int pr = tid & (half - 1);   // one pair a thread: its table entries are read once
+        const float hi = a.rope.hi[pr], lo = a.rope.lo[pr];
+        for (int e = tid / half; e < nb + 16; e += kPageThreads / half) {
+            float pl, ph;
+            split_pos(e < nb ? w.first + 16 * e : e - nb, pl, ph);
+            float2 r;
+            pair_angle<false>(pl, ph, hi, lo, r.x, r.y);
+            s_rot[e * half + pr] = r;
         }
+    }
+    if (rot || nrm) __syncthreads();
+    auto angles = [&](int r, float (&cs)[8], float (&sn)[8]) {
+        const int s = w.off + r;
+        const float4* x = reinterpret_cast<const float4*>(s_rot + (s >> 4) * half + 8 * c);
+        const float4* y = reinterpret_cast<const float4*>(s_rot + (nb + (s & 15)) * half + 8 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // two pairs a load
+            const float4 u = x[i], v = y[i];
+            cs[2 * i] = fmaf(u.x, v.x, -u.y * v.y);
+            sn[2 * i] = fmaf(u.x, v.y, u.y * v.x);
+            cs[2 * i + 1] = fmaf(u.z, v.z, -u.w * v.w);
+            sn[2 * i + 1] = fmaf(u.z, v.w, u.w * v.z);
+        }
+    };
+    float cs[ONE ? UPT : 1][8], sn[ONE ? UPT : 1][8];
+    if (ONE && rot)
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) angles(row(0, i), cs[ONE ? i : 0], sn[ONE ? i : 0]);
+    float p[UPT][8], q[UPT][8];
+    auto turn = [&](int base) {   // raw -> p, q
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-            const int x = base + i * (int)blockDim.x + (int)threadIdx.x, c = x & (U - 1);
-            if (key && a.k_norm) unit_norm(p[i], q[i], a.k_norm, c, a.hd, a.eps);
-            if (key && a.rope.on) {
-                float cs[8], sn[8];
-                unit_angles<false>((long long)len + j0 + (x < units ? x >> ulog : 0), a.rope.hi + 8 * c, a.rope.lo + 8 * c, cs, sn);
-                unit_rotate(p[i], q[i], cs, sn);
+            raw_open(raw[i], p[i], q[i]);
+            if (nrm) unit_norm_staged(p[i], q[i], s_gain, c, a.hd, a.eps);
+            if (rot) {
+                if (!ONE) angles(row(base, i), cs[0], sn[0]);
+                unit_rotate(p[i], q[i], cs[ONE ? i : 0], sn[ONE ? i : 0]);
             }
         }
     };
-    float m = 0.f;
-    for (int base = 0; base < units; base += step) {
-        fetch(base);
+    for (int g = 0; g < a.hpt; ++g) {
+        const float had = w.off > 0 ? scale[g] : 0.f;
+        float m = 0.f;
+        for (int base = 0; base < units; base += step) {
+            if (!ONE && base > 0)
 #pragma unroll
-        for (int i = 0; i < UPT; ++i)
+                for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(base, i)) * a.sm + g * a.sh, half, raw[i]);
+            turn(base);
+            if (ONE && g + 1 < a.hpt)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(p[i][e]), finite_abs(q[i][e])));
-    }
-    m = warp_max(m);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) m = fmaxf(m, red[w]);
-    // largest scale: the new rows', or the one the older codes have
-    float now = pow2i(e4m3_exponent(m));
-    now = fmaxf(now, had);
-    const float inv = 1.f / now;   // a power of two: exact
-    if (threadIdx.x == 0) *sc = now;
-    for (int base = 0; base < units; base += step) {
-        if (step < units) fetch(base);
+                for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(0, i)) * a.sm + (g + 1) * a.sh, half, raw[i]);
 #pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-            const int x = base + i * (int)blockDim.x + (int)threadIdx.x, c = x & (U - 1);
-            if (x >= units) continue;
-            uint8_t* d = dst + (off + (x >> ulog)) * a.c.st + 8 * c;
-            *reinterpret_cast<uint2*>(d) = pack_e4m3(p[i], inv);
-            *reinterpret_cast<uint2*>(d + (a.hd >> 1)) = pack_e4m3(q[i], inv);
+            for (int i = 0; i < UPT; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(p[i][e]), finite_abs(q[i][e])));
         }
-    }
-    if (had > 0.f && had != now) {   // the page's older codes, re-rounded to the larger scale
-        const float f = had * inv;
-        for (int x = threadIdx.x; x < off << ulog; x += blockDim.x) {
-            uint4* d = reinterpret_cast<uint4*>(dst + (x >> ulog) * a.c.st + 16 * (x & (U - 1)));
-            uint4 w = *d;
-            uint32_t* ws = reinterpret_cast<uint32_t*>(&w);
+        m = warp_max(m);
+        if ((tid & 31) == 0) red[g & 1][tid >> 5] = m;
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t r = 0;
+        for (int i = 0; i < kPageThreads / 32; ++i) m = fmaxf(m, red[g & 1][i]);
+        const float now = fmaxf(pow2i(e4m3_exponent(m)), had), inv = 1.f / now;   // powers of two: exact
+        if (tid == 0) scale[g] = now;
+        uint8_t* dg = dst + g * a.c.sh;
+        for (int base = 0; base < units; base += step) {
+            if (!ONE) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(ws[i] >> (16 * h)), __NV_E4M3);
-                    float2 y = __half22float2(__half2(v));
-                    y.x *= f;
-                    y.y *= f;
-                    r |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * h);
-                }
-                ws[i] = r;
+                for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(base, i)) * a.sm + g * a.sh, half, raw[i]);
+                turn(base);
             }
-            *d = w;
+#pragma unroll
+            for (int i = 0; i < UPT; ++i) {
+                const int x = base + i * kPageThreads + tid;
+                if (x >= units) continue;
+                uint8_t* d = dg + (w.off + (x >> ulog)) * a.c.st + 8 * c;
+                *reinterpret_cast<uint2*>(d) = pack_e4m3(p[i], inv);
+                *reinterpret_cast<uint2*>(d + half) = pack_e4m3(q[i], inv);
+            }
         }
+        if (!ONE && g + 1 < a.hpt)
+#pragma unroll
+            for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(0, i)) * a.sm + (g + 1) * a.sh, half, raw[i]);
+        if (had > 0.f && had != now) reround(dg, a.c.st, w.off, ulog, had * inv);
     }
 }
 
@@ -228,23 +386,33 @@ static cudaError_t launch_rows(AppendArgs a, int sms, cudaStream_t s) {
 }
 
 template <typename IT>
-static cudaError_t launch_e4m3(const AppendArgs& a, cudaStream_t s) {
+static cudaError_t launch_e4m3(AppendArgs a, int sms, cudaStream_t s) {
     const int ps = 1 << a.c.ps_log2, nt = (a.M + ps - 2) / ps + 1, U = a.hd >> 4;
     const int units = (a.M < ps ? a.M : ps) * U;
-    const dim3 grid((unsigned)a.B * nt + 1, (unsigned)a.c.Hkv, 2);
+    const unsigned pages = (unsigned)a.B * nt;
     if (units <= 256) {
         const int T = (units + 31) & ~31;
-        append_e4m3_kernel<IT, 1><<<grid, T < 64 ? 64 : T, 0, s>>>(a);
-    } else {
-        int T = ((units + 3) / 4 + 31) & ~31;
-        append_e4m3_kernel<IT, 4><<<grid, T > 512 ? 512 : T, 0, s>>>(a);
+        append_e4m3_kernel<IT><<<dim3(pages + 1, (unsigned)a.c.Hkv, 2), T < 64 ? 64 : T, 0, s>>>(a);
+        return cudaGetLastError();
     }
+    // all heads in one CTA where the pages alone fill the GPU
+    a.hpt = pages * 2 >= (unsigned)sms ? a.c.Hkv : 1;
+    const dim3 grid(pages + 1, (unsigned)(a.c.Hkv / a.hpt), 2);
+    const size_t smem = a.rope.on ? (size_t)((ps >> 4) + 16) * (a.hd >> 1) * sizeof(float2) : 0;
+    const bool one = units <= 2 * kPageThreads;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = one ? cudaFuncSetAttribute(append_e4m3_pages_kernel<IT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                                  : cudaFuncSetAttribute(append_e4m3_pages_kernel<IT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    if (one) append_e4m3_pages_kernel<IT, true><<<grid, kPageThreads, smem, s>>>(a);
+    else append_e4m3_pages_kernel<IT, false><<<grid, kPageThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_append(const AppendArgs& a, int in_dtype, int kv_dtype, int sms, cudaStream_t s) {
     const bool f = in_dtype == MTP_DTYPE_F32;
-    if (kv_dtype == MTP_DTYPE_E4M3) return f ? launch_e4m3<float>(a, s) : launch_e4m3<uint16_t>(a, s);
+    if (kv_dtype == MTP_DTYPE_E4M3) return f ? launch_e4m3<float>(a, sms, s) : launch_e4m3<uint16_t>(a, sms, s);
     if (kv_dtype == MTP_DTYPE_F32) return f ? launch_rows<float, float>(a, sms, s) : launch_rows<uint16_t, float>(a, sms, s);
     return f ? launch_rows<float, uint16_t>(a, sms, s) : launch_rows<uint16_t, uint16_t>(a, sms, s);
 }

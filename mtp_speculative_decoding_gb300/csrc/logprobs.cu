@@ -1,10 +1,10 @@
 // logprobs.cu -- log probability, entropy and top alternatives of rows of
 // logits, in one pass over them.
 //
-// With a reference m near the maximum, S = sum e^(z - m) and T = sum (z - m)
-// e^(z - m): log p_t = (z_t - m) - ln S and the entropy is ln S - T / S.  The
-// bytes of the logits bound it; the exponential (16 lanes a clock and SM) is
-// next at bf16.
+// With a reference m near the maximum, d = (z - m) log2(e), S = sum 2^d and T =
+// sum d 2^d: log p_t = (z_t - m) - ln S and the entropy is ln S - ln 2 T / S.  The bytes of the logits bound it; the
+// exponential (16 lanes a clock and SM) is next at bf16, so the other work of
+// an element is kept to paired fp32 instructions.
 //
 // A row is cut into C pieces, one CTA each, and the C CTAs are one
 // thread-block cluster: the leader reads the others' sums and candidates
@@ -25,7 +25,7 @@ namespace {
 constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
 constexpr int kLpVec = 4;            // 16-byte loads a thread has in flight
 constexpr int kLpCap = 2048;         // candidates of a piece
-constexpr float kL2E = 1.44269504f;
+constexpr float kL2E = 1.44269504f, kLn2 = 0.693147181f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -62,12 +62,32 @@ __device__ __forceinline__ float vec_max(const uint4& v, float) {
     return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
 }
 
-// Sums of one thread relative to its own reference m: the maximum of its
-// first block, moved only when a value is more than 2^40-fold above it.
+// two fp32 values in a register pair
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(unsigned long long v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Sums of one thread relative to its own reference m (a logit): the maximum of
+// its first block, moved only when a value is more than 27 above it.
 struct Sums { float m, S, T; };
 
 __device__ __forceinline__ void move_ref(Sums& s, float m) {
-    const float d = s.m - m, f = ex2(d * kL2E);
+    const float d = (s.m - m) * kL2E, f = ex2(d);
     s.T = f == 0.f ? 0.f : f * fmaf(s.S, d, s.T);
     s.S = f == 0.f ? 0.f : f * s.S;
     s.m = m;
@@ -75,7 +95,7 @@ __device__ __forceinline__ void move_ref(Sums& s, float m) {
 // one value, any value: -inf and NaN add nothing
 __device__ __forceinline__ void add_one(Sums& s, float z) {
     if (!(z > neg_inf())) return;
-    const float d = z - s.m, e = ex2(d * kL2E);
+    const float d = (z - s.m) * kL2E, e = ex2(d);
     if (e == 0.f) return;
     s.S += e;
     s.T = fmaf(e, d, s.T);
@@ -85,29 +105,28 @@ __device__ __forceinline__ void add_one(Sums& s, float z) {
 // products.  Next to a reference so large that a bf16 step there is more than
 // that, to 1/64 of it below.
 __device__ __forceinline__ float lifted(float m) { return m - fmaxf(200.f, fabsf(m) * (1.f / 64.f)); }
-__device__ __forceinline__ void add_vec(Sums& s, const uint4& v, uint16_t) {
-    const float lo = lifted(s.m);
+// Two logits; nm: twice -m log2(e) as rounded, S2, T2: the block's sums of even
+// and odd elements (what nm's rounding left out is put back for the block).
+__device__ __forceinline__ void add_pair(float a, float b, unsigned long long nm, unsigned long long& S2, unsigned long long& T2) {
+    const unsigned long long d = fma2(pair(a, b), pair(kL2E, kL2E), nm);
+    float d0, d1;
+    split(d, d0, d1);
+    const unsigned long long e = pair(ex2(d0), ex2(d1));
+    S2 = add2(S2, e);
+    T2 = fma2(e, d, T2);
+}
+__device__ __forceinline__ void add_vec(const uint4& v, float lo, unsigned long long nm, unsigned long long& S2,
+                                        unsigned long long& T2, uint16_t) {
     uint32_t l;
     asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(l) : "f"(lo));
     const uint32_t w[4] = {max_bf16x2(v.x, l), max_bf16x2(v.y, l), max_bf16x2(v.z, l), max_bf16x2(v.w, l)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float d0 = bf16_lo(w[i]) - s.m, d1 = bf16_hi(w[i]) - s.m;
-        const float e0 = ex2(d0 * kL2E), e1 = ex2(d1 * kL2E);
-        s.S += e0;
-        s.T = fmaf(e0, d0, s.T);
-        s.S += e1;
-        s.T = fmaf(e1, d1, s.T);
-    }
+    for (int i = 0; i < 4; ++i) add_pair(bf16_lo(w[i]), bf16_hi(w[i]), nm, S2, T2);
 }
-__device__ __forceinline__ void add_vec(Sums& s, const uint4& v, float) {
-    const float lo = lifted(s.m);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float d = fmaxf(Vec<float>::get(v, i), lo) - s.m, e = ex2(d * kL2E);
-        s.S += e;
-        s.T = fmaf(e, d, s.T);
-    }
+__device__ __forceinline__ void add_vec(const uint4& v, float lo, unsigned long long nm, unsigned long long& S2,
+                                        unsigned long long& T2, float) {
+    add_pair(fmaxf(__uint_as_float(v.x), lo), fmaxf(__uint_as_float(v.y), lo), nm, S2, T2);
+    add_pair(fmaxf(__uint_as_float(v.z), lo), fmaxf(__uint_as_float(v.w), lo), nm, S2, T2);
 }
 
 struct LpShared {
@@ -195,6 +214,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     if (tid == 0) sh.count = 0;
     __syncthreads();
     Sums s = {neg_inf(), 0.f, 0.f};
+    float lo = 0.f, nm1 = 0.f, left = 0.f, f = 1.f;   // of the reference: what far values are lifted to, -m log2(e),
+                                                      // what its rounding left out, 2^-that
     float tmax = neg_inf();                   // this thread's largest so far
     float tau = neg_inf();                    // K values at or above it lie in earlier blocks
     unsigned long long kth = 0ull;            // set once a compaction knew the K-th key
@@ -212,12 +233,26 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < kLpVec; ++k) bm = fmaxf(bm, vec_max(cur[k], T()));
         if (bm > neg_inf()) {
-            if (!(s.m > neg_inf())) s.m = bm;
-            else if (bm > s.m + 27.f) move_ref(s, bm);
-            if (s.m > -1e37f) {
+            if (!(s.m > neg_inf()) || bm > s.m + 27.f) {
+                if (s.m > neg_inf()) move_ref(s, bm);
+                s.m = bm;
+                lo = lifted(bm);
+                nm1 = -(bm * kL2E);
+                left = fmaf(bm, kL2E, nm1);
+                f = ex2(-left);
+            }
+            if (fabsf(s.m) < 1e5f) {
+                const unsigned long long nm = pair(nm1, nm1);
+                unsigned long long S2 = 0ull, T2 = 0ull;
 #pragma unroll
-                for (int k = 0; k < kLpVec; ++k) add_vec(s, cur[k], T());
-            } else {   // next to the type's lowest value: "200 below" has no room
+                for (int k = 0; k < kLpVec; ++k) add_vec(cur[k], lo, nm, S2, T2, T());
+                float x, y, u, v;
+                split(S2, x, y);
+                split(T2, u, v);
+                x += y;
+                s.S = fmaf(f, x, s.S);
+                s.T = fmaf(f, fmaf(-left, x, u + v), s.T);
+            } else {   // a reference whose products round by whole bits (masks of the type's lowest value), an infinity
 #pragma unroll
                 for (int k = 0; k < kLpVec; ++k)
 #pragma unroll
@@ -352,11 +387,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             if (lane == 0) {
                 sh.wsum[0] = w;
                 const float ls = logf(w.S);
-                if (a.logprob) {
-                    if (zt != zt) zt = neg_inf();
-                    a.logprob[row] = (zt - M) - ls;
-                }
-                if (a.entropy) a.entropy[row] = ls - w.T / w.S;
+                if (a.logprob) a.logprob[row] = ((zt == zt ? zt : neg_inf()) - M) - ls;
+                if (a.entropy) a.entropy[row] = ls - kLn2 * (w.T / w.S);
             }
         }
         if (a.K > 0) {
@@ -398,10 +430,22 @@ cudaError_t launch(const LogprobArgs& a, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDev) ready[dev] = true;
     }
-    // pieces: enough CTAs to fill the GPU, none below one block of loads
+    // Pieces a row: the fewest waves of bytes (an SM's share of the bandwidth is
+    // about 45 bytes a ns), against some 2500 ns that each wave of two CTAs an SM
+    // costs in first loads, joins and cluster barriers; none below half a block
+    // of loads.
     int C = 1;
-    const long long blk = (long long)kLpThreads * kLpVec * Vec<T>::n;
-    while (C < 16 && a.rows * C < 4ll * sms && a.V / (2 * C) >= blk / 2) C *= 2;
+    double best = 1e30;
+    const double row_ns = (double)a.V * sizeof(T) / 45.0;
+    for (int c = 1; c <= 16; c *= 2) {
+        const long long ctas = a.rows * c;
+        const double ns = row_ns * (double)((ctas + sms - 1) / sms) / c + 2500.0 * (double)((ctas + 2 * sms - 1) / (2 * sms));
+        if (c > 1 && a.V / c < (long long)kLpThreads * kLpVec * Vec<T>::n / 2) break;
+        if (ns < best) {
+            best = ns;
+            C = c;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.rows * C));
     cfg.blockDim = dim3(kLpThreads);

@@ -75,44 +75,67 @@ __device__ __forceinline__ void unit_norm(float (&a)[8], float (&b)[8], const fl
     }
 }
 
+// unit_norm with the unit's gains in 16-byte aligned (shared) memory
+__device__ __forceinline__ void unit_norm_staged(float (&a)[8], float (&b)[8], const float* gain, int c, int hd, float eps) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
+    for (int o = hd >> 5; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float r = 1.0f / sqrtf(s / (float)hd + eps);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 g = *reinterpret_cast<const float4*>(gain + 8 * c + 4 * h);
+        const float4 k = *reinterpret_cast<const float4*>(gain + (hd >> 1) + 8 * c + 4 * h);
+        a[4 * h] *= r * g.x; a[4 * h + 1] *= r * g.y; a[4 * h + 2] *= r * g.z; a[4 * h + 3] *= r * g.w;
+        b[4 * h] *= r * k.x; b[4 * h + 1] *= r * k.y; b[4 * h + 2] *= r * k.z; b[4 * h + 3] *= r * k.w;
+    }
+}
+
 // cos and sin of the unit's 8 pairs at position pos.  pos = 4096 ph + pl; each
 // product with the table's high part is split exactly by an fma, whole turns
 // are dropped, and what the remaining fp32 sum cannot hold turns the result
 // by a first-order correction -- the angle keeps about 2^-45 of its size plus
 // 2^-40 turns, so only the rounding of cos and sin themselves is left.
 // FAST: the sine and cosine instructions (2^-20), for rows that round to 16
-// bits or fewer right after.  hi, lo: the table's 8 entries of this unit.
+// bits or fewer right after.
+template <bool FAST>
+__device__ __forceinline__ void pair_angle(float pl, float ph, float h, float l, float& cs, float& sn) {
+    float x = __fmul_rn(pl, h), y = __fmul_rn(ph, h);   // (no contraction: the products' own roundings are wanted)
+    float e = fmaf(pl, h, -x) + fmaf(ph, h, -y);
+    x -= rintf(x);
+    y -= rintf(y);
+    float s = x + y;
+    const float z = s - x;
+    e += (x - (s - z)) + (y - z);      // the rounding of x + y
+    s -= rintf(s);
+    e = fmaf(ph + pl, l, e);           // up to 2^-7 turns at positions of 2^19: most of it joins s
+    const float t = s + e;
+    e -= t - s;
+    s = t;
+    if (FAST) {
+        s -= rintf(s);
+        const float r = 6.2831853f * s;
+        asm("sin.approx.f32 %0, %1;" : "=f"(sn) : "f"(r));
+        asm("cos.approx.f32 %0, %1;" : "=f"(cs) : "f"(r));
+    } else {
+        float sv, cv;
+        sincospif(2.f * s, &sv, &cv);
+        const float d = 6.2831853f * e;
+        cs = fmaf(-sv, d, cv);
+        sn = fmaf(cv, d, sv);
+    }
+}
+__device__ __forceinline__ void split_pos(long long pos, float& pl, float& ph) {
+    pl = (float)(int)(pos & 4095);
+    ph = (float)(int)(pos >> 12) * 4096.f;
+}
+// hi, lo: the table's 8 entries of this unit
 template <bool FAST>
 __device__ __forceinline__ void unit_angles(long long pos, const float* hi, const float* lo, float (&cs)[8], float (&sn)[8]) {
-    const float pl = (float)(int)(pos & 4095), ph = (float)(int)(pos >> 12) * 4096.f, pf = ph + pl;
+    float pl, ph;
+    split_pos(pos, pl, ph);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float h = hi[i], l = lo[i];
-        float x = __fmul_rn(pl, h), y = __fmul_rn(ph, h);   // (no contraction: the products' own roundings are wanted)
-        float e = fmaf(pl, h, -x) + fmaf(ph, h, -y);
-        x -= rintf(x);
-        y -= rintf(y);
-        float s = x + y;
-        const float z = s - x;
-        e += (x - (s - z)) + (y - z);      // the rounding of x + y
-        s -= rintf(s);
-        e = fmaf(pf, l, e);                // up to 2^-7 turns at positions of 2^19: most of it joins s
-        const float t0 = s + e;
-        e -= t0 - s;
-        s = t0;
-        float sv, cv;
-        const float d = 6.2831853f * e;
-        if (FAST) {
-            s -= rintf(s);
-            const float r = 6.2831853f * s;
-            asm("sin.approx.f32 %0, %1;" : "=f"(sn[i]) : "f"(r));
-            asm("cos.approx.f32 %0, %1;" : "=f"(cs[i]) : "f"(r));
-            continue;
-        }
-        sincospif(2.f * s, &sv, &cv);
-        cs[i] = fmaf(-sv, d, cv);
-        sn[i] = fmaf(cv, d, sv);
-    }
+    for (int i = 0; i < 8; ++i) pair_angle<FAST>(pl, ph, hi[i], lo[i], cs[i], sn[i]);
 }
 __device__ __forceinline__ void unit_rotate(float (&a)[8], float (&b)[8], const float (&cs)[8], const float (&sn)[8]) {
 #pragma unroll
