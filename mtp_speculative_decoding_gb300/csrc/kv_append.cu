@@ -38,7 +38,7 @@ __device__ void append_status(const AppendArgs& a) {
 // ---------------------------------------------------------------------------
 // fp32 and bf16 caches: a thread takes one unit (16 elements) of `hpt` KV
 // heads of one row, so that the angles of a row are computed once for those
-// heads; gridDim.y: keys, values
+// heads; gridDim.y: keys and values of every sequence
 // ---------------------------------------------------------------------------
 template <typename IT, typename CT>
 __global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant__ AppendArgs a) {
@@ -47,28 +47,26 @@ __global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant_
         if (blockIdx.y == 0) append_status(a);
         return;
     }
-    if (blockIdx.y == 0) {   // keys: lanes read the tables at different places, which parameters serve one by one
-        if (a.rope.on)
-            for (int i = threadIdx.x; i < a.hd >> 1; i += blockDim.x) {
-                s_hi[i] = a.rope.hi[i];
-                s_lo[i] = a.rope.lo[i];
-            }
-        if (a.k_norm)
-            for (int i = threadIdx.x; i < a.hd; i += blockDim.x) s_gain[i] = a.k_norm[i];
-        __syncthreads();
-    }
-    const int U = a.hd >> 4, groups = a.c.Hkv / a.hpt;
-    const long long total = (long long)a.B * a.M * groups * U;
-    const long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const bool in = x < total;
-    long long r = (in ? x : total - 1) / U;
-    const int c = (int)((in ? x : total - 1) % U), g0 = (int)(r % groups) * a.hpt;
-    r /= groups;
-    const int b = (int)(r / a.M), j = (int)(r % a.M);
-    const bool key = blockIdx.y == 0;
-    const IT* src = reinterpret_cast<const IT*>(key ? a.k : a.v) + b * a.sb + j * a.sm + g0 * a.sh + 8 * c;
+    const int b = blockIdx.y >> 1, ulog = 31 - __clz(a.hd >> 4), groups = a.c.Hkv / a.hpt;
+    const bool key = (blockIdx.y & 1) == 0, rot = key && a.rope.on, nrm = key && a.k_norm;
     const int len = a.kv_len[b], n = a.n_new ? a.n_new[b] : a.M;
-    const bool live = in && seq_ok(len, n, a.M, a.c) && j < n;
+    if (!seq_ok(len, n, a.M, a.c)) return;
+    const unsigned x = blockIdx.x * blockDim.x + threadIdx.x, t = x >> ulog;
+    const int c = (int)(x & ((1u << ulog) - 1u));
+    int j = groups == 1 ? (int)t : (int)(t / (unsigned)groups);
+    if ((groups == 1 ? (blockIdx.x * blockDim.x) >> ulog : ((blockIdx.x * blockDim.x) >> ulog) / (unsigned)groups) >= (unsigned)n) return;
+    const int g0 = ((int)t - j * groups) * a.hpt;
+    if (rot)   // lanes read the tables at different places, which parameters serve one by one
+        for (int i = threadIdx.x; i < a.hd >> 1; i += blockDim.x) {
+            s_hi[i] = a.rope.hi[i];
+            s_lo[i] = a.rope.lo[i];
+        }
+    if (nrm)
+        for (int i = threadIdx.x; i < a.hd; i += blockDim.x) s_gain[i] = a.k_norm[i];
+    if (rot || nrm) __syncthreads();
+    const bool live = j < n;
+    if (!live) j = n - 1;
+    const IT* src = reinterpret_cast<const IT*>(key ? a.k : a.v) + b * a.sb + j * a.sm + g0 * a.sh + 8 * c;
     const long long pos = (long long)len + j;
     CT* dst = nullptr;
     if (live) {
@@ -77,16 +75,14 @@ __global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant_
             dst = reinterpret_cast<CT*>(key ? a.c.k : a.c.v) + pg * a.c.sp + (pos & ((1 << a.c.ps_log2) - 1)) * a.c.st +
                   g0 * a.c.sh + 8 * c;
     }
-    if (!__any_sync(0xffffffffu, dst != nullptr)) return;
     float cs[8], sn[8];
-    const bool rot = key && a.rope.on;
-    if (rot) unit_angles<false>(live ? pos : 0, s_hi + 8 * c, s_lo + 8 * c, cs, sn);
+    if (rot) unit_angles<false>(pos, s_hi + 8 * c, s_lo + 8 * c, cs, sn);
 #pragma unroll 4
     for (int h = 0; h < a.hpt; ++h) {
         float p[8], q[8];
         load8(src + h * a.sh, p);
         load8(src + h * a.sh + (a.hd >> 1), q);
-        if (key && a.k_norm) unit_norm_staged(p, q, s_gain, c, a.hd, a.eps);
+        if (nrm) unit_norm_staged(p, q, s_gain, c, a.hd, a.eps);
         if (rot) unit_rotate(p, q, cs, sn);
         if (dst) {
             store8(dst + h * a.c.sh, p);
@@ -108,17 +104,30 @@ __device__ __forceinline__ int e4m3_exponent(float amax) {
     return k < -40 ? -40 : (k > 40 ? 40 : k);
 }
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
-__device__ __forceinline__ float finite_abs(float x) {
-    const float y = fabsf(x);
-    return y <= 3.402823466e38f ? y : 0.f;   // NaN and infinity do not count
+// The largest finite magnitude of a unit.  fmaxf passes NaN over; an infinity
+// shows in the result, and only then the values are looked at one by one.
+__device__ __forceinline__ float unit_amax(const float (&p)[8], const float (&q)[8], bool finite_only) {
+    float m = 0.f, n = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = fabsf(p[e]), y = fabsf(q[e]);
+        m = fmaxf(m, finite_only && x > 3.402823466e38f ? 0.f : x);
+        n = fmaxf(n, finite_only && y > 3.402823466e38f ? 0.f : y);
+    }
+    return fmaxf(m, n);
 }
-// 8 values times inv as e4m3 codes (nearest even, saturating; NaN and infinity become NaN)
-__device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8], float inv) {
+__device__ __forceinline__ bool is_inf(float x) { return x > 3.402823466e38f; }
+// 8 values times inv as e4m3 codes (nearest even, saturating; NaN becomes NaN,
+// and so does an infinity where `inf` says that there may be one)
+__device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8], float inv, bool inf) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = x[2 * i] - x[2 * i] == 0.f ? x[2 * i] * inv : __uint_as_float(0x7FC00000u);
-        const float hi = x[2 * i + 1] - x[2 * i + 1] == 0.f ? x[2 * i + 1] * inv : __uint_as_float(0x7FC00000u);
+        float lo = x[2 * i] * inv, hi = x[2 * i + 1] * inv;
+        if (inf) {
+            lo = is_inf(fabsf(x[2 * i])) ? __uint_as_float(0x7FC00000u) : lo;
+            hi = is_inf(fabsf(x[2 * i + 1])) ? __uint_as_float(0x7FC00000u) : hi;
+        }
         w[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
     }
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
@@ -199,19 +208,23 @@ __global__ void __launch_bounds__(256) append_e4m3_kernel(const __grid_constant_
     } else if (key && a.k_norm) {
         unit_norm(p, q, a.k_norm, c, a.hd, a.eps);
     }
-    float m = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(p[e]), finite_abs(q[e])));
-    m = warp_max(m);   // (threads without a unit hold the first row's again)
-    if ((x & 31) == 0) red[x >> 5] = m;
-    __syncthreads();
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) m = fmaxf(m, red[i]);
+    auto block_max = [&](float m) {
+        m = warp_max(m);   // (threads without a unit hold the first row's again)
+        __syncthreads();
+        if ((x & 31) == 0) red[x >> 5] = m;
+        __syncthreads();
+        for (int i = 0; i < (int)(blockDim.x >> 5); ++i) m = fmaxf(m, red[i]);
+        return m;
+    };
+    float m = block_max(unit_amax(p, q, false));
+    const bool inf = is_inf(m);
+    if (inf) m = block_max(unit_amax(p, q, true));
     const float now = fmaxf(pow2i(e4m3_exponent(m)), had), inv = 1.f / now;   // powers of two: exact
     if (x == 0) *sc = now;
     if (x < units) {
         uint8_t* d = dst + (w.off + (x >> ulog)) * a.c.st + 8 * c;
-        *reinterpret_cast<uint2*>(d) = pack_e4m3(p, inv);
-        *reinterpret_cast<uint2*>(d + (a.hd >> 1)) = pack_e4m3(q, inv);
+        *reinterpret_cast<uint2*>(d) = pack_e4m3(p, inv, inf);
+        *reinterpret_cast<uint2*>(d + (a.hd >> 1)) = pack_e4m3(q, inv, inf);
     }
     if (had > 0.f && had != now) reround(dst, a.c.st, w.off, ulog, had * inv);
 }
@@ -259,7 +272,7 @@ template <typename IT, bool ONE>
 __global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(const __grid_constant__ AppendArgs a) {
     extern __shared__ __align__(16) float2 s_rot[];   // [ps / 16][hd / 2] bases, [16][hd / 2] steps
     __shared__ __align__(16) float s_gain[512];
-    __shared__ float red[2][kPageThreads / 32];
+    __shared__ __align__(16) float red[2][kPageThreads / 32];
     const int ps = 1 << a.c.ps_log2, nt = (a.M + ps - 2) / ps + 1;
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y == 0 && blockIdx.z == 0) append_status(a);
@@ -326,6 +339,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(cons
             }
         }
     };
+    int turns = 0;
     for (int g = 0; g < a.hpt; ++g) {
         const float had = w.off > 0 ? scale[g] : 0.f;
         float m = 0.f;
@@ -338,15 +352,35 @@ __global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(cons
 #pragma unroll
                 for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(0, i)) * a.sm + (g + 1) * a.sh, half, raw[i]);
 #pragma unroll
-            for (int i = 0; i < UPT; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(p[i][e]), finite_abs(q[i][e])));
+            for (int i = 0; i < UPT; ++i) m = fmaxf(m, unit_amax(p[i], q[i], false));
         }
-        m = warp_max(m);
-        if ((tid & 31) == 0) red[g & 1][tid >> 5] = m;
-        __syncthreads();
+        auto block_max = [&](float m) {
+            m = warp_max(m);
+            if ((tid & 31) == 0) red[turns & 1][tid >> 5] = m;
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPageThreads / 32; ++i) m = fmaxf(m, red[g & 1][i]);
+            for (int i = 0; i < kPageThreads / 128; ++i) {
+                const float4 r = reinterpret_cast<const float4*>(red[turns & 1])[i];
+                m = fmaxf(fmaxf(m, fmaxf(r.x, r.y)), fmaxf(r.z, r.w));
+            }
+            ++turns;
+            return m;
+        };
+        m = block_max(m);
+        const bool inf = is_inf(m);
+        if (inf) {   // the finite values alone
+            m = 0.f;
+            for (int base = 0; base < units; base += step) {
+                if (!ONE) {
+#pragma unroll
+                    for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(base, i)) * a.sm + g * a.sh, half, raw[i]);
+                    turn(base);
+                }
+#pragma unroll
+                for (int i = 0; i < UPT; ++i) m = fmaxf(m, unit_amax(p[i], q[i], true));
+            }
+            m = block_max(m);
+        }
         const float now = fmaxf(pow2i(e4m3_exponent(m)), had), inv = 1.f / now;   // powers of two: exact
         if (tid == 0) scale[g] = now;
         uint8_t* dg = dst + g * a.c.sh;
@@ -361,8 +395,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(cons
                 const int x = base + i * kPageThreads + tid;
                 if (x >= units) continue;
                 uint8_t* d = dg + (w.off + (x >> ulog)) * a.c.st + 8 * c;
-                *reinterpret_cast<uint2*>(d) = pack_e4m3(p[i], inv);
-                *reinterpret_cast<uint2*>(d + half) = pack_e4m3(q[i], inv);
+                *reinterpret_cast<uint2*>(d) = pack_e4m3(p[i], inv, inf);
+                *reinterpret_cast<uint2*>(d + half) = pack_e4m3(q[i], inv, inf);
             }
         }
         if (!ONE && g + 1 < a.hpt)
@@ -379,8 +413,8 @@ static cudaError_t launch_rows(AppendArgs a, int sms, cudaStream_t s) {
     // all heads in one thread where that still fills the GPU: the angles of a
     // row are then computed once; one head per thread for small calls
     a.hpt = rows * U >= (long long)sms * 512 ? a.c.Hkv : 1;
-    const long long total = rows * (a.c.Hkv / a.hpt) * U;
-    const dim3 grid((unsigned)((total + 127) / 128) + 1, 2);
+    const long long per_seq = (long long)a.M * (a.c.Hkv / a.hpt) * U;
+    const dim3 grid((unsigned)((per_seq + 127) / 128) + 1, 2u * a.B);
     append_rows_kernel<IT, CT><<<grid, 128, 0, s>>>(a);
     return cudaGetLastError();
 }

@@ -189,7 +189,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     const long long h = (long long)((reinterpret_cast<uintptr_t>(rowp) & 15) / sizeof(T));
     const long long nv = (a.V + h + EPV - 1) / EPV, per = (nv + C - 1) / C;
     const long long v0 = per * rank, v1 = v0 + per < nv ? v0 + per : nv;
-    auto load = [&](long long v) -> uint4 {
+    // vectors [vs, ve) lie inside the row as well as inside the piece: no test
+    const long long vs = h && v0 == 0 ? 1 : v0, ve = (a.V + h) / EPV < v1 ? (a.V + h) / EPV : v1;
+    const T* origin = rowp - h;
+    auto load_edge = [&](long long v) -> uint4 {
         const long long e0 = v * EPV - h;
         if (v < v1 && e0 >= 0 && e0 + EPV <= a.V) return ld_stream16(rowp + e0);
         uint32_t w[4];
@@ -219,19 +222,29 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     float tmax = neg_inf();                   // this thread's largest so far
     float tau = neg_inf();                    // K values at or above it lie in earlier blocks
     unsigned long long kth = 0ull;            // set once a compaction knew the K-th key
-    int have = 0;                             // candidates before this block
-    uint4 cur[kLpVec], nxt[kLpVec];
+    int have = 0, seen = 0;                   // candidates before this block; when the bound was last taken from them
+    auto load_block = [&](long long base, uint4 (&x)[kLpVec]) {
+        if (base >= vs && base + BLK <= ve) {
+            const T* p = origin + (base + tid) * EPV;
 #pragma unroll
-    for (int k = 0; k < kLpVec; ++k) cur[k] = load(v0 + k * kLpThreads + tid);
+            for (int k = 0; k < kLpVec; ++k) x[k] = ld_stream16(p + k * kLpThreads * EPV);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kLpVec; ++k) x[k] = load_edge(base + k * kLpThreads + tid);
+        }
+    };
+    uint4 cur[kLpVec], nxt[kLpVec];
+    load_block(v0, cur);
     int it = 0;
     for (long long base = v0; base < v1; base += BLK, ++it) {
         const bool more = base + BLK < v1;
-        if (more)
+        if (more) load_block(base + BLK, nxt);
+        float vm[kLpVec], bm = neg_inf();
 #pragma unroll
-            for (int k = 0; k < kLpVec; ++k) nxt[k] = load(base + BLK + k * kLpThreads + tid);
-        float bm = neg_inf();
-#pragma unroll
-        for (int k = 0; k < kLpVec; ++k) bm = fmaxf(bm, vec_max(cur[k], T()));
+        for (int k = 0; k < kLpVec; ++k) {
+            vm[k] = vec_max(cur[k], T());
+            bm = fmaxf(bm, vm[k]);
+        }
         if (bm > neg_inf()) {
             if (!(s.m > neg_inf()) || bm > s.m + 27.f) {
                 if (s.m > neg_inf()) move_ref(s, bm);
@@ -263,7 +276,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             auto push = [&](bool at_least) {
                 if (!(at_least ? bm >= tau : bm > tau)) return;
 #pragma unroll
-                for (int k = 0; k < kLpVec; ++k)
+                for (int k = 0; k < kLpVec; ++k) {
+                    if (!(at_least ? vm[k] >= tau : vm[k] > tau)) continue;
 #pragma unroll
                     for (int i = 0; i < EPV; ++i) {
                         const float z = Vec<T>::get(cur[k], i);
@@ -273,6 +287,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
                                 sh.buf[pos] = pack_argmax(z, (uint32_t)((base + k * kLpThreads + tid) * EPV - h + i));
                         }
                     }
+                }
             };
             if (it > 0) push(false);
             tmax = fmaxf(tmax, bm);
@@ -325,6 +340,18 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
                 if (kth) tau = fmaxf(tau, key_value(kth));
                 cnt = sh.count;
                 __syncthreads();
+            } else if (more && cnt >= a.K && cnt >= seen + a.K && cnt <= kLpThreads) {
+                // the K-th of the candidates themselves bounds better: every
+                // candidate counts the larger ones, the K-th tells the others
+                // (again once as many more have come in)
+                const unsigned long long mine = tid < cnt ? sh.buf[tid] : ~0ull;
+                int r = 0;
+                if (tid < cnt)
+                    for (int i = 0; i < cnt; ++i) r += sh.buf[i] > mine;
+                if (tid < cnt && r == a.K - 1) sh.wkey[0] = mine;
+                __syncthreads();
+                tau = fmaxf(tau, key_value(sh.wkey[0]));
+                seen = cnt;
             }
             have = cnt;
         }
@@ -436,10 +463,11 @@ cudaError_t launch(const LogprobArgs& a, int sms, cudaStream_t s) {
     // of loads.
     int C = 1;
     double best = 1e30;
-    const double row_ns = (double)a.V * sizeof(T) / 45.0;
     for (int c = 1; c <= 16; c *= 2) {
         const long long ctas = a.rows * c;
-        const double ns = row_ns * (double)((ctas + sms - 1) / sms) / c + 2500.0 * (double)((ctas + 2 * sms - 1) / (2 * sms));
+        const double rate = ctas > sms ? 45.0 : 30.0;   // one CTA an SM has too few loads in flight
+        const double ns = (double)a.V * sizeof(T) / rate * (double)((ctas + sms - 1) / sms) / c +
+                          2500.0 * (double)((ctas + 2 * sms - 1) / (2 * sms));
         if (c > 1 && a.V / c < (long long)kLpThreads * kLpVec * Vec<T>::n / 2) break;
         if (ns < best) {
             best = ns;

@@ -61,27 +61,29 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
 }
 
 // RMSNorm of a row spread over U = hd/16 consecutive lanes (a power of two;
-// every lane of the warp takes part)
-__device__ __forceinline__ void unit_norm(float (&a)[8], float (&b)[8], const float* gain, int c, int hd, float eps) {
-    float s = 0.f;
+// every lane of the warp takes part); unit_norm_staged: the gains in 16-byte
+// aligned (shared) memory
+__device__ __forceinline__ float unit_rms(const float (&a)[8], const float (&b)[8], int hd, float eps) {
+    float s = 0.f, t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
+    for (int i = 0; i < 8; ++i) {
+        s = fmaf(a[i], a[i], s);
+        t = fmaf(b[i], b[i], t);
+    }
+    s += t;
     for (int o = hd >> 5; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float r = 1.0f / sqrtf(s / (float)hd + eps);
+    return rsqrtf(fmaf(s, __uint_as_float((uint32_t)(127 - (31 - __clz(hd))) << 23), eps));   // 1 / hd is a power of two
+}
+__device__ __forceinline__ void unit_norm(float (&a)[8], float (&b)[8], const float* gain, int c, int hd, float eps) {
+    const float r = unit_rms(a, b, hd, eps);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         a[i] = a[i] * r * __ldg(gain + 8 * c + i);
         b[i] = b[i] * r * __ldg(gain + (hd >> 1) + 8 * c + i);
     }
 }
-
-// unit_norm with the unit's gains in 16-byte aligned (shared) memory
 __device__ __forceinline__ void unit_norm_staged(float (&a)[8], float (&b)[8], const float* gain, int c, int hd, float eps) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(a[i], a[i], fmaf(b[i], b[i], s));
-    for (int o = hd >> 5; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float r = 1.0f / sqrtf(s / (float)hd + eps);
+    const float r = unit_rms(a, b, hd, eps);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float4 g = *reinterpret_cast<const float4*>(gain + 8 * c + 4 * h);
