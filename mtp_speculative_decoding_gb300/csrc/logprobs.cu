@@ -6,6 +6,8 @@
 // exponential (16 lanes a clock and SM) is next at bf16, so the other work of
 // an element is kept to paired fp32 instructions.
 //
+// The logits come in by bulk copies through a ring in shared memory, so that a
+// thread spends no instructions on addresses and no registers on prefetches.
 // A row is cut into C pieces, one CTA each, and the C CTAs are one
 // thread-block cluster: the leader reads the others' sums and candidates
 // from their shared memory, so no workspace, no counters and no second launch
@@ -22,15 +24,36 @@ namespace mtp {
 
 namespace {
 
-constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
-constexpr int kLpVec = 4;            // 16-byte loads a thread has in flight
-constexpr int kLpCap = 2048;         // candidates of a piece
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpVec = 4;                         // 16-byte vectors of a block a thread takes
+constexpr int kLpBlock = kLpThreads * kLpVec;     // vectors of a block: one bulk copy of 16 KB
+constexpr int kLpStages = 3;                      // blocks in flight; three CTAs share an SM
+constexpr int kLpCap = 2048;                      // candidates of a piece (a first slab of ties fits: 256 threads x 8)
 constexpr float kL2E = 1.44269504f, kLn2 = 0.693147181f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// the largest 64-bit key of a warp, by its halves
+__device__ __forceinline__ unsigned long long warp_max_u32x2(unsigned long long v) {
+    const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(v >> 32));
+    const unsigned lo = __reduce_max_sync(0xffffffffu, (unsigned)(v >> 32) == hi ? (unsigned)v : 0u);
+    return (unsigned long long)hi << 32 | lo;
+}
+__device__ __forceinline__ unsigned long long warp_min_u32x2(unsigned long long v) {
+    const unsigned hi = __reduce_min_sync(0xffffffffu, (unsigned)(v >> 32));
+    const unsigned lo = __reduce_min_sync(0xffffffffu, (unsigned)(v >> 32) == hi ? (unsigned)v : ~0u);
+    return (unsigned long long)hi << 32 | lo;
+}
+// wait of at most a second (a copy takes a few microseconds)
+__device__ __forceinline__ bool mbar_wait_bounded(unsigned long long* bar, unsigned parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_ns() - t0 > 1000000000ull) return false;
+    return true;
 }
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7F800000); }
 
@@ -130,18 +153,36 @@ __device__ __forceinline__ void add_vec(const uint4& v, float lo, unsigned long 
 }
 
 struct LpShared {
+    uint4 ring[kLpStages][kLpBlock];
     unsigned long long buf[kLpCap];           // candidates, in no order
     unsigned long long top[MTP_MAX_TOP];      // the piece's best, descending
-    unsigned long long all[16 * MTP_MAX_TOP]; // the cluster's (leader)
-    unsigned long long wkey[kLpWarps];
-    float wmax[kLpWarps];
+    unsigned long long wkey[kLpWarps];        // what each warp vouches for
+    unsigned long long bound;
+    unsigned long long full[kLpStages], empty[kLpStages];
     Sums wsum[kLpWarps];
     Sums piece;
     int count;
 };
 
-// the K largest of buf[0, count) into top[], descending (0: none)
-__device__ void select_top(LpShared& sh, int n, int K) {
+// Ranks (numbers of larger keys) of n distinct keys; put(key, rank) for each.
+template <typename F>
+__device__ __forceinline__ void rank_all(const unsigned long long* key, int n, F put) {
+    int glog = 0;   // threads of a key: as many as there are
+    while (glog < 5 && n << (glog + 1) <= kLpThreads) ++glog;
+    const int g = 1 << glog;
+    for (int base = 0; base < n; base += kLpThreads >> glog) {
+        const int which = base + ((int)threadIdx.x >> glog);
+        const unsigned long long mine = which < n ? key[which] : ~0ull;
+        int r = 0;
+#pragma unroll 4
+        for (int i = (int)threadIdx.x & (g - 1); i < n; i += g) r += key[i] > mine;
+        for (int o = g >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        if (which < n && ((int)threadIdx.x & (g - 1)) == 0) put(mine, r);
+    }
+}
+
+// the K largest of buf[0, n) into top[], descending (0: none)
+__device__ __noinline__ void select_top(LpShared& sh, int n, int K) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned long long mine[kLpCap / kLpThreads];
 #pragma unroll
@@ -163,14 +204,39 @@ __device__ void select_top(LpShared& sh, int n, int K) {
     __syncthreads();
 }
 
+// A piece whose candidates overflowed (ascending rows): its elements again,
+// 512 at a time, keeping the K best whenever the buffer is nearly full.
+template <typename T>
+__device__ __noinline__ void select_slowly(LpShared& sh, const T* rowp, long long e0, long long e1, int K) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid == 0) sh.count = 0;
+    __syncthreads();
+    unsigned long long kth = 0ull;
+    for (long long e = e0; e < e1; e += kLpThreads) {
+        if (sh.count > kLpCap - kLpThreads) {   // nobody adds before the barrier below
+            select_top(sh, sh.count, K);
+            if (tid < K) sh.buf[tid] = sh.top[tid];
+            kth = sh.top[K - 1];
+            if (tid == 0) sh.count = K;
+        }
+        __syncthreads();
+        const float z = e + tid < e1 ? ld_elem<T>(rowp, e + tid) : neg_inf();
+        const unsigned long long key = pack_argmax(z, (uint32_t)(e + tid));
+        if (z > neg_inf() && key > kth) sh.buf[atomicAdd(&sh.count, 1)] = key;
+        __syncthreads();
+    }
+}
+
 __device__ __forceinline__ float key_value(unsigned long long key) {
     const uint32_t u = (uint32_t)(key >> 32);
     return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_constant__ LogprobArgs a) {
-    __shared__ LpShared sh;
+__global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_constant__ LogprobArgs a) {
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    LpShared& sh = *reinterpret_cast<LpShared*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const long long row = blockIdx.x / C;
@@ -180,80 +246,80 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
         tok = a.tokens[row];
         if (tok < 0 || tok >= a.V) return;   // the whole cluster: nothing of the row is read or written
     }
-    constexpr int EPV = Vec<T>::n, BLK = kLpThreads * kLpVec;
+    constexpr int EPV = Vec<T>::n;
     const T* rowp = reinterpret_cast<const T*>(a.logits) + row * a.stride;
+    // the row in 16-byte vectors from the boundary at or before its start:
+    // vector v holds elements [v * EPV - h, v * EPV - h + EPV); this piece's
+    // whole vectors are [vs, ve), a row's ends that fill none are `loose`
+    const int h = (int)((reinterpret_cast<uintptr_t>(rowp) & 15) / sizeof(T));
+    const long long nv = (a.V + h + EPV - 1) / EPV, per = (nv + C - 1) / C;
+    const long long v0 = per * rank < nv ? per * rank : nv, v1 = v0 + per < nv ? v0 + per : nv;
+    const long long whole = (a.V + h) / EPV;
+    const long long vs = h > 0 && v0 == 0 ? 1 : v0, ve = whole < v1 ? whole : v1;
+    const int nvec = ve > vs ? (int)(ve - vs) : 0, blocks = (nvec + kLpBlock - 1) / kLpBlock;
+    const T* first = rowp - h + vs * EPV;
+    auto fetch = [&](int blk) {   // one thread
+        const int n = nvec - blk * kLpBlock < kLpBlock ? nvec - blk * kLpBlock : kLpBlock;
+        unsigned long long* bar = &sh.full[blk % kLpStages];
+        mbar_arrive_expect_tx(bar, (unsigned)n * 16u);
+        bulk_g2s(sh.ring[blk % kLpStages], first + (long long)blk * kLpBlock * EPV, (unsigned)n * 16u, bar);
+    };
+    if (tid == 0) {
+        for (int i = 0; i < kLpStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], kLpWarps);
+        }
+        mbar_fence_init();
+        for (int i = 0; i < kLpStages && i < blocks; ++i) fetch(i);
+        sh.count = 0;
+    }
     float zt = neg_inf();
     if (tid == 0 && rank == 0 && tok >= 0) zt = ld_elem<T>(rowp, tok);
-    // the row in 16-byte vectors from the boundary at or before its start:
-    // vector v holds elements [v * EPV - h, v * EPV - h + EPV)
-    const long long h = (long long)((reinterpret_cast<uintptr_t>(rowp) & 15) / sizeof(T));
-    const long long nv = (a.V + h + EPV - 1) / EPV, per = (nv + C - 1) / C;
-    const long long v0 = per * rank, v1 = v0 + per < nv ? v0 + per : nv;
-    // vectors [vs, ve) lie inside the row as well as inside the piece: no test
-    const long long vs = h && v0 == 0 ? 1 : v0, ve = (a.V + h) / EPV < v1 ? (a.V + h) / EPV : v1;
-    const T* origin = rowp - h;
-    auto load_edge = [&](long long v) -> uint4 {
-        const long long e0 = v * EPV - h;
-        if (v < v1 && e0 >= 0 && e0 + EPV <= a.V) return ld_stream16(rowp + e0);
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
-        if (v < v1)   // a row's first or last vector: element by element
-            for (int i = 0; i < EPV; ++i) {
-                const long long e = e0 + i;
-                if (e < 0 || e >= a.V) continue;
-                if (sizeof(T) == 2) {
-                    const uint32_t x = reinterpret_cast<const uint16_t*>(rowp)[e];
-                    const uint32_t old = i < 2 ? w[0] : i < 4 ? w[1] : i < 6 ? w[2] : w[3];
-                    const uint32_t nw = i & 1 ? (old & 0xFFFFu) | (x << 16) : (old & 0xFFFF0000u) | x;
-                    if (i < 2) w[0] = nw; else if (i < 4) w[1] = nw; else if (i < 6) w[2] = nw; else w[3] = nw;
-                } else {
-                    const uint32_t x = reinterpret_cast<const uint32_t*>(rowp)[e];
-                    if (i == 0) w[0] = x; else if (i == 1) w[1] = x; else if (i == 2) w[2] = x; else w[3] = x;
-                }
-            }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    };
-    if (tid == 0) sh.count = 0;
+    // a loose element of this thread
+    float loose = neg_inf();
+    long long loose_at = 0;
+    {
+        const int head = h > 0 && v0 == 0 ? (EPV - h < a.V ? EPV - h : (int)a.V) : 0;
+        const int tail = v1 == nv && v0 < nv && whole < nv && !(head && whole == 0) ? (int)(a.V + h - whole * EPV) : 0;
+        if (tid < head) loose_at = tid;
+        else if (tid < head + tail) loose_at = whole * EPV - h + (tid - head);
+        if (tid < head + tail) loose = ld_elem<T>(rowp, loose_at);
+    }
     __syncthreads();
     Sums s = {neg_inf(), 0.f, 0.f};
     float lo = 0.f, nm1 = 0.f, left = 0.f, f = 1.f;   // of the reference: what far values are lifted to, -m log2(e),
                                                       // what its rounding left out, 2^-that
-    float tmax = neg_inf();                   // this thread's largest so far
-    float tau = neg_inf();                    // K values at or above it lie in earlier blocks
-    unsigned long long kth = 0ull;            // set once a compaction knew the K-th key
-    int have = 0, seen = 0;                   // candidates before this block; when the bound was last taken from them
-    auto load_block = [&](long long base, uint4 (&x)[kLpVec]) {
-        if (base >= vs && base + BLK <= ve) {
-            const T* p = origin + (base + tid) * EPV;
-#pragma unroll
-            for (int k = 0; k < kLpVec; ++k) x[k] = ld_stream16(p + k * kLpThreads * EPV);
-        } else {
-#pragma unroll
-            for (int k = 0; k < kLpVec; ++k) x[k] = load_edge(base + k * kLpThreads + tid);
-        }
+    auto refer = [&](float m) {
+        if (s.m > neg_inf()) move_ref(s, m);
+        s.m = m;
+        lo = lifted(m);
+        nm1 = -(m * kL2E);
+        left = fmaf(m, kL2E, nm1);
+        f = ex2(-left);
     };
-    uint4 cur[kLpVec], nxt[kLpVec];
-    load_block(v0, cur);
-    int it = 0;
-    for (long long base = v0; base < v1; base += BLK, ++it) {
-        const bool more = base + BLK < v1;
-        if (more) load_block(base + BLK, nxt);
+    float tmax = neg_inf();                   // this thread's largest so far,
+    unsigned long long best = 0ull;           // and a key not above its own
+    unsigned long long bound = 0ull;          // K keys of the piece are at or above it
+    float tau = neg_inf();                    // its value
+    bool lost = false;                        // a wait gave up
+    for (int it = 0; it < blocks; ++it) {
+        const int stage = it % kLpStages;
+        lost = !mbar_wait_bounded(&sh.full[stage], (unsigned)(it / kLpStages) & 1u) || lost;
+        const int n = nvec - it * kLpBlock;
+        uint4 cur[kLpVec];
         float vm[kLpVec], bm = neg_inf();
+#pragma unroll
+        for (int k = 0; k < kLpVec; ++k) {
+            const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+            cur[k] = k * kLpThreads + tid < n ? sh.ring[stage][k * kLpThreads + tid] : make_uint4(none, none, none, none);
+        }
 #pragma unroll
         for (int k = 0; k < kLpVec; ++k) {
             vm[k] = vec_max(cur[k], T());
             bm = fmaxf(bm, vm[k]);
         }
         if (bm > neg_inf()) {
-            if (!(s.m > neg_inf()) || bm > s.m + 27.f) {
-                if (s.m > neg_inf()) move_ref(s, bm);
-                s.m = bm;
-                lo = lifted(bm);
-                nm1 = -(bm * kL2E);
-                left = fmaf(bm, kL2E, nm1);
-                f = ex2(-left);
-            }
+            if (!(s.m > neg_inf()) || bm > s.m + 27.f) refer(bm);
             if (fabsf(s.m) < 1e5f) {
                 const unsigned long long nm = pair(nm1, nm1);
                 unsigned long long S2 = 0ull, T2 = 0ull;
@@ -272,93 +338,83 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
                     for (int i = 0; i < EPV; ++i) add_one(s, Vec<T>::get(cur[k], i));
             }
         }
-        if (a.K > 0) {
-            auto push = [&](bool at_least) {
-                if (!(at_least ? bm >= tau : bm > tau)) return;
+        if (a.K > 0 && __any_sync(0xffffffffu, it == 0 || (bm >= tau && bm > neg_inf()))) {
+            // Candidates: the keys at or above a lower bound of the K-th.  Every
+            // warp vouches for its ceil(K / 8) largest thread maxima, and the
+            // smallest of those keys is such a bound; so is the smallest of a
+            // warp's 32 thread maxima.  After the first block the other warps'
+            // are read without a barrier: they only grow, so an older one is a
+            // bound as well.
+            const long long at = (vs + (long long)it * kLpBlock + tid) * EPV - h;
+            if (bm > tmax) {
+                tmax = bm;
+                const int k = vm[0] == bm ? 0 : vm[1] == bm ? 1 : vm[2] == bm ? 2 : 3;
+                best = pack_argmax(bm, (uint32_t)(at + k * kLpThreads * EPV + EPV - 1));   // the last it can be
+            }
+            unsigned long long rest = best, w = 0ull;
+            for (int r = 0; r < a.K; r += kLpWarps) {
+                w = warp_max_u32x2(rest);
+                if (rest == w) rest = 0ull;
+            }
+            if (lane == 0) *(volatile unsigned long long*)&sh.wkey[warp] = w;
+            if (it == 0) __syncthreads();
+            w = warp_min_u32x2(*(volatile unsigned long long*)&sh.wkey[lane & (kLpWarps - 1)]);
+            rest = warp_min_u32x2(best);
+            w = w > rest ? w : rest;
+            bound = w > bound ? w : bound;
+            tau = bound ? key_value(bound) : neg_inf();
+            if (bm >= tau && bm > neg_inf()) {
 #pragma unroll
                 for (int k = 0; k < kLpVec; ++k) {
-                    if (!(at_least ? vm[k] >= tau : vm[k] > tau)) continue;
+                    if (!(vm[k] >= tau)) continue;
 #pragma unroll
                     for (int i = 0; i < EPV; ++i) {
                         const float z = Vec<T>::get(cur[k], i);
-                        if ((at_least ? z >= tau : z > tau) && z > neg_inf()) {
-                            const int pos = atomicAdd(&sh.count, 1);
-                            if (pos < kLpCap)
-                                sh.buf[pos] = pack_argmax(z, (uint32_t)((base + k * kLpThreads + tid) * EPV - h + i));
+                        if (z >= tau && z > neg_inf()) {
+                            const unsigned long long key = pack_argmax(z, (uint32_t)(at + k * kLpThreads * EPV + i));
+                            if (key >= bound) {
+                                const int pos = atomicAdd(&sh.count, 1);
+                                if (pos < kLpCap) sh.buf[pos] = key;
+                            }
                         }
                     }
                 }
-            };
-            if (it > 0) push(false);
-            tmax = fmaxf(tmax, bm);
-            // a lower bound of the K-th largest so far: every warp vouches for
-            // its ceil(K / 16) largest thread maxima, the smallest of those counts
-            float wm = warp_max(tmax);
-            if (a.K > kLpWarps) {
-                const unsigned at = __ballot_sync(0xffffffffu, tmax == wm);
-                wm = warp_max(at && lane == __ffs(at) - 1 ? neg_inf() : tmax);
             }
-            if (lane == 0) sh.wmax[warp] = wm;
-            __syncthreads();
-            float t = sh.wmax[0];
-#pragma unroll
-            for (int w = 1; w < kLpWarps; ++w) t = fminf(t, sh.wmax[w]);
-            if (it == 0) {
-                tau = t;
-                push(true);
-                __syncthreads();
-            }
-            tau = fmaxf(tau, t);
-            int cnt = sh.count;
-            __syncthreads();   // every thread has the count before the next block adds to it
-            if (cnt > kLpCap) {
-                // more than the buffer holds (long ties, ascending rows): take this
-                // block again, one value per thread at a time, keeping the K best
-                // whenever the buffer is nearly full
-                if (tid == 0) sh.count = have;
-                __syncthreads();
-#pragma unroll 1
-                for (int e = 0; e < kLpVec * EPV; ++e) {
-                    if (sh.count > kLpCap - kLpThreads) {
-                        select_top(sh, sh.count, a.K);
-                        if (tid < a.K) sh.buf[tid] = sh.top[tid];
-                        kth = sh.top[a.K - 1];
-                        if (tid == 0) sh.count = a.K;
-                    }
-                    __syncthreads();
-                    float z = neg_inf();
-#pragma unroll
-                    for (int k = 0; k < kLpVec; ++k)
-#pragma unroll
-                        for (int i = 0; i < EPV; ++i)
-                            if (k * EPV + i == e) z = Vec<T>::get(cur[k], i);
-                    const unsigned long long key =
-                        pack_argmax(z, (uint32_t)((base + (e / EPV) * kLpThreads + tid) * EPV - h + e % EPV));
-                    if (z > neg_inf() && key > kth) sh.buf[atomicAdd(&sh.count, 1)] = key;
-                    __syncthreads();
-                }
-                if (kth) tau = fmaxf(tau, key_value(kth));
-                cnt = sh.count;
-                __syncthreads();
-            } else if (more && cnt >= a.K && cnt >= seen + a.K && cnt <= kLpThreads) {
-                // the K-th of the candidates themselves bounds better: every
-                // candidate counts the larger ones, the K-th tells the others
-                // (again once as many more have come in)
-                const unsigned long long mine = tid < cnt ? sh.buf[tid] : ~0ull;
-                int r = 0;
-                if (tid < cnt)
-                    for (int i = 0; i < cnt; ++i) r += sh.buf[i] > mine;
-                if (tid < cnt && r == a.K - 1) sh.wkey[0] = mine;
-                __syncthreads();
-                tau = fmaxf(tau, key_value(sh.wkey[0]));
-                seen = cnt;
-            }
-            have = cnt;
         }
-        if (more)
-#pragma unroll
-            for (int k = 0; k < kLpVec; ++k) cur[k] = nxt[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+        // refill the stage before this one, which the other warps have left by now
+        if (tid == 0 && it > 0 && it - 1 + kLpStages < blocks) {
+            const int prev = (it - 1) % kLpStages;
+            lost = !mbar_wait_bounded(&sh.empty[prev], (unsigned)((it - 1) / kLpStages) & 1u) || lost;
+            fence_proxy_async_smem();
+            fetch(it - 1 + kLpStages);
+        }
+        if (a.K > 0 && it == 0 && blocks > 1) {
+            // the K-th of the first block's candidates bounds better still
+            __syncthreads();
+            const int cnt = sh.count;
+            if (tid == 0) sh.bound = 0ull;
+            __syncthreads();
+            if (cnt >= a.K && cnt <= kLpThreads)
+                rank_all(sh.buf, cnt, [&](unsigned long long key, int r) {
+                    if (r == a.K - 1) sh.bound = key;
+                });
+            __syncthreads();
+            bound = sh.bound > bound ? sh.bound : bound;
+            tau = bound ? key_value(bound) : neg_inf();
+        }
     }
+    if (loose > neg_inf()) {
+        if (!(s.m > neg_inf()) || loose > s.m + 27.f) refer(loose);
+        add_one(s, loose);
+        const unsigned long long key = pack_argmax(loose, (uint32_t)loose_at);
+        if (a.K > 0 && key >= bound) {
+            const int pos = atomicAdd(&sh.count, 1);
+            if (pos < kLpCap) sh.buf[pos] = key;
+        }
+    }
+    if (lost) s.S = __uint_as_float(0x7FC00000u);   // (a copy that never came: no answer rather than a wrong one)
     // the piece's sums
     float M = warp_max(s.m);
     {
@@ -385,15 +441,18 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
         if (lane == 0) sh.piece = {M, w.S, w.T};
     }
     if (a.K > 0) {
-        const int n = sh.count;
-        if (n <= kLpThreads) {   // every candidate counts the larger ones
-            const unsigned long long mine = tid < n ? sh.buf[tid] : 0ull;
+        int n = sh.count;
+        if (n > kLpCap) {
+            const long long e0 = v0 * EPV - h, e1 = v1 * EPV - h;
+            select_slowly<T>(sh, rowp, e0 > 0 ? e0 : 0, e1 < a.V ? e1 : a.V, a.K);
+            n = sh.count;
+        }
+        if (n <= 2 * kLpThreads) {   // every candidate counts the larger ones
             if (tid < a.K) sh.top[tid] = 0ull;
-            int r = 0;
-            if (tid < n)
-                for (int i = 0; i < n; ++i) r += sh.buf[i] > mine;
             __syncthreads();
-            if (tid < n && r < a.K) sh.top[r] = mine;
+            rank_all(sh.buf, n, [&](unsigned long long key, int r) {
+                if (r < a.K) sh.top[r] = key;
+            });
         } else {
             select_top(sh, n, a.K);
         }
@@ -419,23 +478,33 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             }
         }
         if (a.K > 0) {
+            // the pieces' best; a piece's k-th cannot be among the K best if K keys
+            // of another piece are larger, so most are dropped before the ranking
             const int n = C * a.K;
-            unsigned long long mine = 0ull;
-            if (tid < n) {
-                mine = cluster.map_shared_rank(sh.top, tid / a.K)[tid % a.K];
-                sh.all[tid] = mine;
+            unsigned long long mine[2], least = 0ull;   // (16 pieces x 32 keys: two a thread)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int x = tid + i * kLpThreads;
+                mine[i] = x < n ? cluster.map_shared_rank(sh.top, x / a.K)[x % a.K] : 0ull;
+            }
+            if (tid < C) least = cluster.map_shared_rank(sh.top, tid)[a.K - 1];
+            if (tid == 0) sh.count = 0;
+            if (warp == 0) {
+                least = warp_max_u64(least);
+                if (lane == 0) sh.bound = least;
             }
             __syncthreads();
-            int r = 0, real = 0;
-            if (tid < n)
-                for (int i = 0; i < n; ++i) {
-                    r += sh.all[i] > mine;
-                    real += sh.all[i] != 0ull;
-                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (mine[i] != 0ull && mine[i] >= sh.bound) sh.buf[atomicAdd(&sh.count, 1)] = mine[i];
+            __syncthreads();
+            const int real = sh.count;
             const float m = sh.wsum[0].m, ls = logf(sh.wsum[0].S);
-            const bool put = mine != 0ull && r < a.K;
-            if (put && a.top_ids) a.top_ids[row * a.K + r] = (int32_t)unpack_index(mine);
-            if (put && a.top_logprobs) a.top_logprobs[row * a.K + r] = (key_value(mine) - m) - ls;
+            rank_all(sh.buf, real, [&](unsigned long long key, int r) {
+                if (r >= a.K) return;
+                if (a.top_ids) a.top_ids[row * a.K + r] = (int32_t)unpack_index(key);
+                if (a.top_logprobs) a.top_logprobs[row * a.K + r] = (key_value(key) - m) - ls;
+            });
             if (tid < a.K && tid >= real) {   // fewer logits above -inf than K
                 if (a.top_ids) a.top_ids[row * a.K + tid] = -1;
                 if (a.top_logprobs) a.top_logprobs[row * a.K + tid] = neg_inf();
@@ -455,20 +524,21 @@ cudaError_t launch(const LogprobArgs& a, int sms, cudaStream_t s) {
     if (dev < 0 || dev >= kMaxDev || !ready[dev]) {   // clusters of 16 are opt-in
         e = cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LpShared));
+        if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDev) ready[dev] = true;
     }
     // Pieces a row: the fewest waves of bytes (an SM's share of the bandwidth is
-    // about 45 bytes a ns), against some 2500 ns that each wave of two CTAs an SM
-    // costs in first loads, joins and cluster barriers; none below half a block
-    // of loads.
+    // about 45 bytes a ns, which takes three CTAs), against some 2500 ns that each
+    // wave of three CTAs an SM costs in first loads, joins and cluster barriers;
+    // none below half a block.
     int C = 1;
     double best = 1e30;
     for (int c = 1; c <= 16; c *= 2) {
-        const long long ctas = a.rows * c;
-        const double rate = ctas > sms ? 45.0 : 30.0;   // one CTA an SM has too few loads in flight
-        const double ns = (double)a.V * sizeof(T) / rate * (double)((ctas + sms - 1) / sms) / c +
-                          2500.0 * (double)((ctas + 2 * sms - 1) / (2 * sms));
-        if (c > 1 && a.V / c < (long long)kLpThreads * kLpVec * Vec<T>::n / 2) break;
+        if (c > 1 && a.V / c < (long long)kLpBlock * Vec<T>::n / 2) break;
+        const long long ctas = a.rows * c, deep = (ctas + sms - 1) / sms;
+        const double rate = deep >= 3 ? 45.0 : deep == 2 ? 40.0 : 25.0;
+        const double ns = (double)a.V * sizeof(T) / rate * (double)deep / c + 2500.0 * (double)((deep + 2) / 3);
         if (ns < best) {
             best = ns;
             C = c;
@@ -477,6 +547,7 @@ cudaError_t launch(const LogprobArgs& a, int sms, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.rows * C));
     cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = sizeof(LpShared);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
