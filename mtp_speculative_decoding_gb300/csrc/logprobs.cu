@@ -24,11 +24,11 @@ namespace mtp {
 
 namespace {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
 constexpr int kLpVec = 4;                         // 16-byte vectors of a block a thread takes
-constexpr int kLpBlock = kLpThreads * kLpVec;     // vectors of a block: one bulk copy of 16 KB
-constexpr int kLpStages = 3;                      // blocks in flight; three CTAs share an SM
-constexpr int kLpCap = 2048;                      // candidates of a piece (a first slab of ties fits: 256 threads x 8)
+constexpr int kLpBlock = kLpThreads * kLpVec;     // vectors of a block: one bulk copy of 32 KB
+constexpr int kLpStages = 2;                      // blocks in shared memory; two CTAs share an SM
+constexpr int kLpCap = 4096;                      // candidates of a piece (a first slab of ties fits: 512 threads x 8)
 constexpr float kL2E = 1.44269504f, kLn2 = 0.693147181f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -57,6 +57,8 @@ __device__ __forceinline__ bool mbar_wait_bounded(unsigned long long* bar, unsig
 }
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7F800000); }
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(uint16_t x) { return bf16_to_f32(x); }
 template <typename T> struct Vec;
 template <> struct Vec<uint16_t> {
     static constexpr int n = 8;
@@ -155,30 +157,73 @@ __device__ __forceinline__ void add_vec(const uint4& v, float lo, unsigned long 
 struct LpShared {
     uint4 ring[kLpStages][kLpBlock];
     unsigned long long buf[kLpCap];           // candidates, in no order
+    unsigned long long sel[kLpThreads];       // those still above the bound at the end
     unsigned long long top[MTP_MAX_TOP];      // the piece's best, descending
-    unsigned long long wkey[kLpWarps];        // what each warp vouches for
+    unsigned long long wkey[8 * kLpWarps];    // the first block's largest thread maxima, up to 8 a warp
     unsigned long long bound;
     unsigned long long full[kLpStages], empty[kLpStages];
     Sums wsum[kLpWarps];
     Sums piece;
-    int count;
+    int count, nsel;                          // candidates; entries of sel
 };
 
-// Ranks (numbers of larger keys) of n distinct keys; put(key, rank) for each.
-template <typename F>
-__device__ __forceinline__ void rank_all(const unsigned long long* key, int n, F put) {
-    int glog = 0;   // threads of a key: as many as there are
+// The code below a block's sums runs a few times a CTA, and what it costs is
+// mostly the fetching of its instructions: it is kept in functions that the
+// several places share.
+
+// The K largest of n <= 512 distinct keys into out[], descending: every key
+// counts the larger ones, with as many threads as there are.  (Barriers are
+// the caller's.)
+__device__ __noinline__ void rank_keys(const unsigned long long* key, int n, int K, unsigned long long* out) {
+    int glog = 0;
     while (glog < 5 && n << (glog + 1) <= kLpThreads) ++glog;
-    const int g = 1 << glog;
-    for (int base = 0; base < n; base += kLpThreads >> glog) {
-        const int which = base + ((int)threadIdx.x >> glog);
-        const unsigned long long mine = which < n ? key[which] : ~0ull;
-        int r = 0;
-#pragma unroll 4
-        for (int i = (int)threadIdx.x & (g - 1); i < n; i += g) r += key[i] > mine;
-        for (int o = g >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-        if (which < n && ((int)threadIdx.x & (g - 1)) == 0) put(mine, r);
+    const int g = 1 << glog, which = (int)threadIdx.x >> glog;
+    const unsigned long long mine = which < n ? key[which] : ~0ull;
+    int r = 0;
+#pragma unroll 1
+    for (int i = (int)threadIdx.x & (g - 1); i < n; i += g) r += key[i] > mine;
+#pragma unroll 1
+    for (int o = g >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    if (which < n && r < K) out[r] = mine;
+}
+// A key that K of n <= 256 keys are at or above (0: there are fewer than K), by
+// one warp: the longest 16-bit prefix that K keys reach, bit by bit, and the
+// smallest key that reaches it.
+__device__ __noinline__ unsigned long long bound_of(const unsigned long long* keys, int n, int K) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = lane + 32 * i < n ? keys[lane + 32 * i] : 0ull;
+    unsigned p = 0u;
+#pragma unroll 1
+    for (unsigned bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+        const unsigned t = p | bit;
+        unsigned c = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c += (unsigned)(x[i] >> 32) >= t;
+        if (__reduce_add_sync(0xffffffffu, c) >= (unsigned)K) p = t;
     }
+    if (p == 0u) return 0ull;
+    unsigned long long m = ~0ull;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if ((unsigned)(x[i] >> 32) >= p && x[i] < m) m = x[i];
+    return warp_min_u32x2(m);
+}
+// sums of a warp's lanes (m = -inf: none), relative to the largest reference
+__device__ __noinline__ Sums join_warp(Sums w) {
+    const float M = warp_max(w.m);
+    if (M > neg_inf()) {
+        if (w.m > neg_inf()) move_ref(w, M);
+        else w = {M, 0.f, 0.f};
+    }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) {
+        w.S += __shfl_xor_sync(0xffffffffu, w.S, o);
+        w.T += __shfl_xor_sync(0xffffffffu, w.T, o);
+    }
+    w.m = M;
+    return w;
 }
 
 // the K largest of buf[0, n) into top[], descending (0: none)
@@ -234,7 +279,7 @@ __device__ __forceinline__ float key_value(unsigned long long key) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_constant__ LogprobArgs a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     LpShared& sh = *reinterpret_cast<LpShared*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
@@ -272,7 +317,9 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
         mbar_fence_init();
         for (int i = 0; i < kLpStages && i < blocks; ++i) fetch(i);
         sh.count = 0;
+        sh.nsel = 0;
     }
+    if (tid < a.K) sh.top[tid] = 0ull;
     float zt = neg_inf();
     if (tid == 0 && rank == 0 && tok >= 0) zt = ld_elem<T>(rowp, tok);
     // a loose element of this thread
@@ -297,14 +344,20 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
         left = fmaf(m, kL2E, nm1);
         f = ex2(-left);
     };
-    float tmax = neg_inf();                   // this thread's largest so far,
-    unsigned long long best = 0ull;           // and a key not above its own
     unsigned long long bound = 0ull;          // K keys of the piece are at or above it
     float tau = neg_inf();                    // its value
+    int check = 3;                            // the block after which it is next taken from the candidates
     bool lost = false;                        // a wait gave up
     for (int it = 0; it < blocks; ++it) {
         const int stage = it % kLpStages;
         lost = !mbar_wait_bounded(&sh.full[stage], (unsigned)(it / kLpStages) & 1u) || lost;
+        if (tid == 0 && it > 0 && it - 1 + kLpStages < blocks) {
+            // refill the stage before this one, which the other warps leave about now
+            const int prev = (it - 1) % kLpStages;
+            lost = !mbar_wait_bounded(&sh.empty[prev], (unsigned)((it - 1) / kLpStages) & 1u) || lost;
+            fence_proxy_async_smem();
+            fetch(it - 1 + kLpStages);
+        }
         const int n = nvec - it * kLpBlock;
         uint4 cur[kLpVec];
         float vm[kLpVec], bm = neg_inf();
@@ -332,77 +385,76 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
                 s.S = fmaf(f, x, s.S);
                 s.T = fmaf(f, fmaf(-left, x, u + v), s.T);
             } else {   // a reference whose products round by whole bits (masks of the type's lowest value), an infinity
-#pragma unroll
-                for (int k = 0; k < kLpVec; ++k)
-#pragma unroll
-                    for (int i = 0; i < EPV; ++i) add_one(s, Vec<T>::get(cur[k], i));
+#pragma unroll 1
+                for (int i = 0; i < kLpVec * EPV; ++i) {
+                    const int v = i / EPV * kLpThreads + tid;
+                    if (v < n) add_one(s, to_float(reinterpret_cast<const T*>(sh.ring[stage])[v * EPV + i % EPV]));
+                }
             }
         }
-        if (a.K > 0 && __any_sync(0xffffffffu, it == 0 || (bm >= tau && bm > neg_inf()))) {
-            // Candidates: the keys at or above a lower bound of the K-th.  Every
-            // warp vouches for its ceil(K / 8) largest thread maxima, and the
-            // smallest of those keys is such a bound; so is the smallest of a
-            // warp's 32 thread maxima.  After the first block the other warps'
-            // are read without a barrier: they only grow, so an older one is a
-            // bound as well.
-            const long long at = (vs + (long long)it * kLpBlock + tid) * EPV - h;
-            if (bm > tmax) {
-                tmax = bm;
+        if (a.K > 0) {
+            // Candidates: the keys at or above a lower bound of the K-th.
+            const long long at = (vs + (long long)it * kLpBlock) * EPV - h;   // element 0 of the block
+            if (it == 0) {
+                // The first bound is the K-th of the largest thread maxima (the K best
+                // mostly lie in different threads): up to eight of every warp.  (A
+                // maximum's key with the last index that it can have is not above
+                // its own.)
                 const int k = vm[0] == bm ? 0 : vm[1] == bm ? 1 : vm[2] == bm ? 2 : 3;
-                best = pack_argmax(bm, (uint32_t)(at + k * kLpThreads * EPV + EPV - 1));   // the last it can be
+                unsigned long long rest =
+                    bm > neg_inf() ? pack_argmax(bm, (uint32_t)(at + (k * kLpThreads + tid) * EPV + EPV - 1)) : 0ull;
+                const int R = a.K < 8 ? a.K : 8;
+#pragma unroll 1
+                for (int r = 0; r < R; ++r) {
+                    const unsigned long long w = warp_max_u32x2(rest);
+                    if (lane == 0) sh.wkey[r * kLpWarps + warp] = w;
+                    if (rest == w) rest = 0ull;
+                }
+                __syncthreads();
+                if (warp == 0) {
+                    const unsigned long long b = bound_of(sh.wkey, R * kLpWarps, a.K);
+                    if (lane == 0) sh.bound = b;
+                }
+                __syncthreads();
+                bound = sh.bound;
+                tau = bound ? key_value(bound) : neg_inf();
             }
-            unsigned long long rest = best, w = 0ull;
-            for (int r = 0; r < a.K; r += kLpWarps) {
-                w = warp_max_u32x2(rest);
-                if (rest == w) rest = 0ull;
-            }
-            if (lane == 0) *(volatile unsigned long long*)&sh.wkey[warp] = w;
-            if (it == 0) __syncthreads();
-            w = warp_min_u32x2(*(volatile unsigned long long*)&sh.wkey[lane & (kLpWarps - 1)]);
-            rest = warp_min_u32x2(best);
-            w = w > rest ? w : rest;
-            bound = w > bound ? w : bound;
-            tau = bound ? key_value(bound) : neg_inf();
-            if (bm >= tau && bm > neg_inf()) {
+            int mask = 0;   // this lane's vectors that hold a candidate
 #pragma unroll
-                for (int k = 0; k < kLpVec; ++k) {
-                    if (!(vm[k] >= tau)) continue;
+            for (int k = 0; k < kLpVec; ++k) mask |= vm[k] >= tau && vm[k] > neg_inf() ? 1 << k : 0;
+#pragma unroll 1
+            while (__any_sync(0xffffffffu, mask != 0)) {
+                const int v = (__ffs(mask) - 1) * kLpThreads + tid;
+                if (mask) {
+                    const uint4 x = sh.ring[stage][v];
 #pragma unroll
                     for (int i = 0; i < EPV; ++i) {
-                        const float z = Vec<T>::get(cur[k], i);
+                        const float z = Vec<T>::get(x, i);
                         if (z >= tau && z > neg_inf()) {
-                            const unsigned long long key = pack_argmax(z, (uint32_t)(at + k * kLpThreads * EPV + i));
-                            if (key >= bound) {
-                                const int pos = atomicAdd(&sh.count, 1);
-                                if (pos < kLpCap) sh.buf[pos] = key;
-                            }
+                            const unsigned long long key = pack_argmax(z, (uint32_t)(at + v * EPV + i));
+                            const int pos = key >= bound ? atomicAdd(&sh.count, 1) : kLpCap;
+                            if (pos < kLpCap) sh.buf[pos] = key;
                         }
                     }
                 }
+                mask &= mask - 1;
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);
-        // refill the stage before this one, which the other warps have left by now
-        if (tid == 0 && it > 0 && it - 1 + kLpStages < blocks) {
-            const int prev = (it - 1) % kLpStages;
-            lost = !mbar_wait_bounded(&sh.empty[prev], (unsigned)((it - 1) / kLpStages) & 1u) || lost;
-            fence_proxy_async_smem();
-            fetch(it - 1 + kLpStages);
-        }
-        if (a.K > 0 && it == 0 && blocks > 1) {
-            // the K-th of the first block's candidates bounds better still
+        if (a.K > 0 && it == check && it + 1 < blocks) {
+            // the candidates so far bound better; again after blocks 12, 39, .., so
+            // that each block adds fewer
             __syncthreads();
             const int cnt = sh.count;
-            if (tid == 0) sh.bound = 0ull;
+            if (warp == 0 && cnt <= 256) {
+                const unsigned long long b = bound_of(sh.buf, cnt, a.K);
+                if (lane == 0) sh.bound = b;
+            }
             __syncthreads();
-            if (cnt >= a.K && cnt <= kLpThreads)
-                rank_all(sh.buf, cnt, [&](unsigned long long key, int r) {
-                    if (r == a.K - 1) sh.bound = key;
-                });
-            __syncthreads();
-            bound = sh.bound > bound ? sh.bound : bound;
+            bound = sh.bound;   // (not below the one before: K candidates are at or above that)
             tau = bound ? key_value(bound) : neg_inf();
+            check = 3 * check + 3;
         }
     }
     if (loose > neg_inf()) {
@@ -416,29 +468,12 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
     }
     if (lost) s.S = __uint_as_float(0x7FC00000u);   // (a copy that never came: no answer rather than a wrong one)
     // the piece's sums
-    float M = warp_max(s.m);
-    {
-        Sums w = s;
-        if (M > neg_inf()) {
-            if (w.m > neg_inf()) move_ref(w, M);
-            else w = {M, 0.f, 0.f};
-        }
-        w.S = warp_sum(w.S);
-        w.T = warp_sum(w.T);
-        w.m = M;
-        if (lane == 0) sh.wsum[warp] = w;
-    }
+    s = join_warp(s);
+    if (lane == 0) sh.wsum[warp] = s;
     __syncthreads();
     if (warp == 0) {
-        Sums w = lane < kLpWarps ? sh.wsum[lane] : Sums{neg_inf(), 0.f, 0.f};
-        M = warp_max(w.m);
-        if (M > neg_inf()) {
-            if (w.m > neg_inf()) move_ref(w, M);
-            else w = {M, 0.f, 0.f};
-        }
-        w.S = warp_sum(w.S);
-        w.T = warp_sum(w.T);
-        if (lane == 0) sh.piece = {M, w.S, w.T};
+        s = join_warp(lane < kLpWarps ? sh.wsum[lane] : Sums{neg_inf(), 0.f, 0.f});
+        if (lane == 0) sh.piece = s;
     }
     if (a.K > 0) {
         int n = sh.count;
@@ -447,67 +482,62 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
             select_slowly<T>(sh, rowp, e0 > 0 ? e0 : 0, e1 < a.V ? e1 : a.V, a.K);
             n = sh.count;
         }
-        if (n <= 2 * kLpThreads) {   // every candidate counts the larger ones
-            if (tid < a.K) sh.top[tid] = 0ull;
-            __syncthreads();
-            rank_all(sh.buf, n, [&](unsigned long long key, int r) {
-                if (r < a.K) sh.top[r] = key;
-            });
-        } else {
-            select_top(sh, n, a.K);
+        if (tid < a.K) sh.top[tid] = 0ull;
+        for (int i = tid; i < n; i += kLpThreads) {
+            const unsigned long long key = sh.buf[i];
+            if (key >= bound) {   // (what is below it by now cannot be among the K)
+                const int pos = atomicAdd(&sh.nsel, 1);
+                if (pos < kLpThreads) sh.sel[pos] = key;
+            }
         }
+        __syncthreads();
+        if (sh.nsel <= kLpThreads) rank_keys(sh.sel, sh.nsel, a.K, sh.top);
+        else select_top(sh, n, a.K);
     }
-    __syncthreads();
     if (C > 1) cluster.sync();
+    else __syncthreads();
     if (rank == 0) {
         if (warp == 0) {
-            Sums w = lane < C ? *cluster.map_shared_rank(&sh.piece, lane < C ? lane : 0) : Sums{neg_inf(), 0.f, 0.f};
-            M = warp_max(w.m);
-            if (M > neg_inf()) {
-                if (w.m > neg_inf()) move_ref(w, M);
-                else w = {M, 0.f, 0.f};
-            }
-            w.S = warp_sum(w.S);
-            w.T = warp_sum(w.T);
-            w.m = M;
+            Sums w = {neg_inf(), 0.f, 0.f};
+            if (lane < C) w = *cluster.map_shared_rank(&sh.piece, lane);
+            w = join_warp(w);
             if (lane == 0) {
                 sh.wsum[0] = w;
                 const float ls = logf(w.S);
-                if (a.logprob) a.logprob[row] = ((zt == zt ? zt : neg_inf()) - M) - ls;
+                if (a.logprob) a.logprob[row] = ((zt == zt ? zt : neg_inf()) - w.m) - ls;
                 if (a.entropy) a.entropy[row] = ls - kLn2 * (w.T / w.S);
             }
         }
         if (a.K > 0) {
-            // the pieces' best; a piece's k-th cannot be among the K best if K keys
-            // of another piece are larger, so most are dropped before the ranking
-            const int n = C * a.K;
-            unsigned long long mine[2], least = 0ull;   // (16 pieces x 32 keys: two a thread)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int x = tid + i * kLpThreads;
-                mine[i] = x < n ? cluster.map_shared_rank(sh.top, x / a.K)[x % a.K] : 0ull;
-            }
-            if (tid < C) least = cluster.map_shared_rank(sh.top, tid)[a.K - 1];
-            if (tid == 0) sh.count = 0;
-            if (warp == 0) {
-                least = warp_max_u64(least);
-                if (lane == 0) sh.bound = least;
+            int real = a.K;
+            const unsigned long long* best = sh.top;   // one piece: its own
+            if (C > 1) {
+                // a piece's k-th cannot be among the K best if K keys of another are
+                // larger, so most are dropped before the ranking
+                const int n = C * a.K;   // at most 16 pieces x 32 keys: one a thread
+                unsigned long long mine = 0ull, least = 0ull;
+                if (tid < n) mine = cluster.map_shared_rank(sh.top, tid / a.K)[tid % a.K];
+                if (warp == 0) {
+                    if (lane < C) least = cluster.map_shared_rank(sh.top, lane)[a.K - 1];
+                    least = warp_max_u32x2(least);
+                    if (lane == 0) {
+                        sh.bound = least;
+                        sh.count = 0;
+                    }
+                }
+                __syncthreads();
+                if (mine != 0ull && mine >= sh.bound) sh.buf[atomicAdd(&sh.count, 1)] = mine;
+                __syncthreads();
+                real = sh.count;
+                rank_keys(sh.buf, real, a.K, sh.sel);
+                best = sh.sel;
             }
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (mine[i] != 0ull && mine[i] >= sh.bound) sh.buf[atomicAdd(&sh.count, 1)] = mine[i];
-            __syncthreads();
-            const int real = sh.count;
-            const float m = sh.wsum[0].m, ls = logf(sh.wsum[0].S);
-            rank_all(sh.buf, real, [&](unsigned long long key, int r) {
-                if (r >= a.K) return;
-                if (a.top_ids) a.top_ids[row * a.K + r] = (int32_t)unpack_index(key);
-                if (a.top_logprobs) a.top_logprobs[row * a.K + r] = (key_value(key) - m) - ls;
-            });
-            if (tid < a.K && tid >= real) {   // fewer logits above -inf than K
-                if (a.top_ids) a.top_ids[row * a.K + tid] = -1;
-                if (a.top_logprobs) a.top_logprobs[row * a.K + tid] = neg_inf();
+            if (tid < a.K) {
+                const unsigned long long key = tid < real ? best[tid] : 0ull;   // 0: fewer logits above -inf than K
+                if (a.top_ids) a.top_ids[row * a.K + tid] = key ? (int32_t)unpack_index(key) : -1;
+                if (a.top_logprobs)
+                    a.top_logprobs[row * a.K + tid] = key ? (key_value(key) - sh.wsum[0].m) - logf(sh.wsum[0].S) : neg_inf();
             }
         }
     }
@@ -529,16 +559,16 @@ cudaError_t launch(const LogprobArgs& a, int sms, cudaStream_t s) {
         if (dev >= 0 && dev < kMaxDev) ready[dev] = true;
     }
     // Pieces a row: the fewest waves of bytes (an SM's share of the bandwidth is
-    // about 45 bytes a ns, which takes three CTAs), against some 2500 ns that each
-    // wave of three CTAs an SM costs in first loads, joins and cluster barriers;
+    // about 45 bytes a ns, which takes two CTAs), against some 2500 ns that each
+    // wave of two CTAs an SM costs in first loads, joins and cluster barriers;
     // none below half a block.
     int C = 1;
     double best = 1e30;
     for (int c = 1; c <= 16; c *= 2) {
         if (c > 1 && a.V / c < (long long)kLpBlock * Vec<T>::n / 2) break;
         const long long ctas = a.rows * c, deep = (ctas + sms - 1) / sms;
-        const double rate = deep >= 3 ? 45.0 : deep == 2 ? 40.0 : 25.0;
-        const double ns = (double)a.V * sizeof(T) / rate * (double)deep / c + 2500.0 * (double)((deep + 2) / 3);
+        const double rate = deep >= 2 ? 45.0 : 30.0;
+        const double ns = (double)a.V * sizeof(T) / rate * (double)deep / c + 2500.0 * (double)((deep + 1) / 2);
         if (ns < best) {
             best = ns;
             C = c;
