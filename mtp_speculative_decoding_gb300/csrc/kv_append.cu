@@ -117,20 +117,24 @@ __device__ __forceinline__ float unit_amax(const float (&p)[8], const float (&q)
     return fmaxf(m, n);
 }
 __device__ __forceinline__ bool is_inf(float x) { return x > 3.402823466e38f; }
-// 8 values times inv as e4m3 codes (nearest even, saturating; NaN becomes NaN,
-// and so does an infinity where `inf` says that there may be one)
-__device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8], float inv, bool inf) {
-    uint32_t w[4];
+// infinities to NaN (a unit of a page whose maximum showed one)
+__device__ __forceinline__ void drop_inf(float (&p)[8], float (&q)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float lo = x[2 * i] * inv, hi = x[2 * i + 1] * inv;
-        if (inf) {
-            lo = is_inf(fabsf(x[2 * i])) ? __uint_as_float(0x7FC00000u) : lo;
-            hi = is_inf(fabsf(x[2 * i + 1])) ? __uint_as_float(0x7FC00000u) : hi;
-        }
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+    for (int e = 0; e < 8; ++e) {
+        if (is_inf(fabsf(p[e]))) p[e] = __uint_as_float(0x7FC00000u);
+        if (is_inf(fabsf(q[e]))) q[e] = __uint_as_float(0x7FC00000u);
     }
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+// 8 values times inv as e4m3 codes (nearest even, saturating; NaN becomes NaN)
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t join16(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x5410); }
+__device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8], float inv) {
+    return make_uint2(join16(e4m3x2(x[0] * inv, x[1] * inv), e4m3x2(x[2] * inv, x[3] * inv)),
+                      join16(e4m3x2(x[4] * inv, x[5] * inv), e4m3x2(x[6] * inv, x[7] * inv)));
 }
 
 // The page's older codes, re-rounded to a scale that grew by 1/f.
@@ -218,25 +222,30 @@ __global__ void __launch_bounds__(256) append_e4m3_kernel(const __grid_constant_
     };
     float m = block_max(unit_amax(p, q, false));
     const bool inf = is_inf(m);
-    if (inf) m = block_max(unit_amax(p, q, true));
+    if (inf) {
+        m = block_max(unit_amax(p, q, true));
+        drop_inf(p, q);
+    }
     const float now = fmaxf(pow2i(e4m3_exponent(m)), had), inv = 1.f / now;   // powers of two: exact
     if (x == 0) *sc = now;
     if (x < units) {
         uint8_t* d = dst + (w.off + (x >> ulog)) * a.c.st + 8 * c;
-        *reinterpret_cast<uint2*>(d) = pack_e4m3(p, inv, inf);
-        *reinterpret_cast<uint2*>(d + (a.hd >> 1)) = pack_e4m3(q, inv, inf);
+        *reinterpret_cast<uint2*>(d) = pack_e4m3(p, inv);
+        *reinterpret_cast<uint2*>(d + (a.hd >> 1)) = pack_e4m3(q, inv);
     }
     if (had > 0.f && had != now) reround(dst, a.c.st, w.off, ulog, had * inv);
 }
 
-// Many rows a page (prompts): a CTA of 512 threads takes the keys or the
-// values of a page for `hpt` KV heads after one another; the next head's rows
-// are on their way while this one's are rounded, and the angles are computed
-// once for all heads, slot s of the page as the product of the rotations by its
-// 16-slot base and by s % 16 (20 sines a pair for a page of 64 instead of 64;
-// the product costs the angle 3 u).  ONE: a head's rows fit two units a thread
-// and stay in registers between the maximum and the rounding; larger pages are
-// read twice, the second time from L2.
+// Many rows a page (prompts): a CTA of up to 512 threads takes the keys or the
+// values of a page for `hpt` KV heads after one another, a thread two units of
+// them; the next head's rows are on their way while this one's are rounded, and
+// the angles are computed once for all heads, slot s of the page as the product
+// of the rotations by its 16-slot base and by s % 16 (20 sines a pair for a page
+// of 64 instead of 64; the product costs the angle 3 u).  The norm's factor of
+// a row only scales it, so it joins the maximum and the scale's inverse.  ONE:
+// the page has at most 1024 units of a head, and they stay in registers between
+// the maximum and the rounding; larger pages are read twice, the second time
+// from L2.
 constexpr int kPageThreads = 512;
 
 template <typename IT> struct Raw { uint4 v[4 * sizeof(IT) / 4]; };   // a unit as loaded
@@ -268,11 +277,24 @@ __device__ __forceinline__ void raw_open(const Raw<float>& r, float (&p)[8], flo
     }
 }
 
+// gains, without the row's factor, which is returned
+__device__ __forceinline__ float unit_gain(float (&a)[8], float (&b)[8], const float* gain, int c, int hd, float eps) {
+    const float r = unit_rms(a, b, hd, eps);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 g = *reinterpret_cast<const float4*>(gain + 8 * c + 4 * h);
+        const float4 k = *reinterpret_cast<const float4*>(gain + (hd >> 1) + 8 * c + 4 * h);
+        a[4 * h] *= g.x; a[4 * h + 1] *= g.y; a[4 * h + 2] *= g.z; a[4 * h + 3] *= g.w;
+        b[4 * h] *= k.x; b[4 * h + 1] *= k.y; b[4 * h + 2] *= k.z; b[4 * h + 3] *= k.w;
+    }
+    return r;
+}
+
 template <typename IT, bool ONE>
 __global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(const __grid_constant__ AppendArgs a) {
     extern __shared__ __align__(16) float2 s_rot[];   // [ps / 16][hd / 2] bases, [16][hd / 2] steps
     __shared__ __align__(16) float s_gain[512];
-    __shared__ __align__(16) float red[2][kPageThreads / 32];
+    __shared__ unsigned red[2][32];
     const int ps = 1 << a.c.ps_log2, nt = (a.M + ps - 2) / ps + 1;
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y == 0 && blockIdx.z == 0) append_status(a);
@@ -282,34 +304,39 @@ __global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(cons
     if (!page_rows(a, nt, w)) return;
     constexpr int UPT = 2;
     const bool key = blockIdx.z == 0, rot = key && a.rope.on, nrm = key && a.k_norm;
-    const int tid = threadIdx.x, U = a.hd >> 4, ulog = 31 - __clz(U), units = (w.j1 - w.j0) << ulog, half = a.hd >> 1;
-    const int g0 = blockIdx.y * a.hpt, step = kPageThreads * UPT;
-    const int c = tid & (U - 1);   // the same for all of a thread's units
-    const IT* src = reinterpret_cast<const IT*>(key ? a.k : a.v) + w.b * a.sb + g0 * a.sh + 8 * c;
-    uint8_t* dst = reinterpret_cast<uint8_t*>(key ? a.c.k : a.c.v) + w.page * a.c.sp + g0 * a.c.sh;
+    const int tid = threadIdx.x, T = blockDim.x, lane = tid & 31, ulog = 27 - __clz(a.hd), half = a.hd >> 1;
+    const int units = (w.j1 - w.j0) << ulog, g0 = blockIdx.y * a.hpt;
+    const int c = tid & ((1 << ulog) - 1);   // the same for all of a thread's units
+    const IT* src = reinterpret_cast<const IT*>(key ? a.k : a.v) + w.b * a.sb + w.j0 * a.sm + g0 * a.sh + 8 * c;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(key ? a.c.k : a.c.v) + w.page * a.c.sp + w.off * a.c.st + g0 * a.c.sh + 8 * c;
     float* scale = (key ? a.c.ks : a.c.vs) + (long long)w.page * a.c.Hkv + g0;
-    auto row = [&](int base, int i) {
-        const int x = base + i * kPageThreads + tid;
-        return x < units ? x >> ulog : 0;
-    };
+    auto row = [&](int x) { return x < units ? x >> ulog : 0; };
+    const IT* from[UPT];   // the thread's units of this head, and where they go
+    uint8_t* to[UPT];
     Raw<IT> raw[UPT];
 #pragma unroll
-    for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(0, i)) * a.sm, half, raw[i]);
+    for (int i = 0; i < UPT; ++i) {
+        from[i] = src + row(tid + i * T) * a.sm;
+        to[i] = tid + i * T < units ? dst + row(tid + i * T) * a.c.st : nullptr;
+        raw_load(from[i], half, raw[i]);
+    }
     if (nrm)
-        for (int i = tid; i < a.hd; i += kPageThreads) s_gain[i] = a.k_norm[i];
+        for (int i = tid; i < a.hd; i += T) s_gain[i] = a.k_norm[i];
     const int nb = ps >> 4;
     if (rot) {
-        const int pr = tid & (half - 1);   // one pair a thread: its table entries are read once
+        const int pr = tid & (half - 1), step = T / half;   // one pair a thread: its table entries are read once
         const float hi = a.rope.hi[pr], lo = a.rope.lo[pr];
-        for (int e = tid / half; e < nb + 16; e += kPageThreads / half) {
-            float pl, ph;
-            split_pos(e < nb ? w.first + 16 * e : e - nb, pl, ph);
-            float2 r;
-            pair_angle<false>(pl, ph, hi, lo, r.x, r.y);
-            s_rot[e * half + pr] = r;
-        }
+        if (tid < step * half)
+            for (int e = tid / half; e < nb + 16; e += step) {
+                float pl, ph;
+                split_pos(e < nb ? w.first + 16 * e : e - nb, pl, ph);
+                float2 r;
+                pair_angle<false>(pl, ph, hi, lo, r.x, r.y);
+                s_rot[e * half + pr] = r;
+            }
     }
-    if (rot || nrm) __syncthreads();
+    if (tid < 32) red[0][tid] = red[1][tid] = 0u;   // (warps that are not there)
+    __syncthreads();
     auto angles = [&](int r, float (&cs)[8], float (&sn)[8]) {
         const int s = w.off + r;
         const float4* x = reinterpret_cast<const float4*>(s_rot + (s >> 4) * half + 8 * c);
@@ -326,83 +353,89 @@ __global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(cons
     float cs[ONE ? UPT : 1][8], sn[ONE ? UPT : 1][8];
     if (ONE && rot)
 #pragma unroll
-        for (int i = 0; i < UPT; ++i) angles(row(0, i), cs[ONE ? i : 0], sn[ONE ? i : 0]);
-    float p[UPT][8], q[UPT][8];
-    auto turn = [&](int base) {   // raw -> p, q
-#pragma unroll
-        for (int i = 0; i < UPT; ++i) {
-            raw_open(raw[i], p[i], q[i]);
-            if (nrm) unit_norm_staged(p[i], q[i], s_gain, c, a.hd, a.eps);
-            if (rot) {
-                if (!ONE) angles(row(base, i), cs[0], sn[0]);
-                unit_rotate(p[i], q[i], cs[ONE ? i : 0], sn[ONE ? i : 0]);
-            }
+        for (int i = 0; i < UPT; ++i) angles(row(tid + i * T), cs[ONE ? i : 0], sn[ONE ? i : 0]);
+    float p[UPT][8], q[UPT][8], f[UPT];   // a unit is f (p, q)
+    auto turn = [&](int x, int i) {        // raw -> p, q, f
+        raw_open(raw[i], p[i], q[i]);
+        f[i] = 1.f;
+        if (nrm) f[i] = unit_gain(p[i], q[i], s_gain, c, a.hd, a.eps);
+        if (rot) {
+            if (!ONE) angles(row(x), cs[0], sn[0]);
+            unit_rotate(p[i], q[i], cs[ONE ? i : 0], sn[ONE ? i : 0]);
         }
     };
+    // a unit's largest magnitude; its finite ones' where it is asked for
+    auto unit_max = [&](int i, bool finite_only) { return unit_amax(p[i], q[i], finite_only) * f[i]; };
     int turns = 0;
+    auto block_max = [&](float m) {   // (magnitudes order as their bits)
+        const unsigned u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (lane == 0) red[turns & 1][tid >> 5] = u;
+        __syncthreads();
+        m = __uint_as_float(__reduce_max_sync(0xffffffffu, red[turns & 1][lane]));
+        ++turns;
+        return m;
+    };
+#pragma unroll 1
     for (int g = 0; g < a.hpt; ++g) {
         const float had = w.off > 0 ? scale[g] : 0.f;
         float m = 0.f;
-        for (int base = 0; base < units; base += step) {
-            if (!ONE && base > 0)
+        if (ONE) {
 #pragma unroll
-                for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(base, i)) * a.sm + g * a.sh, half, raw[i]);
-            turn(base);
-            if (ONE && g + 1 < a.hpt)
-#pragma unroll
-                for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(0, i)) * a.sm + (g + 1) * a.sh, half, raw[i]);
-#pragma unroll
-            for (int i = 0; i < UPT; ++i) m = fmaxf(m, unit_amax(p[i], q[i], false));
-        }
-        auto block_max = [&](float m) {
-            m = warp_max(m);
-            if ((tid & 31) == 0) red[turns & 1][tid >> 5] = m;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kPageThreads / 128; ++i) {
-                const float4 r = reinterpret_cast<const float4*>(red[turns & 1])[i];
-                m = fmaxf(fmaxf(m, fmaxf(r.x, r.y)), fmaxf(r.z, r.w));
+            for (int i = 0; i < UPT; ++i) {
+                turn(0, i);
+                from[i] += a.sh;
+                if (g + 1 < a.hpt) raw_load(from[i], half, raw[i]);
             }
-            ++turns;
-            return m;
-        };
+#pragma unroll
+            for (int i = 0; i < UPT; ++i) m = fmaxf(m, unit_max(i, false));
+        } else {
+            for (int base = tid; base - tid < units; base += T) {
+                raw_load(src + row(base) * a.sm + g * a.sh, half, raw[0]);
+                turn(base, 0);
+                m = fmaxf(m, unit_max(0, false));
+            }
+        }
         m = block_max(m);
         const bool inf = is_inf(m);
         if (inf) {   // the finite values alone
             m = 0.f;
-            for (int base = 0; base < units; base += step) {
-                if (!ONE) {
+            if (ONE) {
 #pragma unroll
-                    for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(base, i)) * a.sm + g * a.sh, half, raw[i]);
-                    turn(base);
+                for (int i = 0; i < UPT; ++i) m = fmaxf(m, is_inf(f[i]) ? 0.f : unit_max(i, true));
+            } else {
+                for (int base = tid; base - tid < units; base += T) {
+                    raw_load(src + row(base) * a.sm + g * a.sh, half, raw[0]);
+                    turn(base, 0);
+                    m = fmaxf(m, is_inf(f[0]) ? 0.f : unit_max(0, true));
                 }
-#pragma unroll
-                for (int i = 0; i < UPT; ++i) m = fmaxf(m, unit_amax(p[i], q[i], true));
             }
-            m = block_max(m);
+            m = block_max(is_inf(m) ? 3.402823466e38f : m);
         }
         const float now = fmaxf(pow2i(e4m3_exponent(m)), had), inv = 1.f / now;   // powers of two: exact
         if (tid == 0) scale[g] = now;
-        uint8_t* dg = dst + g * a.c.sh;
-        for (int base = 0; base < units; base += step) {
-            if (!ONE) {
-#pragma unroll
-                for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(base, i)) * a.sm + g * a.sh, half, raw[i]);
-                turn(base);
-            }
+        if (ONE) {
 #pragma unroll
             for (int i = 0; i < UPT; ++i) {
-                const int x = base + i * kPageThreads + tid;
-                if (x >= units) continue;
-                uint8_t* d = dg + (w.off + (x >> ulog)) * a.c.st + 8 * c;
-                *reinterpret_cast<uint2*>(d) = pack_e4m3(p[i], inv, inf);
-                *reinterpret_cast<uint2*>(d + half) = pack_e4m3(q[i], inv, inf);
+                if (inf) drop_inf(p[i], q[i]);
+                if (to[i] != nullptr) {
+                    *reinterpret_cast<uint2*>(to[i]) = pack_e4m3(p[i], inv * f[i]);
+                    *reinterpret_cast<uint2*>(to[i] + half) = pack_e4m3(q[i], inv * f[i]);
+                    to[i] += a.c.sh;
+                }
+            }
+        } else {
+            for (int base = tid; base - tid < units; base += T) {
+                raw_load(src + row(base) * a.sm + g * a.sh, half, raw[0]);
+                turn(base, 0);
+                if (inf) drop_inf(p[0], q[0]);
+                if (base < units) {
+                    uint8_t* d = dst + g * a.c.sh + (base >> ulog) * a.c.st;
+                    *reinterpret_cast<uint2*>(d) = pack_e4m3(p[0], inv * f[0]);
+                    *reinterpret_cast<uint2*>(d + half) = pack_e4m3(q[0], inv * f[0]);
+                }
             }
         }
-        if (!ONE && g + 1 < a.hpt)
-#pragma unroll
-            for (int i = 0; i < UPT; ++i) raw_load(src + (w.j0 + row(0, i)) * a.sm + (g + 1) * a.sh, half, raw[i]);
-        if (had > 0.f && had != now) reround(dg, a.c.st, w.off, ulog, had * inv);
+        if (had > 0.f && had != now) reround(dst - 8 * c - w.off * a.c.st + g * a.c.sh, a.c.st, w.off, ulog, had * inv);
     }
 }
 
@@ -433,14 +466,15 @@ static cudaError_t launch_e4m3(AppendArgs a, int sms, cudaStream_t s) {
     a.hpt = pages * 2 >= (unsigned)sms ? a.c.Hkv : 1;
     const dim3 grid(pages + 1, (unsigned)(a.c.Hkv / a.hpt), 2);
     const size_t smem = a.rope.on ? (size_t)((ps >> 4) + 16) * (a.hd >> 1) * sizeof(float2) : 0;
-    const bool one = units <= 2 * kPageThreads;
+    const bool one = units <= 1024;
+    const int T = one ? ((units + 1) / 2 + 31) & ~31 : kPageThreads;
     if (smem > 40 * 1024) {
         const cudaError_t e = one ? cudaFuncSetAttribute(append_e4m3_pages_kernel<IT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
                                   : cudaFuncSetAttribute(append_e4m3_pages_kernel<IT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    if (one) append_e4m3_pages_kernel<IT, true><<<grid, kPageThreads, smem, s>>>(a);
-    else append_e4m3_pages_kernel<IT, false><<<grid, kPageThreads, smem, s>>>(a);
+    if (one) append_e4m3_pages_kernel<IT, true><<<grid, T, smem, s>>>(a);
+    else append_e4m3_pages_kernel<IT, false><<<grid, T, smem, s>>>(a);
     return cudaGetLastError();
 }
 
