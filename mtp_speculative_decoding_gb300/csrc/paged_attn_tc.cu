@@ -435,6 +435,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         long long x = x0;
         Segment s = {}, nx = {};
         bool have = false;
+        constexpr int U = HD / 16, RP = 256 / U;   // threads of a query row, rows of a pass
+        const int qc = tid % U, qr = tid / U;
+        uint4 raw0 = make_uint4(0, 0, 0, 0), raw1 = raw0;
+        // this thread's unit of row r of segment nx, as loaded
+        auto load_q = [&](int r, uint4& v0, uint4& v1, int& j) {
+            const int at = nx.rt * RT + r;
+            j = (int)udiv((unsigned)at, (unsigned)a.G);
+            const uint16_t* src =
+                reinterpret_cast<const uint16_t*>(a.q) + nx.b * a.sb + j * a.sm + (nx.g * a.G + at - j * a.G) * a.sh + 8 * qc;
+            v0 = ld_stream16(src);
+            v1 = ld_stream16(src + HD / 2);
+        };
+        // the segment at x, and its first rows on their way
+        int raw_j = 0;
+        auto open_next = [&](long long at) {
+            nx = segment_at(a, plan, at, xe, blockIdx.x);
+            if (qr < nx.rows) load_q(qr, raw0, raw1, raw_j);
+        };
+        if (x < xe) open_next(x);
         int4 split = make_int4(0, 0, 0, -1);
         float l[RW], m[RW], c[RW];
         // A turn prepares the next segment's queries (its scores' MMAs start
@@ -443,32 +462,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         for (;;) {
             const bool more = x < xe;
             if (more) {
-                nx = segment_at(a, plan, x, xe, blockIdx.x);
                 if (nx.slot >= 0 && nx.t0 == 0) split = split_record(a, nx, T, x);
                 const int pn = par0 ^ 1;
                 const int r0 = nx.rt * RT;
                 // ---- queries: norm, rotation, scale, parts ----
                 {
-                    constexpr int U = HD / 16, RP = 256 / U;
-                    const int c = tid % U;
-    #pragma unroll 1
+                    const int c = qc;
+#pragma unroll 1
                     for (int rb = 0; rb < RT; rb += RP) {
-                        const int r = rb + tid / U;
+                        const int r = rb + qr;
                         if (RP > RT && r >= RT) break;   // whole warps
                         const bool in = r < nx.rows;
                         float p[8], q[8];
                         bool fin = true;
                         float amax = 0.f;
                         if (__any_sync(0xffffffffu, in)) {
-                            const int j = in ? (int)udiv((unsigned)(r0 + r), (unsigned)a.G) : 0, h = in ? (r0 + r) - j * a.G : 0;
-                            const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + nx.b * a.sb + j * a.sm + (nx.g * a.G + h) * a.sh + 8 * c;
-                            load8(src, p);
-                            load8(src + HD / 2, q);
+                            int j = raw_j;
+                            if (rb > 0) {
+                                j = 0;
+                                if (in) load_q(r, raw0, raw1, j);
+                            }
+                            open_unit(raw0, p);
+                            open_unit(raw1, q);
                             float cs[8], sn[8];
                             if (a.rope.on) unit_angles<true>((long long)nx.len + j, s_hi + 8 * c, s_lo + 8 * c, cs, sn);
                             if (a.q_norm) unit_norm(p, q, a.q_norm, c, HD, a.eps);
                             if (a.rope.on) unit_rotate(p, q, cs, sn);
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 p[e] = in ? p[e] * a.scale : 0.f;
                                 q[e] = in ? q[e] * a.scale : 0.f;
@@ -476,7 +496,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                                 fin = fin && p[e] - p[e] == 0.f && q[e] - q[e] == 0.f;
                             }
                         } else {
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
                         }
                         if (E4M3) {
@@ -489,15 +509,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                             if (k > 100) k = 100;
                             const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
                             if (c == 0) s_c[r] = fin ? __uint_as_float((uint32_t)(127 + k) << 23) : __uint_as_float(0x7FC00000u);
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 p[e] *= inv;
                                 q[e] *= inv;
                             }
-    #pragma unroll
+#pragma unroll
                             for (int part = 0; part < 3; ++part) {
                                 uint32_t w[4];
-    #pragma unroll
+#pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     float* v = i < 2 ? p + 4 * i : q + 4 * (i - 2);
                                     uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
@@ -510,7 +530,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                                     v[2] -= a1.x;
                                     v[3] -= a1.y;
                                 }
-    #pragma unroll
+#pragma unroll
                                 for (int half = 0; half < 2; ++half) {
                                     const int byte = half * (HD / 2) + 8 * c, box = byte / S::ROWB, in_row = byte % S::ROWB;
                                     unsigned char* d = sQ + (box * S::NQ + part) * RT * S::ROWB + swz<S::ROWB>(r, in_row >> 4) + (in_row & 8);
@@ -518,17 +538,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                                 }
                             }
                         } else {
-    #pragma unroll
+#pragma unroll
                             for (int part = 0; part < 2; ++part) {
                                 uint32_t w[8];
-    #pragma unroll
+#pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     float* v = i < 4 ? p + 2 * i : q + 2 * (i - 4);
                                     w[i] = pack_bf16(v[0], v[1]);
                                     v[0] -= bf16_lo(w[i]);
                                     v[1] -= bf16_hi(w[i]);
                                 }
-    #pragma unroll
+#pragma unroll
                                 for (int half = 0; half < 2; ++half) {
                                     const int byte = half * HD + 16 * c, box = byte / S::ROWB;
                                     *reinterpret_cast<uint4*>(sQ + (box * S::NQ + part) * RT * S::ROWB +
@@ -633,6 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 // every row attends every position of the tile
                 const bool whole = m_all[t % kTcMeta] && t0 + kTcTile - 1 <= p_first &&
                                    (a.c.window == 0 || t0 > p_last - a.c.window || t0 + kTcTile <= a.c.sink);
+                if (k == s.n - 1 && x + s.n < xe) open_next(x + s.n);   // its rows come in during this tile
                 wait(s_full + buf, par);
                 tc_fence_after();
                 float z[RW];
