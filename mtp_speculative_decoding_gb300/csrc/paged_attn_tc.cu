@@ -29,13 +29,27 @@ namespace mtp {
 namespace {
 
 // ---- tensor-core helpers of this kernel ----
-__device__ __forceinline__ void umma_f8(unsigned int d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
-        : "memory");
+// D[tmem] (+)= A B^T with the descriptors' low words given and their high words
+// fixed: the unrolled issue loops then cost two additions an MMA
+template <bool F8>
+__device__ __forceinline__ void umma(unsigned int d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                     uint32_t acc) {
+    if (F8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+            "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+            : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(unsigned int taddr, uint32_t* r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -65,32 +79,21 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)), "l"(pol)
         : "memory");
 }
-// shared-memory matrix descriptor: 128- or 64-byte swizzled rows of ROWB
-// bytes, 8-row groups following one another; lead: bytes between the ROWB-wide
-// blocks of an M-major operand (0: the same block again, for rows of 64
-// dimensions under an M of 128 -- the upper half of the accumulator repeats
-// the lower and is not read)
+// Shared-memory matrix descriptors, as (low, high) words; low: address / 16 plus
+// the leading offset (an address below 256 KB leaves it alone when added to).
+// Tiles of 128- or 64-byte swizzled rows of ROWB bytes, 8-row groups following
+// one another; lead: bytes between the ROWB-wide blocks of an M-major operand
+// (0: the same block again, for rows of 64 dimensions under an M of 128 -- the
+// upper half of the accumulator repeats the lower and is not read)
+__host__ __device__ constexpr uint32_t desc_lead(uint32_t lead) { return (lead >> 4) << 16; }
 template <int ROWB>
-__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((lead >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((8 * ROWB) >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)(ROWB == 128 ? 2 : 4) << 61;
-    return d;
+__host__ __device__ constexpr uint32_t desc_rows_hi() {
+    return ((8 * ROWB) >> 4) | 1u << 14 | (ROWB == 128 ? 2u : 4u) << 29;
 }
 // P: its rows (N) are contiguous, 16 bytes of them a position, no swizzle; 8
 // positions are a 128-byte core, positions follow densely, 16-byte row blocks
 // are 2048 bytes apart
-__device__ __forceinline__ uint64_t desc_p(uint32_t addr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(128 >> 4) << 16;
-    d |= (uint64_t)(2048 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    return d;
-}
+constexpr uint32_t kDescPHi = (2048 >> 4) | 1u << 14;
 // fp32 accumulator, M x N; types 0 / 1: e4m3 / e5m2 (kind f8f6f4), 1: bf16 (kind f16)
 // (mn: both operands M- / N-major)
 __host__ __device__ constexpr uint32_t instr(int ta, int tb, bool mn, int M, int N) {
@@ -346,8 +349,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         // ------------------------------------------------------------------
         constexpr uint32_t idS = E4M3 ? instr(0, 0, false, 128, S::SCOLS) : instr(1, 1, false, 128, S::SCOLS);
         constexpr uint32_t idO = E4M3 ? instr(0, 1, true, 128, S::NO * RT) : instr(1, 1, true, 128, S::NO * RT);
-        const uint32_t q0 = smem_addr(sQ), p0 = smem_addr(sP), r0 = smem_addr(ring);
-        const bool leader = elect_one();
+        constexpr uint32_t hiR = desc_rows_hi<S::ROWB>();
+        const uint32_t q0 = (smem_addr(sQ) >> 4) + desc_lead(16), p0 = (smem_addr(sP) >> 4) + desc_lead(128), r0 = smem_addr(ring) >> 4;
+        constexpr int KT = E4M3 ? 32 : 16;   // positions of an MMA over V
         unsigned int slot = 0, phase = 0, ti = 0, seg = 0;
         bool ok = true;
         auto next = [&] {
@@ -372,22 +376,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     for (int d = 0; d < S::D && ok; ++d) {
                         hold(full + slot, phase);
                         if (!ok) break;
-                        if (leader) {
+                        const uint32_t al = r0 + slot * (S::SLOTB >> 4) + desc_lead(16), bl = q0 + d * (S::NBOX * S::NQ * RT * S::ROWB >> 4);
+                        if (elect_one()) {
 #pragma unroll
                             for (int nb = 0; nb < S::NBOX; ++nb)
 #pragma unroll
-                                for (int ks = 0; ks < S::ROWB / 32; ++ks) {
-                                    const uint64_t ad = desc<S::ROWB>(r0 + slot * S::SLOTB + nb * S::BOXB + ks * 32, 16);
-                                    const uint64_t bd = desc<S::ROWB>(q0 + (d * S::NBOX + nb) * S::NQ * RT * S::ROWB + ks * 32, 16);
-                                    const uint32_t acc = d > 0 || nb > 0 || ks > 0;
-                                    if (E4M3) umma_f8(tmem + buf * S::SCOLS, ad, bd, idS, acc);
-                                    else umma_bf16(tmem + buf * S::SCOLS, ad, bd, idS, acc);
-                                }
+                                for (int ks = 0; ks < S::ROWB / 32; ++ks)
+                                    umma<E4M3>(tmem + buf * S::SCOLS, al + (nb * S::BOXB + ks * 32 >> 4), hiR,
+                                               bl + (nb * S::NQ * RT * S::ROWB + ks * 32 >> 4), hiR, idS, d > 0 || nb > 0 || ks > 0);
                             umma_commit(empty + slot);
                         }
+                        __syncwarp();
                         next();
                     }
-                    if (ok && leader) umma_commit(s_full + buf);
+                    if (ok && elect_one()) umma_commit(s_full + buf);
+                    __syncwarp();
                 }
                 if (k > 0 && ok) {   // O^T of tile k - 1
                     const unsigned int t = ti + k - 1, buf = t & 1;
@@ -395,29 +398,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     for (int d = 0; d < S::D && ok; ++d) {
                         hold(full + slot, phase);
                         if (!ok) break;
-                        if (leader) {
-                            constexpr int KT = E4M3 ? 32 : 16;   // positions of an MMA
+                        const uint32_t al = r0 + slot * (S::SLOTB >> 4) + desc_lead(S::NBOX == 2 ? S::BOXB : 0), bl = p0 + buf * (S::PB >> 4);
+                        if (elect_one()) {
 #pragma unroll
                             for (int ks = 0; ks < kTcTile / KT; ++ks)
 #pragma unroll
-                                for (int part = 0; part < S::NP / S::NO; ++part) {
-                                    const uint64_t ad = desc<S::ROWB>(r0 + slot * S::SLOTB + ks * KT * S::ROWB, S::NBOX == 2 ? S::BOXB : 0);
-                                    const uint64_t bd = desc_p(p0 + buf * S::PB + part * (RT * S::ESZ / 16) * 2048 + ks * KT * 16);
-                                    const uint32_t acc = k > 1 || ks > 0 || part > 0;
-                                    if (E4M3) umma_f8(tmem + S::O0 + d * S::NO * RT, ad, bd, idO, acc);
-                                    else umma_bf16(tmem + S::O0 + d * S::NO * RT, ad, bd, idO, acc);
-                                }
+                                for (int part = 0; part < S::NP / S::NO; ++part)
+                                    umma<E4M3>(tmem + S::O0 + d * S::NO * RT, al + (ks * KT * S::ROWB >> 4), hiR,
+                                               bl + (part * (RT * S::ESZ / 16) * 2048 + ks * KT * 16 >> 4), kDescPHi, idO,
+                                               k > 1 || ks > 0 || part > 0);
                             umma_commit(empty + slot);
                         }
+                        __syncwarp();
                         next();
                     }
-                    if (ok && leader) umma_commit(pv_done + buf);
+                    if (ok && elect_one()) umma_commit(pv_done + buf);
+                    __syncwarp();
                 }
             }
             ti += s.n;
             x += s.n;
         }
-        if (leader) umma_commit(end_bar);   // whatever was issued has ended before the CTA frees its memory
+        if (elect_one()) umma_commit(end_bar);   // whatever was issued has ended before the CTA frees its memory
         const unsigned long long t0 = global_ns();
         while (!mbar_try_wait(end_bar, 0) && global_ns() - t0 < a.timeout_ns) {}
         __syncwarp();
