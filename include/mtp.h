@@ -475,7 +475,8 @@ int mtp_kv_append(const mtp_kv_cache *c, int B, int M, const int32_t *kv_len, co
  *              bytes
  * fp32 queries are computed in fp32 throughout.  bf16 queries against a bf16
  * or e4m3 cache with head_dim 64, 128, 256 or 512 run on the tensor cores: the
- * probabilities are then rounded to bf16 precision (sums and maxima fp32).
+ * probabilities then keep 16 bits (bf16 cache) or 9 (e4m3 cache), sums and
+ * maxima 32.
  * Slots that hold no attended position are never used, whatever they contain.
  * A row that attends nothing (all its pages absent) gives zeros.  A sequence
  * whose kv_len or n_new is out of range is left out, positions on absent pages

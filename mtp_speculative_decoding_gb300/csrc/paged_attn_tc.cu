@@ -8,11 +8,11 @@
 // it lies in the page (its dimensions contiguous: the M-major operand).  K and
 // V go from the pages to the tensor core by TMA alone; an e4m3 cache is
 // multiplied as e4m3, exactly, so its bytes are the only traffic.  What would
-// lose bits is split instead: a query row into two bf16 parts (against bf16) or
-// three e4m3 parts under a power of two of its own (2^-12), a probability is
-// bf16 (against bf16), or three e5m2 parts (2^-9; e5m2 for its range: a weight
-// 2^-28 below the largest still counts).  The sum over the parts is the MMA's
-// own accumulation.
+// lose bits is split instead: against bf16, a query row and a probability into
+// two bf16 parts each (2^-16); against e4m3, a query row into three e4m3 parts
+// under a power of two of its own (2^-12) and a probability into three e5m2
+// parts (2^-9; e5m2 for its range: a weight 2^-28 below the largest still
+// counts).
 //
 // Softmax: a thread is one position of the tile and holds its RT scores.  The
 // reference m of a row (the running maximum) moves only when a score exceeds
@@ -143,7 +143,8 @@ struct Shape {
     static constexpr int NQ = E4M3 ? 3 : 2;                        // parts of Q
     static constexpr int QBOX = HD * ESZ / ROWB;                   // boxes of a Q row
     static constexpr int QB = NQ * QBOX * RT * ROWB;
-    static constexpr int NP = E4M3 ? 3 : 1;                        // parts of P
+    static constexpr int NP = E4M3 ? 3 : 2;                        // parts of P
+    static constexpr int PBUF = tc_p_bufs(E4M3, RT);               // tiles of P
     static constexpr int PB = NP * RT * ESZ * kTcTile;
     // The parts of an operand lie side by side in N where tensor memory has the
     // columns (one MMA instead of NQ or NP: an MMA takes about 40 ns here
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     unsigned char* ring = base;
     unsigned char* sQ = ring + (size_t)NS * S::SLOTB;
     unsigned char* sP = sQ + S::QB;
-    float* s_hi = reinterpret_cast<float*>(sP + 2 * S::PB);   // [HD/2], [HD/2]: rotation table
+    float* s_hi = reinterpret_cast<float*>(sP + S::PBUF * S::PB);   // [HD/2], [HD/2]: rotation table
     float* s_lo = s_hi + HD / 2;
     float* m_ks = s_lo + HD / 2;                               // [kTcMeta][8] key scale (0: page not loaded)
     float* m_vs = m_ks + kTcMeta * 8;                          // [kTcMeta][8] exponent of the value scale
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     for (int d = 0; d < S::D && ok; ++d) {
                         hold(full + slot, phase);
                         if (!ok) break;
-                        const uint32_t al = r0 + slot * (S::SLOTB >> 4) + desc_lead(S::NBOX == 2 ? S::BOXB : 0), bl = p0 + buf * (S::PB >> 4);
+                        const uint32_t al = r0 + slot * (S::SLOTB >> 4) + desc_lead(S::NBOX == 2 ? S::BOXB : 0), bl = p0 + (t % S::PBUF) * (S::PB >> 4);
                         if (elect_one()) {
 #pragma unroll
                             for (int ks = 0; ks < kTcTile / KT; ++ks)
@@ -610,7 +611,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
                         o[r] = __uint_as_float(v[0][r]);
-                        if (S::NO == 3) o[r] += __uint_as_float(v[1 % S::NO][r]) + __uint_as_float(v[2 % S::NO][r]);
+#pragma unroll
+                        for (int part = 1; part < S::NO; ++part) o[r] += __uint_as_float(v[part][r]);
                     }
                     for (int f = 0; f < nfix; ++f) {   // values that are not finite, to the rows that attend them
                         const int t = s_fix2[pe * kTcFix + f];
@@ -725,9 +727,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                         tc_fence_before();
                     }
                 }
-                // P of tile t - 2 is read
-                if (t >= 2) wait(pv_done + buf, par ^ 1);
-                unsigned char* P = sP + buf * S::PB + tok * 16;
+                // the tile whose P lay here is read
+                if (t >= S::PBUF) wait(pv_done + ((t - S::PBUF) & 1), ((t - S::PBUF) >> 1) & 1);
+                unsigned char* P = sP + (t % S::PBUF) * S::PB + tok * 16;
                 if (E4M3) {
                     const float unscale = fexp2(-ev);
                     uint32_t w[3][RW / 4];   // four rows a word
@@ -760,7 +762,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 } else {
 #pragma unroll
                     for (int i = 0; i < RW / 8; ++i) {
-                        uint32_t w[4];
+                        uint32_t w[4], v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int r = 8 * i + 2 * e;
@@ -768,8 +770,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                             l[r] += e0;
                             l[r + 1] += e1;
                             w[e] = pack_bf16(e0, e1);
+                            v[e] = pack_bf16(e0 - bf16_lo(w[e]), e1 - bf16_hi(w[e]));
                         }
                         *reinterpret_cast<uint4*>(P + (rw / 8 + i) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(P + ((RT + rw) / 8 + i) * 2048) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
                 if (!whole) {

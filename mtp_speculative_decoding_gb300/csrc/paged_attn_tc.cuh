@@ -20,10 +20,12 @@ struct PagedTcArgs {
     int slots;                        // ring slots
 };
 
+// tiles of P in shared memory: one where two would leave the ring too little
+__host__ __device__ constexpr int tc_p_bufs(bool e4m3, int RT) { return !e4m3 && RT > 32 ? 1 : 2; }
 // bytes of shared memory besides the ring
 __host__ __device__ constexpr int tc_other(bool e4m3, int hd, int RT, int B) {
     return (e4m3 ? 3 : 2 * 2) * RT * hd                          // Q, in parts
-           + 2 * (e4m3 ? 3 * RT * 128 : 2 * RT * 128)            // P, two tiles
+           + tc_p_bufs(e4m3, RT) * (e4m3 ? 3 : 2 * 2) * RT * 128 // P, in parts
            + kTcMeta * 8 * 2 * 4 + kTcMeta * 4                   // page scales
            + RT * 4 * (4 + 3 + 4) + 2 * kTcFix * 4 + hd * 4          // row tables, list, rotation table
            + (2 * kTcSlotsMax + kTcMeta + 16) * 8 + 33 * 8 + 64 + plan_bytes(B) + 1024;
