@@ -198,8 +198,12 @@ struct PagedAttnArgs {
     void* out;
     WsHeader* hdr;
     int* cta_status;           // [grid]: MTP_OK or an error, written by every CTA
-    int4* split;               // [grid]: the item that begins in CTA c's share and ends in another's, written by every
-                               // CTA for the merge: sequence, KV head, first row | rows << 16, last CTA (-1: none)
+    // For the merge, [grid]: an item that begins in one CTA's share and ends in
+    // another's: KV head, first row | rows << 16, first CTA, last CTA (-1: none).
+    // Entry c is CTA c's (at most one item begins in its share and ends behind
+    // it), or, where there are no more items than CTAs, every item has its own.
+    int4* split;
+    int by_item, rows_max;     // that, and rows of an item at most (min(RT, M G))
     float* part;               // [2 grid] slots of RT * (hd + 2) floats
     int RT, rt_log2, tile_log2, grid;
     unsigned long long timeout_ns;
@@ -338,9 +342,16 @@ __device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const Plan
     return s;
 }
 
-// what CTA c leaves in a.split for an item that begins in its share at tile x
-__device__ __forceinline__ int4 split_record(const PagedAttnArgs& a, const Segment& s, long long T, long long x) {
-    return make_int4(s.b, s.g, s.rt * a.RT | s.rows << 16, share_of(T, x + s.map.n - 1, a.grid));
+// row tiles that an item index counts for every sequence and KV head
+__device__ __forceinline__ int item_tiles(const PagedAttnArgs& a) { return (a.M * a.G + a.RT - 1) >> a.rt_log2; }
+// what CTA c notes for an item that begins in its share at tile x (one thread;
+// `mine`: its own entry, written at its end)
+__device__ __forceinline__ void note_split(const PagedAttnArgs& a, const Segment& s, long long T, long long x, int c, int4& mine) {
+    if (s.t0 != 0) return;
+    int4 r = make_int4(0, 0, 0, -1);
+    if (s.slot >= 0) r = make_int4(s.b * a.c.Hkv + s.g, s.rt * a.RT | s.rows << 16, c, share_of(T, x + s.map.n - 1, a.grid));
+    if (a.by_item) a.split[(s.b * a.c.Hkv + s.g) * item_tiles(a) + s.rt] = r;
+    else if (s.slot >= 0) mine = r;
 }
 
 // floats of one partial slot

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
     while (x < xe) {
         const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
         const int r0 = s.rt * a.RT;
-        if (s.slot >= 0 && s.t0 == 0) split = split_record(a, s, T, x);
+        if (tid == 0) note_split(a, s, T, x, blockIdx.x, split);
         // queries: norm, rotation, scale
         for (int i0 = 0; i0 < kCcRows * U; i0 += kCcThreads) {
             const int i = i0 + tid, r = i / U, c = i % U;
@@ -204,13 +204,13 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
     const int any = __syncthreads_or(bad);
     if (tid == 0) {
         a.cta_status[blockIdx.x] = any ? MTP_ERR_ARG : MTP_OK;
-        a.split[blockIdx.x] = split;
+        if (!a.by_item) a.split[blockIdx.x] = split;
     }
 }
 
 // ---------------------------------------------------------------------------
 // merge: a CTA takes one row of an item that begins in CTA c0's share of the
-// attention and ends in another's (an item that one CTA held whole is written
+// attention and ends in CTA c1's (an item that one CTA held whole is written
 // already).  out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  The
 // parts are spread over the CTA's thread groups (hd / 4 threads each, four
 // dimensions a thread), eight a turn with all their loads in flight, so it is
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     __shared__ float4 s_o[kMergeThreads];
     __shared__ float2 s_ml[kMergeThreads];
     const int tid = threadIdx.x;
-    const int c0 = (int)blockIdx.x >> a.rt_log2, r = (int)blockIdx.x & (a.RT - 1), hd = a.hd;
+    const int idx = (int)(blockIdx.x / (unsigned)a.rows_max), r = (int)blockIdx.x - idx * a.rows_max, hd = a.hd;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == gridDim.x - 1) {   // the call's status from the CTAs'
@@ -246,9 +246,13 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         }
         return;
     }
-    const int4 it = a.split[c0];
-    const int c1 = it.w;
-    if (c1 < 0 || r >= it.z >> 16) return;
+    const int4 it = a.split[idx];
+    if (a.by_item) {   // an item without tiles has no note
+        const int b = idx / (a.c.Hkv * item_tiles(a)), len = a.kv_len[b], n = a.n_new ? a.n_new[b] : a.M;
+        if (!seq_ok(len, n, a.M, a.c) || n * a.G <= (idx % item_tiles(a)) << a.rt_log2) return;
+    }
+    const int c0 = it.z, c1 = it.w;
+    if (c1 < 0 || r >= it.y >> 16) return;
     const long long psz = part_floats(a.RT, hd);
     auto slot = [&](int c) { return a.part + (c == c0 ? 2 * c + 1 : 2 * c) * psz; };
     const int gt = hd >> 2, groups = kMergeThreads / gt;   // threads of a group, groups
@@ -312,8 +316,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     acc.y *= inv;
     acc.z *= inv;
     acc.w *= inv;
-    const int rr = (it.z & 0xFFFF) + r, j = (int)udiv((unsigned)rr, (unsigned)a.G);
-    QT* o = reinterpret_cast<QT*>(a.out) + (((long long)it.x * a.M + j) * a.Hq + it.y * a.G + rr - j * a.G) * hd;
+    const int rr = (it.y & 0xFFFF) + r, j = (int)udiv((unsigned)rr, (unsigned)a.G), b = it.x / a.c.Hkv, g = it.x - b * a.c.Hkv;
+    QT* o = reinterpret_cast<QT*>(a.out) + (((long long)b * a.M + j) * a.Hq + g * a.G + rr - j * a.G) * hd;
     put4(o + d, acc);
 }
 
@@ -344,7 +348,8 @@ cudaError_t launch_paged_attn_cc(const PagedAttnArgs& a, int dtype, int kv_dtype
 
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.grid * a.RT + 1);
+    const long long items = (long long)a.B * a.c.Hkv * ((a.M * a.G + a.RT - 1) / a.RT);
+    cfg.gridDim = dim3((unsigned)(a.by_item ? items : a.grid) * a.rows_max + 1);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];

@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         for (;;) {
             const bool more = x < xe;
             if (more) {
-                if (nx.slot >= 0 && nx.t0 == 0) split = split_record(a, nx, T, x);
+                if (tid == 0) note_split(a, nx, T, x, blockIdx.x, split);
                 const int pn = par0 ^ 1;
                 const int r0 = nx.rt * RT;
                 // ---- queries: norm, rotation, scale, parts ----
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             g0 += 2 * s.n * S::D;
             x += s.n;
         }
-        if (tid == 0) a.split[blockIdx.x] = split;
+        if (tid == 0 && !a.by_item) a.split[blockIdx.x] = split;
     }
     __syncthreads();
     if (tid == 0) a.cta_status[blockIdx.x] = s_abort ? MTP_ERR_TIMEOUT : s_bad ? MTP_ERR_ARG : MTP_OK;
