@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         const unsigned long long pol = l2_evict_first();
         unsigned int slot = 0, phase = 0, ti = 0;
         bool ok = true, bad = false;
+        int4 split = make_int4(0, 0, 0, -1);
         const int per_batch = 32 >> np_log2;
         long long x = x0;
         while (x < xe && ok) {
@@ -332,8 +333,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 pv_pg = kp;
                 pv_y = ky;
             }
+            if (lane == 0) note_split(a, s, T, x, blockIdx.x, split);
             x += s.n;
         }
+        if (lane == 0 && !a.by_item) a.split[blockIdx.x] = split;
         if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
         if (!ok) {   // gave up: this warp's copies in flight end before the CTA does
             const unsigned long long t0 = global_ns();
@@ -465,7 +468,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         for (;;) {
             const bool more = x < xe;
             if (more) {
-                if (tid == 0) note_split(a, nx, T, x, blockIdx.x, split);
                 const int pn = par0 ^ 1;
                 const int r0 = nx.rt * RT;
                 // ---- queries: norm, rotation, scale, parts ----
@@ -800,7 +802,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                             for (int i = 0; i < CH; i += 2) *chunk(i + wg) = make_uint4(0, 0, 0, 0);
                             continue;
                         }
-#pragma unroll 2
+                        // one look at the whole row (the largest magnitude bits), value by
+                        // value only where that shows something
+                        uint32_t top = 0u;
+#pragma unroll
+                        for (int i = 0; i < CH; i += 2) {
+                            const uint4 v = *chunk(i + wg);
+                            constexpr uint32_t mask = E4M3 ? 0x7F7F7F7Fu : 0x7FFF7FFFu;
+                            top = E4M3 ? __vmaxu4(__vmaxu4(top, v.x & mask), __vmaxu4(v.y & mask, __vmaxu4(v.z & mask, v.w & mask)))
+                                       : __vmaxu2(__vmaxu2(top, v.x & mask), __vmaxu2(v.y & mask, __vmaxu2(v.z & mask, v.w & mask)));
+                        }
+                        if (E4M3 ? __vcmpeq4(top, 0x7F7F7F7Fu) == 0u : __vcmpgeu2(top, 0x7F807F80u) == 0u) continue;
+#pragma unroll 1
                         for (int i = wg; i < CH; i += 2) {
                             uint4* e = chunk(i);
                             uint4 v = *e;
@@ -842,7 +855,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             g0 += 2 * s.n * S::D;
             x += s.n;
         }
-        if (tid == 0 && !a.by_item) a.split[blockIdx.x] = split;
     }
     __syncthreads();
     if (tid == 0) a.cta_status[blockIdx.x] = s_abort ? MTP_ERR_TIMEOUT : s_bad ? MTP_ERR_ARG : MTP_OK;
