@@ -112,16 +112,19 @@ struct AttnPlan {
     int RT, tile_log2, grid;
     size_t status, split, part, end;
 };
-AttnPlan attn_plan(const mtp_kv_cache* c, int M, int n_q_heads, bool tc, int sms) {
+// (the workspace does not depend on the batch, so that one sized for more sequences serves fewer)
+AttnPlan attn_plan(const mtp_kv_cache* c, int B, int M, int n_q_heads, bool tc, int sms) {
     AttnPlan p;
     p.tc = tc;
-    p.RT = tc ? tc_rows(M * (n_q_heads / c->n_kv_heads), c->head_dim) : kCcRows;
+    const int rows = M * (n_q_heads / c->n_kv_heads);
+    p.RT = tc ? tc_rows(c->kv_dtype == MTP_DTYPE_E4M3, rows, c->head_dim, B) : kCcRows;
+    const int most = tc ? tc_rows_max(rows, c->head_dim) : kCcRows;
     p.tile_log2 = tc ? kTcTileLog2 : kCcTileLog2;
     p.grid = tc ? sms : 2 * sms;
     size_t off = sizeof(WsHeader);
     p.status = off; off = al256(off + (size_t)p.grid * sizeof(int));
     p.split = off;  off = al256(off + (size_t)p.grid * sizeof(int4));
-    p.part = off;   off = al256(off + 2 * (size_t)p.grid * part_floats(p.RT, c->head_dim) * sizeof(float));
+    p.part = off;   off = al256(off + 2 * (size_t)p.grid * part_floats(most, c->head_dim) * sizeof(float));
     p.end = off;
     return p;
 }
@@ -142,7 +145,7 @@ size_t mtp_kv_workspace_size(const mtp_kv_cache* c, int B, int M, int n_q_heads)
     int sms = num_sms();
     if (sms <= 0) sms = 152;   // no device (a host-side size query)
     if (M > MTP_MAX_ATTN_ROWS) M = MTP_MAX_ATTN_ROWS;
-    const size_t cc = attn_plan(c, M, n_q_heads, false, sms).end, tc = attn_plan(c, M, n_q_heads, true, sms).end;
+    const size_t cc = attn_plan(c, B, M, n_q_heads, false, sms).end, tc = attn_plan(c, B, M, n_q_heads, true, sms).end;
     return cc > tc ? cc : tc;
 }
 
@@ -189,7 +192,7 @@ int mtp_paged_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, cons
     if (!out || misaligned(out, 16)) return MTP_ERR_ARG;
     const int sms = num_sms();
     if (sms <= 0) return MTP_ERR_CUDA;
-    const AttnPlan p = attn_plan(c, M, n_q_heads, tc_path(c, dtype), sms);
+    const AttnPlan p = attn_plan(c, B, M, n_q_heads, tc_path(c, dtype), sms);
     if (!ws || misaligned(ws, 256) || ws_bytes < p.end) return MTP_ERR_WORKSPACE;
     char* base = static_cast<char*>(ws);
     PagedTcArgs t;

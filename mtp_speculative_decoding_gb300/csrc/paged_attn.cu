@@ -252,7 +252,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         if (!seq_ok(len, n, a.M, a.c) || n * a.G <= (idx % item_tiles(a)) << a.rt_log2) return;
     }
     const int c0 = it.z, c1 = it.w;
-    if (c1 < 0 || r >= it.y >> 16) return;
+    // (an attention that gave up may have left no note: whatever is there stays in bounds)
+    if (c1 < 0 || c0 < 0 || c0 >= a.grid || c1 >= a.grid || r >= it.y >> 16 || (it.y & 0xFFFF) + r >= a.M * a.G || it.x < 0 ||
+        it.x >= a.B * a.c.Hkv)
+        return;
     const long long psz = part_floats(a.RT, hd);
     auto slot = [&](int c) { return a.part + (c == c0 ? 2 * c + 1 : 2 * c) * psz; };
     const int gt = hd >> 2, groups = (int)blockDim.x / gt;   // threads of a group, groups

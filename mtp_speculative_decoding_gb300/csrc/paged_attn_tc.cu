@@ -144,7 +144,7 @@ struct Shape {
     static constexpr int QBOX = HD * ESZ / ROWB;                   // boxes of a Q row
     static constexpr int QB = NQ * QBOX * RT * ROWB;
     static constexpr int NP = E4M3 ? 3 : 2;                        // parts of P
-    static constexpr int PBUF = tc_p_bufs(E4M3, RT);               // tiles of P
+    static constexpr int PBUF = tc_p_bufs(E4M3, HD, RT);               // tiles of P
     static constexpr int PB = NP * RT * ESZ * kTcTile;
     // The parts of an operand lie side by side in N where tensor memory has the
     // columns (one MMA instead of NQ or NP: an MMA takes about 40 ns here

@@ -21,11 +21,11 @@ struct PagedTcArgs {
 };
 
 // tiles of P in shared memory: one where two would leave the ring too little
-__host__ __device__ constexpr int tc_p_bufs(bool e4m3, int RT) { return !e4m3 && RT > 32 ? 1 : 2; }
+__host__ __device__ constexpr int tc_p_bufs(bool e4m3, int hd, int RT) { return !e4m3 && RT * hd > 32 * 256 ? 1 : 2; }
 // bytes of shared memory besides the ring
 __host__ __device__ constexpr int tc_other(bool e4m3, int hd, int RT, int B) {
     return (e4m3 ? 3 : 2 * 2) * RT * hd                          // Q, in parts
-           + tc_p_bufs(e4m3, RT) * (e4m3 ? 3 : 2 * 2) * RT * 128 // P, in parts
+           + tc_p_bufs(e4m3, hd, RT) * (e4m3 ? 3 : 2 * 2) * RT * 128 // P, in parts
            + kTcMeta * 8 * 2 * 4 + kTcMeta * 4                   // page scales
            + RT * 4 * (4 + 3 + 4) + 2 * kTcFix * 4 + hd * 4          // row tables, list, rotation table
            + (2 * kTcSlotsMax + kTcMeta + 16) * 8 + 33 * 8 + 64 + plan_bytes(B) + 1024;
@@ -39,9 +39,15 @@ __host__ __device__ constexpr int tc_slots(bool e4m3, int hd, int RT, int B) {
     return n;
 }
 
-// rows of a row tile: the smallest of 16, 32, 64 that holds all rows (64, or
-// 32 at head dimension 512, where the queries of more rows leave no ring)
-inline int tc_rows(int rows, int hd) { return rows <= 16 ? 16 : rows <= 32 || hd == 512 ? 32 : 64; }
+// Rows of a row tile: the smallest of 16, 32, 64 that holds all rows (at head
+// dimension 512 at most 32: the queries of more leave no ring), fewer where a
+// value tile would not fit the ring beside a large batch's plan.
+inline int tc_rows_max(int rows, int hd) { return rows <= 16 ? 16 : rows <= 32 || hd == 512 ? 32 : 64; }
+inline int tc_rows(bool e4m3, int rows, int hd, int B) {
+    int RT = tc_rows_max(rows, hd);
+    while (RT > 16 && tc_slots(e4m3, hd, RT, B) < (hd + 127) / 128) RT /= 2;
+    return RT;
+}
 
 // one translation unit each (paged_attn_tc.cu)
 cudaError_t launch_paged_attn_tc_bf16(const PagedTcArgs& p, cudaStream_t s);

@@ -77,6 +77,15 @@ CASES = [
     ("f32", "bf16", 64, 1, 4, 32, 2, [65], None, False, 1e4, 0, 0, "head"),
     ("bf16", "f32", 512, 1, 3, 32, 2, [150], None, True, 1e6, 50, 7, "slot"),
     ("e4m3", "f32", 256, 2, 4, 64, 4, [180, 63], None, True, 1e6, 0, 0, "head"),
+    # more rows than a 16-row tile at the largest head dimension, and of all tile heights
+    ("bf16", "bf16", 512, 1, 8, 32, 4, [300, 3], [4, 1], True, 1e6, 0, 0, "head"),
+    ("e4m3", "bf16", 512, 2, 16, 64, 3, [260], None, False, 1e6, 0, 0, "slot"),
+    ("e4m3", "bf16", 64, 1, 16, 16, 64, [200, 0], [64, 7], True, 1e4, 0, 0, "head"),
+    ("e4m3", "bf16", 128, 1, 8, 64, 33, [150], None, True, 1e4, 70, 9, "slot"),
+    ("bf16", "bf16", 64, 2, 4, 32, 8, [513, 40], None, True, 1e4, 0, 0, "slot"),
+    # sequences that bring nothing between ones that do, each cut into parts
+    ("bf16", "bf16", 128, 1, 4, 64, 2, [1500, 900, 0, 2000], [2, 0, 0, 1], False, 1e4, 0, 0, "head"),
+    ("f32", "f32", 64, 1, 2, 16, 2, [400, 300, 200], [0, 2, 0], False, 1e4, 0, 0, "head"),
 ]
 
 
@@ -110,6 +119,35 @@ def test_many_sequences_of_ragged_lengths(kv):
     check(pool, out, q, None, lens, n, 1e6)
     again, _ = run(pool, q, lens, n, rope_theta=1e6)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("kv,hd,G,M", [("bf16", 512, 8, 3), ("e4m3", 256, 4, 3), ("bf16", 64, 2, 1)])
+def test_the_largest_batch(kv, hd, G, M):
+    """MTP_MAX_PAGED_BATCH sequences, one call of append and one of attention."""
+    m = mtp()
+    B, page = m.MTP_MAX_PAGED_BATCH, 16
+    g = torch.Generator().manual_seed(31)
+    lens = torch.randint(0, 40, (B,), generator=g).tolist()
+    n = torch.randint(0, M + 1, (B,), generator=g).tolist()
+    pool = pc.Pool(B, 4, page, 1, hd, kv, seed=32)
+    pool.fill(lens, seed=33)
+    q = queries(B, M, G, hd, torch.bfloat16, seed=34, extra=2)
+    qkv = torch.randn(B, M, 2 * hd, device="cuda").to(torch.bfloat16)
+    h = pool.handle(rope_theta=1e4)
+    ws = m.alloc_workspace(m.kv_workspace_size(h, B, M, G))
+    m.kv_append(h, qkv[..., :hd].unflatten(-1, (1, hd)), qkv[..., hd:].unflatten(-1, (1, hd)), i32(lens), ws, n_new=i32(n))
+    assert m.last_error(ws) == m.MTP_OK
+    out, st = run(pool, q, lens, n, ws=ws, rope_theta=1e4)
+    assert st == m.MTP_OK
+    pick = list(range(0, B, 37)) + [B - 1]
+    sub = pc.Pool.__new__(pc.Pool)
+    sub.__dict__.update(pool.__dict__)
+    sub.table = pool.table[pick]
+    check(sub, out[pick], q[pick], None, [lens[b] for b in pick], [n[b] for b in pick], 1e4)
+    # a workspace sized for the largest batch serves a small one
+    out2, st = run(sub, q[pick], [lens[b] for b in pick], [n[b] for b in pick], ws=ws, rope_theta=1e4)
+    assert st == m.MTP_OK
+    check(sub, out2, q[pick], None, [lens[b] for b in pick], [n[b] for b in pick], 1e4)
 
 
 def test_one_long_sequence():
