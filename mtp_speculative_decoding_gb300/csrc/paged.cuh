@@ -180,10 +180,12 @@ cudaError_t launch_kv_append(const AppendArgs& a, int in_dtype, int kv_dtype, in
 // ---------------------------------------------------------------------------
 // An item is (sequence, KV head, row tile): RT of the sequence's n * G
 // rows (row r: new row r / G, query head r % G of the group) against its
-// attended positions in tiles of `tile` positions.  The items' tiles lie end
-// to end, sequence-major, T in all; CTA c takes tiles [T c / grid, T (c + 1) /
-// grid), so ragged lengths cost the same on every CTA.  A segment is the part
-// of one item inside one CTA's range.  A whole item is written out directly;
+// attended positions in tiles of `tile` positions.  The items lie end to end,
+// sequence-major, each as `open` units (what it costs a CTA to begin an item:
+// its queries, an epilogue, and a pipeline that fills anew) and one unit a
+// tile; T units in all.  CTA c takes the units [T c / grid, T (c + 1) / grid),
+// so ragged lengths cost the same on every CTA.  A segment is the part of one
+// item's tiles inside one CTA's range.  A whole item is written out directly;
 // a part is left as (o, m, l) in slot 2c if it begins inside the item (at most
 // the CTA's first) and in 2c + 1 if it only ends there (at most its last), and
 // a second kernel merges the parts.
@@ -206,6 +208,7 @@ struct PagedAttnArgs {
     int by_item, rows_max;     // that, and rows of an item at most (min(RT, M G))
     float* part;               // [2 grid] slots of RT * (hd + 2) floats
     int RT, rt_log2, tile_log2, grid;
+    int open_max;              // units before an item's tiles at most
     unsigned long long timeout_ns;
     RopeTab rope;
 };
@@ -238,23 +241,23 @@ __device__ __forceinline__ int row_tiles(const PagedAttnArgs& a, int n) { return
 
 // What a CTA keeps of the call's sequences in shared memory.
 struct Plan {
-    long long* pre;            // [B + 1] tiles before a sequence
+    long long* pre;            // [B + 1] units before a sequence
     int2* len;                 // [B] kv_len, n_new
+    int open;                  // units before an item's tiles
 };
 __host__ __device__ constexpr int plan_bytes(int B) { return (2 * B + 1) * 8; }
+constexpr int kPlanTmp = 2 * 16;   // two words a warp
 
-// Fills the plan (tmp: shared, 33); false for this thread if it saw lengths
-// that are out of range.
+// Fills the plan (tmp: shared, kPlanTmp); false for this thread if it saw
+// lengths that are out of range.
 template <int THREADS>
-__device__ __forceinline__ bool schedule(const PagedAttnArgs& a, const Plan& plan, long long* tmp) {
+__device__ __forceinline__ bool schedule(const PagedAttnArgs& a, Plan& plan, long long* tmp) {
+    static_assert(THREADS <= 512, "kPlanTmp");
     const int per = (a.B + THREADS - 1) / THREADS, b0 = (int)threadIdx.x * per;
     const int b1 = b0 + per < a.B ? b0 + per : a.B;
     long long* pre = plan.pre;
-    auto tiles = [&](int b) {
-        const int2 l = plan.len[b];
-        return (long long)tile_map(a, l.x, l.y).n * row_tiles(a, l.y) * a.c.Hkv;
-    };
-    long long sum = 0;
+    auto items = [&](int2 l) { return (long long)row_tiles(a, l.y) * a.c.Hkv; };
+    long long sum = 0, its = 0;   // tiles and items
     bool good = true;
     for (int b = b0; b < b1; ++b) {
         int2 l = make_int2(a.kv_len[b], a.n_new ? a.n_new[b] : a.M);
@@ -263,30 +266,47 @@ __device__ __forceinline__ bool schedule(const PagedAttnArgs& a, const Plan& pla
             good = false;
         }
         plan.len[b] = l;
-        sum += tiles(b);
+        sum += tile_map(a, l.x, l.y).n * items(l);
+        its += items(l);
     }
-    long long inc = sum;
+    long long inc = sum, itc = its;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+        const long long w = __shfl_up_sync(0xffffffffu, itc, o);
+        if (lane >= o) {
+            inc += v;
+            itc += w;
+        }
     }
-    if (lane == 31) tmp[warp] = inc;
+    if (lane == 31) {
+        tmp[warp] = inc;
+        tmp[16 + warp] = itc;
+    }
     __syncthreads();
-    long long base = inc - sum;
-    for (int w = 0; w < warp; ++w) base += tmp[w];
+    long long base = inc - sum, all = 0;
+    itc -= its;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) {
+            base += tmp[w];
+            itc += tmp[16 + w];
+        }
+        all += tmp[w];
+    }
+    // where a share is few tiles, how they spread counts for more
+    plan.open = a.open_max;
+    while (plan.open > 0 && 2ll * plan.open * a.grid > all) --plan.open;
+    base += plan.open * itc;
     for (int b = b0; b < b1; ++b) {
+        const int2 l = plan.len[b];
         pre[b] = base;
-        base += tiles(b);
+        base += (plan.open + tile_map(a, l.x, l.y).n) * items(l);
         if (b == a.B - 1) pre[a.B] = base;
     }
     __syncthreads();
     return good;
 }
-// first tile of CTA c's share, and the CTA whose share holds tile x.  With
-// fewer tiles than CTAs the first T CTAs take one each (no share between two
-// others is empty, so the merge reads written slots only).
 // a / b; small numbers by one approximate division and a correction (an
 // integer division is some 20 dependent instructions)
 __device__ __forceinline__ unsigned udiv(unsigned a, unsigned b) {
@@ -296,6 +316,10 @@ __device__ __forceinline__ unsigned udiv(unsigned a, unsigned b) {
     q += r < 0 ? -1 : r >= (int)b ? 1 : 0;
     return q;
 }
+// first unit of CTA c's share, and the CTA whose share holds unit x.  With
+// fewer units than CTAs the first T CTAs take one each.  So every CTA between
+// the first and the last that hold tiles of an item holds one too: the merge
+// reads written slots only.
 __device__ __forceinline__ long long share_lo(long long T, int c, int grid) {
     if (T < grid) return c < T ? c : T;
     if (T < (1ll << 31) / (grid + 1)) return udiv((unsigned)T * (unsigned)c, (unsigned)grid);   // (a 64-bit division is slower still)
@@ -312,9 +336,11 @@ struct Segment {
     int t0, n;                 // the item's tiles [t0, t0 + n)
     int len, n_new;            // of the sequence
     int rows, slot;            // rows of this tile, partial slot (-1: whole item)
+    long long x, next;         // unit of its first tile, and where the one behind it begins
     TileMap map;
 };
-// CTA c's segment at x of its range [.., xe)
+// CTA c's segment at x of its range [.., xe); n <= 0 if the range ends before
+// its first tile (only where the whole range lies before an item's tiles)
 __device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const Plan& plan, long long x, long long xe, int c) {
     Segment s;
     int b = 0;
@@ -329,13 +355,20 @@ __device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const Plan
     s.n_new = l.y;
     s.map = tile_map(a, l.x, l.y);
     const long long rel = x - plan.pre[b];
-    const unsigned item = rel < (1ll << 31) ? udiv((unsigned)rel, (unsigned)s.map.n) : (unsigned)(rel / s.map.n);
-    s.t0 = (int)(rel - (long long)item * s.map.n);
+    const unsigned units = (unsigned)(plan.open + s.map.n);
+    const unsigned item = rel < (1ll << 31) ? udiv((unsigned)rel, units) : (unsigned)(rel / units);
+    s.t0 = (int)(rel - (long long)item * units) - plan.open;
+    s.x = x;
+    if (s.t0 < 0) {
+        s.x -= s.t0;
+        s.t0 = 0;
+    }
     const unsigned nrt = (unsigned)row_tiles(a, l.y);
     s.g = (int)udiv(item, nrt);
     s.rt = (int)(item - s.g * nrt);
-    const long long left = xe - x;
+    const long long left = xe - s.x;
     s.n = s.map.n - s.t0 < left ? s.map.n - s.t0 : (int)left;
+    s.next = s.x + s.n + (s.t0 + s.n == s.map.n ? plan.open : 0);
     const int R = l.y * a.G - s.rt * a.RT;
     s.rows = R < a.RT ? R : a.RT;
     s.slot = s.t0 > 0 ? 2 * c : (s.n < s.map.n ? 2 * c + 1 : -1);
@@ -344,12 +377,12 @@ __device__ __forceinline__ Segment segment_at(const PagedAttnArgs& a, const Plan
 
 // row tiles that an item index counts for every sequence and KV head
 __device__ __forceinline__ int item_tiles(const PagedAttnArgs& a) { return (a.M * a.G + a.RT - 1) >> a.rt_log2; }
-// what CTA c notes for an item that begins in its share at tile x (one thread;
+// what CTA c notes for an item whose tiles begin in its share (one thread;
 // `mine`: its own entry, written at its end)
-__device__ __forceinline__ void note_split(const PagedAttnArgs& a, const Segment& s, long long T, long long x, int c, int4& mine) {
+__device__ __forceinline__ void note_split(const PagedAttnArgs& a, const Segment& s, long long T, int c, int4& mine) {
     if (s.t0 != 0) return;
     int4 r = make_int4(0, 0, 0, -1);
-    if (s.slot >= 0) r = make_int4(s.b * a.c.Hkv + s.g, s.rt * a.RT | s.rows << 16, c, share_of(T, x + s.map.n - 1, a.grid));
+    if (s.slot >= 0) r = make_int4(s.b * a.c.Hkv + s.g, s.rt * a.RT | s.rows << 16, c, share_of(T, s.x + s.map.n - 1, a.grid));
     if (a.by_item) a.split[(s.b * a.c.Hkv + s.g) * item_tiles(a) + s.rt] = r;
     else if (s.slot >= 0) mine = r;
 }

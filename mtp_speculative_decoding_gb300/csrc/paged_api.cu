@@ -213,7 +213,7 @@ int mtp_paged_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, cons
     const long long items = (long long)B * c->n_kv_heads * ((M * a.G + p.RT - 1) / p.RT);
     a.by_item = items <= p.grid;   // one merge CTA per row of an item, instead of per row of every CTA's
     a.rows_max = M * a.G < p.RT ? M * a.G : p.RT;
-    a.tile_log2 = p.tile_log2; a.grid = p.grid;
+    a.tile_log2 = p.tile_log2; a.grid = p.grid; a.open_max = p.tc ? kTcOpen : 0;
     a.timeout_ns = kWaitLimitNs;
     fill_rope(&a.rope, c->rope_theta, c->head_dim);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

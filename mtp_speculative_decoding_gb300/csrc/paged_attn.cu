@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
     Plan plan;
     plan.pre = reinterpret_cast<long long*>(sf + kCcRows);
     plan.len = reinterpret_cast<int2*>(plan.pre + a.B + 1);
-    __shared__ long long tmp[33];
+    __shared__ long long tmp[kPlanTmp];
     __shared__ const KT *skp[kCcTile], *svp[kCcTile];   // a position's K and V rows (null: absent)
     __shared__ float sks[kCcTile], svs[kCcTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -52,8 +52,9 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
     const QT* q = reinterpret_cast<const QT*>(a.q);
     while (x < xe) {
         const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
+        if (s.n <= 0) break;
         const int r0 = s.rt * a.RT;
-        if (tid == 0) note_split(a, s, T, x, blockIdx.x, split);
+        if (tid == 0) note_split(a, s, T, blockIdx.x, split);
         // queries: norm, rotation, scale
         for (int i0 = 0; i0 < kCcRows * U; i0 += kCcThreads) {
             const int i = i0 + tid, r = i / U, c = i % U;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
                 part[a.RT * (hd + 1) + r] = sf[r];
             }
         }
-        x += s.n;
+        x = s.next;
     }
     const int any = __syncthreads_or(bad);
     if (tid == 0) {

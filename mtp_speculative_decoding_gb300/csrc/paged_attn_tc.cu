@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                        *s_free = s_full + 2, *p_full = s_free + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *end_bar = q_full + 1;
     long long* tmp = reinterpret_cast<long long*>(end_bar + 1);
     Plan plan;
-    plan.pre = tmp + 33;
+    plan.pre = tmp + kPlanTmp;
     plan.len = reinterpret_cast<int2*>(plan.pre + a.B + 1);
     __shared__ unsigned int s_tmem;
     __shared__ int s_nfix[2], s_bad;
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         long long x = x0;
         while (x < xe && ok) {
             const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
+            if (s.n <= 0) break;
             const int end = s.len + s.n_new;
             const int lo = a.c.window > 0 && s.len + 1 > a.c.window ? s.len + 1 - a.c.window : 0;
             const int hi = a.c.window > 0 && end > a.c.window ? end - a.c.window : 0;
@@ -333,8 +334,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 pv_pg = kp;
                 pv_y = ky;
             }
-            if (lane == 0) note_split(a, s, T, x, blockIdx.x, split);
-            x += s.n;
+            if (lane == 0) note_split(a, s, T, blockIdx.x, split);
+            x = s.next;
         }
         if (lane == 0 && !a.by_item) a.split[blockIdx.x] = split;
         if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
@@ -371,6 +372,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
         long long x = x0;
         while (x < xe && ok) {
             const Segment s = segment_at(a, plan, x, xe, blockIdx.x);
+            if (s.n <= 0) break;
             hold(q_full, seg & 1);
             ++seg;
             for (int k = 0; k <= s.n && ok; ++k) {
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 }
             }
             ti += s.n;
-            x += s.n;
+            x = s.next;
         }
         if (elect_one()) umma_commit(end_bar);   // whatever was issued has ended before the CTA frees its memory
         const unsigned long long t0 = global_ns();
@@ -460,6 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             if (qr < nx.rows) load_q(qr, raw0, raw1, raw_j);
         };
         if (x < xe) open_next(x);
+        if (nx.n <= 0) x = xe;
         int4 split = make_int4(0, 0, 0, -1);
         float l[RW], m[RW], c[RW];
         // A turn prepares the next segment's queries (its scores' MMAs start
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 // every row attends every position of the tile
                 const bool whole = m_all[t % kTcMeta] && t0 + kTcTile - 1 <= p_first &&
                                    (a.c.window == 0 || t0 > p_last - a.c.window || t0 + kTcTile <= a.c.sink);
-                if (k == s.n - 1 && x + s.n < xe) open_next(x + s.n);   // its rows come in during this tile
+                if (k == s.n - 1 && s.next < xe) open_next(s.next);   // its rows come in during this tile
                 wait(s_full + buf, par);
                 tc_fence_after();
                 float z[RW];
@@ -853,7 +856,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
             }
             ti += s.n;
             g0 += 2 * s.n * S::D;
-            x += s.n;
+            x = s.next;
         }
     }
     __syncthreads();

@@ -11,6 +11,11 @@ namespace mtp {
 constexpr int kTcTileLog2 = 7, kTcTile = 1 << kTcTileLog2;          // positions of a tile: the MMA's M side
 constexpr int kTcSlotsMax = 24;       // ring slots of a CTA at most
 constexpr int kTcMeta = 16;           // tiles of page scales the producer may be ahead
+// What beginning an item costs a CTA, in tiles.  16 sequences of 2k to 32k
+// positions in e4m3 / 64 sequences of 4096 / 64 windows of 1024 in bf16 (head
+// dimension 256, 4 KV heads) take 110.6 / 98.3 / 46.4 us with 0, 101.5 / 97.9 /
+// 43.9 with 3 and 99.0 / 99.4 / 44.4 with 5.
+constexpr int kTcOpen = 3;
 constexpr int kTcFix = 256;           // positions listed as not finite
 constexpr int kTcSmemLimit = 227 * 1024 - 64;   // beside the static words
 
@@ -28,7 +33,7 @@ __host__ __device__ constexpr int tc_other(bool e4m3, int hd, int RT, int B) {
            + tc_p_bufs(e4m3, hd, RT) * (e4m3 ? 3 : 2 * 2) * RT * 128 // P, in parts
            + kTcMeta * 8 * 2 * 4 + kTcMeta * 4                   // page scales
            + RT * 4 * (4 + 3 + 4) + 2 * kTcFix * 4 + hd * 4          // row tables, list, rotation table
-           + (2 * kTcSlotsMax + kTcMeta + 16) * 8 + 33 * 8 + 64 + plan_bytes(B) + 1024;
+           + (2 * kTcSlotsMax + kTcMeta + 16) * 8 + kPlanTmp * 8 + 64 + plan_bytes(B) + 1024;
 }
 __host__ __device__ constexpr int tc_slot_bytes(bool e4m3, int hd) { return kTcTile * (hd < 128 ? hd : 128) * (e4m3 ? 1 : 2); }
 __host__ __device__ constexpr int tc_slots(bool e4m3, int hd, int RT, int B) {
