@@ -9,8 +9,8 @@
 // The logits come in by bulk copies through a ring in shared memory, so that a
 // thread spends no instructions on addresses and no registers on prefetches.
 // A row is cut into C pieces, one CTA each, and the C CTAs are one
-// thread-block cluster: the leader reads the others' sums and candidates
-// from their shared memory, so no workspace, no counters and no second launch
+// thread-block cluster: the others leave their sums and candidates in the
+// leader's shared memory, so no workspace, no counters and no second launch
 // are needed.
 #include "logprobs.cuh"
 
@@ -25,10 +25,10 @@ namespace mtp {
 namespace {
 
 constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
-constexpr int kLpVec = 4;                         // 16-byte vectors of a block a thread takes
-constexpr int kLpBlock = kLpThreads * kLpVec;     // vectors of a block: one bulk copy of 32 KB
-constexpr int kLpStages = 2;                      // blocks in shared memory; two CTAs share an SM
+constexpr int kLpRing = 8 * kLpThreads;           // 16-byte vectors in shared memory: 64 KB; two CTAs share an SM
+constexpr int kLpStagesMax = 4;
 constexpr int kLpCap = 4096;                      // candidates of a piece (a first slab of ties fits: 512 threads x 8)
+constexpr int kLpMaxC = 16;                       // pieces of a row
 constexpr float kL2E = 1.44269504f, kLn2 = 0.693147181f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -42,11 +42,6 @@ __device__ __forceinline__ unsigned long long warp_max_u32x2(unsigned long long 
     const unsigned lo = __reduce_max_sync(0xffffffffu, (unsigned)(v >> 32) == hi ? (unsigned)v : 0u);
     return (unsigned long long)hi << 32 | lo;
 }
-__device__ __forceinline__ unsigned long long warp_min_u32x2(unsigned long long v) {
-    const unsigned hi = __reduce_min_sync(0xffffffffu, (unsigned)(v >> 32));
-    const unsigned lo = __reduce_min_sync(0xffffffffu, (unsigned)(v >> 32) == hi ? (unsigned)v : ~0u);
-    return (unsigned long long)hi << 32 | lo;
-}
 // wait of at most a second (a copy takes a few microseconds)
 __device__ __forceinline__ bool mbar_wait_bounded(unsigned long long* bar, unsigned parity) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -55,6 +50,10 @@ __device__ __forceinline__ bool mbar_wait_bounded(unsigned long long* bar, unsig
         if (global_ns() - t0 > 1000000000ull) return false;
     return true;
 }
+// the cluster's barrier (whole warps; orders shared memory of all its CTAs)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7F800000); }
 
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -155,16 +154,20 @@ __device__ __forceinline__ void add_vec(const uint4& v, float lo, unsigned long 
 }
 
 struct LpShared {
-    uint4 ring[kLpStages][kLpBlock];
+    uint4 ring[kLpRing];
     unsigned long long buf[kLpCap];           // candidates, in no order
     unsigned long long sel[kLpThreads];       // those still above the bound at the end
-    unsigned long long top[MTP_MAX_TOP];      // the piece's best, descending
-    unsigned long long wkey[8 * kLpWarps];    // the first block's largest thread maxima, up to 8 a warp
+    unsigned long long top[MTP_MAX_TOP];      // the K best of select_top, descending
+    unsigned long long wkey[2 * kLpWarps];    // the largest thread maxima of a warp
+    unsigned long long full[kLpStagesMax], empty[kLpStagesMax];
     unsigned long long bound;
-    unsigned long long full[kLpStages], empty[kLpStages];
     Sums wsum[kLpWarps];
-    Sums piece;
     int count, nsel;                          // candidates; entries of sel
+    // the leader's: what the pieces' CTAs leave here
+    unsigned long long tops[kLpMaxC * MTP_MAX_TOP];   // [C][K], descending
+    Sums pieces[kLpMaxC];
+    float m, ls;                              // the row's reference, and ln of its sum
+    int nmerge;                               // entries of buf that the leader ranks
 };
 
 // The code below a block's sums runs a few times a CTA, and what it costs is
@@ -180,35 +183,37 @@ __device__ __noinline__ void rank_keys(const unsigned long long* key, int n, int
     const int g = 1 << glog, which = (int)threadIdx.x >> glog;
     const unsigned long long mine = which < n ? key[which] : ~0ull;
     int r = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = (int)threadIdx.x & (g - 1); i < n; i += g) r += key[i] > mine;
 #pragma unroll 1
     for (int o = g >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (which < n && r < K) out[r] = mine;
 }
-// A key that K of n <= 256 keys are at or above (0: there are fewer than K), by
-// one warp: the longest 16-bit prefix that K keys reach, bit by bit, and the
-// smallest key that reaches it.
-__device__ __noinline__ unsigned long long bound_of(const unsigned long long* keys, int n, int K) {
-    const int lane = threadIdx.x & 31;
-    unsigned long long x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = lane + 32 * i < n ? keys[lane + 32 * i] : 0ull;
-    unsigned p = 0u;
+// the K-th largest of a warp's distinct keys (0: none; 0 if there are fewer)
+__device__ __noinline__ unsigned long long kth_of(unsigned long long mine, int K) {
+    int c = 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) c += __shfl_sync(0xffffffffu, mine, i) > mine;
+    const unsigned hit = __ballot_sync(0xffffffffu, mine != 0ull && c == K - 1);
+    return hit ? __shfl_sync(0xffffffffu, mine, __ffs(hit) - 1) : 0ull;
+}
+// A key that K of the CTA's elements are at or above (0: not known): the K-th of
+// the largest few `best` of every warp, one element of each thread (0: none).
+__device__ __noinline__ unsigned long long bound_of(LpShared& sh, unsigned long long best, int K) {
+    const int lane = threadIdx.x & 31, warp = (int)threadIdx.x >> 5, R = K <= kLpWarps / 2 ? 1 : 2, n = R * kLpWarps;
 #pragma unroll 1
-    for (unsigned bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
-        const unsigned t = p | bit;
-        unsigned c = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c += (unsigned)(x[i] >> 32) >= t;
-        if (__reduce_add_sync(0xffffffffu, c) >= (unsigned)K) p = t;
+    for (int r = 0; r < R; ++r) {
+        const unsigned long long w = warp_max_u32x2(best);
+        if (lane == 0) sh.wkey[r * kLpWarps + warp] = w;
+        if (best == w) best = 0ull;
     }
-    if (p == 0u) return 0ull;
-    unsigned long long m = ~0ull;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if ((unsigned)(x[i] >> 32) >= p && x[i] < m) m = x[i];
-    return warp_min_u32x2(m);
+    __syncthreads();
+    if (warp == 0) {
+        const unsigned long long b = kth_of(lane < n ? sh.wkey[lane] : 0ull, K);
+        if (lane == 0) sh.bound = b;
+    }
+    __syncthreads();
+    return sh.bound;
 }
 // sums of a warp's lanes (m = -inf: none), relative to the largest reference
 __device__ __noinline__ Sums join_warp(Sums w) {
@@ -278,10 +283,13 @@ __device__ __forceinline__ float key_value(unsigned long long key) {
     return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
 
-template <typename T>
+template <typename T, int VEC>
 __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_constant__ LogprobArgs a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     LpShared& sh = *reinterpret_cast<LpShared*>(smem_raw);
+    // 16-byte vectors of a block that a thread takes, all of a block's, blocks in shared memory
+    constexpr int kLpVec = VEC, kLpBlock = kLpThreads * VEC, kLpStages = kLpRing / kLpBlock;
+    static_assert(kLpStages <= kLpStagesMax, "barriers");
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const long long row = blockIdx.x / C;
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
         const int n = nvec - blk * kLpBlock < kLpBlock ? nvec - blk * kLpBlock : kLpBlock;
         unsigned long long* bar = &sh.full[blk % kLpStages];
         mbar_arrive_expect_tx(bar, (unsigned)n * 16u);
-        bulk_g2s(sh.ring[blk % kLpStages], first + (long long)blk * kLpBlock * EPV, (unsigned)n * 16u, bar);
+        bulk_g2s(sh.ring + blk % kLpStages * kLpBlock, first + (long long)blk * kLpBlock * EPV, (unsigned)n * 16u, bar);
     };
     if (tid == 0) {
         for (int i = 0; i < kLpStages; ++i) {
@@ -318,8 +326,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
         for (int i = 0; i < kLpStages && i < blocks; ++i) fetch(i);
         sh.count = 0;
         sh.nsel = 0;
+        sh.nmerge = 0;
     }
-    if (tid < a.K) sh.top[tid] = 0ull;
+    if (C > 1) cluster_arrive_relaxed();   // waited for before the leader's memory is written: it has started by then
     float zt = neg_inf();
     if (tid == 0 && rank == 0 && tok >= 0) zt = ld_elem<T>(rowp, tok);
     // a loose element of this thread
@@ -346,7 +355,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     };
     unsigned long long bound = 0ull;          // K keys of the piece are at or above it
     float tau = neg_inf();                    // its value
-    int check = 3;                            // the block after which it is next taken from the candidates
+    float run = neg_inf();                    // this thread's largest element so far,
+    uint32_t run_at = 0u;                     // and the last index that it can have (not above its own key)
+    int check = 0;                            // the block at which the bound is next taken
     bool lost = false;                        // a wait gave up
     for (int it = 0; it < blocks; ++it) {
         const int stage = it % kLpStages;
@@ -364,7 +375,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < kLpVec; ++k) {
             const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
-            cur[k] = k * kLpThreads + tid < n ? sh.ring[stage][k * kLpThreads + tid] : make_uint4(none, none, none, none);
+            cur[k] = k * kLpThreads + tid < n ? sh.ring[stage * kLpBlock + k * kLpThreads + tid] : make_uint4(none, none, none, none);
         }
 #pragma unroll
         for (int k = 0; k < kLpVec; ++k) {
@@ -388,36 +399,27 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
 #pragma unroll 1
                 for (int i = 0; i < kLpVec * EPV; ++i) {
                     const int v = i / EPV * kLpThreads + tid;
-                    if (v < n) add_one(s, to_float(reinterpret_cast<const T*>(sh.ring[stage])[v * EPV + i % EPV]));
+                    if (v < n) add_one(s, to_float(reinterpret_cast<const T*>(sh.ring + stage * kLpBlock)[v * EPV + i % EPV]));
                 }
             }
         }
         if (a.K > 0) {
             // Candidates: the keys at or above a lower bound of the K-th.
             const long long at = (vs + (long long)it * kLpBlock) * EPV - h;   // element 0 of the block
-            if (it == 0) {
-                // The first bound is the K-th of the largest thread maxima (the K best
-                // mostly lie in different threads): up to eight of every warp.  (A
-                // maximum's key with the last index that it can have is not above
-                // its own.)
-                const int k = vm[0] == bm ? 0 : vm[1] == bm ? 1 : vm[2] == bm ? 2 : 3;
-                unsigned long long rest =
-                    bm > neg_inf() ? pack_argmax(bm, (uint32_t)(at + (k * kLpThreads + tid) * EPV + EPV - 1)) : 0ull;
-                const int R = a.K < 8 ? a.K : 8;
-#pragma unroll 1
-                for (int r = 0; r < R; ++r) {
-                    const unsigned long long w = warp_max_u32x2(rest);
-                    if (lane == 0) sh.wkey[r * kLpWarps + warp] = w;
-                    if (rest == w) rest = 0ull;
-                }
-                __syncthreads();
-                if (warp == 0) {
-                    const unsigned long long b = bound_of(sh.wkey, R * kLpWarps, a.K);
-                    if (lane == 0) sh.bound = b;
-                }
-                __syncthreads();
-                bound = sh.bound;
+            if (bm > run) {
+                int k = 0;
+#pragma unroll
+                for (int i = VEC - 1; i >= 0; --i)
+                    if (vm[i] == bm) k = i;
+                run = bm;
+                run_at = (uint32_t)(at + (k * kLpThreads + tid) * EPV + EPV - 1);
+            }
+            // At blocks 0, 3, 12, 39, ..: the K best mostly lie in different
+            // threads.
+            if (it == check) {
+                bound = bound_of(sh, run > neg_inf() ? pack_argmax(run, run_at) : 0ull, a.K);
                 tau = bound ? key_value(bound) : neg_inf();
+                check = 3 * check + 3;
             }
             int mask = 0;   // this lane's vectors that hold a candidate
 #pragma unroll
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             while (__any_sync(0xffffffffu, mask != 0)) {
                 const int v = (__ffs(mask) - 1) * kLpThreads + tid;
                 if (mask) {
-                    const uint4 x = sh.ring[stage][v];
+                    const uint4 x = sh.ring[stage * kLpBlock + v];
 #pragma unroll
                     for (int i = 0; i < EPV; ++i) {
                         const float z = Vec<T>::get(x, i);
@@ -442,20 +444,6 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);
-        if (a.K > 0 && it == check && it + 1 < blocks) {
-            // the candidates so far bound better; again after blocks 12, 39, .., so
-            // that each block adds fewer
-            __syncthreads();
-            const int cnt = sh.count;
-            if (warp == 0 && cnt <= 256) {
-                const unsigned long long b = bound_of(sh.buf, cnt, a.K);
-                if (lane == 0) sh.bound = b;
-            }
-            __syncthreads();
-            bound = sh.bound;   // (not below the one before: K candidates are at or above that)
-            tau = bound ? key_value(bound) : neg_inf();
-            check = 3 * check + 3;
-        }
     }
     if (loose > neg_inf()) {
         if (!(s.m > neg_inf()) || loose > s.m + 27.f) refer(loose);
@@ -473,7 +461,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     __syncthreads();
     if (warp == 0) {
         s = join_warp(lane < kLpWarps ? sh.wsum[lane] : Sums{neg_inf(), 0.f, 0.f});
-        if (lane == 0) sh.piece = s;
+        if (C > 1) cluster_wait();
+        if (lane == 0) *cluster.map_shared_rank(&sh.pieces[rank], 0) = s;
+    } else if (C > 1) {
+        cluster_wait();
     }
     if (a.K > 0) {
         int n = sh.count;
@@ -482,90 +473,96 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             select_slowly<T>(sh, rowp, e0 > 0 ? e0 : 0, e1 < a.V ? e1 : a.V, a.K);
             n = sh.count;
         }
-        if (tid < a.K) sh.top[tid] = 0ull;
-        for (int i = tid; i < n; i += kLpThreads) {
-            const unsigned long long key = sh.buf[i];
-            if (key >= bound) {   // (what is below it by now cannot be among the K)
-                const int pos = atomicAdd(&sh.nsel, 1);
-                if (pos < kLpThreads) sh.sel[pos] = key;
-            }
-        }
-        __syncthreads();
-        if (sh.nsel <= kLpThreads) rank_keys(sh.sel, sh.nsel, a.K, sh.top);
-        else select_top(sh, n, a.K);
-    }
-    if (C > 1) cluster.sync();
-    else __syncthreads();
-    if (rank == 0) {
-        if (warp == 0) {
-            Sums w = {neg_inf(), 0.f, 0.f};
-            if (lane < C) w = *cluster.map_shared_rank(&sh.piece, lane);
-            w = join_warp(w);
-            if (lane == 0) {
-                sh.wsum[0] = w;
-                const float ls = logf(w.S);
-                if (a.logprob) a.logprob[row] = ((zt == zt ? zt : neg_inf()) - w.m) - ls;
-                if (a.entropy) a.entropy[row] = ls - kLn2 * (w.T / w.S);
-            }
-        }
-        if (a.K > 0) {
-            int real = a.K;
-            const unsigned long long* best = sh.top;   // one piece: its own
-            if (C > 1) {
-                // a piece's k-th cannot be among the K best if K keys of another are
-                // larger, so most are dropped before the ranking
-                const int n = C * a.K;   // at most 16 pieces x 32 keys: one a thread
-                unsigned long long mine = 0ull, least = 0ull;
-                if (tid < n) mine = cluster.map_shared_rank(sh.top, tid / a.K)[tid % a.K];
-                if (warp == 0) {
-                    if (lane < C) least = cluster.map_shared_rank(sh.top, lane)[a.K - 1];
-                    least = warp_max_u32x2(least);
-                    if (lane == 0) {
-                        sh.bound = least;
-                        sh.count = 0;
-                    }
+        const unsigned long long* from = sh.buf;
+        if (n > kLpThreads) {
+            for (int i = tid; i < n; i += kLpThreads) {
+                const unsigned long long key = sh.buf[i];
+                if (key >= bound) {   // (what is below it by now cannot be among the K)
+                    const int pos = atomicAdd(&sh.nsel, 1);
+                    if (pos < kLpThreads) sh.sel[pos] = key;
                 }
-                __syncthreads();
-                if (mine != 0ull && mine >= sh.bound) sh.buf[atomicAdd(&sh.count, 1)] = mine;
-                __syncthreads();
-                real = sh.count;
-                rank_keys(sh.buf, real, a.K, sh.sel);
-                best = sh.sel;
             }
             __syncthreads();
-            if (tid < a.K) {
-                const unsigned long long key = tid < real ? best[tid] : 0ull;   // 0: fewer logits above -inf than K
-                if (a.top_ids) a.top_ids[row * a.K + tid] = key ? (int32_t)unpack_index(key) : -1;
-                if (a.top_logprobs)
-                    a.top_logprobs[row * a.K + tid] = key ? (key_value(key) - sh.wsum[0].m) - logf(sh.wsum[0].S) : neg_inf();
-            }
+            from = sh.sel;
+        }
+        const int m = n > kLpThreads ? sh.nsel : n;
+        unsigned long long* out = cluster.map_shared_rank(sh.tops, 0) + rank * a.K;
+        if (m <= kLpThreads) {
+            rank_keys(from, m, a.K, out);
+            if (tid >= m && tid < a.K) out[tid] = 0ull;
+        } else {
+            select_top(sh, n, a.K);
+            if (tid < a.K) out[tid] = sh.top[tid];
         }
     }
-    if (C > 1) cluster.sync();   // the leader has read this CTA's shared memory
+    if (C > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    if (rank != 0) return;
+    if (warp == 0) {
+        const Sums w = join_warp(lane < C ? sh.pieces[lane] : Sums{neg_inf(), 0.f, 0.f});
+        if (lane == 0) {
+            const float ls = logf(w.S);
+            sh.m = w.m;
+            sh.ls = ls;
+            if (a.logprob) a.logprob[row] = ((zt == zt ? zt : neg_inf()) - w.m) - ls;
+            if (a.entropy) a.entropy[row] = ls - kLn2 * (w.T / w.S);
+        }
+    }
+    if (a.K > 0) {
+        int real = a.K;
+        const unsigned long long* best = sh.tops;   // one piece: its own
+        if (C > 1) {
+            // the K-th of the pieces' first few bounds the K-th of all, so most
+            // are dropped before the ranking
+            const int n = C * a.K;   // at most 16 pieces x 32 keys: one a thread
+            const unsigned long long mine = tid < n ? sh.tops[tid] : 0ull;
+            const int p = lane & (C - 1), q = lane / C;   // C is a power of two
+            if (warp == 0) {
+                const unsigned long long b = kth_of(q < a.K ? sh.tops[p * a.K + q] : 0ull, a.K);
+                if (lane == 0) sh.bound = b;
+            }
+            __syncthreads();
+            if (mine != 0ull && mine >= sh.bound) sh.buf[atomicAdd(&sh.nmerge, 1)] = mine;
+            __syncthreads();
+            real = sh.nmerge;
+            rank_keys(sh.buf, real, a.K, sh.sel);
+            best = sh.sel;
+        }
+        __syncthreads();
+        if (tid < a.K) {
+            const unsigned long long key = tid < real ? best[tid] : 0ull;   // 0: fewer logits above -inf than K
+            if (a.top_ids) a.top_ids[row * a.K + tid] = key ? (int32_t)unpack_index(key) : -1;
+            if (a.top_logprobs) a.top_logprobs[row * a.K + tid] = key ? (key_value(key) - sh.m) - sh.ls : neg_inf();
+        }
+    }
 }
 
 constexpr int kMaxDev = 64;
-template <typename T>
+template <typename T, int VEC>
 cudaError_t launch(const LogprobArgs& a, int sms, cudaStream_t s) {
     static bool ready[kMaxDev] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDev || !ready[dev]) {   // clusters of 16 are opt-in
-        e = cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(logprob_kernel<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LpShared));
+        e = cudaFuncSetAttribute(logprob_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LpShared));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDev) ready[dev] = true;
     }
     // Pieces a row: the fewest waves of bytes (an SM's share of the bandwidth is
     // about 45 bytes a ns, which takes two CTAs), against some 2500 ns that each
     // wave of two CTAs an SM costs in first loads, joins and cluster barriers;
-    // none below half a block.
+    // none below 16 KB.
     int C = 1;
     double best = 1e30;
-    for (int c = 1; c <= 16; c *= 2) {
-        if (c > 1 && a.V / c < (long long)kLpBlock * Vec<T>::n / 2) break;
+    for (int c = 1; c <= kLpMaxC; c *= 2) {
+        if (c > 1 && a.V / c < 4ll * kLpThreads * Vec<T>::n / 2) break;
         const long long ctas = a.rows * c, deep = (ctas + sms - 1) / sms;
         const double rate = deep >= 2 ? 45.0 : 30.0;
         const double ns = (double)a.V * sizeof(T) / rate * (double)deep / c + 2500.0 * (double)((deep + 1) / 2);
@@ -586,13 +583,18 @@ cudaError_t launch(const LogprobArgs& a, int sms, cudaStream_t s) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprob_kernel<T>, a);
+    return cudaLaunchKernelEx(&cfg, logprob_kernel<T, VEC>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobArgs& a, int ldtype, int sms, cudaStream_t s) {
-    return ldtype == MTP_DTYPE_BF16 ? launch<uint16_t>(a, sms, s) : launch<float>(a, sms, s);
+    // Blocks of 32 KB; of 16 KB for fp32 logits without alternatives (128 rows of
+    // 248320: 24.1 us, 26.5 with 32 KB; with one alternative 36.1 against 34.4,
+    // because the first block bounds less; 144 rows of 262144 bf16 logits without
+    // alternatives 18.3 against 17.7).
+    if (ldtype == MTP_DTYPE_BF16) return launch<uint16_t, 4>(a, sms, s);
+    return a.K > 0 ? launch<float, 4>(a, sms, s) : launch<float, 2>(a, sms, s);
 }
 
 }  // namespace mtp
