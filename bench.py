@@ -279,18 +279,16 @@ class ClockSampler:
 
 
 def kernel_source_hash() -> str:
-    """sha256 prefix over the library's CUDA sources and its public header:
+    """sha256 prefix over the sources of the kernels that the workloads launch:
     ties a recorded ncu traffic figure to the kernel it was taken on."""
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "mtp_speculative_decoding_gb300", "csrc")
-    for fn in sorted(os.listdir(csrc)):
-        if fn.endswith((".cu", ".cuh", ".h")):
-            h.update(fn.encode())
-            with open(os.path.join(csrc, fn), "rb") as f:
-                h.update(f.read())
-    with open(os.path.join(ROOT, "include", "mtp.h"), "rb") as f:
-        h.update(f.read())
+    for fn in ("common.cuh", "draft.cuh", "draft_dispatch.cu", "draft_inst.cu", "draft_kernel.cuh", "noalloc.cu",
+               "sample.cuh", "verify.cu", "verify.cuh"):
+        h.update(fn.encode())
+        with open(os.path.join(csrc, fn), "rb") as f:
+            h.update(f.read())
     return h.hexdigest()[:16]
 
 
