@@ -1,9 +1,10 @@
 // kv_append.cu -- new key and value rows into a paged KV cache: RMSNorm and
 // rotation of the keys, one rounding to the cache's type.
 //
-// key = rope(rmsnorm(k), p), value = v.  Both are bound by the bytes in and
-// out (small calls: by the launch and two dependent loads, the length and then
-// the page).
+// key = rope(rmsnorm(k), p), value = v.  Long calls are bound by the bytes in
+// and out or by the instructions of an element (norm, angle, maximum,
+// rounding), small ones by the launch and two dependent loads, the length and
+// then the page.
 #include "paged.cuh"
 
 #include <cuda_fp8.h>
@@ -38,7 +39,10 @@ __device__ void append_status(const AppendArgs& a) {
 // ---------------------------------------------------------------------------
 // fp32 and bf16 caches: a thread takes one unit (16 elements) of `hpt` KV
 // heads of one row, so that the angles of a row are computed once for those
-// heads; gridDim.y: keys and values of every sequence
+// heads; gridDim.y: keys and values of every sequence.
+// One sequence, 8191 rows x 8 heads of 128, fp32 to bf16 (101 MB): 19.8 us, 5.1
+// TB/s (bound by the bytes; a copy takes 14.9).  One sequence, 4 rows x 4 heads
+// of 256, bf16: 3.5 us.
 // ---------------------------------------------------------------------------
 template <typename IT, typename CT>
 __global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant__ AppendArgs a) {
@@ -182,7 +186,9 @@ __device__ __forceinline__ bool page_rows(const AppendArgs& a, int nt, PageRows&
 }
 
 // Few rows a page (decoding): a CTA takes one KV head; every thread's one unit
-// stays in registers between the maximum and the rounding.
+// stays in registers between the maximum and the rounding.  64 sequences x 3
+// rows x 4 heads of 256: 4.7 us, all of it latency (launch, length, page, row,
+// barrier).
 template <typename IT>
 __global__ void __launch_bounds__(256) append_e4m3_kernel(const __grid_constant__ AppendArgs a) {
     const int ps = 1 << a.c.ps_log2, nt = (a.M + ps - 2) / ps + 1;
@@ -246,6 +252,10 @@ __global__ void __launch_bounds__(256) append_e4m3_kernel(const __grid_constant_
 // the page has at most 1024 units of a head, and they stay in registers between
 // the maximum and the rounding; larger pages are read twice, the second time
 // from L2.
+// 8 sequences of up to 4096 rows x 4 heads of 256, bf16 in (a ragged batch of 104
+// MB in and out): 44.6 us, 2.3 TB/s.  The 16 warps of an SM (123 registers a
+// thread hold two units) bound it: they issue 46% of the time and wait at a
+// barrier a head, on shared-memory tables and on each other's pipes.
 constexpr int kPageThreads = 512;
 
 template <typename IT> struct Raw { uint4 v[4 * sizeof(IT) / 4]; };   // a unit as loaded
