@@ -130,10 +130,32 @@ __device__ __forceinline__ bool vote_or(int wg, bool p) {
 }
 __device__ __forceinline__ void wg_sync(int wg) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + wg) : "memory"); }
 __device__ __forceinline__ void both_sync() { asm volatile("barrier.cta.sync.aligned 3, 256;" ::: "memory"); }
-__device__ __forceinline__ float redux_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
+// N rows' sums or maxima over a warp's lanes: at each step a lane hands half of
+// its rows over, so that N - 1 exchanges (and a few for N below 32) do what 5 N
+// would.  Lane i ends with row i / (32 / N).
+template <bool MAX, int N>
+__device__ __forceinline__ float rows_reduce(const float (&x)[N], int lane) {
+    auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+    float v[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float keep = lane & 16 ? x[i + N / 2] : x[i], give = lane & 16 ? x[i] : x[i + N / 2];
+        v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 16));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        const int n = N * o / 32;   // rows that stay
+        if (n > 0) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float keep = lane & o ? v[i + n] : v[i], give = lane & o ? v[i] : v[i + n];
+                v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+            }
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+        }
+    }
+    return v[0];
 }
 __device__ __forceinline__ float fexp2(float x) {
     float y;
@@ -188,10 +210,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     float* s_lo = s_hi + HD / 2;
     float* m_ks = s_lo + HD / 2;                               // [kTcMeta][8] key scale (0: page not loaded)
     float* m_vs = m_ks + kTcMeta * 8;                          // [kTcMeta][8] exponent of the value scale
-    float* s_m = m_vs + kTcMeta * 8;                           // [RT] reference
-    float* s_f = s_m + RT;                                     // [RT] rescale factor
+    float* s_inv = m_vs + kTcMeta * 8;                         // [RT] one over the row's sum
+    float* s_f = s_inv + RT;                                   // [RT] rescale factor
     float* s_c = s_f + RT;                                     // [RT] scale of the query row
-    float* s_red = s_c + RT;                                   // [4][RT]
+    float* s_red = s_c + RT;                                   // [RT][4]: a row's sum or maximum of every warp
     int* s_pos2 = reinterpret_cast<int*>(s_red + 4 * RT);      // [2][RT] position of the row
     int* s_row2 = s_pos2 + 2 * RT;                             // [2][RT] output row
     int* s_fix2 = s_row2 + 2 * RT;                             // [2][kTcFix]
@@ -592,23 +614,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 const unsigned int last = ti - 1;
                 const int pe = par0;
                 wg_sync(wg);   // the last tile's column maxima are read
+                {
+                    const float v = rows_reduce<false, RW>(l, lane);
+                    if (lane % (32 / RW) == 0) s_red[(rw + lane / (32 / RW)) * 4 + w4] = v;
+                }
+                float* part = s.slot >= 0 ? a.part + s.slot * part_floats(RT, HD) : nullptr;
+                if (part) {
 #pragma unroll
-                for (int r = 0; r < RW; ++r) {
-                    const float v = warp_sum(l[r]);
-                    if (lane == 0) s_red[w4 * RT + rw + r] = v;
+                    for (int r = 0; r < RW; ++r)
+                        if (tok == r) part[RT * HD + rw + r] = m[r];
+                }
+                wg_sync(wg);
+                if (tok < RW) {
+                    const float4 q = *reinterpret_cast<const float4*>(s_red + (rw + tok) * 4);
+                    const float v = (q.x + q.y) + (q.z + q.w);
+                    s_inv[rw + tok] = v == 0.f ? 0.f : 1.f / v;
+                    if (part) part[RT * (HD + 1) + rw + tok] = v;
                 }
                 both_sync();
-                float* part = s.slot >= 0 ? a.part + s.slot * part_floats(RT, HD) : nullptr;
-#pragma unroll
-                for (int r = 0; r < RW; ++r) {
-                    const float* q = s_red + rw + r;
-                    const float v = (q[0] + q[RT]) + (q[2 * RT] + q[3 * RT]);
-                    l[r] = part ? 1.f : v == 0.f ? 0.f : 1.f / v;
-                    if (part && tok == r) {
-                        part[RT * HD + rw + r] = m[r];
-                        part[RT * (HD + 1) + rw + r] = v;
-                    }
-                }
                 const int nfix = s_nfix[pe] < kTcFix ? s_nfix[pe] : kTcFix;
                 wait(pv_done + (last & 1), (last >> 1) & 1);
                 tc_fence_after();
@@ -645,7 +668,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     for (int r = 0; r < RW; ++r) {
                         if (rw + r >= s.rows) break;
                         if (part) part[(rw + r) * HD + d] = o[r];
-                        else reinterpret_cast<uint16_t*>(a.out)[(long long)s_row2[pe * RT + rw + r] * HD + d] = (uint16_t)pack_bf16(o[r] * l[r], 0.f);
+                        else reinterpret_cast<uint16_t*>(a.out)[(long long)s_row2[pe * RT + rw + r] * HD + d] = (uint16_t)pack_bf16(o[r] * s_inv[rw + r], 0.f);
                     }
                 }
                 tc_fence_before();
@@ -677,16 +700,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 tc_fence_after();
                 float z[RW];
                 {
-                    uint32_t v[S::NQ][RW];
+                    constexpr int CW = RW < 16 ? RW : 16;   // rows at a time: all parts of 32 would spill
 #pragma unroll
-                    for (int part = 0; part < S::NQ; ++part)
+                    for (int b = 0; b < RW; b += CW) {
+                        uint32_t v[S::NQ][CW];
 #pragma unroll
-                        for (int i = 0; i < RW; i += 8) tmem_ld8(my + buf * S::SCOLS + part * RT + rw + i, v[part] + i);
-                    tmem_ld_wait();
+                        for (int part = 0; part < S::NQ; ++part)
 #pragma unroll
-                    for (int r = 0; r < RW; ++r) {
-                        z[r] = __uint_as_float(v[0][r]) + __uint_as_float(v[1][r]);
-                        if (S::NQ == 3) z[r] += __uint_as_float(v[S::NQ - 1][r]);
+                            for (int i = 0; i < CW; i += 8) tmem_ld8(my + buf * S::SCOLS + part * RT + rw + b + i, v[part] + i);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int r = 0; r < CW; ++r) {
+                            z[b + r] = __uint_as_float(v[0][r]) + __uint_as_float(v[1][r]);
+                            if (S::NQ == 3) z[b + r] += __uint_as_float(v[S::NQ - 1][r]);
+                        }
                     }
                 }
                 tc_fence_before();
@@ -697,26 +724,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                     for (int r = 0; r < RW; ++r) z[r] = fmaf(z[r], ks * c[r], ev);
                 }
                 if (!whole) {
-                    const bool here = ks != 0.f;
+                    // rows at positions [pos, pos + span) attend this one (see attends())
+                    const unsigned span = ks == 0.f ? 0u : a.c.window == 0 || pos < a.c.sink ? 1u << 31 : (unsigned)a.c.window;
+                    const int4* rows = reinterpret_cast<const int4*>(s_pos2 + par0 * RT + rw);
 #pragma unroll
-                    for (int r = 0; r < RW; ++r)
-                        if (!(here && attends(a.c, pos, s_pos2[par0 * RT + rw + r]))) z[r] = -__int_as_float(0x7F800000);
+                    for (int r = 0; r < RW; r += 4) {
+                        const int4 p = rows[r / 4];
+                        if ((unsigned)(p.x - pos) >= span) z[r] = -__int_as_float(0x7F800000);
+                        if ((unsigned)(p.y - pos) >= span) z[r + 1] = -__int_as_float(0x7F800000);
+                        if ((unsigned)(p.z - pos) >= span) z[r + 2] = -__int_as_float(0x7F800000);
+                        if ((unsigned)(p.w - pos) >= span) z[r + 3] = -__int_as_float(0x7F800000);
+                    }
                 }
                 bool over = false;
 #pragma unroll
                 for (int r = 0; r < RW; ++r) over = over || z[r] > m[r] + S::kSlack;
                 if (vote_or(wg, over)) {
                     // move the references: the column maxima of this tile
-#pragma unroll
-                    for (int r = 0; r < RW; ++r) {
-                        const float mx = redux_max(z[r]);
-                        if (lane == 0) s_red[w4 * RT + rw + r] = mx;
-                    }
+                    const float mx = rows_reduce<true, RW>(z, lane);
+                    if (lane % (32 / RW) == 0) s_red[(rw + lane / (32 / RW)) * 4 + w4] = mx;
                     wg_sync(wg);
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
-                        const float* q = s_red + rw + r;
-                        const float mn = fmaxf(fmaxf(fmaxf(q[0], q[RT]), fmaxf(q[2 * RT], q[3 * RT])), m[r]);
+                        const float4 q = *reinterpret_cast<const float4*>(s_red + (rw + r) * 4);
+                        const float mn = fmaxf(fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)), m[r]);
                         const float f = fexp2(m[r] - mn);
                         l[r] *= f;
                         m[r] = mn;
