@@ -165,7 +165,7 @@ struct LpShared {
     unsigned long long buf[kLpCap];           // candidates, in no order
     unsigned long long sel[kLpThreads];       // those still above the bound at the end
     unsigned long long top[MTP_MAX_TOP];      // the K best of select_top, descending
-    unsigned long long wkey[2 * kLpWarps];    // the largest thread maxima of a warp
+    unsigned long long wkey[64];              // the largest thread maxima of the warps
     unsigned long long full[kLpStagesMax], empty[kLpStagesMax];
     unsigned long long bound;
     Sums wsum[kLpWarps];
@@ -196,27 +196,38 @@ __device__ __noinline__ void rank_keys(const unsigned long long* key, int n, int
     for (int o = g >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (which < n && r < K) out[r] = mine;
 }
-// the K-th largest of a warp's distinct keys (0: none; 0 if there are fewer)
-__device__ __noinline__ unsigned long long kth_of(unsigned long long mine, int K) {
-    int c = 0;
+// the K-th largest of n <= 64 distinct keys in shared memory, by one warp (0 is
+// no key; 0 if there are fewer)
+__device__ __noinline__ unsigned long long kth_of(const unsigned long long* keys, int n, int K) {
+    const int lane = threadIdx.x & 31;
+    const unsigned long long a = lane < n ? keys[lane] : 0ull, b = lane + 32 < n ? keys[lane + 32] : 0ull;
+    int ca = 0, cb = 0;
 #pragma unroll 8
-    for (int i = 0; i < 32; ++i) c += __shfl_sync(0xffffffffu, mine, i) > mine;
-    const unsigned hit = __ballot_sync(0xffffffffu, mine != 0ull && c == K - 1);
-    return hit ? __shfl_sync(0xffffffffu, mine, __ffs(hit) - 1) : 0ull;
+    for (int i = 0; i < n; ++i) {
+        const unsigned long long x = keys[i];
+        ca += x > a;
+        cb += x > b;
+    }
+    const bool ha = a != 0ull && ca == K - 1, hb = b != 0ull && cb == K - 1;
+    const unsigned hit = __ballot_sync(0xffffffffu, ha || hb);
+    return hit ? __shfl_sync(0xffffffffu, ha ? a : b, __ffs(hit) - 1) : 0ull;
 }
 // A key that K of the CTA's elements are at or above (0: not known): the K-th of
-// the largest few `best` of every warp, one element of each thread (0: none).
-__device__ __noinline__ unsigned long long bound_of(LpShared& sh, unsigned long long best, int K) {
-    const int lane = threadIdx.x & 31, warp = (int)threadIdx.x >> 5, R = K <= kLpWarps / 2 ? 1 : 2, n = R * kLpWarps;
+// the largest few `best` of each of the first W warps, one element of each thread (0: none).
+__device__ __noinline__ unsigned long long bound_of(LpShared& sh, unsigned long long best, int W, int K) {
+    const int lane = threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+    const int R = (3 * K / 2 + W) / W, n = R * W;   // half as many again as K, 64 in all at most
+    if (warp < W) {
 #pragma unroll 1
-    for (int r = 0; r < R; ++r) {
-        const unsigned long long w = warp_max_u32x2(best);
-        if (lane == 0) sh.wkey[r * kLpWarps + warp] = w;
-        if (best == w) best = 0ull;
+        for (int r = 0; r < R; ++r) {
+            const unsigned long long w = warp_max_u32x2(best);
+            if (lane == 0) sh.wkey[r * W + warp] = w;
+            if (best == w) best = 0ull;
+        }
     }
     __syncthreads();
     if (warp == 0) {
-        const unsigned long long b = kth_of(lane < n ? sh.wkey[lane] : 0ull, K);
+        const unsigned long long b = kth_of(sh.wkey, n, K);
         if (lane == 0) sh.bound = b;
     }
     __syncthreads();
@@ -365,6 +376,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     float run = neg_inf();                    // this thread's largest element so far,
     uint32_t run_at = 0u;                     // and the last index that it can have (not above its own key)
     int check = 0;                            // the block at which the bound is next taken
+    const int warps = nvec < kLpThreads ? (nvec + 31) / 32 : kLpWarps;   // that hold elements
     bool lost = false;                        // a wait gave up
     for (int it = 0; it < blocks; ++it) {
         const int stage = it % kLpStages;
@@ -424,7 +436,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             // At blocks 0, 3, 12, 39, ..: the K best mostly lie in different
             // threads.
             if (it == check) {
-                bound = bound_of(sh, run > neg_inf() ? pack_argmax(run, run_at) : 0ull, a.K);
+                bound = bound_of(sh, run > neg_inf() ? pack_argmax(run, run_at) : 0ull, warps, a.K);
                 tau = bound ? key_value(bound) : neg_inf();
                 check = 3 * check + 3;
             }
@@ -481,7 +493,11 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             n = sh.count;
         }
         const unsigned long long* from = sh.buf;
-        if (n > kLpThreads) {
+        if (n > kLpThreads) {   // a bound from the candidates themselves: every thread's largest of its share
+            unsigned long long best = 0ull;
+            for (int i = tid; i < n; i += kLpThreads) best = sh.buf[i] > best ? sh.buf[i] : best;
+            const unsigned long long b = bound_of(sh, best, kLpWarps, a.K);
+            bound = b > bound ? b : bound;
             for (int i = tid; i < n; i += kLpThreads) {
                 const unsigned long long key = sh.buf[i];
                 if (key >= bound) {   // (what is below it by now cannot be among the K)
@@ -529,7 +545,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             const unsigned long long mine = tid < n ? sh.tops[tid] : 0ull;
             const int p = lane & (C - 1), q = lane / C;   // C is a power of two
             if (warp == 0) {
-                const unsigned long long b = kth_of(q < a.K ? sh.tops[p * a.K + q] : 0ull, a.K);
+                sh.wkey[lane] = q < a.K ? sh.tops[p * a.K + q] : 0ull;
+                __syncwarp();
+                const unsigned long long b = kth_of(sh.wkey, 32, a.K);
                 if (lane == 0) sh.bound = b;
             }
             __syncthreads();
