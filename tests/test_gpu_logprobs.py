@@ -176,3 +176,23 @@ def test_more_than_32_bits_of_logits():
     assert abs(float(lp[16999]) - (5 - math.log(131071 + math.exp(5)))) < 1e-4
     assert abs(float(lp[16000]) + math.log(131072)) < 1e-4 and ids[16999].tolist() == [131071, 0] and ids[16000].tolist() == [0, 1]
     assert lp[0] == 7.0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,K", [(2154, 32), (600, 32), (4099, 20), (1100, 1), (517, 8)])
+def test_rows_that_few_warps_hold(dtype, V, K):
+    z = logits(37, V, dtype, 61)
+    tok = torch.arange(37, dtype=torch.int32, device="cuda") * 13
+    check(z, tok, K, run(z, tok, K))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("at,n", [(0, 1000), (70001, 1000), (131000, 200), (5, 31), (199000, 1000)])
+def test_an_allowed_set_that_lies_together(dtype, at, n):
+    """Everything masked but one run of logits: a few warps hold all candidates."""
+    z = logits(5, 200000, dtype, 62)
+    keep = torch.zeros(200000, dtype=torch.bool, device="cuda")
+    keep[at:at + n] = True
+    z = z.masked_fill(~keep, -math.inf)
+    tok = torch.full((5,), at, dtype=torch.int32, device="cuda")
+    check(z, tok, 32, run(z, tok, 32))

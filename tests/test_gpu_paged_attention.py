@@ -121,6 +121,25 @@ def test_many_sequences_of_ragged_lengths(kv):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("kv,hd,hkv,G,M", [("bf16", 64, 2, 2, 2), ("e4m3", 128, 4, 2, 1), ("bf16", 64, 1, 16, 9)])
+def test_many_short_sequences_beside_long_ones(kv, hd, hkv, G, M):
+    """Shares that count what beginning an item costs: CTAs with many items of
+    one tile, with a part of a long one, and with none."""
+    g = torch.Generator().manual_seed(41)
+    B, page = 500, 16
+    lens = torch.randint(0, 120, (B,), generator=g).tolist()
+    for b, x in ((0, 3000), (3, 5001), (250, 6000), (251, 0), (499, 4345)):
+        lens[b] = x
+    n = torch.randint(0, M + 1, (B,), generator=g).tolist()
+    n[0] = n[250] = n[499] = M
+    pool = pc.Pool(B, (max(lens) + M) // page + 2, page, hkv, hd, kv, seed=42)
+    pool.fill([a + c for a, c in zip(lens, n)], seed=43)
+    q = queries(B, M, hkv * G, hd, torch.bfloat16, seed=44)
+    out, st = run(pool, q, lens, n, rope_theta=1e6)
+    assert st == mtp().MTP_OK
+    check(pool, out, q, None, lens, n, 1e6)
+
+
 @pytest.mark.parametrize("kv,hd,G,M", [("bf16", 512, 8, 3), ("e4m3", 256, 4, 3), ("bf16", 64, 2, 1)])
 def test_the_largest_batch(kv, hd, G, M):
     """MTP_MAX_PAGED_BATCH sequences, one call of append and one of attention."""
