@@ -30,7 +30,7 @@ constexpr int kCcThreads = 128;
 // shared memory.  Not the bytes bound it but a group's few rows against
 // every position in fp32 through shared memory: 64 sequences x 3 rows of fp32 queries over
 // 4096 positions of an e4m3 cache (16 heads, 4 KV heads of 256) take 2080 us,
-// where the tensor cores take 98 for bf16 queries; one sequence x 4 rows over
+// where the tensor cores take 97 for bf16 queries; one sequence x 4 rows over
 // 8192 positions of a bf16 cache 92 us.  Warp w scores rows 4w..4w+3 with lane = position; thread d
 // owns output dimensions d, d + 128, .. of all 16 rows.
 template <typename QT, typename KT>

@@ -13,8 +13,8 @@ constexpr int kTcSlotsMax = 24;       // ring slots of a CTA at most
 constexpr int kTcMeta = 16;           // tiles of page scales the producer may be ahead
 // What beginning an item costs a CTA, in tiles.  16 sequences of 2k to 32k
 // positions in e4m3 / 64 sequences of 4096 / 64 windows of 1024 in bf16 (head
-// dimension 256, 4 KV heads) take 110.6 / 98.3 / 46.4 us with 0, 101.5 / 97.9 /
-// 43.9 with 3 and 99.0 / 99.4 / 44.4 with 5.
+// dimension 256, 4 KV heads) take 105.6 / 97.2 / 44.8 us with 0, 99.2 / 96.8 /
+// 43.0 with 3 and 98.6 / 98.3 / 43.5 with 5.
 constexpr int kTcOpen = 3;
 constexpr int kTcFix = 256;           // positions listed as not finite
 constexpr int kTcSmemLimit = 227 * 1024 - 64;   // beside the static words
