@@ -334,15 +334,19 @@ __global__ void __launch_bounds__(kPageThreads, 1) append_e4m3_pages_kernel(cons
         for (int i = tid; i < a.hd; i += T) s_gain[i] = a.k_norm[i];
     const int nb = ps >> 4;
     if (rot) {
-        const int pr = tid & (half - 1), step = T / half;   // one pair a thread: its table entries are read once
-        const float hi = a.rope.hi[pr], lo = a.rope.lo[pr];
+        // one pair a thread, whose table entries are read once; a second one where
+        // there are fewer threads than pairs (head_dim 512, calls of 9 to 14 rows)
+        const int step = T < half ? 1 : T / half;
         if (tid < step * half)
-            for (int e = tid / half; e < nb + 16; e += step) {
-                float pl, ph;
-                split_pos(e < nb ? w.first + 16 * e : e - nb, pl, ph);
-                float2 r;
-                pair_angle<false>(pl, ph, hi, lo, r.x, r.y);
-                s_rot[e * half + pr] = r;
+            for (int pr = tid & (half - 1); pr < half; pr += T) {
+                const float hi = a.rope.hi[pr], lo = a.rope.lo[pr];
+                for (int e = tid / half; e < nb + 16; e += step) {
+                    float pl, ph;
+                    split_pos(e < nb ? w.first + 16 * e : e - nb, pl, ph);
+                    float2 r;
+                    pair_angle<false>(pl, ph, hi, lo, r.x, r.y);
+                    s_rot[e * half + pr] = r;
+                }
             }
     }
     if (tid < 32) red[0][tid] = red[1][tid] = 0u;   // (warps that are not there)
