@@ -1,0 +1,154 @@
+"""mtp_paged_attention where single values decide: the bits that the
+tensor-core path keeps of a probability, NaN values and page scales."""
+import pytest
+import torch
+
+import paged_common as pc
+from test_gpu_paged_attention import check, queries, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from mtp_speculative_decoding_gb300 import build
+    build.build()
+
+
+def mtp():
+    import mtp_speculative_decoding_gb300 as m
+    return m
+
+
+def put(pool, w, t, x):
+    """Row t of sequence 0, KV head 0, becomes x (e4m3: codes under a scale of 1)."""
+    pg, sl = int(pool.table[0, t // pool.page]), t % pool.page
+    x = torch.as_tensor(x, dtype=torch.float32, device="cuda")
+    if pool.dtype == "e4m3":
+        getattr(pool, w).view(torch.uint8)[pg, 0, sl] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        getattr(pool, w)[pg, 0, sl] = x.to(pool.k.dtype)
+
+
+# ---------------------------------------------------------------------------
+# the bits of a probability
+# ---------------------------------------------------------------------------
+
+def parts_left(e, dtype, parts):
+    """What `parts` successive roundings to dtype leave of e."""
+    for _ in range(parts):
+        e = e - e.to(torch.float32).to(dtype).double()
+    return e
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_the_bits_of_a_probability(kv):
+    """Two groups of positions with values +1 and -1 whose probabilities nearly
+    cancel, chosen so that one operand part fewer than the path keeps would
+    round every one of a group up and of the other down.
+
+    The probabilities keep 16 bits (bf16: two parts, off by at most 2^-16 of
+    each) or 9 (e4m3: three e5m2 parts, 2^-9, of a binary16 that is off by
+    2^-11).  Everything else: the query is 1 in the dimensions that the keys
+    use, so a score z (at most 1.1 in size) is a sum of 4 products, each off
+    by what the query's parts leave (2^-16 or 2^-12) of sum |q k| <= 1.2 and
+    by the accumulation's 2 (2 hd + 80) u; a probability is off by twice
+    that (numerator and sum).  The two sums run over 129 terms: 2 (2 T + 200)
+    u of the mass.  The output rounds to bf16, 2^-8 of itself, and it is
+    small: at most 2^-8 of the mass, or 2^-5 against e4m3."""
+    hd, n, T = 128, 64, 129
+    low = {"bf16": torch.bfloat16, "e4m3": torch.float8_e5m2}[kv]
+    keeps = {"bf16": 2, "e4m3": 3}[kv]
+    # keys: one or two representable numbers whose sum is the score, in natural units
+    if kv == "bf16":
+        a = -torch.arange(32, 160, dtype=torch.float64) / 256                       # bf16 numbers
+    else:
+        a = -torch.arange(8, 16, dtype=torch.float64) / 16                          # e4m3 numbers
+    b = -torch.arange(8, 16, dtype=torch.float64) / 512
+    c = (a[:, None] + b[None]).reshape(-1)
+    e = torch.exp(c)                                                                # relative to the largest, exp(0)
+    assert float(c.min()) > -1.1
+    scale = 2.0 ** (11 if kv == "e4m3" else 0)                                      # where the path places the largest
+    fewer = parts_left(e * scale, low, keeps - 1) / scale / e
+    best = None
+    for i in fewer.argsort()[:24].tolist():                                         # left over: negative, so too large
+        for j in fewer.argsort(descending=True)[:24].tolist():
+            gap = abs(float((e[i] - e[j]) / (e[i] + e[j])))
+            lost = float(fewer[j] - fewer[i]) / 2
+            if gap < (2.0 ** -8 if kv == "bf16" else 2.0 ** -5) and (best is None or lost > best[0]):
+                best = (lost, i, j)
+    lost, i, j = best
+    pool = pc.Pool(1, 9, 16, 1, hd, kv, seed=1)
+    pool.fill([T], seed=2)
+    if kv == "e4m3":
+        pool.ks[:] = 1.0
+        pool.vs[:] = 1.0
+    for t in range(T):
+        which = 0 if t == 0 else i if t % 2 else j
+        k, v = torch.zeros(hd), torch.zeros(hd)
+        if t > 0:
+            k[0], k[1] = float(a[which // 8]), float(b[which % 8])
+            v[:] = 1.0 if t % 2 else -1.0
+        put(pool, "k", t, k)
+        put(pool, "v", t, v)
+    q = torch.zeros(1, 1, 1, hd, dtype=torch.bfloat16, device="cuda")
+    q[..., :2] = 1.0
+    out, st = run(pool, q, [T - 1], scale=1.0)
+    assert st == mtp().MTP_OK
+    w = torch.exp(pool.rows("k", 0, list(range(T)))[0, :, :2].sum(-1))
+    v = pool.rows("v", 0, list(range(T)))[0]
+    ref, mass = (w @ v) / w.sum(), (w @ v.abs()) / w.sum()
+    z_err = 1.2 * ((2.0 ** -16 if kv == "bf16" else 2.0 ** -12) + 2 * (2 * hd + 80) * pc.U)
+    tol = ((2.0 ** -16 if kv == "bf16" else 2.0 ** -9 + 2.0 ** -11) + 2 * z_err + 2 * (2 * T + 200) * pc.U) * mass
+    assert lost * 128 / 129 > 1.5 * float((tol / mass).max()), "the case would not show a part fewer"
+    assert ((out[0, 0, 0].double() - ref).abs() <= tol + 2.0 ** -8 * (ref.abs() + tol)).all()
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite
+# ---------------------------------------------------------------------------
+
+def same_where_not_finite(out, ref):
+    out = out.double()
+    assert torch.equal(torch.isnan(out), torch.isnan(ref))
+    assert torch.equal(torch.isinf(out), torch.isinf(ref))
+    assert torch.equal(out[torch.isinf(out)], ref[torch.isinf(ref)])
+
+
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+@pytest.mark.parametrize("hd,G,M", [(128, 4, 6), (64, 8, 6), (256, 2, 6)])
+def test_nan_codes_of_an_8_bit_cache_stay_with_the_rows_that_attend_them(hd, G, M, qt):
+    lens, page = [123], 16
+    for window in (0, 50):
+        pool = pc.Pool(1, 10, page, 1, hd, "e4m3", seed=9)
+        pool.fill([129], seed=10)
+        codes = pool.v.view(torch.uint8)
+        for t, d in ((126, 3), (127, 40), (128, 5), (75, 9), (72, 10), (20, 11)):
+            codes[int(pool.table[0, t // page]), 0, t % page, d] = 0x7F
+        pool.k.view(torch.uint8)[int(pool.table[0, 8]), 0, 0, 0] = 0xFF        # position 128: only the last row attends it
+        q = queries(1, M, G, hd, torch.bfloat16 if qt == "bf16" else torch.float32, seed=11)
+        out, st = run(pool, q, lens, rope_theta=1e4, window=window)
+        assert st == mtp().MTP_OK
+        ref, mass, dots = pc.attention(pool, q, None, lens, [M], 1e4, window)
+        assert torch.isnan(out[0, 5]).all()
+        same_where_not_finite(out[0, :5], ref[0, :5])
+        tol = pc.attention_tol(ref, mass, dots, hd, 129, qt == "bf16")
+        fine = torch.isfinite(ref)
+        assert ((out.double() - ref).abs()[fine] <= tol[fine]).all()
+
+
+# ---------------------------------------------------------------------------
+# page scales
+# ---------------------------------------------------------------------------
+
+def test_the_borders_of_a_scale():
+    for s in (2.0 ** -40, 2.0 ** 40):
+        pool = pc.Pool(1, 3, 16, 1, 128, "e4m3", seed=17)
+        pool.fill([20], seed=18)
+        pool.vs[pool.table[0].long()] = s
+        pool.ks[pool.table[0].long()] = 2.0 ** -40
+        for dt in (torch.bfloat16, torch.float32):
+            q = queries(1, 1, 4, 128, dt, seed=19)
+            out, st = run(pool, q, [19], scale=2.0 ** 30)
+            assert st == mtp().MTP_OK
+            check(pool, out, q, None, [19], [1], 0.0, scale=2.0 ** 30)
