@@ -387,6 +387,10 @@ __device__ __forceinline__ void note_split(const PagedAttnArgs& a, const Segment
     else if (s.slot >= 0) mine = r;
 }
 
+// The running maximum of a row that has attended nothing: below every score of
+// an attended position, and finite, so that no difference from it is a NaN.
+constexpr float kNoScore = -3.402823466e38f;
+
 // floats of one partial slot
 __host__ __device__ constexpr long long part_floats(int RT, int hd) { return (long long)RT * (hd + 2); }
 

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
             for (int i = 0; i < 4; ++i) acc[r][i] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            m[i] = -1e30f;
+            m[i] = kNoScore;
             l[i] = 0.f;
         }
         const int p_last = s.len + (r0 + s.rows - 1) / a.G;   // position of the tile's last row
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     auto slot = [&](int c) { return a.part + (c == c0 ? 2 * c + 1 : 2 * c) * psz; };
     const int gt = hd >> 2, groups = (int)blockDim.x / gt;   // threads of a group, groups
     const int my = tid / gt, d = 4 * (tid - my * gt);
-    float M = -1e30f, l = 0.f;
+    float M = kNoScore, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int cb = c0 + my; cb <= c1; cb += kMergeBatch * groups) {
         float m[kMergeBatch], ls[kMergeBatch];
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 #pragma unroll
         for (int k = 0; k < kMergeBatch; ++k) {
             const int c = cb + k * groups;
-            m[k] = -1e30f;
+            m[k] = kNoScore;
             ls[k] = 0.f;
             o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (c > c1) continue;

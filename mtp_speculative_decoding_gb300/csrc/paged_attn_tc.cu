@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
                 l[r] = 0.f;
-                m[r] = -1e30f;
+                m[r] = kNoScore;
                 c[r] = E4M3 ? s_c[rw + r] : 1.f;
             }
 

@@ -1,5 +1,6 @@
 """mtp_paged_attention where single values decide: the bits that the
-tensor-core path keeps of a probability, NaN values and page scales."""
+tensor-core path keeps of a probability, NaN values, scores of any
+size, and page scales."""
 import pytest
 import torch
 
@@ -135,6 +136,43 @@ def test_nan_codes_of_an_8_bit_cache_stay_with_the_rows_that_attend_them(hd, G, 
         tol = pc.attention_tol(ref, mass, dots, hd, 129, qt == "bf16")
         fine = torch.isfinite(ref)
         assert ((out.double() - ref).abs()[fine] <= tol[fine]).all()
+
+
+# ---------------------------------------------------------------------------
+# scores of any size
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv,qt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("e4m3", "bf16"), ("e4m3", "f32")])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_scores_of_any_size(kv, qt, sign):
+    """Every score is the same number of 2^100's size, so the weights are equal
+    and the output is the mean of the values."""
+    hd, lens, M = 128, [400], 2
+    pool = pc.Pool(1, 27, 16, 1, hd, kv, seed=12)
+    pool.fill([402], seed=13)
+    pages = pool.table[0].long()
+    if kv == "e4m3":
+        pool.k.view(torch.uint8)[pages] = torch.tensor(sign).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+        pool.ks[pages] = 2.0 ** 38
+        pool.vs[pages] = 2.0 ** -6
+        q = torch.full((1, M, 4, hd), 2.0 ** 60, dtype=torch.bfloat16, device="cuda")
+    else:
+        pool.k[pages] = sign * 2.0 ** 49
+        q = torch.full((1, M, 4, hd), 2.0 ** 49, dtype=torch.bfloat16, device="cuda")
+    q = q if qt == "bf16" else q.float()
+    out, st = run(pool, q, lens, scale=1.0)
+    assert st == mtp().MTP_OK
+    for j in range(M):
+        v = pool.rows("v", 0, list(range(lens[0] + j + 1)))[0]
+        ref, mass = v.mean(0), v.abs().mean(0)
+        tol = (2 * 402 + 200) * pc.U * mass
+        if qt == "bf16":
+            tol = tol + 2.0 ** -8 * (ref.abs() + mass * 2.0 ** -9)
+            if kv == "e4m3":
+                tol = tol + 2.0 ** -9 * mass
+        else:
+            tol = tol + pc.U * ref.abs()
+        assert ((out[0, j].double() - ref).abs() <= tol).all(), j
 
 
 # ---------------------------------------------------------------------------
