@@ -211,7 +211,8 @@ typedef struct mtp_sample_params {
  *   kv_dtype   MTP_DTYPE_F32, MTP_DTYPE_BF16, or MTP_DTYPE_E4M3: 8-bit codes,
  *              the value is code * k_scale[page * n_kv_heads + g] (v_scale
  *              for v), fp32 [n_pages, n_kv_heads], powers of two within
- *              [2^-40, 2^40] (what mtp_kv_append writes)
+ *              [2^-40, 2^40] (what mtp_kv_append writes); an attended page
+ *              with any other scale counts as absent
  *   head_dim   32, 64, 128, 256 or 512 (strides: multiples of 16 bytes, k and
  *              v 16-byte aligned)
  *   page_size  16, 32, 64, 128 or 256

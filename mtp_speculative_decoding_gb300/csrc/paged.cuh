@@ -213,6 +213,14 @@ struct PagedAttnArgs {
     RopeTab rope;
 };
 
+// An e4m3 page's scale is one that the attention takes: a power of two within
+// [2^-40, 2^40].  The tensor cores fold the value scale's exponent into the
+// scores, so any other would be computed wrongly there.
+__device__ __forceinline__ bool scale_ok(float s) {
+    const uint32_t u = __float_as_uint(s);
+    return (u & 0x7FFFFFu) == 0u && u >= (127u - 40u) << 23 && u <= (127u + 40u) << 23;
+}
+
 // attended tiles of a sequence: tiles [0, st) (the sink) and [lt, et)
 struct TileMap { int st, lt, n; };
 __device__ __forceinline__ TileMap tile_map(const PagedAttnArgs& a, int len, int n) {

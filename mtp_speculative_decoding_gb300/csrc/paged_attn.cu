@@ -101,14 +101,16 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
                 float ks = 1.f, vs = 1.f;
                 if (s.rows > 0 && t <= p_last) {
                     const int pg = a.c.table[(long long)s.b * a.c.max_pages + (t >> a.c.ps_log2)];
-                    if ((unsigned)pg < (unsigned)a.c.n_pages) {
+                    bool there = (unsigned)pg < (unsigned)a.c.n_pages;
+                    if (there && a.c.ks) {
+                        ks = a.c.ks[(long long)pg * a.c.Hkv + s.g];
+                        vs = a.c.vs[(long long)pg * a.c.Hkv + s.g];
+                        there = scale_ok(ks) && scale_ok(vs);
+                    }
+                    if (there) {
                         const long long o = pg * a.c.sp + s.g * a.c.sh + (t & ((1 << a.c.ps_log2) - 1)) * a.c.st;
                         kp = reinterpret_cast<const KT*>(a.c.k) + o;
                         vp = reinterpret_cast<const KT*>(a.c.v) + o;
-                        if (a.c.ks) {
-                            ks = a.c.ks[(long long)pg * a.c.Hkv + s.g];
-                            vs = a.c.vs[(long long)pg * a.c.Hkv + s.g];
-                        }
                     } else {
                         // absent: an error only where a row attends it
                         for (int r = 0; r < s.rows; r += a.G) bad = bad || attends(a.c, t, s.len + (r0 + r) / a.G);

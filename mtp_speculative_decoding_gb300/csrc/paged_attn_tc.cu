@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     unsigned char* sP = sQ + S::QB;
     float* s_hi = reinterpret_cast<float*>(sP + S::PBUF * S::PB);   // [HD/2], [HD/2]: rotation table
     float* s_lo = s_hi + HD / 2;
-    float* m_ks = s_lo + HD / 2;                               // [kTcMeta][8] key scale (0: page not loaded)
+    float* m_ks = s_lo + HD / 2;                               // [kTcMeta][8] key scale (0: page not loaded or not used)
     float* m_vs = m_ks + kTcMeta * 8;                          // [kTcMeta][8] exponent of the value scale
     float* s_inv = m_vs + kTcMeta * 8;                         // [RT] one over the row's sum
     float* s_f = s_inv + RT;                                   // [RT] rescale factor
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
     int* s_pos2 = reinterpret_cast<int*>(s_red + 4 * RT);      // [2][RT] position of the row
     int* s_row2 = s_pos2 + 2 * RT;                             // [2][RT] output row
     int* s_fix2 = s_row2 + 2 * RT;                             // [2][kTcFix]
-    int* m_all = s_fix2 + 2 * kTcFix;                          // [kTcMeta] every page of the tile is loaded
+    int* m_all = s_fix2 + 2 * kTcFix;                          // [kTcMeta] every page of the tile is used
     unsigned long long* bars = reinterpret_cast<unsigned long long*>(m_all + kTcMeta);
     unsigned long long *full = bars, *empty = full + kTcSlotsMax, *meta_full = empty + kTcSlotsMax, *s_full = meta_full + kTcMeta,
                        *s_free = s_full + 2, *p_full = s_free + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *end_bar = q_full + 1;
@@ -346,17 +346,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                         }
                     }
                     if (key) {   // the tile's scales, while its keys are on their way
+                        float ks = kp >= 0 ? 1.f : 0.f;   // 0: masked
                         if (lane < np) {
-                            float ks = kp >= 0 ? 1.f : 0.f, vs = 0.f;
+                            float vs = 0.f;
                             if (E4M3 && kp >= 0) {
                                 const long long o = (long long)kp * a.c.Hkv + s.g;
-                                ks = a.c.ks[o];
-                                vs = (float)((int)((__float_as_uint(a.c.vs[o]) >> 23) & 0xFF) - 127);
+                                const float kss = a.c.ks[o], vss = a.c.vs[o];
+                                const bool fits = scale_ok(kss) && scale_ok(vss);   // else the page counts as absent
+                                bad = bad || !fits;
+                                ks = fits ? kss : 0.f;
+                                vs = (float)((int)(__float_as_uint(fits ? vss : 1.f) >> 23) - 127);
                             }
                             m_ks[(ti % kTcMeta) * 8 + lane] = ks;
                             m_vs[(ti % kTcMeta) * 8 + lane] = vs;
                         }
-                        const bool all = __all_sync(0xffffffffu, lane >= np || kp >= 0);
+                        const bool all = __all_sync(0xffffffffu, lane >= np || ks != 0.f);
                         if (lane == 0) m_all[ti % kTcMeta] = all;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(meta_full + ti % kTcMeta);

@@ -1,6 +1,6 @@
 """mtp_paged_attention where single values decide: the bits that the
 tensor-core path keeps of a probability, NaN values, scores of any
-size, and page scales."""
+size, and page scales that are none."""
 import pytest
 import torch
 
@@ -116,6 +116,8 @@ def same_where_not_finite(out, ref):
     assert torch.equal(out[torch.isinf(out)], ref[torch.isinf(ref)])
 
 
+INF = float("inf")
+NAN = float("nan")
 @pytest.mark.parametrize("qt", ["bf16", "f32"])
 @pytest.mark.parametrize("hd,G,M", [(128, 4, 6), (64, 8, 6), (256, 2, 6)])
 def test_nan_codes_of_an_8_bit_cache_stay_with_the_rows_that_attend_them(hd, G, M, qt):
@@ -178,6 +180,29 @@ def test_scores_of_any_size(kv, qt, sign):
 # ---------------------------------------------------------------------------
 # page scales
 # ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("bad", [0.0, -0.25, 0.3, 2.0 ** -41, 2.0 ** 41, INF, NAN])
+def test_a_scale_that_is_no_power_of_two_is_reported(bad, which, qt):
+    """Such a page counts as absent: its positions are masked, and the status
+    says so; the other pages' are not touched.  Where no row attends the page
+    its scales are not looked at."""
+    m = mtp()
+    lens, M, page, hd = [200], 2, 16, 128
+    pool = pc.Pool(1, 14, page, 2, hd, "e4m3", seed=14)
+    pool.fill([202], seed=15)
+    q = queries(1, M, 8, hd, torch.bfloat16 if qt == "bf16" else torch.float32, seed=16)
+    good = getattr(pool, which).clone()
+    getattr(pool, which)[int(pool.table[0, 3])] = bad
+    out, st = run(pool, q, lens, rope_theta=1e4)
+    assert st == m.MTP_ERR_ARG
+    out2, st2 = run(pool, q, lens, rope_theta=1e4, window=32)
+    assert st2 == m.MTP_OK
+    getattr(pool, which).copy_(good)
+    check(pool, out, q, None, lens, [M], 1e4, absent={(0, t) for t in range(48, 64)})
+    check(pool, out2, q, None, lens, [M], 1e4, window=32)
+
 
 def test_the_borders_of_a_scale():
     for s in (2.0 ** -40, 2.0 ** 40):
