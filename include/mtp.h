@@ -479,6 +479,10 @@ int mtp_kv_append(const mtp_kv_cache *c, int B, int M, const int32_t *kv_len, co
  * probabilities then keep 16 bits (bf16 cache) or 9 (e4m3 cache), sums and
  * maxima 32.
  * Slots that hold no attended position are never used, whatever they contain.
+ * An attended value that is infinite gives that infinity in its dimension, NaN
+ * or infinities of both signs give NaN; other dimensions and rows that do not
+ * attend it are not touched.  An attended key that is not finite may make the
+ * row's outputs NaN.
  * A row that attends nothing (all its pages absent) gives zeros.  A sequence
  * whose kv_len or n_new is out of range is left out, positions on absent pages
  * are masked, and both set the status word to MTP_ERR_ARG.

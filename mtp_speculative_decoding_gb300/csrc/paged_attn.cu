@@ -24,6 +24,13 @@ __device__ __forceinline__ void kv8(const uint8_t* p, float s, float (&x)[8]) {
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(uint16_t* p, float x) { *p = (uint16_t)pack_bf16(x, 0.f); }
 
+// 2^x, never 0: an infinite value keeps its sign whatever its weight (0 times it
+// would be a NaN); a finite one's share is at most 2^-149 of it too much
+__device__ __forceinline__ float weight(float x) {
+    const float w = exp2f(x);
+    return w == 0.f ? __uint_as_float(1u) : w;
+}
+
 constexpr int kCcThreads = 128;
 
 // One CTA: 16 rows x 32 positions a tile, K and then V staged as fp32 in
@@ -152,8 +159,8 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
                 const bool see = r < s.rows && skp[lane] && attends(a.c, t0 + lane, s.len + (r0 + r) / a.G);
                 const float v = see ? z[i] : -__int_as_float(0x7F800000);
                 const float mn = fmaxf(m[i], warp_max(v));
-                const float p = exp2f(v - mn);
-                const float f = exp2f(m[i] - mn);
+                const float p = weight(v - mn);
+                const float f = weight(m[i] - mn);
                 l[i] = l[i] * f + warp_sum(see ? p : 0.f);
                 m[i] = mn;
                 sp[r * kCcTile + lane] = see ? p : -1.f;   // -1: masked, whatever the value row holds
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         float nm = M;
 #pragma unroll
         for (int k = 0; k < kMergeBatch; ++k) nm = fmaxf(nm, m[k]);
-        const float f = exp2f(M - nm);
+        const float f = weight(M - nm);
         acc.x *= f;
         acc.y *= f;
         acc.z *= f;
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         M = nm;
 #pragma unroll
         for (int k = 0; k < kMergeBatch; ++k) {
-            const float w = exp2f(m[k] - nm);
+            const float w = weight(m[k] - nm);
             acc.x = fmaf(w, o[k].x, acc.x);
             acc.y = fmaf(w, o[k].y, acc.y);
             acc.z = fmaf(w, o[k].z, acc.z);
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     for (int k = 0; k < groups; ++k) {
         const float2 ml = s_ml[tid + k * gt];
         const float4 o = s_o[tid + k * gt];
-        const float w = exp2f(ml.x - M);
+        const float w = weight(ml.x - M);
         acc.x = fmaf(w, o.x, acc.x);
         acc.y = fmaf(w, o.y, acc.y);
         acc.z = fmaf(w, o.z, acc.z);

@@ -193,6 +193,65 @@ struct Shape {
     static constexpr float kSlack = E4M3 ? 4.f : 8.f, kBias = E4M3 ? 11.f : 0.f;
 };
 
+// A segment's dimensions tok, tok + 128, .. where the product left a result that
+// is not finite.  An attended infinity is a NaN there (the second part of its weight is
+// often 0, or negative), so such a row takes its answer from the attended values
+// that are not finite: one pass over the segment's values, by the thread that
+// wrote the result.  Rows whose sum is a NaN stay as they are, and so does what
+// overflowed without such a value.
+template <int RW>
+__device__ __noinline__ void infinite_values(const PagedAttnArgs* pa, Plan plan, long long x, int tok, const int* pos,
+                                             const int* row, const float* inv, float* part, int rows) {
+    const PagedAttnArgs& a = *pa;
+    const int hd = a.hd;
+    const Segment s = segment_at(a, plan, x, share_lo(plan.pre[a.B], blockIdx.x + 1, a.grid), blockIdx.x);
+    constexpr int LK = 8, PER = kTcTile / LK;   // values in flight: slots of one page
+#pragma unroll 1
+    for (int d = tok; d < hd; d += 128) {
+        float acc[RW];
+        uint32_t odd = 0u, found = 0u;
+#pragma unroll 1
+        for (int r = 0; r < RW && r < rows; ++r) {
+            const float o = part ? part[r * hd + d] : bf16_to_f32(reinterpret_cast<const uint16_t*>(a.out)[(long long)row[r] * hd + d]);
+            if (o - o != 0.f && inv[r] == inv[r]) odd |= 1u << r;
+        }
+        if (odd == 0u) continue;
+#pragma unroll 1
+        for (int i = 0; i < s.n * PER; ++i) {
+            const int t = tile_at(s.map, s.t0 + i / PER) * kTcTile + i % PER * LK;
+            if (t >= s.len + s.n_new) continue;
+            const int pg = a.c.table[(long long)s.b * a.c.max_pages + (t >> a.c.ps_log2)];
+            if ((unsigned)pg >= (unsigned)a.c.n_pages) continue;
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v) + pg * a.c.sp + s.g * a.c.sh +
+                                (t & ((1 << a.c.ps_log2) - 1)) * a.c.st + d;
+            uint16_t x[LK];
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < LK; ++e) x[e] = v[e * a.c.st];
+#pragma unroll
+            for (int e = 0; e < LK; ++e) any = any || (x[e] & 0x7F80u) == 0x7F80u;
+            if (!any) continue;
+#pragma unroll 1
+            for (int e = 0; e < LK; ++e) {
+                const float val = bf16_to_f32(v[e * a.c.st]);
+                if (val - val == 0.f) continue;
+#pragma unroll 1
+                for (int r = 0; r < RW; ++r)
+                    if (odd >> r & 1u && attends(a.c, t + e, pos[r])) {
+                        acc[r] = found >> r & 1u ? acc[r] + val : val;
+                        found |= 1u << r;
+                    }
+            }
+        }
+#pragma unroll 1
+        for (int r = 0; r < RW; ++r) {
+            if (!(found >> r & 1u)) continue;
+            if (part) part[r * hd + d] = acc[r];
+            else reinterpret_cast<uint16_t*>(a.out)[(long long)row[r] * hd + d] = (uint16_t)pack_bf16(acc[r], 0.f);
+        }
+    }
+}
+
 constexpr int kTcThreads = 320;
 
 template <bool E4M3, int HD, int RT>
@@ -639,6 +698,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                 const int nfix = s_nfix[pe] < kTcFix ? s_nfix[pe] : kTcFix;
                 wait(pv_done + (last & 1), (last >> 1) & 1);
                 tc_fence_after();
+                float odd = 0.f;   // NaN: the product left something that is not finite
 #pragma unroll 1
                 for (int d0 = 0; d0 < S::D; ++d0) {
                     uint32_t v[S::NO][RW];
@@ -656,6 +716,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
 #pragma unroll
                         for (int part = 1; part < S::NO; ++part) o[r] += __uint_as_float(v[part][r]);
                     }
+                    if (!E4M3)
+#pragma unroll
+                        for (int r = 0; r < RW; ++r) odd = fmaf(o[r], 0.f, odd);
                     for (int f = 0; f < nfix; ++f) {   // values that are not finite, to the rows that attend them
                         const int t = s_fix2[pe * kTcFix + f];
                         const int pg = a.c.table[(long long)s.b * a.c.max_pages + (t >> a.c.ps_log2)];
@@ -675,6 +738,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attn_tc_kernel(const __gr
                         else reinterpret_cast<uint16_t*>(a.out)[(long long)s_row2[pe * RT + rw + r] * HD + d] = (uint16_t)pack_bf16(o[r] * s_inv[rw + r], 0.f);
                     }
                 }
+                if (!E4M3 && __builtin_expect(!(odd == 0.f), 0))
+                    infinite_values<RW>(&a, plan, s.x, tok, s_pos2 + pe * RT + rw, s_row2 + pe * RT + rw, s_inv + rw,
+                                        part ? part + rw * HD : nullptr, s.rows - rw);
                 tc_fence_before();
             }
             both_sync();   // the next segment's row tables stand; this one's are read

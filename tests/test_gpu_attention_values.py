@@ -1,6 +1,8 @@
 """mtp_paged_attention where single values decide: the bits that the
-tensor-core path keeps of a probability, NaN values, scores of any
+tensor-core path keeps of a probability, infinite and NaN values, scores of any
 size, and page scales that are none."""
+import math
+
 import pytest
 import torch
 
@@ -118,6 +120,62 @@ def same_where_not_finite(out, ref):
 
 INF = float("inf")
 NAN = float("nan")
+PLANTED = [  # position, dimension, value: far back, in the middle of a tile, in the last one, pairs that cancel, NaN
+    (5, 3, INF), (300, 4, -INF), (130, 7, INF), (520, 7, INF), (131, 9, INF), (640, 9, -INF), (200, 11, NAN), (690, 12, -INF),
+    (700, 14, INF), (701, 15, INF), (702, 15, -INF), (703, 16, NAN), (0, 40, -INF)]
+
+
+@pytest.mark.parametrize("spread", [1.0, 8.0])
+@pytest.mark.parametrize("kv,qt,hd,G,M,window", [
+    ("bf16", "bf16", 64, 2, 4, 0), ("bf16", "bf16", 128, 4, 4, 0), ("bf16", "bf16", 256, 4, 4, 0), ("bf16", "bf16", 512, 4, 4, 0),
+    ("bf16", "bf16", 128, 8, 4, 0), ("bf16", "bf16", 256, 16, 4, 0), ("bf16", "bf16", 64, 16, 4, 0), ("bf16", "bf16", 512, 8, 4, 0),
+    ("bf16", "bf16", 128, 4, 4, 190), ("bf16", "f32", 128, 2, 4, 0), ("f32", "f32", 64, 2, 4, 190), ("bf16", "bf16", 32, 2, 4, 0)])
+def test_infinite_values_that_rows_attend(kv, qt, hd, G, M, window, spread):
+    """An infinity among the attended values gives that infinity in its
+    dimension, whatever its weight is, two of them of different signs or a NaN
+    give NaN, and every other output stays what it is.  spread 8: the scores
+    lie hundreds apart, so most weights are below what fp32 holds."""
+    lens = [700]
+    pool = pc.Pool(1, 45, 16, 1, hd, kv, seed=3)
+    pool.fill([704], seed=4)
+    for t, d, x in PLANTED:
+        pool.v[int(pool.table[0, t // 16]), 0, t % 16, d % hd] = x
+    q = queries(1, M, G, hd, torch.bfloat16 if qt == "bf16" else torch.float32, seed=5) * spread
+    scale = None if spread == 1.0 else 4.0 / math.sqrt(hd)
+    out, st = run(pool, q, lens, rope_theta=1e4, window=window, scale=scale)
+    assert st == mtp().MTP_OK
+    # weights of 64 bits: none is 0
+    ref, mass, dots = pc.attention(pool, q, None, lens, [M], 1e4, window, 0, scale)
+    same_where_not_finite(out, ref)
+    tol = pc.attention_tol(ref, mass, dots, hd, 704, qt == "bf16")
+    fine = torch.isfinite(ref)
+    assert ((out.double() - ref).abs()[fine] <= tol[fine]).all()
+
+
+@pytest.mark.parametrize("hd,G,M", [(128, 4, 3), (256, 8, 4), (64, 16, 4)])
+def test_infinite_values_of_whole_items(hd, G, M):
+    """Many sequences, so that most are not cut into parts."""
+    B, page = 200, 16
+    lens = [(37 * b) % 300 for b in range(B)]
+    pool = pc.Pool(B, (max(lens) + M) // page + 1, page, 1, hd, "bf16", seed=6)
+    pool.fill([n + M for n in lens], seed=7)
+    for b in range(0, B, 3):
+        t = (11 * b) % (lens[b] + 1)
+        pool.v[int(pool.table[b, t // page]), 0, t % page, b % hd] = INF if b % 2 else -INF
+    q = queries(B, M, G, hd, torch.bfloat16, seed=8)
+    out, st = run(pool, q, lens, rope_theta=1e4)
+    assert st == mtp().MTP_OK
+    pick = list(range(0, B, 7))
+    sub = pc.Pool.__new__(pc.Pool)
+    sub.__dict__.update(pool.__dict__)
+    sub.table = pool.table[pick]
+    ref, mass, dots = pc.attention(sub, q[pick], None, [lens[b] for b in pick], [M] * len(pick), 1e4)
+    same_where_not_finite(out[pick], ref)
+    tol = pc.attention_tol(ref, mass, dots, hd, 310, True)
+    fine = torch.isfinite(ref)
+    assert ((out[pick].double() - ref).abs()[fine] <= tol[fine]).all()
+
+
 @pytest.mark.parametrize("qt", ["bf16", "f32"])
 @pytest.mark.parametrize("hd,G,M", [(128, 4, 6), (64, 8, 6), (256, 2, 6)])
 def test_nan_codes_of_an_8_bit_cache_stay_with_the_rows_that_attend_them(hd, G, M, qt):
