@@ -486,9 +486,10 @@ static cudaError_t launch_e4m3(AppendArgs a, int sms, cudaStream_t s) {
     const size_t smem = a.rope.on ? (size_t)((ps >> 4) + 16) * (a.hd >> 1) * sizeof(float2) : 0;
     const bool one = units <= 1024;
     const int T = one ? ((units + 1) / 2 + 31) & ~31 : kPageThreads;
-    if (smem > 40 * 1024) {
-        const cudaError_t e = one ? cudaFuncSetAttribute(append_e4m3_pages_kernel<IT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-                                  : cudaFuncSetAttribute(append_e4m3_pages_kernel<IT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 40 * 1024) {   // the most (head_dim 512, pages of 256), so that two host threads' calls do not disturb each other
+        constexpr int most = ((MTP_MAX_PAGE_SIZE >> 4) + 16) * 256 * (int)sizeof(float2);
+        const cudaError_t e = one ? cudaFuncSetAttribute(append_e4m3_pages_kernel<IT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)
+                                  : cudaFuncSetAttribute(append_e4m3_pages_kernel<IT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
     if (one) append_e4m3_pages_kernel<IT, true><<<grid, T, smem, s>>>(a);

@@ -345,14 +345,14 @@ size_t cc_smem(const PagedAttnArgs& a) {
     return ((size_t)kCcRows * a.hd + (size_t)kCcTile * (a.hd + 4) + kCcRows * kCcTile + kCcRows) * sizeof(float) +
            (size_t)plan_bytes(a.B);
 }
+// most that any call asks for
+constexpr int kCcSmemMax = (kCcRows * 512 + kCcTile * (512 + 4) + kCcRows * kCcTile + kCcRows) * (int)sizeof(float) + plan_bytes(MTP_MAX_PAGED_BATCH);
 template <typename QT, typename KT>
 cudaError_t cc(const PagedAttnArgs& a, cudaStream_t s) {
-    const size_t smem = cc_smem(a);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_attn_cc_kernel<QT, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    paged_attn_cc_kernel<QT, KT><<<a.grid, kCcThreads, smem, s>>>(a);
+    // the most, so that calls of two sizes from two host threads do not disturb each other
+    const cudaError_t e = cudaFuncSetAttribute(paged_attn_cc_kernel<QT, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCcSmemMax);
+    if (e != cudaSuccess) return e;
+    paged_attn_cc_kernel<QT, KT><<<a.grid, kCcThreads, cc_smem(a), s>>>(a);
     return cudaGetLastError();
 }
 template <typename QT>
