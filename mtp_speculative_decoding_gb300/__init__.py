@@ -437,12 +437,15 @@ def make_kv_cache(k, v, page_table, k_scale=None, v_scale=None, window: int = 0,
             raise ValueError("scales are for an e4m3 cache only")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
         raise ValueError("page_table: contiguous int32 [B, max_pages]")
+    if any(t is not None and t.get_device() != k.get_device() for t in (v, page_table, k_scale, v_scale)):
+        raise ValueError("the cache's tensors must live on one device")
     sp, sh, st, _ = k.stride()
     n, hkv, ps, hd = k.shape
     cache = KVCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
                     v_scale.data_ptr() if v_scale is not None else None, page_table.data_ptr(), sp, sh, st, n, ps,
                     page_table.shape[1], hkv, hd, dt, window, sink, rope_theta, 0)
-    cache.table_rows = page_table.shape[0]   # for the calls' check of their batch
+    # for the calls' checks of their batch and of the current device
+    cache.table_rows, cache.device = page_table.shape[0], k.get_device()
     return cache
 
 
@@ -495,6 +498,14 @@ def _plain(dev: int, t, dtype, shape, what: str):
     return _on(dev, t, what)
 
 
+def _cache_fits(cache: KVCache, B: int, dev: int) -> None:
+    """make_kv_cache's handles: the batch is in the table, the cache on the current device."""
+    if B > getattr(cache, "table_rows", B):
+        raise ValueError("more sequences than page_table has rows")
+    if getattr(cache, "device", dev) != dev:
+        raise ValueError(f"the cache lives on cuda:{cache.device}, the current device is cuda:{dev}")
+
+
 def _code(rt: _Runtime, t, what: str) -> int:
     c = rt.code.get(t.dtype)
     if c is None:
@@ -515,8 +526,7 @@ def kv_append(cache: KVCache, k_new, v_new, kv_len, ws, n_new=None, k_norm=None,
     B, M, hkv, hd = shape
     if hkv != cache.n_kv_heads or hd != cache.head_dim:
         raise ValueError("the rows' heads are not the cache's")
-    if B > getattr(cache, "table_rows", B):
-        raise ValueError("more sequences than page_table has rows")
+    _cache_fits(cache, B, dev)
     rc = rt.lib.mtp_kv_append(C.byref(cache), B, M, _plain(dev, kv_len, rt.i32, (B,), "kv_len"),
                               _plain(dev, n_new, rt.i32, (B,), "n_new"), _on(dev, k_new, "k_new"), _on(dev, v_new, "v_new"),
                               _code(rt, k_new, "k_new"), strides[0], strides[1], strides[2],
@@ -538,8 +548,7 @@ def paged_attention(cache: KVCache, q, kv_len, out, ws, n_new=None, q_norm=None,
     if len(shape) != 4 or shape[3] != cache.head_dim or strides[3] != 1:
         raise ValueError("q: [B, M, n_q_heads, head_dim] with the cache's head_dim, contiguous")
     B, M, hq, hd = shape
-    if B > getattr(cache, "table_rows", B):
-        raise ValueError("more sequences than page_table has rows")
+    _cache_fits(cache, B, dev)
     rc = rt.lib.mtp_paged_attention(C.byref(cache), B, M, hq, _plain(dev, kv_len, rt.i32, (B,), "kv_len"),
                                     _plain(dev, n_new, rt.i32, (B,), "n_new"), _on(dev, q, "q"), _code(rt, q, "q"),
                                     strides[0], strides[1], strides[2], _plain(dev, q_norm, rt.f32, (hd,), "q_norm"), rms_eps,
