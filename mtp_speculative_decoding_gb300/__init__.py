@@ -421,7 +421,7 @@ def make_kv_cache(k, v, page_table, k_scale=None, v_scale=None, window: int = 0,
     page_size, n_kv_heads, head_dim] is passed as its permuted view) in fp32,
     bf16 or float8_e4m3fn; page_table [B, max_pages] int32; k_scale, v_scale
     [n_pages, n_kv_heads] fp32 for an e4m3 cache.  rope_theta 0: keys and
-    queries are not rotated (see mtp_kv_cache)."""
+    queries are not rotated (see mtp_kv_cache).  The handle keeps the tensors."""
     import torch
     _require_cuda(k, v, page_table, k_scale, v_scale)
     if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(-1) != 1:
@@ -446,6 +446,7 @@ def make_kv_cache(k, v, page_table, k_scale=None, v_scale=None, window: int = 0,
                     page_table.shape[1], hkv, hd, dt, window, sink, rope_theta, 0)
     # for the calls' checks of their batch and of the current device
     cache.table_rows, cache.device = page_table.shape[0], k.get_device()
+    cache.tensors = (k, v, page_table, k_scale, v_scale)   # the handle holds their addresses
     return cache
 
 

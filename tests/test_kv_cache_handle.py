@@ -1,5 +1,8 @@
 """The paged cache's handle in the binding: which device its tensors live on.
 Stand-ins for CUDA tensors, so no GPU is needed; no call reaches the library."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -106,3 +109,17 @@ def test_a_handle_filled_by_hand_is_taken(monkeypatch):
     for call in both(by_hand, 0):
         call()
     assert rt.calls == ["append", "attention"]
+
+
+def test_the_handle_keeps_its_tensors():
+    """It holds their addresses: a table made in the call's argument list must
+    not be freed under it."""
+    d = parts(0, torch.float8_e4m3fn)
+    refs = [weakref.ref(t) for t in d.values()]
+    cache = mtp.make_kv_cache(**d)
+    del d
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del cache
+    gc.collect()
+    assert all(r() is None for r in refs)
