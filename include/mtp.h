@@ -503,7 +503,8 @@ int mtp_paged_attention(const mtp_kv_cache *c, int B, int M, int n_q_heads, cons
  *                     on ties; -1 and -inf behind the last one
  * NaN logits are left out as if they were -inf; -inf is never an alternative.
  * A row with a +inf logit, or with nothing above -inf, gives NaN log
- * probabilities and entropy.  A row whose token is outside
+ * probabilities and entropy.  A row whose logits do not reach the kernel within
+ * a second gives NaN, and -1 for every alternative.  A row whose token is outside
  * [0, V) (the -1 padding of a verify's out_tokens) is not read and its
  * outputs keep their values; tokens NULL: every row, out_logprob not written.
  * Each output may be NULL (top_k 0: both alternatives' arrays unused).

@@ -49,12 +49,18 @@ __device__ __forceinline__ unsigned long long warp_max_u32x2(unsigned long long 
     const unsigned lo = __reduce_max_sync(0xffffffffu, (unsigned)(v >> 32) == hi ? (unsigned)v : 0u);
     return (unsigned long long)hi << 32 | lo;
 }
-// wait of at most a second (a copy takes a few microseconds)
-__device__ __forceinline__ bool mbar_wait_bounded(unsigned long long* bar, unsigned parity) {
+// wait of at most ns (a copy takes a few microseconds); after one of the CTA gave
+// up every other does too
+__device__ __forceinline__ bool mbar_wait_bounded(unsigned long long* bar, unsigned parity, volatile int* lost, unsigned long long ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (global_ns() - t0 > 1000000000ull) return false;
+    while (!mbar_try_wait(bar, parity)) {
+        if (*lost) return false;
+        if (global_ns() - t0 > ns) {
+            *lost = 1;
+            return false;
+        }
+    }
     return true;
 }
 // the cluster's barrier (whole warps; orders shared memory of all its CTAs)
@@ -170,9 +176,11 @@ struct LpShared {
     unsigned long long bound;
     Sums wsum[kLpWarps];
     int count, nsel;                          // candidates; entries of sel
+    volatile int lost;                        // a wait gave up
     // the leader's: what the pieces' CTAs leave here
     unsigned long long tops[kLpMaxC * MTP_MAX_TOP];   // [C][K], descending
     Sums pieces[kLpMaxC];
+    int piece_lost[kLpMaxC];
     float m, ls;                              // the row's reference, and ln of its sum
     int nmerge;                               // entries of buf that the leader ranks
 };
@@ -345,6 +353,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
         sh.count = 0;
         sh.nsel = 0;
         sh.nmerge = 0;
+        sh.lost = 0;
     }
     if (C > 1) cluster_arrive_relaxed();   // waited for before the leader's memory is written: it has started by then
     float zt = neg_inf();
@@ -377,16 +386,20 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     uint32_t run_at = 0u;                     // and the last index that it can have (not above its own key)
     int check = 0;                            // the block at which the bound is next taken
     const int warps = nvec < kLpThreads ? (nvec + 31) / 32 : kLpWarps;   // that hold elements
-    bool lost = false;                        // a wait gave up
+    bool lost = false;                        // a wait of this thread gave up
+    int fetched = blocks < kLpStages ? blocks : kLpStages;   // (thread 0)
     for (int it = 0; it < blocks; ++it) {
         const int stage = it % kLpStages;
-        lost = !mbar_wait_bounded(&sh.full[stage], (unsigned)(it / kLpStages) & 1u) || lost;
-        if (tid == 0 && it > 0 && it - 1 + kLpStages < blocks) {
+        lost = !mbar_wait_bounded(&sh.full[stage], (unsigned)(it / kLpStages) & 1u, &sh.lost, a.timeout_ns) || lost;
+        if (tid == 0 && !lost && it > 0 && it - 1 + kLpStages < blocks) {
             // refill the stage before this one, which the other warps leave about now
             const int prev = (it - 1) % kLpStages;
-            lost = !mbar_wait_bounded(&sh.empty[prev], (unsigned)((it - 1) / kLpStages) & 1u) || lost;
-            fence_proxy_async_smem();
-            fetch(it - 1 + kLpStages);
+            lost = !mbar_wait_bounded(&sh.empty[prev], (unsigned)((it - 1) / kLpStages) & 1u, &sh.lost, a.timeout_ns);
+            if (!lost) {
+                fence_proxy_async_smem();
+                fetch(it - 1 + kLpStages);
+                ++fetched;
+            }
         }
         const int n = nvec - it * kLpBlock;
         uint4 cur[kLpVec];
@@ -473,7 +486,11 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
             if (pos < kLpCap) sh.buf[pos] = key;
         }
     }
-    if (lost) s.S = __uint_as_float(0x7FC00000u);   // (a copy that never came: no answer rather than a wrong one)
+    if (tid == 0 && lost) {   // gave up: the copies in flight end before the CTA does
+        const unsigned long long t0 = global_ns();
+        for (int i = fetched > kLpStages ? fetched - kLpStages : 0; i < fetched; ++i)
+            while (!mbar_try_wait(&sh.full[i % kLpStages], (unsigned)(i / kLpStages) & 1u) && global_ns() - t0 < a.timeout_ns) {}
+    }
     // the piece's sums
     s = join_warp(s);
     if (lane == 0) sh.wsum[warp] = s;
@@ -481,7 +498,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     if (warp == 0) {
         s = join_warp(lane < kLpWarps ? sh.wsum[lane] : Sums{neg_inf(), 0.f, 0.f});
         if (C > 1) cluster_wait();
-        if (lane == 0) *cluster.map_shared_rank(&sh.pieces[rank], 0) = s;
+        if (lane == 0) {
+            *cluster.map_shared_rank(&sh.pieces[rank], 0) = s;
+            *cluster.map_shared_rank(&sh.piece_lost[rank], 0) = sh.lost;
+        }
     } else if (C > 1) {
         cluster_wait();
     }
@@ -527,8 +547,11 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
     if (rank != 0) return;
     if (warp == 0) {
         const Sums w = join_warp(lane < C ? sh.pieces[lane] : Sums{neg_inf(), 0.f, 0.f});
+        // a piece whose copies never came: no answer rather than a wrong one
+        const bool none = __any_sync(0xffffffffu, lane < C && sh.piece_lost[lane] != 0);
         if (lane == 0) {
-            const float ls = logf(w.S);
+            const float ls = none ? __uint_as_float(0x7FC00000u) : logf(w.S);
+            sh.lost = none;
             sh.m = w.m;
             sh.ls = ls;
             if (a.logprob) a.logprob[row] = ((zt == zt ? zt : neg_inf()) - w.m) - ls;
@@ -559,9 +582,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const __grid_con
         }
         __syncthreads();
         if (tid < a.K) {
-            const unsigned long long key = tid < real ? best[tid] : 0ull;   // 0: fewer logits above -inf than K
+            const unsigned long long key = tid < real && !sh.lost ? best[tid] : 0ull;   // 0: fewer logits above -inf than K
             if (a.top_ids) a.top_ids[row * a.K + tid] = key ? (int32_t)unpack_index(key) : -1;
-            if (a.top_logprobs) a.top_logprobs[row * a.K + tid] = key ? (key_value(key) - sh.m) - sh.ls : neg_inf();
+            if (a.top_logprobs) a.top_logprobs[row * a.K + tid] = key ? (key_value(key) - sh.m) - sh.ls : sh.lost ? sh.ls : neg_inf();
         }
     }
 }

@@ -15,6 +15,7 @@ struct LogprobArgs {
     float *logprob, *entropy;
     int32_t* top_ids;
     float* top_logprobs;
+    unsigned long long timeout_ns;   // of a wait inside the kernel
 };
 cudaError_t launch_logprobs(const LogprobArgs& a, int ldtype, int sms, cudaStream_t s);
 

@@ -249,6 +249,7 @@ int mtp_token_logprobs(const void* logits, int ldtype, int64_t rows, int V, int6
     a.tokens = tokens; a.K = out_top_ids || out_top_logprobs ? top_k : 0;
     a.logprob = tokens ? out_logprob : nullptr; a.entropy = out_entropy;
     a.top_ids = out_top_ids; a.top_logprobs = out_top_logprobs;
+    a.timeout_ns = kWaitLimitNs;
     return launch_logprobs(a, ldtype, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
 
