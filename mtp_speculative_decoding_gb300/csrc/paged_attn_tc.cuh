@@ -38,9 +38,7 @@ __host__ __device__ constexpr int tc_other(bool e4m3, int hd, int RT, int B) {
 __host__ __device__ constexpr int tc_slot_bytes(bool e4m3, int hd) { return kTcTile * (hd < 128 ? hd : 128) * (e4m3 ? 1 : 2); }
 __host__ __device__ constexpr int tc_slots(bool e4m3, int hd, int RT, int B) {
     int n = (kTcSmemLimit - tc_other(e4m3, hd, RT, B)) / tc_slot_bytes(e4m3, hd);
-    const int d = hd < 128 ? 1 : hd / 128;
     if (n > kTcSlotsMax) n = kTcSlotsMax;
-    if (n > 24 * d) n = 24 * d;
     return n;
 }
 
