@@ -476,8 +476,10 @@ int mtp_kv_append(const mtp_kv_cache *c, int B, int M, const int32_t *kv_len, co
  *              bytes
  * fp32 queries are computed in fp32 throughout.  bf16 queries against a bf16
  * or e4m3 cache with head_dim 64, 128, 256 or 512 run on the tensor cores: the
- * probabilities then keep 16 bits (bf16 cache) or 9 (e4m3 cache), sums and
- * maxima 32.
+ * rotated queries then keep 16 bits (bf16 cache) or 12 (e4m3 cache), the
+ * probabilities 16 or 9, sums and maxima 32.  Against e4m3 what keeps 9 bits is
+ * a probability times its page's value scale, down to 2^-19 of the row's
+ * largest; below it keeps fewer, and none under 2^-28.
  * Slots that hold no attended position are never used, whatever they contain.
  * An attended value that is infinite gives that infinity in its dimension, NaN
  * or infinities of both signs give NaN; other dimensions and rows that do not
