@@ -278,16 +278,21 @@ class ClockSampler:
                 "reasons": sorted(reasons), "samples": len(sm)}
 
 
+TARGET_STEP_SOURCES = ("kv_append", "logprobs", "paged")   # operators that no workload launches
+
+
 def kernel_source_hash() -> str:
-    """sha256 prefix over the sources of the kernels that the workloads launch:
-    ties a recorded ncu traffic figure to the kernel it was taken on."""
+    """sha256 prefix over the library's CUDA sources, kernels and host plans,
+    and its public header, without the operators that no workload launches:
+    ties a recorded ncu traffic figure to what it was taken on."""
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "mtp_speculative_decoding_gb300", "csrc")
-    for fn in ("common.cuh", "draft.cuh", "draft_dispatch.cu", "draft_inst.cu", "draft_kernel.cuh", "noalloc.cu",
-               "sample.cuh", "verify.cu", "verify.cuh"):
-        h.update(fn.encode())
-        with open(os.path.join(csrc, fn), "rb") as f:
+    files = [os.path.join(csrc, fn) for fn in sorted(os.listdir(csrc))
+             if fn.endswith((".cu", ".cuh", ".h")) and not fn.startswith(TARGET_STEP_SOURCES)]
+    for path in files + [os.path.join(ROOT, "include", "mtp.h")]:
+        h.update(os.path.basename(path).encode())
+        with open(path, "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
 
