@@ -14,10 +14,10 @@
 // leader's shared memory, so no workspace, no counters and no second launch
 // are needed.
 //
-// 128 rows of 248320 fp32 logits: 24.5 us, 5.2 TB/s; 144 rows of 262144 bf16
-// logits: 17.8 us (4.2 TB/s), 24.8 with one alternative, 28.7 with twenty
+// 128 rows of 248320 fp32 logits: 24.8 us, 5.1 TB/s; 144 rows of 262144 bf16
+// logits: 17.4 us (4.3 TB/s), 24.6 with one alternative, 28.9 with twenty
 // (the bound on the K-th and the ranking at the end are chains of barriers that
-// two CTAs an SM cannot hide); 4 rows with five alternatives: 7.9 us, all
+// two CTAs an SM cannot hide); 4 rows with five alternatives: 8.0 us, all
 // latency.
 #include "logprobs.cuh"
 

@@ -35,11 +35,12 @@ constexpr int kCcThreads = 128;
 
 // One CTA: 16 rows x 32 positions a tile, K and then V staged as fp32 in
 // shared memory.  Not the bytes bound it but a group's few rows against
-// every position in fp32 through shared memory: 64 sequences x 3 rows of fp32 queries over
-// 4096 positions of an e4m3 cache (16 heads, 4 KV heads of 256) take 2080 us,
-// where the tensor cores take 97 for bf16 queries; one sequence x 4 rows over
-// 8192 positions of a bf16 cache 92 us.  Warp w scores rows 4w..4w+3 with lane = position; thread d
-// owns output dimensions d, d + 128, .. of all 16 rows.
+// every position in fp32 through shared memory: 64 sequences x 3 rows of fp32
+// queries over 4096 positions of an e4m3 cache (16 heads, 4 KV heads of 256)
+// take 2060 us, where the tensor cores take 98 for bf16 queries; one sequence x
+// 4 rows over 8192 positions of a bf16 cache 72 us.  Warp w scores rows 4w..4w+3
+// with lane = position; thread d owns output dimensions d, d + 128, .. of all 16
+// rows.
 template <typename QT, typename KT>
 __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_constant__ PagedAttnArgs a) {
     extern __shared__ __align__(16) float sm[];

@@ -11,8 +11,8 @@
 // lose bits is split instead: against bf16, a query row and a probability into
 // two bf16 parts each (2^-16); against e4m3, a query row into three e4m3 parts
 // under a power of two of its own (2^-12) and a probability into three e5m2
-// parts (2^-9; e5m2 for its range: a weight 2^-28 below the largest still
-// counts).
+// parts (2^-9; e5m2 for its range: a weight keeps all 9 bits down to 2^-19 of the
+// largest and counts down to 2^-28).
 //
 // Softmax: a thread is one position of the tile and holds its RT scores.  The
 // reference m of a row (the running maximum) moves only when a score exceeds
@@ -24,13 +24,13 @@
 // warpgroups; warp 8: TMA producer; warp 9: MMA issue.
 //
 // The bytes of K and V bound it where batches are large: 64 sequences x 3 rows
-// over 4096 positions, e4m3, 16 heads over 4 KV heads of 256 (537 MB): 97 us
-// with the merge, 5.6 TB/s (a copy's rate would take 79); the same heads over
+// over 4096 positions, e4m3, 16 heads over 4 KV heads of 256 (537 MB): 98 us
+// with the merge, 5.5 TB/s (a copy's rate would take 79); the same heads over
 // windows of 1024 in bf16 (193 MB): 43 us; 16 sequences x up to 5 rows over 2k
-// to 32k positions, e4m3 (558 MB): 99 us, where the rows take RT = 32 and the
+// to 32k positions, e4m3 (558 MB): 100 us, where the rows take RT = 32 and the
 // issue of small MMAs (40 to 80 ns each) comes up to the bytes.  One sequence
-// is a chain of latencies: 4 rows over 8192 positions 14.6 us, 1 row over 999
-// 10.7 us (4 to 5 us to the first MMA: lengths, pages, TMA, the queries' norm and
+// is a chain of latencies: 4 rows over 8192 positions 14.7 us, 1 row over 999
+// 10.9 us (4 to 5 us to the first MMA: lengths, pages, TMA, the queries' norm and
 // rotation; 3 us in the merge).
 #include "paged_attn_tc.cuh"
 
