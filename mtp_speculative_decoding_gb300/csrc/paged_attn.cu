@@ -26,10 +26,8 @@ __device__ __forceinline__ void put(uint16_t* p, float x) { *p = (uint16_t)pack_
 
 // 2^x, never 0: an infinite value keeps its sign whatever its weight (0 times it
 // would be a NaN); a finite one's share is at most 2^-149 of it too much
-__device__ __forceinline__ float weight(float x) {
-    const float w = exp2f(x);
-    return w == 0.f ? __uint_as_float(1u) : w;
-}
+__device__ __forceinline__ float least(float w) { return w == 0.f ? __uint_as_float(1u) : w; }
+__device__ __forceinline__ float weight(float x) { return least(exp2f(x)); }
 
 constexpr int kCcThreads = 128;
 
@@ -160,11 +158,11 @@ __global__ void __launch_bounds__(kCcThreads) paged_attn_cc_kernel(const __grid_
                 const bool see = r < s.rows && skp[lane] && attends(a.c, t0 + lane, s.len + (r0 + r) / a.G);
                 const float v = see ? z[i] : -__int_as_float(0x7F800000);
                 const float mn = fmaxf(m[i], warp_max(v));
-                const float p = weight(v - mn);
+                const float p = exp2f(v - mn);   // (the sum takes it as it is: a row of scores of -inf has none)
                 const float f = weight(m[i] - mn);
                 l[i] = l[i] * f + warp_sum(see ? p : 0.f);
                 m[i] = mn;
-                sp[r * kCcTile + lane] = see ? p : -1.f;   // -1: masked, whatever the value row holds
+                sp[r * kCcTile + lane] = see ? least(p) : -1.f;   // -1: masked, whatever the value row holds
                 if (lane == 0) sf[r] = f;
             }
             __syncthreads();

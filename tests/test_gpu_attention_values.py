@@ -235,6 +235,23 @@ def test_scores_of_any_size(kv, qt, sign):
         assert ((out[0, j].double() - ref).abs() <= tol).all(), j
 
 
+@pytest.mark.parametrize("kv,qt,hd", [("f32", "f32", 64), ("bf16", "f32", 128), ("bf16", "bf16", 32)])
+def test_scores_of_minus_infinity_on_the_cuda_cores(kv, qt, hd):
+    """A key whose score is -inf has no weight, and a row with no other scores
+    gives zeros."""
+    pool = pc.Pool(2, 3, 16, 1, hd, kv, seed=20)
+    pool.fill([33, 20], seed=21)
+    q = queries(2, 1, 2, hd, torch.bfloat16 if qt == "bf16" else torch.float32, seed=22)
+    q[..., 0] = 1.0
+    gone = [(0, t) for t in (0, 7, 31, 32)] + [(1, t) for t in range(20)]
+    for b, t in gone:
+        pool.k[int(pool.table[b, t // 16]), 0, t % 16, 0] = -INF
+    out, st = run(pool, q, [32, 19])
+    assert st == mtp().MTP_OK
+    check(pool, out, q, None, [32, 19], [1, 1], 0.0, absent=set(gone))
+    assert not out[1].any()
+
+
 # ---------------------------------------------------------------------------
 # page scales
 # ---------------------------------------------------------------------------
