@@ -1,7 +1,7 @@
 /*
  * mtp.h -- C ABI of the GB300 MTP speculative-decoding hot path.
  *
- * Eight operations, all asynchronous on a caller-supplied CUDA stream:
+ * Eleven operations, all asynchronous on a caller-supplied CUDA stream:
  *
  *   mtp_draft_block    N chained draft steps of an MTP assistant head that
  *                      cross-attends into the target's KV cache, in ONE
@@ -22,6 +22,12 @@
  *                      step, or plain decoding) attend that cache.
  *   mtp_token_logprobs log probability, entropy and top alternatives of given
  *                      tokens from rows of logits.
+ *   mtp_rotate_axes    query and key rows normed and rotated by several
+ *                      positions (time, height, width of images and video).
+ *   mtp_prompt_attention  the rows of whole prompts, packed one after another,
+ *                      attend that cache.
+ *   mtp_prefix_attention  the new rows of sequences that share long prefixes
+ *                      attend that cache, a group's prefix once for all.
  *
  * Definitions are those of the pages this library implements:
  *   [G4] "Gemma 4 MTP -- Multi-Token Prediction speculative decoding":
@@ -91,6 +97,8 @@ enum { MTP_WQ_NONE = 0, MTP_WQ_Q8_0 = 1, MTP_WQ_Q4_0 = 2 };
 #define MTP_MAX_ATTN_ROWS 64        /* rows per sequence of one mtp_paged_attention call */
 #define MTP_MAX_PAGE_SIZE 256       /* slots of a page */
 #define MTP_MAX_TOP 32              /* alternatives per row of mtp_token_logprobs */
+#define MTP_MAX_PROMPT_ROWS 1048576 /* packed rows of one mtp_prompt_attention or mtp_rotate_axes call */
+#define MTP_MAX_AXES 4              /* positions per row of mtp_rotate_axes */
 
 /* Sizes and scalars of the assistant head ([G4] sec. 3-4).
  *   d_t        backbone (target) width: token embedding, h_prev, LM head input
@@ -495,6 +503,92 @@ int mtp_paged_attention(const mtp_kv_cache *c, int B, int M, int n_q_heads, cons
                         int64_t q_stride_b, int64_t q_stride_m, int64_t q_stride_h,
                         const float *q_norm, float rms_eps, float attn_scale, void *out,
                         void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/* Rows normed and rotated by several positions, for targets whose tokens have a
+ * place in time, height and width: row t, head h (queries and, where k is given,
+ * keys; each with its own norm),
+ *   y = rope(rmsnorm(x; norm)), the norm only where it is given; with P = the sum
+ *       of sections, the pairs (i, i + P), i < P, turn by
+ *       positions[axis(i), t] * theta^(-i / P), dimensions from 2 P on are not
+ *       turned
+ *   interleaved 0: axis(i) is the section that holds i (the sections one after
+ *       another); otherwise axis(i) = i mod n_axes while i < n_axes *
+ *       sections[i mod n_axes], else 0
+ * rounded once to dtype.  The rows then go to a cache with rope_theta 0
+ * (mtp_kv_append without k_norm) and attend it without q_norm.
+ *   positions  int32 [n_axes, rows], any sign
+ *   sections   HOST pointer, [n_axes] >= 0; P a multiple of 8, 2 P <= head_dim
+ *   q, k       rows in dtype (F32 or BF16): row (t, head h) at t*stride_m +
+ *              h*stride_h (elements; 16-byte multiples, 16-byte aligned),
+ *              head_dim (32, 64, 128, 256 or 512) contiguous; k NULL: queries
+ *              alone
+ *   out_q, out_k  the same with their own strides.  An output may be its input
+ *              (the same address and strides); else it overlaps no input
+ *   q_norm, k_norm  fp32 [head_dim] or NULL;  rms_eps their epsilon
+ * 1 <= rows <= MTP_MAX_PROMPT_ROWS, 1 <= n_axes <= MTP_MAX_AXES, theta > 0.  One
+ * launch, no workspace. */
+int mtp_rotate_axes(int64_t rows, int n_axes, const int32_t *positions, const int32_t *sections, int interleaved,
+                    float theta, int head_dim, int dtype,
+                    const void *q, int n_q_heads, int64_t q_stride_m, int64_t q_stride_h,
+                    const void *k, int n_k_heads, int64_t k_stride_m, int64_t k_stride_h,
+                    const float *q_norm, const float *k_norm, float rms_eps,
+                    void *out_q, int64_t out_q_stride_m, int64_t out_q_stride_h,
+                    void *out_k, int64_t out_k_stride_m, int64_t out_k_stride_h, mtp_stream_t stream);
+
+/* Workspace bytes of mtp_prompt_attention on this cache for at most B sequences
+ * with at most T rows in all, and of mtp_prefix_attention for at most B sequences
+ * of at most M rows.  0 for invalid sizes. */
+size_t mtp_prompt_workspace_size(const mtp_kv_cache *c, int B, int64_t T, int n_q_heads);
+size_t mtp_prefix_workspace_size(const mtp_kv_cache *c, int B, int M, int n_q_heads);
+
+/* Attention of whole prompts (or pieces of them) over the cache: the rows of B
+ * sequences lie one after another, sequence b's are rows [row_start[b],
+ * row_start[b + 1]) of T; row row_start[b] + j, at position kv_len[b] + j, attends
+ * as a row of mtp_paged_attention does (norm, rotation, scale, window and sink,
+ * absent pages, values that are not finite).  The keys and values of all rows are
+ * in the cache already.
+ *   kv_len [B] int32: positions cached before the rows
+ *   row_start [B + 1] int32, ascending, within [0, T]; rows of no sequence (in
+ *              front of row_start[0], behind row_start[B]) keep their bytes
+ *   q          rows in dtype (F32 or BF16): row (t, head h) at t*q_stride_m +
+ *              h*q_stride_h (elements; 16-byte multiples, 16-byte aligned)
+ *   out [T, n_q_heads, head_dim] in dtype
+ * fp32 queries are computed in fp32 throughout, with any cache.  bf16 queries
+ * against a bf16 or e4m3 cache with head_dim 64, 128 or 256 run on the tensor
+ * cores: rotated queries and probabilities are then rounded to bf16 (e4m3 cache:
+ * to fp16), maxima, sums and outputs are fp32.
+ * A sequence whose kv_len or rows are out of range is left out, positions on
+ * absent pages are masked, and both set the status word to MTP_ERR_ARG.
+ * 1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= T <= MTP_MAX_PROMPT_ROWS, T * n_q_heads <
+ * 2^31, at most 16 query heads per KV head. */
+int mtp_prompt_attention(const mtp_kv_cache *c, int B, int64_t T, int n_q_heads, const int32_t *kv_len,
+                         const int32_t *row_start, const void *q, int dtype, int64_t q_stride_m, int64_t q_stride_h,
+                         const float *q_norm, float rms_eps, float attn_scale, void *out,
+                         void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/* Attention of the new rows of sequences that share prefixes: as
+ * mtp_paged_attention, but the sequences [group_start[i], group_start[i + 1]) have
+ * their positions [0, prefix_len[i]) in common, on the pages of sequence
+ * group_start[i]'s row of page_table (the other sequences' entries for whole pages
+ * of it are not read).  A group's prefix is read and computed once for all of its
+ * rows, and every sequence's own positions [prefix_len[i], kv_len + j] for itself.
+ *   kv_len [B] int32 >= prefix_len of its group: the prefix counts;  n_new [B] or
+ *              NULL, q, q_norm, attn_scale, out: as for mtp_paged_attention
+ *   group_start [n_groups + 1] int32, ascending, within [0, B]; sequences of no
+ *              group have no prefix
+ *   prefix_len [n_groups] int32 >= 0, of any length (a prefix may end inside a page)
+ * The cache's window must be 0 (MTP_ERR_UNSUPPORTED otherwise: a sliding layer's
+ * rows attend few positions of a long prefix, and mtp_paged_attention reads only
+ * those).  Types and roundings as for mtp_prompt_attention.
+ * A sequence whose kv_len, n_new, prefix_len or group is out of range is left out,
+ * positions on absent pages are masked, and both set the status word to
+ * MTP_ERR_ARG.  1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= M <= MTP_MAX_ATTN_ROWS,
+ * 0 <= n_groups <= B, at most 16 query heads per KV head. */
+int mtp_prefix_attention(const mtp_kv_cache *c, int B, int M, int n_q_heads, const int32_t *kv_len, const int32_t *n_new,
+                         int n_groups, const int32_t *group_start, const int32_t *prefix_len,
+                         const void *q, int dtype, int64_t q_stride_b, int64_t q_stride_m, int64_t q_stride_h,
+                         const float *q_norm, float rms_eps, float attn_scale, void *out,
+                         void *ws, size_t ws_bytes, mtp_stream_t stream);
 
 /* Log probabilities of given tokens: for row r of logits [rows, V] in ldtype
  * (rows row_stride elements apart), with lse = log sum_v exp z_v,

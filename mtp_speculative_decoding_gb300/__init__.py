@@ -38,12 +38,16 @@ MTP_MAX_APPEND_ROWS = 65536
 MTP_MAX_ATTN_ROWS = 64
 MTP_MAX_PAGE_SIZE = 256
 MTP_MAX_TOP = 32
+MTP_MAX_PROMPT_ROWS = 1048576
+MTP_MAX_AXES = 4
 
 # every entry point include/mtp.h declares
 EXPORTS = ("mtp_workspace_size", "mtp_draft_block", "mtp_verify_greedy", "mtp_verify_sample",
            "mtp_sample_drafts", "mtp_quantize_q8_0", "mtp_last_error", "mtp_strerror", "mtp_debug_barrier_timeout",
            "mtp_verify_greedy_noalloc", "mtp_nextn_draft", "mtp_quantize_q4_0",
-           "mtp_kv_workspace_size", "mtp_kv_append", "mtp_paged_attention", "mtp_token_logprobs")
+           "mtp_kv_workspace_size", "mtp_kv_append", "mtp_paged_attention", "mtp_token_logprobs",
+           "mtp_rotate_axes", "mtp_prompt_workspace_size", "mtp_prompt_attention", "mtp_prefix_workspace_size",
+           "mtp_prefix_attention")
 
 
 class MTPError(RuntimeError):
@@ -143,6 +147,17 @@ def lib():
             L.mtp_paged_attention.restype = I
             L.mtp_token_logprobs.argtypes = [P, I, L64, I, L64, P, I, P, P, P, P, P]
             L.mtp_token_logprobs.restype = I
+            L.mtp_rotate_axes.argtypes = [L64, I, P, P, I, F, I, I, P, I, L64, L64, P, I, L64, L64, P, P, F, P, L64, L64, P, L64,
+                                          L64, P]
+            L.mtp_rotate_axes.restype = I
+            L.mtp_prompt_workspace_size.argtypes = [P, I, L64, I]
+            L.mtp_prompt_workspace_size.restype = Z
+            L.mtp_prompt_attention.argtypes = [P, I, L64, I, P, P, P, I, L64, L64, P, F, F, P, P, Z, P]
+            L.mtp_prompt_attention.restype = I
+            L.mtp_prefix_workspace_size.argtypes = [P, I, I, I]
+            L.mtp_prefix_workspace_size.restype = Z
+            L.mtp_prefix_attention.argtypes = [P, I, I, I, P, P, I, P, P, P, I, L64, L64, L64, P, F, F, P, P, Z, P]
+            L.mtp_prefix_attention.restype = I
             _lib = L
     return _lib
 
@@ -557,6 +572,105 @@ def paged_attention(cache: KVCache, q, kv_len, out, ws, n_new=None, q_norm=None,
                                     _on(dev, ws, "ws"), ws.numel(), rt.raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise MTPError(rc, "mtp_paged_attention")
+
+
+def prompt_workspace_size(cache: KVCache, B: int, T: int, n_q_heads: int) -> int:
+    """Workspace bytes of prompt_attention for B sequences with at most T rows in all."""
+    n = lib().mtp_prompt_workspace_size(C.byref(cache), B, T, n_q_heads)
+    if n == 0:
+        raise MTPError(MTP_ERR_ARG, "mtp_prompt_workspace_size")
+    return int(n)
+
+
+def prefix_workspace_size(cache: KVCache, B: int, M: int, n_q_heads: int) -> int:
+    """Workspace bytes of prefix_attention for B sequences of at most M rows."""
+    n = lib().mtp_prefix_workspace_size(C.byref(cache), B, M, n_q_heads)
+    if n == 0:
+        raise MTPError(MTP_ERR_ARG, "mtp_prefix_workspace_size")
+    return int(n)
+
+
+def prompt_attention(cache: KVCache, q, row_start, kv_len, out, ws, q_norm=None, rms_eps: float = 1e-6,
+                     attn_scale: float | None = None, stream=None) -> None:
+    """Launch mtp_prompt_attention on the current stream: packed rows q [T,
+    n_q_heads, head_dim] (fp32 or bf16, head_dim contiguous), rows
+    [row_start[b], row_start[b + 1]) those of sequence b at positions kv_len[b] +
+    j, attend the cache, which holds their keys and values already; out [T,
+    n_q_heads, head_dim] contiguous in q's dtype."""
+    rt = _runtime or _rt()
+    dev = rt.device()
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != cache.head_dim or strides[2] != 1:
+        raise ValueError("q: [T, n_q_heads, head_dim] with the cache's head_dim, contiguous")
+    B = kv_len.shape[0]
+    _cache_fits(cache, B, dev)
+    rc = rt.lib.mtp_prompt_attention(C.byref(cache), B, shape[0], shape[1], _plain(dev, kv_len, rt.i32, (B,), "kv_len"),
+                                     _plain(dev, row_start, rt.i32, (B + 1,), "row_start"), _on(dev, q, "q"), _code(rt, q, "q"),
+                                     strides[0], strides[1], _plain(dev, q_norm, rt.f32, (shape[2],), "q_norm"), rms_eps,
+                                     0.0 if attn_scale is None else attn_scale, _plain(dev, out, q.dtype, shape, "out"),
+                                     _on(dev, ws, "ws"), ws.numel(), rt.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise MTPError(rc, "mtp_prompt_attention")
+
+
+def prefix_attention(cache: KVCache, q, kv_len, group_start, prefix_len, out, ws, n_new=None, q_norm=None,
+                     rms_eps: float = 1e-6, attn_scale: float | None = None, stream=None) -> None:
+    """Launch mtp_prefix_attention on the current stream: rows q [B, M,
+    n_q_heads, head_dim] as for paged_attention, of sequences that share prefixes:
+    those of group i, [group_start[i], group_start[i + 1]), have the positions below
+    prefix_len[i] in common, on the first one's pages (group_start int32 [groups +
+    1], prefix_len int32 [groups])."""
+    rt = _runtime or _rt()
+    dev = rt.device()
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 4 or shape[3] != cache.head_dim or strides[3] != 1:
+        raise ValueError("q: [B, M, n_q_heads, head_dim] with the cache's head_dim, contiguous")
+    B, M, hq, hd = shape
+    groups = prefix_len.shape[0]
+    _cache_fits(cache, B, dev)
+    rc = rt.lib.mtp_prefix_attention(C.byref(cache), B, M, hq, _plain(dev, kv_len, rt.i32, (B,), "kv_len"),
+                                     _plain(dev, n_new, rt.i32, (B,), "n_new"), groups,
+                                     _plain(dev, group_start, rt.i32, (groups + 1,), "group_start"),
+                                     _plain(dev, prefix_len, rt.i32, (groups,), "prefix_len"), _on(dev, q, "q"), _code(rt, q, "q"),
+                                     strides[0], strides[1], strides[2], _plain(dev, q_norm, rt.f32, (hd,), "q_norm"), rms_eps,
+                                     0.0 if attn_scale is None else attn_scale, _plain(dev, out, q.dtype, shape, "out"),
+                                     _on(dev, ws, "ws"), ws.numel(), rt.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise MTPError(rc, "mtp_prefix_attention")
+
+
+def rotate_axes(q, k, positions, sections, theta: float, out_q, out_k=None, interleaved: bool = False, q_norm=None,
+                k_norm=None, rms_eps: float = 1e-6, stream=None) -> None:
+    """Launch mtp_rotate_axes on the current stream: rows q [T, n_q_heads,
+    head_dim] and k [T, n_k_heads, head_dim] (or None) of one dtype (fp32 or bf16,
+    head_dim contiguous), normed where a gain is given and rotated by positions
+    int32 [axes, T], sections[a] pairs by axis a; into out_q and out_k, which may
+    be q and k themselves."""
+    rt = _runtime or _rt()
+    dev = rt.device()
+    shape, code = q.shape, _code(rt, q, "q")
+    if len(shape) != 3 or q.stride(2) != 1:
+        raise ValueError("q: [T, n_q_heads, head_dim], head_dim contiguous")
+    T, hq, hd = shape
+    n = len(sections)
+    if out_q.shape != shape or out_q.dtype != q.dtype or out_q.stride(2) != 1:
+        raise ValueError("out_q: q's shape and dtype, head_dim contiguous")
+    hk, ks, os = 0, (0, 0), (0, 0)
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != T or k.shape[2] != hd or k.dtype != q.dtype or k.stride(2) != 1:
+            raise ValueError("k: [T, n_k_heads, head_dim] in q's dtype, head_dim contiguous")
+        if out_k is None or out_k.shape != k.shape or out_k.dtype != q.dtype or out_k.stride(2) != 1:
+            raise ValueError("out_k: k's shape and dtype, head_dim contiguous")
+        hk, ks, os = k.shape[1], k.stride(), out_k.stride()
+    s, o = q.stride(), out_q.stride()
+    rc = rt.lib.mtp_rotate_axes(T, n, _plain(dev, positions, rt.i32, (n, T), "positions"), (C.c_int32 * n)(*sections),
+                                1 if interleaved else 0, theta, hd, code, _on(dev, q, "q"), hq, s[0], s[1], _on(dev, k, "k"), hk,
+                                ks[0], ks[1], _plain(dev, q_norm, rt.f32, (hd,), "q_norm"),
+                                _plain(dev, k_norm, rt.f32, (hd,), "k_norm"), rms_eps, _on(dev, out_q, "out_q"), o[0], o[1],
+                                _on(dev, out_k, "out_k") if k is not None else 0, os[0], os[1],
+                                rt.raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise MTPError(rc, "mtp_rotate_axes")
 
 
 def token_logprobs(logits, tokens, out_logprob, out_entropy=None, out_top_ids=None, out_top_logprobs=None,

@@ -1,5 +1,7 @@
-// paged_api.cu -- the C ABI of the paged KV cache's append and attention and
-// of the token log probabilities: argument checks, workspace layout, launches.
+// paged_api.cu -- the C ABI of the paged KV cache's append and attention (a
+// verify step's rows, prompts, shared prefixes), of the rotation by several
+// positions and of the token log probabilities: argument checks, workspace
+// layout, launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -12,6 +14,7 @@
 #include "mtp.h"
 #include "paged.cuh"
 #include "paged_attn_tc.cuh"
+#include "rows.cuh"
 
 using namespace mtp;
 
@@ -134,6 +137,37 @@ bool heads_ok(const mtp_kv_cache* c, int n_q_heads, int* rc) {
     return *rc == MTP_OK;
 }
 
+// prompts and shared prefixes: what both calls check and fill alike
+size_t rows_workspace(const mtp_kv_cache*, int, int, int64_t, int) { return sizeof(WsHeader); }
+int rows_call(const mtp_kv_cache* c, int B, int n_q_heads, const int32_t* kv_len, const void* q, int dtype, int64_t sb, int64_t sm,
+              int64_t sh, const float* q_norm, float rms_eps, float attn_scale, const void* out) {
+    int rc = check_cache(c, true);
+    if (rc != MTP_OK) return rc;
+    if (B < 1 || B > MTP_MAX_PAGED_BATCH) return MTP_ERR_ARG;
+    if (!heads_ok(c, n_q_heads, &rc)) return rc;
+    if (dtype != MTP_DTYPE_F32 && dtype != MTP_DTYPE_BF16) return MTP_ERR_UNSUPPORTED;
+    if (!kv_len || misaligned(kv_len, 4) || misaligned(q_norm, 4)) return MTP_ERR_ARG;
+    if (!(rms_eps >= 0.f) || !(attn_scale >= 0.f) || isinf(attn_scale)) return MTP_ERR_ARG;
+    if ((rc = check_rows(q, dtype, sb, sm, sh)) != MTP_OK) return rc;
+    return !out || misaligned(out, 16) ? MTP_ERR_ARG : MTP_OK;
+}
+
+RowsArgs rows_args(const mtp_kv_cache* c, int B, int n_q_heads, const int32_t* kv_len, const void* q, int64_t sb, int64_t sm,
+                   int64_t sh, const float* q_norm, float rms_eps, float attn_scale, void* out, void* ws) {
+    RowsArgs a;
+    a.c = device_cache(c);
+    a.hd = c->head_dim; a.B = B; a.Hq = n_q_heads; a.G = n_q_heads / c->n_kv_heads;
+    a.M = 0; a.T = 0; a.n_groups = 0;
+    a.kv_len = kv_len; a.n_new = nullptr; a.row_start = nullptr; a.group_start = nullptr; a.prefix_len = nullptr;
+    a.q = q; a.sb = sb; a.sm = sm; a.sh = sh;
+    a.q_norm = q_norm; a.eps = rms_eps;
+    a.scale = (float)((attn_scale > 0.f ? (double)attn_scale : 1.0 / sqrt((double)c->head_dim)) * 1.4426950408889634074);
+    a.out = out;
+    a.hdr = static_cast<WsHeader*>(ws);
+    fill_rope(&a.rope, c->rope_theta, c->head_dim);
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -229,6 +263,99 @@ int mtp_paged_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, cons
     }
     if (e != cudaSuccess) return MTP_ERR_CUDA;
     return launch_paged_merge(a, dtype, s) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+}
+
+size_t mtp_prompt_workspace_size(const mtp_kv_cache* c, int B, int64_t T, int n_q_heads) {
+    int rc;
+    if (check_cache(c, false) != MTP_OK || B < 1 || B > MTP_MAX_PAGED_BATCH || T < 1 || T > MTP_MAX_PROMPT_ROWS) return 0;
+    if (!heads_ok(c, n_q_heads, &rc) || T * n_q_heads >= 1ll << 31) return 0;
+    return rows_workspace(c, B, 0, T, n_q_heads);
+}
+
+size_t mtp_prefix_workspace_size(const mtp_kv_cache* c, int B, int M, int n_q_heads) {
+    int rc;
+    if (check_cache(c, false) != MTP_OK || B < 1 || B > MTP_MAX_PAGED_BATCH || M < 1 || M > MTP_MAX_ATTN_ROWS) return 0;
+    if (!heads_ok(c, n_q_heads, &rc) || (int64_t)B * M * n_q_heads >= 1ll << 31) return 0;
+    return rows_workspace(c, B, M, (int64_t)B * M, n_q_heads);
+}
+
+int mtp_prompt_attention(const mtp_kv_cache* c, int B, int64_t T, int n_q_heads, const int32_t* kv_len, const int32_t* row_start,
+                         const void* q, int dtype, int64_t q_stride_m, int64_t q_stride_h, const float* q_norm, float rms_eps,
+                         float attn_scale, void* out, void* ws, size_t ws_bytes, mtp_stream_t stream) {
+    const int rc = rows_call(c, B, n_q_heads, kv_len, q, dtype, 0, q_stride_m, q_stride_h, q_norm, rms_eps, attn_scale, out);
+    if (rc != MTP_OK) return rc;
+    if (T < 1 || T > MTP_MAX_PROMPT_ROWS || !row_start || misaligned(row_start, 4)) return MTP_ERR_ARG;
+    if (T * n_q_heads >= 1ll << 31) return MTP_ERR_UNSUPPORTED;
+    if (!ws || misaligned(ws, 256) || ws_bytes < rows_workspace(c, B, 0, T, n_q_heads)) return MTP_ERR_WORKSPACE;
+    if (num_sms() <= 0) return MTP_ERR_CUDA;
+    RowsArgs a = rows_args(c, B, n_q_heads, kv_len, q, 0, q_stride_m, q_stride_h, q_norm, rms_eps, attn_scale, out, ws);
+    a.T = (int)T;
+    a.row_start = row_start;
+    return launch_rows_cc(a, dtype, c->kv_dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+}
+
+int mtp_prefix_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, const int32_t* kv_len, const int32_t* n_new, int n_groups,
+                         const int32_t* group_start, const int32_t* prefix_len, const void* q, int dtype, int64_t q_stride_b,
+                         int64_t q_stride_m, int64_t q_stride_h, const float* q_norm, float rms_eps, float attn_scale, void* out,
+                         void* ws, size_t ws_bytes, mtp_stream_t stream) {
+    const int rc = rows_call(c, B, n_q_heads, kv_len, q, dtype, q_stride_b, q_stride_m, q_stride_h, q_norm, rms_eps, attn_scale, out);
+    if (rc != MTP_OK) return rc;
+    if (M < 1 || M > MTP_MAX_ATTN_ROWS || misaligned(n_new, 4) || n_groups < 0 || n_groups > B) return MTP_ERR_ARG;
+    if (n_groups > 0 && (!group_start || !prefix_len || misaligned(group_start, 4) || misaligned(prefix_len, 4))) return MTP_ERR_ARG;
+    if (c->window > 0 || (int64_t)B * M * n_q_heads >= 1ll << 31) return MTP_ERR_UNSUPPORTED;
+    if (!ws || misaligned(ws, 256) || ws_bytes < rows_workspace(c, B, M, (int64_t)B * M, n_q_heads)) return MTP_ERR_WORKSPACE;
+    if (num_sms() <= 0) return MTP_ERR_CUDA;
+    RowsArgs a = rows_args(c, B, n_q_heads, kv_len, q, q_stride_b, q_stride_m, q_stride_h, q_norm, rms_eps, attn_scale, out, ws);
+    a.M = M;
+    a.n_new = n_new;
+    a.n_groups = n_groups; a.group_start = group_start; a.prefix_len = prefix_len;
+    return launch_rows_cc(a, dtype, c->kv_dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+}
+
+int mtp_rotate_axes(int64_t rows, int n_axes, const int32_t* positions, const int32_t* sections, int interleaved, float theta,
+                    int head_dim, int dtype, const void* q, int n_q_heads, int64_t q_stride_m, int64_t q_stride_h, const void* k,
+                    int n_k_heads, int64_t k_stride_m, int64_t k_stride_h, const float* q_norm, const float* k_norm, float rms_eps,
+                    void* out_q, int64_t out_q_stride_m, int64_t out_q_stride_h, void* out_k, int64_t out_k_stride_m,
+                    int64_t out_k_stride_h, mtp_stream_t stream) {
+    if (rows < 1 || rows > MTP_MAX_PROMPT_ROWS || n_axes < 1 || n_axes > MTP_MAX_AXES || !sections) return MTP_ERR_ARG;
+    const int hd = head_dim;
+    if (hd != 32 && hd != 64 && hd != 128 && hd != 256 && hd != 512) return MTP_ERR_UNSUPPORTED;
+    if (dtype != MTP_DTYPE_F32 && dtype != MTP_DTYPE_BF16) return MTP_ERR_UNSUPPORTED;
+    if (!positions || misaligned(positions, 4) || misaligned(q_norm, 4) || misaligned(k_norm, 4)) return MTP_ERR_ARG;
+    if (!(theta > 0.f) || isinf(theta) || !(rms_eps >= 0.f)) return MTP_ERR_ARG;
+    int64_t pairs = 0;
+    for (int i = 0; i < n_axes; ++i) {
+        if (sections[i] < 0) return MTP_ERR_ARG;
+        pairs += sections[i];
+    }
+    if (pairs < 1 || 2 * pairs > hd) return MTP_ERR_ARG;
+    if (pairs % 8) return MTP_ERR_UNSUPPORTED;
+    if (n_q_heads < 1 || n_q_heads > 16384 || (k && (n_k_heads < 1 || n_k_heads > 16384))) return MTP_ERR_ARG;
+    int rc;
+    if ((rc = check_rows(q, dtype, 0, q_stride_m, q_stride_h)) != MTP_OK) return rc;
+    if ((rc = check_rows(out_q, dtype, 0, out_q_stride_m, out_q_stride_h)) != MTP_OK) return rc;
+    if (k && ((rc = check_rows(k, dtype, 0, k_stride_m, k_stride_h)) != MTP_OK ||
+              (rc = check_rows(out_k, dtype, 0, out_k_stride_m, out_k_stride_h)) != MTP_OK))
+        return rc;
+    if (rows * (n_q_heads + (k ? n_k_heads : 0)) >= 1ll << 31) return MTP_ERR_UNSUPPORTED;
+    const int sms = num_sms();
+    if (sms <= 0) return MTP_ERR_CUDA;
+    RotateArgs a;
+    a.in[0] = q; a.in[1] = k; a.out[0] = out_q; a.out[1] = out_k;
+    a.in_sm[0] = q_stride_m; a.in_sh[0] = q_stride_h; a.in_sm[1] = k_stride_m; a.in_sh[1] = k_stride_h;
+    a.out_sm[0] = out_q_stride_m; a.out_sh[0] = out_q_stride_h; a.out_sm[1] = out_k_stride_m; a.out_sh[1] = out_k_stride_h;
+    a.norm[0] = q_norm; a.norm[1] = k_norm;
+    a.heads[0] = n_q_heads; a.heads[1] = k ? n_k_heads : 0;
+    a.pos = positions;
+    a.rows = (int)rows; a.hd = hd; a.pairs = (int)pairs;
+    a.eps = rms_eps;
+    fill_rope(&a.rope, theta, 2 * (int)pairs);
+    for (int i = 0, at = 0, end = sections[0]; i < (int)pairs; ++i) {
+        while (i >= end) end += sections[++at];
+        const int turn = i % n_axes;
+        a.axis[i] = (uint8_t)(interleaved ? (i < (int64_t)n_axes * sections[turn] ? turn : 0) : at);
+    }
+    return launch_rotate_axes(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
 
 int mtp_token_logprobs(const void* logits, int ldtype, int64_t rows, int V, int64_t row_stride, const int32_t* tokens,

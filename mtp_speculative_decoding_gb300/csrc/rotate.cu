@@ -1,0 +1,99 @@
+// rotate.cu -- query and key rows normed and rotated by several positions.
+//
+// y = rope(rmsnorm(x)), where the pair (i, i + pairs) turns by the position of
+// its axis times theta^(-i / pairs).  A thread takes one unit (8 pairs, or 16
+// elements behind the rotated ones) of `hpt` heads of one row, so that the
+// angles of a row are computed once for those heads.  Long calls are bound by
+// the bytes in and out, short ones by the launch and two dependent loads.
+#include "rows.cuh"
+
+namespace mtp {
+
+namespace {
+
+// (plain loads: the rows may be rewritten in place)
+__device__ __forceinline__ uint4 ld16(const void* p) {
+    uint4 r;
+    asm("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ void in8(const float* p, float (&x)[8]) {
+    const uint4 u = ld16(p), w = ld16(p + 4);
+    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    x[4] = __uint_as_float(w.x); x[5] = __uint_as_float(w.y); x[6] = __uint_as_float(w.z); x[7] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void in8(const uint16_t* p, float (&x)[8]) { open_unit(ld16(p), x); }
+
+constexpr int kRotThreads = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_constant__ RotateArgs a) {
+    constexpr bool FAST = sizeof(T) == 2;
+    const int U = a.hd >> 4, ulog = 31 - __clz(U), all = a.groups[0] + a.groups[1];
+    const long long x = (long long)blockIdx.x * kRotThreads + threadIdx.x, unit = x >> ulog;
+    const int c = (int)(x & (U - 1));
+    int row = (int)(unit / all), grp = (int)(unit - (long long)row * all);
+    const bool live = row < a.rows;   // (whole rows' lanes; the others go along for the shuffles)
+    if (!live) {
+        row = a.rows - 1;
+        grp = 0;
+    }
+    const int which = grp >= a.groups[0] ? 1 : 0;
+    if (which) grp -= a.groups[0];
+    const int h0 = grp * a.hpt, h1 = h0 + a.hpt < a.heads[which] ? h0 + a.hpt : a.heads[which];
+    const bool turn = 8 * c < a.pairs;
+    // the unit's two runs of eight elements
+    const int e0 = turn ? 8 * c : 2 * a.pairs + 16 * (c - (a.pairs >> 3)), e1 = turn ? a.pairs + 8 * c : e0 + 8;
+    float cs[8], sn[8];
+    if (turn) {
+        const int32_t* pos = a.pos + row;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float pl, ph;
+            split_pos(pos[(long long)a.axis[8 * c + i] * a.rows], pl, ph);
+            pair_angle<FAST>(pl, ph, a.rope.hi[8 * c + i], a.rope.lo[8 * c + i], cs[i], sn[i]);
+        }
+    }
+    const T* src = reinterpret_cast<const T*>(a.in[which]) + row * a.in_sm[which];
+    T* dst = reinterpret_cast<T*>(a.out[which]) + row * a.out_sm[which];
+    const float* gain = a.norm[which];
+    float g0[8], g1[8];
+    if (gain)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g0[i] = __ldg(gain + e0 + i);
+            g1[i] = __ldg(gain + e1 + i);
+        }
+    for (int i = 0; i < a.hpt; ++i) {
+        const int h = h0 + i < h1 ? h0 + i : h1 - 1;   // (every lane of the warp takes part in the norm)
+        float p[8], q[8];
+        in8(src + h * a.in_sh[which] + e0, p);
+        in8(src + h * a.in_sh[which] + e1, q);
+        const float r = unit_rms(p, q, a.hd, a.eps);
+        if (gain)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                p[e] *= r * g0[e];
+                q[e] *= r * g1[e];
+            }
+        if (turn) unit_rotate(p, q, cs, sn);
+        if (live && h0 + i < h1) {
+            store8(dst + h * a.out_sh[which] + e0, p);
+            store8(dst + h * a.out_sh[which] + e1, q);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rotate_axes(RotateArgs a, int dtype, int sms, cudaStream_t s) {
+    a.hpt = 1;
+    for (int w = 0; w < 2; ++w) a.groups[w] = (a.heads[w] + a.hpt - 1) / a.hpt;
+    const long long threads = (long long)a.rows * (a.groups[0] + a.groups[1]) * (a.hd >> 4);
+    const unsigned grid = (unsigned)((threads + kRotThreads - 1) / kRotThreads);
+    if (dtype == MTP_DTYPE_F32) rotate_axes_kernel<float><<<grid, kRotThreads, 0, s>>>(a);
+    else rotate_axes_kernel<uint16_t><<<grid, kRotThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace mtp
