@@ -14,7 +14,7 @@
 #include "mtp.h"
 #include "paged.cuh"
 #include "paged_attn_tc.cuh"
-#include "rows.cuh"
+#include "rows_attn_tc.cuh"
 
 using namespace mtp;
 
@@ -91,8 +91,8 @@ bool tc_path(const mtp_kv_cache* c, int dtype) {
 }
 
 // (dimension, slot, KV head, page) map of k or v: boxes of one 128-byte (64 for
-// rows of 64 bytes) swizzled column by min(page_size, 128) slots
-bool encode_pages(CUtensorMap* m, const void* base, const mtp_kv_cache* c) {
+// rows of 64 bytes) swizzled column by min(page_size, rows) slots
+bool encode_pages(CUtensorMap* m, const void* base, const mtp_kv_cache* c, int rows = kTcTile) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const int esz = elem_size(c->kv_dtype);
@@ -102,7 +102,7 @@ bool encode_pages(CUtensorMap* m, const void* base, const mtp_kv_cache* c) {
     // a stride that no index uses may be anything: give it a legal value
     const cuuint64_t strides[3] = {(cuuint64_t)c->stride_t * esz, c->n_kv_heads > 1 ? (cuuint64_t)c->stride_h * esz : row,
                                    c->n_pages > 1 ? (cuuint64_t)c->stride_p * esz : row};
-    const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / esz), (cuuint32_t)(c->page_size < kTcTile ? c->page_size : kTcTile), 1, 1};
+    const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / esz), (cuuint32_t)(c->page_size < rows ? c->page_size : rows), 1, 1};
     const cuuint32_t one[4] = {1, 1, 1, 1};
     return enc(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -138,7 +138,49 @@ bool heads_ok(const mtp_kv_cache* c, int n_q_heads, int* rc) {
 }
 
 // prompts and shared prefixes: what both calls check and fill alike
-size_t rows_workspace(const mtp_kv_cache*, int, int, int64_t, int) { return sizeof(WsHeader); }
+// (on the tensor cores if the queries are bf16)
+bool rows_tc(const mtp_kv_cache* c) {
+    return c->kv_dtype != MTP_DTYPE_F32 && (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256);
+}
+struct RowsSpace {
+    size_t status, note, head, pre, cum, odd, part, part_ml, dense, dense_ml, end;
+    int workers;
+};
+// (every field grows with B, M and T, so that a workspace sized for more serves less)
+RowsSpace rows_space(const mtp_kv_cache* c, int B, int M, int64_t T, int n_q_heads, int sms) {
+    RowsSpace p = {};
+    const int hd = c->head_dim;
+    size_t off = sizeof(WsHeader);
+    auto take = [&](size_t n) {
+        const size_t at = off;
+        off = al256(off + n);
+        return at;
+    };
+    if (rows_tc(c)) {
+        const size_t rows = (size_t)T * n_q_heads;
+        p.workers = sms / rows_pair(hd);
+        p.status = take((size_t)sms * sizeof(int));
+        p.note = take((size_t)p.workers * sizeof(int4));
+        p.head = take(sizeof(int2));
+        p.pre = take((2 * (size_t)B + 1) * sizeof(long long));
+        p.cum = take(((size_t)B + 1) * sizeof(int));
+        p.part_ml = take(2 * (size_t)p.workers * kRowTile * sizeof(float2));
+        p.part = take(2 * (size_t)p.workers * kRowTile * hd * sizeof(float));
+        if (M > 0) {
+            p.dense_ml = take(2 * rows * sizeof(float2));
+            p.dense = take(2 * rows * hd * sizeof(float));
+        } else {
+            p.odd = take((rows + 4095) / 4096 * 4096);
+        }
+    }
+    p.end = off;
+    return p;
+}
+size_t rows_workspace(const mtp_kv_cache* c, int B, int M, int64_t T, int n_q_heads) {
+    int sms = num_sms();
+    if (sms <= 0) sms = 152;   // no device (a host-side size query)
+    return rows_space(c, B, M, T, n_q_heads, sms).end;
+}
 int rows_call(const mtp_kv_cache* c, int B, int n_q_heads, const int32_t* kv_len, const void* q, int dtype, int64_t sb, int64_t sm,
               int64_t sh, const float* q_norm, float rms_eps, float attn_scale, const void* out) {
     int rc = check_cache(c, true);
@@ -166,6 +208,34 @@ RowsArgs rows_args(const mtp_kv_cache* c, int B, int n_q_heads, const int32_t* k
     a.hdr = static_cast<WsHeader*>(ws);
     fill_rope(&a.rope, c->rope_theta, c->head_dim);
     return a;
+}
+
+int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, void* ws, int sms, cudaStream_t s) {
+    if (dtype != MTP_DTYPE_BF16 || !rows_tc(c)) return launch_rows_cc(a, dtype, c->kv_dtype, s) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+    const RowsSpace p = rows_space(c, a.B, a.M, T, a.Hq, sms);
+    char* base = static_cast<char*>(ws);
+    RowsTcParams pp;
+    RowsTcArgs& t = pp.t;
+    t.a = a;
+    t.workers = p.workers;
+    const long long U = (long long)kPosTile * a.G;
+    t.window_units = U * ((a.c.sink + (long long)kPosTile - 1) / kPosTile + (a.c.window + (kRowTile - 1) / a.G) / kPosTile + 2);
+    t.cta_status = reinterpret_cast<int*>(base + p.status);
+    t.note = reinterpret_cast<int4*>(base + p.note);
+    t.plan_head = reinterpret_cast<int2*>(base + p.head);
+    t.plan_pre = reinterpret_cast<long long*>(base + p.pre);
+    t.plan_cum = reinterpret_cast<int*>(base + p.cum);
+    t.part = reinterpret_cast<float*>(base + p.part);
+    t.part_ml = reinterpret_cast<float2*>(base + p.part_ml);
+    t.odd = reinterpret_cast<uint8_t*>(base + p.odd);
+    t.dense = reinterpret_cast<float*>(base + p.dense);
+    t.dense_ml = reinterpret_cast<float2*>(base + p.dense_ml);
+    t.timeout_ns = kWaitLimitNs;
+    // (a stride beyond 2^40 bytes has no map)
+    if (!encode_pages(&pp.tk, c->k, c, kPosTile / rows_pair(c->head_dim)) || !encode_pages(&pp.tv, c->v, c, kPosTile)) return MTP_ERR_UNSUPPORTED;
+    const bool e4m3 = c->kv_dtype == MTP_DTYPE_E4M3;
+    if ((e4m3 ? launch_rows_tc_e4m3(pp, s) : launch_rows_tc_bf16(pp, s)) != cudaSuccess) return MTP_ERR_CUDA;
+    return launch_rows_merge(t, c->kv_dtype, s) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
 
 }  // namespace
@@ -287,11 +357,12 @@ int mtp_prompt_attention(const mtp_kv_cache* c, int B, int64_t T, int n_q_heads,
     if (T < 1 || T > MTP_MAX_PROMPT_ROWS || !row_start || misaligned(row_start, 4)) return MTP_ERR_ARG;
     if (T * n_q_heads >= 1ll << 31) return MTP_ERR_UNSUPPORTED;
     if (!ws || misaligned(ws, 256) || ws_bytes < rows_workspace(c, B, 0, T, n_q_heads)) return MTP_ERR_WORKSPACE;
-    if (num_sms() <= 0) return MTP_ERR_CUDA;
+    const int sms = num_sms();
+    if (sms <= 0) return MTP_ERR_CUDA;
     RowsArgs a = rows_args(c, B, n_q_heads, kv_len, q, 0, q_stride_m, q_stride_h, q_norm, rms_eps, attn_scale, out, ws);
     a.T = (int)T;
     a.row_start = row_start;
-    return launch_rows_cc(a, dtype, c->kv_dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+    return launch_rows(c, a, dtype, T, ws, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int mtp_prefix_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, const int32_t* kv_len, const int32_t* n_new, int n_groups,
@@ -304,12 +375,13 @@ int mtp_prefix_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, con
     if (n_groups > 0 && (!group_start || !prefix_len || misaligned(group_start, 4) || misaligned(prefix_len, 4))) return MTP_ERR_ARG;
     if (c->window > 0 || (int64_t)B * M * n_q_heads >= 1ll << 31) return MTP_ERR_UNSUPPORTED;
     if (!ws || misaligned(ws, 256) || ws_bytes < rows_workspace(c, B, M, (int64_t)B * M, n_q_heads)) return MTP_ERR_WORKSPACE;
-    if (num_sms() <= 0) return MTP_ERR_CUDA;
+    const int sms = num_sms();
+    if (sms <= 0) return MTP_ERR_CUDA;
     RowsArgs a = rows_args(c, B, n_q_heads, kv_len, q, q_stride_b, q_stride_m, q_stride_h, q_norm, rms_eps, attn_scale, out, ws);
     a.M = M;
     a.n_new = n_new;
     a.n_groups = n_groups; a.group_start = group_start; a.prefix_len = prefix_len;
-    return launch_rows_cc(a, dtype, c->kv_dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+    return launch_rows(c, a, dtype, (int64_t)B * M, ws, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int mtp_rotate_axes(int64_t rows, int n_axes, const int32_t* positions, const int32_t* sections, int interleaved, float theta,

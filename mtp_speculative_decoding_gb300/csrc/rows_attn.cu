@@ -1,12 +1,14 @@
 // rows_attn.cu -- attention of many rows over the paged cache on the CUDA cores:
 // a warp takes one row (a token's query head) and walks the positions that it
-// attends.
+// attends.  It serves fp32 queries or caches and the head dimensions 32 and 512,
+// and the rows whose product on the tensor cores is not finite; with it, the merge
+// of what the tensor cores left in parts.
 //
 // Every score, maximum, sum and output is fp32.  A row's units (16 elements, see
 // paged.cuh) lie in hd / 16 lanes, so the warp holds 32 / (hd / 16) positions at
 // a time and reads each key and value as 16-byte pieces; every lane group keeps
 // a running maximum and sum of its own, merged at the end.
-#include "rows.cuh"
+#include "rows_attn_tc.cuh"
 
 namespace mtp {
 
@@ -184,7 +186,205 @@ cudaError_t cc_kv(const RowsArgs& a, int kv_dtype, cudaStream_t s) {
     return kv_dtype == MTP_DTYPE_F32 ? cc<QT, float>(a, s) : kv_dtype == MTP_DTYPE_BF16 ? cc<QT, uint16_t>(a, s) : cc<QT, uint8_t>(a, s);
 }
 
+// ---------------------------------------------------------------------------
+// merge of the parts that the tensor cores left: out = sum_s 2^(m_s - M) o_s /
+// sum_s 2^(m_s - M) l_s over a row's parts, hd / 4 threads a row with four
+// dimensions each.  A prompt's row has parts where its item was cut between
+// workers; with shared prefixes every row has its prefix's and its own.  A result
+// that is not finite is computed again by attend_row, and so are the rows that the
+// attention marked.
+// ---------------------------------------------------------------------------
+constexpr int kMergeRowThreads = 256, kOddRows = 16 * kMergeRowThreads;   // rows whose marks a CTA looks at
+
+struct RowParts {
+    long long dense;                  // the row's place in `dense` (< 0: in slots)
+    int w0, w1;                       // workers of its slots (w1 < w0: no part)
+    int r;                            // row of the slots
+};
+// parts of row r of (block, KV head)
+__device__ RowParts parts_of(const RowsTcArgs& t, const RowsPlan& plan, int blk, int g, int r, long long dense) {
+    RowParts p = {-1, 0, -1, r % kRowTile};
+    const Block k = block_at(t.a, plan.cum, blk);
+    if (r >= k.n * t.a.G) return p;
+    const Item it = item_of(t, plan, k, blk, g, r / kRowTile);
+    const long long T = plan.pre[rows_blocks(t.a)];
+    p.w0 = worker_of(T, plan.workers, it.tiles_at);
+    p.w1 = worker_of(T, plan.workers, it.tiles_at + (long long)(it.n - 1) * kPosTile * t.a.G);
+    if (p.w0 == p.w1) p.dense = dense;
+    return p;
+}
+
+template <typename KT>
+__global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int ctas, int merges) {
+    __shared__ RowParts s_parts[2][kMergeRowThreads / 16];
+    __shared__ int4 s_row[kMergeRowThreads / 16];           // sequence (< 0: none), token, query head
+    __shared__ int s_list[kOddRows];
+    __shared__ int s_n;
+    const RowsArgs& a = t.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s_n = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if ((int)blockIdx.x == (int)gridDim.x - 1) {   // the call's status from the CTAs'
+        int bad = 0;
+        for (int c = tid; c < ctas; c += kMergeRowThreads) {
+            const int st = t.cta_status[c];
+            if (st == MTP_ERR_TIMEOUT) bad |= 2;
+            else if (st != MTP_OK) bad |= 1;
+        }
+        const int any1 = __syncthreads_or(bad & 1), any2 = __syncthreads_or(bad & 2);
+        if (tid == 0) {
+            a.hdr->status = any2 ? MTP_ERR_TIMEOUT : any1 ? MTP_ERR_ARG : MTP_OK;
+            a.hdr->barrier = 0;
+            a.hdr->done = 0;
+        }
+        return;
+    }
+    auto again = [&](long long id) {   // the whole warp
+        const int tok = (int)(id / a.Hq), h = (int)(id - (long long)tok * a.Hq), b = a.M > 0 ? tok / a.M : last_at_most(a.row_start, a.B, tok);
+        Seq s;
+        if (!seq_at(a, b, s)) return;
+        const int j = (int)(tok - s.row0);
+        if (j >= 0 && j < s.n) attend_row<uint16_t, KT>(a, s, b, j, h, lane);
+    };
+    if ((int)blockIdx.x >= merges) {   // rows that the attention marked
+        const long long first = (long long)(blockIdx.x - merges) * kOddRows, rows = (long long)a.T * a.Hq;
+        __syncthreads();
+        const uint4 v = *reinterpret_cast<const uint4*>(t.odd + first + 16 * tid);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (v.x | v.y | v.z | v.w)
+            for (int i = 0; i < 16; ++i)
+                if ((w[i >> 2] >> (8 * (i & 3))) & 0xFFu && first + 16 * tid + i < rows) s_list[atomicAdd(&s_n, 1)] = 16 * tid + i;
+        __syncthreads();
+        for (int i = warp; i < s_n; i += kMergeRowThreads / 32) again(first + s_list[i]);
+        return;
+    }
+    const int hd = a.hd, gt = hd >> 2, per = kMergeRowThreads / gt, sub = tid / gt, d = 4 * (tid - sub * gt);
+    if (tid < per) {
+        RowParts p0 = {-1, 0, -1, 0}, p1 = p0;
+        int4 row = make_int4(-1, 0, 0, 0);
+        if (a.M == 0) {
+            const int rows_at = kRowTile / per, w = blockIdx.x / rows_at, r = (blockIdx.x - w * rows_at) * per + tid;
+            const int4 n = t.note[w];
+            // (an attention that gave up may have left anything: it stays in bounds)
+            if (n.x >= 0 && n.x < a.B && n.y >= 0 && n.y < a.c.Hkv && n.z >= 0 && n.w > w && n.w < t.workers) {
+                const Block k = block_at(a, nullptr, n.x);
+                const long long at = (long long)n.z * kRowTile + r;
+                if (at < (long long)k.n * a.G) {
+                    const RowPlace pl = row_place(a, nullptr, k, n.y, (int)at);
+                    p0.w0 = w;
+                    p0.w1 = n.w;
+                    p0.r = r;
+                    row = make_int4(pl.b, pl.j, (int)(pl.out % a.Hq), 0);
+                }
+            }
+        } else {
+            const long long id = (long long)blockIdx.x * per + tid;
+            const int tok = (int)(id / a.Hq), b = tok / a.M, j = tok - b * a.M, h = (int)(id - (long long)tok * a.Hq);
+            Seq s;
+            if (b < a.B && seq_at(a, b, s) && j < s.n) {
+                RowsPlan plan;
+                const int2 head = *t.plan_head;
+                plan.open = head.x;
+                plan.workers = head.y;
+                plan.pre = t.plan_pre;
+                plan.cum = t.plan_cum;
+                const int g = h / a.G;
+                p0 = parts_of(t, plan, a.n_groups + b, g, j * a.G + h - g * a.G, (long long)a.B * a.M * a.Hq + id);
+                if (s.group >= 0 && s.P > 0) p1 = parts_of(t, plan, s.group, g, (plan.cum[b] - plan.cum[s.first] + j) * a.G + h - g * a.G, id);
+                row = make_int4(b, j, h, 0);
+            }
+        }
+        s_parts[0][tid] = p0;
+        s_parts[1][tid] = p1;
+        s_row[tid] = row;
+        s_list[tid] = 0;   // 1: the row's result is not finite
+    }
+    __syncthreads();
+    const int4 row = s_row[sub];
+    if (row.x >= 0) {
+        float M = kNoScore, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const RowParts p = s_parts[which][sub];
+            constexpr int N = 4;   // parts in flight
+#pragma unroll 1
+            for (int w = p.w0; w <= p.w1; w += N) {
+                float2 ml[N];
+                float4 o[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    ml[i] = make_float2(kNoScore, 0.f);
+                    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w + i > p.w1) continue;
+                    const long long at = (2ll * (w + i) + (w + i == p.w0 ? 1 : 0)) * kRowTile + p.r;
+                    ml[i] = p.dense >= 0 ? t.dense_ml[p.dense] : t.part_ml[at];
+                    o[i] = *reinterpret_cast<const float4*>((p.dense >= 0 ? t.dense + p.dense * hd : t.part + at * hd) + d);
+                }
+                float mn = M;
+#pragma unroll
+                for (int i = 0; i < N; ++i) mn = fmaxf(mn, ml[i].x);
+                const float f = exp2f(M - mn);
+                acc.x *= f;
+                acc.y *= f;
+                acc.z *= f;
+                acc.w *= f;
+                l *= f;
+                M = mn;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float e = exp2f(ml[i].x - mn);
+                    acc.x = fmaf(e, o[i].x, acc.x);
+                    acc.y = fmaf(e, o[i].y, acc.y);
+                    acc.z = fmaf(e, o[i].z, acc.z);
+                    acc.w = fmaf(e, o[i].w, acc.w);
+                    l = fmaf(e, ml[i].y, l);
+                }
+            }
+        }
+        const float inv = zero_sum(l);
+        acc.x *= inv;
+        acc.y *= inv;
+        acc.z *= inv;
+        acc.w *= inv;
+        Seq s;
+        seq_at(a, row.x, s);
+        const long long id = (s.row0 + row.y) * a.Hq + row.z;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + id * hd + d) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+        const float odd = fmaf(acc.x, 0.f, fmaf(acc.y, 0.f, fmaf(acc.z, 0.f, acc.w * 0.f)));
+        if (!(odd == 0.f)) s_list[sub] = 1;
+    }
+    __syncthreads();
+    for (int i = warp; i < per; i += kMergeRowThreads / 32) {
+        const int4 r = s_row[i];
+        if (r.x < 0 || s_list[i] != 1) continue;
+        Seq s;
+        seq_at(a, r.x, s);
+        attend_row<uint16_t, KT>(a, s, r.x, r.y, r.z, lane);
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_rows_merge(const RowsTcArgs& t, int kv_dtype, cudaStream_t s) {
+    const RowsArgs& a = t.a;
+    const int per = kMergeRowThreads / (a.hd >> 2);
+    const long long rows = a.M > 0 ? (long long)a.B * a.M * a.Hq : (long long)t.workers * kRowTile;
+    const long long merges = (rows + per - 1) / per, odd = a.M > 0 ? 0 : ((long long)a.T * a.Hq + kOddRows - 1) / kOddRows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(merges + odd + 1));
+    cfg.blockDim = dim3(kMergeRowThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its CTAs come in while the attention ends
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const int ctas = t.workers * rows_pair(a.hd);
+    return kv_dtype == MTP_DTYPE_E4M3 ? cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint8_t>, t, ctas, (int)merges)
+                                      : cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint16_t>, t, ctas, (int)merges);
+}
 
 cudaError_t launch_rows_cc(const RowsArgs& a, int dtype, int kv_dtype, cudaStream_t s) {
     return dtype == MTP_DTYPE_F32 ? cc_kv<float>(a, kv_dtype, s) : cc_kv<uint16_t>(a, kv_dtype, s);

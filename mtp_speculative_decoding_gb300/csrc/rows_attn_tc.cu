@@ -1,0 +1,988 @@
+// rows_attn_tc.cu -- attention of many rows over the paged cache on tcgen05
+// tensor cores: whole prompts, and batches that share prefixes.
+//
+// The rows take the MMA's M side: S [rows, 128 positions] = Q K^T, with the
+// queries normed, rotated and rounded once into shared memory, and O [rows, hd]
+// += P V, with P read from tensor memory, where the softmax leaves it over the
+// scores it came from, and V's tile as it lies in the page (its dimensions
+// contiguous: the N-major operand).  K and V come from the pages by TMA; an e4m3
+// cache's codes are opened to fp16, which holds them exactly, and multiplied
+// with queries and probabilities in fp16, the page scales folded into the
+// scores.
+//
+// A worker holds 256 rows.  Head dimensions 64 and 128: one CTA with two row
+// tiles of 128, whose softmax and MMAs take turns.  Head dimension 256: a pair
+// of CTAs (cta_group::2, M = 256) with a row tile each, because the accumulator
+// fills half of the tensor memory; each CTA brings half of every K and V tile,
+// which halves their traffic, and the scores have two buffers.
+//
+// Softmax: a thread is a row.  The reference m of a row (the running maximum)
+// moves only when a score exceeds it by more than 2^kSlack, so the accumulator is
+// rescaled a few times at most.
+//
+// A result that is not finite is computed again, position by position, by the
+// kernel behind this one (rows_attn.cu): the products here multiply masked
+// positions by a weight of zero, which makes a NaN of an infinity.
+#include "rows_attn_tc.cuh"
+
+namespace mtp {
+
+namespace {
+
+// ---- instructions of this kernel; CG: CTAs of an MMA ----
+template <int CG>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+            : "memory");
+}
+// A from tensor memory
+template <int CG>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+            : "memory");
+}
+// arrive once on `bar` (of both CTAs of a pair) when the MMAs issued so far are done
+template <int CG>
+__device__ __forceinline__ void commit(unsigned long long* bar) {
+    if (CG == 1) umma_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                         smem_addr(bar)),
+                     "h"((unsigned short)3)
+                     : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void alloc_columns(unsigned int* dst, unsigned int n) {
+    if (CG == 1) {
+        tmem_alloc(dst, n);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(n) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void free_columns(unsigned int at, unsigned int n) {
+    if (CG == 1) tmem_dealloc(at, n);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(n) : "memory");
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// arrive on the leading CTA's barrier of the same place
+template <int CG>
+__device__ __forceinline__ void arrive_lead(unsigned long long* bar) {
+    if (CG == 1) mbar_arrive(bar);
+    else
+        asm volatile(
+            "{\n\t.reg .b32 a;\n\t"
+            "mapa.shared::cluster.u32 a, %0, 0;\n\t"
+            "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ bool try_wait(unsigned long long* bar, unsigned int parity) {
+    if (CG == 1) return mbar_try_wait(bar, parity);
+    unsigned int ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool elect() {
+    unsigned int p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void ld32(uint32_t at, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(
+            r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tma_4d(void* dst, const void* tmap, int x, int y, int z, int w, unsigned long long* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            smem_addr(dst)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+// two lanes of fp32 in one instruction
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Operand rows of 128 bytes under the 128-byte swizzle, 8-row groups following
+// one another: K-major operands (Q, K: a row, 64 dimensions), and the N-major V (a
+// position, 64 dimensions; `lead`: bytes between its 64-wide blocks)
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+__host__ __device__ constexpr uint32_t lead_bits(uint32_t lead) { return (lead >> 4) << 16; }
+// fp32 accumulator, M x N, bf16 (1) or fp16 (0) operands, B N-major or not
+__host__ __device__ constexpr uint32_t idesc(int type, bool bn, int M, int N) {
+    return (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | (bn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ int swz128(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
+
+template <bool E4M3, int HD>
+struct RowShape {
+    static constexpr int CG = rows_pair(HD), NQ = 2 / CG;          // CTAs of a worker, row tiles of a CTA
+    static constexpr int KP = kPosTile / CG, VD = HD / CG;         // positions of K, dimensions of V in this CTA
+    static constexpr int QB = 128 * HD * 2;                        // bytes of a row tile
+    static constexpr int SLOTB = rows_slot_bytes(HD), RAWB = SLOTB / 2;
+    static constexpr int SW = 4 * NQ;                              // softmax warps
+    static constexpr int STAGE = SW, CONV = SW + 4, PROD = SW + 4 + (E4M3 ? 4 : 0), MMA = PROD + 1;
+    static constexpr int THREADS = (MMA + 1) * 32;
+    static constexpr int O0 = 256, OC = HD;                        // accumulators' columns, behind two score buffers of 128
+    // a probability is 2^(z - m), at most 2^kSlack; in fp16 times 2^kBias
+    static constexpr float kSlack = E4M3 ? 4.f : 8.f, kBias = E4M3 ? 11.f : 0.f;
+    // place of V tile k and K tile k among a piece's n tile pairs
+    static __device__ __forceinline__ unsigned v_at(int k, int n) { return CG == 1 ? 2 * k + 1 : k == n - 1 ? 2 * n - 1 : 2 * k + 2; }
+};
+
+template <bool E4M3, int HD>
+__global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcParams pp, int NS) {
+    using S = RowShape<E4M3, HD>;
+    constexpr int CG = S::CG, NQ = S::NQ, NR = rows_raw(E4M3, HD);
+    const RowsTcArgs& t = pp.t;
+    const RowsArgs& a = t.a;
+    extern __shared__ unsigned char raw_smem[];
+    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+    unsigned char* sQ = base;
+    unsigned char* ring = sQ + NQ * S::QB;
+    unsigned char* raw = ring + (size_t)NS * S::SLOTB;
+    uint4* m_bits = reinterpret_cast<uint4*>(raw + (size_t)NR * S::RAWB);       // [kRowsMeta] positions that are there
+    float2* m_sc = reinterpret_cast<float2*>(m_bits + kRowsMeta);               // [kRowsMeta][8] key scale, value scale's exponent, every 16 positions
+    int4* m_flag = reinterpret_cast<int4*>(m_sc + kRowsMeta * 8);               // [kRowsMeta] x: all positions there
+    float* s_hi = reinterpret_cast<float*>(m_flag + kRowsMeta);                 // rotation table
+    float* s_lo = s_hi + HD / 2;
+    float* s_c = s_lo + HD / 2;                                                 // [2][kRowTile] e4m3: a query row's scale, by pieces in turn
+    unsigned long long* bars = reinterpret_cast<unsigned long long*>(s_c + 2 * kRowTile);
+    unsigned long long *full = bars, *empty = full + kRowsSlots, *peer = empty + kRowsSlots, *rfull = peer + kRowsSlots,
+                       *rempty = rfull + kRowsRaw, *meta = rempty + kRowsRaw, *s_full = meta + kRowsMeta, *p_full = s_full + 2,
+                       *pv_done = p_full + 2, *o_free = pv_done + 2, *q_full = o_free + 2, *q_free = q_full + 1, *end_bar = q_free + 1;
+    long long* tmp = reinterpret_cast<long long*>(bars + 3 * kRowsSlots + 2 * kRowsRaw + kRowsMeta + 16);   // [64]
+    long long* s_pre = tmp + 64;
+    int* s_cum = reinterpret_cast<int*>(s_pre + rows_blocks(a) + 1);
+    __shared__ unsigned int s_tmem;
+    __shared__ int s_bad;
+    __shared__ volatile int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int rank = CG == 1 ? 0 : (int)cta_rank(), me = (int)blockIdx.x / CG;
+    if (tid == 0) {
+        for (int i = 0; i < kRowsSlots; ++i) {
+            mbar_init(full + i, E4M3 ? 4 : 1);
+            mbar_init(empty + i, 1);
+            mbar_init(peer + i, 1);
+        }
+        for (int i = 0; i < kRowsRaw; ++i) {
+            mbar_init(rfull + i, 1);
+            mbar_init(rempty + i, 4);
+        }
+        for (int i = 0; i < kRowsMeta; ++i) mbar_init(meta + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4 * CG);
+            mbar_init(pv_done + i, 1);
+            mbar_init(o_free + i, 4 * CG);
+        }
+        mbar_init(q_full, 4 * CG);
+        mbar_init(q_free, 1);
+        mbar_init(end_bar, 1);
+        s_bad = 0;
+        s_abort = 0;
+    }
+    mbar_fence_init();
+    if (a.rope.on)
+        for (int i = tid; i < HD / 2; i += S::THREADS) {
+            s_hi[i] = a.rope.hi[i];
+            s_lo[i] = a.rope.lo[i];
+        }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    RowsPlan plan;
+    const bool good = make_plan<S::THREADS>(t, plan, s_pre, s_cum, tmp);
+    if (CG == 2) pair_sync();   // the peer's barriers stand
+    if (warp == S::MMA) alloc_columns<CG>(&s_tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+    if (blockIdx.x == 0 && !good) s_bad = 1;
+    if (blockIdx.x == 0) {   // what the merge needs of the plan
+        if (tid == 0) *t.plan_head = make_int2(plan.open, plan.workers);
+        for (int i = tid; i <= rows_blocks(a); i += S::THREADS) t.plan_pre[i] = s_pre[i];
+        if (a.n_groups > 0)
+            for (int i = tid; i <= a.B; i += S::THREADS) t.plan_cum[i] = s_cum[i];
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long T = s_pre[rows_blocks(a)];
+    const long long xs = me < plan.workers ? share_at(T, plan.workers, me) : T, xe = me < plan.workers ? share_at(T, plan.workers, me + 1) : T;
+    // bounded wait; after one gave up every other does too
+    auto wait = [&](unsigned long long* bar, unsigned int parity) -> bool {
+        if (try_wait<CG>(bar, parity)) return true;
+        const unsigned long long t0 = global_ns();
+        while (!try_wait<CG>(bar, parity)) {
+            if (s_abort) return false;
+            if (global_ns() - t0 > t.timeout_ns) {
+                s_abort = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+    auto wait_all = [&](unsigned long long* bar, unsigned int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    // the next piece with tiles in it at x or behind; x moves to the item behind it
+    auto next_piece = [&](long long& x, Piece& p) -> bool {
+        while (x < xe) {
+            p = piece_at(t, plan, x, xs, xe);
+            x = p.next;
+            if (p.n > 0) return true;
+        }
+        return false;
+    };
+    const int ps = 1 << a.c.ps_log2;
+    const uint32_t idS = idesc(E4M3 ? 0 : 1, false, 128 * CG, kPosTile), idO = idesc(E4M3 ? 0 : 1, true, 128 * CG, HD);
+
+    if (warp == S::PROD) {
+        // ------------------------------------------------------------------
+        // producer: K and V tiles in the order the MMAs take them; lane i of a tile
+        // holds page i of its positions
+        // ------------------------------------------------------------------
+        const int vl = a.c.ps_log2 < 7 ? a.c.ps_log2 : 7, kl = vl < (CG == 2 ? 6 : 7) ? vl : (CG == 2 ? 6 : 7);   // box rows (log2)
+        const int vr = 1 << vl, nv = kPosTile >> vl, kr = 1 << kl, nk = S::KP >> kl;
+        constexpr int KB = E4M3 ? (HD < 128 ? 64 : 128) : 64;   // dimensions of a box
+        constexpr int ESZ = E4M3 ? 1 : 2;
+        const int SLOTS = E4M3 ? NR : NS;
+        unsigned char* dst0 = E4M3 ? raw : ring;
+        constexpr int DSTB = E4M3 ? S::RAWB : S::SLOTB;
+        unsigned long long *bf = E4M3 ? rfull : full, *be = E4M3 ? rempty : empty;
+        unsigned slot = 0, phase = 0, ti = 0;
+        bool ok = true, bad = false;
+        int4 note = make_int4(-1, 0, 0, 0);
+        Piece p;
+        long long x = xs;
+        while (ok && next_piece(x, p)) {
+            const int* tab = a.c.table + (long long)p.k.b0 * a.c.max_pages;
+            const int end = p.k.group ? p.k.hi : p.it.p_last + 1;
+            const int wlo = a.c.window > 0 && p.it.p_first + 1 > a.c.window ? p.it.p_first + 1 - a.c.window : 0;
+            const int wfar = a.c.window > 0 && p.it.p_last + 1 > a.c.window ? p.it.p_last + 1 - a.c.window : 0;
+            const int sink = a.c.sink < wfar ? a.c.sink : wfar;
+            auto entry = [&](int k) -> int {   // page of this lane's positions of tile k; below 0: not loaded
+                if (k >= p.n || lane >= nv) return -2;
+                const int p0 = tile_of(p.it, p.t0 + k) * kPosTile + (lane << vl);
+                if (p0 >= end || p0 + vr <= p.k.lo || (p0 + vr <= wlo && p0 >= sink)) return -2;
+                const int pg = tab[p0 >> a.c.ps_log2];
+                if ((unsigned)pg < (unsigned)a.c.n_pages) return pg;
+                bad = true;
+                return -1;
+            };
+            auto load = [&](bool key, int tile, int pg) {
+                ok = wait_all(be + slot, phase ^ 1);
+                if (!ok) return;
+                unsigned char* dst = dst0 + (size_t)slot * DSTB;
+                const int pos = tile * kPosTile;
+                if (key) {
+                    const int off = rank * S::KP + (lane << kl);      // this lane's first position in the tile
+                    const int kp = __shfl_sync(0xffffffffu, pg, (off >> vl) & 31);
+                    const bool mine = lane < nk && kp >= 0;
+                    const unsigned cnt = __popc(__ballot_sync(0xffffffffu, mine));
+                    if (lane == 0) mbar_arrive_expect_tx(bf + slot, cnt * (unsigned)(kr * HD * ESZ));
+                    __syncwarp();
+                    if (mine)
+#pragma unroll
+                        for (int c = 0; c < HD / KB; ++c)
+                            tma_4d(dst + c * (S::KP * KB * ESZ) + (lane << kl) * (KB * ESZ), &pp.tk, c * KB, (pos + off) & (ps - 1), p.g, kp, bf + slot);
+                } else {
+                    const bool mine = lane < nv && pg >= 0;
+                    const unsigned cnt = __popc(__ballot_sync(0xffffffffu, mine));
+                    if (lane == 0) mbar_arrive_expect_tx(bf + slot, cnt * (unsigned)(vr * S::VD * ESZ));
+                    __syncwarp();
+                    if (mine)
+#pragma unroll
+                        for (int c = 0; c < S::VD / KB; ++c)
+                            tma_4d(dst + c * (kPosTile * KB * ESZ) + (lane << vl) * (KB * ESZ), &pp.tv, rank * S::VD + c * KB,
+                                   (pos + (lane << vl)) & (ps - 1), p.g, pg, bf + slot);
+                }
+                if (++slot == (unsigned)SLOTS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            };
+            int npg = entry(0), held = -2, held_tile = 0;
+            for (int k = 0; k <= p.n && ok; ++k) {
+                const int pg = npg, tile = k < p.n ? tile_of(p.it, p.t0 + k) : 0;
+                npg = entry(k + 1);
+                if (k < p.n) {
+                    load(true, tile, pg);
+                    // the tile's masks and scales, while its keys are on their way
+                    bool there = pg >= 0;
+                    float ks = 1.f, ev = 0.f;
+                    if (E4M3 && there) {
+                        const long long o = (long long)pg * a.c.Hkv + p.g;
+                        const float kss = a.c.ks[o], vss = a.c.vs[o];
+                        there = scale_ok(kss) && scale_ok(vss);   // else the page counts as absent
+                        bad = bad || !there;
+                        ks = there ? kss : 0.f;
+                        ev = there ? (float)((int)(__float_as_uint(vss) >> 23) - 127) : 0.f;
+                    }
+                    // lane i < 8: positions [16 i, 16 i + 16)
+                    const int src = lane < 8 ? (lane << 4) >> vl : 0;
+                    const bool th = __shfl_sync(0xffffffffu, (int)there, src) != 0;
+                    const float k8 = __shfl_sync(0xffffffffu, ks, src), e8 = __shfl_sync(0xffffffffu, ev, src);
+                    const unsigned have = __ballot_sync(0xffffffffu, lane < 8 && th) & 0xFFu;
+                    const unsigned mi = ti % kRowsMeta;
+                    if (lane < 8 && E4M3) m_sc[mi * 8 + lane] = make_float2(k8, e8);
+                    if (lane == 0) {
+                        auto word = [&](int i) { return ((have >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((have >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u); };
+                        m_bits[mi] = make_uint4(word(0), word(1), word(2), word(3));
+                        m_flag[mi] = make_int4(have == 0xFFu, 0, 0, 0);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(meta + mi);
+                    ++ti;
+                }
+                if (CG == 1) {
+                    if (k < p.n && ok) load(false, tile, pg);
+                } else {
+                    if (k > 0 && ok) load(false, held_tile, held);
+                    held = pg;
+                    held_tile = tile;
+                }
+            }
+            if (p.slot == 2 && p.t0 == 0)
+                note = make_int4(p.blk, p.g, p.rt, worker_of(T, plan.workers, p.it.tiles_at + (long long)(p.it.n - 1) * kPosTile * a.G));
+        }
+        if (rank == 0 && lane == 0 && a.M == 0) t.note[me] = note;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
+        if (!ok) {   // gave up: this warp's copies in flight end before the CTA does
+            const unsigned long long t0 = global_ns();
+            for (int i = 0; i < SLOTS; ++i) {
+                const unsigned ph = i < (int)slot ? phase : phase ^ 1;
+                while (!try_wait<CG>(bf + i, ph) && global_ns() - t0 < t.timeout_ns) {}
+            }
+        }
+    } else if (E4M3 && warp >= S::CONV && warp < S::CONV + 4) {
+        // ------------------------------------------------------------------
+        // codes to fp16: a thread opens 16 of them at a time
+        // ------------------------------------------------------------------
+        const int ct = tid - S::CONV * 32;
+        unsigned slot = 0, phase = 0, rs = 0, rp = 0;
+        bool ok = true;
+        Piece p;
+        long long x = xs;
+        while (ok && next_piece(x, p)) {
+            for (int i = 0; i < 2 * p.n && ok; ++i) {
+                // K tiles and V tiles take turns: K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. Kn-1 Vn-2 Vn-1
+                const bool key = CG == 1 ? (i & 1) == 0 : i == 0 || ((i & 1) != 0 && i != 2 * p.n - 1);
+                ok = wait_all(rfull + rs, rp);
+                ok = ok && wait_all(empty + slot, phase ^ 1);
+                if (!ok) break;
+                const unsigned char* src = raw + (size_t)rs * S::RAWB;
+                unsigned char* dst = ring + (size_t)slot * S::SLOTB;
+                // raw: boxes of CW codes a row (swizzled), K: KP rows x HD, V: 128 rows x VD; both RAWB bytes
+                constexpr int CW = HD < 128 ? 64 : 128;
+                const int rows = key ? S::KP : kPosTile;
+#pragma unroll
+                for (int c0 = 0; c0 < S::RAWB / 16; c0 += 128) {
+                    const int c = c0 + ct, box = c / (rows * (CW / 16)), in = c % (rows * (CW / 16)), r = in / (CW / 16), ch = in % (CW / 16);
+                    const int at = box * rows * CW + (CW == 128 ? swz128(r, ch) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + at);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] & 0xFFFFu), __NV_E4M3);
+                        const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] >> 16), __NV_E4M3);
+                        o[2 * e] = (uint32_t)h0.x | (uint32_t)h0.y << 16;
+                        o[2 * e + 1] = (uint32_t)h1.x | (uint32_t)h1.y << 16;
+                    }
+                    const int d = box * CW + ch * 16;   // first dimension
+                    unsigned char* q = dst + (d >> 6) * rows * 128;
+                    *reinterpret_cast<uint4*>(q + swz128(r, (d & 63) >> 3)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(q + swz128(r, ((d & 63) >> 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(full + slot);
+                    mbar_arrive(rempty + rs);
+                }
+                if (++slot == (unsigned)NS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                if (++rs == (unsigned)NR) {
+                    rs = 0;
+                    rp ^= 1;
+                }
+            }
+        }
+    } else if (warp == S::MMA) {
+        // ------------------------------------------------------------------
+        // MMA issue: the whole warp walks, one elected lane issues; the second CTA
+        // of a pair tells the first what has come in
+        // ------------------------------------------------------------------
+        unsigned slot = 0, phase = 0, seg = 0;
+        bool ok = true;
+        auto hold = [&](unsigned long long* bar, unsigned parity) {
+            ok = ok && wait_all(bar, parity);
+            tc_fence_after();
+        };
+        auto next = [&] {
+            if (++slot == (unsigned)NS) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        Piece p;
+        long long x = xs;
+        if (CG == 2 && rank == 1) {
+            while (ok && next_piece(x, p))
+                for (int i = 0; i < 2 * p.n && ok; ++i) {
+                    hold(full + slot, phase);
+                    if (ok && lane == 0) arrive_lead<CG>(peer + slot);
+                    __syncwarp();
+                    next();
+                }
+        } else {
+            const uint32_t q0 = smem_addr(sQ) >> 4, r0 = smem_addr(ring) >> 4;
+            unsigned tq[2] = {0u, 0u}, sq[2] = {0u, 0u};   // tiles and pieces of a row tile so far
+            auto arrived = [&] {
+                hold(full + slot, phase);
+                if (CG == 2) hold(peer + slot, phase);
+            };
+            auto scores = [&](int q, int buf) {
+                const uint32_t al = q0 + q * (S::QB >> 4) + lead_bits(16), bl = r0 + slot * (S::SLOTB >> 4) + lead_bits(16);
+                if (ok && elect()) {
+#pragma unroll
+                    for (int b = 0; b < HD / 64; ++b)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_ss<CG>(tmem + buf * 128, al + (b * 128 * 128 + ks * 32 >> 4), bl + (b * S::KP * 128 + ks * 32 >> 4), kDescHi, idS,
+                                        b > 0 || ks > 0);
+                    commit<CG>(s_full + buf);
+                }
+                __syncwarp();
+            };
+            auto values = [&](int q, int buf, bool first) {
+                const uint32_t bl = r0 + slot * (S::SLOTB >> 4) + lead_bits(S::VD > 64 ? kPosTile * 128 : 16);
+                if (ok && elect()) {
+#pragma unroll
+                    for (int ks = 0; ks < kPosTile / 16; ++ks)
+                        umma_ts<CG>(tmem + S::O0 + q * S::OC, tmem + buf * 128 + ks * 8, bl + (ks * 16 * 128 >> 4), kDescHi, idO, !first || ks > 0);
+                    commit<CG>(pv_done + buf);   // (a pair's tiles take turns, as a wait may be two tiles behind)
+                }
+                __syncwarp();
+            };
+            auto done = [&] {   // the slot may be filled again
+                if (ok && elect()) commit<CG>(empty + slot);
+                __syncwarp();
+                next();
+            };
+            while (ok && next_piece(x, p)) {
+                hold(q_full, seg & 1);
+                ++seg;
+                if (CG == 2) {
+                    const unsigned t0 = tq[0];
+                    for (int k = 0; k <= p.n && ok; ++k) {
+                        if (k < p.n) {
+                            arrived();
+                            scores(0, (t0 + k) & 1);
+                            done();
+                            if (k == p.n - 1 && ok && elect()) commit<CG>(q_free);
+                            __syncwarp();
+                        }
+                        if (k > 0) {
+                            const unsigned u = t0 + k - 1;
+                            if (k == 1) hold(o_free, (sq[0] & 1) ^ 1);
+                            hold(p_full + (u & 1), (u >> 1) & 1);
+                            arrived();
+                            values(0, u & 1, k == 1);
+                            done();
+                        }
+                    }
+                    tq[0] += p.n;
+                    ++sq[0];
+                } else {
+                    const int nq = p.it.rows > 128 ? 2 : 1;
+                    // slots take turns: K tile k, V tile k
+                    unsigned vslot = 0, vphase = 0;
+                    for (int k = 0; k <= p.n && ok; ++k) {
+                        const bool more = k < p.n;
+                        if (more) arrived();
+                        if (k > 0) {
+                            ok = ok && wait_all(full + vslot, vphase);
+                            tc_fence_after();
+                        }
+                        for (int q = 0; q < nq && ok; ++q) {
+                            if (k > 0) {
+                                if (k == 1) hold(o_free + q, (sq[q] & 1) ^ 1);
+                                hold(p_full + q, (tq[q] + k - 1) & 1);
+                                const unsigned ks = slot;
+                                slot = vslot;
+                                values(q, q, k == 1);
+                                slot = ks;
+                            }
+                            if (more) scores(q, q);
+                        }
+                        if (k > 0 && ok && elect()) commit<CG>(empty + vslot);
+                        __syncwarp();
+                        if (more) {
+                            done();
+                            if (k == p.n - 1 && ok && elect()) commit<CG>(q_free);
+                            __syncwarp();
+                            vslot = slot;
+                            vphase = phase;
+                            next();
+                        }
+                    }
+                    for (int q = 0; q < nq; ++q) {
+                        tq[q] += p.n;
+                        ++sq[q];
+                    }
+                }
+            }
+            if (elect()) commit<CG>(end_bar);   // whatever was issued has ended before its memory goes
+            __syncwarp();
+        }
+        const unsigned long long t0 = global_ns();
+        while (!try_wait<CG>(end_bar, 0) && global_ns() - t0 < 2 * t.timeout_ns) {}
+        __syncwarp();
+    } else if (warp >= S::STAGE && warp < S::STAGE + 4) {
+        // ------------------------------------------------------------------
+        // queries: norm, rotation, scale, one rounding; a thread has one unit of
+        // consecutive rows, so the heads of a token share its angles
+        // ------------------------------------------------------------------
+        constexpr int U = HD / 16, PER = NQ * U, NB = 4;   // units of a row, rows of a thread, rows in flight
+        const int st = tid - S::STAGE * 32, c = st % U, rq = (st / U) * PER;
+        unsigned seg = 0;
+        bool ok = true;
+        Piece p;
+        long long x = xs;
+        while (ok && next_piece(x, p)) {
+            const int r0 = p.it.r0 + rank * 128, left = p.it.rows - rank * 128;   // this CTA's rows
+            uint4 u[NB][2];
+            int pos[NB];
+            auto fetch = [&](int i0) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int r = rq + i0 + i;
+                    pos[i] = -1;
+                    u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
+                    if (r < left) {
+                        const RowPlace w = row_place(a, s_cum, p.k, p.g, r0 + r);
+                        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + w.q + 8 * c;
+                        u[i][0] = ld_stream16(src);
+                        u[i][1] = ld_stream16(src + HD / 2);
+                        pos[i] = w.pos;
+                    }
+                }
+            };
+            fetch(0);
+            ok = wait_all(q_free, (seg & 1) ^ 1);
+            if (!ok) break;
+            float cs[8], sn[8];
+            int have = -1;
+#pragma unroll 1
+            for (int i0 = 0; i0 < PER; i0 += NB) {
+                if (i0 > 0) fetch(i0);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int r = rq + i0 + i;
+                    float v[8], w[8];
+                    open_unit(u[i][0], v);
+                    open_unit(u[i][1], w);
+                    if (a.rope.on && pos[i] >= 0 && pos[i] != have) {
+                        unit_angles<true>((long long)pos[i], s_hi + 8 * c, s_lo + 8 * c, cs, sn);
+                        have = pos[i];
+                    }
+                    if (a.q_norm) unit_norm(v, w, a.q_norm, c, HD, a.eps);
+                    if (a.rope.on && pos[i] >= 0) unit_rotate(v, w, cs, sn);
+                    float f = a.scale;
+                    if (E4M3) {   // the largest of the row into [128, 256): no bits lost to fp16's range
+                        float big = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(v[e]), fabsf(w[e])));
+                        for (int o = U >> 1; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                        int x2 = (int)(__float_as_uint(big * a.scale) >> 23) - 127 - 7;
+                        x2 = x2 < -100 ? -100 : x2 > 100 ? 100 : x2;
+                        f *= __uint_as_float((uint32_t)(127 - x2) << 23);
+                        if (c == 0) s_c[(seg & 1) * kRowTile + r] = __uint_as_float((uint32_t)(127 + x2) << 23);
+                    }
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[e] = E4M3 ? pack_f16(v[2 * e] * f, v[2 * e + 1] * f) : pack_bf16(v[2 * e] * f, v[2 * e + 1] * f);
+                        o[4 + e] = E4M3 ? pack_f16(w[2 * e] * f, w[2 * e + 1] * f) : pack_bf16(w[2 * e] * f, w[2 * e + 1] * f);
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int d = half * (HD / 2) + 8 * c;
+                        *reinterpret_cast<uint4*>(sQ + (r >> 7) * S::QB + (d >> 6) * 128 * 128 + swz128(r & 127, (d & 63) >> 3)) =
+                            make_uint4(o[4 * half], o[4 * half + 1], o[4 * half + 2], o[4 * half + 3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_lead<CG>(q_full);
+            ++seg;
+        }
+    } else {
+        // ------------------------------------------------------------------
+        // softmax and epilogue: thread = row
+        // ------------------------------------------------------------------
+        const int q = warp >> 2, row = tid & 127;            // row tile of this CTA, row of it
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        unsigned tc = 0, ti = 0, g0 = 0, seg = 0;            // tiles of this row tile, of the CTA; ring slots and pieces before this one
+        // tile i of this row tile is in the accumulator
+        auto meet_values = [&](unsigned i) {
+            wait(pv_done + (CG == 2 ? i & 1 : q), CG == 2 ? (i >> 1) & 1 : i & 1);
+            __syncwarp();
+            tc_fence_after();
+        };
+        auto meet = [&](unsigned long long* bar, unsigned parity) {
+            wait(bar, parity);
+            __syncwarp();
+        };
+        Piece p;
+        long long x = xs;
+        for (; next_piece(x, p); ++seg) {
+            const int ofs = (CG == 2 ? rank : q) * 128;      // of the row tile in the item
+            if (CG == 1 && p.it.rows <= ofs) {               // not there: the other row tile's alone
+                for (int k = 0; k < p.n; ++k, ++ti) meet(meta + ti % kRowsMeta, (ti / kRowsMeta) & 1);   // (in step with the phases)
+                g0 += 2 * p.n;
+                continue;
+            }
+            const bool live = ofs + row < p.it.rows;
+            const RowPlace w = row_place(a, s_cum, p.k, p.g, p.it.r0 + (live ? ofs + row : p.it.rows - 1));
+            const int end = p.k.group ? p.k.hi : w.pos + 1;   // attends [.., end)
+            float m = kNoScore, l = 0.f, qc = 1.f;
+            for (int k = 0; k < p.n; ++k) {
+                const int buf = CG == 2 ? (int)(tc & 1) : q;
+                const uint32_t sat = tmem + lanes + buf * 128;
+                const int t0 = tile_of(p.it, p.t0 + k) * kPosTile;
+                const unsigned mi = ti % kRowsMeta;
+                meet(meta + mi, (ti / kRowsMeta) & 1);
+                const bool all = m_flag[mi].x != 0;
+                // every row of the item attends every position of the tile
+                const bool whole = all && t0 >= p.k.lo && (p.k.group ? t0 + kPosTile <= p.k.hi : t0 + kPosTile - 1 <= p.it.p_first) &&
+                                   (a.c.window == 0 || t0 > p.it.p_last - a.c.window || t0 + kPosTile <= a.c.sink);
+                uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+                if (!whole) {
+                    const uint4 b = m_bits[mi];
+                    bits[0] = b.x; bits[1] = b.y; bits[2] = b.z; bits[3] = b.w;
+                    const int low = a.c.window > 0 && w.pos + 1 > a.c.window ? w.pos + 1 - a.c.window : 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c0 = t0 + 32 * i;
+                        auto below = [&](int e) { return e - c0 >= 32 ? ~0u : e - c0 <= 0 ? 0u : (1u << (e - c0)) - 1u; };   // positions < e
+                        uint32_t on = below(end) & ~below(p.k.lo);
+                        if (low > 0) on &= ~below(low) | below(a.c.sink);
+                        bits[i] &= on;
+                    }
+                }
+                meet(s_full + buf, CG == 2 ? (tc >> 1) & 1 : tc & 1);
+                tc_fence_after();
+                if (E4M3 && k == 0) qc = s_c[(seg & 1) * kRowTile + (CG == 2 ? 0 : ofs) + row];
+                // ---- the row's largest score of the tile ----
+                float mx = -__int_as_float(0x7F800000);
+                auto score = [&](const uint32_t (&r)[32], int c, float (&z)[32]) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(r[i]);
+                    if (E4M3) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float2 sc = m_sc[mi * 8 + 2 * c + h];
+                            sc.x *= qc;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 y = fma2(make_float2(z[16 * h + i], z[16 * h + i + 1]), make_float2(sc.x, sc.x), make_float2(sc.y, sc.y));
+                                z[16 * h + i] = y.x;
+                                z[16 * h + i + 1] = y.y;
+                            }
+                        }
+                    }
+                    if (!whole)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) z[i] = bits[c] >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
+                };
+                {
+                    uint32_t r[2][32];
+                    ld32(sat, r[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_wait();
+                        if (c < 3) ld32(sat + 32 * (c + 1), r[(c + 1) & 1]);
+                        float z[32];
+                        score(r[c & 1], c, z);
+                        float y = -__int_as_float(0x7F800000);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            mx = max3(mx, z[i], z[i + 1]);
+                            y = max3(y, z[i + 2], z[i + 3]);
+                        }
+                        mx = fmaxf(mx, y);
+                    }
+                }
+                if (__any_sync(0xffffffffu, mx > m + S::kSlack)) {
+                    // move the references, and with them what has been summed
+                    const float mn = fmaxf(mx, m), f = ex2(m - mn);
+                    l *= f;
+                    m = mn;
+                    if (k > 0) {
+                        meet_values(tc - 1);
+#pragma unroll 1
+                        for (int c = 0; c < HD; c += 32) {
+                            uint32_t r[32];
+                            ld32(tmem + lanes + S::O0 + q * S::OC + c, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                            st32(tmem + lanes + S::O0 + q * S::OC + c, r);
+                        }
+                        st_wait();
+                        tc_fence_before();
+                    }
+                }
+                // ---- probabilities, over the scores ----
+                {
+                    uint32_t r[2][32];
+                    ld32(sat, r[0]);
+                    const float2 neg = make_float2(S::kBias - m, S::kBias - m);
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_wait();
+                        if (c < 3) ld32(sat + 32 * (c + 1), r[(c + 1) & 1]);
+                        float z[32];
+                        score(r[c & 1], c, z);
+                        uint32_t o[16];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+                                float2 e = add2(make_float2(z[i], z[i + 1]), neg);
+                                e.x = ex2(e.x);
+                                e.y = ex2(e.y);
+                                if (E4M3) part = add2(part, e);
+                                else sum = add2(sum, e);
+                                o[i >> 1] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                            }
+                            if (E4M3) {   // without the value scale
+                                const float un = ex2(-m_sc[mi * 8 + 2 * c + h].y);
+                                sum = fma2(part, make_float2(un, un), sum);
+                            }
+                        }
+                        st16(sat + 16 * c, o);
+                    }
+                    l += sum.x + sum.y;
+                }
+                if (!whole && q == 0) {
+                    // value rows that no row of the item attends may hold anything: zero
+                    // them (this thread's position; a weight of zero would make a NaN of it)
+                    const uint4 b = m_bits[mi];
+                    const int pos = t0 + row;
+                    const uint32_t word = row < 32 ? b.x : row < 64 ? b.y : row < 96 ? b.z : b.w;
+                    const int last = p.k.group ? p.k.hi : p.it.p_last + 1;
+                    const bool any = (word >> (row & 31) & 1u) && pos >= p.k.lo && pos < last &&
+                                     (a.c.window == 0 || pos > p.it.p_first - a.c.window || pos < a.c.sink);
+                    if (!__all_sync(0xffffffffu, any)) {
+                        const unsigned v = g0 + S::v_at(k, p.n);
+                        meet(full + v % (unsigned)NS, (v / (unsigned)NS) & 1);
+                        if (!any) {
+                            unsigned char* at = ring + (size_t)(v % (unsigned)NS) * S::SLOTB;
+#pragma unroll 1
+                            for (int c = 0; c < S::VD / 64; ++c)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    *reinterpret_cast<uint4*>(at + c * kPosTile * 128 + swz128(row, i)) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_lead<CG>(p_full + buf);
+                ++tc;
+                ++ti;
+            }
+            g0 += 2 * p.n;
+            // ---- the accumulator ----
+            meet_values(tc - 1);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool out = p.slot == 0 && a.M == 0;        // the row's whole result
+            float* part = nullptr;
+            if (!out && live) {
+                if (p.slot == 0) {
+                    const long long r = (p.k.group ? 0 : (long long)a.B * a.M * a.Hq) + w.out;
+                    part = t.dense + r * HD;
+                    t.dense_ml[r] = make_float2(m, l);
+                } else {
+                    const long long r = (2ll * me + p.slot - 1) * kRowTile + ofs + row;
+                    part = t.part + r * HD;
+                    t.part_ml[r] = make_float2(m, l);
+                }
+            }
+            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + w.out * HD;
+            float odd = 0.f;   // NaN: the product left something that is not finite
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 32) {
+                uint32_t r[32];
+                ld32(tmem + lanes + S::O0 + q * S::OC + c, r);
+                tmem_ld_wait();
+                if (!live) {
+                } else if (out) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            v[e] = __uint_as_float(r[i + e]) * inv;
+                            odd = fmaf(v[e], 0.f, odd);
+                        }
+                        store8(dst + c + i, v);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(part + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                }
+                __syncwarp();
+            }
+            if (a.M == 0 && live) t.odd[w.out] = out && !(odd == 0.f);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_lead<CG>(o_free + q);
+        }
+    }
+    __syncthreads();
+    if (tid == 0) t.cta_status[blockIdx.x] = s_abort ? MTP_ERR_TIMEOUT : s_bad ? MTP_ERR_ARG : MTP_OK;
+    if (CG == 2) pair_sync();   // nothing of the peer's is on its way here
+    if (warp == S::MMA) free_columns<CG>(tmem, 512);
+}
+
+template <bool E4M3, int HD>
+cudaError_t go(const RowsTcParams& p, cudaStream_t s) {
+    using S = RowShape<E4M3, HD>;
+    static int ready[64] = {0};   // the attribute is set, per device
+    const int NS = rows_slots(E4M3, HD, p.t.a.B, p.t.a.n_groups);
+    const int smem = NS * S::SLOTB + S::NQ * S::QB + rows_raw(E4M3, HD) * S::RAWB + rows_other(HD, p.t.a.B, p.t.a.n_groups);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || ready[dev] == 0) {
+        e = cudaFuncSetAttribute(rows_tc_kernel<E4M3, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmemLimit);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) ready[dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.t.workers * S::CG));
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up while the kernel before it ends
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = S::CG;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = S::CG == 1 ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, rows_tc_kernel<E4M3, HD>, p, NS);
+}
+
+}  // namespace
+
+#ifdef MTP_PAGED_E4M3
+cudaError_t launch_rows_tc_e4m3(const RowsTcParams& p, cudaStream_t s) {
+    constexpr bool E = true;
+#else
+cudaError_t launch_rows_tc_bf16(const RowsTcParams& p, cudaStream_t s) {
+    constexpr bool E = false;
+#endif
+    switch (p.t.a.hd) {
+    case 64: return go<E, 64>(p, s);
+    case 128: return go<E, 128>(p, s);
+    case 256: return go<E, 256>(p, s);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace mtp
