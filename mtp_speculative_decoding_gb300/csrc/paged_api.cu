@@ -110,6 +110,16 @@ bool encode_pages(CUtensorMap* m, const void* base, const mtp_kv_cache* c, int r
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// (dimension, row) map of staged rows of 16-bit values: boxes of a 128-byte column by 128 rows
+bool encode_rows(CUtensorMap* m, void* base, int hd, int64_t rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)hd * 2};
+    const cuuint32_t box[2] = {64, 128}, one[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct AttnPlan {
     bool tc;
     int RT, tile_log2, grid;
@@ -143,7 +153,7 @@ bool rows_tc(const mtp_kv_cache* c) {
     return c->kv_dtype != MTP_DTYPE_F32 && (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256);
 }
 struct RowsSpace {
-    size_t status, note, head, pre, cum, odd, part, part_ml, dense, dense_ml, end;
+    size_t status, note, head, worker, blocks, staged, q_scale, odd, part, part_ml, dense, dense_ml, end;
     int workers;
 };
 // (every field grows with B, M and T, so that a workspace sized for more serves less)
@@ -159,13 +169,15 @@ RowsSpace rows_space(const mtp_kv_cache* c, int B, int M, int64_t T, int n_q_hea
     if (rows_tc(c)) {
         const size_t rows = (size_t)T * n_q_heads;
         p.workers = sms / rows_pair(hd);
-        p.status = take((size_t)sms * sizeof(int));
+        p.status = take(((size_t)sms + 1) * sizeof(int));
         p.note = take((size_t)p.workers * sizeof(int4));
-        p.head = take(sizeof(int2));
-        p.pre = take((2 * (size_t)B + 1) * sizeof(long long));
-        p.cum = take(((size_t)B + 1) * sizeof(int));
+        p.head = take(sizeof(PlanHead));
+        p.worker = take((size_t)p.workers * sizeof(WorkerRec));
+        p.blocks = take(2 * (size_t)B * sizeof(BlockRec));
         p.part_ml = take(2 * (size_t)p.workers * kRowTile * sizeof(float2));
         p.part = take(2 * (size_t)p.workers * kRowTile * hd * sizeof(float));
+        p.staged = take(rows * hd * 2);
+        p.q_scale = take(rows * sizeof(float));
         if (M > 0) {
             p.dense_ml = take(2 * rows * sizeof(float2));
             p.dense = take(2 * rows * hd * sizeof(float));
@@ -222,9 +234,11 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
     t.window_units = U * ((a.c.sink + (long long)kPosTile - 1) / kPosTile + (a.c.window + (kRowTile - 1) / a.G) / kPosTile + 2);
     t.cta_status = reinterpret_cast<int*>(base + p.status);
     t.note = reinterpret_cast<int4*>(base + p.note);
-    t.plan_head = reinterpret_cast<int2*>(base + p.head);
-    t.plan_pre = reinterpret_cast<long long*>(base + p.pre);
-    t.plan_cum = reinterpret_cast<int*>(base + p.cum);
+    t.head = reinterpret_cast<PlanHead*>(base + p.head);
+    t.worker = reinterpret_cast<WorkerRec*>(base + p.worker);
+    t.blocks = reinterpret_cast<BlockRec*>(base + p.blocks);
+    t.staged = reinterpret_cast<uint16_t*>(base + p.staged);
+    t.q_scale = reinterpret_cast<float*>(base + p.q_scale);
     t.part = reinterpret_cast<float*>(base + p.part);
     t.part_ml = reinterpret_cast<float2*>(base + p.part_ml);
     t.odd = reinterpret_cast<uint8_t*>(base + p.odd);
@@ -232,8 +246,11 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
     t.dense_ml = reinterpret_cast<float2*>(base + p.dense_ml);
     t.timeout_ns = kWaitLimitNs;
     // (a stride beyond 2^40 bytes has no map)
-    if (!encode_pages(&pp.tk, c->k, c, kPosTile / rows_pair(c->head_dim)) || !encode_pages(&pp.tv, c->v, c, kPosTile)) return MTP_ERR_UNSUPPORTED;
+    if (!encode_pages(&pp.tk, c->k, c, kPosTile / rows_pair(c->head_dim)) || !encode_pages(&pp.tv, c->v, c, kPosTile) ||
+        !encode_rows(&pp.tq, t.staged, c->head_dim, T * a.Hq))
+        return MTP_ERR_UNSUPPORTED;
     const bool e4m3 = c->kv_dtype == MTP_DTYPE_E4M3;
+    if (launch_rows_prepare(t, c->kv_dtype, sms, s) != cudaSuccess) return MTP_ERR_CUDA;
     if ((e4m3 ? launch_rows_tc_e4m3(pp, s) : launch_rows_tc_bf16(pp, s)) != cudaSuccess) return MTP_ERR_CUDA;
     return launch_rows_merge(t, c->kv_dtype, s) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }

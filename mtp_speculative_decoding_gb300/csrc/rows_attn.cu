@@ -202,20 +202,22 @@ struct RowParts {
     int r;                            // row of the slots
 };
 // parts of row r of (block, KV head)
-__device__ RowParts parts_of(const RowsTcArgs& t, const RowsPlan& plan, int blk, int g, int r, long long dense) {
+__device__ RowParts parts_of(const RowsTcArgs& t, const PlanHead& plan, int blk, int g, int r, long long dense) {
     RowParts p = {-1, 0, -1, r % kRowTile};
-    const Block k = block_at(t.a, plan.cum, blk);
+    const BlockRec k = t.blocks[blk];
+    const int rt = r / kRowTile;
     if (r >= k.n * t.a.G) return p;
-    const Item it = item_of(t, plan, k, blk, g, r / kRowTile);
-    const long long T = plan.pre[rows_blocks(t.a)];
-    p.w0 = worker_of(T, plan.workers, it.tiles_at);
-    p.w1 = worker_of(T, plan.workers, it.tiles_at + (long long)(it.n - 1) * kPosTile * t.a.G);
-    if (p.w0 == p.w1) p.dense = dense;
+    const Item it = item_of(t.a, k, rt);
+    const long long U = (long long)kPosTile * t.a.G;
+    const long long at = k.pre + g * units_before(t, k, plan.open, row_tiles_of(t.a, k)) + units_before(t, k, plan.open, rt) + plan.open * U;
+    p.w0 = worker_of(plan.T, plan.workers, at);
+    p.w1 = worker_of(plan.T, plan.workers, at + (it.n - 1) * U);
+    if (p.w0 == p.w1) p.dense = k.q_row + (long long)g * k.q_stride + r + dense;
     return p;
 }
 
 template <typename KT>
-__global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int ctas, int merges) {
+__global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int statuses, int merges) {
     __shared__ RowParts s_parts[2][kMergeRowThreads / 16];
     __shared__ int4 s_row[kMergeRowThreads / 16];           // sequence (< 0: none), token, query head
     __shared__ int s_list[kOddRows];
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __gr
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((int)blockIdx.x == (int)gridDim.x - 1) {   // the call's status from the CTAs'
         int bad = 0;
-        for (int c = tid; c < ctas; c += kMergeRowThreads) {
+        for (int c = tid; c < statuses; c += kMergeRowThreads) {
             const int st = t.cta_status[c];
             if (st == MTP_ERR_TIMEOUT) bad |= 2;
             else if (st != MTP_OK) bad |= 1;
@@ -268,14 +270,13 @@ __global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __gr
             const int4 n = t.note[w];
             // (an attention that gave up may have left anything: it stays in bounds)
             if (n.x >= 0 && n.x < a.B && n.y >= 0 && n.y < a.c.Hkv && n.z >= 0 && n.w > w && n.w < t.workers) {
-                const Block k = block_at(a, nullptr, n.x);
                 const long long at = (long long)n.z * kRowTile + r;
-                if (at < (long long)k.n * a.G) {
-                    const RowPlace pl = row_place(a, nullptr, k, n.y, (int)at);
+                if (at < (long long)t.blocks[n.x].n * a.G) {
+                    const int j = (int)at / a.G;
                     p0.w0 = w;
                     p0.w1 = n.w;
                     p0.r = r;
-                    row = make_int4(pl.b, pl.j, (int)(pl.out % a.Hq), 0);
+                    row = make_int4(n.x, j, n.y * a.G + (int)at - j * a.G, 0);
                 }
             }
         } else {
@@ -283,15 +284,11 @@ __global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __gr
             const int tok = (int)(id / a.Hq), b = tok / a.M, j = tok - b * a.M, h = (int)(id - (long long)tok * a.Hq);
             Seq s;
             if (b < a.B && seq_at(a, b, s) && j < s.n) {
-                RowsPlan plan;
-                const int2 head = *t.plan_head;
-                plan.open = head.x;
-                plan.workers = head.y;
-                plan.pre = t.plan_pre;
-                plan.cum = t.plan_cum;
-                const int g = h / a.G;
-                p0 = parts_of(t, plan, a.n_groups + b, g, j * a.G + h - g * a.G, (long long)a.B * a.M * a.Hq + id);
-                if (s.group >= 0 && s.P > 0) p1 = parts_of(t, plan, s.group, g, (plan.cum[b] - plan.cum[s.first] + j) * a.G + h - g * a.G, id);
+                const PlanHead plan = *t.head;
+                const int g = h / a.G, r = j * a.G + h - g * a.G;
+                p0 = parts_of(t, plan, a.n_groups + b, g, r, (long long)a.B * a.M * a.Hq);
+                if (s.group >= 0 && s.P > 0)   // the sequence's first row among its group's
+                    p1 = parts_of(t, plan, s.group, g, (int)(t.blocks[a.n_groups + b].q_row - t.blocks[s.group].q_row) + r, 0);
                 row = make_int4(b, j, h, 0);
             }
         }
@@ -381,9 +378,9 @@ cudaError_t launch_rows_merge(const RowsTcArgs& t, int kv_dtype, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const int ctas = t.workers * rows_pair(a.hd);
-    return kv_dtype == MTP_DTYPE_E4M3 ? cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint8_t>, t, ctas, (int)merges)
-                                      : cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint16_t>, t, ctas, (int)merges);
+    const int statuses = t.workers * rows_pair(a.hd) + 1;   // the CTAs' and the plan's
+    return kv_dtype == MTP_DTYPE_E4M3 ? cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint8_t>, t, statuses, (int)merges)
+                                      : cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint16_t>, t, statuses, (int)merges);
 }
 
 cudaError_t launch_rows_cc(const RowsArgs& a, int dtype, int kv_dtype, cudaStream_t s) {

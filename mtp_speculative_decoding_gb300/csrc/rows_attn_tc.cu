@@ -1,9 +1,9 @@
 // rows_attn_tc.cu -- attention of many rows over the paged cache on tcgen05
 // tensor cores: whole prompts, and batches that share prefixes.
 //
-// The rows take the MMA's M side: S [rows, 128 positions] = Q K^T, with the
-// queries normed, rotated and rounded once into shared memory, and O [rows, hd]
-// += P V, with P read from tensor memory, where the softmax leaves it over the
+// The rows take the MMA's M side: S [rows, 128 positions] = Q K^T, with the rows
+// as rows_prepare.cu has staged them (normed, rotated, rounded once), and O [rows,
+// hd] += P V, with P read from tensor memory, where the softmax leaves it over the
 // scores it came from, and V's tile as it lies in the page (its dimensions
 // contiguous: the N-major operand).  K and V come from the pages by TMA; an e4m3
 // cache's codes are opened to fp16, which holds them exactly, and multiplied
@@ -158,6 +158,18 @@ __device__ __forceinline__ void tma_4d(void* dst, const void* tmap, int x, int y
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_2d(void* dst, const void* tmap, int x, int y, unsigned long long* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(tmap), "r"(x), "r"(y), "r"(smem_addr(bar))
+                 : "memory");
+}
+// 32 bytes (a whole sector) in one store
+__device__ __forceinline__ void store_32b(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -205,19 +217,20 @@ struct RowShape {
     static constexpr int QB = 128 * HD * 2;                        // bytes of a row tile
     static constexpr int SLOTB = rows_slot_bytes(HD), RAWB = SLOTB / 2;
     static constexpr int SW = 4 * NQ;                              // softmax warps
-    static constexpr int STAGE = SW, CONV = SW + 4, PROD = SW + 4 + (E4M3 ? 4 : 0), MMA = PROD + 1;
-    static constexpr int THREADS = (MMA + 1) * 32;
+    static constexpr int CONV = SW, PROD = SW + (E4M3 ? 4 : 0), MMA = PROD + 1, QUERY = PROD + 2;
+    static constexpr int THREADS = (QUERY + 1) * 32;
     static constexpr int O0 = 256, OC = HD;                        // accumulators' columns, behind two score buffers of 128
     // a probability is 2^(z - m), at most 2^kSlack; in fp16 times 2^kBias
     static constexpr float kSlack = E4M3 ? 4.f : 8.f, kBias = E4M3 ? 11.f : 0.f;
-    // place of V tile k and K tile k among a piece's n tile pairs
+    // place of V tile k among a piece's n tile pairs
     static __device__ __forceinline__ unsigned v_at(int k, int n) { return CG == 1 ? 2 * k + 1 : k == n - 1 ? 2 * n - 1 : 2 * k + 2; }
 };
 
 template <bool E4M3, int HD>
-__global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcParams pp, int NS) {
+__global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcParams pp) {
     using S = RowShape<E4M3, HD>;
-    constexpr int CG = S::CG, NQ = S::NQ, NR = rows_raw(E4M3, HD);
+    constexpr int CG = S::CG, NQ = S::NQ, NR = rows_raw(E4M3, HD), NS = rows_slots(E4M3, HD);
+    static_assert(NS >= 2 && NS <= kRowsSlots && NR <= kRowsRaw, "ring");
     const RowsTcArgs& t = pp.t;
     const RowsArgs& a = t.a;
     extern __shared__ unsigned char raw_smem[];
@@ -228,16 +241,11 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
     uint4* m_bits = reinterpret_cast<uint4*>(raw + (size_t)NR * S::RAWB);       // [kRowsMeta] positions that are there
     float2* m_sc = reinterpret_cast<float2*>(m_bits + kRowsMeta);               // [kRowsMeta][8] key scale, value scale's exponent, every 16 positions
     int4* m_flag = reinterpret_cast<int4*>(m_sc + kRowsMeta * 8);               // [kRowsMeta] x: all positions there
-    float* s_hi = reinterpret_cast<float*>(m_flag + kRowsMeta);                 // rotation table
-    float* s_lo = s_hi + HD / 2;
-    float* s_c = s_lo + HD / 2;                                                 // [2][kRowTile] e4m3: a query row's scale, by pieces in turn
-    unsigned long long* bars = reinterpret_cast<unsigned long long*>(s_c + 2 * kRowTile);
+    unsigned long long* bars = reinterpret_cast<unsigned long long*>(m_flag + kRowsMeta);
     unsigned long long *full = bars, *empty = full + kRowsSlots, *peer = empty + kRowsSlots, *rfull = peer + kRowsSlots,
                        *rempty = rfull + kRowsRaw, *meta = rempty + kRowsRaw, *s_full = meta + kRowsMeta, *p_full = s_full + 2,
-                       *pv_done = p_full + 2, *o_free = pv_done + 2, *q_full = o_free + 2, *q_free = q_full + 1, *end_bar = q_free + 1;
-    long long* tmp = reinterpret_cast<long long*>(bars + 3 * kRowsSlots + 2 * kRowsRaw + kRowsMeta + 16);   // [64]
-    long long* s_pre = tmp + 64;
-    int* s_cum = reinterpret_cast<int*>(s_pre + rows_blocks(a) + 1);
+                       *pv_done = p_full + 2, *o_free = pv_done + 2, *q_full = o_free + 2, *q_peer = q_full + 1, *q_free = q_peer + 1,
+                       *end_bar = q_free + 1;
     __shared__ unsigned int s_tmem;
     __shared__ int s_bad;
     __shared__ volatile int s_abort;
@@ -260,37 +268,22 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             mbar_init(pv_done + i, 1);
             mbar_init(o_free + i, 4 * CG);
         }
-        mbar_init(q_full, 4 * CG);
+        mbar_init(q_full, 1);
+        mbar_init(q_peer, 1);
         mbar_init(q_free, 1);
         mbar_init(end_bar, 1);
         s_bad = 0;
         s_abort = 0;
     }
     mbar_fence_init();
-    if (a.rope.on)
-        for (int i = tid; i < HD / 2; i += S::THREADS) {
-            s_hi[i] = a.rope.hi[i];
-            s_lo[i] = a.rope.lo[i];
-        }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    RowsPlan plan;
-    const bool good = make_plan<S::THREADS>(t, plan, s_pre, s_cum, tmp);
     if (CG == 2) pair_sync();   // the peer's barriers stand
     if (warp == S::MMA) alloc_columns<CG>(&s_tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-    if (blockIdx.x == 0 && !good) s_bad = 1;
-    if (blockIdx.x == 0) {   // what the merge needs of the plan
-        if (tid == 0) *t.plan_head = make_int2(plan.open, plan.workers);
-        for (int i = tid; i <= rows_blocks(a); i += S::THREADS) t.plan_pre[i] = s_pre[i];
-        if (a.n_groups > 0)
-            for (int i = tid; i <= a.B; i += S::THREADS) t.plan_cum[i] = s_cum[i];
-    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long T = s_pre[rows_blocks(a)];
-    const long long xs = me < plan.workers ? share_at(T, plan.workers, me) : T, xe = me < plan.workers ? share_at(T, plan.workers, me + 1) : T;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the plan and the staged rows are there
     // bounded wait; after one gave up every other does too
     auto wait = [&](unsigned long long* bar, unsigned int parity) -> bool {
         if (try_wait<CG>(bar, parity)) return true;
@@ -305,17 +298,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         return true;
     };
     auto wait_all = [&](unsigned long long* bar, unsigned int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    // the next piece with tiles in it at x or behind; x moves to the item behind it
-    auto next_piece = [&](long long& x, Piece& p) -> bool {
-        while (x < xe) {
-            p = piece_at(t, plan, x, xs, xe);
-            x = p.next;
-            if (p.n > 0) return true;
-        }
-        return false;
-    };
     const int ps = 1 << a.c.ps_log2;
-    const uint32_t idS = idesc(E4M3 ? 0 : 1, false, 128 * CG, kPosTile), idO = idesc(E4M3 ? 0 : 1, true, 128 * CG, HD);
+    constexpr uint32_t idS = idesc(E4M3 ? 0 : 1, false, 128 * CG, kPosTile), idO = idesc(E4M3 ? 0 : 1, true, 128 * CG, HD);
 
     if (warp == S::PROD) {
         // ------------------------------------------------------------------
@@ -326,17 +310,16 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         const int vr = 1 << vl, nv = kPosTile >> vl, kr = 1 << kl, nk = S::KP >> kl;
         constexpr int KB = E4M3 ? (HD < 128 ? 64 : 128) : 64;   // dimensions of a box
         constexpr int ESZ = E4M3 ? 1 : 2;
-        const int SLOTS = E4M3 ? NR : NS;
+        constexpr int SLOTS = E4M3 ? NR : NS, DSTB = E4M3 ? S::RAWB : S::SLOTB;
         unsigned char* dst0 = E4M3 ? raw : ring;
-        constexpr int DSTB = E4M3 ? S::RAWB : S::SLOTB;
         unsigned long long *bf = E4M3 ? rfull : full, *be = E4M3 ? rempty : empty;
         unsigned slot = 0, phase = 0, ti = 0;
         bool ok = true, bad = false;
         int4 note = make_int4(-1, 0, 0, 0);
-        Piece p;
-        long long x = xs;
-        while (ok && next_piece(x, p)) {
-            const int* tab = a.c.table + (long long)p.k.b0 * a.c.max_pages;
+        Walk p;
+        p.start(t, me);
+        while (ok && p.next(t)) {
+            const int* tab = a.c.table + (long long)p.k.table * a.c.max_pages;
             const int end = p.k.group ? p.k.hi : p.it.p_last + 1;
             const int wlo = a.c.window > 0 && p.it.p_first + 1 > a.c.window ? p.it.p_first + 1 - a.c.window : 0;
             const int wfar = a.c.window > 0 && p.it.p_last + 1 > a.c.window ? p.it.p_last + 1 - a.c.window : 0;
@@ -383,6 +366,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
             };
             int npg = entry(0), held = -2, held_tile = 0;
+#pragma unroll 1
             for (int k = 0; k <= p.n && ok; ++k) {
                 const int pg = npg, tile = k < p.n ? tile_of(p.it, p.t0 + k) : 0;
                 npg = entry(k + 1);
@@ -423,8 +407,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     held_tile = tile;
                 }
             }
-            if (p.slot == 2 && p.t0 == 0)
-                note = make_int4(p.blk, p.g, p.rt, worker_of(T, plan.workers, p.it.tiles_at + (long long)(p.it.n - 1) * kPosTile * a.G));
+            if (p.slot == 2 && p.t0 == 0 && a.M == 0)
+                note = make_int4(p.blk, p.g, p.rt, worker_of(t.head->T, t.head->workers, p.tiles_at + (long long)(p.it.n - 1) * kPosTile * a.G));
         }
         if (rank == 0 && lane == 0 && a.M == 0) t.note[me] = note;
         if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
@@ -435,6 +419,31 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 while (!try_wait<CG>(bf + i, ph) && global_ns() - t0 < t.timeout_ns) {}
             }
         }
+    } else if (warp == S::QUERY) {
+        // ------------------------------------------------------------------
+        // the items' staged rows; the second CTA of a pair tells the first
+        // ------------------------------------------------------------------
+        unsigned seg = 0;
+        bool ok = true;
+        Walk p;
+        p.start(t, me);
+        while (ok && p.next(t)) {
+            ok = wait_all(q_free, (seg & 1) ^ 1);
+            if (!ok) break;
+            const int tiles = CG == 1 && p.it.rows <= 128 ? 1 : NQ;
+            const long long row = p.k.q_row + (long long)p.g * p.k.q_stride + p.it.r0 + rank * 128;
+            if (lane == 0) mbar_arrive_expect_tx(q_full, (unsigned)(tiles * S::QB));
+            __syncwarp();
+            if (lane < tiles * (HD / 64)) {
+                const int q = lane / (HD / 64), c = lane % (HD / 64);
+                tma_2d(sQ + q * S::QB + c * 128 * 128, &pp.tq, c * 64, (int)row + q * 128, q_full);
+            }
+            __syncwarp();
+            ok = wait_all(q_full, seg & 1);
+            if (CG == 2 && rank == 1 && ok && lane == 0) arrive_lead<CG>(q_peer);
+            __syncwarp();
+            ++seg;
+        }
     } else if (E4M3 && warp >= S::CONV && warp < S::CONV + 4) {
         // ------------------------------------------------------------------
         // codes to fp16: a thread opens 16 of them at a time
@@ -442,9 +451,10 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         const int ct = tid - S::CONV * 32;
         unsigned slot = 0, phase = 0, rs = 0, rp = 0;
         bool ok = true;
-        Piece p;
-        long long x = xs;
-        while (ok && next_piece(x, p)) {
+        Walk p;
+        p.start(t, me);
+        while (ok && p.next(t)) {
+#pragma unroll 1
             for (int i = 0; i < 2 * p.n && ok; ++i) {
                 // K tiles and V tiles take turns: K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. Kn-1 Vn-2 Vn-1
                 const bool key = CG == 1 ? (i & 1) == 0 : i == 0 || ((i & 1) != 0 && i != 2 * p.n - 1);
@@ -508,10 +518,10 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 phase ^= 1;
             }
         };
-        Piece p;
-        long long x = xs;
+        Walk p;
+        p.start(t, me);
         if (CG == 2 && rank == 1) {
-            while (ok && next_piece(x, p))
+            while (ok && p.next(t))
                 for (int i = 0; i < 2 * p.n && ok; ++i) {
                     hold(full + slot, phase);
                     if (ok && lane == 0) arrive_lead<CG>(peer + slot);
@@ -538,8 +548,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
                 __syncwarp();
             };
-            auto values = [&](int q, int buf, bool first) {
-                const uint32_t bl = r0 + slot * (S::SLOTB >> 4) + lead_bits(S::VD > 64 ? kPosTile * 128 : 16);
+            auto values = [&](int q, int buf, unsigned at, bool first) {
+                const uint32_t bl = r0 + at * (S::SLOTB >> 4) + lead_bits(S::VD > 64 ? kPosTile * 128 : 16);
                 if (ok && elect()) {
 #pragma unroll
                     for (int ks = 0; ks < kPosTile / 16; ++ks)
@@ -553,11 +563,13 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 __syncwarp();
                 next();
             };
-            while (ok && next_piece(x, p)) {
+            while (ok && p.next(t)) {
                 hold(q_full, seg & 1);
+                if (CG == 2) hold(q_peer, seg & 1);
                 ++seg;
                 if (CG == 2) {
                     const unsigned t0 = tq[0];
+#pragma unroll 1
                     for (int k = 0; k <= p.n && ok; ++k) {
                         if (k < p.n) {
                             arrived();
@@ -571,7 +583,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                             if (k == 1) hold(o_free, (sq[0] & 1) ^ 1);
                             hold(p_full + (u & 1), (u >> 1) & 1);
                             arrived();
-                            values(0, u & 1, k == 1);
+                            values(0, u & 1, slot, k == 1);
                             done();
                         }
                     }
@@ -581,21 +593,18 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     const int nq = p.it.rows > 128 ? 2 : 1;
                     // slots take turns: K tile k, V tile k
                     unsigned vslot = 0, vphase = 0;
+#pragma unroll 1
                     for (int k = 0; k <= p.n && ok; ++k) {
                         const bool more = k < p.n;
                         if (more) arrived();
-                        if (k > 0) {
-                            ok = ok && wait_all(full + vslot, vphase);
-                            tc_fence_after();
-                        }
-                        for (int q = 0; q < nq && ok; ++q) {
+                        if (k > 0) hold(full + vslot, vphase);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            if (q >= nq) break;
                             if (k > 0) {
                                 if (k == 1) hold(o_free + q, (sq[q] & 1) ^ 1);
                                 hold(p_full + q, (tq[q] + k - 1) & 1);
-                                const unsigned ks = slot;
-                                slot = vslot;
-                                values(q, q, k == 1);
-                                slot = ks;
+                                values(q, q, vslot, k == 1);
                             }
                             if (more) scores(q, q);
                         }
@@ -610,10 +619,12 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                             next();
                         }
                     }
-                    for (int q = 0; q < nq; ++q) {
-                        tq[q] += p.n;
-                        ++sq[q];
-                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (q < nq) {
+                            tq[q] += p.n;
+                            ++sq[q];
+                        }
                 }
             }
             if (elect()) commit<CG>(end_bar);   // whatever was issued has ended before its memory goes
@@ -622,106 +633,26 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         const unsigned long long t0 = global_ns();
         while (!try_wait<CG>(end_bar, 0) && global_ns() - t0 < 2 * t.timeout_ns) {}
         __syncwarp();
-    } else if (warp >= S::STAGE && warp < S::STAGE + 4) {
-        // ------------------------------------------------------------------
-        // queries: norm, rotation, scale, one rounding; a thread has one unit of
-        // consecutive rows, so the heads of a token share its angles
-        // ------------------------------------------------------------------
-        constexpr int U = HD / 16, PER = NQ * U, NB = 4;   // units of a row, rows of a thread, rows in flight
-        const int st = tid - S::STAGE * 32, c = st % U, rq = (st / U) * PER;
-        unsigned seg = 0;
-        bool ok = true;
-        Piece p;
-        long long x = xs;
-        while (ok && next_piece(x, p)) {
-            const int r0 = p.it.r0 + rank * 128, left = p.it.rows - rank * 128;   // this CTA's rows
-            uint4 u[NB][2];
-            int pos[NB];
-            auto fetch = [&](int i0) {
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const int r = rq + i0 + i;
-                    pos[i] = -1;
-                    u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
-                    if (r < left) {
-                        const RowPlace w = row_place(a, s_cum, p.k, p.g, r0 + r);
-                        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + w.q + 8 * c;
-                        u[i][0] = ld_stream16(src);
-                        u[i][1] = ld_stream16(src + HD / 2);
-                        pos[i] = w.pos;
-                    }
-                }
-            };
-            fetch(0);
-            ok = wait_all(q_free, (seg & 1) ^ 1);
-            if (!ok) break;
-            float cs[8], sn[8];
-            int have = -1;
-#pragma unroll 1
-            for (int i0 = 0; i0 < PER; i0 += NB) {
-                if (i0 > 0) fetch(i0);
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const int r = rq + i0 + i;
-                    float v[8], w[8];
-                    open_unit(u[i][0], v);
-                    open_unit(u[i][1], w);
-                    if (a.rope.on && pos[i] >= 0 && pos[i] != have) {
-                        unit_angles<true>((long long)pos[i], s_hi + 8 * c, s_lo + 8 * c, cs, sn);
-                        have = pos[i];
-                    }
-                    if (a.q_norm) unit_norm(v, w, a.q_norm, c, HD, a.eps);
-                    if (a.rope.on && pos[i] >= 0) unit_rotate(v, w, cs, sn);
-                    float f = a.scale;
-                    if (E4M3) {   // the largest of the row into [128, 256): no bits lost to fp16's range
-                        float big = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(v[e]), fabsf(w[e])));
-                        for (int o = U >> 1; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                        int x2 = (int)(__float_as_uint(big * a.scale) >> 23) - 127 - 7;
-                        x2 = x2 < -100 ? -100 : x2 > 100 ? 100 : x2;
-                        f *= __uint_as_float((uint32_t)(127 - x2) << 23);
-                        if (c == 0) s_c[(seg & 1) * kRowTile + r] = __uint_as_float((uint32_t)(127 + x2) << 23);
-                    }
-                    uint32_t o[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[e] = E4M3 ? pack_f16(v[2 * e] * f, v[2 * e + 1] * f) : pack_bf16(v[2 * e] * f, v[2 * e + 1] * f);
-                        o[4 + e] = E4M3 ? pack_f16(w[2 * e] * f, w[2 * e + 1] * f) : pack_bf16(w[2 * e] * f, w[2 * e + 1] * f);
-                    }
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int d = half * (HD / 2) + 8 * c;
-                        *reinterpret_cast<uint4*>(sQ + (r >> 7) * S::QB + (d >> 6) * 128 * 128 + swz128(r & 127, (d & 63) >> 3)) =
-                            make_uint4(o[4 * half], o[4 * half + 1], o[4 * half + 2], o[4 * half + 3]);
-                    }
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_lead<CG>(q_full);
-            ++seg;
-        }
     } else {
         // ------------------------------------------------------------------
         // softmax and epilogue: thread = row
         // ------------------------------------------------------------------
         const int q = warp >> 2, row = tid & 127;            // row tile of this CTA, row of it
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        unsigned tc = 0, ti = 0, g0 = 0, seg = 0;            // tiles of this row tile, of the CTA; ring slots and pieces before this one
+        unsigned tc = 0, ti = 0, g0 = 0;                     // tiles of this row tile, of the CTA; ring slots before this piece
+        auto meet = [&](unsigned long long* bar, unsigned parity) {
+            wait(bar, parity);
+            __syncwarp();
+        };
         // tile i of this row tile is in the accumulator
         auto meet_values = [&](unsigned i) {
             wait(pv_done + (CG == 2 ? i & 1 : q), CG == 2 ? (i >> 1) & 1 : i & 1);
             __syncwarp();
             tc_fence_after();
         };
-        auto meet = [&](unsigned long long* bar, unsigned parity) {
-            wait(bar, parity);
-            __syncwarp();
-        };
-        Piece p;
-        long long x = xs;
-        for (; next_piece(x, p); ++seg) {
+        Walk p;
+        p.start(t, me);
+        while (p.next(t)) {
             const int ofs = (CG == 2 ? rank : q) * 128;      // of the row tile in the item
             if (CG == 1 && p.it.rows <= ofs) {               // not there: the other row tile's alone
                 for (int k = 0; k < p.n; ++k, ++ti) meet(meta + ti % kRowsMeta, (ti / kRowsMeta) & 1);   // (in step with the phases)
@@ -729,24 +660,26 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 continue;
             }
             const bool live = ofs + row < p.it.rows;
-            const RowPlace w = row_place(a, s_cum, p.k, p.g, p.it.r0 + (live ? ofs + row : p.it.rows - 1));
-            const int end = p.k.group ? p.k.hi : w.pos + 1;   // attends [.., end)
-            float m = kNoScore, l = 0.f, qc = 1.f;
+            const int r = p.it.r0 + (live ? ofs + row : p.it.rows - 1), tok = (int)udiv((unsigned)r, (unsigned)a.G);   // row of the block, its token
+            const int pos_q = p.k.len + tok, end = p.k.group ? p.k.hi : pos_q + 1;   // attends [.., end)
+            // what a score is multiplied by: the softmax scale, and what the staged row was divided by
+            const float qc = E4M3 ? t.q_scale[p.k.q_row + (long long)p.g * p.k.q_stride + r] : a.scale;
+            float m = kNoScore, l = 0.f;
+#pragma unroll 1
             for (int k = 0; k < p.n; ++k) {
                 const int buf = CG == 2 ? (int)(tc & 1) : q;
                 const uint32_t sat = tmem + lanes + buf * 128;
                 const int t0 = tile_of(p.it, p.t0 + k) * kPosTile;
                 const unsigned mi = ti % kRowsMeta;
                 meet(meta + mi, (ti / kRowsMeta) & 1);
-                const bool all = m_flag[mi].x != 0;
                 // every row of the item attends every position of the tile
-                const bool whole = all && t0 >= p.k.lo && (p.k.group ? t0 + kPosTile <= p.k.hi : t0 + kPosTile - 1 <= p.it.p_first) &&
+                const bool whole = m_flag[mi].x != 0 && t0 >= p.k.lo && (p.k.group ? t0 + kPosTile <= p.k.hi : t0 + kPosTile - 1 <= p.it.p_first) &&
                                    (a.c.window == 0 || t0 > p.it.p_last - a.c.window || t0 + kPosTile <= a.c.sink);
                 uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
                 if (!whole) {
                     const uint4 b = m_bits[mi];
                     bits[0] = b.x; bits[1] = b.y; bits[2] = b.z; bits[3] = b.w;
-                    const int low = a.c.window > 0 && w.pos + 1 > a.c.window ? w.pos + 1 - a.c.window : 0;
+                    const int low = a.c.window > 0 && pos_q + 1 > a.c.window ? pos_q + 1 - a.c.window : 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int c0 = t0 + 32 * i;
@@ -758,48 +691,38 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
                 meet(s_full + buf, CG == 2 ? (tc >> 1) & 1 : tc & 1);
                 tc_fence_after();
-                if (E4M3 && k == 0) qc = s_c[(seg & 1) * kRowTile + (CG == 2 ? 0 : ofs) + row];
-                // ---- the row's largest score of the tile ----
+                // ---- the row's largest score of the tile (in bits; fp16: with the value scale) ----
                 float mx = -__int_as_float(0x7F800000);
-                auto score = [&](const uint32_t (&r)[32], int c, float (&z)[32]) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(r[i]);
-                    if (E4M3) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float2 sc = m_sc[mi * 8 + 2 * c + h];
-                            sc.x *= qc;
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float2 y = fma2(make_float2(z[16 * h + i], z[16 * h + i + 1]), make_float2(sc.x, sc.x), make_float2(sc.y, sc.y));
-                                z[16 * h + i] = y.x;
-                                z[16 * h + i + 1] = y.y;
-                            }
-                        }
-                    }
-                    if (!whole)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) z[i] = bits[c] >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
-                };
                 {
-                    uint32_t r[2][32];
-                    ld32(sat, r[0]);
+                    uint32_t s[2][32];
+                    ld32(sat, s[0]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld_wait();
-                        if (c < 3) ld32(sat + 32 * (c + 1), r[(c + 1) & 1]);
-                        float z[32];
-                        score(r[c & 1], c, z);
-                        float y = -__int_as_float(0x7F800000);
+                        if (c < 3) ld32(sat + 32 * (c + 1), s[(c + 1) & 1]);
+                        float* z = reinterpret_cast<float*>(s[c & 1]);
+                        if (!whole)
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            mx = max3(mx, z[i], z[i + 1]);
-                            y = max3(y, z[i + 2], z[i + 3]);
+                            for (int i = 0; i < 32; ++i) z[i] = bits[c] >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float x = z[16 * h], y = z[16 * h + 1];
+#pragma unroll
+                            for (int i = 2; i < 16; i += 4) {
+                                x = max3(x, z[16 * h + i], z[16 * h + i + 1]);
+                                if (i + 3 < 16) y = max3(y, z[16 * h + i + 2], z[16 * h + i + 3]);
+                            }
+                            x = fmaxf(x, y);
+                            if (E4M3) {
+                                const float2 sc = m_sc[mi * 8 + 2 * c + h];
+                                x = fmaf(x, sc.x * qc, sc.y);
+                            }
+                            mx = fmaxf(mx, x);
                         }
-                        mx = fmaxf(mx, y);
                     }
+                    if (!E4M3) mx *= qc;
                 }
-                if (__any_sync(0xffffffffu, mx > m + S::kSlack)) {
+                if (__any_sync(0xffffffffu, live && mx > m + S::kSlack)) {
                     // move the references, and with them what has been summed
                     const float mn = fmaxf(mx, m), f = ex2(m - mn);
                     l *= f;
@@ -808,12 +731,12 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         meet_values(tc - 1);
 #pragma unroll 1
                         for (int c = 0; c < HD; c += 32) {
-                            uint32_t r[32];
-                            ld32(tmem + lanes + S::O0 + q * S::OC + c, r);
+                            uint32_t o[32];
+                            ld32(tmem + lanes + S::O0 + q * S::OC + c, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                            st32(tmem + lanes + S::O0 + q * S::OC + c, r);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            st32(tmem + lanes + S::O0 + q * S::OC + c, o);
                         }
                         st_wait();
                         tc_fence_before();
@@ -821,33 +744,38 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
                 // ---- probabilities, over the scores ----
                 {
-                    uint32_t r[2][32];
-                    ld32(sat, r[0]);
-                    const float2 neg = make_float2(S::kBias - m, S::kBias - m);
+                    uint32_t s[2][32];
+                    ld32(sat, s[0]);
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld_wait();
-                        if (c < 3) ld32(sat + 32 * (c + 1), r[(c + 1) & 1]);
-                        float z[32];
-                        score(r[c & 1], c, z);
+                        if (c < 3) ld32(sat + 32 * (c + 1), s[(c + 1) & 1]);
+                        float* z = reinterpret_cast<float*>(s[c & 1]);
+                        if (!whole)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) z[i] = bits[c] >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
                         uint32_t o[16];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            float2 part = make_float2(0.f, 0.f);
+                            float2 mul = make_float2(qc, qc), add = make_float2(-m, -m), part = make_float2(0.f, 0.f);
+                            float un = 1.f;
+                            if (E4M3) {
+                                const float2 sc = m_sc[mi * 8 + 2 * c + h];
+                                mul.x = mul.y = sc.x * qc;
+                                add.x = add.y = sc.y + S::kBias - m;
+                                un = ex2(-sc.y);   // the sum goes without the value scale
+                            }
 #pragma unroll
                             for (int i = 16 * h; i < 16 * h + 16; i += 2) {
-                                float2 e = add2(make_float2(z[i], z[i + 1]), neg);
+                                float2 e = fma2(make_float2(z[i], z[i + 1]), mul, add);
                                 e.x = ex2(e.x);
                                 e.y = ex2(e.y);
                                 if (E4M3) part = add2(part, e);
                                 else sum = add2(sum, e);
                                 o[i >> 1] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
                             }
-                            if (E4M3) {   // without the value scale
-                                const float un = ex2(-m_sc[mi * 8 + 2 * c + h].y);
-                                sum = fma2(part, make_float2(un, un), sum);
-                            }
+                            if (E4M3) sum = fma2(part, make_float2(un, un), sum);
                         }
                         st16(sat + 16 * c, o);
                     }
@@ -886,50 +814,50 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             }
             g0 += 2 * p.n;
             // ---- the accumulator ----
-            meet_values(tc - 1);
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const bool out = p.slot == 0 && a.M == 0;        // the row's whole result
+            const long long orow = ((long long)p.k.row0 + tok) * a.Hq + p.g * a.G + r - tok * a.G;   // (sequences)
+            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + orow * HD;
             float* part = nullptr;
             if (!out && live) {
                 if (p.slot == 0) {
-                    const long long r = (p.k.group ? 0 : (long long)a.B * a.M * a.Hq) + w.out;
-                    part = t.dense + r * HD;
-                    t.dense_ml[r] = make_float2(m, l);
+                    const long long at = p.k.q_row + (long long)p.g * p.k.q_stride + r + (p.k.group ? 0 : (long long)a.B * a.M * a.Hq);
+                    part = t.dense + at * HD;
+                    t.dense_ml[at] = make_float2(m, l);
                 } else {
-                    const long long r = (2ll * me + p.slot - 1) * kRowTile + ofs + row;
-                    part = t.part + r * HD;
-                    t.part_ml[r] = make_float2(m, l);
+                    const long long at = (2ll * me + p.slot - 1) * kRowTile + ofs + row;
+                    part = t.part + at * HD;
+                    t.part_ml[at] = make_float2(m, l);
                 }
             }
-            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + w.out * HD;
+            meet_values(tc - 1);
             float odd = 0.f;   // NaN: the product left something that is not finite
 #pragma unroll 1
             for (int c = 0; c < HD; c += 32) {
-                uint32_t r[32];
-                ld32(tmem + lanes + S::O0 + q * S::OC + c, r);
+                uint32_t o[32];
+                ld32(tmem + lanes + S::O0 + q * S::OC + c, o);
                 tmem_ld_wait();
                 if (!live) {
                 } else if (out) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            v[e] = __uint_as_float(r[i + e]) * inv;
-                            odd = fmaf(v[e], 0.f, odd);
-                        }
-                        store8(dst + c + i, v);
+                    for (int i = 0; i < 32; i += 2) {
+                        const float x = __uint_as_float(o[i]) * inv, y = __uint_as_float(o[i + 1]) * inv;
+                        odd = fmaf(x, 0.f, fmaf(y, 0.f, odd));
+                        w[i >> 1] = pack_bf16(x, y);
                     }
+                    store_32b(dst + c, w);
+                    store_32b(dst + c + 16, w + 8);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4*>(part + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                    for (int i = 0; i < 32; i += 8) store_32b(part + c + i, o + i);
                 }
                 __syncwarp();
             }
-            if (a.M == 0 && live) t.odd[w.out] = out && !(odd == 0.f);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_lead<CG>(o_free + q);
+            if (a.M == 0 && live) t.odd[orow] = out && !(odd == 0.f);
         }
     }
     __syncthreads();
@@ -942,8 +870,8 @@ template <bool E4M3, int HD>
 cudaError_t go(const RowsTcParams& p, cudaStream_t s) {
     using S = RowShape<E4M3, HD>;
     static int ready[64] = {0};   // the attribute is set, per device
-    const int NS = rows_slots(E4M3, HD, p.t.a.B, p.t.a.n_groups);
-    const int smem = NS * S::SLOTB + S::NQ * S::QB + rows_raw(E4M3, HD) * S::RAWB + rows_other(HD, p.t.a.B, p.t.a.n_groups);
+    constexpr int smem = rows_slots(E4M3, HD) * S::SLOTB + S::NQ * S::QB + rows_raw(E4M3, HD) * S::RAWB + kRowsOther;
+    static_assert(smem <= kRowsSmemLimit, "shared memory");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -965,7 +893,7 @@ cudaError_t go(const RowsTcParams& p, cudaStream_t s) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = S::CG == 1 ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, rows_tc_kernel<E4M3, HD>, p, NS);
+    return cudaLaunchKernelEx(&cfg, rows_tc_kernel<E4M3, HD>, p);
 }
 
 }  // namespace

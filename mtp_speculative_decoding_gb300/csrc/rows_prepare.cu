@@ -1,0 +1,314 @@
+// rows_prepare.cu -- what the attention of many rows on the tensor cores starts
+// from: the rows as operands (normed, rotated, rounded once), and the plan of the
+// call (see rows_attn_tc.cuh), by one CTA of the same launch.
+//
+// The rows of an item end up one after another, whatever the heads of a group are,
+// so the attention fetches them by tensor copies.  Norm and rotation inside the
+// attention kernel cost it 15 us an item (256 rows x 256) between two pieces of
+// work; here they cost their bytes.
+#include "rows_attn_tc.cuh"
+
+namespace mtp {
+
+namespace {
+
+constexpr int kPrepThreads = 256;
+
+// sums of v over the threads in front of this one, and over all of the CTA
+__device__ __forceinline__ long long scan(long long v, long long* s, long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    __syncthreads();
+    if (lane == 31) s[warp] = inc;
+    __syncthreads();
+    long long base = inc - v;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
+        if (w < warp) base += s[w];
+        total += s[w];
+    }
+    return base;
+}
+
+// Tokens before every sequence (shared prefixes), and whether this thread saw
+// something out of range.
+__device__ __forceinline__ bool count_tokens(const RowsArgs& a, int* cum, long long* tmp) {
+    bool good = true;
+    const int per = (a.B + kPrepThreads - 1) / kPrepThreads, b0 = (int)threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
+    int n[(MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads], sum = 0;
+#pragma unroll
+    for (int i = 0; i < (MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads; ++i) {
+        n[i] = 0;
+        if (b0 + i < b1) {
+            Seq s;
+            good = seq_at(a, b0 + i, s) && good;
+            n[i] = s.n;
+            sum += s.n;
+        }
+    }
+    long long all;
+    int at = (int)scan(sum, tmp, all);
+#pragma unroll
+    for (int i = 0; i < (MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads; ++i)
+        if (b0 + i < b1) {
+            cum[b0 + i] = at;
+            at += n[i];
+        }
+    if (threadIdx.x == 0) cum[a.B] = (int)all;
+    __syncthreads();
+    return good;
+}
+
+// The staged row of (sequence, token 0, KV head 0), and the rows of a KV head there.
+// Prompts: a sequence's own rows.  Shared prefixes: its group's.
+struct StagedAt { long long row; int stride; };
+__device__ __forceinline__ StagedAt staged_at(const RowsArgs& a, const int* cum, const Seq& s, int b) {
+    StagedAt w;
+    if (a.M == 0) {
+        w.row = s.row0 * a.Hq;
+        w.stride = s.n * a.G;
+    } else {
+        const int g0 = s.group >= 0 ? s.first : b, g1 = s.group >= 0 ? a.group_start[s.group + 1] : b + 1;
+        w.stride = (cum[g1] - cum[g0]) * a.G;
+        w.row = (long long)cum[g0] * a.Hq + (cum[b] - cum[g0]) * a.G;
+    }
+    return w;
+}
+
+__device__ BlockRec block_at(const RowsArgs& a, const int* cum, int blk, bool& good) {
+    BlockRec k = {};
+    if (blk < a.n_groups) {
+        const int g0 = a.group_start[blk], g1 = a.group_start[blk + 1], P = a.prefix_len[blk];
+        const bool ok = g0 >= 0 && g0 <= g1 && g1 <= a.B && P >= 0 && P <= (long long)a.c.max_pages << a.c.ps_log2;
+        good = good && ok;
+        k.group = 1;
+        if (ok) {
+            k.n = P > 0 ? cum[g1] - cum[g0] : 0;
+            k.hi = P;
+            k.table = g0;
+            k.q_stride = k.n * a.G;
+            k.q_row = (long long)cum[g0] * a.Hq;
+        }
+        return k;
+    }
+    Seq s;
+    const int b = blk - a.n_groups;
+    good = seq_at(a, b, s) && good;
+    k.table = b;
+    if (s.n > 0) {
+        const StagedAt w = staged_at(a, cum, s, b);
+        k.n = s.n;
+        k.len = s.len;
+        k.lo = s.P;
+        k.hi = s.len + s.n;
+        k.q_stride = w.stride;
+        k.q_row = w.row;
+        k.row0 = (int)s.row0;
+    }
+    return k;
+}
+
+__device__ void make_plan(const RowsTcArgs& t, const int* cum, long long* tmp, long long* pre, bool good) {
+    const RowsArgs& a = t.a;
+    const int tid = threadIdx.x, nb = rows_blocks(a), per = (nb + kPrepThreads - 1) / kPrepThreads, k0 = tid * per,
+              k1 = k0 + per < nb ? k0 + per : nb;
+    const long long U = (long long)kPosTile * a.G;
+    long long tiles = 0, items = 0;
+    for (int i = k0; i < k1; ++i) {
+        const BlockRec k = block_at(a, cum, i, good);
+        t.blocks[i] = k;
+        const int nrt = row_tiles_of(a, k);
+        tiles += a.c.Hkv * tile_units(t, k, nrt);
+        items += (long long)a.c.Hkv * nrt;
+    }
+    long long units, n_items;
+    long long at = scan(tiles, tmp, units);
+    const long long it = scan(items, tmp, n_items);
+    // where a share is few tiles, how they spread counts for more
+    int open = kRowsOpen;
+    while (open > 0 && 2ll * open * U * t.workers > units) --open;
+    at += it * open * U;
+    const long long T = units + n_items * open * U, most = T / U;
+    const int workers = most < t.workers ? (most > 1 ? (int)most : 1) : t.workers;
+    for (int i = k0; i < k1; ++i) {
+        pre[i] = at;
+        BlockRec k = t.blocks[i];
+        t.blocks[i].pre = at;
+        at += a.c.Hkv * units_before(t, k, open, row_tiles_of(a, k));
+    }
+    __syncthreads();   // (the records of the other threads too)
+    for (int w = tid; w < t.workers; w += kPrepThreads) {
+        WorkerRec r = {};
+        r.xs = w < workers ? share_at(T, workers, w) : T;
+        r.xe = w < workers ? share_at(T, workers, w + 1) : T;
+        if (r.xs < r.xe) {
+            int b = 0;
+            for (int hi = nb - 1; b < hi;) {   // the last block that begins at xs or before
+                const int mid = (b + hi + 1) >> 1;
+                if (pre[mid] <= r.xs) b = mid;
+                else hi = mid - 1;
+            }
+            const BlockRec k = t.blocks[b];
+            const int nrt = row_tiles_of(a, k);
+            const long long head = units_before(t, k, open, nrt);
+            long long rel = r.xs - pre[b];
+            const int g = (int)quotient(rel, head);
+            rel -= g * head;
+            int rt = 0;
+            for (int hi = nrt - 1; rt < hi;) {
+                const int mid = (rt + hi + 1) >> 1;
+                if (units_before(t, k, open, mid) <= rel) rt = mid;
+                else hi = mid - 1;
+            }
+            r.blk = b;
+            r.g = g;
+            r.rt = rt;
+            r.begin = pre[b] + g * head + units_before(t, k, open, rt);
+        } else {
+            r.begin = T;
+        }
+        t.worker[w] = r;
+    }
+    if (tid == 0) {
+        PlanHead h;
+        h.T = T;
+        h.open = open;
+        h.workers = workers;
+        *t.head = h;
+    }
+    const int any = __syncthreads_or(!good);
+    if (tid == 0) t.cta_status[t.workers * rows_pair(a.hd)] = any ? MTP_ERR_ARG : MTP_OK;
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid_constant__ RowsTcArgs t, int hpt) {
+    extern __shared__ __align__(16) unsigned char sm[];
+    __shared__ long long tmp[kPrepThreads / 32];
+    __shared__ __align__(16) float s_hi[256], s_lo[256];
+    const RowsArgs& a = t.a;
+    int* cum = reinterpret_cast<int*>(sm);                                     // [B + 1] prompts: row_start
+    long long* pre = reinterpret_cast<long long*>(sm + (((size_t)a.B + 2) * 4 + 7) / 8 * 8);   // the plan's CTA: [blocks]
+    const int tid = threadIdx.x;
+    const bool planner = blockIdx.x == 0;
+    if (a.rope.on && !planner)
+        for (int i = tid; i < a.hd >> 1; i += kPrepThreads) {
+            s_hi[i] = a.rope.hi[i];
+            s_lo[i] = a.rope.lo[i];
+        }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool good = true;
+    if (a.M > 0) good = count_tokens(a, cum, tmp);
+    else
+        for (int i = tid; i <= a.B; i += kPrepThreads) cum[i] = a.row_start[i];
+    __syncthreads();
+    if (planner) {
+        make_plan(t, cum, tmp, pre, good);
+        return;
+    }
+    const int hd = a.hd, U = hd >> 4, ulog = 31 - __clz(U), groups = (a.Hq + hpt - 1) / hpt, half = hd >> 1;
+    const long long x = ((long long)(blockIdx.x - 1) * kPrepThreads + tid) >> ulog;
+    const int c = tid & (U - 1), toks = a.M > 0 ? a.B * a.M : a.T;
+    int tok = (int)(x / groups);
+    const int h0 = (int)(x - (long long)tok * groups) * hpt;
+    // (whole rows' lanes are out of range together; all lanes go along for the shuffles)
+    bool live = tok < toks;
+    if (!live) tok = toks - 1;
+    const int b = a.M > 0 ? tok / a.M : last_at_most(cum, a.B, tok);
+    Seq s;
+    live = seq_at(a, b, s) && live;
+    const int j = (int)(tok - s.row0);
+    live = live && j >= 0 && j < s.n;
+    if (!__any_sync(0xffffffffu, live)) return;
+    const StagedAt w = live ? staged_at(a, cum, s, b) : StagedAt{0, 0};
+    const long long src0 = live ? s.q0 + j * a.sm : 0;
+    float cs[8], sn[8];
+    if (a.rope.on) unit_angles<true>((long long)(live ? s.len + j : 0), s_hi + 8 * c, s_lo + 8 * c, cs, sn);
+    float g0[8], g1[8];
+    if (a.q_norm)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g0[i] = __ldg(a.q_norm + 8 * c + i);
+            g1[i] = __ldg(a.q_norm + half + 8 * c + i);
+        }
+#pragma unroll 2
+    for (int i = 0; i < hpt; ++i) {
+        const int h = h0 + i < a.Hq ? h0 + i : a.Hq - 1;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (live ? src0 + h * a.sh : 0) + 8 * c;
+        float p[8], q[8];
+        load8(src, p);
+        load8(src + half, q);
+        if (a.q_norm) {
+            const float r = unit_rms(p, q, hd, a.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                p[e] *= r * g0[e];
+                q[e] *= r * g1[e];
+            }
+        }
+        if (a.rope.on) unit_rotate(p, q, cs, sn);
+        const int g = h / a.G;
+        const long long row = w.row + (long long)g * w.stride + j * a.G + h - g * a.G;
+        const bool mine = live && h0 + i < a.Hq;
+        uint4 o[2];
+        if (E4M3) {   // the largest of the row into [128, 256): no bits lost to fp16's range
+            float big = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(p[e]), fabsf(q[e])));
+            for (int k = U >> 1; k > 0; k >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
+            int x2 = (int)(__float_as_uint(big) >> 23) - 127 - 7;
+            x2 = x2 < -100 ? -100 : x2 > 100 ? 100 : x2;
+            const float f = __uint_as_float((uint32_t)(127 - x2) << 23);
+            if (mine && c == 0) t.q_scale[row] = __uint_as_float((uint32_t)(127 + x2) << 23) * a.scale;
+            auto half2 = [&](float lo, float hi) {
+                uint32_t r;
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi * f), "f"(lo * f));
+                return r;
+            };
+            o[0] = make_uint4(half2(p[0], p[1]), half2(p[2], p[3]), half2(p[4], p[5]), half2(p[6], p[7]));
+            o[1] = make_uint4(half2(q[0], q[1]), half2(q[2], q[3]), half2(q[4], q[5]), half2(q[6], q[7]));
+        } else {
+            o[0] = make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+            o[1] = make_uint4(pack_bf16(q[0], q[1]), pack_bf16(q[2], q[3]), pack_bf16(q[4], q[5]), pack_bf16(q[6], q[7]));
+        }
+        if (mine) {
+            uint16_t* dst = t.staged + row * hd + 8 * c;
+            *reinterpret_cast<uint4*>(dst) = o[0];
+            *reinterpret_cast<uint4*>(dst + half) = o[1];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rows_prepare(const RowsTcArgs& t, int kv_dtype, int sms, cudaStream_t s) {
+    const RowsArgs& a = t.a;
+    const long long toks = a.M > 0 ? (long long)a.B * a.M : a.T;
+    const int U = a.hd >> 4;
+    // as many heads in one thread as leave 512 threads an SM: the angles of a row are
+    // computed once for them
+    int hpt = 1;
+    while (hpt < a.Hq && toks * U * ((a.Hq + 2 * hpt - 1) / (2 * hpt)) >= (long long)sms * 512) hpt *= 2;
+    const long long threads = toks * U * ((a.Hq + hpt - 1) / hpt);
+    const int ctas = (int)((threads + kPrepThreads - 1) / kPrepThreads);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas + 1);
+    cfg.blockDim = dim3(kPrepThreads);
+    cfg.dynamicSmemBytes = (((size_t)a.B + 2) * 4 + 7) / 8 * 8 + (size_t)rows_blocks(a) * 8;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return kv_dtype == MTP_DTYPE_E4M3 ? cudaLaunchKernelEx(&cfg, rows_prepare_kernel<true>, t, hpt)
+                                      : cudaLaunchKernelEx(&cfg, rows_prepare_kernel<false>, t, hpt);
+}
+
+}  // namespace mtp
