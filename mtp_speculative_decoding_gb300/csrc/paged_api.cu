@@ -170,7 +170,7 @@ RowsSpace rows_space(const mtp_kv_cache* c, int B, int M, int64_t T, int n_q_hea
         const size_t rows = (size_t)T * n_q_heads;
         p.workers = sms / rows_pair(hd);
         p.status = take(((size_t)sms + 1) * sizeof(int));
-        p.note = take((size_t)p.workers * sizeof(int4));
+        p.note = take((size_t)p.workers * sizeof(RowNote));
         p.head = take(sizeof(PlanHead));
         p.worker = take((size_t)p.workers * sizeof(WorkerRec));
         p.blocks = take(2 * (size_t)B * sizeof(BlockRec));
@@ -233,7 +233,7 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
     const long long U = (long long)kPosTile * a.G;
     t.window_units = U * ((a.c.sink + (long long)kPosTile - 1) / kPosTile + (a.c.window + (kRowTile - 1) / a.G) / kPosTile + 2);
     t.cta_status = reinterpret_cast<int*>(base + p.status);
-    t.note = reinterpret_cast<int4*>(base + p.note);
+    t.note = reinterpret_cast<RowNote*>(base + p.note);
     t.head = reinterpret_cast<PlanHead*>(base + p.head);
     t.worker = reinterpret_cast<WorkerRec*>(base + p.worker);
     t.blocks = reinterpret_cast<BlockRec*>(base + p.blocks);

@@ -195,16 +195,18 @@ cudaError_t cc_kv(const RowsArgs& a, int kv_dtype, cudaStream_t s) {
 // attention marked.
 // ---------------------------------------------------------------------------
 constexpr int kMergeRowThreads = 256, kOddRows = 16 * kMergeRowThreads;   // rows whose marks a CTA looks at
+// rows of a CTA: few enough CTAs for one chain of dependent loads to pass over the
+// GPU in two turns or so (with 4 rows a CTA the merge of 152 cut items took 65 us)
+constexpr int kMergePrompt = 32, kMergePrefix = 16;
 
 struct RowParts {
     long long dense;                  // the row's place in `dense` (< 0: in slots)
     int w0, w1;                       // workers of its slots (w1 < w0: no part)
     int r;                            // row of the slots
 };
-// parts of row r of (block, KV head)
-__device__ RowParts parts_of(const RowsTcArgs& t, const PlanHead& plan, int blk, int g, int r, long long dense) {
+// parts of row r of a block's KV head
+__device__ RowParts parts_of(const RowsTcArgs& t, const PlanHead& plan, const BlockRec& k, int g, int r, long long dense) {
     RowParts p = {-1, 0, -1, r % kRowTile};
-    const BlockRec k = t.blocks[blk];
     const int rt = r / kRowTile;
     if (r >= k.n * t.a.G) return p;
     const Item it = item_of(t.a, k, rt);
@@ -216,14 +218,25 @@ __device__ RowParts parts_of(const RowsTcArgs& t, const PlanHead& plan, int blk,
     return p;
 }
 
+// attend_row out of line: seldom called, and the merge keeps its registers
 template <typename KT>
-__global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int statuses, int merges) {
-    __shared__ RowParts s_parts[2][kMergeRowThreads / 16];
-    __shared__ int4 s_row[kMergeRowThreads / 16];           // sequence (< 0: none), token, query head
-    __shared__ int s_list[kOddRows];
+__device__ __noinline__ void attend_again(const RowsArgs* a, long long id) {
+    const int tok = (int)(id / a->Hq), h = (int)(id - (long long)tok * a->Hq), b = a->M > 0 ? tok / a->M : last_at_most(a->row_start, a->B, tok);
+    Seq s;
+    if (!seq_at(*a, b, s)) return;
+    const int j = (int)(tok - s.row0);
+    if (j >= 0 && j < s.n) attend_row<uint16_t, KT>(*a, s, b, j, h, threadIdx.x & 31);
+}
+
+template <typename KT>
+__global__ void __launch_bounds__(kMergeRowThreads, 4) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int statuses, int merges) {
+    __shared__ RowParts s_parts[2][kMergePrompt];
+    __shared__ long long s_row[kMergePrompt];               // row of out (in heads; < 0: none)
+    __shared__ int s_odd[kMergePrompt];                     // the row's result is not finite
+    __shared__ uint16_t s_list[kOddRows];
     __shared__ int s_n;
     const RowsArgs& a = t.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) s_n = 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -242,13 +255,6 @@ __global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __gr
         }
         return;
     }
-    auto again = [&](long long id) {   // the whole warp
-        const int tok = (int)(id / a.Hq), h = (int)(id - (long long)tok * a.Hq), b = a.M > 0 ? tok / a.M : last_at_most(a.row_start, a.B, tok);
-        Seq s;
-        if (!seq_at(a, b, s)) return;
-        const int j = (int)(tok - s.row0);
-        if (j >= 0 && j < s.n) attend_row<uint16_t, KT>(a, s, b, j, h, lane);
-    };
     if ((int)blockIdx.x >= merges) {   // rows that the attention marked
         const long long first = (long long)(blockIdx.x - merges) * kOddRows, rows = (long long)a.T * a.Hq;
         __syncthreads();
@@ -256,72 +262,78 @@ __global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __gr
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if (v.x | v.y | v.z | v.w)
             for (int i = 0; i < 16; ++i)
-                if ((w[i >> 2] >> (8 * (i & 3))) & 0xFFu && first + 16 * tid + i < rows) s_list[atomicAdd(&s_n, 1)] = 16 * tid + i;
+                if ((w[i >> 2] >> (8 * (i & 3))) & 0xFFu && first + 16 * tid + i < rows) s_list[atomicAdd(&s_n, 1)] = (uint16_t)(16 * tid + i);
         __syncthreads();
-        for (int i = warp; i < s_n; i += kMergeRowThreads / 32) again(first + s_list[i]);
+        for (int i = warp; i < s_n; i += kMergeRowThreads / 32) attend_again<KT>(&a, first + s_list[i]);
         return;
     }
     const int hd = a.hd, gt = hd >> 2, per = kMergeRowThreads / gt, sub = tid / gt, d = 4 * (tid - sub * gt);
-    if (tid < per) {
+    const int rc = a.M == 0 ? kMergePrompt : kMergePrefix;
+    if (tid < rc) {
         RowParts p0 = {-1, 0, -1, 0}, p1 = p0;
-        int4 row = make_int4(-1, 0, 0, 0);
+        long long row = -1;
         if (a.M == 0) {
-            const int rows_at = kRowTile / per, w = blockIdx.x / rows_at, r = (blockIdx.x - w * rows_at) * per + tid;
-            const int4 n = t.note[w];
+            const int rows_at = kRowTile / kMergePrompt, w = blockIdx.x / rows_at, r = (blockIdx.x - w * rows_at) * kMergePrompt + tid;
+            const RowNote n = t.note[w];
             // (an attention that gave up may have left anything: it stays in bounds)
-            if (n.x >= 0 && n.x < a.B && n.y >= 0 && n.y < a.c.Hkv && n.z >= 0 && n.w > w && n.w < t.workers) {
-                const long long at = (long long)n.z * kRowTile + r;
-                if (at < (long long)t.blocks[n.x].n * a.G) {
-                    const int j = (int)at / a.G;
-                    p0.w0 = w;
-                    p0.w1 = n.w;
-                    p0.r = r;
-                    row = make_int4(n.x, j, n.y * a.G + (int)at - j * a.G, 0);
-                }
+            if (n.last > w && n.last < t.workers && r < n.rows && n.rows <= kRowTile && n.r0 >= 0 && n.g >= 0 && n.g < a.c.Hkv) {
+                const int at = n.r0 + r, j = at / a.G;
+                row = ((long long)n.row0 + j) * a.Hq + n.g * a.G + at - j * a.G;
+                if (row < 0 || row >= (long long)a.T * a.Hq) row = -1;
+                p0.w0 = w;
+                p0.w1 = n.last;
+                p0.r = r;
             }
         } else {
-            const long long id = (long long)blockIdx.x * per + tid;
+            const long long id = (long long)blockIdx.x * kMergePrefix + tid;
             const int tok = (int)(id / a.Hq), b = tok / a.M, j = tok - b * a.M, h = (int)(id - (long long)tok * a.Hq);
-            Seq s;
-            if (b < a.B && seq_at(a, b, s) && j < s.n) {
+            if (b < a.B) {
                 const PlanHead plan = *t.head;
-                const int g = h / a.G, r = j * a.G + h - g * a.G;
-                p0 = parts_of(t, plan, a.n_groups + b, g, r, (long long)a.B * a.M * a.Hq);
-                if (s.group >= 0 && s.P > 0)   // the sequence's first row among its group's
-                    p1 = parts_of(t, plan, s.group, g, (int)(t.blocks[a.n_groups + b].q_row - t.blocks[s.group].q_row) + r, 0);
-                row = make_int4(b, j, h, 0);
+                const BlockRec own = t.blocks[a.n_groups + b];
+                if (j < own.n) {
+                    const int g = h / a.G, r = j * a.G + h - g * a.G;
+                    p0 = parts_of(t, plan, own, g, r, (long long)a.B * a.M * a.Hq);
+                    if (own.lo > 0) {   // the sequence's first row among its group's
+                        const int i = last_at_most(a.group_start, a.n_groups, b);
+                        const BlockRec grp = t.blocks[i];
+                        p1 = parts_of(t, plan, grp, g, (int)(own.q_row - grp.q_row) + r, 0);
+                    }
+                    row = id;
+                }
             }
         }
         s_parts[0][tid] = p0;
         s_parts[1][tid] = p1;
         s_row[tid] = row;
-        s_list[tid] = 0;   // 1: the row's result is not finite
+        s_odd[tid] = 0;
     }
     __syncthreads();
-    const int4 row = s_row[sub];
-    if (row.x >= 0) {
+#pragma unroll 2
+    for (int i = sub; i < rc; i += per) {
+        const long long row = s_row[i];
+        if (row < 0) continue;
         float M = kNoScore, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll
         for (int which = 0; which < 2; ++which) {
-            const RowParts p = s_parts[which][sub];
+            const RowParts p = s_parts[which][i];
             constexpr int N = 4;   // parts in flight
 #pragma unroll 1
             for (int w = p.w0; w <= p.w1; w += N) {
                 float2 ml[N];
                 float4 o[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    ml[i] = make_float2(kNoScore, 0.f);
-                    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (w + i > p.w1) continue;
-                    const long long at = (2ll * (w + i) + (w + i == p.w0 ? 1 : 0)) * kRowTile + p.r;
-                    ml[i] = p.dense >= 0 ? t.dense_ml[p.dense] : t.part_ml[at];
-                    o[i] = *reinterpret_cast<const float4*>((p.dense >= 0 ? t.dense + p.dense * hd : t.part + at * hd) + d);
+                for (int e = 0; e < N; ++e) {
+                    ml[e] = make_float2(kNoScore, 0.f);
+                    o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w + e > p.w1) continue;
+                    const long long at = (2ll * (w + e) + (w + e == p.w0 ? 1 : 0)) * kRowTile + p.r;
+                    ml[e] = p.dense >= 0 ? t.dense_ml[p.dense] : t.part_ml[at];
+                    o[e] = *reinterpret_cast<const float4*>((p.dense >= 0 ? t.dense + p.dense * hd : t.part + at * hd) + d);
                 }
                 float mn = M;
 #pragma unroll
-                for (int i = 0; i < N; ++i) mn = fmaxf(mn, ml[i].x);
+                for (int e = 0; e < N; ++e) mn = fmaxf(mn, ml[e].x);
                 const float f = exp2f(M - mn);
                 acc.x *= f;
                 acc.y *= f;
@@ -330,13 +342,13 @@ __global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __gr
                 l *= f;
                 M = mn;
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float e = exp2f(ml[i].x - mn);
-                    acc.x = fmaf(e, o[i].x, acc.x);
-                    acc.y = fmaf(e, o[i].y, acc.y);
-                    acc.z = fmaf(e, o[i].z, acc.z);
-                    acc.w = fmaf(e, o[i].w, acc.w);
-                    l = fmaf(e, ml[i].y, l);
+                for (int e = 0; e < N; ++e) {
+                    const float x = exp2f(ml[e].x - mn);
+                    acc.x = fmaf(x, o[e].x, acc.x);
+                    acc.y = fmaf(x, o[e].y, acc.y);
+                    acc.z = fmaf(x, o[e].z, acc.z);
+                    acc.w = fmaf(x, o[e].w, acc.w);
+                    l = fmaf(x, ml[e].y, l);
                 }
             }
         }
@@ -345,30 +357,21 @@ __global__ void __launch_bounds__(kMergeRowThreads) rows_merge_kernel(const __gr
         acc.y *= inv;
         acc.z *= inv;
         acc.w *= inv;
-        Seq s;
-        seq_at(a, row.x, s);
-        const long long id = (s.row0 + row.y) * a.Hq + row.z;
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + id * hd + d) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + row * hd + d) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
         const float odd = fmaf(acc.x, 0.f, fmaf(acc.y, 0.f, fmaf(acc.z, 0.f, acc.w * 0.f)));
-        if (!(odd == 0.f)) s_list[sub] = 1;
+        if (!(odd == 0.f)) s_odd[i] = 1;
     }
     __syncthreads();
-    for (int i = warp; i < per; i += kMergeRowThreads / 32) {
-        const int4 r = s_row[i];
-        if (r.x < 0 || s_list[i] != 1) continue;
-        Seq s;
-        seq_at(a, r.x, s);
-        attend_row<uint16_t, KT>(a, s, r.x, r.y, r.z, lane);
-    }
+    for (int i = warp; i < rc; i += kMergeRowThreads / 32)
+        if (s_odd[i]) attend_again<KT>(&a, s_row[i]);
 }
 
 }  // namespace
 
 cudaError_t launch_rows_merge(const RowsTcArgs& t, int kv_dtype, cudaStream_t s) {
     const RowsArgs& a = t.a;
-    const int per = kMergeRowThreads / (a.hd >> 2);
-    const long long rows = a.M > 0 ? (long long)a.B * a.M * a.Hq : (long long)t.workers * kRowTile;
-    const long long merges = (rows + per - 1) / per, odd = a.M > 0 ? 0 : ((long long)a.T * a.Hq + kOddRows - 1) / kOddRows;
+    const long long merges = a.M > 0 ? ((long long)a.B * a.M * a.Hq + kMergePrefix - 1) / kMergePrefix : (long long)t.workers * (kRowTile / kMergePrompt);
+    const long long odd = a.M > 0 ? 0 : ((long long)a.T * a.Hq + kOddRows - 1) / kOddRows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(merges + odd + 1));
     cfg.blockDim = dim3(kMergeRowThreads);

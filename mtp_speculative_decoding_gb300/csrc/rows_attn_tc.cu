@@ -142,14 +142,6 @@ __device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
         : "memory");
 }
-__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(
-            r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
-        : "memory");
-}
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_4d(void* dst, const void* tmap, int x, int y, int z, int w, unsigned long long* bar) {
     asm volatile(
@@ -315,7 +307,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         unsigned long long *bf = E4M3 ? rfull : full, *be = E4M3 ? rempty : empty;
         unsigned slot = 0, phase = 0, ti = 0;
         bool ok = true, bad = false;
-        int4 note = make_int4(-1, 0, 0, 0);
+        RowNote note = {-1, 0, 0, 0, 0, 0, {0, 0}};
         Walk p;
         p.start(t, me);
         while (ok && p.next(t)) {
@@ -408,7 +400,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
             }
             if (p.slot == 2 && p.t0 == 0 && a.M == 0)
-                note = make_int4(p.blk, p.g, p.rt, worker_of(t.head->T, t.head->workers, p.tiles_at + (long long)(p.it.n - 1) * kPosTile * a.G));
+                note = RowNote{worker_of(t.head->T, t.head->workers, p.tiles_at + (long long)(p.it.n - 1) * kPosTile * a.G), p.it.rows, p.it.r0,
+                               p.g, p.k.row0, p.k.table, {0, 0}};
         }
         if (rank == 0 && lane == 0 && a.M == 0) t.note[me] = note;
         if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
@@ -691,38 +684,59 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
                 meet(s_full + buf, CG == 2 ? (tc >> 1) & 1 : tc & 1);
                 tc_fence_after();
-                // ---- the row's largest score of the tile (in bits; fp16: with the value scale) ----
-                float mx = -__int_as_float(0x7F800000);
-                {
-                    uint32_t s[2][32];
-                    ld32(sat, s[0]);
+                // ---- probabilities against the reference there is; where a score lies above it,
+                // once more against a new one (the scores stay in place until all is well) ----
+                uint32_t o[64];
+#pragma unroll 1
+                for (int turn = 0;; ++turn) {
+                    uint32_t s[2][16];
+                    tmem_ld16(sat, s[0]);
+                    float2 sum = make_float2(0.f, 0.f);
+                    float mx = -__int_as_float(0x7F800000);   // the row's largest score (in bits; fp16: with the value scale)
+                    const float2 mul = make_float2(qc, qc), add = make_float2(-m, -m);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 8; ++c) {
                         tmem_ld_wait();
-                        if (c < 3) ld32(sat + 32 * (c + 1), s[(c + 1) & 1]);
+                        if (c < 7) tmem_ld16(sat + 16 * (c + 1), s[(c + 1) & 1]);
                         float* z = reinterpret_cast<float*>(s[c & 1]);
-                        if (!whole)
+                        if (!whole) {
+                            const uint32_t on = bits[c >> 1] >> (16 * (c & 1));
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) z[i] = bits[c] >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float x = z[16 * h], y = z[16 * h + 1];
-#pragma unroll
-                            for (int i = 2; i < 16; i += 4) {
-                                x = max3(x, z[16 * h + i], z[16 * h + i + 1]);
-                                if (i + 3 < 16) y = max3(y, z[16 * h + i + 2], z[16 * h + i + 3]);
-                            }
-                            x = fmaxf(x, y);
-                            if (E4M3) {
-                                const float2 sc = m_sc[mi * 8 + 2 * c + h];
-                                x = fmaf(x, sc.x * qc, sc.y);
-                            }
-                            mx = fmaxf(mx, x);
+                            for (int i = 0; i < 16; ++i) z[i] = on >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
                         }
+                        float x = z[0], y = z[1];
+#pragma unroll
+                        for (int i = 2; i < 14; i += 4) {
+                            x = max3(x, z[i], z[i + 1]);
+                            y = max3(y, z[i + 2], z[i + 3]);
+                        }
+                        x = max3(x, y, fmaxf(z[14], z[15]));
+                        float2 cm = mul, ca = add, part = make_float2(0.f, 0.f);
+                        float un = 1.f;
+                        if (E4M3) {
+                            const float2 sc = m_sc[mi * 8 + c];
+                            cm.x = cm.y = sc.x * qc;
+                            ca.x = ca.y = sc.y + S::kBias - m;
+                            un = ex2(-sc.y);   // the sum goes without the value scale
+                            x = fmaf(x, cm.x, sc.y);
+                        }
+                        mx = fmaxf(mx, x);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            float2 e = fma2(make_float2(z[i], z[i + 1]), cm, ca);
+                            e.x = ex2(e.x);
+                            e.y = ex2(e.y);
+                            if (E4M3) part = add2(part, e);
+                            else sum = add2(sum, e);
+                            o[8 * c + (i >> 1)] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                        }
+                        if (E4M3) sum = fma2(part, make_float2(un, un), sum);
                     }
                     if (!E4M3) mx *= qc;
-                }
-                if (__any_sync(0xffffffffu, live && mx > m + S::kSlack)) {
+                    if (turn > 0 || !__any_sync(0xffffffffu, live && mx > m + S::kSlack)) {
+                        l += sum.x + sum.y;
+                        break;
+                    }
                     // move the references, and with them what has been summed
                     const float mn = fmaxf(mx, m), f = ex2(m - mn);
                     l *= f;
@@ -731,56 +745,19 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         meet_values(tc - 1);
 #pragma unroll 1
                         for (int c = 0; c < HD; c += 32) {
-                            uint32_t o[32];
-                            ld32(tmem + lanes + S::O0 + q * S::OC + c, o);
+                            uint32_t v[32];
+                            ld32(tmem + lanes + S::O0 + q * S::OC + c, v);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            st32(tmem + lanes + S::O0 + q * S::OC + c, o);
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                            st32(tmem + lanes + S::O0 + q * S::OC + c, v);
                         }
                         st_wait();
                         tc_fence_before();
                     }
                 }
-                // ---- probabilities, over the scores ----
-                {
-                    uint32_t s[2][32];
-                    ld32(sat, s[0]);
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld_wait();
-                        if (c < 3) ld32(sat + 32 * (c + 1), s[(c + 1) & 1]);
-                        float* z = reinterpret_cast<float*>(s[c & 1]);
-                        if (!whole)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) z[i] = bits[c] >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
-                        uint32_t o[16];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float2 mul = make_float2(qc, qc), add = make_float2(-m, -m), part = make_float2(0.f, 0.f);
-                            float un = 1.f;
-                            if (E4M3) {
-                                const float2 sc = m_sc[mi * 8 + 2 * c + h];
-                                mul.x = mul.y = sc.x * qc;
-                                add.x = add.y = sc.y + S::kBias - m;
-                                un = ex2(-sc.y);   // the sum goes without the value scale
-                            }
-#pragma unroll
-                            for (int i = 16 * h; i < 16 * h + 16; i += 2) {
-                                float2 e = fma2(make_float2(z[i], z[i + 1]), mul, add);
-                                e.x = ex2(e.x);
-                                e.y = ex2(e.y);
-                                if (E4M3) part = add2(part, e);
-                                else sum = add2(sum, e);
-                                o[i >> 1] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
-                            }
-                            if (E4M3) sum = fma2(part, make_float2(un, un), sum);
-                        }
-                        st16(sat + 16 * c, o);
-                    }
-                    l += sum.x + sum.y;
-                }
+                st32(sat, *reinterpret_cast<const uint32_t(*)[32]>(o));   // over the scores
+                st32(sat + 32, *reinterpret_cast<const uint32_t(*)[32]>(o + 32));
                 if (!whole && q == 0) {
                     // value rows that no row of the item attends may hold anything: zero
                     // them (this thread's position; a weight of zero would make a NaN of it)

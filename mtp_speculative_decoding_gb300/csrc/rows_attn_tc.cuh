@@ -47,6 +47,13 @@ struct __align__(16) WorkerRec {
     long long begin;                  // the item's first unit
     int blk, g, rt, pad_;
 };
+// an item that begins in a worker's share and ends behind it
+struct __align__(16) RowNote {
+    int last;                         // worker with its last tile (-1: there is no such item)
+    int rows, r0, g;                  // rows [r0, r0 + rows) of the block, KV head
+    int row0, b;                      // the sequence's first token in out, the sequence
+    int pad_[2];
+};
 struct PlanHead {
     long long T;                      // units in all
     int open, workers;                // units before an item's tiles / U; workers with a share
@@ -65,7 +72,7 @@ struct RowsTcArgs {
     uint16_t* staged;                 // [rows][hd]
     float* q_scale;                   // e4m3: [rows] a staged row's power of two times the softmax scale
     int* cta_status;                  // [CTAs], and behind them the plan's
-    int4* note;                       // prompts, [workers]: the item that begins in a worker's share and ends behind it
+    RowNote* note;                    // prompts, [workers]
     float* part;                      // [2 workers][kRowTile][hd]
     float2* part_ml;                  // their maxima and sums
     uint8_t* odd;                     // prompts, [T * Hq]: the row's result is not finite
