@@ -105,6 +105,18 @@ __device__ __forceinline__ void arrive_lead(unsigned long long* bar) {
             "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
             : "memory");
 }
+// The same for what lies in tensor memory alone, which the tcgen05 fences order: a
+// release at cluster scope would wait for the epilogue's stores to global memory.
+template <int CG>
+__device__ __forceinline__ void arrive_lead_relaxed(unsigned long long* bar) {
+    if (CG == 1) mbar_arrive(bar);
+    else
+        asm volatile(
+            "{\n\t.reg .b32 a;\n\t"
+            "mapa.shared::cluster.u32 a, %0, 0;\n\t"
+            "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
+            : "memory");
+}
 template <int CG>
 __device__ __forceinline__ bool try_wait(unsigned long long* bar, unsigned int parity) {
     if (CG == 1) return mbar_try_wait(bar, parity);
@@ -758,6 +770,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
                 st32(sat, *reinterpret_cast<const uint32_t(*)[32]>(o));   // over the scores
                 st32(sat + 32, *reinterpret_cast<const uint32_t(*)[32]>(o + 32));
+                bool zeroed = false;
                 if (!whole && q == 0) {
                     // value rows that no row of the item attends may hold anything: zero
                     // them (this thread's position; a weight of zero would make a NaN of it)
@@ -780,12 +793,16 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
+                        zeroed = true;
                     }
                 }
                 st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_lead<CG>(p_full + buf);
+                if (lane == 0) {
+                    if (zeroed) arrive_lead<CG>(p_full + buf);
+                    else arrive_lead_relaxed<CG>(p_full + buf);
+                }
                 ++tc;
                 ++ti;
             }
@@ -833,7 +850,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_lead<CG>(o_free + q);
+            if (lane == 0) arrive_lead_relaxed<CG>(o_free + q);
             if (a.M == 0 && live) t.odd[orow] = out && !(odd == 0.f);
         }
     }
