@@ -182,7 +182,7 @@ RowsSpace rows_space(const mtp_kv_cache* c, int B, int M, int64_t T, int n_q_hea
             p.dense_ml = take(2 * rows * sizeof(float2));
             p.dense = take(2 * rows * hd * sizeof(float));
         } else {
-            p.odd = take((rows + 4095) / 4096 * 4096);
+            p.odd = take(2 * ((rows + 4095) / 4096 * 4096));
         }
     }
     p.end = off;
@@ -242,6 +242,7 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
     t.part = reinterpret_cast<float*>(base + p.part);
     t.part_ml = reinterpret_cast<float2*>(base + p.part_ml);
     t.odd = reinterpret_cast<uint8_t*>(base + p.odd);
+    t.odd_plane = (T * a.Hq + 4095) / 4096 * 4096;
     t.dense = reinterpret_cast<float*>(base + p.dense);
     t.dense_ml = reinterpret_cast<float2*>(base + p.dense_ml);
     t.timeout_ns = kWaitLimitNs;

@@ -229,7 +229,7 @@ __device__ __noinline__ void attend_again(const RowsArgs* a, long long id) {
 }
 
 template <typename KT>
-__global__ void __launch_bounds__(kMergeRowThreads, 4) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int statuses, int merges) {
+__global__ void __launch_bounds__(kMergeRowThreads, 4) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int statuses, int merges, int planes) {
     __shared__ RowParts s_parts[2][kMergePrompt];
     __shared__ long long s_row[kMergePrompt];               // row of out (in heads; < 0: none)
     __shared__ int s_odd[kMergePrompt];                     // the row's result is not finite
@@ -258,7 +258,14 @@ __global__ void __launch_bounds__(kMergeRowThreads, 4) rows_merge_kernel(const _
     if ((int)blockIdx.x >= merges) {   // rows that the attention marked
         const long long first = (long long)(blockIdx.x - merges) * kOddRows, rows = (long long)a.T * a.Hq;
         __syncthreads();
-        const uint4 v = *reinterpret_cast<const uint4*>(t.odd + first + 16 * tid);
+        uint4 v = *reinterpret_cast<const uint4*>(t.odd + first + 16 * tid);
+        if (planes > 1) {   // the marks of both threads of a row
+            const uint4 w = *reinterpret_cast<const uint4*>(t.odd + t.odd_plane + first + 16 * tid);
+            v.x |= w.x;
+            v.y |= w.y;
+            v.z |= w.z;
+            v.w |= w.w;
+        }
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         if (v.x | v.y | v.z | v.w)
             for (int i = 0; i < 16; ++i)
@@ -381,9 +388,10 @@ cudaError_t launch_rows_merge(const RowsTcArgs& t, int kv_dtype, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    const int planes = rows_halves(kv_dtype == MTP_DTYPE_E4M3, a.hd);
     const int statuses = t.workers * rows_pair(a.hd) + 1;   // the CTAs' and the plan's
-    return kv_dtype == MTP_DTYPE_E4M3 ? cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint8_t>, t, statuses, (int)merges)
-                                      : cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint16_t>, t, statuses, (int)merges);
+    return kv_dtype == MTP_DTYPE_E4M3 ? cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint8_t>, t, statuses, (int)merges, planes)
+                                      : cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint16_t>, t, statuses, (int)merges, planes);
 }
 
 cudaError_t launch_rows_cc(const RowsArgs& a, int dtype, int kv_dtype, cudaStream_t s) {

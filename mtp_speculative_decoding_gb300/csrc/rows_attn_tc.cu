@@ -174,6 +174,20 @@ __device__ __forceinline__ void store_32b(void* p, const uint32_t* w) {
                  "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
+// two warps (64 threads) at barrier `id`: whether any of them says so
+__device__ __forceinline__ bool pair_vote(int id, bool x) {
+    unsigned int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %1, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((unsigned)x)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void pair_barrier(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -220,7 +234,9 @@ struct RowShape {
     static constexpr int KP = kPosTile / CG, VD = HD / CG;         // positions of K, dimensions of V in this CTA
     static constexpr int QB = 128 * HD * 2;                        // bytes of a row tile
     static constexpr int SLOTB = rows_slot_bytes(HD), RAWB = SLOTB / 2;
-    static constexpr int SW = 4 * NQ;                              // softmax warps
+    static constexpr int NH = rows_halves(E4M3, HD);               // threads of a row: each takes its share of a tile's positions
+    static constexpr int CW = kPosTile / NH;                       // positions of a thread
+    static constexpr int SW = 4 * NQ * NH;                         // softmax warps
     static constexpr int CONV = SW, PROD = SW + (E4M3 ? 4 : 0), MMA = PROD + 1, QUERY = PROD + 2;
     static constexpr int THREADS = (QUERY + 1) * 32;
     static constexpr int O0 = 256, OC = HD;                        // accumulators' columns, behind two score buffers of 128
@@ -245,7 +261,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
     uint4* m_bits = reinterpret_cast<uint4*>(raw + (size_t)NR * S::RAWB);       // [kRowsMeta] positions that are there
     float2* m_sc = reinterpret_cast<float2*>(m_bits + kRowsMeta);               // [kRowsMeta][8] key scale, value scale's exponent, every 16 positions
     int4* m_flag = reinterpret_cast<int4*>(m_sc + kRowsMeta * 8);               // [kRowsMeta] x: all positions there
-    unsigned long long* bars = reinterpret_cast<unsigned long long*>(m_flag + kRowsMeta);
+    float* s_x = reinterpret_cast<float*>(m_flag + kRowsMeta);                  // [NQ][2][128] what the threads of a row tell each other
+    unsigned long long* bars = reinterpret_cast<unsigned long long*>(s_x + 2 * kRowTile);
     unsigned long long *full = bars, *empty = full + kRowsSlots, *peer = empty + kRowsSlots, *rfull = peer + kRowsSlots,
                        *rempty = rfull + kRowsRaw, *meta = rempty + kRowsRaw, *s_full = meta + kRowsMeta, *p_full = s_full + 2,
                        *pv_done = p_full + 2, *o_free = pv_done + 2, *q_full = o_free + 2, *q_peer = q_full + 1, *q_free = q_peer + 1,
@@ -268,9 +285,9 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         for (int i = 0; i < kRowsMeta; ++i) mbar_init(meta + i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 4 * CG);
+            mbar_init(p_full + i, 4 * CG * S::NH);
             mbar_init(pv_done + i, 1);
-            mbar_init(o_free + i, 4 * CG);
+            mbar_init(o_free + i, 4 * CG * S::NH);
         }
         mbar_init(q_full, 1);
         mbar_init(q_peer, 1);
@@ -568,40 +585,44 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 __syncwarp();
                 next();
             };
-            while (ok && p.next(t)) {
+            bool more_pieces = p.next(t);
+            while (ok && more_pieces) {
+                const int n = p.n, nq = p.it.rows > 128 ? 2 : 1;   // (p moves on before this piece's last product)
                 hold(q_full, seg & 1);
                 if (CG == 2) hold(q_peer, seg & 1);
                 ++seg;
                 if (CG == 2) {
                     const unsigned t0 = tq[0];
 #pragma unroll 1
-                    for (int k = 0; k <= p.n && ok; ++k) {
-                        if (k < p.n) {
+                    for (int k = 0; k <= n && ok; ++k) {
+                        if (k < n) {
                             arrived();
                             scores(0, (t0 + k) & 1);
                             done();
-                            if (k == p.n - 1 && ok && elect()) commit<CG>(q_free);
+                            if (k == n - 1 && ok && elect()) commit<CG>(q_free);
                             __syncwarp();
+                        } else {
+                            more_pieces = p.next(t);
                         }
                         if (k > 0) {
                             const unsigned u = t0 + k - 1;
                             if (k == 1) hold(o_free, (sq[0] & 1) ^ 1);
-                            hold(p_full + (u & 1), (u >> 1) & 1);
                             arrived();
+                            hold(p_full + (u & 1), (u >> 1) & 1);
                             values(0, u & 1, slot, k == 1);
                             done();
                         }
                     }
-                    tq[0] += p.n;
+                    tq[0] += n;
                     ++sq[0];
                 } else {
-                    const int nq = p.it.rows > 128 ? 2 : 1;
                     // slots take turns: K tile k, V tile k
                     unsigned vslot = 0, vphase = 0;
 #pragma unroll 1
-                    for (int k = 0; k <= p.n && ok; ++k) {
-                        const bool more = k < p.n;
+                    for (int k = 0; k <= n && ok; ++k) {
+                        const bool more = k < n;
                         if (more) arrived();
+                        else more_pieces = p.next(t);
                         if (k > 0) hold(full + vslot, vphase);
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
@@ -617,7 +638,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         __syncwarp();
                         if (more) {
                             done();
-                            if (k == p.n - 1 && ok && elect()) commit<CG>(q_free);
+                            if (k == n - 1 && ok && elect()) commit<CG>(q_free);
                             __syncwarp();
                             vslot = slot;
                             vphase = phase;
@@ -627,7 +648,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
                         if (q < nq) {
-                            tq[q] += p.n;
+                            tq[q] += n;
                             ++sq[q];
                         }
                 }
@@ -642,8 +663,10 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         // ------------------------------------------------------------------
         // softmax and epilogue: thread = row
         // ------------------------------------------------------------------
-        const int q = warp >> 2, row = tid & 127;            // row tile of this CTA, row of it
+        constexpr int NH = S::NH, CW = S::CW;
+        const int q = warp / (4 * NH), half = (warp >> 2) % NH, row = tid & 127;   // row tile of this CTA, share of a tile, row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t oat = tmem + lanes + S::O0 + q * S::OC + half * (HD / NH);   // this thread's part of the accumulator
         unsigned tc = 0, ti = 0, g0 = 0;                     // tiles of this row tile, of the CTA; ring slots before this piece
         auto meet = [&](unsigned long long* bar, unsigned parity) {
             wait(bar, parity);
@@ -655,18 +678,34 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             __syncwarp();
             tc_fence_after();
         };
+        // the warps of the same 32 rows: whether any of their threads says so; and what the
+        // other thread of this row has
+        auto any_of_rows = [&](bool x) -> bool {
+            if (NH == 1) return __any_sync(0xffffffffu, x);
+            return pair_vote(1 + q * 4 + (warp & 3), x);
+        };
+        auto others = [&](float x) -> float {
+            s_x[(q * 2 + half) * 128 + row] = x;
+            pair_barrier(1 + q * 4 + (warp & 3));
+            const float y = s_x[(q * 2 + (half ^ 1)) * 128 + row];
+            pair_barrier(1 + q * 4 + (warp & 3));
+            return y;
+        };
         Walk p;
         p.start(t, me);
-        while (p.next(t)) {
+        bool more_pieces = p.next(t);
+        while (more_pieces) {
             const int ofs = (CG == 2 ? rank : q) * 128;      // of the row tile in the item
             if (CG == 1 && p.it.rows <= ofs) {               // not there: the other row tile's alone
                 for (int k = 0; k < p.n; ++k, ++ti) meet(meta + ti % kRowsMeta, (ti / kRowsMeta) & 1);   // (in step with the phases)
                 g0 += 2 * p.n;
+                more_pieces = p.next(t);
                 continue;
             }
             const bool live = ofs + row < p.it.rows;
             const int r = p.it.r0 + (live ? ofs + row : p.it.rows - 1), tok = (int)udiv((unsigned)r, (unsigned)a.G);   // row of the block, its token
             const int pos_q = p.k.len + tok, end = p.k.group ? p.k.hi : pos_q + 1;   // attends [.., end)
+            const int low = a.c.window > 0 && pos_q + 1 > a.c.window ? pos_q + 1 - a.c.window : 0;
             // what a score is multiplied by: the softmax scale, and what the staged row was divided by
             const float qc = E4M3 ? t.q_scale[p.k.q_row + (long long)p.g * p.k.q_stride + r] : a.scale;
             float m = kNoScore, l = 0.f;
@@ -680,103 +719,130 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 // every row of the item attends every position of the tile
                 const bool whole = m_flag[mi].x != 0 && t0 >= p.k.lo && (p.k.group ? t0 + kPosTile <= p.k.hi : t0 + kPosTile - 1 <= p.it.p_first) &&
                                    (a.c.window == 0 || t0 > p.it.p_last - a.c.window || t0 + kPosTile <= a.c.sink);
-                uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
-                if (!whole) {
-                    const uint4 b = m_bits[mi];
-                    bits[0] = b.x; bits[1] = b.y; bits[2] = b.z; bits[3] = b.w;
-                    const int low = a.c.window > 0 && pos_q + 1 > a.c.window ? pos_q + 1 - a.c.window : 0;
+                uint32_t bits[CW / 32];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c0 = t0 + 32 * i;
-                        auto below = [&](int e) { return e - c0 >= 32 ? ~0u : e - c0 <= 0 ? 0u : (1u << (e - c0)) - 1u; };   // positions < e
-                        uint32_t on = below(end) & ~below(p.k.lo);
-                        if (low > 0) on &= ~below(low) | below(a.c.sink);
-                        bits[i] &= on;
-                    }
-                }
+                for (int i = 0; i < CW / 32; ++i) bits[i] = ~0u;
+                auto on_bits = [&](int i) {   // positions [32 i, 32 i + 32) of the tile that this row attends
+                    const uint32_t there = reinterpret_cast<const uint32_t*>(m_bits + mi)[i];
+                    const int c0 = t0 + 32 * i;
+                    auto below = [&](int e) { return e - c0 >= 32 ? ~0u : e - c0 <= 0 ? 0u : (1u << (e - c0)) - 1u; };   // positions < e
+                    uint32_t on = below(end) & ~below(p.k.lo);
+                    if (low > 0) on &= ~below(low) | below(a.c.sink);
+                    return there & on;
+                };
+                if (!whole)
+#pragma unroll
+                    for (int i = 0; i < CW / 32; ++i) bits[i] = on_bits(half * (CW / 32) + i);
                 meet(s_full + buf, CG == 2 ? (tc >> 1) & 1 : tc & 1);
                 tc_fence_after();
+                if (k == 0) {
+                    // a first reference from the tile's first 16 positions: seldom does a score lie
+                    // 2^kSlack above it
+                    uint32_t s[16];
+                    tmem_ld16(sat, s);
+                    tmem_ld_wait();
+                    const uint32_t on = whole ? ~0u : on_bits(0);
+                    float x = -__int_as_float(0x7F800000);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x = fmaxf(x, on >> i & 1u ? __uint_as_float(s[i]) : -__int_as_float(0x7F800000));
+                    if (E4M3) x = fmaf(x, m_sc[mi * 8].x * qc, m_sc[mi * 8].y);
+                    else x *= qc;
+                    m = fmaxf(m, x);
+                }
                 // ---- probabilities against the reference there is; where a score lies above it,
                 // once more against a new one (the scores stay in place until all is well) ----
-                uint32_t o[64];
+                constexpr int CH = E4M3 && NH == 1 ? 16 : 32;   // positions of a load (registers)
+                uint32_t o[CW / 2];
 #pragma unroll 1
                 for (int turn = 0;; ++turn) {
-                    uint32_t s[2][16];
-                    tmem_ld16(sat, s[0]);
-                    float2 sum = make_float2(0.f, 0.f);
+                    uint32_t s[2][CH];
+                    auto fetch = [&](int c) {
+                        if constexpr (CH == 16) tmem_ld16(sat + half * CW + CH * c, s[c & 1]);
+                        else ld32(sat + half * CW + CH * c, s[c & 1]);
+                    };
+                    fetch(0);
+                    if (CW / CH == 2) fetch(1);
+                    float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
                     float mx = -__int_as_float(0x7F800000);   // the row's largest score (in bits; fp16: with the value scale)
-                    const float2 mul = make_float2(qc, qc), add = make_float2(-m, -m);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        tmem_ld_wait();
-                        if (c < 7) tmem_ld16(sat + 16 * (c + 1), s[(c + 1) & 1]);
-                        float* z = reinterpret_cast<float*>(s[c & 1]);
-                        if (!whole) {
-                            const uint32_t on = bits[c >> 1] >> (16 * (c & 1));
+                    for (int c = 0; c < CW / CH; ++c) {
+                        if (c == 0 || CW / CH > 2) tmem_ld_wait();
+                        if (CW / CH > 2 && c + 1 < CW / CH) fetch(c + 1);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) z[i] = on >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
-                        }
-                        float x = z[0], y = z[1];
+                        for (int h = 0; h < CH / 16; ++h) {
+                            float* z = reinterpret_cast<float*>(s[c & 1]) + 16 * h;
+                            const int at = c * CH + 16 * h;     // of this thread's positions
+                            if (!whole) {
+                                const uint32_t on = bits[at >> 5] >> (at & 31);
 #pragma unroll
-                        for (int i = 2; i < 14; i += 4) {
-                            x = max3(x, z[i], z[i + 1]);
-                            y = max3(y, z[i + 2], z[i + 3]);
-                        }
-                        x = max3(x, y, fmaxf(z[14], z[15]));
-                        float2 cm = mul, ca = add, part = make_float2(0.f, 0.f);
-                        float un = 1.f;
-                        if (E4M3) {
-                            const float2 sc = m_sc[mi * 8 + c];
-                            cm.x = cm.y = sc.x * qc;
-                            ca.x = ca.y = sc.y + S::kBias - m;
-                            un = ex2(-sc.y);   // the sum goes without the value scale
-                            x = fmaf(x, cm.x, sc.y);
-                        }
-                        mx = fmaxf(mx, x);
+                                for (int i = 0; i < 16; ++i) z[i] = on >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
+                            }
+                            float x = z[0], y = z[1];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float2 e = fma2(make_float2(z[i], z[i + 1]), cm, ca);
-                            e.x = ex2(e.x);
-                            e.y = ex2(e.y);
-                            if (E4M3) part = add2(part, e);
-                            else sum = add2(sum, e);
-                            o[8 * c + (i >> 1)] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                            for (int i = 2; i < 14; i += 4) {
+                                x = max3(x, z[i], z[i + 1]);
+                                y = max3(y, z[i + 2], z[i + 3]);
+                            }
+                            x = max3(x, y, fmaxf(z[14], z[15]));
+                            float2 cm = make_float2(qc, qc), ca = make_float2(-m, -m), part = make_float2(0.f, 0.f);
+                            float un = 1.f;
+                            if (E4M3) {
+                                const float2 sc = m_sc[mi * 8 + half * (CW / 16) + (at >> 4)];
+                                cm.x = cm.y = sc.x * qc;
+                                ca.x = ca.y = sc.y + S::kBias - m;
+                                un = ex2(-sc.y);   // the sum goes without the value scale
+                                x = fmaf(x, cm.x, sc.y);
+                            }
+                            mx = fmaxf(mx, x);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                float2 e = fma2(make_float2(z[i], z[i + 1]), cm, ca);
+                                e.x = ex2(e.x);
+                                e.y = ex2(e.y);
+                                if (E4M3) part = add2(part, e);
+                                else if (i & 2) sum2 = add2(sum2, e);
+                                else sum = add2(sum, e);
+                                o[(at + i) >> 1] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                            }
+                            if (E4M3) sum = fma2(part, make_float2(un, un), sum);
                         }
-                        if (E4M3) sum = fma2(part, make_float2(un, un), sum);
                     }
                     if (!E4M3) mx *= qc;
-                    if (turn > 0 || !__any_sync(0xffffffffu, live && mx > m + S::kSlack)) {
-                        l += sum.x + sum.y;
+                    // (with two threads a row the vote says also that both have read their scores)
+                    const bool over = any_of_rows(live && mx > m + S::kSlack);
+                    if (turn > 0 || !over) {
+                        l += (sum.x + sum.y) + (sum2.x + sum2.y);
                         break;
                     }
                     // move the references, and with them what has been summed
+                    if (NH == 2) mx = fmaxf(mx, others(mx));
                     const float mn = fmaxf(mx, m), f = ex2(m - mn);
                     l *= f;
                     m = mn;
                     if (k > 0) {
                         meet_values(tc - 1);
 #pragma unroll 1
-                        for (int c = 0; c < HD; c += 32) {
+                        for (int c = 0; c < HD / NH; c += 32) {
                             uint32_t v[32];
-                            ld32(tmem + lanes + S::O0 + q * S::OC + c, v);
+                            ld32(oat + c, v);
                             tmem_ld_wait();
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                            st32(tmem + lanes + S::O0 + q * S::OC + c, v);
+                            st32(oat + c, v);
                         }
                         st_wait();
                         tc_fence_before();
                     }
                 }
-                st32(sat, *reinterpret_cast<const uint32_t(*)[32]>(o));   // over the scores
-                st32(sat + 32, *reinterpret_cast<const uint32_t(*)[32]>(o + 32));
+#pragma unroll
+                for (int i = 0; i < CW / 64; ++i)   // over the scores
+                    st32(sat + half * (CW / 2) + 32 * i, *reinterpret_cast<const uint32_t(*)[32]>(o + 32 * i));
                 bool zeroed = false;
-                if (!whole && q == 0) {
+                if (!whole && q == 0 && half == 0) {
                     // value rows that no row of the item attends may hold anything: zero
                     // them (this thread's position; a weight of zero would make a NaN of it)
-                    const uint4 b = m_bits[mi];
                     const int pos = t0 + row;
-                    const uint32_t word = row < 32 ? b.x : row < 64 ? b.y : row < 96 ? b.z : b.w;
+                    const uint32_t word = reinterpret_cast<const uint32_t*>(m_bits + mi)[row >> 5];
                     const int last = p.k.group ? p.k.hi : p.it.p_last + 1;
                     const bool any = (word >> (row & 31) & 1u) && pos >= p.k.lo && pos < last &&
                                      (a.c.window == 0 || pos > p.it.p_first - a.c.window || pos < a.c.sink);
@@ -808,50 +874,52 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             }
             g0 += 2 * p.n;
             // ---- the accumulator ----
+            if (NH == 2) l += others(l);
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const bool out = p.slot == 0 && a.M == 0;        // the row's whole result
             const long long orow = ((long long)p.k.row0 + tok) * a.Hq + p.g * a.G + r - tok * a.G;   // (sequences)
-            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + orow * HD;
+            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + orow * HD + half * (HD / NH);
             float* part = nullptr;
             if (!out && live) {
                 if (p.slot == 0) {
                     const long long at = p.k.q_row + (long long)p.g * p.k.q_stride + r + (p.k.group ? 0 : (long long)a.B * a.M * a.Hq);
-                    part = t.dense + at * HD;
-                    t.dense_ml[at] = make_float2(m, l);
+                    part = t.dense + at * HD + half * (HD / NH);
+                    if (half == 0) t.dense_ml[at] = make_float2(m, l);
                 } else {
                     const long long at = (2ll * me + p.slot - 1) * kRowTile + ofs + row;
-                    part = t.part + at * HD;
-                    t.part_ml[at] = make_float2(m, l);
+                    part = t.part + at * HD + half * (HD / NH);
+                    if (half == 0) t.part_ml[at] = make_float2(m, l);
                 }
             }
+            more_pieces = p.next(t);                         // while the last product runs
             meet_values(tc - 1);
-            float odd = 0.f;   // NaN: the product left something that is not finite
+            float odd[4] = {0.f, 0.f, 0.f, 0.f};             // NaN: the product left something that is not finite
 #pragma unroll 1
-            for (int c = 0; c < HD; c += 32) {
-                uint32_t o[32];
-                ld32(tmem + lanes + S::O0 + q * S::OC + c, o);
+            for (int c = 0; c < HD / NH; c += 32) {
+                uint32_t v[32];
+                ld32(oat + c, v);
                 tmem_ld_wait();
                 if (!live) {
                 } else if (out) {
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        const float x = __uint_as_float(o[i]) * inv, y = __uint_as_float(o[i + 1]) * inv;
-                        odd = fmaf(x, 0.f, fmaf(y, 0.f, odd));
+                        const float x = __uint_as_float(v[i]) * inv, y = __uint_as_float(v[i + 1]) * inv;
+                        odd[i >> 1 & 3] = fmaf(x, 0.f, fmaf(y, 0.f, odd[i >> 1 & 3]));
                         w[i >> 1] = pack_bf16(x, y);
                     }
                     store_32b(dst + c, w);
                     store_32b(dst + c + 16, w + 8);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) store_32b(part + c + i, o + i);
+                    for (int i = 0; i < 32; i += 8) store_32b(part + c + i, v + i);
                 }
                 __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_lead_relaxed<CG>(o_free + q);
-            if (a.M == 0 && live) t.odd[orow] = out && !(odd == 0.f);
+            if (a.M == 0 && live) t.odd[half * t.odd_plane + orow] = out && !((odd[0] + odd[1]) + (odd[2] + odd[3]) == 0.f);
         }
     }
     __syncthreads();

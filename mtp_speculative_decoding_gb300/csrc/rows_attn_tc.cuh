@@ -75,7 +75,8 @@ struct RowsTcArgs {
     RowNote* note;                    // prompts, [workers]
     float* part;                      // [2 workers][kRowTile][hd]
     float2* part_ml;                  // their maxima and sums
-    uint8_t* odd;                     // prompts, [T * Hq]: the row's result is not finite
+    uint8_t* odd;                     // prompts, [2][odd_plane]: the row's result is not finite, by each thread that has a share of it
+    long long odd_plane;              // T * Hq, rounded up
     float* dense;                     // shared prefixes, [2][rows][hd] by staged rows: a row's prefix and own part, where one worker had it whole
     float2* dense_ml;
     unsigned long long timeout_ns;
@@ -223,7 +224,9 @@ __host__ __device__ constexpr int rows_slot_bytes(int hd) { return kPosTile * hd
 constexpr int kRowsMeta = 16;         // tiles whose masks and scales the producer may be ahead
 constexpr int kRowsSlots = 8, kRowsRaw = 4;   // ring slots at most
 constexpr int kRowsSmemLimit = 227 * 1024 - 64;
-constexpr int kRowsOther = 1024 + kRowsMeta * (16 + 64 + 16) + (3 * kRowsSlots + 2 * kRowsRaw + kRowsMeta + 16) * 8;
+// threads that share a row of a tile in the softmax
+__host__ __device__ constexpr int rows_halves(bool e4m3, int hd) { return hd == 256 ? 2 : 1; }
+constexpr int kRowsOther = 1024 + 2 * kRowTile * 4 + kRowsMeta * (16 + 64 + 16) + (3 * kRowsSlots + 2 * kRowsRaw + kRowsMeta + 16) * 8;
 // 8-bit caches: codes as they come in take half a slot each
 __host__ __device__ constexpr int rows_raw(bool e4m3, int hd) { return e4m3 ? (hd == 64 ? 4 : 3) : 0; }
 __host__ __device__ constexpr int rows_slots(bool e4m3, int hd) {
