@@ -437,7 +437,7 @@ int mtp_rotate_axes(int64_t rows, int n_axes, const int32_t* positions, const in
     a.norm[0] = q_norm; a.norm[1] = k_norm;
     a.heads[0] = n_q_heads; a.heads[1] = k ? n_k_heads : 0;
     a.pos = positions;
-    a.rows = (int)rows; a.hd = hd; a.pairs = (int)pairs;
+    a.axes = n_axes; a.rows = (int)rows; a.hd = hd; a.pairs = (int)pairs;
     a.eps = rms_eps;
     fill_rope(&a.rope, theta, 2 * (int)pairs);
     for (int i = 0, at = 0, end = sections[0]; i < (int)pairs; ++i) {

@@ -29,6 +29,15 @@ constexpr int kRotThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_constant__ RotateArgs a) {
     constexpr bool FAST = sizeof(T) == 2;
+    // lanes read the tables at different places, which parameters serve one by one
+    __shared__ __align__(16) float s_hi[256], s_lo[256];
+    __shared__ __align__(16) uint8_t s_axis[256];
+    for (int i = threadIdx.x; i < a.pairs; i += kRotThreads) {
+        s_hi[i] = a.rope.hi[i];
+        s_lo[i] = a.rope.lo[i];
+        s_axis[i] = a.axis[i];
+    }
+    __syncthreads();
     const int U = a.hd >> 4, ulog = 31 - __clz(U), all = a.groups[0] + a.groups[1];
     const long long x = (long long)blockIdx.x * kRotThreads + threadIdx.x, unit = x >> ulog;
     const int c = (int)(x & (U - 1));
@@ -44,16 +53,6 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
     const bool turn = 8 * c < a.pairs;
     // the unit's two runs of eight elements
     const int e0 = turn ? 8 * c : 2 * a.pairs + 16 * (c - (a.pairs >> 3)), e1 = turn ? a.pairs + 8 * c : e0 + 8;
-    float cs[8], sn[8];
-    if (turn) {
-        const int32_t* pos = a.pos + row;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float pl, ph;
-            split_pos(pos[(long long)a.axis[8 * c + i] * a.rows], pl, ph);
-            pair_angle<FAST>(pl, ph, a.rope.hi[8 * c + i], a.rope.lo[8 * c + i], cs[i], sn[i]);
-        }
-    }
     const T* src = reinterpret_cast<const T*>(a.in[which]) + row * a.in_sm[which];
     T* dst = reinterpret_cast<T*>(a.out[which]) + row * a.out_sm[which];
     const float* gain = a.norm[which];
@@ -64,22 +63,46 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
             g0[i] = __ldg(gain + e0 + i);
             g1[i] = __ldg(gain + e1 + i);
         }
-    for (int i = 0; i < a.hpt; ++i) {
-        const int h = h0 + i < h1 ? h0 + i : h1 - 1;   // (every lane of the warp takes part in the norm)
-        float p[8], q[8];
-        in8(src + h * a.in_sh[which] + e0, p);
-        in8(src + h * a.in_sh[which] + e1, q);
-        const float r = unit_rms(p, q, a.hd, a.eps);
-        if (gain)
+    float cs[8], sn[8];
+    if (turn) {
+        int at[MTP_MAX_AXES];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                p[e] *= r * g0[e];
-                q[e] *= r * g1[e];
+        for (int i = 0; i < MTP_MAX_AXES; ++i) at[i] = i < a.axes ? a.pos[(long long)i * a.rows + row] : 0;
+        const uint2 ax = *reinterpret_cast<const uint2*>(s_axis + 8 * c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned k = ((i < 4 ? ax.x : ax.y) >> (8 * (i & 3))) & 3u;
+            const int pos = k & 2u ? (k & 1u ? at[3] : at[2]) : (k & 1u ? at[1] : at[0]);
+            float pl, ph;
+            split_pos(pos, pl, ph);
+            pair_angle<FAST>(pl, ph, s_hi[8 * c + i], s_lo[8 * c + i], cs[i], sn[i]);
+        }
+    }
+    constexpr int N = sizeof(T) == 2 ? 4 : 2;   // heads in flight
+#pragma unroll 1
+    for (int i0 = 0; i0 < a.hpt; i0 += N) {
+        float p[N][8], q[N][8];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int h = h0 + i0 + i < h1 ? h0 + i0 + i : h1 - 1;   // (every lane of the warp takes part in the norm)
+            in8(src + h * a.in_sh[which] + e0, p[i]);
+            in8(src + h * a.in_sh[which] + e1, q[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int h = h0 + i0 + i;
+            const float r = unit_rms(p[i], q[i], a.hd, a.eps);
+            if (gain)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[i][e] *= r * g0[e];
+                    q[i][e] *= r * g1[e];
+                }
+            if (turn) unit_rotate(p[i], q[i], cs, sn);
+            if (live && h < h1) {
+                store8(dst + h * a.out_sh[which] + e0, p[i]);
+                store8(dst + h * a.out_sh[which] + e1, q[i]);
             }
-        if (turn) unit_rotate(p, q, cs, sn);
-        if (live && h0 + i < h1) {
-            store8(dst + h * a.out_sh[which] + e0, p);
-            store8(dst + h * a.out_sh[which] + e1, q);
         }
     }
 }
@@ -87,7 +110,10 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
 }  // namespace
 
 cudaError_t launch_rotate_axes(RotateArgs a, int dtype, int sms, cudaStream_t s) {
+    // as many heads in one thread as leave 512 threads an SM: an angle costs as much as
+    // the rest of four elements
     a.hpt = 1;
+    while (a.hpt < 16 && (long long)a.rows * ((a.heads[0] + a.heads[1]) / (2 * a.hpt)) * (a.hd >> 4) >= (long long)sms * 512) a.hpt *= 2;
     for (int w = 0; w < 2; ++w) a.groups[w] = (a.heads[w] + a.hpt - 1) / a.hpt;
     const long long threads = (long long)a.rows * (a.groups[0] + a.groups[1]) * (a.hd >> 4);
     const unsigned grid = (unsigned)((threads + kRotThreads - 1) / kRotThreads);

@@ -89,7 +89,7 @@ struct RotateArgs {
     const float* norm[2];
     int heads[2];
     const int32_t* pos;             // [axes, rows]
-    int rows, hd, pairs;
+    int axes, rows, hd, pairs;
     float eps;
     int hpt, groups[2];             // heads a thread; thread groups of the queries and of the keys
     RopeTab rope;
