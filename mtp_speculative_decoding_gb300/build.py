@@ -24,7 +24,9 @@ UNITS = [("api", "api.cu", []), ("verify", "verify.cu", []), ("noalloc", "noallo
          ("draft_dispatch", "draft_dispatch.cu", []), ("paged_api", "paged_api.cu", []),
          ("kv_append", "kv_append.cu", []), ("paged_attn", "paged_attn.cu", []), ("logprobs", "logprobs.cu", []),
          ("rows_attn", "rows_attn.cu", []), ("rows_prepare", "rows_prepare.cu", []), ("rows_attn_tc_bf16", "rows_attn_tc.cu", []),
-         ("rows_attn_tc_e4m3", "rows_attn_tc.cu", ["-DMTP_PAGED_E4M3"]), ("rotate", "rotate.cu", []),
+         ("rows_attn_tc_e4m3", "rows_attn_tc.cu", ["-DMTP_PAGED_E4M3"]),
+         ("rows_attn_tc_bf16_shared", "rows_attn_tc.cu", ["-DMTP_ROWS_SHARED"]),
+         ("rows_attn_tc_e4m3_shared", "rows_attn_tc.cu", ["-DMTP_PAGED_E4M3", "-DMTP_ROWS_SHARED"]), ("rotate", "rotate.cu", []),
          ("paged_attn_tc_bf16", "paged_attn_tc.cu", []), ("paged_attn_tc_e4m3", "paged_attn_tc.cu", ["-DMTP_PAGED_E4M3"])]
 for _hd in (32, 64, 128, 256, 512):
     for _name, _bf, _tc in (("f32", 0, 0), ("bf16_cc", 1, 0), ("bf16_tc", 1, 1)):

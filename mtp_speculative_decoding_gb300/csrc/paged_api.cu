@@ -153,7 +153,7 @@ bool rows_tc(const mtp_kv_cache* c) {
     return c->kv_dtype != MTP_DTYPE_F32 && (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256);
 }
 struct RowsSpace {
-    size_t status, note, head, worker, blocks, staged, q_scale, odd, part, part_ml, dense, dense_ml, end;
+    size_t status, note, head, worker, blocks, items, cum, cumt, lens, staged, q_scale, odd, part, part_ml, dense, dense_ml, end;
     int workers;
 };
 // (every field grows with B, M and T, so that a workspace sized for more serves less)
@@ -173,7 +173,13 @@ RowsSpace rows_space(const mtp_kv_cache* c, int B, int M, int64_t T, int n_q_hea
         p.note = take((size_t)p.workers * sizeof(RowNote));
         p.head = take(sizeof(PlanHead));
         p.worker = take((size_t)p.workers * sizeof(WorkerRec));
-        p.blocks = take(2 * (size_t)B * sizeof(BlockRec));
+        p.blocks = take((M > 0 ? 3 : 1) * (size_t)B * sizeof(BlockRec));
+        if (M > 0) {
+            p.items = take(((size_t)B * M * (n_q_heads / c->n_kv_heads) / kRowTile + B + 2) * sizeof(int));
+            p.cum = take(((size_t)B + 1) * sizeof(int));
+            p.cumt = take(((size_t)B + 1) * sizeof(int));
+            p.lens = take((size_t)B * sizeof(int));
+        }
         p.part_ml = take(2 * (size_t)p.workers * kRowTile * sizeof(float2));
         p.part = take(2 * (size_t)p.workers * kRowTile * hd * sizeof(float));
         p.staged = take(rows * hd * 2);
@@ -237,6 +243,10 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
     t.head = reinterpret_cast<PlanHead*>(base + p.head);
     t.worker = reinterpret_cast<WorkerRec*>(base + p.worker);
     t.blocks = reinterpret_cast<BlockRec*>(base + p.blocks);
+    t.items = reinterpret_cast<int*>(base + p.items);
+    t.cum = reinterpret_cast<int*>(base + p.cum);
+    t.cumt = reinterpret_cast<int*>(base + p.cumt);
+    t.lens = reinterpret_cast<int*>(base + p.lens);
     t.staged = reinterpret_cast<uint16_t*>(base + p.staged);
     t.q_scale = reinterpret_cast<float*>(base + p.q_scale);
     t.part = reinterpret_cast<float*>(base + p.part);
@@ -252,7 +262,8 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
         return MTP_ERR_UNSUPPORTED;
     const bool e4m3 = c->kv_dtype == MTP_DTYPE_E4M3;
     if (launch_rows_prepare(t, c->kv_dtype, sms, s) != cudaSuccess) return MTP_ERR_CUDA;
-    if ((e4m3 ? launch_rows_tc_e4m3(pp, s) : launch_rows_tc_bf16(pp, s)) != cudaSuccess) return MTP_ERR_CUDA;
+    const auto launch = a.M > 0 ? (e4m3 ? launch_rows_tc_e4m3_shared : launch_rows_tc_bf16_shared) : (e4m3 ? launch_rows_tc_e4m3 : launch_rows_tc_bf16);
+    if (launch(pp, s) != cudaSuccess) return MTP_ERR_CUDA;
     return launch_rows_merge(t, c->kv_dtype, s) == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
 

@@ -188,33 +188,43 @@ cudaError_t cc_kv(const RowsArgs& a, int kv_dtype, cudaStream_t s) {
 
 // ---------------------------------------------------------------------------
 // merge of the parts that the tensor cores left: out = sum_s 2^(m_s - M) o_s /
-// sum_s 2^(m_s - M) l_s over a row's parts, hd / 4 threads a row with four
-// dimensions each.  A prompt's row has parts where its item was cut between
-// workers; with shared prefixes every row has its prefix's and its own.  A result
-// that is not finite is computed again by attend_row, and so are the rows that the
-// attention marked.
+// sum_s 2^(m_s - M) l_s over a row's parts, hd / 16 threads a row.  A prompt's row has
+// parts where its item was cut between workers; with shared prefixes every row has its
+// prefix's and its own.  A result that is not finite is computed again by attend_row,
+// and so are the rows that the attention marked.
 // ---------------------------------------------------------------------------
 constexpr int kMergeRowThreads = 256, kOddRows = 16 * kMergeRowThreads;   // rows whose marks a CTA looks at
-// rows of a CTA: few enough CTAs for one chain of dependent loads to pass over the
-// GPU in two turns or so (with 4 rows a CTA the merge of 152 cut items took 65 us)
-constexpr int kMergePrompt = 32, kMergePrefix = 16;
+__host__ __device__ constexpr int merge_rows(int hd) { return kMergeRowThreads / (hd >> 4); }   // rows of a CTA
 
 struct RowParts {
     long long dense;                  // the row's place in `dense` (< 0: in slots)
-    int w0, w1;                       // workers of its slots (w1 < w0: no part)
+    int w0, w1;                       // workers of its parts (w1 < w0: none)
+    int first;                        // worker in whose share the item begins
     int r;                            // row of the slots
 };
-// parts of row r of a block's KV head
-__device__ RowParts parts_of(const RowsTcArgs& t, const PlanHead& plan, const BlockRec& k, int g, int r, long long dense) {
-    RowParts p = {-1, 0, -1, r % kRowTile};
+// parts of row r (of sequence seq) of a block's KV head; `dense`: where its rows begin there
+__device__ __forceinline__ RowParts parts_of(const RowsTcArgs& t, const Sequences& sq, const PlanHead& plan, const BlockRec& k, int g, int r,
+                                             int seq, long long dense) {
     const int rt = r / kRowTile;
-    if (r >= k.n * t.a.G) return p;
-    const Item it = item_of(t.a, k, rt);
+    const Item it = item_of<true>(t.a, sq, k, rt);
     const long long U = (long long)kPosTile * t.a.G;
     const long long at = k.pre + g * units_before(t, k, plan.open, row_tiles_of(t.a, k)) + units_before(t, k, plan.open, rt) + plan.open * U;
-    p.w0 = worker_of(plan.T, plan.workers, at);
-    p.w1 = worker_of(plan.T, plan.workers, at + (it.n - 1) * U);
-    if (p.w0 == p.w1) p.dense = k.q_row + (long long)g * k.q_stride + r + dense;
+    int x0 = 0, x1 = it.n - 1;        // tiles that the row has a share in: a sequence's, or all
+    if (k.kind == kOwn) {
+        x0 = sq.cumt[seq] - it.lt;
+        x1 = sq.cumt[seq + 1] - it.lt - 1;
+    }
+    RowParts p;
+    p.first = worker_of(plan.T, plan.workers, at);
+    p.dense = -1;
+    p.r = r % kRowTile;
+    if (p.first == worker_of(plan.T, plan.workers, at + (it.n - 1) * U)) {
+        p.dense = k.q_row + (long long)g * k.q_stride + r + dense;
+        p.w0 = p.w1 = p.first;
+        return p;
+    }
+    p.w0 = worker_of(plan.T, plan.workers, at + x0 * U);
+    p.w1 = worker_of(plan.T, plan.workers, at + x1 * U);
     return p;
 }
 
@@ -228,16 +238,17 @@ __device__ __noinline__ void attend_again(const RowsArgs* a, long long id) {
     if (j >= 0 && j < s.n) attend_row<uint16_t, KT>(*a, s, b, j, h, threadIdx.x & 31);
 }
 
-template <typename KT>
-__global__ void __launch_bounds__(kMergeRowThreads, 4) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int statuses, int merges, int planes) {
-    __shared__ RowParts s_parts[2][kMergePrompt];
-    __shared__ long long s_row[kMergePrompt];               // row of out (in heads; < 0: none)
-    __shared__ int s_odd[kMergePrompt];                     // the row's result is not finite
-    __shared__ uint16_t s_list[kOddRows];
+template <typename KT, bool PROMPT>
+__global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_kernel(const __grid_constant__ RowsTcArgs t, int statuses, int merges,
+                                                                                     int planes) {
+    __shared__ long long s_odd[merge_rows(64)];             // rows of out whose result is not finite (< 0: none)
+    __shared__ uint16_t s_list[PROMPT ? kOddRows : 1];
     __shared__ int s_n;
     const RowsArgs& a = t.a;
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) s_n = 0;
+    if (tid < merge_rows(64)) s_odd[tid] = -1;
+    __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((int)blockIdx.x == (int)gridDim.x - 1) {   // the call's status from the CTAs'
@@ -255,9 +266,8 @@ __global__ void __launch_bounds__(kMergeRowThreads, 4) rows_merge_kernel(const _
         }
         return;
     }
-    if ((int)blockIdx.x >= merges) {   // rows that the attention marked
+    if (PROMPT && (int)blockIdx.x >= merges) {   // rows that the attention marked
         const long long first = (long long)(blockIdx.x - merges) * kOddRows, rows = (long long)a.T * a.Hq;
-        __syncthreads();
         uint4 v = *reinterpret_cast<const uint4*>(t.odd + first + 16 * tid);
         if (planes > 1) {   // the marks of both threads of a row
             const uint4 w = *reinterpret_cast<const uint4*>(t.odd + t.odd_plane + first + 16 * tid);
@@ -274,110 +284,131 @@ __global__ void __launch_bounds__(kMergeRowThreads, 4) rows_merge_kernel(const _
         for (int i = warp; i < s_n; i += kMergeRowThreads / 32) attend_again<KT>(&a, first + s_list[i]);
         return;
     }
-    const int hd = a.hd, gt = hd >> 2, per = kMergeRowThreads / gt, sub = tid / gt, d = 4 * (tid - sub * gt);
-    const int rc = a.M == 0 ? kMergePrompt : kMergePrefix;
-    if (tid < rc) {
-        RowParts p0 = {-1, 0, -1, 0}, p1 = p0;
-        long long row = -1;
-        if (a.M == 0) {
-            const int rows_at = kRowTile / kMergePrompt, w = blockIdx.x / rows_at, r = (blockIdx.x - w * rows_at) * kMergePrompt + tid;
-            const RowNote n = t.note[w];
-            // (an attention that gave up may have left anything: it stays in bounds)
-            if (n.last > w && n.last < t.workers && r < n.rows && n.rows <= kRowTile && n.r0 >= 0 && n.g >= 0 && n.g < a.c.Hkv) {
-                const int at = n.r0 + r, j = at / a.G;
-                row = ((long long)n.row0 + j) * a.Hq + n.g * a.G + at - j * a.G;
-                if (row < 0 || row >= (long long)a.T * a.Hq) row = -1;
-                p0.w0 = w;
-                p0.w1 = n.last;
-                p0.r = r;
-            }
-        } else {
-            const long long id = (long long)blockIdx.x * kMergePrefix + tid;
-            const int tok = (int)(id / a.Hq), b = tok / a.M, j = tok - b * a.M, h = (int)(id - (long long)tok * a.Hq);
-            if (b < a.B) {
-                const PlanHead plan = *t.head;
-                const BlockRec own = t.blocks[a.n_groups + b];
-                if (j < own.n) {
-                    const int g = h / a.G, r = j * a.G + h - g * a.G;
-                    p0 = parts_of(t, plan, own, g, r, (long long)a.B * a.M * a.Hq);
-                    if (own.lo > 0) {   // the sequence's first row among its group's
-                        const int i = last_at_most(a.group_start, a.n_groups, b);
-                        const BlockRec grp = t.blocks[i];
-                        p1 = parts_of(t, plan, grp, g, (int)(own.q_row - grp.q_row) + r, 0);
-                    }
-                    row = id;
+    const int hd = a.hd, gt = hd >> 4, per = kMergeRowThreads / gt, sub = tid / gt, d = 4 * (tid - sub * gt), quarter = hd >> 2;
+    RowParts parts[2];
+    long long row = -1;                                     // row of out (in heads)
+    parts[0].w0 = parts[1].w0 = 0;
+    parts[0].w1 = parts[1].w1 = -1;
+    parts[0].dense = parts[1].dense = -1;
+    if (PROMPT) {
+        const int chunks = kRowTile / per > 0 ? kRowTile / per : 1, w = blockIdx.x / chunks, r = (blockIdx.x - w * chunks) * per + sub;
+        const RowNote n = t.note[w];
+        // (an attention that gave up may have left anything: it stays in bounds)
+        if (n.last > w && n.last < t.workers && r < n.rows && n.rows <= kRowTile && n.r0 >= 0 && n.g >= 0 && n.g < a.c.Hkv) {
+            const int at = n.r0 + r, j = at / a.G;
+            row = ((long long)n.row0 + j) * a.Hq + n.g * a.G + at - j * a.G;
+            if (row >= (long long)a.T * a.Hq) row = -1;
+            parts[0].w0 = parts[0].first = w;
+            parts[0].w1 = n.last;
+            parts[0].r = r;
+        }
+    } else {
+        const long long id = (long long)blockIdx.x * per + sub;
+        const int tok = (int)(id / a.Hq), b = tok / a.M, j = tok - b * a.M, h = (int)(id - (long long)tok * a.Hq);
+        if (b < a.B) {
+            const PlanHead plan = *t.head;
+            const Sequences sq = {t.cum, t.cumt, t.lens};
+            const int c0 = sq.cum[b], g = h / a.G, rj = j * a.G + h - g * a.G;
+            if (j < sq.cum[b + 1] - c0) {
+                const long long own_at = (long long)a.B * a.M * a.Hq;
+                const int i = a.n_groups > 0 ? last_at_most(a.group_start, a.n_groups, b) : 0;
+                const BlockRec seq = t.blocks[2 * a.n_groups + b];
+                if (seq.n > 0) {
+                    parts[0] = parts_of(t, sq, plan, seq, g, rj, b, own_at);
+                } else {   // of group i
+                    const BlockRec own = t.blocks[a.n_groups + i], pre = t.blocks[i];
+                    const int r = (c0 - sq.cum[own.table]) * a.G + rj;
+                    parts[0] = parts_of(t, sq, plan, own, g, r, b, own_at);
+                    if (pre.n > 0) parts[1] = parts_of(t, sq, plan, pre, g, r, b, 0);
                 }
+                row = id;
             }
         }
-        s_parts[0][tid] = p0;
-        s_parts[1][tid] = p1;
-        s_row[tid] = row;
-        s_odd[tid] = 0;
     }
-    __syncthreads();
-#pragma unroll 2
-    for (int i = sub; i < rc; i += per) {
-        const long long row = s_row[i];
-        if (row < 0) continue;
+    if (row >= 0) {
         float M = kNoScore, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc[4];
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const RowParts p = s_parts[which][i];
-            constexpr int N = 4;   // parts in flight
+        for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int N = PROMPT ? 2 : 4;   // parts in flight
+#pragma unroll
+        for (int which = 0; which < (PROMPT ? 1 : 2); ++which) {
+            const RowParts p = parts[which];
 #pragma unroll 1
             for (int w = p.w0; w <= p.w1; w += N) {
                 float2 ml[N];
-                float4 o[N];
+                float4 o[N][4];
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
                     ml[e] = make_float2(kNoScore, 0.f);
-                    o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[e][i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (w + e > p.w1) continue;
-                    const long long at = (2ll * (w + e) + (w + e == p.w0 ? 1 : 0)) * kRowTile + p.r;
+                    const long long at = (2ll * (w + e) + (w + e == p.first ? 1 : 0)) * kRowTile + p.r;
+                    const float* src = (p.dense >= 0 ? t.dense + p.dense * hd : t.part + at * hd) + d;
                     ml[e] = p.dense >= 0 ? t.dense_ml[p.dense] : t.part_ml[at];
-                    o[e] = *reinterpret_cast<const float4*>((p.dense >= 0 ? t.dense + p.dense * hd : t.part + at * hd) + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[e][i] = *reinterpret_cast<const float4*>(src + i * quarter);
                 }
                 float mn = M;
 #pragma unroll
                 for (int e = 0; e < N; ++e) mn = fmaxf(mn, ml[e].x);
                 const float f = exp2f(M - mn);
-                acc.x *= f;
-                acc.y *= f;
-                acc.z *= f;
-                acc.w *= f;
                 l *= f;
                 M = mn;
+                float x[N];
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const float x = exp2f(ml[e].x - mn);
-                    acc.x = fmaf(x, o[e].x, acc.x);
-                    acc.y = fmaf(x, o[e].y, acc.y);
-                    acc.z = fmaf(x, o[e].z, acc.z);
-                    acc.w = fmaf(x, o[e].w, acc.w);
-                    l = fmaf(x, ml[e].y, l);
+                    x[e] = exp2f(ml[e].x - mn);
+                    l = fmaf(x[e], ml[e].y, l);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[i].x *= f;
+                    acc[i].y *= f;
+                    acc[i].z *= f;
+                    acc[i].w *= f;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        acc[i].x = fmaf(x[e], o[e][i].x, acc[i].x);
+                        acc[i].y = fmaf(x[e], o[e][i].y, acc[i].y);
+                        acc[i].z = fmaf(x[e], o[e][i].z, acc[i].z);
+                        acc[i].w = fmaf(x[e], o[e][i].w, acc[i].w);
+                    }
                 }
             }
         }
         const float inv = zero_sum(l);
-        acc.x *= inv;
-        acc.y *= inv;
-        acc.z *= inv;
-        acc.w *= inv;
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + row * hd + d) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-        const float odd = fmaf(acc.x, 0.f, fmaf(acc.y, 0.f, fmaf(acc.z, 0.f, acc.w * 0.f)));
-        if (!(odd == 0.f)) s_odd[i] = 1;
+        float odd = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[i].x *= inv;
+            acc[i].y *= inv;
+            acc[i].z *= inv;
+            acc[i].w *= inv;
+            odd += fmaf(acc[i].x, 0.f, fmaf(acc[i].y, 0.f, fmaf(acc[i].z, 0.f, acc[i].w * 0.f)));
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + row * hd + d + i * quarter) =
+                make_uint2(pack_bf16(acc[i].x, acc[i].y), pack_bf16(acc[i].z, acc[i].w));
+        }
+        if (!(odd == 0.f)) s_odd[sub] = row;
     }
     __syncthreads();
-    for (int i = warp; i < rc; i += kMergeRowThreads / 32)
-        if (s_odd[i]) attend_again<KT>(&a, s_row[i]);
+    for (int i = warp; i < per; i += kMergeRowThreads / 32)
+        if (s_odd[i] >= 0) attend_again<KT>(&a, s_odd[i]);
+}
+
+template <typename KT>
+cudaError_t merge(const cudaLaunchConfig_t& cfg, const RowsTcArgs& t, int statuses, int merges, int planes) {
+    return t.a.M > 0 ? cudaLaunchKernelEx(&cfg, rows_merge_kernel<KT, false>, t, statuses, merges, planes)
+                     : cudaLaunchKernelEx(&cfg, rows_merge_kernel<KT, true>, t, statuses, merges, planes);
 }
 
 }  // namespace
 
 cudaError_t launch_rows_merge(const RowsTcArgs& t, int kv_dtype, cudaStream_t s) {
     const RowsArgs& a = t.a;
-    const long long merges = a.M > 0 ? ((long long)a.B * a.M * a.Hq + kMergePrefix - 1) / kMergePrefix : (long long)t.workers * (kRowTile / kMergePrompt);
+    const int per = merge_rows(a.hd);
+    const long long merges = a.M > 0 ? ((long long)a.B * a.M * a.Hq + per - 1) / per : (long long)t.workers * (kRowTile / per);
     const long long odd = a.M > 0 ? 0 : ((long long)a.T * a.Hq + kOddRows - 1) / kOddRows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(merges + odd + 1));
@@ -390,8 +421,7 @@ cudaError_t launch_rows_merge(const RowsTcArgs& t, int kv_dtype, cudaStream_t s)
     cfg.numAttrs = 1;
     const int planes = rows_halves(kv_dtype == MTP_DTYPE_E4M3, a.hd);
     const int statuses = t.workers * rows_pair(a.hd) + 1;   // the CTAs' and the plan's
-    return kv_dtype == MTP_DTYPE_E4M3 ? cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint8_t>, t, statuses, (int)merges, planes)
-                                      : cudaLaunchKernelEx(&cfg, rows_merge_kernel<uint16_t>, t, statuses, (int)merges, planes);
+    return kv_dtype == MTP_DTYPE_E4M3 ? merge<uint8_t>(cfg, t, statuses, (int)merges, planes) : merge<uint16_t>(cfg, t, statuses, (int)merges, planes);
 }
 
 cudaError_t launch_rows_cc(const RowsArgs& a, int dtype, int kv_dtype, cudaStream_t s) {

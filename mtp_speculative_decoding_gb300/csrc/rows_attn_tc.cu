@@ -170,7 +170,7 @@ __device__ __forceinline__ void tma_2d(void* dst, const void* tmap, int x, int y
 }
 // 32 bytes (a whole sector) in one store
 __device__ __forceinline__ void store_32b(void* p, const uint32_t* w) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
                  "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
@@ -246,7 +246,7 @@ struct RowShape {
     static __device__ __forceinline__ unsigned v_at(int k, int n) { return CG == 1 ? 2 * k + 1 : k == n - 1 ? 2 * n - 1 : 2 * k + 2; }
 };
 
-template <bool E4M3, int HD>
+template <bool E4M3, int HD, bool SHARED>
 __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcParams pp) {
     using S = RowShape<E4M3, HD>;
     constexpr int CG = S::CG, NQ = S::NQ, NR = rows_raw(E4M3, HD), NS = rows_slots(E4M3, HD);
@@ -260,13 +260,15 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
     unsigned char* raw = ring + (size_t)NS * S::SLOTB;
     uint4* m_bits = reinterpret_cast<uint4*>(raw + (size_t)NR * S::RAWB);       // [kRowsMeta] positions that are there
     float2* m_sc = reinterpret_cast<float2*>(m_bits + kRowsMeta);               // [kRowsMeta][8] key scale, value scale's exponent, every 16 positions
-    int4* m_flag = reinterpret_cast<int4*>(m_sc + kRowsMeta * 8);               // [kRowsMeta] x: all positions there
+    int4* m_flag = reinterpret_cast<int4*>(m_sc + kRowsMeta * 8);               // [kRowsMeta] x: row tiles, 4: all positions there; y: sequence; z, w: the tile's [pos, end)
     float* s_x = reinterpret_cast<float*>(m_flag + kRowsMeta);                  // [NQ][2][128] what the threads of a row tell each other
     unsigned long long* bars = reinterpret_cast<unsigned long long*>(s_x + 2 * kRowTile);
     unsigned long long *full = bars, *empty = full + kRowsSlots, *peer = empty + kRowsSlots, *rfull = peer + kRowsSlots,
                        *rempty = rfull + kRowsRaw, *meta = rempty + kRowsRaw, *s_full = meta + kRowsMeta, *p_full = s_full + 2,
                        *pv_done = p_full + 2, *o_free = pv_done + 2, *q_full = o_free + 2, *q_peer = q_full + 1, *q_free = q_peer + 1,
                        *end_bar = q_free + 1;
+    int* s_tab = reinterpret_cast<int*>(bars + 3 * kRowsSlots + 2 * kRowsRaw + kRowsMeta + 16);   // shared prefixes: the sequences' tables
+    const Sequences sq = {s_tab, s_tab + a.B + 1, s_tab + 2 * a.B + 2};
     __shared__ unsigned int s_tmem;
     __shared__ int s_bad;
     __shared__ volatile int s_abort;
@@ -305,6 +307,14 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the plan and the staged rows are there
+    if (SHARED && a.n_groups > 0) {
+        for (int i = tid; i <= a.B; i += S::THREADS) {
+            s_tab[i] = t.cum[i];
+            s_tab[a.B + 1 + i] = t.cumt[i];
+            if (i < a.B) s_tab[2 * a.B + 2 + i] = t.lens[i];
+        }
+        __syncthreads();
+    }
     // bounded wait; after one gave up every other does too
     auto wait = [&](unsigned long long* bar, unsigned int parity) -> bool {
         if (try_wait<CG>(bar, parity)) return true;
@@ -337,28 +347,26 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         unsigned slot = 0, phase = 0, ti = 0;
         bool ok = true, bad = false;
         RowNote note = {-1, 0, 0, 0, 0, 0, {0, 0}};
-        Walk p;
-        p.start(t, me);
+        Walk<SHARED> p;
+        p.start(t, sq, me);
         while (ok && p.next(t)) {
-            const int* tab = a.c.table + (long long)p.k.table * a.c.max_pages;
-            const int end = p.k.group ? p.k.hi : p.it.p_last + 1;
             const int wlo = a.c.window > 0 && p.it.p_first + 1 > a.c.window ? p.it.p_first + 1 - a.c.window : 0;
             const int wfar = a.c.window > 0 && p.it.p_last + 1 > a.c.window ? p.it.p_last + 1 - a.c.window : 0;
             const int sink = a.c.sink < wfar ? a.c.sink : wfar;
-            auto entry = [&](int k) -> int {   // page of this lane's positions of tile k; below 0: not loaded
-                if (k >= p.n || lane >= nv) return -2;
-                const int p0 = tile_of(p.it, p.t0 + k) * kPosTile + (lane << vl);
-                if (p0 >= end || p0 + vr <= p.k.lo || (p0 + vr <= wlo && p0 >= sink)) return -2;
-                const int pg = tab[p0 >> a.c.ps_log2];
+            auto entry = [&](int k, Tile& tl) -> int {   // page of this lane's positions of tile k; below 0: not loaded
+                if (k >= p.n) return -2;
+                tl = tile_of<SHARED>(a, sq, p.k, p.it, p.t0 + k);
+                const int p0 = tl.pos + (lane << vl);
+                if (lane >= nv || p0 >= tl.end || p0 + vr <= p.k.lo || (p0 + vr <= wlo && p0 >= sink)) return -2;
+                const int pg = a.c.table[(long long)tl.seq * a.c.max_pages + (p0 >> a.c.ps_log2)];
                 if ((unsigned)pg < (unsigned)a.c.n_pages) return pg;
                 bad = true;
                 return -1;
             };
-            auto load = [&](bool key, int tile, int pg) {
+            auto load = [&](bool key, int pos, int pg) {
                 ok = wait_all(be + slot, phase ^ 1);
                 if (!ok) return;
                 unsigned char* dst = dst0 + (size_t)slot * DSTB;
-                const int pos = tile * kPosTile;
                 if (key) {
                     const int off = rank * S::KP + (lane << kl);      // this lane's first position in the tile
                     const int kp = __shfl_sync(0xffffffffu, pg, (off >> vl) & 31);
@@ -386,13 +394,15 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     phase ^= 1;
                 }
             };
-            int npg = entry(0), held = -2, held_tile = 0;
+            Tile nt = {};
+            int npg = entry(0, nt), held = -2, held_pos = 0;
 #pragma unroll 1
             for (int k = 0; k <= p.n && ok; ++k) {
-                const int pg = npg, tile = k < p.n ? tile_of(p.it, p.t0 + k) : 0;
-                npg = entry(k + 1);
+                const int pg = npg;
+                const Tile tile = nt;
+                npg = entry(k + 1, nt);
                 if (k < p.n) {
-                    load(true, tile, pg);
+                    load(true, tile.pos, pg);
                     // the tile's masks and scales, while its keys are on their way
                     bool there = pg >= 0;
                     float ks = 1.f, ev = 0.f;
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         const float kss = a.c.ks[o], vss = a.c.vs[o];
                         there = scale_ok(kss) && scale_ok(vss);   // else the page counts as absent
                         bad = bad || !there;
-                        ks = there ? kss : 0.f;
+                        ks = there ? kss : 1.f;
                         ev = there ? (float)((int)(__float_as_uint(vss) >> 23) - 127) : 0.f;
                     }
                     // lane i < 8: positions [16 i, 16 i + 16)
@@ -414,25 +424,25 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     if (lane == 0) {
                         auto word = [&](int i) { return ((have >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((have >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u); };
                         m_bits[mi] = make_uint4(word(0), word(1), word(2), word(3));
-                        m_flag[mi] = make_int4(have == 0xFFu, 0, 0, 0);
+                        m_flag[mi] = make_int4((have == 0xFFu ? 4 : 0) | tile.rows, tile.seq, tile.pos, tile.end);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(meta + mi);
                     ++ti;
                 }
                 if (CG == 1) {
-                    if (k < p.n && ok) load(false, tile, pg);
+                    if (k < p.n && ok) load(false, tile.pos, pg);
                 } else {
-                    if (k > 0 && ok) load(false, held_tile, held);
+                    if (k > 0 && ok) load(false, held_pos, held);
                     held = pg;
-                    held_tile = tile;
+                    held_pos = tile.pos;
                 }
             }
-            if (p.slot == 2 && p.t0 == 0 && a.M == 0)
+            if (!SHARED && p.slot == 2 && p.t0 == 0)
                 note = RowNote{worker_of(t.head->T, t.head->workers, p.tiles_at + (long long)(p.it.n - 1) * kPosTile * a.G), p.it.rows, p.it.r0,
                                p.g, p.k.row0, p.k.table, {0, 0}};
         }
-        if (rank == 0 && lane == 0 && a.M == 0) t.note[me] = note;
+        if (!SHARED && rank == 0 && lane == 0) t.note[me] = note;
         if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
         if (!ok) {   // gave up: this warp's copies in flight end before the CTA does
             const unsigned long long t0 = global_ns();
@@ -447,8 +457,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         // ------------------------------------------------------------------
         unsigned seg = 0;
         bool ok = true;
-        Walk p;
-        p.start(t, me);
+        Walk<SHARED> p;
+        p.start(t, sq, me);
         while (ok && p.next(t)) {
             ok = wait_all(q_free, (seg & 1) ^ 1);
             if (!ok) break;
@@ -473,8 +483,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         const int ct = tid - S::CONV * 32;
         unsigned slot = 0, phase = 0, rs = 0, rp = 0;
         bool ok = true;
-        Walk p;
-        p.start(t, me);
+        Walk<SHARED> p;
+        p.start(t, sq, me);
         while (ok && p.next(t)) {
 #pragma unroll 1
             for (int i = 0; i < 2 * p.n && ok; ++i) {
@@ -540,8 +550,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 phase ^= 1;
             }
         };
-        Walk p;
-        p.start(t, me);
+        Walk<SHARED> p;
+        p.start(t, sq, me);
         if (CG == 2 && rank == 1) {
             while (ok && p.next(t))
                 for (int i = 0; i < 2 * p.n && ok; ++i) {
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
         } else {
             const uint32_t q0 = smem_addr(sQ) >> 4, r0 = smem_addr(ring) >> 4;
-            unsigned tq[2] = {0u, 0u}, sq[2] = {0u, 0u};   // tiles and pieces of a row tile so far
+            unsigned tq[2] = {0u, 0u}, sq_n[2] = {0u, 0u};   // tiles and pieces of a row tile so far
             auto arrived = [&] {
                 hold(full + slot, phase);
                 if (CG == 2) hold(peer + slot, phase);
@@ -587,7 +597,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             };
             bool more_pieces = p.next(t);
             while (ok && more_pieces) {
-                const int n = p.n, nq = p.it.rows > 128 ? 2 : 1;   // (p moves on before this piece's last product)
+                const int n = p.n;   // (p moves on before this piece's last product)
                 hold(q_full, seg & 1);
                 if (CG == 2) hold(q_peer, seg & 1);
                 ++seg;
@@ -606,7 +616,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         }
                         if (k > 0) {
                             const unsigned u = t0 + k - 1;
-                            if (k == 1) hold(o_free, (sq[0] & 1) ^ 1);
+                            if (k == 1) hold(o_free, (sq_n[0] & 1) ^ 1);
                             arrived();
                             hold(p_full + (u & 1), (u >> 1) & 1);
                             values(0, u & 1, slot, k == 1);
@@ -614,26 +624,35 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         }
                     }
                     tq[0] += n;
-                    ++sq[0];
+                    ++sq_n[0];
                 } else {
-                    // slots take turns: K tile k, V tile k
+                    // slots take turns: K tile k, V tile k; a tile concerns one row tile or both
                     unsigned vslot = 0, vphase = 0;
+                    int rows = 0, had = 0;           // row tiles of tile k - 1, of the piece so far
+                    auto rows_at = [&](int k) { return SHARED && p.k.kind == kOwn ? tile_of<SHARED>(a, sq, p.k, p.it, p.t0 + k).rows : p.it.rows > 128 ? 3 : 1; };
+                    int ahead = rows_at(0);          // looked up while the products before run
 #pragma unroll 1
                     for (int k = 0; k <= n && ok; ++k) {
                         const bool more = k < n;
+                        const int now = more ? ahead : 0;
                         if (more) arrived();
                         else more_pieces = p.next(t);
                         if (k > 0) hold(full + vslot, vphase);
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            if (q >= nq) break;
-                            if (k > 0) {
-                                if (k == 1) hold(o_free + q, (sq[q] & 1) ^ 1);
-                                hold(p_full + q, (tq[q] + k - 1) & 1);
-                                values(q, q, vslot, k == 1);
+                            if (rows >> q & 1) {
+                                const bool first = !(had >> q & 1);
+                                if (first) hold(o_free + q, (sq_n[q] & 1) ^ 1);
+                                hold(p_full + q, (tq[q] - 1) & 1);
+                                values(q, q, vslot, first);
+                                had |= 1 << q;
                             }
-                            if (more) scores(q, q);
+                            if (now >> q & 1) {
+                                scores(q, q);
+                                ++tq[q];
+                            }
                         }
+                        rows = now;
                         if (k > 0 && ok && elect()) commit<CG>(empty + vslot);
                         __syncwarp();
                         if (more) {
@@ -643,14 +662,11 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                             vslot = slot;
                             vphase = phase;
                             next();
+                            if (k + 1 < n) ahead = rows_at(k + 1);
                         }
                     }
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        if (q < nq) {
-                            tq[q] += n;
-                            ++sq[q];
-                        }
+                    for (int q = 0; q < 2; ++q) sq_n[q] += had >> q & 1;
                 }
             }
             if (elect()) commit<CG>(end_bar);   // whatever was issued has ended before its memory goes
@@ -691,33 +707,42 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             pair_barrier(1 + q * 4 + (warp & 3));
             return y;
         };
-        Walk p;
-        p.start(t, me);
+        Walk<SHARED> p;
+        p.start(t, sq, me);
         bool more_pieces = p.next(t);
         while (more_pieces) {
             const int ofs = (CG == 2 ? rank : q) * 128;      // of the row tile in the item
-            if (CG == 1 && p.it.rows <= ofs) {               // not there: the other row tile's alone
-                for (int k = 0; k < p.n; ++k, ++ti) meet(meta + ti % kRowsMeta, (ti / kRowsMeta) & 1);   // (in step with the phases)
-                g0 += 2 * p.n;
-                more_pieces = p.next(t);
-                continue;
-            }
             const bool live = ofs + row < p.it.rows;
-            const int r = p.it.r0 + (live ? ofs + row : p.it.rows - 1), tok = (int)udiv((unsigned)r, (unsigned)a.G);   // row of the block, its token
-            const int pos_q = p.k.len + tok, end = p.k.group ? p.k.hi : pos_q + 1;   // attends [.., end)
+            const int r = p.it.r0 + (live ? ofs + row : p.it.rows - 1);   // row of the block
+            int tok = (int)udiv((unsigned)r, (unsigned)a.G), seq = p.k.table, pos_q = p.k.len + tok;   // its token, sequence, position
+            if (SHARED && p.k.kind == kOwn) {
+                const int x = sq.cum[p.k.table] + tok;
+                seq += last_at_most(sq.cum + p.k.table, p.k.len - p.k.table, x);
+                pos_q = sq.lens[seq] + x - sq.cum[seq];
+            }
+            const int end = SHARED && p.k.kind == kPrefix ? p.k.hi : pos_q + 1;     // attends [.., end)
             const int low = a.c.window > 0 && pos_q + 1 > a.c.window ? pos_q + 1 - a.c.window : 0;
             // what a score is multiplied by: the softmax scale, and what the staged row was divided by
             const float qc = E4M3 ? t.q_scale[p.k.q_row + (long long)p.g * p.k.q_stride + r] : a.scale;
             float m = kNoScore, l = 0.f;
+            bool none = true, touched = false;               // no tile of this row tile yet; of this row
 #pragma unroll 1
-            for (int k = 0; k < p.n; ++k) {
-                const int buf = CG == 2 ? (int)(tc & 1) : q;
-                const uint32_t sat = tmem + lanes + buf * 128;
-                const int t0 = tile_of(p.it, p.t0 + k) * kPosTile;
+            for (int k = 0; k < p.n; ++k, ++ti) {
                 const unsigned mi = ti % kRowsMeta;
                 meet(meta + mi, (ti / kRowsMeta) & 1);
+                const int4 flag = m_flag[mi];
+                const int t0 = SHARED ? flag.z : tile_of<SHARED>(a, sq, p.k, p.it, p.t0 + k).pos;
+                const bool mine = !SHARED || p.k.kind != kOwn || seq == flag.y;   // the tile is on this row's sequence
+                int zq = 0;                                  // the row tile that looks after the tile's values
+                if (CG == 1) {
+                    if (!(flag.x >> q & 1)) continue;        // the other row tile's alone
+                    zq = flag.x & 1 ? 0 : 1;
+                }
+                const int buf = CG == 2 ? (int)(tc & 1) : q;
+                const uint32_t sat = tmem + lanes + buf * 128;
                 // every row of the item attends every position of the tile
-                const bool whole = m_flag[mi].x != 0 && t0 >= p.k.lo && (p.k.group ? t0 + kPosTile <= p.k.hi : t0 + kPosTile - 1 <= p.it.p_first) &&
+                const bool whole = (flag.x & 4) && (!SHARED || (p.k.kind != kOwn && t0 >= p.k.lo)) &&
+                                   (SHARED && p.k.kind == kPrefix ? t0 + kPosTile <= p.k.hi : t0 + kPosTile - 1 <= p.it.p_first) &&
                                    (a.c.window == 0 || t0 > p.it.p_last - a.c.window || t0 + kPosTile <= a.c.sink);
                 uint32_t bits[CW / 32];
 #pragma unroll
@@ -728,14 +753,14 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     auto below = [&](int e) { return e - c0 >= 32 ? ~0u : e - c0 <= 0 ? 0u : (1u << (e - c0)) - 1u; };   // positions < e
                     uint32_t on = below(end) & ~below(p.k.lo);
                     if (low > 0) on &= ~below(low) | below(a.c.sink);
-                    return there & on;
+                    return mine ? there & on : 0u;
                 };
                 if (!whole)
 #pragma unroll
                     for (int i = 0; i < CW / 32; ++i) bits[i] = on_bits(half * (CW / 32) + i);
                 meet(s_full + buf, CG == 2 ? (tc >> 1) & 1 : tc & 1);
                 tc_fence_after();
-                if (k == 0) {
+                if (none) {
                     // a first reference from the tile's first 16 positions: seldom does a score lie
                     // 2^kSlack above it
                     uint32_t s[16];
@@ -749,12 +774,14 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     else x *= qc;
                     m = fmaxf(m, x);
                 }
+                const bool idle = SHARED && p.k.kind == kOwn && !__any_sync(0xffffffffu, mine);   // none of this warp's rows: weights of zero
+                if (SHARED) touched = touched || mine;
                 // ---- probabilities against the reference there is; where a score lies above it,
                 // once more against a new one (the scores stay in place until all is well) ----
                 constexpr int CH = E4M3 && NH == 1 ? 16 : 32;   // positions of a load (registers)
                 uint32_t o[CW / 2];
 #pragma unroll 1
-                for (int turn = 0;; ++turn) {
+                for (int turn = 0; !idle; ++turn) {
                     uint32_t s[2][CH];
                     auto fetch = [&](int c) {
                         if constexpr (CH == 16) tmem_ld16(sat + half * CW + CH * c, s[c & 1]);
@@ -819,7 +846,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     const float mn = fmaxf(mx, m), f = ex2(m - mn);
                     l *= f;
                     m = mn;
-                    if (k > 0) {
+                    if (!none) {
                         meet_values(tc - 1);
 #pragma unroll 1
                         for (int c = 0; c < HD / NH; c += 32) {
@@ -834,17 +861,22 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         tc_fence_before();
                     }
                 }
+                if (idle) {
+                    if (NH == 2) pair_barrier(1 + q * 4 + (warp & 3));   // (both have read: the first reference)
+#pragma unroll
+                    for (int i = 0; i < CW / 2; ++i) o[i] = 0u;
+                }
+                none = false;
 #pragma unroll
                 for (int i = 0; i < CW / 64; ++i)   // over the scores
                     st32(sat + half * (CW / 2) + 32 * i, *reinterpret_cast<const uint32_t(*)[32]>(o + 32 * i));
                 bool zeroed = false;
-                if (!whole && q == 0 && half == 0) {
+                if (!whole && q == zq && half == 0) {
                     // value rows that no row of the item attends may hold anything: zero
                     // them (this thread's position; a weight of zero would make a NaN of it)
                     const int pos = t0 + row;
                     const uint32_t word = reinterpret_cast<const uint32_t*>(m_bits + mi)[row >> 5];
-                    const int last = p.k.group ? p.k.hi : p.it.p_last + 1;
-                    const bool any = (word >> (row & 31) & 1u) && pos >= p.k.lo && pos < last &&
+                    const bool any = (word >> (row & 31) & 1u) && pos >= p.k.lo && pos < flag.w &&
                                      (a.c.window == 0 || pos > p.it.p_first - a.c.window || pos < a.c.sink);
                     if (!__all_sync(0xffffffffu, any)) {
                         const unsigned v = g0 + S::v_at(k, p.n);
@@ -870,19 +902,23 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     else arrive_lead_relaxed<CG>(p_full + buf);
                 }
                 ++tc;
-                ++ti;
             }
             g0 += 2 * p.n;
+            if (none) {                                      // nothing of this row tile
+                more_pieces = p.next(t);
+                continue;
+            }
             // ---- the accumulator ----
             if (NH == 2) l += others(l);
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool out = p.slot == 0 && a.M == 0;        // the row's whole result
+            const bool out = !SHARED && p.slot == 0;        // the row's whole result
             const long long orow = ((long long)p.k.row0 + tok) * a.Hq + p.g * a.G + r - tok * a.G;   // (sequences)
             uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + orow * HD + half * (HD / NH);
             float* part = nullptr;
-            if (!out && live) {
-                if (p.slot == 0) {
-                    const long long at = p.k.q_row + (long long)p.g * p.k.q_stride + r + (p.k.group ? 0 : (long long)a.B * a.M * a.Hq);
+            const bool keep = live && (!SHARED || touched);
+            if (!out && keep) {
+                if (SHARED && p.slot == 0) {
+                    const long long at = p.k.q_row + (long long)p.g * p.k.q_stride + r + (p.k.kind == kPrefix ? 0 : (long long)a.B * a.M * a.Hq);
                     part = t.dense + at * HD + half * (HD / NH);
                     if (half == 0) t.dense_ml[at] = make_float2(m, l);
                 } else {
@@ -899,7 +935,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 uint32_t v[32];
                 ld32(oat + c, v);
                 tmem_ld_wait();
-                if (!live) {
+                if (!keep) {
                 } else if (out) {
                     uint32_t w[16];
 #pragma unroll
@@ -919,7 +955,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_lead_relaxed<CG>(o_free + q);
-            if (a.M == 0 && live) t.odd[half * t.odd_plane + orow] = out && !((odd[0] + odd[1]) + (odd[2] + odd[3]) == 0.f);
+            if (!SHARED && live) t.odd[half * t.odd_plane + orow] = out && !((odd[0] + odd[1]) + (odd[2] + odd[3]) == 0.f);
         }
     }
     __syncthreads();
@@ -928,17 +964,18 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
     if (warp == S::MMA) free_columns<CG>(tmem, 512);
 }
 
-template <bool E4M3, int HD>
+template <bool E4M3, int HD, bool SHARED>
 cudaError_t go(const RowsTcParams& p, cudaStream_t s) {
     using S = RowShape<E4M3, HD>;
     static int ready[64] = {0};   // the attribute is set, per device
-    constexpr int smem = rows_slots(E4M3, HD) * S::SLOTB + S::NQ * S::QB + rows_raw(E4M3, HD) * S::RAWB + kRowsOther;
-    static_assert(smem <= kRowsSmemLimit, "shared memory");
+    constexpr int base = rows_slots(E4M3, HD) * S::SLOTB + S::NQ * S::QB + rows_raw(E4M3, HD) * S::RAWB + kRowsOther;
+    static_assert(base + rows_tables(MTP_MAX_PAGED_BATCH) <= kRowsSmemLimit, "shared memory");
+    const int smem = base + (p.t.a.n_groups > 0 ? rows_tables(p.t.a.B) : 0);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || ready[dev] == 0) {
-        e = cudaFuncSetAttribute(rows_tc_kernel<E4M3, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmemLimit);
+        e = cudaFuncSetAttribute(rows_tc_kernel<E4M3, HD, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmemLimit);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev] = 1;
     }
@@ -955,22 +992,33 @@ cudaError_t go(const RowsTcParams& p, cudaStream_t s) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = S::CG == 1 ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, rows_tc_kernel<E4M3, HD>, p);
+    return cudaLaunchKernelEx(&cfg, rows_tc_kernel<E4M3, HD, SHARED>, p);
 }
 
 }  // namespace
 
 #ifdef MTP_PAGED_E4M3
-cudaError_t launch_rows_tc_e4m3(const RowsTcParams& p, cudaStream_t s) {
-    constexpr bool E = true;
+#define MTP_ROWS_FORMAT e4m3
+constexpr bool kE4m3 = true;
 #else
-cudaError_t launch_rows_tc_bf16(const RowsTcParams& p, cudaStream_t s) {
-    constexpr bool E = false;
+#define MTP_ROWS_FORMAT bf16
+constexpr bool kE4m3 = false;
 #endif
+#ifdef MTP_ROWS_SHARED
+#define MTP_ROWS_NAME(f) MTP_ROWS_NAME_(f, _shared)
+constexpr bool kShared = true;
+#else
+#define MTP_ROWS_NAME(f) MTP_ROWS_NAME_(f, )
+constexpr bool kShared = false;
+#endif
+#define MTP_ROWS_NAME_(f, s) launch_rows_tc_##f##s
+#define MTP_ROWS_LAUNCH(f) MTP_ROWS_NAME(f)
+
+cudaError_t MTP_ROWS_LAUNCH(MTP_ROWS_FORMAT)(const RowsTcParams& p, cudaStream_t s) {
     switch (p.t.a.hd) {
-    case 64: return go<E, 64>(p, s);
-    case 128: return go<E, 128>(p, s);
-    case 256: return go<E, 256>(p, s);
+    case 64: return go<kE4m3, 64, kShared>(p, s);
+    case 128: return go<kE4m3, 128, kShared>(p, s);
+    case 256: return go<kE4m3, 256, kShared>(p, s);
     default: return cudaErrorInvalidValue;
     }
 }

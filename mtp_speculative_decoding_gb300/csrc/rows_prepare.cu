@@ -36,31 +36,46 @@ __device__ __forceinline__ long long scan(long long v, long long* s, long long& 
     return base;
 }
 
-// Tokens before every sequence (shared prefixes), and whether this thread saw
-// something out of range.
-__device__ __forceinline__ bool count_tokens(const RowsArgs& a, int* cum, long long* tmp) {
+// own tiles of a sequence
+__device__ __forceinline__ int own_tiles(const Seq& s) { return s.n > 0 ? (s.len + s.n - 1) / kPosTile - s.P / kPosTile + 1 : 0; }
+
+// Tokens and own tiles before every sequence, cached positions (shared prefixes); false
+// if this thread saw something out of range.  cumt, lens null: tokens alone.
+__device__ __forceinline__ bool count_tokens(const RowsArgs& a, int* cum, int* cumt, int* lens, long long* tmp) {
     bool good = true;
+    constexpr int MAX = (MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads;
     const int per = (a.B + kPrepThreads - 1) / kPrepThreads, b0 = (int)threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
-    int n[(MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads], sum = 0;
+    int n[MAX], tl[MAX];
+    long long sum = 0;
 #pragma unroll
-    for (int i = 0; i < (MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads; ++i) {
-        n[i] = 0;
+    for (int i = 0; i < MAX; ++i) {
+        n[i] = tl[i] = 0;
         if (b0 + i < b1) {
             Seq s;
             good = seq_at(a, b0 + i, s) && good;
             n[i] = s.n;
-            sum += s.n;
+            tl[i] = own_tiles(s);
+            if (lens) lens[b0 + i] = s.len;
+            sum += (long long)s.n << 40 | tl[i];   // (at most 2^16 tokens, 2^34 tiles)
         }
     }
     long long all;
-    int at = (int)scan(sum, tmp, all);
+    const long long before = scan(sum, tmp, all);
+    int at = (int)(before >> 40), tat = (int)(before & 0xFFFFFFFFFFll);
 #pragma unroll
-    for (int i = 0; i < (MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads; ++i)
+    for (int i = 0; i < MAX; ++i)
         if (b0 + i < b1) {
             cum[b0 + i] = at;
             at += n[i];
+            if (cumt) {
+                cumt[b0 + i] = tat;
+                tat += tl[i];
+            }
         }
-    if (threadIdx.x == 0) cum[a.B] = (int)all;
+    if (threadIdx.x == 0) {
+        cum[a.B] = (int)(all >> 40);
+        if (cumt) cumt[a.B] = (int)(all & 0xFFFFFFFFFFll);
+    }
     __syncthreads();
     return good;
 }
@@ -83,29 +98,31 @@ __device__ __forceinline__ StagedAt staged_at(const RowsArgs& a, const int* cum,
 
 __device__ BlockRec block_at(const RowsArgs& a, const int* cum, int blk, bool& good) {
     BlockRec k = {};
-    if (blk < a.n_groups) {
-        const int g0 = a.group_start[blk], g1 = a.group_start[blk + 1], P = a.prefix_len[blk];
+    if (blk < 2 * a.n_groups) {
+        const bool own = blk >= a.n_groups;
+        const int i = own ? blk - a.n_groups : blk, g0 = a.group_start[i], g1 = a.group_start[i + 1], P = a.prefix_len[i];
         const bool ok = g0 >= 0 && g0 <= g1 && g1 <= a.B && P >= 0 && P <= (long long)a.c.max_pages << a.c.ps_log2;
         good = good && ok;
-        k.group = 1;
+        k.kind = own ? kOwn : kPrefix;
         if (ok) {
-            k.n = P > 0 ? cum[g1] - cum[g0] : 0;
-            k.hi = P;
+            k.n = own || P > 0 ? cum[g1] - cum[g0] : 0;
+            k.len = own ? g1 : 0;
+            k.lo = own ? P : 0;
+            k.hi = own ? 0 : P;
             k.table = g0;
-            k.q_stride = k.n * a.G;
+            k.q_stride = (cum[g1] - cum[g0]) * a.G;
             k.q_row = (long long)cum[g0] * a.Hq;
         }
         return k;
     }
     Seq s;
-    const int b = blk - a.n_groups;
+    const int b = blk - 2 * a.n_groups;
     good = seq_at(a, b, s) && good;
     k.table = b;
-    if (s.n > 0) {
+    if (s.n > 0 && s.group < 0) {
         const StagedAt w = staged_at(a, cum, s, b);
         k.n = s.n;
         k.len = s.len;
-        k.lo = s.P;
         k.hi = s.len + s.n;
         k.q_stride = w.stride;
         k.q_row = w.row;
@@ -114,14 +131,47 @@ __device__ BlockRec block_at(const RowsArgs& a, const int* cum, int blk, bool& g
     return k;
 }
 
-__device__ void make_plan(const RowsTcArgs& t, const int* cum, long long* tmp, long long* pre, bool good) {
+// The tiles before each item of the groups' own positions, group by group, and the
+// groups' first entries (rt0: [n_groups + 1] row tiles before a group)
+__device__ void count_items(const RowsTcArgs& t, const Sequences& sq, int* rt0, long long* tmp) {
+    const RowsArgs& a = t.a;
+    bool good = true;
+    const int tid = threadIdx.x, per = (a.n_groups + kPrepThreads - 1) / kPrepThreads, i0 = tid * per,
+              i1 = i0 + per < a.n_groups ? i0 + per : a.n_groups;
+    long long sum = 0, all;
+    for (int i = i0; i < i1; ++i) sum += row_tiles_of(a, block_at(a, sq.cum, a.n_groups + i, good));
+    int at = (int)scan(sum, tmp, all);
+    for (int i = i0; i < i1; ++i) {
+        rt0[i] = at;
+        at += row_tiles_of(a, block_at(a, sq.cum, a.n_groups + i, good));
+    }
+    if (tid == 0) rt0[a.n_groups] = (int)all;
+    __syncthreads();
+    const int items = (int)all, pi = (items + kPrepThreads - 1) / kPrepThreads, x0 = tid * pi, x1 = x0 + pi < items ? x0 + pi : items;
+    auto tiles = [&](int x) {
+        const int i = last_at_most(rt0, a.n_groups, x);
+        return item_of<true>(a, sq, block_at(a, sq.cum, a.n_groups + i, good), x - rt0[i]).n;
+    };
+    sum = 0;
+    for (int x = x0; x < x1; ++x) sum += tiles(x);
+    at = (int)scan(sum, tmp, all);
+    for (int x = x0; x < x1; ++x) {
+        t.items[x] = at;
+        at += tiles(x);
+    }
+    if (tid == 0) t.items[items] = (int)all;
+    __syncthreads();
+}
+
+__device__ void make_plan(const RowsTcArgs& t, const int* cum, const int* rt0, long long* tmp, long long* pre, bool good) {
     const RowsArgs& a = t.a;
     const int tid = threadIdx.x, nb = rows_blocks(a), per = (nb + kPrepThreads - 1) / kPrepThreads, k0 = tid * per,
               k1 = k0 + per < nb ? k0 + per : nb;
     const long long U = (long long)kPosTile * a.G;
     long long tiles = 0, items = 0;
     for (int i = k0; i < k1; ++i) {
-        const BlockRec k = block_at(a, cum, i, good);
+        BlockRec k = block_at(a, cum, i, good);
+        if (k.kind == kOwn) k.row0 = rt0[i - a.n_groups];
         t.blocks[i] = k;
         const int nrt = row_tiles_of(a, k);
         tiles += a.c.Hkv * tile_units(t, k, nrt);
@@ -186,6 +236,8 @@ __device__ void make_plan(const RowsTcArgs& t, const int* cum, long long* tmp, l
     if (tid == 0) t.cta_status[t.workers * rows_pair(a.hd)] = any ? MTP_ERR_ARG : MTP_OK;
 }
 
+__host__ __device__ constexpr size_t prep_ints(int B, int n_groups) { return (((size_t)3 * B + n_groups + 4) * 4 + 7) / 8 * 8; }
+
 template <bool E4M3>
 __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid_constant__ RowsTcArgs t, int hpt) {
     extern __shared__ __align__(16) unsigned char sm[];
@@ -193,7 +245,9 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
     __shared__ __align__(16) float s_hi[256], s_lo[256];
     const RowsArgs& a = t.a;
     int* cum = reinterpret_cast<int*>(sm);                                     // [B + 1] prompts: row_start
-    long long* pre = reinterpret_cast<long long*>(sm + (((size_t)a.B + 2) * 4 + 7) / 8 * 8);   // the plan's CTA: [blocks]
+    // the plan's CTA: own tiles before a sequence, cached positions, row tiles before a group, units before a block
+    int *cumt = cum + a.B + 1, *lens = cumt + a.B + 1, *rt0 = lens + a.B;
+    long long* pre = reinterpret_cast<long long*>(sm + prep_ints(a.B, a.n_groups));
     const int tid = threadIdx.x;
     const bool planner = blockIdx.x == 0;
     if (a.rope.on && !planner)
@@ -204,12 +258,20 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     bool good = true;
-    if (a.M > 0) good = count_tokens(a, cum, tmp);
+    if (a.M > 0) good = count_tokens(a, cum, planner ? cumt : nullptr, planner ? lens : nullptr, tmp);
     else
         for (int i = tid; i <= a.B; i += kPrepThreads) cum[i] = a.row_start[i];
     __syncthreads();
     if (planner) {
-        make_plan(t, cum, tmp, pre, good);
+        if (a.M > 0) {
+            for (int i = tid; i <= a.B; i += kPrepThreads) {
+                t.cum[i] = cum[i];
+                t.cumt[i] = cumt[i];
+                if (i < a.B) t.lens[i] = lens[i];
+            }
+            count_items(t, Sequences{cum, cumt, lens}, rt0, tmp);
+        }
+        make_plan(t, cum, rt0, tmp, pre, good);
         return;
     }
     const int hd = a.hd, U = hd >> 4, ulog = 31 - __clz(U), groups = (a.Hq + hpt - 1) / hpt, half = hd >> 1;
@@ -300,7 +362,7 @@ cudaError_t launch_rows_prepare(const RowsTcArgs& t, int kv_dtype, int sms, cuda
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas + 1);
     cfg.blockDim = dim3(kPrepThreads);
-    cfg.dynamicSmemBytes = (((size_t)a.B + 2) * 4 + 7) / 8 * 8 + (size_t)rows_blocks(a) * 8;
+    cfg.dynamicSmemBytes = prep_ints(a.B, a.n_groups) + (size_t)rows_blocks(a) * 8;   // (at most 41 KB)
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
