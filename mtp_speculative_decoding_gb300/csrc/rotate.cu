@@ -84,20 +84,27 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
         float p[N][8], q[N][8];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int h = h0 + i0 + i < h1 ? h0 + i0 + i : h1 - 1;   // (every lane of the warp takes part in the norm)
-            in8(src + h * a.in_sh[which] + e0, p[i]);
-            in8(src + h * a.in_sh[which] + e1, q[i]);
+            const int h = h0 + i0 + i;
+            if (h < h1) {
+                in8(src + h * a.in_sh[which] + e0, p[i]);
+                in8(src + h * a.in_sh[which] + e1, q[i]);
+            } else {   // (every lane of the warp takes part in the norm)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[i][e] = q[i][e] = 0.f;
+            }
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int h = h0 + i0 + i;
-            const float r = unit_rms(p[i], q[i], a.hd, a.eps);
-            if (gain)
+            if (a.norm[0] || a.norm[1]) {   // (queries and keys may share a warp: all lanes take part)
+                const float r = unit_rms(p[i], q[i], a.hd, a.eps);
+                if (gain)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    p[i][e] *= r * g0[e];
-                    q[i][e] *= r * g1[e];
-                }
+                    for (int e = 0; e < 8; ++e) {
+                        p[i][e] *= r * g0[e];
+                        q[i][e] *= r * g1[e];
+                    }
+            }
             if (turn) unit_rotate(p[i], q[i], cs, sn);
             if (live && h < h1) {
                 store8(dst + h * a.out_sh[which] + e0, p[i]);

@@ -41,8 +41,9 @@ __device__ __forceinline__ int last_at_most(const int32_t* start, int n, int x) 
     }
     return lo;
 }
-// false: its lengths, rows or group are out of range (s.n is 0 then)
-__device__ __forceinline__ bool seq_at(const RowsArgs& a, int b, Seq& s) {
+// false: its lengths, rows or group are out of range (s.n is 0 then).  starts,
+// lengths: copies of group_start and prefix_len.
+__device__ __forceinline__ bool seq_at(const RowsArgs& a, int b, Seq& s, const int32_t* starts, const int32_t* lengths) {
     s.len = a.kv_len[b];
     s.P = 0;
     s.first = b;
@@ -54,15 +55,15 @@ __device__ __forceinline__ bool seq_at(const RowsArgs& a, int b, Seq& s) {
         s.q0 = b * a.sb;
         ok = s.n >= 0 && s.n <= a.M;
         if (a.n_groups > 0) {
-            const int i = last_at_most(a.group_start, a.n_groups, b), g0 = a.group_start[i], g1 = a.group_start[i + 1];
+            const int i = last_at_most(starts, a.n_groups, b), g0 = starts[i], g1 = starts[i + 1];
             if (g0 >= 0 && g0 <= b && b < g1 && g1 <= a.B) {
-                s.P = a.prefix_len[i];
+                s.P = lengths[i];
                 s.first = g0;
                 s.group = i;
                 ok = ok && s.P >= 0 && s.P <= s.len;
             } else {
                 // outside every group where the bounds ascend: before the first or behind the last
-                ok = ok && (b < a.group_start[0] || (i == a.n_groups - 1 && g0 <= g1 && b >= g1));
+                ok = ok && (b < starts[0] || (i == a.n_groups - 1 && g0 <= g1 && b >= g1));
             }
         }
     } else {
@@ -76,6 +77,8 @@ __device__ __forceinline__ bool seq_at(const RowsArgs& a, int b, Seq& s) {
     if (!ok) s.n = 0;
     return ok;
 }
+
+__device__ __forceinline__ bool seq_at(const RowsArgs& a, int b, Seq& s) { return seq_at(a, b, s, a.group_start, a.prefix_len); }
 
 cudaError_t launch_rows_cc(const RowsArgs& a, int dtype, int kv_dtype, cudaStream_t s);
 

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
                                                                                      int planes) {
     __shared__ long long s_odd[merge_rows(64)];             // rows of out whose result is not finite (< 0: none)
     __shared__ uint16_t s_list[PROMPT ? kOddRows : 1];
-    __shared__ int s_n;
+    __shared__ int s_n, s_cum[PROMPT ? 1 : MTP_MAX_PAGED_BATCH + 1], s_cumt[PROMPT ? 1 : MTP_MAX_PAGED_BATCH + 1];
     const RowsArgs& a = t.a;
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) s_n = 0;
@@ -251,6 +251,13 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!PROMPT) {   // (searched below)
+        for (int i = tid; i <= a.B; i += kMergeRowThreads) {
+            s_cum[i] = t.cum[i];
+            s_cumt[i] = t.cumt[i];
+        }
+        __syncthreads();
+    }
     if ((int)blockIdx.x == (int)gridDim.x - 1) {   // the call's status from the CTAs'
         int bad = 0;
         for (int c = tid; c < statuses; c += kMergeRowThreads) {
@@ -307,7 +314,7 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
         const int tok = (int)(id / a.Hq), b = tok / a.M, j = tok - b * a.M, h = (int)(id - (long long)tok * a.Hq);
         if (b < a.B) {
             const PlanHead plan = *t.head;
-            const Sequences sq = {t.cum, t.cumt, t.lens};
+            const Sequences sq = {s_cum, s_cumt, nullptr};
             const int c0 = sq.cum[b], g = h / a.G, rj = j * a.G + h - g * a.G;
             if (j < sq.cum[b + 1] - c0) {
                 const long long own_at = (long long)a.B * a.M * a.Hq;

@@ -228,6 +228,32 @@ __host__ __device__ constexpr uint32_t idesc(int type, bool bn, int M, int N) {
 }
 __device__ __forceinline__ int swz128(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
 
+// e4m3 codes (boxes of 128 or 64 a row, swizzled) to fp16 rows of 64 dimensions, the 16
+// codes of a chunk at a time; thread ct of 128
+template <int ROWS, int HD, int BYTES>
+__device__ __forceinline__ void open_codes(const unsigned char* src, unsigned char* dst, int ct) {
+    constexpr int CW = HD < 128 ? 64 : 128, CH = CW / 16;   // codes and chunks of a row
+#pragma unroll
+    for (int c0 = 0; c0 < BYTES / 16; c0 += 128) {
+        const int c = c0 + ct, box = c / (ROWS * CH), r = c / CH % ROWS, ch = c % CH;
+        const uint4 v = *reinterpret_cast<const uint4*>(src + box * ROWS * CW + (CW == 128 ? swz128(r, ch) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+                : "=r"(o[2 * e]), "=r"(o[2 * e + 1])
+                : "r"(w[e]));
+        // (lanes of the row's second half begin with the other piece: eight lanes then write
+        // to all banks)
+        unsigned char* q = dst + (box * (CW / 64) + ch / 4) * ROWS * 128;
+        const int turn = ch / 4 & 1, p0 = 2 * (ch & 3) + turn, p1 = p0 ^ 1;
+        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(q + swz128(r, p0)) = turn ? hi : lo;
+        *reinterpret_cast<uint4*>(q + swz128(r, p1)) = turn ? lo : hi;
+    }
+}
+
 template <bool E4M3, int HD>
 struct RowShape {
     static constexpr int CG = rows_pair(HD), NQ = 2 / CG;          // CTAs of a worker, row tiles of a CTA
@@ -299,6 +325,10 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         s_abort = 0;
     }
     mbar_fence_init();
+    if (tid < 3) {
+        const CUtensorMap* m = tid == 0 ? &pp.tk : tid == 1 ? &pp.tv : &pp.tq;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
     if (CG == 2) pair_sync();   // the peer's barriers stand
     if (warp == S::MMA) alloc_columns<CG>(&s_tmem, 512);
     tc_fence_before();
@@ -307,6 +337,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the plan and the staged rows are there
+    const WorkerRec first = t.worker[me];
     if (SHARED && a.n_groups > 0) {
         for (int i = tid; i <= a.B; i += S::THREADS) {
             s_tab[i] = t.cum[i];
@@ -348,7 +379,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         bool ok = true, bad = false;
         RowNote note = {-1, 0, 0, 0, 0, 0, {0, 0}};
         Walk<SHARED> p;
-        p.start(t, sq, me);
+        p.start(first, sq);
         while (ok && p.next(t)) {
             const int wlo = a.c.window > 0 && p.it.p_first + 1 > a.c.window ? p.it.p_first + 1 - a.c.window : 0;
             const int wfar = a.c.window > 0 && p.it.p_last + 1 > a.c.window ? p.it.p_last + 1 - a.c.window : 0;
@@ -458,7 +489,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         unsigned seg = 0;
         bool ok = true;
         Walk<SHARED> p;
-        p.start(t, sq, me);
+        p.start(first, sq);
         while (ok && p.next(t)) {
             ok = wait_all(q_free, (seg & 1) ^ 1);
             if (!ok) break;
@@ -484,7 +515,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         unsigned slot = 0, phase = 0, rs = 0, rp = 0;
         bool ok = true;
         Walk<SHARED> p;
-        p.start(t, sq, me);
+        p.start(first, sq);
         while (ok && p.next(t)) {
 #pragma unroll 1
             for (int i = 0; i < 2 * p.n && ok; ++i) {
@@ -495,28 +526,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 if (!ok) break;
                 const unsigned char* src = raw + (size_t)rs * S::RAWB;
                 unsigned char* dst = ring + (size_t)slot * S::SLOTB;
-                // raw: boxes of CW codes a row (swizzled), K: KP rows x HD, V: 128 rows x VD; both RAWB bytes
-                constexpr int CW = HD < 128 ? 64 : 128;
-                const int rows = key ? S::KP : kPosTile;
-#pragma unroll
-                for (int c0 = 0; c0 < S::RAWB / 16; c0 += 128) {
-                    const int c = c0 + ct, box = c / (rows * (CW / 16)), in = c % (rows * (CW / 16)), r = in / (CW / 16), ch = in % (CW / 16);
-                    const int at = box * rows * CW + (CW == 128 ? swz128(r, ch) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + at);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] & 0xFFFFu), __NV_E4M3);
-                        const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] >> 16), __NV_E4M3);
-                        o[2 * e] = (uint32_t)h0.x | (uint32_t)h0.y << 16;
-                        o[2 * e + 1] = (uint32_t)h1.x | (uint32_t)h1.y << 16;
-                    }
-                    const int d = box * CW + ch * 16;   // first dimension
-                    unsigned char* q = dst + (d >> 6) * rows * 128;
-                    *reinterpret_cast<uint4*>(q + swz128(r, (d & 63) >> 3)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(q + swz128(r, ((d & 63) >> 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
+                if (key) open_codes<S::KP, HD, S::RAWB>(src, dst, ct);
+                else open_codes<kPosTile, HD, S::RAWB>(src, dst, ct);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -551,7 +562,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             }
         };
         Walk<SHARED> p;
-        p.start(t, sq, me);
+        p.start(first, sq);
         if (CG == 2 && rank == 1) {
             while (ok && p.next(t))
                 for (int i = 0; i < 2 * p.n && ok; ++i) {
@@ -708,7 +719,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             return y;
         };
         Walk<SHARED> p;
-        p.start(t, sq, me);
+        p.start(first, sq);
         bool more_pieces = p.next(t);
         while (more_pieces) {
             const int ofs = (CG == 2 ? rank : q) * 128;      // of the row tile in the item
@@ -778,7 +789,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 if (SHARED) touched = touched || mine;
                 // ---- probabilities against the reference there is; where a score lies above it,
                 // once more against a new one (the scores stay in place until all is well) ----
-                constexpr int CH = E4M3 && NH == 1 ? 16 : 32;   // positions of a load (registers)
+                constexpr int CH = HD < 256 ? 16 : 32;   // positions of a load (registers)
                 uint32_t o[CW / 2];
 #pragma unroll 1
                 for (int turn = 0; !idle; ++turn) {

@@ -51,7 +51,9 @@ static_assert(sizeof(BlockRec) == 48, "three 16-byte loads");
 struct __align__(16) WorkerRec {
     long long xs, xe;                 // share of the line
     long long begin;                  // the item's first unit
-    int blk, g, rt, pad_;
+    int blk, g, rt;
+    int open;                         // units before an item's tiles / U
+    BlockRec k;                       // the item's block
 };
 // an item that begins in a worker's share and ends behind it
 struct __align__(16) RowNote {
@@ -218,20 +220,19 @@ struct Walk {
     int nb, ng, nr;                   // of the next item
     int t0, n;                        // tiles [t0, t0 + n) of the item
     int slot;                         // 0: the whole item; 1: it began before; 2: it ends behind
-    int open, held;                   // units before an item's tiles / U; block that k is (-1: none)
+    int open, held;                   // units before an item's tiles / U; block that k is
     Sequences sq;
 
-    __device__ __forceinline__ void start(const RowsTcArgs& t, const Sequences& s, int worker) {
+    __device__ __forceinline__ void start(const WorkerRec& w, const Sequences& s) {
         sq = s;
-        const WorkerRec w = t.worker[worker];
         at = w.begin;
         xs = w.xs;
         xe = w.xe;
-        nb = w.blk;
+        held = nb = w.blk;
         ng = w.g;
         nr = w.rt;
-        open = t.head->open;
-        held = -1;
+        open = w.open;
+        k = w.k;
     }
     __device__ __forceinline__ bool next(const RowsTcArgs& t) {
         const int U = kPosTile * t.a.G;

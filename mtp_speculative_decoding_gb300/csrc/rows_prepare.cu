@@ -14,6 +14,9 @@ namespace {
 
 constexpr int kPrepThreads = 256;
 
+// group_start and prefix_len, copied to shared memory
+struct Groups { const int32_t *start, *len; };
+
 // sums of v over the threads in front of this one, and over all of the CTA
 __device__ __forceinline__ long long scan(long long v, long long* s, long long& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -41,7 +44,7 @@ __device__ __forceinline__ int own_tiles(const Seq& s) { return s.n > 0 ? (s.len
 
 // Tokens and own tiles before every sequence, cached positions (shared prefixes); false
 // if this thread saw something out of range.  cumt, lens null: tokens alone.
-__device__ __forceinline__ bool count_tokens(const RowsArgs& a, int* cum, int* cumt, int* lens, long long* tmp) {
+__device__ __forceinline__ bool count_tokens(const RowsArgs& a, const Groups& gr, int* cum, int* cumt, int* lens, long long* tmp) {
     bool good = true;
     constexpr int MAX = (MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads;
     const int per = (a.B + kPrepThreads - 1) / kPrepThreads, b0 = (int)threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
@@ -52,7 +55,7 @@ __device__ __forceinline__ bool count_tokens(const RowsArgs& a, int* cum, int* c
         n[i] = tl[i] = 0;
         if (b0 + i < b1) {
             Seq s;
-            good = seq_at(a, b0 + i, s) && good;
+            good = seq_at(a, b0 + i, s, gr.start, gr.len) && good;
             n[i] = s.n;
             tl[i] = own_tiles(s);
             if (lens) lens[b0 + i] = s.len;
@@ -83,24 +86,24 @@ __device__ __forceinline__ bool count_tokens(const RowsArgs& a, int* cum, int* c
 // The staged row of (sequence, token 0, KV head 0), and the rows of a KV head there.
 // Prompts: a sequence's own rows.  Shared prefixes: its group's.
 struct StagedAt { long long row; int stride; };
-__device__ __forceinline__ StagedAt staged_at(const RowsArgs& a, const int* cum, const Seq& s, int b) {
+__device__ __forceinline__ StagedAt staged_at(const RowsArgs& a, const Groups& gr, const int* cum, const Seq& s, int b) {
     StagedAt w;
     if (a.M == 0) {
         w.row = s.row0 * a.Hq;
         w.stride = s.n * a.G;
     } else {
-        const int g0 = s.group >= 0 ? s.first : b, g1 = s.group >= 0 ? a.group_start[s.group + 1] : b + 1;
+        const int g0 = s.group >= 0 ? s.first : b, g1 = s.group >= 0 ? gr.start[s.group + 1] : b + 1;
         w.stride = (cum[g1] - cum[g0]) * a.G;
         w.row = (long long)cum[g0] * a.Hq + (cum[b] - cum[g0]) * a.G;
     }
     return w;
 }
 
-__device__ BlockRec block_at(const RowsArgs& a, const int* cum, int blk, bool& good) {
+__device__ BlockRec block_at(const RowsArgs& a, const Groups& gr, const int* cum, int blk, bool& good) {
     BlockRec k = {};
     if (blk < 2 * a.n_groups) {
         const bool own = blk >= a.n_groups;
-        const int i = own ? blk - a.n_groups : blk, g0 = a.group_start[i], g1 = a.group_start[i + 1], P = a.prefix_len[i];
+        const int i = own ? blk - a.n_groups : blk, g0 = gr.start[i], g1 = gr.start[i + 1], P = gr.len[i];
         const bool ok = g0 >= 0 && g0 <= g1 && g1 <= a.B && P >= 0 && P <= (long long)a.c.max_pages << a.c.ps_log2;
         good = good && ok;
         k.kind = own ? kOwn : kPrefix;
@@ -117,10 +120,10 @@ __device__ BlockRec block_at(const RowsArgs& a, const int* cum, int blk, bool& g
     }
     Seq s;
     const int b = blk - 2 * a.n_groups;
-    good = seq_at(a, b, s) && good;
+    good = seq_at(a, b, s, gr.start, gr.len) && good;
     k.table = b;
     if (s.n > 0 && s.group < 0) {
-        const StagedAt w = staged_at(a, cum, s, b);
+        const StagedAt w = staged_at(a, gr, cum, s, b);
         k.n = s.n;
         k.len = s.len;
         k.hi = s.len + s.n;
@@ -133,24 +136,24 @@ __device__ BlockRec block_at(const RowsArgs& a, const int* cum, int blk, bool& g
 
 // The tiles before each item of the groups' own positions, group by group, and the
 // groups' first entries (rt0: [n_groups + 1] row tiles before a group)
-__device__ void count_items(const RowsTcArgs& t, const Sequences& sq, int* rt0, long long* tmp) {
+__device__ void count_items(const RowsTcArgs& t, const Groups& gr, const Sequences& sq, int* rt0, long long* tmp) {
     const RowsArgs& a = t.a;
     bool good = true;
     const int tid = threadIdx.x, per = (a.n_groups + kPrepThreads - 1) / kPrepThreads, i0 = tid * per,
               i1 = i0 + per < a.n_groups ? i0 + per : a.n_groups;
     long long sum = 0, all;
-    for (int i = i0; i < i1; ++i) sum += row_tiles_of(a, block_at(a, sq.cum, a.n_groups + i, good));
+    for (int i = i0; i < i1; ++i) sum += row_tiles_of(a, block_at(a, gr, sq.cum, a.n_groups + i, good));
     int at = (int)scan(sum, tmp, all);
     for (int i = i0; i < i1; ++i) {
         rt0[i] = at;
-        at += row_tiles_of(a, block_at(a, sq.cum, a.n_groups + i, good));
+        at += row_tiles_of(a, block_at(a, gr, sq.cum, a.n_groups + i, good));
     }
     if (tid == 0) rt0[a.n_groups] = (int)all;
     __syncthreads();
     const int items = (int)all, pi = (items + kPrepThreads - 1) / kPrepThreads, x0 = tid * pi, x1 = x0 + pi < items ? x0 + pi : items;
     auto tiles = [&](int x) {
         const int i = last_at_most(rt0, a.n_groups, x);
-        return item_of<true>(a, sq, block_at(a, sq.cum, a.n_groups + i, good), x - rt0[i]).n;
+        return item_of<true>(a, sq, block_at(a, gr, sq.cum, a.n_groups + i, good), x - rt0[i]).n;
     };
     sum = 0;
     for (int x = x0; x < x1; ++x) sum += tiles(x);
@@ -163,19 +166,20 @@ __device__ void count_items(const RowsTcArgs& t, const Sequences& sq, int* rt0, 
     __syncthreads();
 }
 
-__device__ void make_plan(const RowsTcArgs& t, const int* cum, const int* rt0, long long* tmp, long long* pre, bool good) {
+__device__ void make_plan(const RowsTcArgs& t, const Groups& gr, const int* cum, const int* rt0, long long* tmp, long long* pre, int* nrt, bool good) {
     const RowsArgs& a = t.a;
     const int tid = threadIdx.x, nb = rows_blocks(a), per = (nb + kPrepThreads - 1) / kPrepThreads, k0 = tid * per,
               k1 = k0 + per < nb ? k0 + per : nb;
     const long long U = (long long)kPosTile * a.G;
     long long tiles = 0, items = 0;
     for (int i = k0; i < k1; ++i) {
-        BlockRec k = block_at(a, cum, i, good);
+        BlockRec k = block_at(a, gr, cum, i, good);
         if (k.kind == kOwn) k.row0 = rt0[i - a.n_groups];
         t.blocks[i] = k;
-        const int nrt = row_tiles_of(a, k);
-        tiles += a.c.Hkv * tile_units(t, k, nrt);
-        items += (long long)a.c.Hkv * nrt;
+        nrt[i] = row_tiles_of(a, k);
+        pre[i] = a.c.Hkv * tile_units(t, k, nrt[i]);
+        tiles += pre[i];
+        items += (long long)a.c.Hkv * nrt[i];
     }
     long long units, n_items;
     long long at = scan(tiles, tmp, units);
@@ -184,17 +188,18 @@ __device__ void make_plan(const RowsTcArgs& t, const int* cum, const int* rt0, l
     int open = kRowsOpen;
     while (open > 0 && 2ll * open * U * t.workers > units) --open;
     at += it * open * U;
-    const long long T = units + n_items * open * U, most = T / U;
+    const long long T = units + n_items * open * U, most = quotient(T, U);
     const int workers = most < t.workers ? (most > 1 ? (int)most : 1) : t.workers;
     for (int i = k0; i < k1; ++i) {
+        const long long u = pre[i] + (long long)a.c.Hkv * nrt[i] * open * U;
         pre[i] = at;
-        BlockRec k = t.blocks[i];
         t.blocks[i].pre = at;
-        at += a.c.Hkv * units_before(t, k, open, row_tiles_of(a, k));
+        at += u;
     }
     __syncthreads();   // (the records of the other threads too)
     for (int w = tid; w < t.workers; w += kPrepThreads) {
         WorkerRec r = {};
+        r.open = open;
         r.xs = w < workers ? share_at(T, workers, w) : T;
         r.xe = w < workers ? share_at(T, workers, w + 1) : T;
         if (r.xs < r.xe) {
@@ -205,13 +210,12 @@ __device__ void make_plan(const RowsTcArgs& t, const int* cum, const int* rt0, l
                 else hi = mid - 1;
             }
             const BlockRec k = t.blocks[b];
-            const int nrt = row_tiles_of(a, k);
-            const long long head = units_before(t, k, open, nrt);
+            const long long head = units_before(t, k, open, nrt[b]);
             long long rel = r.xs - pre[b];
             const int g = (int)quotient(rel, head);
             rel -= g * head;
             int rt = 0;
-            for (int hi = nrt - 1; rt < hi;) {
+            for (int hi = nrt[b] - 1; rt < hi;) {
                 const int mid = (rt + hi + 1) >> 1;
                 if (units_before(t, k, open, mid) <= rel) rt = mid;
                 else hi = mid - 1;
@@ -220,6 +224,7 @@ __device__ void make_plan(const RowsTcArgs& t, const int* cum, const int* rt0, l
             r.g = g;
             r.rt = rt;
             r.begin = pre[b] + g * head + units_before(t, k, open, rt);
+            r.k = k;
         } else {
             r.begin = T;
         }
@@ -236,7 +241,7 @@ __device__ void make_plan(const RowsTcArgs& t, const int* cum, const int* rt0, l
     if (tid == 0) t.cta_status[t.workers * rows_pair(a.hd)] = any ? MTP_ERR_ARG : MTP_OK;
 }
 
-__host__ __device__ constexpr size_t prep_ints(int B, int n_groups) { return (((size_t)3 * B + n_groups + 4) * 4 + 7) / 8 * 8; }
+__host__ __device__ constexpr size_t prep_ints(int B, int n_groups) { return (((size_t)4 * B + 5 * n_groups + 8) * 4 + 7) / 8 * 8; }
 
 template <bool E4M3>
 __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid_constant__ RowsTcArgs t, int hpt) {
@@ -245,9 +250,11 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
     __shared__ __align__(16) float s_hi[256], s_lo[256];
     const RowsArgs& a = t.a;
     int* cum = reinterpret_cast<int*>(sm);                                     // [B + 1] prompts: row_start
-    // the plan's CTA: own tiles before a sequence, cached positions, row tiles before a group, units before a block
-    int *cumt = cum + a.B + 1, *lens = cumt + a.B + 1, *rt0 = lens + a.B;
+    int *g_start = cum + a.B + 1, *g_len = g_start + a.n_groups + 1;           // [n_groups + 1], [n_groups]
+    // the plan's CTA: own tiles before a sequence, cached positions, row tiles before a group and of a block, units before a block
+    int *cumt = g_len + a.n_groups, *lens = cumt + a.B + 1, *rt0 = lens + a.B, *nrt = rt0 + a.n_groups + 1;
     long long* pre = reinterpret_cast<long long*>(sm + prep_ints(a.B, a.n_groups));
+    const Groups gr = {g_start, g_len};
     const int tid = threadIdx.x;
     const bool planner = blockIdx.x == 0;
     if (a.rope.on && !planner)
@@ -258,7 +265,14 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     bool good = true;
-    if (a.M > 0) good = count_tokens(a, cum, planner ? cumt : nullptr, planner ? lens : nullptr, tmp);
+    if (a.n_groups > 0) {
+        for (int i = tid; i <= a.n_groups; i += kPrepThreads) {
+            g_start[i] = a.group_start[i];
+            if (i < a.n_groups) g_len[i] = a.prefix_len[i];
+        }
+        __syncthreads();
+    }
+    if (a.M > 0) good = count_tokens(a, gr, cum, planner ? cumt : nullptr, planner ? lens : nullptr, tmp);
     else
         for (int i = tid; i <= a.B; i += kPrepThreads) cum[i] = a.row_start[i];
     __syncthreads();
@@ -269,9 +283,9 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
                 t.cumt[i] = cumt[i];
                 if (i < a.B) t.lens[i] = lens[i];
             }
-            count_items(t, Sequences{cum, cumt, lens}, rt0, tmp);
+            count_items(t, gr, Sequences{cum, cumt, lens}, rt0, tmp);
         }
-        make_plan(t, cum, rt0, tmp, pre, good);
+        make_plan(t, gr, cum, rt0, tmp, pre, nrt, good);
         return;
     }
     const int hd = a.hd, U = hd >> 4, ulog = 31 - __clz(U), groups = (a.Hq + hpt - 1) / hpt, half = hd >> 1;
@@ -284,11 +298,11 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
     if (!live) tok = toks - 1;
     const int b = a.M > 0 ? tok / a.M : last_at_most(cum, a.B, tok);
     Seq s;
-    live = seq_at(a, b, s) && live;
+    live = seq_at(a, b, s, gr.start, gr.len) && live;
     const int j = (int)(tok - s.row0);
     live = live && j >= 0 && j < s.n;
     if (!__any_sync(0xffffffffu, live)) return;
-    const StagedAt w = live ? staged_at(a, cum, s, b) : StagedAt{0, 0};
+    const StagedAt w = live ? staged_at(a, gr, cum, s, b) : StagedAt{0, 0};
     const long long src0 = live ? s.q0 + j * a.sm : 0;
     float cs[8], sn[8];
     if (a.rope.on) unit_angles<true>((long long)(live ? s.len + j : 0), s_hi + 8 * c, s_lo + 8 * c, cs, sn);
@@ -299,50 +313,62 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
             g0[i] = __ldg(a.q_norm + 8 * c + i);
             g1[i] = __ldg(a.q_norm + half + 8 * c + i);
         }
-#pragma unroll 2
-    for (int i = 0; i < hpt; ++i) {
-        const int h = h0 + i < a.Hq ? h0 + i : a.Hq - 1;
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (live ? src0 + h * a.sh : 0) + 8 * c;
-        float p[8], q[8];
-        load8(src, p);
-        load8(src + half, q);
-        if (a.q_norm) {
-            const float r = unit_rms(p, q, hd, a.eps);
+    constexpr int N = 4;   // heads in flight
+#pragma unroll 1
+    for (int i0 = 0; i0 < hpt; i0 += N) {
+        uint4 raw[N][2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                p[e] *= r * g0[e];
-                q[e] *= r * g1[e];
+        for (int i = 0; i < N; ++i) {
+            const int h = h0 + i0 + i < a.Hq ? h0 + i0 + i : a.Hq - 1;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (live ? src0 + h * a.sh : 0) + 8 * c;
+            raw[i][0] = ld_stream16(src);
+            raw[i][1] = ld_stream16(src + half);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i0 + i >= hpt) break;
+            const int h = h0 + i0 + i;
+            float p[8], q[8];
+            open_unit(raw[i][0], p);
+            open_unit(raw[i][1], q);
+            if (a.q_norm) {
+                const float r = unit_rms(p, q, hd, a.eps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] *= r * g0[e];
+                    q[e] *= r * g1[e];
+                }
             }
-        }
-        if (a.rope.on) unit_rotate(p, q, cs, sn);
-        const int g = h / a.G;
-        const long long row = w.row + (long long)g * w.stride + j * a.G + h - g * a.G;
-        const bool mine = live && h0 + i < a.Hq;
-        uint4 o[2];
-        if (E4M3) {   // the largest of the row into [128, 256): no bits lost to fp16's range
-            float big = 0.f;
+            if (a.rope.on) unit_rotate(p, q, cs, sn);
+            const int g = (int)udiv((unsigned)h, (unsigned)a.G);
+            const long long row = w.row + (long long)g * w.stride + j * a.G + h - g * a.G;
+            const bool mine = live && h < a.Hq;
+            uint4 o[2];
+            if (E4M3) {   // the largest of the row into [128, 256): no bits lost to fp16's range
+                float big = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(p[e]), fabsf(q[e])));
-            for (int k = U >> 1; k > 0; k >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
-            int x2 = (int)(__float_as_uint(big) >> 23) - 127 - 7;
-            x2 = x2 < -100 ? -100 : x2 > 100 ? 100 : x2;
-            const float f = __uint_as_float((uint32_t)(127 - x2) << 23);
-            if (mine && c == 0) t.q_scale[row] = __uint_as_float((uint32_t)(127 + x2) << 23) * a.scale;
-            auto half2 = [&](float lo, float hi) {
-                uint32_t r;
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi * f), "f"(lo * f));
-                return r;
-            };
-            o[0] = make_uint4(half2(p[0], p[1]), half2(p[2], p[3]), half2(p[4], p[5]), half2(p[6], p[7]));
-            o[1] = make_uint4(half2(q[0], q[1]), half2(q[2], q[3]), half2(q[4], q[5]), half2(q[6], q[7]));
-        } else {
-            o[0] = make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
-            o[1] = make_uint4(pack_bf16(q[0], q[1]), pack_bf16(q[2], q[3]), pack_bf16(q[4], q[5]), pack_bf16(q[6], q[7]));
-        }
-        if (mine) {
-            uint16_t* dst = t.staged + row * hd + 8 * c;
-            *reinterpret_cast<uint4*>(dst) = o[0];
-            *reinterpret_cast<uint4*>(dst + half) = o[1];
+                for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(p[e]), fabsf(q[e])));
+                for (int k = U >> 1; k > 0; k >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
+                int x2 = (int)(__float_as_uint(big) >> 23) - 127 - 7;
+                x2 = x2 < -100 ? -100 : x2 > 100 ? 100 : x2;
+                const float f = __uint_as_float((uint32_t)(127 - x2) << 23);
+                if (mine && c == 0) t.q_scale[row] = __uint_as_float((uint32_t)(127 + x2) << 23) * a.scale;
+                auto half2 = [&](float lo, float hi) {
+                    uint32_t r;
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi * f), "f"(lo * f));
+                    return r;
+                };
+                o[0] = make_uint4(half2(p[0], p[1]), half2(p[2], p[3]), half2(p[4], p[5]), half2(p[6], p[7]));
+                o[1] = make_uint4(half2(q[0], q[1]), half2(q[2], q[3]), half2(q[4], q[5]), half2(q[6], q[7]));
+            } else {
+                o[0] = make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+                o[1] = make_uint4(pack_bf16(q[0], q[1]), pack_bf16(q[2], q[3]), pack_bf16(q[4], q[5]), pack_bf16(q[6], q[7]));
+            }
+            if (mine) {
+                uint16_t* dst = t.staged + row * hd + 8 * c;
+                *reinterpret_cast<uint4*>(dst) = o[0];
+                *reinterpret_cast<uint4*>(dst + half) = o[1];
+            }
         }
     }
 }
@@ -362,7 +388,13 @@ cudaError_t launch_rows_prepare(const RowsTcArgs& t, int kv_dtype, int sms, cuda
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas + 1);
     cfg.blockDim = dim3(kPrepThreads);
-    cfg.dynamicSmemBytes = prep_ints(a.B, a.n_groups) + (size_t)rows_blocks(a) * 8;   // (at most 41 KB)
+    cfg.dynamicSmemBytes = prep_ints(a.B, a.n_groups) + (size_t)rows_blocks(a) * 8;
+    if (cfg.dynamicSmemBytes > 40 * 1024) {   // the most, so that two host threads' calls do not disturb each other
+        constexpr int most = (int)(prep_ints(MTP_MAX_PAGED_BATCH, MTP_MAX_PAGED_BATCH) + 3 * MTP_MAX_PAGED_BATCH * 8);
+        const cudaError_t e = kv_dtype == MTP_DTYPE_E4M3 ? cudaFuncSetAttribute(rows_prepare_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)
+                                                         : cudaFuncSetAttribute(rows_prepare_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e != cudaSuccess) return e;
+    }
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
