@@ -84,14 +84,9 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
         float p[N][8], q[N][8];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int h = h0 + i0 + i;
-            if (h < h1) {
-                in8(src + h * a.in_sh[which] + e0, p[i]);
-                in8(src + h * a.in_sh[which] + e1, q[i]);
-            } else {   // (every lane of the warp takes part in the norm)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[i][e] = q[i][e] = 0.f;
-            }
+            const int h = h0 + i0 + i < h1 ? h0 + i0 + i : h1 - 1;   // (every lane of the warp takes part in the norm)
+            in8(src + h * a.in_sh[which] + e0, p[i]);
+            in8(src + h * a.in_sh[which] + e1, q[i]);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -119,8 +114,10 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
 cudaError_t launch_rotate_axes(RotateArgs a, int dtype, int sms, cudaStream_t s) {
     // as many heads in one thread as leave 512 threads an SM: an angle costs as much as
     // the rest of four elements
+    // (and no more than divide both, where that leaves four: a group's missing heads cost as
+    // much as others)
     a.hpt = 1;
-    while (a.hpt < 16 && (long long)a.rows * ((a.heads[0] + a.heads[1]) / (2 * a.hpt)) * (a.hd >> 4) >= (long long)sms * 512) a.hpt *= 2;
+    while (a.hpt < 16 && (a.hpt < 4 || (a.heads[0] | a.heads[1]) % (2 * a.hpt) == 0) && (long long)a.rows * ((a.heads[0] + a.heads[1]) / (2 * a.hpt)) * (a.hd >> 4) >= (long long)sms * 512) a.hpt *= 2;
     for (int w = 0; w < 2; ++w) a.groups[w] = (a.heads[w] + a.hpt - 1) / a.hpt;
     const long long threads = (long long)a.rows * (a.groups[0] + a.groups[1]) * (a.hd >> 4);
     const unsigned grid = (unsigned)((threads + kRotThreads - 1) / kRotThreads);

@@ -272,6 +272,11 @@ struct RowShape {
     static __device__ __forceinline__ unsigned v_at(int k, int n) { return CG == 1 ? 2 * k + 1 : k == n - 1 ? 2 * n - 1 : 2 * k + 2; }
 };
 
+// Score buffer of a tile that concerns one row tile: two such in a row take turns, so
+// that one's scores are computed while the other's weights are (both row tiles: a buffer
+// each).  rows, was: row tiles of this tile and of the one before, side: the buffer then.
+__device__ __forceinline__ int score_side(int rows, int was, int side) { return rows == 3 || was == 3 ? 0 : side ^ 1; }
+
 template <bool E4M3, int HD, bool SHARED>
 __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcParams pp) {
     using S = RowShape<E4M3, HD>;
@@ -286,12 +291,12 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
     unsigned char* raw = ring + (size_t)NS * S::SLOTB;
     uint4* m_bits = reinterpret_cast<uint4*>(raw + (size_t)NR * S::RAWB);       // [kRowsMeta] positions that are there
     float2* m_sc = reinterpret_cast<float2*>(m_bits + kRowsMeta);               // [kRowsMeta][8] key scale, value scale's exponent, every 16 positions
-    int4* m_flag = reinterpret_cast<int4*>(m_sc + kRowsMeta * 8);               // [kRowsMeta] x: row tiles, 4: all positions there; y: sequence; z, w: the tile's [pos, end)
+    int4* m_flag = reinterpret_cast<int4*>(m_sc + kRowsMeta * 8);               // [kRowsMeta] x: row tiles, 4: all positions there, 8: score buffer (one row tile); y: sequence; z, w: the tile's [pos, end)
     float* s_x = reinterpret_cast<float*>(m_flag + kRowsMeta);                  // [NQ][2][128] what the threads of a row tell each other
     unsigned long long* bars = reinterpret_cast<unsigned long long*>(s_x + 2 * kRowTile);
     unsigned long long *full = bars, *empty = full + kRowsSlots, *peer = empty + kRowsSlots, *rfull = peer + kRowsSlots,
-                       *rempty = rfull + kRowsRaw, *meta = rempty + kRowsRaw, *s_full = meta + kRowsMeta, *p_full = s_full + 2,
-                       *pv_done = p_full + 2, *o_free = pv_done + 2, *q_full = o_free + 2, *q_peer = q_full + 1, *q_free = q_peer + 1,
+                       *rempty = rfull + kRowsRaw, *meta = rempty + kRowsRaw, *s_full = meta + kRowsMeta, *p_full = s_full + 4,
+                       *pv_done = p_full + 2, *o_free = pv_done + 4, *q_full = o_free + 2, *q_peer = q_full + 1, *q_free = q_peer + 1,
                        *end_bar = q_free + 1;
     int* s_tab = reinterpret_cast<int*>(bars + 3 * kRowsSlots + 2 * kRowsRaw + kRowsMeta + 16);   // shared prefixes: the sequences' tables
     const Sequences sq = {s_tab, s_tab + a.B + 1, s_tab + 2 * a.B + 2};
@@ -311,10 +316,12 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             mbar_init(rempty + i, 4);
         }
         for (int i = 0; i < kRowsMeta; ++i) mbar_init(meta + i, 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(s_full + i, 1);     // [row tile][score buffer]
+            mbar_init(pv_done + i, 1);    // [row tile][its tiles in turns: a wait may be two of them behind]
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 4 * CG * S::NH);
-            mbar_init(pv_done + i, 1);
+            mbar_init(p_full + i, 4 * CG * S::NH);   // [score buffer]
             mbar_init(o_free + i, 4 * CG * S::NH);
         }
         mbar_init(q_full, 1);
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
             };
             Tile nt = {};
-            int npg = entry(0, nt), held = -2, held_pos = 0;
+            int npg = entry(0, nt), held = -2, held_pos = 0, was = 3, side = 0;
 #pragma unroll 1
             for (int k = 0; k <= p.n && ok; ++k) {
                 const int pg = npg;
@@ -451,11 +458,13 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     const float k8 = __shfl_sync(0xffffffffu, ks, src), e8 = __shfl_sync(0xffffffffu, ev, src);
                     const unsigned have = __ballot_sync(0xffffffffu, lane < 8 && th) & 0xFFu;
                     const unsigned mi = ti % kRowsMeta;
+                    side = score_side(tile.rows, was, side);
+                    was = tile.rows;
                     if (lane < 8 && E4M3) m_sc[mi * 8 + lane] = make_float2(k8, e8);
                     if (lane == 0) {
                         auto word = [&](int i) { return ((have >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((have >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u); };
                         m_bits[mi] = make_uint4(word(0), word(1), word(2), word(3));
-                        m_flag[mi] = make_int4((have == 0xFFu ? 4 : 0) | tile.rows, tile.seq, tile.pos, tile.end);
+                        m_flag[mi] = make_int4((have == 0xFFu ? 4 : 0) | tile.rows | side << 3, tile.seq, tile.pos, tile.end);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(meta + mi);
@@ -573,7 +582,9 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 }
         } else {
             const uint32_t q0 = smem_addr(sQ) >> 4, r0 = smem_addr(ring) >> 4;
-            unsigned tq[2] = {0u, 0u}, sq_n[2] = {0u, 0u};   // tiles and pieces of a row tile so far
+            // bit i: odd uses of score buffer i, pieces and products of row tile i so far (a pair's
+            // score buffers take turns: t0 tiles)
+            unsigned sbit = 0u, pbit = 0u, vbit = 0u, t0 = 0u;
             auto arrived = [&] {
                 hold(full + slot, phase);
                 if (CG == 2) hold(peer + slot, phase);
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         for (int ks = 0; ks < 4; ++ks)
                             umma_ss<CG>(tmem + buf * 128, al + (b * 128 * 128 + ks * 32 >> 4), bl + (b * S::KP * 128 + ks * 32 >> 4), kDescHi, idS,
                                         b > 0 || ks > 0);
-                    commit<CG>(s_full + buf);
+                    commit<CG>(s_full + 2 * q + buf);
                 }
                 __syncwarp();
             };
@@ -597,9 +608,10 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
 #pragma unroll
                     for (int ks = 0; ks < kPosTile / 16; ++ks)
                         umma_ts<CG>(tmem + S::O0 + q * S::OC, tmem + buf * 128 + ks * 8, bl + (ks * 16 * 128 >> 4), kDescHi, idO, !first || ks > 0);
-                    commit<CG>(pv_done + buf);   // (a pair's tiles take turns, as a wait may be two tiles behind)
+                    commit<CG>(pv_done + 2 * q + (vbit >> q & 1u));
                 }
                 __syncwarp();
+                vbit ^= 1u << q;
             };
             auto done = [&] {   // the slot may be filled again
                 if (ok && elect()) commit<CG>(empty + slot);
@@ -613,7 +625,6 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 if (CG == 2) hold(q_peer, seg & 1);
                 ++seg;
                 if (CG == 2) {
-                    const unsigned t0 = tq[0];
 #pragma unroll 1
                     for (int k = 0; k <= n && ok; ++k) {
                         if (k < n) {
@@ -627,41 +638,60 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                         }
                         if (k > 0) {
                             const unsigned u = t0 + k - 1;
-                            if (k == 1) hold(o_free, (sq_n[0] & 1) ^ 1);
+                            if (k == 1) hold(o_free, (pbit & 1u) ^ 1u);
                             arrived();
                             hold(p_full + (u & 1), (u >> 1) & 1);
                             values(0, u & 1, slot, k == 1);
                             done();
                         }
                     }
-                    tq[0] += n;
-                    ++sq_n[0];
+                    t0 += n;
+                    pbit ^= 1u;
                 } else {
                     // slots take turns: K tile k, V tile k; a tile concerns one row tile or both
                     unsigned vslot = 0, vphase = 0;
                     int rows = 0, had = 0;           // row tiles of tile k - 1, of the piece so far
+                    int side = 0;                    // score buffer of tile k - 1
                     auto rows_at = [&](int k) { return SHARED && p.k.kind == kOwn ? tile_of<SHARED>(a, sq, p.k, p.it, p.t0 + k).rows : p.it.rows > 128 ? 3 : 1; };
                     int ahead = rows_at(0);          // looked up while the products before run
+                    auto score = [&](int q, int buf) {
+                        scores(q, buf);
+                        sbit ^= 1u << buf;
+                    };
+                    auto value = [&](int q, int buf) {
+                        const bool first = !(had >> q & 1);
+                        if (first) hold(o_free + q, (pbit >> q & 1u) ^ 1u);
+                        hold(p_full + buf, (sbit >> buf & 1u) ^ 1u);
+                        values(q, buf, vslot, first);
+                        had |= 1 << q;
+                    };
 #pragma unroll 1
                     for (int k = 0; k <= n && ok; ++k) {
                         const bool more = k < n;
                         const int now = more ? ahead : 0;
                         if (more) arrived();
                         else more_pieces = p.next(t);
-                        if (k > 0) hold(full + vslot, vphase);
+                        if (rows == 3 || !SHARED) {
+                            if (k > 0) hold(full + vslot, vphase);
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            if (rows >> q & 1) {
-                                const bool first = !(had >> q & 1);
-                                if (first) hold(o_free + q, (sq_n[q] & 1) ^ 1);
-                                hold(p_full + q, (tq[q] - 1) & 1);
-                                values(q, q, vslot, first);
-                                had |= 1 << q;
+                            for (int q = 0; q < 2; ++q) {
+                                if (rows >> q & 1) value(q, q);
+                                if (now == 3 || (!SHARED && now >> q & 1)) score(q, q);
                             }
-                            if (now >> q & 1) {
-                                scores(q, q);
-                                ++tq[q];
+                            if (SHARED && (now == 1 || now == 2)) score(now - 1, 0);
+                            side = 0;
+                        } else {
+                            const int to = score_side(now, k == 0 ? 3 : rows, side);
+                            if (now == 1 || now == 2) score(now - 1, to);
+                            if (k > 0) {
+                                hold(full + vslot, vphase);
+                                value(rows - 1, side);
                             }
+                            if (now == 3) {
+                                score(0, 0);
+                                score(1, 1);
+                            }
+                            side = to;
                         }
                         rows = now;
                         if (k > 0 && ok && elect()) commit<CG>(empty + vslot);
@@ -676,8 +706,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                             if (k + 1 < n) ahead = rows_at(k + 1);
                         }
                     }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) sq_n[q] += had >> q & 1;
+                    pbit ^= (unsigned)had;
                 }
             }
             if (elect()) commit<CG>(end_bar);   // whatever was issued has ended before its memory goes
@@ -695,13 +724,14 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t oat = tmem + lanes + S::O0 + q * S::OC + half * (HD / NH);   // this thread's part of the accumulator
         unsigned tc = 0, ti = 0, g0 = 0;                     // tiles of this row tile, of the CTA; ring slots before this piece
+        unsigned used = 0;                                   // bit b: odd uses of score buffer b by this row tile
         auto meet = [&](unsigned long long* bar, unsigned parity) {
             wait(bar, parity);
             __syncwarp();
         };
         // tile i of this row tile is in the accumulator
         auto meet_values = [&](unsigned i) {
-            wait(pv_done + (CG == 2 ? i & 1 : q), CG == 2 ? (i >> 1) & 1 : i & 1);
+            wait(pv_done + 2 * q + (i & 1), (i >> 1) & 1);
             __syncwarp();
             tc_fence_after();
         };
@@ -745,11 +775,14 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 const int t0 = SHARED ? flag.z : tile_of<SHARED>(a, sq, p.k, p.it, p.t0 + k).pos;
                 const bool mine = !SHARED || p.k.kind != kOwn || seq == flag.y;   // the tile is on this row's sequence
                 int zq = 0;                                  // the row tile that looks after the tile's values
+                int buf = CG == 2 ? (int)(tc & 1) : q;
                 if (CG == 1) {
                     if (!(flag.x >> q & 1)) continue;        // the other row tile's alone
+                    if (SHARED && (flag.x & 3) != 3) buf = flag.x >> 3 & 1;
                     zq = flag.x & 1 ? 0 : 1;
                 }
-                const int buf = CG == 2 ? (int)(tc & 1) : q;
+                const unsigned parity = used >> buf & 1u;
+                used ^= 1u << buf;
                 const uint32_t sat = tmem + lanes + buf * 128;
                 // every row of the item attends every position of the tile
                 const bool whole = (flag.x & 4) && (!SHARED || (p.k.kind != kOwn && t0 >= p.k.lo)) &&
@@ -769,9 +802,9 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 if (!whole)
 #pragma unroll
                     for (int i = 0; i < CW / 32; ++i) bits[i] = on_bits(half * (CW / 32) + i);
-                meet(s_full + buf, CG == 2 ? (tc >> 1) & 1 : tc & 1);
+                meet(s_full + 2 * q + buf, parity);
                 tc_fence_after();
-                if (none) {
+                if (none || (SHARED && __any_sync(0xffffffffu, mine && !touched))) {
                     // a first reference from the tile's first 16 positions: seldom does a score lie
                     // 2^kSlack above it
                     uint32_t s[16];
@@ -783,10 +816,9 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     for (int i = 0; i < 16; ++i) x = fmaxf(x, on >> i & 1u ? __uint_as_float(s[i]) : -__int_as_float(0x7F800000));
                     if (E4M3) x = fmaf(x, m_sc[mi * 8].x * qc, m_sc[mi * 8].y);
                     else x *= qc;
-                    m = fmaxf(m, x);
+                    if (!SHARED || !touched) m = fmaxf(m, x);
                 }
                 const bool idle = SHARED && p.k.kind == kOwn && !__any_sync(0xffffffffu, mine);   // none of this warp's rows: weights of zero
-                if (SHARED) touched = touched || mine;
                 // ---- probabilities against the reference there is; where a score lies above it,
                 // once more against a new one (the scores stay in place until all is well) ----
                 constexpr int CH = HD < 256 ? 16 : 32;   // positions of a load (registers)
@@ -855,9 +887,10 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     // move the references, and with them what has been summed
                     if (NH == 2) mx = fmaxf(mx, others(mx));
                     const float mn = fmaxf(mx, m), f = ex2(m - mn);
+                    const bool scale = any_of_rows((!SHARED || touched) && f != 1.f);   // (where nothing is summed yet all is zero)
                     l *= f;
                     m = mn;
-                    if (!none) {
+                    if (!none && scale) {
                         meet_values(tc - 1);
 #pragma unroll 1
                         for (int c = 0; c < HD / NH; c += 32) {
@@ -878,6 +911,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     for (int i = 0; i < CW / 2; ++i) o[i] = 0u;
                 }
                 none = false;
+                if (SHARED) touched = touched || mine;
 #pragma unroll
                 for (int i = 0; i < CW / 64; ++i)   // over the scores
                     st32(sat + half * (CW / 2) + 32 * i, *reinterpret_cast<const uint32_t(*)[32]>(o + 32 * i));
