@@ -589,34 +589,34 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 hold(full + slot, phase);
                 if (CG == 2) hold(peer + slot, phase);
             };
-            auto scores = [&](int q, int buf) {
-                const uint32_t al = q0 + q * (S::QB >> 4) + lead_bits(16), bl = r0 + slot * (S::SLOTB >> 4) + lead_bits(16);
+            // the products of a step, by one lane: first P V of tile k - 1, then Q K^T of tile k (each
+            // where it is asked for), and what they free
+            auto issue = [&](bool pv, int q, int pbuf, unsigned at, bool first, bool v_done, bool qk, int sq_, int sbuf, bool k_done, bool q_done) {
                 if (ok && elect()) {
+                    if (pv) {
+                        const uint32_t bl = r0 + at * (S::SLOTB >> 4) + lead_bits(S::VD > 64 ? kPosTile * 128 : 16);
 #pragma unroll
-                    for (int b = 0; b < HD / 64; ++b)
+                        for (int ks = 0; ks < kPosTile / 16; ++ks)
+                            umma_ts<CG>(tmem + S::O0 + q * S::OC, tmem + pbuf * 128 + ks * 8, bl + (ks * 16 * 128 >> 4), kDescHi, idO, !first || ks > 0);
+                        commit<CG>(pv_done + 2 * q + (vbit >> q & 1u));
+                        if (v_done) commit<CG>(empty + at);
+                    }
+                    if (qk) {
+                        const uint32_t al = q0 + sq_ * (S::QB >> 4) + lead_bits(16), bl = r0 + slot * (S::SLOTB >> 4) + lead_bits(16);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            umma_ss<CG>(tmem + buf * 128, al + (b * 128 * 128 + ks * 32 >> 4), bl + (b * S::KP * 128 + ks * 32 >> 4), kDescHi, idS,
-                                        b > 0 || ks > 0);
-                    commit<CG>(s_full + 2 * q + buf);
+                        for (int b = 0; b < HD / 64; ++b)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                umma_ss<CG>(tmem + sbuf * 128, al + (b * 128 * 128 + ks * 32 >> 4), bl + (b * S::KP * 128 + ks * 32 >> 4), kDescHi,
+                                            idS, b > 0 || ks > 0);
+                        commit<CG>(s_full + 2 * sq_ + sbuf);
+                        if (k_done) commit<CG>(empty + slot);
+                        if (q_done) commit<CG>(q_free);
+                    }
                 }
                 __syncwarp();
-            };
-            auto values = [&](int q, int buf, unsigned at, bool first) {
-                const uint32_t bl = r0 + at * (S::SLOTB >> 4) + lead_bits(S::VD > 64 ? kPosTile * 128 : 16);
-                if (ok && elect()) {
-#pragma unroll
-                    for (int ks = 0; ks < kPosTile / 16; ++ks)
-                        umma_ts<CG>(tmem + S::O0 + q * S::OC, tmem + buf * 128 + ks * 8, bl + (ks * 16 * 128 >> 4), kDescHi, idO, !first || ks > 0);
-                    commit<CG>(pv_done + 2 * q + (vbit >> q & 1u));
-                }
-                __syncwarp();
-                vbit ^= 1u << q;
-            };
-            auto done = [&] {   // the slot may be filled again
-                if (ok && elect()) commit<CG>(empty + slot);
-                __syncwarp();
-                next();
+                if (pv) vbit ^= 1u << q;
+                if (qk) sbit ^= 1u << sbuf;
             };
             bool more_pieces = p.next(t);
             while (ok && more_pieces) {
@@ -629,10 +629,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     for (int k = 0; k <= n && ok; ++k) {
                         if (k < n) {
                             arrived();
-                            scores(0, (t0 + k) & 1);
-                            done();
-                            if (k == n - 1 && ok && elect()) commit<CG>(q_free);
-                            __syncwarp();
+                            issue(false, 0, 0, 0, false, false, true, 0, (t0 + k) & 1, true, k == n - 1);
+                            next();
                         } else {
                             more_pieces = p.next(t);
                         }
@@ -641,8 +639,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                             if (k == 1) hold(o_free, (pbit & 1u) ^ 1u);
                             arrived();
                             hold(p_full + (u & 1), (u >> 1) & 1);
-                            values(0, u & 1, slot, k == 1);
-                            done();
+                            issue(true, 0, u & 1, slot, k == 1, true, false, 0, 0, false, false);
+                            next();
                         }
                     }
                     t0 += n;
@@ -654,52 +652,53 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     int side = 0;                    // score buffer of tile k - 1
                     auto rows_at = [&](int k) { return SHARED && p.k.kind == kOwn ? tile_of<SHARED>(a, sq, p.k, p.it, p.t0 + k).rows : p.it.rows > 128 ? 3 : 1; };
                     int ahead = rows_at(0);          // looked up while the products before run
-                    auto score = [&](int q, int buf) {
-                        scores(q, buf);
-                        sbit ^= 1u << buf;
-                    };
-                    auto value = [&](int q, int buf) {
-                        const bool first = !(had >> q & 1);
-                        if (first) hold(o_free + q, (pbit >> q & 1u) ^ 1u);
+                    auto weights = [&](int q, int buf) {   // row tile q's of tile k - 1 are there, and its accumulator is free
+                        if (!(had >> q & 1)) hold(o_free + q, (pbit >> q & 1u) ^ 1u);
                         hold(p_full + buf, (sbit >> buf & 1u) ^ 1u);
-                        values(q, buf, vslot, first);
-                        had |= 1 << q;
                     };
 #pragma unroll 1
                     for (int k = 0; k <= n && ok; ++k) {
-                        const bool more = k < n;
+                        const bool more = k < n, end = k == n - 1;
                         const int now = more ? ahead : 0;
                         if (more) arrived();
                         else more_pieces = p.next(t);
-                        if (rows == 3 || !SHARED) {
-                            if (k > 0) hold(full + vslot, vphase);
+                        if (k > 0) hold(full + vslot, vphase);
+                        if (!SHARED || (rows == 3 && now != 1 && now != 2)) {   // a buffer a row tile
 #pragma unroll
                             for (int q = 0; q < 2; ++q) {
-                                if (rows >> q & 1) value(q, q);
-                                if (now == 3 || (!SHARED && now >> q & 1)) score(q, q);
+                                const bool pv = rows >> q & 1, qk = now >> q & 1, last = q == 1 || !((rows | now) >> 1);
+                                if (!pv && !qk) continue;
+                                if (pv) weights(q, q);
+                                issue(pv, q, q, vslot, !(had >> q & 1), last, qk, q, q, last, last && end);
+                                if (pv) had |= 1 << q;
                             }
-                            if (SHARED && (now == 1 || now == 2)) score(now - 1, 0);
                             side = 0;
                         } else {
                             const int to = score_side(now, k == 0 ? 3 : rows, side);
-                            if (now == 1 || now == 2) score(now - 1, to);
-                            if (k > 0) {
-                                hold(full + vslot, vphase);
-                                value(rows - 1, side);
+                            const bool one = now == 1 || now == 2;
+                            // (scores of one row tile first, unless both buffers hold weights)
+                            if (one && rows != 3) issue(false, 0, 0, 0, false, false, true, now - 1, to, true, end);
+                            if (rows == 3) {
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    weights(q, q);
+                                    issue(true, q, q, vslot, !(had >> q & 1), q == 1, false, 0, 0, false, false);
+                                }
+                            } else if (rows) {
+                                weights(rows - 1, side);
+                                issue(true, rows - 1, side, vslot, !(had >> (rows - 1) & 1), true, false, 0, 0, false, false);
                             }
+                            had |= rows;
+                            if (one && rows == 3) issue(false, 0, 0, 0, false, false, true, now - 1, to, true, end);
                             if (now == 3) {
-                                score(0, 0);
-                                score(1, 1);
+                                issue(false, 0, 0, 0, false, false, true, 0, 0, false, false);
+                                issue(false, 0, 0, 0, false, false, true, 1, 1, true, end);
                             }
                             side = to;
                         }
                         rows = now;
-                        if (k > 0 && ok && elect()) commit<CG>(empty + vslot);
-                        __syncwarp();
                         if (more) {
-                            done();
-                            if (k == n - 1 && ok && elect()) commit<CG>(q_free);
-                            __syncwarp();
+                            next();
                             vslot = slot;
                             vphase = phase;
                             next();
