@@ -193,7 +193,7 @@ cudaError_t cc_kv(const RowsArgs& a, int kv_dtype, cudaStream_t s) {
 // prefix's and its own.  A result that is not finite is computed again by attend_row,
 // and so are the rows that the attention marked.
 // ---------------------------------------------------------------------------
-constexpr int kMergeRowThreads = 256, kOddRows = 16 * kMergeRowThreads;   // rows whose marks a CTA looks at
+constexpr int kMergeRowThreads = 256, kOddRows = 2 * kMergeRowThreads;    // rows whose marks a CTA looks at
 __host__ __device__ constexpr int merge_rows(int hd) { return kMergeRowThreads / (hd >> 4); }   // rows of a CTA
 
 struct RowParts {
@@ -275,18 +275,10 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
     }
     if (PROMPT && (int)blockIdx.x >= merges) {   // rows that the attention marked
         const long long first = (long long)(blockIdx.x - merges) * kOddRows, rows = (long long)a.T * a.Hq;
-        uint4 v = *reinterpret_cast<const uint4*>(t.odd + first + 16 * tid);
-        if (planes > 1) {   // the marks of both threads of a row
-            const uint4 w = *reinterpret_cast<const uint4*>(t.odd + t.odd_plane + first + 16 * tid);
-            v.x |= w.x;
-            v.y |= w.y;
-            v.z |= w.z;
-            v.w |= w.w;
-        }
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        if (v.x | v.y | v.z | v.w)
-            for (int i = 0; i < 16; ++i)
-                if ((w[i >> 2] >> (8 * (i & 3))) & 0xFFu && first + 16 * tid + i < rows) s_list[atomicAdd(&s_n, 1)] = (uint16_t)(16 * tid + i);
+        uint32_t v = *reinterpret_cast<const uint16_t*>(t.odd + first + 2 * tid);
+        if (planes > 1) v |= *reinterpret_cast<const uint16_t*>(t.odd + t.odd_plane + first + 2 * tid);   // (both threads of a row)
+        for (int i = 0; v && i < 2; ++i)
+            if ((v >> (8 * i)) & 0xFFu && first + 2 * tid + i < rows) s_list[atomicAdd(&s_n, 1)] = (uint16_t)(2 * tid + i);
         __syncthreads();
         for (int i = warp; i < s_n; i += kMergeRowThreads / 32) attend_again<KT>(&a, first + s_list[i]);
         return;

@@ -16,9 +16,12 @@
 // fills half of the tensor memory; each CTA brings half of every K and V tile,
 // which halves their traffic, and the scores have two buffers.
 //
-// Softmax: a thread is a row.  The reference m of a row (the running maximum)
-// moves only when a score exceeds it by more than 2^kSlack, so the accumulator is
-// rescaled a few times at most.
+// Softmax: a thread is a row, or half of one.  The reference m of a row moves only
+// when scores lie far above it, so the accumulator is rescaled a few times at most.
+// Up to head dimension 128 the softmax is the bound, and there it is the sums of the
+// probabilities that say so (a tile's largest score is looked for only then: 285 to
+// 270 us at 8192 tokens, e4m3 523 to 500); at 256 the products are, and the largest
+// score of each tile needs fewer registers (e4m3: 430 us against 448).
 //
 // A result that is not finite is computed again, position by position, by the
 // kernel behind this one (rows_attn.cu): the products here multiply masked
@@ -266,8 +269,11 @@ struct RowShape {
     static constexpr int CONV = SW, PROD = SW + (E4M3 ? 4 : 0), MMA = PROD + 1, QUERY = PROD + 2;
     static constexpr int THREADS = (QUERY + 1) * 32;
     static constexpr int O0 = 256, OC = HD;                        // accumulators' columns, behind two score buffers of 128
-    // a probability is 2^(z - m), at most 2^kSlack; in fp16 times 2^kBias
-    static constexpr float kSlack = E4M3 ? 4.f : 8.f, kBias = E4M3 ? 11.f : 0.f;
+    // A probability is 2^(z - m), at most 2^kSlack; in fp16 times 2^kBias.  kMost, where their
+    // sums are looked at: what a thread's probabilities of a tile (fp16: any 16 of them) may sum
+    // to; 128 of at most one (16 of 2^kBias) stay below.
+    static constexpr bool SUMS = HD < 256;
+    static constexpr float kBias = E4M3 ? 11.f : 0.f, kSlack = E4M3 ? 4.f : 8.f, kMost = E4M3 ? 60000.f : 256.f;
     // place of V tile k among a piece's n tile pairs
     static __device__ __forceinline__ unsigned v_at(int k, int n) { return CG == 1 ? 2 * k + 1 : k == n - 1 ? 2 * n - 1 : 2 * k + 2; }
 };
@@ -804,8 +810,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                 meet(s_full + 2 * q + buf, parity);
                 tc_fence_after();
                 if (none || (SHARED && __any_sync(0xffffffffu, mine && !touched))) {
-                    // a first reference from the tile's first 16 positions: seldom does a score lie
-                    // 2^kSlack above it
+                    // a first reference from the tile's first 16 positions: seldom does a score lie far
+                    // above it
                     uint32_t s[16];
                     tmem_ld16(sat, s);
                     tmem_ld_wait();
@@ -818,8 +824,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     if (!SHARED || !touched) m = fmaxf(m, x);
                 }
                 const bool idle = SHARED && p.k.kind == kOwn && !__any_sync(0xffffffffu, mine);   // none of this warp's rows: weights of zero
-                // ---- probabilities against the reference there is; where a score lies above it,
-                // once more against a new one (the scores stay in place until all is well) ----
+                // ---- probabilities against the reference there is; where a score lies too far above
+                // it, once more against the largest one (the scores stay in place until all is well) ----
                 constexpr int CH = HD < 256 ? 16 : 32;   // positions of a load (registers)
                 uint32_t o[CW / 2];
 #pragma unroll 1
@@ -832,6 +838,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                     fetch(0);
                     if (CW / CH == 2) fetch(1);
                     float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
+                    float most = 0.f;   // fp16: the largest sum of 16 probabilities
                     float mx = -__int_as_float(0x7F800000);   // the row's largest score (in bits; fp16: with the value scale)
 #pragma unroll
                     for (int c = 0; c < CW / CH; ++c) {
@@ -846,13 +853,17 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) z[i] = on >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
                             }
-                            float x = z[0], y = z[1];
+                            float x = 0.f;
+                            if (!S::SUMS) {
+                                x = z[0];
+                                float y = z[1];
 #pragma unroll
-                            for (int i = 2; i < 14; i += 4) {
-                                x = max3(x, z[i], z[i + 1]);
-                                y = max3(y, z[i + 2], z[i + 3]);
+                                for (int i = 2; i < 14; i += 4) {
+                                    x = max3(x, z[i], z[i + 1]);
+                                    y = max3(y, z[i + 2], z[i + 3]);
+                                }
+                                x = max3(x, y, fmaxf(z[14], z[15]));
                             }
-                            x = max3(x, y, fmaxf(z[14], z[15]));
                             float2 cm = make_float2(qc, qc), ca = make_float2(-m, -m), part = make_float2(0.f, 0.f);
                             float un = 1.f;
                             if (E4M3) {
@@ -860,9 +871,9 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                                 cm.x = cm.y = sc.x * qc;
                                 ca.x = ca.y = sc.y + S::kBias - m;
                                 un = ex2(-sc.y);   // the sum goes without the value scale
-                                x = fmaf(x, cm.x, sc.y);
+                                if (!S::SUMS) x = fmaf(x, cm.x, sc.y);
                             }
-                            mx = fmaxf(mx, x);
+                            if (!S::SUMS) mx = fmaxf(mx, x);
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
                                 float2 e = fma2(make_float2(z[i], z[i + 1]), cm, ca);
@@ -873,17 +884,39 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
                                 else sum = add2(sum, e);
                                 o[(at + i) >> 1] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
                             }
-                            if (E4M3) sum = fma2(part, make_float2(un, un), sum);
+                            if (E4M3) {
+                                sum = fma2(part, make_float2(un, un), sum);
+                                if (S::SUMS) most = fmaxf(most, part.x + part.y);
+                            }
                         }
                     }
-                    if (!E4M3) mx *= qc;
+                    const float all = (sum.x + sum.y) + (sum2.x + sum2.y);
                     // (with two threads a row the vote says also that both have read their scores)
-                    const bool over = any_of_rows(live && mx > m + S::kSlack);
+                    if (!S::SUMS && !E4M3) mx *= qc;
+                    const bool over = any_of_rows(live && (S::SUMS ? (E4M3 ? most : all) > S::kMost : mx > m + S::kSlack));
                     if (turn > 0 || !over) {
-                        l += (sum.x + sum.y) + (sum2.x + sum2.y);
+                        l += all;
                         break;
                     }
                     // move the references, and with them what has been summed
+                    if (S::SUMS)
+#pragma unroll
+                        for (int c = 0; c < CW / 16; ++c) {
+                            uint32_t v[16];
+                            tmem_ld16(sat + half * CW + 16 * c, v);
+                            tmem_ld_wait();
+                            const uint32_t on = bits[c >> 1] >> (16 * (c & 1));
+                            float x = -__int_as_float(0x7F800000);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) x = fmaxf(x, on >> i & 1u ? __uint_as_float(v[i]) : -__int_as_float(0x7F800000));
+                            if (E4M3) {
+                                const float2 sc = m_sc[mi * 8 + half * (CW / 16) + c];
+                                x = fmaf(x, sc.x * qc, sc.y);
+                            } else {
+                                x *= qc;
+                            }
+                            mx = fmaxf(mx, x);
+                        }
                     if (NH == 2) mx = fmaxf(mx, others(mx));
                     const float mn = fmaxf(mx, m), f = ex2(m - mn);
                     const bool scale = any_of_rows((!SHARED || touched) && f != 1.f);   // (where nothing is summed yet all is zero)
