@@ -153,7 +153,7 @@ bool rows_tc(const mtp_kv_cache* c) {
     return c->kv_dtype != MTP_DTYPE_F32 && (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256);
 }
 struct RowsSpace {
-    size_t status, note, head, worker, blocks, items, cum, cumt, lens, staged, q_scale, odd, part, part_ml, dense, dense_ml, end;
+    size_t status, note, row_parts, head, worker, blocks, items, cum, cumt, lens, staged, q_scale, odd, part, part_ml, dense, dense_ml, end;
     int workers;
 };
 // (every field grows with B, M and T, so that a workspace sized for more serves less)
@@ -185,6 +185,7 @@ RowsSpace rows_space(const mtp_kv_cache* c, int B, int M, int64_t T, int n_q_hea
         p.staged = take(rows * hd * 2);
         p.q_scale = take(rows * sizeof(float));
         if (M > 0) {
+            p.row_parts = take(2 * rows * sizeof(RowPart));
             p.dense_ml = take(2 * rows * sizeof(float2));
             p.dense = take(2 * rows * hd * sizeof(float));
         } else {
@@ -240,6 +241,7 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
     t.window_units = U * ((a.c.sink + (long long)kPosTile - 1) / kPosTile + (a.c.window + (kRowTile - 1) / a.G) / kPosTile + 2);
     t.cta_status = reinterpret_cast<int*>(base + p.status);
     t.note = reinterpret_cast<RowNote*>(base + p.note);
+    t.row_parts = reinterpret_cast<RowPart*>(base + p.row_parts);
     t.head = reinterpret_cast<PlanHead*>(base + p.head);
     t.worker = reinterpret_cast<WorkerRec*>(base + p.worker);
     t.blocks = reinterpret_cast<BlockRec*>(base + p.blocks);

@@ -196,38 +196,6 @@ cudaError_t cc_kv(const RowsArgs& a, int kv_dtype, cudaStream_t s) {
 constexpr int kMergeRowThreads = 256, kOddRows = 2 * kMergeRowThreads;    // rows whose marks a CTA looks at
 __host__ __device__ constexpr int merge_rows(int hd) { return kMergeRowThreads / (hd >> 4); }   // rows of a CTA
 
-struct RowParts {
-    long long dense;                  // the row's place in `dense` (< 0: in slots)
-    int w0, w1;                       // workers of its parts (w1 < w0: none)
-    int first;                        // worker in whose share the item begins
-    int r;                            // row of the slots
-};
-// parts of row r (of sequence seq) of a block's KV head; `dense`: where its rows begin there
-__device__ __forceinline__ RowParts parts_of(const RowsTcArgs& t, const Sequences& sq, const PlanHead& plan, const BlockRec& k, int g, int r,
-                                             int seq, long long dense) {
-    const int rt = r / kRowTile;
-    const Item it = item_of<true>(t.a, sq, k, rt);
-    const long long U = (long long)kPosTile * t.a.G;
-    const long long at = k.pre + g * units_before(t, k, plan.open, row_tiles_of(t.a, k)) + units_before(t, k, plan.open, rt) + plan.open * U;
-    int x0 = 0, x1 = it.n - 1;        // tiles that the row has a share in: a sequence's, or all
-    if (k.kind == kOwn) {
-        x0 = sq.cumt[seq] - it.lt;
-        x1 = sq.cumt[seq + 1] - it.lt - 1;
-    }
-    RowParts p;
-    p.first = worker_of(plan.T, plan.workers, at);
-    p.dense = -1;
-    p.r = r % kRowTile;
-    if (p.first == worker_of(plan.T, plan.workers, at + (it.n - 1) * U)) {
-        p.dense = k.q_row + (long long)g * k.q_stride + r + dense;
-        p.w0 = p.w1 = p.first;
-        return p;
-    }
-    p.w0 = worker_of(plan.T, plan.workers, at + x0 * U);
-    p.w1 = worker_of(plan.T, plan.workers, at + x1 * U);
-    return p;
-}
-
 // attend_row out of line: seldom called, and the merge keeps its registers
 template <typename KT>
 __device__ __noinline__ void attend_again(const RowsArgs* a, long long id) {
@@ -243,7 +211,7 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
                                                                                      int planes) {
     __shared__ long long s_odd[merge_rows(64)];             // rows of out whose result is not finite (< 0: none)
     __shared__ uint16_t s_list[PROMPT ? kOddRows : 1];
-    __shared__ int s_n, s_cum[PROMPT ? 1 : MTP_MAX_PAGED_BATCH + 1], s_cumt[PROMPT ? 1 : MTP_MAX_PAGED_BATCH + 1];
+    __shared__ int s_n;
     const RowsArgs& a = t.a;
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) s_n = 0;
@@ -251,13 +219,6 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!PROMPT) {   // (searched below)
-        for (int i = tid; i <= a.B; i += kMergeRowThreads) {
-            s_cum[i] = t.cum[i];
-            s_cumt[i] = t.cumt[i];
-        }
-        __syncthreads();
-    }
     if ((int)blockIdx.x == (int)gridDim.x - 1) {   // the call's status from the CTAs'
         int bad = 0;
         for (int c = tid; c < statuses; c += kMergeRowThreads) {
@@ -284,11 +245,8 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
         return;
     }
     const int hd = a.hd, gt = hd >> 4, per = kMergeRowThreads / gt, sub = tid / gt, d = 4 * (tid - sub * gt), quarter = hd >> 2;
-    RowParts parts[2];
+    RowPart parts[2];
     long long row = -1;                                     // row of out (in heads)
-    parts[0].w0 = parts[1].w0 = 0;
-    parts[0].w1 = parts[1].w1 = -1;
-    parts[0].dense = parts[1].dense = -1;
     if (PROMPT) {
         const int chunks = kRowTile / per > 0 ? kRowTile / per : 1, w = blockIdx.x / chunks, r = (blockIdx.x - w * chunks) * per + sub;
         const RowNote n = t.note[w];
@@ -297,31 +255,14 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
             const int at = n.r0 + r, j = at / a.G;
             row = ((long long)n.row0 + j) * a.Hq + n.g * a.G + at - j * a.G;
             if (row >= (long long)a.T * a.Hq) row = -1;
-            parts[0].w0 = parts[0].first = w;
-            parts[0].w1 = n.last;
-            parts[0].r = r;
+            parts[0] = {RowPart::kSlots, (uint16_t)w, (uint16_t)n.last, (uint16_t)w, (uint16_t)r, 1};
         }
     } else {
         const long long id = (long long)blockIdx.x * per + sub;
-        const int tok = (int)(id / a.Hq), b = tok / a.M, j = tok - b * a.M, h = (int)(id - (long long)tok * a.Hq);
-        if (b < a.B) {
-            const PlanHead plan = *t.head;
-            const Sequences sq = {s_cum, s_cumt, nullptr};
-            const int c0 = sq.cum[b], g = h / a.G, rj = j * a.G + h - g * a.G;
-            if (j < sq.cum[b + 1] - c0) {
-                const long long own_at = (long long)a.B * a.M * a.Hq;
-                const int i = a.n_groups > 0 ? last_at_most(a.group_start, a.n_groups, b) : 0;
-                const BlockRec seq = t.blocks[2 * a.n_groups + b];
-                if (seq.n > 0) {
-                    parts[0] = parts_of(t, sq, plan, seq, g, rj, b, own_at);
-                } else {   // of group i
-                    const BlockRec own = t.blocks[a.n_groups + i], pre = t.blocks[i];
-                    const int r = (c0 - sq.cum[own.table]) * a.G + rj;
-                    parts[0] = parts_of(t, sq, plan, own, g, r, b, own_at);
-                    if (pre.n > 0) parts[1] = parts_of(t, sq, plan, pre, g, r, b, 0);
-                }
-                row = id;
-            }
+        if (id < (long long)a.B * a.M * a.Hq) {
+            parts[0] = t.row_parts[2 * id];
+            parts[1] = t.row_parts[2 * id + 1];
+            if (parts[0].there) row = id;
         }
     }
     if (row >= 0) {
@@ -332,7 +273,9 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
         constexpr int N = PROMPT ? 2 : 4;   // parts in flight
 #pragma unroll
         for (int which = 0; which < (PROMPT ? 1 : 2); ++which) {
-            const RowParts p = parts[which];
+            const RowPart p = parts[which];
+            if (!p.there) continue;
+            const bool dense = p.dense != RowPart::kSlots;
 #pragma unroll 1
             for (int w = p.w0; w <= p.w1; w += N) {
                 float2 ml[N];
@@ -344,8 +287,8 @@ __global__ void __launch_bounds__(kMergeRowThreads, PROMPT ? 3 : 2) rows_merge_k
                     for (int i = 0; i < 4; ++i) o[e][i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (w + e > p.w1) continue;
                     const long long at = (2ll * (w + e) + (w + e == p.first ? 1 : 0)) * kRowTile + p.r;
-                    const float* src = (p.dense >= 0 ? t.dense + p.dense * hd : t.part + at * hd) + d;
-                    ml[e] = p.dense >= 0 ? t.dense_ml[p.dense] : t.part_ml[at];
+                    const float* src = (dense ? t.dense + (long long)p.dense * hd : t.part + at * hd) + d;
+                    ml[e] = dense ? t.dense_ml[p.dense] : t.part_ml[at];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[e][i] = *reinterpret_cast<const float4*>(src + i * quarter);
                 }

@@ -257,7 +257,7 @@ __device__ __forceinline__ void open_codes(const unsigned char* src, unsigned ch
     }
 }
 
-template <bool E4M3, int HD>
+template <bool E4M3, int HD, bool SHARED>
 struct RowShape {
     static constexpr int CG = rows_pair(HD), NQ = 2 / CG;          // CTAs of a worker, row tiles of a CTA
     static constexpr int KP = kPosTile / CG, VD = HD / CG;         // positions of K, dimensions of V in this CTA
@@ -266,8 +266,8 @@ struct RowShape {
     static constexpr int NH = rows_halves(E4M3, HD);               // threads of a row: each takes its share of a tile's positions
     static constexpr int CW = kPosTile / NH;                       // positions of a thread
     static constexpr int SW = 4 * NQ * NH;                         // softmax warps
-    static constexpr int CONV = SW, PROD = SW + (E4M3 ? 4 : 0), MMA = PROD + 1, QUERY = PROD + 2;
-    static constexpr int THREADS = (QUERY + 1) * 32;
+    static constexpr int CONV = SW, PROD = SW + (E4M3 ? 4 : 0), MMA = PROD + 1, QUERY = PROD + 2, PARTS = PROD + 3;
+    static constexpr int THREADS = (SHARED ? PARTS + 1 : QUERY + 1) * 32;
     static constexpr int O0 = 256, OC = HD;                        // accumulators' columns, behind two score buffers of 128
     // A probability is 2^(z - m), at most 2^kSlack; in fp16 times 2^kBias.  kMost, where their
     // sums are looked at: what a thread's probabilities of a tile (fp16: any 16 of them) may sum
@@ -278,14 +278,41 @@ struct RowShape {
     static __device__ __forceinline__ unsigned v_at(int k, int n) { return CG == 1 ? 2 * k + 1 : k == n - 1 ? 2 * n - 1 : 2 * k + 2; }
 };
 
+// The part that row r (of sequence seq) of a block's KV head leaves; `dense`: where the
+// block's rows begin there
+__device__ __forceinline__ RowPart part_of(const RowsTcArgs& t, const Sequences& sq, const PlanHead& plan, const BlockRec& k, int g, int r,
+                                           int seq, long long dense) {
+    const int rt = r / kRowTile;
+    const Item it = item_of<true>(t.a, sq, k, rt);
+    const long long U = (long long)kPosTile * t.a.G;
+    const long long at = k.pre + g * units_before(t, k, plan.open, row_tiles_of(t.a, k)) + units_before(t, k, plan.open, rt) + plan.open * U;
+    int x0 = 0, x1 = it.n - 1;        // tiles that the row has a share in: a sequence's, or all
+    if (k.kind == kOwn) {
+        x0 = sq.cumt[seq] - it.lt;
+        x1 = sq.cumt[seq + 1] - it.lt - 1;
+    }
+    RowPart p;
+    p.there = 1;
+    p.dense = RowPart::kSlots;
+    p.r = (uint16_t)(r % kRowTile);
+    p.first = p.w0 = p.w1 = (uint16_t)worker_of(plan.T, plan.workers, at);
+    if (p.first == worker_of(plan.T, plan.workers, at + (it.n - 1) * U)) {
+        p.dense = (uint32_t)(k.q_row + (long long)g * k.q_stride + r + dense);
+    } else {
+        p.w0 = (uint16_t)worker_of(plan.T, plan.workers, at + x0 * U);
+        p.w1 = (uint16_t)worker_of(plan.T, plan.workers, at + x1 * U);
+    }
+    return p;
+}
+
 // Score buffer of a tile that concerns one row tile: two such in a row take turns, so
 // that one's scores are computed while the other's weights are (both row tiles: a buffer
 // each).  rows, was: row tiles of this tile and of the one before, side: the buffer then.
 __device__ __forceinline__ int score_side(int rows, int was, int side) { return rows == 3 || was == 3 ? 0 : side ^ 1; }
 
 template <bool E4M3, int HD, bool SHARED>
-__global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcParams pp) {
-    using S = RowShape<E4M3, HD>;
+__global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcParams pp) {
+    using S = RowShape<E4M3, HD, SHARED>;
     constexpr int CG = S::CG, NQ = S::NQ, NR = rows_raw(E4M3, HD), NS = rows_slots(E4M3, HD);
     static_assert(NS >= 2 && NS <= kRowsSlots && NR <= kRowsRaw, "ring");
     const RowsTcArgs& t = pp.t;
@@ -521,6 +548,33 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
             if (CG == 2 && rank == 1 && ok && lane == 0) arrive_lead<CG>(q_peer);
             __syncwarp();
             ++seg;
+        }
+    } else if (SHARED && warp == S::PARTS) {
+        // ------------------------------------------------------------------
+        // where the parts of the rows will lie, for the merge (which would take 8 us for
+        // it with nothing beside it): lane = row of out
+        // ------------------------------------------------------------------
+        const PlanHead plan = *t.head;
+        const Sequences s = a.n_groups > 0 ? sq : Sequences{t.cum, t.cumt, t.lens};
+        const long long rows = (long long)a.B * a.M * a.Hq;
+        for (long long id = (long long)blockIdx.x * 32 + lane; id < rows; id += (long long)gridDim.x * 32) {
+            const int tok = (int)(id / a.Hq), h = (int)(id - (long long)tok * a.Hq), b = tok / a.M, j = tok - b * a.M, c0 = s.cum[b];
+            RowPart own = {}, pre = {};
+            if (j < s.cum[b + 1] - c0) {
+                const int g = h / a.G, rj = j * a.G + h - g * a.G;
+                const BlockRec k = t.blocks[2 * a.n_groups + b];
+                if (k.n > 0) {
+                    own = part_of(t, s, plan, k, g, rj, b, rows);
+                } else {   // of a group
+                    const int i = last_at_most(a.group_start, a.n_groups, b);
+                    const BlockRec o = t.blocks[a.n_groups + i], p = t.blocks[i];
+                    const int r = (c0 - s.cum[o.table]) * a.G + rj;
+                    own = part_of(t, s, plan, o, g, r, b, rows);
+                    if (p.n > 0) pre = part_of(t, s, plan, p, g, r, b, 0);
+                }
+            }
+            t.row_parts[2 * id] = own;
+            t.row_parts[2 * id + 1] = pre;
         }
     } else if (E4M3 && warp >= S::CONV && warp < S::CONV + 4) {
         // ------------------------------------------------------------------
@@ -1043,7 +1097,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD>::THREADS, 1) rows_tc_kernel
 
 template <bool E4M3, int HD, bool SHARED>
 cudaError_t go(const RowsTcParams& p, cudaStream_t s) {
-    using S = RowShape<E4M3, HD>;
+    using S = RowShape<E4M3, HD, SHARED>;
     static int ready[64] = {0};   // the attribute is set, per device
     constexpr int base = rows_slots(E4M3, HD) * S::SLOTB + S::NQ * S::QB + rows_raw(E4M3, HD) * S::RAWB + kRowsOther;
     static_assert(base + rows_tables(MTP_MAX_PAGED_BATCH) <= kRowsSmemLimit, "shared memory");

@@ -62,6 +62,16 @@ struct __align__(16) RowNote {
     int row0, b;                      // the sequence's first token in out, the sequence
     int pad_[2];
 };
+// a part of a row's result with shared prefixes: in `dense`, or in slots of workers
+struct __align__(16) RowPart {
+    static constexpr uint32_t kSlots = ~0u;
+    uint32_t dense;                   // the row's place in `dense`
+    uint16_t w0, w1;                  // first and last worker that has a tile of it
+    uint16_t first;                   // worker in whose share its item begins
+    uint16_t r;                       // row of the slots
+    int there;                        // 0: no such part
+};
+static_assert(sizeof(RowPart) == 16, "one load");
 struct PlanHead {
     long long T;                      // units in all
     int open, workers;                // units before an item's tiles / U; workers with a share
@@ -83,6 +93,7 @@ struct RowsTcArgs {
     float* q_scale;                   // e4m3: [rows] a staged row's power of two times the softmax scale
     int* cta_status;                  // [CTAs], and behind them the plan's
     RowNote* note;                    // prompts, [workers]
+    RowPart* row_parts;               // shared prefixes, [B * M * Hq][2]: a row's own part and its prefix's
     float* part;                      // [2 workers][kRowTile][hd]
     float2* part_ml;                  // their maxima and sums
     uint8_t* odd;                     // prompts, [2][odd_plane]: the row's result is not finite, by each thread that has a share of it
