@@ -278,7 +278,7 @@ class ClockSampler:
                 "reasons": sorted(reasons), "samples": len(sm)}
 
 
-TARGET_STEP_SOURCES = ("kv_append", "logprobs", "paged")   # operators that no workload launches
+TARGET_STEP_SOURCES = ("kv_append", "logprobs", "paged", "rotate", "rows")   # operators that no workload launches
 
 
 def kernel_source_hash() -> str:

@@ -583,7 +583,8 @@ int mtp_prompt_attention(const mtp_kv_cache *c, int B, int64_t T, int n_q_heads,
  * A sequence whose kv_len, n_new, prefix_len or group is out of range is left out,
  * positions on absent pages are masked, and both set the status word to
  * MTP_ERR_ARG.  1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= M <= MTP_MAX_ATTN_ROWS,
- * 0 <= n_groups <= B, at most 16 query heads per KV head. */
+ * 0 <= n_groups <= B, at most 16 query heads per KV head, B * (max_pages *
+ * page_size / 128 + 2) < 2^31. */
 int mtp_prefix_attention(const mtp_kv_cache *c, int B, int M, int n_q_heads, const int32_t *kv_len, const int32_t *n_new,
                          int n_groups, const int32_t *group_start, const int32_t *prefix_len,
                          const void *q, int dtype, int64_t q_stride_b, int64_t q_stride_m, int64_t q_stride_h,

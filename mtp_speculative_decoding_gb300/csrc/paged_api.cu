@@ -104,10 +104,12 @@ bool encode_pages(CUtensorMap* m, const void* base, const mtp_kv_cache* c, int r
                                    c->n_pages > 1 ? (cuuint64_t)c->stride_p * esz : row};
     const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / esz), (cuuint32_t)(c->page_size < rows ? c->page_size : rows), 1, 1};
     const cuuint32_t one[4] = {1, 1, 1, 1};
-    return enc(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
-               strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encoded([&] {
+        return enc(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                   strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 // (dimension, row) map of staged rows of 16-bit values: boxes of a 128-byte column by 128 rows
@@ -116,8 +118,10 @@ bool encode_rows(CUtensorMap* m, void* base, int hd, int64_t rows) {
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)hd * 2};
     const cuuint32_t box[2] = {64, 128}, one[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encoded([&] {
+        return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 struct AttnPlan {
@@ -151,6 +155,11 @@ bool heads_ok(const mtp_kv_cache* c, int n_q_heads, int* rc) {
 // (on the tensor cores if the queries are bf16)
 bool rows_tc(const mtp_kv_cache* c) {
     return c->kv_dtype != MTP_DTYPE_F32 && (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256);
+}
+// (the tiles of shared prefixes' sequences are counted in 31 bits)
+bool prefix_fits(const mtp_kv_cache* c, int B, int M, int n_q_heads) {
+    const int64_t tiles = B * ((int64_t)c->max_pages * c->page_size / kPosTile + 2);
+    return (int64_t)B * M * n_q_heads < 1ll << 31 && tiles < 1ll << 31;
 }
 struct RowsSpace {
     size_t status, note, row_parts, head, worker, blocks, items, cum, cumt, lens, staged, q_scale, odd, part, part_ml, dense, dense_ml, end;
@@ -376,7 +385,7 @@ size_t mtp_prompt_workspace_size(const mtp_kv_cache* c, int B, int64_t T, int n_
 size_t mtp_prefix_workspace_size(const mtp_kv_cache* c, int B, int M, int n_q_heads) {
     int rc;
     if (check_cache(c, false) != MTP_OK || B < 1 || B > MTP_MAX_PAGED_BATCH || M < 1 || M > MTP_MAX_ATTN_ROWS) return 0;
-    if (!heads_ok(c, n_q_heads, &rc) || (int64_t)B * M * n_q_heads >= 1ll << 31) return 0;
+    if (!heads_ok(c, n_q_heads, &rc) || !prefix_fits(c, B, M, n_q_heads)) return 0;
     return rows_workspace(c, B, M, (int64_t)B * M, n_q_heads);
 }
 
@@ -404,7 +413,7 @@ int mtp_prefix_attention(const mtp_kv_cache* c, int B, int M, int n_q_heads, con
     if (rc != MTP_OK) return rc;
     if (M < 1 || M > MTP_MAX_ATTN_ROWS || misaligned(n_new, 4) || n_groups < 0 || n_groups > B) return MTP_ERR_ARG;
     if (n_groups > 0 && (!group_start || !prefix_len || misaligned(group_start, 4) || misaligned(prefix_len, 4))) return MTP_ERR_ARG;
-    if (c->window > 0 || (int64_t)B * M * n_q_heads >= 1ll << 31) return MTP_ERR_UNSUPPORTED;
+    if (c->window > 0 || !prefix_fits(c, B, M, n_q_heads)) return MTP_ERR_UNSUPPORTED;
     if (!ws || misaligned(ws, 256) || ws_bytes < rows_workspace(c, B, M, (int64_t)B * M, n_q_heads)) return MTP_ERR_WORKSPACE;
     const int sms = num_sms();
     if (sms <= 0) return MTP_ERR_CUDA;

@@ -117,3 +117,12 @@ def test_binding_refuses_wrong_shapes():
                  (q, k, i(3, 5), (24, 20, 20), 1e4, q[:4], k), (q, k.half(), i(3, 5), (24, 20, 20), 1e4, q, k.half())):
         with pytest.raises(ValueError):
             mtp.rotate_axes(*args)
+
+
+def test_more_cached_positions_than_the_plan_counts_are_refused():
+    c = cache(max_pages=0x7FFFFF00 // 16, page_size=16)
+    for size, call, most in ((mtp.prefix_workspace_size, prefix, 127),):
+        assert size(c, most, 3, 8) > 0
+        with pytest.raises(mtp.MTPError):
+            size(c, most + 1, 3, 8)
+        assert call(c, B=most + 1) == UNS
