@@ -361,7 +361,7 @@ cudaError_t launch_rows_merge(const RowsTcArgs& t, int kv_dtype, cudaStream_t s)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const int planes = rows_halves(kv_dtype == MTP_DTYPE_E4M3, a.hd);
+    const int planes = rows_halves(a.hd);
     const int statuses = t.workers * rows_pair(a.hd) + 1;   // the CTAs' and the plan's
     return kv_dtype == MTP_DTYPE_E4M3 ? merge<uint8_t>(cfg, t, statuses, (int)merges, planes) : merge<uint16_t>(cfg, t, statuses, (int)merges, planes);
 }

@@ -263,7 +263,7 @@ struct RowShape {
     static constexpr int KP = kPosTile / CG, VD = HD / CG;         // positions of K, dimensions of V in this CTA
     static constexpr int QB = 128 * HD * 2;                        // bytes of a row tile
     static constexpr int SLOTB = rows_slot_bytes(HD), RAWB = SLOTB / 2;
-    static constexpr int NH = rows_halves(E4M3, HD);               // threads of a row: each takes its share of a tile's positions
+    static constexpr int NH = rows_halves(HD);               // threads of a row: each takes its share of a tile's positions
     static constexpr int CW = kPosTile / NH;                       // positions of a thread
     static constexpr int SW = 4 * NQ * NH;                         // softmax warps
     static constexpr int CONV = SW, PROD = SW + (E4M3 ? 4 : 0), MMA = PROD + 1, QUERY = PROD + 2, PARTS = PROD + 3;
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
     unsigned long long *full = bars, *empty = full + kRowsSlots, *peer = empty + kRowsSlots, *rfull = peer + kRowsSlots,
                        *rempty = rfull + kRowsRaw, *meta = rempty + kRowsRaw, *s_full = meta + kRowsMeta, *p_full = s_full + 4,
                        *pv_done = p_full + 2, *o_free = pv_done + 4, *q_full = o_free + 2, *q_peer = q_full + 1, *q_free = q_peer + 1,
-                       *end_bar = q_free + 1;
-    int* s_tab = reinterpret_cast<int*>(bars + 3 * kRowsSlots + 2 * kRowsRaw + kRowsMeta + 16);   // shared prefixes: the sequences' tables
+                       *end_bar = q_free + 1, *mfree = end_bar + 1;
+    int* s_tab = reinterpret_cast<int*>(bars + 3 * kRowsSlots + 2 * kRowsRaw + 2 * kRowsMeta + 16);   // shared prefixes: the sequences' tables
     const Sequences sq = {s_tab, s_tab + a.B + 1, s_tab + 2 * a.B + 2};
     __shared__ unsigned int s_tmem;
     __shared__ int s_bad;
@@ -348,7 +348,10 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
             mbar_init(rfull + i, 1);
             mbar_init(rempty + i, 4);
         }
-        for (int i = 0; i < kRowsMeta; ++i) mbar_init(meta + i, 1);
+        for (int i = 0; i < kRowsMeta; ++i) {
+            mbar_init(meta + i, 1);
+            mbar_init(mfree + i, S::SW);
+        }
         for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);     // [row tile][score buffer]
             mbar_init(pv_done + i, 1);    // [row tile][its tiles in turns: a wait may be two of them behind]
@@ -491,6 +494,12 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
                     const float k8 = __shfl_sync(0xffffffffu, ks, src), e8 = __shfl_sync(0xffffffffu, ev, src);
                     const unsigned have = __ballot_sync(0xffffffffu, lane < 8 && th) & 0xFFu;
                     const unsigned mi = ti % kRowsMeta;
+                    // (a pair's warps all answer every tile, so none of them is that far behind; here a
+                    // row tile's warps pass over the other's tiles)
+                    if (CG == 1) {
+                        ok = wait_all(mfree + mi, ((ti / kRowsMeta) & 1) ^ 1);
+                        if (!ok) break;
+                    }
                     side = score_side(tile.rows, was, side);
                     was = tile.rows;
                     if (lane < 8 && E4M3) m_sc[mi * 8 + lane] = make_float2(k8, e8);
@@ -836,7 +845,11 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
                 int zq = 0;                                  // the row tile that looks after the tile's values
                 int buf = CG == 2 ? (int)(tc & 1) : q;
                 if (CG == 1) {
-                    if (!(flag.x >> q & 1)) continue;        // the other row tile's alone
+                    if (!(flag.x >> q & 1)) {                // the other row tile's alone
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(mfree + mi);
+                        continue;
+                    }
                     if (SHARED && (flag.x & 3) != 3) buf = flag.x >> 3 & 1;
                     zq = flag.x & 1 ? 0 : 1;
                 }
@@ -1031,6 +1044,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
                 if (lane == 0) {
                     if (zeroed) arrive_lead<CG>(p_full + buf);
                     else arrive_lead_relaxed<CG>(p_full + buf);
+                    if (CG == 1) mbar_arrive(mfree + mi);
                 }
                 ++tc;
             }

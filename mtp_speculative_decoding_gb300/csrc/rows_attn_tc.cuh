@@ -12,7 +12,9 @@ namespace mtp {
 constexpr int kRowTile = 256;         // rows of an item
 constexpr int kPosTile = 128;         // positions of a tile
 // What beginning an item costs, in tiles (an epilogue, and a pipeline that fills
-// anew).
+// anew).  Measured with 0, 1, 2, 3, 4, 6: 13 packed prompts of up to 2048 tokens take 186,
+// 175, 175, 181, 181, 190 us, one of 8192 at head dimension 256 396, 373, 366, 369, 373,
+// 379.
 constexpr int kRowsOpen = 2;
 
 // A block is rows and positions: a sequence's rows against its positions (prompts,
@@ -282,12 +284,14 @@ struct Walk {
 __host__ __device__ constexpr int rows_pair(int hd) { return hd == 256 ? 2 : 1; }        // CTAs of a worker
 __host__ __device__ constexpr int rows_q_bytes(int hd) { return kRowTile / rows_pair(hd) * hd * 2; }
 __host__ __device__ constexpr int rows_slot_bytes(int hd) { return kPosTile * hd * 2 / rows_pair(hd); }
-constexpr int kRowsMeta = 16;         // tiles whose masks and scales the producer may be ahead
+constexpr int kRowsMeta = 16;         // tiles whose masks and scales may be there at a time
 constexpr int kRowsSlots = 8, kRowsRaw = 4;   // ring slots at most
 constexpr int kRowsSmemLimit = 227 * 1024 - 64;
-// threads that share a row of a tile in the softmax
-__host__ __device__ constexpr int rows_halves(bool e4m3, int hd) { return hd == 256 ? 2 : 1; }
-constexpr int kRowsOther = 1024 + 2 * kRowTile * 4 + kRowsMeta * (16 + 64 + 16) + (3 * kRowsSlots + 2 * kRowsRaw + kRowsMeta + 16) * 8;
+// threads that share a row of a tile in the softmax: a pair of CTAs has one row tile each and
+// registers for two (one CTA with two row tiles was slower so: 351 against 276 us for 8192
+// tokens at head dimension 128)
+__host__ __device__ constexpr int rows_halves(int hd) { return rows_pair(hd); }
+constexpr int kRowsOther = 1024 + 2 * kRowTile * 4 + kRowsMeta * (16 + 64 + 16) + (3 * kRowsSlots + 2 * kRowsRaw + 2 * kRowsMeta + 16) * 8;
 // the sequences' tables, behind the rest
 __host__ __device__ constexpr int rows_tables(int B) { return (3 * B + 2) * 4; }
 // 8-bit caches: codes as they come in take half a slot each
