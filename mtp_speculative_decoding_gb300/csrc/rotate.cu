@@ -4,7 +4,10 @@
 // its axis times theta^(-i / pairs).  A thread takes one unit (8 pairs, or 16
 // elements behind the rotated ones) of `hpt` heads of one row, so that the
 // angles of a row are computed once for those heads.  Long calls are bound by
-// the bytes in and out, short ones by the launch and two dependent loads.
+// the bytes in and out (8192 rows of 24 heads of 128, bf16: 18.6 us, 5.4 TB/s),
+// in fp32 with a norm also by their instructions at 16 warps an SM (4093 rows of
+// 20 heads of 256: 37.1 us, 4.5 TB/s), short ones by the launch and two dependent
+// loads (4 rows: 9.3 us captured).
 #include "rows.cuh"
 
 namespace mtp {
@@ -14,7 +17,7 @@ namespace {
 // (plain loads: the rows may be rewritten in place)
 __device__ __forceinline__ uint4 ld16(const void* p) {
     uint4 r;
-    asm("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
 __device__ __forceinline__ void in8(const float* p, float (&x)[8]) {
@@ -63,6 +66,19 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
             g0[i] = __ldg(gain + e0 + i);
             g1[i] = __ldg(gain + e1 + i);
         }
+    // heads in flight, the first ones while the angles are computed (fp32: 40.0 us with two
+    // that come in behind them, 37.1 so)
+    constexpr int N = 4;
+    float p[N][8], q[N][8];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int h = h0 + i0 + i < h1 ? h0 + i0 + i : h1 - 1;   // (every lane of the warp takes part in the norm)
+            in8(src + h * a.in_sh[which] + e0, p[i]);
+            in8(src + h * a.in_sh[which] + e1, q[i]);
+        }
+    };
+    fetch(0);
     float cs[8], sn[8];
     if (turn) {
         int at[MTP_MAX_AXES];
@@ -78,16 +94,8 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
             pair_angle<FAST>(pl, ph, s_hi[8 * c + i], s_lo[8 * c + i], cs[i], sn[i]);
         }
     }
-    constexpr int N = sizeof(T) == 2 ? 4 : 2;   // heads in flight
 #pragma unroll 1
     for (int i0 = 0; i0 < a.hpt; i0 += N) {
-        float p[N][8], q[N][8];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int h = h0 + i0 + i < h1 ? h0 + i0 + i : h1 - 1;   // (every lane of the warp takes part in the norm)
-            in8(src + h * a.in_sh[which] + e0, p[i]);
-            in8(src + h * a.in_sh[which] + e1, q[i]);
-        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int h = h0 + i0 + i;
@@ -106,6 +114,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
                 store8(dst + h * a.out_sh[which] + e1, q[i]);
             }
         }
+        if (i0 + N < a.hpt) fetch(i0 + N);
     }
 }
 
@@ -113,11 +122,13 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
 
 cudaError_t launch_rotate_axes(RotateArgs a, int dtype, int sms, cudaStream_t s) {
     // as many heads in one thread as leave 512 threads an SM: an angle costs as much as
-    // the rest of four elements
-    // (and no more than divide both, where that leaves four: a group's missing heads cost as
-    // much as others)
+    // the rest of four elements (128 to 1024 threads measure alike; with 2048 8192 rows of
+    // bf16 take 20.7 us instead of 18.6), and no more than divide both counts, where that
+    // leaves four: a group's missing heads cost as much as others
     a.hpt = 1;
-    while (a.hpt < 16 && (a.hpt < 4 || (a.heads[0] | a.heads[1]) % (2 * a.hpt) == 0) && (long long)a.rows * ((a.heads[0] + a.heads[1]) / (2 * a.hpt)) * (a.hd >> 4) >= (long long)sms * 512) a.hpt *= 2;
+    while (a.hpt < 16 && (a.hpt < 4 || (a.heads[0] | a.heads[1]) % (2 * a.hpt) == 0) &&
+           (long long)a.rows * ((a.heads[0] + a.heads[1]) / (2 * a.hpt)) * (a.hd >> 4) >= (long long)sms * 512)
+        a.hpt *= 2;
     for (int w = 0; w < 2; ++w) a.groups[w] = (a.heads[w] + a.hpt - 1) / a.hpt;
     const long long threads = (long long)a.rows * (a.groups[0] + a.groups[1]) * (a.hd >> 4);
     const unsigned grid = (unsigned)((threads + kRotThreads - 1) / kRotThreads);
