@@ -18,10 +18,12 @@
 //
 // Softmax: a thread is a row, or half of one.  The reference m of a row moves only
 // when scores lie far above it, so the accumulator is rescaled a few times at most.
-// Up to head dimension 128 the softmax is the bound, and there it is the sums of the
-// probabilities that say so (a tile's largest score is looked for only then: 285 to
-// 270 us at 8192 tokens, e4m3 523 to 500); at 256 the products are, and the largest
-// score of each tile needs fewer registers (e4m3: 430 us against 448).
+// What says so depends on what the registers of a thread hold.  Head dimension 256, half a
+// row a thread: the largest score of the tile, found beside the probabilities.  Up to 128,
+// where the softmax is the bound: over bf16 caches the sum of the probabilities (a tile's
+// largest score is looked for only then: 285 to 270 us at 8192 tokens of 128 dimensions;
+// at 256 dimensions e4m3 430 to 448); over e4m3 ones, with fewer registers, a look over
+// the scores first, so that no probability waits for the last one (515 to 496 us).
 //
 // Roundings.  bf16 caches: a rotated query and a probability once to bf16 (2^-8 each);
 // two parts of either, as the attention of a verify step has them, would double one
@@ -170,6 +172,13 @@ __device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
         : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+        : "memory");
+}
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_4d(void* dst, const void* tmap, int x, int y, int z, int w, unsigned long long* bar) {
     asm volatile(
@@ -210,6 +219,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float most_of(const float* z) {   // of 16
+    float x = z[0], y = z[1];
+#pragma unroll
+    for (int i = 2; i < 14; i += 4) {
+        x = max3(x, z[i], z[i + 1]);
+        y = max3(y, z[i + 2], z[i + 3]);
+    }
+    return max3(x, y, fmaxf(z[14], z[15]));
+}
 // two lanes of fp32 in one instruction
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     float2 r;
@@ -284,10 +302,10 @@ struct RowShape {
     static constexpr int O0 = 256, OC = HD;                        // accumulators' columns, behind two score buffers of 128
     // A probability is 2^(z - m), at most 2^kSlack; in fp16 times 2^kBias: with 2^15 at most it
     // stays finite, and down to 2^-25 of the reference it keeps all bits of a normal fp16.
-    // kMost, where their sums are looked at: what a thread's probabilities of a tile (fp16: any
-    // 16 of them) may sum to; 128 of at most one (16 of 2^kBias) stay below.
-    static constexpr bool SUMS = HD < 256;
-    static constexpr float kBias = E4M3 ? 11.f : 0.f, kSlack = E4M3 ? 4.f : 8.f, kMost = E4M3 ? 60000.f : 256.f;
+    // TWO: the scores are looked over first.  SUMS: the probabilities' sum is looked at; kMost is
+    // what those of a tile may sum to (128 of at most one stay below).
+    static constexpr bool TWO = HD < 256 && E4M3, SUMS = HD < 256 && !TWO;
+    static constexpr float kBias = E4M3 ? 11.f : 0.f, kSlack = E4M3 ? 4.f : 8.f, kMost = 256.f;
     // place of V tile k among a piece's n tile pairs
     static __device__ __forceinline__ unsigned v_at(int k, int n) { return CG == 1 ? 2 * k + 1 : k == n - 1 ? 2 * n - 1 : 2 * k + 2; }
 };
@@ -890,7 +908,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
                     for (int i = 0; i < CW / 32; ++i) bits[i] = on_bits(half * (CW / 32) + i);
                 meet(s_full + 2 * q + buf, parity);
                 tc_fence_after();
-                if (none || (SHARED && __any_sync(0xffffffffu, mine && !touched))) {
+                if (!S::TWO && (none || (SHARED && __any_sync(0xffffffffu, mine && !touched)))) {
                     // a first reference from the tile's first 16 positions: seldom does a score lie far
                     // above it
                     uint32_t s[16];
@@ -906,98 +924,11 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
                 }
                 const bool idle = SHARED && p.k.kind == kOwn && !__any_sync(0xffffffffu, mine);   // none of this warp's rows: weights of zero
                 // ---- probabilities against the reference there is; where a score lies too far above
-                // it, once more against the largest one (the scores stay in place until all is well) ----
+                // it, once more against the largest one (the scores stay in place until all is well;
+                // TWO: the reference is right at once, and probabilities go over the scores piece by piece) ----
                 constexpr int CH = HD < 256 ? 16 : 32;   // positions of a load (registers)
-                uint32_t o[CW / 2];
-#pragma unroll 1
-                for (int turn = 0; !idle; ++turn) {
-                    uint32_t s[2][CH];
-                    auto fetch = [&](int c) {
-                        if constexpr (CH == 16) tmem_ld16(sat + half * CW + CH * c, s[c & 1]);
-                        else ld32(sat + half * CW + CH * c, s[c & 1]);
-                    };
-                    fetch(0);
-                    if (CW / CH == 2) fetch(1);
-                    float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
-                    float most = 0.f;   // fp16: the largest sum of 16 probabilities
-                    float mx = -__int_as_float(0x7F800000);   // the row's largest score (in bits; fp16: with the value scale)
-#pragma unroll
-                    for (int c = 0; c < CW / CH; ++c) {
-                        if (c == 0 || CW / CH > 2) tmem_ld_wait();
-                        if (CW / CH > 2 && c + 1 < CW / CH) fetch(c + 1);
-#pragma unroll
-                        for (int h = 0; h < CH / 16; ++h) {
-                            float* z = reinterpret_cast<float*>(s[c & 1]) + 16 * h;
-                            const int at = c * CH + 16 * h;     // of this thread's positions
-                            if (!whole) {
-                                const uint32_t on = bits[at >> 5] >> (at & 31);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) z[i] = on >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
-                            }
-                            float x = 0.f;
-                            if (!S::SUMS) {
-                                x = z[0];
-                                float y = z[1];
-#pragma unroll
-                                for (int i = 2; i < 14; i += 4) {
-                                    x = max3(x, z[i], z[i + 1]);
-                                    y = max3(y, z[i + 2], z[i + 3]);
-                                }
-                                x = max3(x, y, fmaxf(z[14], z[15]));
-                            }
-                            float2 cm = make_float2(qc, qc), ca = make_float2(-m, -m), part = make_float2(0.f, 0.f);
-                            float un = 1.f;
-                            if (E4M3) {
-                                const float2 sc = m_sc[mi * 8 + half * (CW / 16) + (at >> 4)];
-                                cm.x = cm.y = sc.x * qc;
-                                ca.x = ca.y = sc.y + S::kBias - m;
-                                un = ex2(-sc.y);   // the sum goes without the value scale
-                                if (!S::SUMS) x = fmaf(x, cm.x, sc.y);
-                            }
-                            if (!S::SUMS) mx = fmaxf(mx, x);
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float2 e = fma2(make_float2(z[i], z[i + 1]), cm, ca);
-                                e.x = ex2(e.x);
-                                e.y = ex2(e.y);
-                                if (E4M3) part = add2(part, e);
-                                else if (i & 2) sum2 = add2(sum2, e);
-                                else sum = add2(sum, e);
-                                o[(at + i) >> 1] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
-                            }
-                            if (E4M3) {
-                                sum = fma2(part, make_float2(un, un), sum);
-                                if (S::SUMS) most = fmaxf(most, part.x + part.y);
-                            }
-                        }
-                    }
-                    const float all = (sum.x + sum.y) + (sum2.x + sum2.y);
-                    // (with two threads a row the vote says also that both have read their scores)
-                    if (!S::SUMS && !E4M3) mx *= qc;
-                    const bool over = any_of_rows(live && (S::SUMS ? (E4M3 ? most : all) > S::kMost : mx > m + S::kSlack));
-                    if (turn > 0 || !over) {
-                        l += all;
-                        break;
-                    }
-                    // move the references, and with them what has been summed
-                    if (S::SUMS)
-#pragma unroll
-                        for (int c = 0; c < CW / 16; ++c) {
-                            uint32_t v[16];
-                            tmem_ld16(sat + half * CW + 16 * c, v);
-                            tmem_ld_wait();
-                            const uint32_t on = bits[c >> 1] >> (16 * (c & 1));
-                            float x = -__int_as_float(0x7F800000);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) x = fmaxf(x, on >> i & 1u ? __uint_as_float(v[i]) : -__int_as_float(0x7F800000));
-                            if (E4M3) {
-                                const float2 sc = m_sc[mi * 8 + half * (CW / 16) + c];
-                                x = fmaf(x, sc.x * qc, sc.y);
-                            } else {
-                                x *= qc;
-                            }
-                            mx = fmaxf(mx, x);
-                        }
+                // the references to mx, and with them what has been summed
+                auto move = [&](float mx) {
                     if (NH == 2) mx = fmaxf(mx, others(mx));
                     const float mn = fmaxf(mx, m), f = ex2(m - mn);
                     const bool scale = any_of_rows((!SHARED || touched) && f != 1.f);   // (where nothing is summed yet all is zero)
@@ -1017,17 +948,119 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
                         st_wait();
                         tc_fence_before();
                     }
+                };
+                if (S::TWO && !idle) {
+                    float mx = -__int_as_float(0x7F800000);   // the row's largest score, in bits, with the value scale
+                    uint32_t v[2][32];
+                    ld32(sat, v[0]);
+#pragma unroll
+                    for (int c = 0; c < CW / 32; ++c) {
+                        tmem_ld_wait();
+                        if (c + 1 < CW / 32) ld32(sat + 32 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float* z = reinterpret_cast<float*>(v[c & 1]) + 16 * h;
+                            if (!whole) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) z[i] = bits[c] >> (16 * h + i) & 1u ? z[i] : -__int_as_float(0x7F800000);
+                            }
+                            const float2 sc = m_sc[mi * 8 + 2 * c + h];
+                            mx = fmaxf(mx, fmaf(most_of(z), sc.x * qc, sc.y));
+                        }
+                    }
+                    if (any_of_rows(live && mx > m + S::kSlack)) move(mx);
+                }
+                uint32_t o[S::TWO ? 16 : CW / 2];
+#pragma unroll 1
+                for (int turn = 0; !idle; ++turn) {
+                    uint32_t s[2][CH];
+                    auto fetch = [&](int c) {
+                        if constexpr (CH == 16) tmem_ld16(sat + half * CW + CH * c, s[c & 1]);
+                        else ld32(sat + half * CW + CH * c, s[c & 1]);
+                    };
+                    fetch(0);
+                    if (CW / CH == 2) fetch(1);
+                    float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
+                    float mx = -__int_as_float(0x7F800000);   // the row's largest score (in bits; fp16: with the value scale)
+#pragma unroll
+                    for (int c = 0; c < CW / CH; ++c) {
+                        if (c == 0 || CW / CH > 2) tmem_ld_wait();
+                        if (CW / CH > 2 && c + 1 < CW / CH) fetch(c + 1);
+#pragma unroll
+                        for (int h = 0; h < CH / 16; ++h) {
+                            float* z = reinterpret_cast<float*>(s[c & 1]) + 16 * h;
+                            const int at = c * CH + 16 * h;     // of this thread's positions
+                            if (!whole) {
+                                const uint32_t on = bits[at >> 5] >> (at & 31);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) z[i] = on >> i & 1u ? z[i] : -__int_as_float(0x7F800000);
+                            }
+                            float x = S::SUMS || S::TWO ? 0.f : most_of(z);
+                            float2 cm = make_float2(qc, qc), ca = make_float2(-m, -m), part = make_float2(0.f, 0.f);
+                            float un = 1.f;
+                            if (E4M3) {
+                                const float2 sc = m_sc[mi * 8 + half * (CW / 16) + (at >> 4)];
+                                cm.x = cm.y = sc.x * qc;
+                                ca.x = ca.y = sc.y + S::kBias - m;
+                                un = ex2(-sc.y);   // the sum goes without the value scale
+                                x = fmaf(x, cm.x, sc.y);
+                            }
+                            if (!S::SUMS) mx = fmaxf(mx, x);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                float2 e = fma2(make_float2(z[i], z[i + 1]), cm, ca);
+                                e.x = ex2(e.x);
+                                e.y = ex2(e.y);
+                                if (E4M3) part = add2(part, e);
+                                else if (i & 2) sum2 = add2(sum2, e);
+                                else sum = add2(sum, e);
+                                o[(at + i) >> 1 & (S::TWO ? 15 : CW / 2 - 1)] = E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                            }
+                            if (E4M3) sum = fma2(part, make_float2(un, un), sum);
+                            // over scores that have been read: the columns in front of these
+                            if constexpr (S::TWO)
+                                if (at & 16) st16(sat + half * (CW / 2) + (at >> 1) - 8, o);
+                        }
+                    }
+                    const float all = (sum.x + sum.y) + (sum2.x + sum2.y);
+                    if (S::TWO) {
+                        l += all;
+                        break;
+                    }
+                    if (!S::SUMS && !E4M3) mx *= qc;
+                    // (with two threads a row the vote says also that both have read their scores)
+                    const bool over = any_of_rows(live && (S::SUMS ? all > S::kMost : mx > m + S::kSlack));
+                    if (turn > 0 || !over) {
+                        l += all;
+                        break;
+                    }
+                    if (S::SUMS)
+#pragma unroll
+                        for (int c = 0; c < CW / 16; ++c) {
+                            uint32_t v[16];
+                            tmem_ld16(sat + half * CW + 16 * c, v);
+                            tmem_ld_wait();
+                            const uint32_t on = bits[c >> 1] >> (16 * (c & 1));
+                            float x = -__int_as_float(0x7F800000);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) x = fmaxf(x, on >> i & 1u ? __uint_as_float(v[i]) : -__int_as_float(0x7F800000));
+                            mx = fmaxf(mx, x * qc);
+                        }
+                    move(mx);
                 }
                 if (idle) {
                     if (NH == 2) pair_barrier(1 + q * 4 + (warp & 3));   // (both have read: the first reference)
 #pragma unroll
-                    for (int i = 0; i < CW / 2; ++i) o[i] = 0u;
+                    for (int i = 0; i < (S::TWO ? 16 : CW / 2); ++i) o[i] = 0u;
+                    if constexpr (S::TWO)
+                        for (int i = 0; i < CW / 32; ++i) st16(sat + half * (CW / 2) + 16 * i, o);
                 }
                 none = false;
                 if (SHARED) touched = touched || mine;
+                if constexpr (!S::TWO)
 #pragma unroll
-                for (int i = 0; i < CW / 64; ++i)   // over the scores
-                    st32(sat + half * (CW / 2) + 32 * i, *reinterpret_cast<const uint32_t(*)[32]>(o + 32 * i));
+                    for (int i = 0; i < CW / 64; ++i)   // over the scores
+                        st32(sat + half * (CW / 2) + 32 * i, *reinterpret_cast<const uint32_t(*)[32]>(o + 32 * i));
                 bool zeroed = false;
                 if (!whole && q == zq && half == 0) {
                     // value rows that no row of the item attends may hold anything: zero
