@@ -92,7 +92,7 @@ enum { MTP_WQ_NONE = 0, MTP_WQ_Q8_0 = 1, MTP_WQ_Q4_0 = 2 };
 #define MTP_MAX_VERIFY_BATCH 65536  /* sequences of one verify or draw call */
 #define MTP_MAX_CENTROIDS 8192      /* centroids of a centroid-routed LM head */
 #define MTP_MAX_CATCHUP 16          /* catch-up rows per sequence of one mtp_nextn_draft call */
-#define MTP_MAX_PAGED_BATCH 1024    /* sequences of one mtp_kv_append or mtp_paged_attention call */
+#define MTP_MAX_PAGED_BATCH 1024    /* sequences of one mtp_kv_append or attention call over a paged cache */
 #define MTP_MAX_APPEND_ROWS 65536   /* rows per sequence of one mtp_kv_append call */
 #define MTP_MAX_ATTN_ROWS 64        /* rows per sequence of one mtp_paged_attention call */
 #define MTP_MAX_PAGE_SIZE 256       /* slots of a page */
@@ -552,7 +552,7 @@ size_t mtp_prefix_workspace_size(const mtp_kv_cache *c, int B, int M, int n_q_he
  *              front of row_start[0], behind row_start[B]) keep their bytes
  *   q          rows in dtype (F32 or BF16): row (t, head h) at t*q_stride_m +
  *              h*q_stride_h (elements; 16-byte multiples, 16-byte aligned)
- *   out [T, n_q_heads, head_dim] in dtype
+ *   out [T, n_q_heads, head_dim] in dtype; it overlaps no input
  * fp32 queries are computed in fp32 throughout, with any cache.  bf16 queries
  * against a bf16 or e4m3 cache with head_dim 64, 128 or 256 run on the tensor
  * cores: rotated queries and probabilities are then rounded to bf16 (e4m3 cache:
@@ -580,7 +580,8 @@ int mtp_prompt_attention(const mtp_kv_cache *c, int B, int64_t T, int n_q_heads,
  * The cache's window must be 0 (MTP_ERR_UNSUPPORTED otherwise: a sliding layer's
  * rows attend few positions of a long prefix, and mtp_paged_attention reads only
  * those).  Types and roundings as for mtp_prompt_attention.
- * A sequence whose kv_len, n_new, prefix_len or group is out of range is left out,
+ * A sequence whose kv_len, n_new, prefix_len or group is out of range is left out
+ * (group_start that does not ascend: any of them may be),
  * positions on absent pages are masked, and both set the status word to
  * MTP_ERR_ARG.  1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= M <= MTP_MAX_ATTN_ROWS,
  * 0 <= n_groups <= B, at most 16 query heads per KV head, B * (max_pages *

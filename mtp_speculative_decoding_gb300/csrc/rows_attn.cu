@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_cc_kernel(const __grid_const
         for (int b = threadIdx.x; b < a.B; b += kRowThreads) {
             Seq s;
             bad = !seq_at(a, b, s) || bad;
+            if (b < a.n_groups) bad = bad || a.group_start[b] > a.group_start[b + 1];
         }
     const long long row = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     const int tok = (int)(row / a.Hq), h = (int)(row - (long long)tok * a.Hq);

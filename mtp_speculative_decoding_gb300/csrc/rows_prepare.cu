@@ -269,11 +269,23 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
     asm volatile("griddepcontrol.wait;" ::: "memory");
     bool good = true;
     if (a.n_groups > 0) {
+        bool ascend = true;
         for (int i = tid; i <= a.n_groups; i += kPrepThreads) {
             g_start[i] = a.group_start[i];
-            if (i < a.n_groups) g_len[i] = a.prefix_len[i];
+            if (i < a.n_groups) {
+                g_len[i] = a.prefix_len[i];
+                ascend = ascend && g_start[i] <= a.group_start[i + 1];
+            }
         }
-        __syncthreads();
+        // groups that overlap could be more items than the plan has room for: one group of all
+        // sequences with no possible prefix then, so that all are left out
+        if (!__syncthreads_and(ascend)) {
+            for (int i = tid; i <= a.n_groups; i += kPrepThreads) {
+                g_start[i] = i > 0 ? a.B : 0;
+                if (i < a.n_groups) g_len[i] = -1;
+            }
+            __syncthreads();
+        }
     }
     if (a.M > 0) good = count_tokens(a, gr, cum, planner ? cumt : nullptr, planner ? lens : nullptr, tmp);
     else

@@ -152,3 +152,16 @@ def test_every_row_computed_again(kv, hd):
     rc.check(x.out[:700][..., keep], ref[..., keep], mass[..., keep], dots, 700, "f32")
     ref = rc.attend(x.pool, 1, x.q[700:], None, 0, 1e4)
     rc.check(x.out[700:], *ref, 50, kv)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+def test_groups_that_overlap_are_reported(kv):
+    """Bounds that go up and down again: many groups of all sequences, more items than a plan holds."""
+    x = Prefix(12, 16, 90, 128, kv, 9)
+    start = i32([0, 12] * 6 + [0])
+    x.m.prefix_attention(x.h, x.q, x.at[0], start, i32([90] * 12), x.out, x.ws)
+    assert x.m.last_error(x.ws) == x.m.MTP_ERR_ARG
+    if kv == "bf16":
+        assert (x.out == 7.0).all()
+    x.call()
+    x.check()
