@@ -138,14 +138,11 @@ __device__ __forceinline__ long long tile_units(const RowsTcArgs& t, const Block
 __device__ __forceinline__ long long units_before(const RowsTcArgs& t, const BlockRec& k, int open, long long i) {
     return tile_units(t, k, i) + i * open * (long long)(kPosTile * t.a.G);
 }
-// worker w's share of T units begins at share_at(T, w); the worker that has unit x
-__device__ __forceinline__ long long share_at(long long T, int workers, int w) {
-    const long long base = T / workers, rem = T - base * workers;
-    return base * w + (w < rem ? w : rem);
-}
 __device__ __forceinline__ long long quotient(long long a, long long b) {   // a / b, neither negative
     return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
+// Shares of T units are even, the first T mod workers of them one longer: the worker that
+// has unit x
 __device__ __forceinline__ int worker_of(long long T, int workers, long long x) {
     const long long base = quotient(T, workers), rem = T - base * workers;
     return (int)(x < rem * (base + 1) ? quotient(x, base + 1) : rem + quotient(x - rem * (base + 1), base));

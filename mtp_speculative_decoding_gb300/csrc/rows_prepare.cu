@@ -20,11 +20,16 @@ constexpr int kPrepThreads = 256;
 // group_start and prefix_len, copied to shared memory
 struct Groups { const int32_t *start, *len; };
 
+// The plan's code runs once a call, on one SM, and its instructions come from memory each
+// time: no loop is unrolled and nothing is computed twice (8192 prompt rows: 360 to 352 us;
+// 64 sequences behind a prefix: 56.4 to 55.1).  Out of line, with its structs on the stack, it
+// is slower (57.0 to 59.3).
+
 // sums of v over the threads in front of this one, and over all of the CTA
 __device__ __forceinline__ long long scan(long long v, long long* s, long long& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long inc = v;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += u;
@@ -34,7 +39,7 @@ __device__ __forceinline__ long long scan(long long v, long long* s, long long& 
     __syncthreads();
     long long base = inc - v;
     total = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < kPrepThreads / 32; ++w) {
         if (w < warp) base += s[w];
         total += s[w];
@@ -49,35 +54,34 @@ __device__ __forceinline__ int own_tiles(const Seq& s) { return s.n > 0 ? (s.len
 // if this thread saw something out of range.  cumt, lens null: tokens alone.
 __device__ __forceinline__ bool count_tokens(const RowsArgs& a, const Groups& gr, int* cum, int* cumt, int* lens, long long* tmp) {
     bool good = true;
-    constexpr int MAX = (MTP_MAX_PAGED_BATCH + kPrepThreads - 1) / kPrepThreads;
     const int per = (a.B + kPrepThreads - 1) / kPrepThreads, b0 = (int)threadIdx.x * per, b1 = b0 + per < a.B ? b0 + per : a.B;
-    int n[MAX], tl[MAX];
     long long sum = 0;
-#pragma unroll
-    for (int i = 0; i < MAX; ++i) {
-        n[i] = tl[i] = 0;
-        if (b0 + i < b1) {
-            Seq s;
-            good = seq_at(a, b0 + i, s, gr.start, gr.len) && good;
-            n[i] = s.n;
-            tl[i] = own_tiles(s);
-            if (lens) lens[b0 + i] = s.len;
-            sum += (long long)s.n << 40 | tl[i];   // (at most 2^16 tokens, 2^34 tiles)
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        Seq s;
+        good = seq_at(a, b, s, gr.start, gr.len) && good;
+        const int tl = own_tiles(s);
+        cum[b] = s.n;
+        if (cumt) {
+            cumt[b] = tl;
+            lens[b] = s.len;
         }
+        sum += (long long)s.n << 40 | tl;          // (at most 2^16 tokens, 2^31 tiles)
     }
     long long all;
     const long long before = scan(sum, tmp, all);
     int at = (int)(before >> 40), tat = (int)(before & 0xFFFFFFFFFFll);
-#pragma unroll
-    for (int i = 0; i < MAX; ++i)
-        if (b0 + i < b1) {
-            cum[b0 + i] = at;
-            at += n[i];
-            if (cumt) {
-                cumt[b0 + i] = tat;
-                tat += tl[i];
-            }
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        const int n = cum[b];
+        cum[b] = at;
+        at += n;
+        if (cumt) {
+            const int tl = cumt[b];
+            cumt[b] = tat;
+            tat += tl;
         }
+    }
     if (threadIdx.x == 0) {
         cum[a.B] = (int)(all >> 40);
         if (cumt) cumt[a.B] = (int)(all & 0xFFFFFFFFFFll);
@@ -102,7 +106,7 @@ __device__ __forceinline__ StagedAt staged_at(const RowsArgs& a, const Groups& g
     return w;
 }
 
-__device__ BlockRec block_at(const RowsArgs& a, const Groups& gr, const int* cum, int blk, bool& good) {
+__device__ __forceinline__ BlockRec block_at(const RowsArgs& a, const Groups& gr, const int* cum, int blk, bool& good) {
     BlockRec k = {};
     if (blk < 2 * a.n_groups) {
         const bool own = blk >= a.n_groups;
@@ -145,25 +149,30 @@ __device__ void count_items(const RowsTcArgs& t, const Groups& gr, const Sequenc
     const int tid = threadIdx.x, per = (a.n_groups + kPrepThreads - 1) / kPrepThreads, i0 = tid * per,
               i1 = i0 + per < a.n_groups ? i0 + per : a.n_groups;
     long long sum = 0, all;
-    for (int i = i0; i < i1; ++i) sum += row_tiles_of(a, block_at(a, gr, sq.cum, a.n_groups + i, good));
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) sum += rt0[i] = row_tiles_of(a, block_at(a, gr, sq.cum, a.n_groups + i, good));
     int at = (int)scan(sum, tmp, all);
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
+        const int n = rt0[i];
         rt0[i] = at;
-        at += row_tiles_of(a, block_at(a, gr, sq.cum, a.n_groups + i, good));
+        at += n;
     }
     if (tid == 0) rt0[a.n_groups] = (int)all;
     __syncthreads();
     const int items = (int)all, pi = (items + kPrepThreads - 1) / kPrepThreads, x0 = tid * pi, x1 = x0 + pi < items ? x0 + pi : items;
-    auto tiles = [&](int x) {
-        const int i = last_at_most(rt0, a.n_groups, x);
-        return item_of<true>(a, sq, block_at(a, gr, sq.cum, a.n_groups + i, good), x - rt0[i]).n;
-    };
     sum = 0;
-    for (int x = x0; x < x1; ++x) sum += tiles(x);
-    at = (int)scan(sum, tmp, all);
+#pragma unroll 1
     for (int x = x0; x < x1; ++x) {
+        const int i = last_at_most(rt0, a.n_groups, x);
+        sum += t.items[x] = item_of<true>(a, sq, block_at(a, gr, sq.cum, a.n_groups + i, good), x - rt0[i]).n;
+    }
+    at = (int)scan(sum, tmp, all);
+#pragma unroll 1
+    for (int x = x0; x < x1; ++x) {
+        const int n = t.items[x];
         t.items[x] = at;
-        at += tiles(x);
+        at += n;
     }
     if (tid == 0) t.items[items] = (int)all;
     __syncthreads();
@@ -175,6 +184,7 @@ __device__ void make_plan(const RowsTcArgs& t, const Groups& gr, const int* cum,
               k1 = k0 + per < nb ? k0 + per : nb;
     const long long U = (long long)kPosTile * a.G;
     long long tiles = 0, items = 0;
+#pragma unroll 1
     for (int i = k0; i < k1; ++i) {
         BlockRec k = block_at(a, gr, cum, i, good);
         if (k.kind == kOwn) k.row0 = rt0[i - a.n_groups];
@@ -193,6 +203,7 @@ __device__ void make_plan(const RowsTcArgs& t, const Groups& gr, const int* cum,
     at += it * open * U;
     const long long T = units + n_items * open * U, most = quotient(T, U);
     const int workers = most < t.workers ? (most > 1 ? (int)most : 1) : t.workers;
+#pragma unroll 1
     for (int i = k0; i < k1; ++i) {
         const long long u = pre[i] + (long long)a.c.Hkv * nrt[i] * open * U;
         pre[i] = at;
@@ -200,11 +211,13 @@ __device__ void make_plan(const RowsTcArgs& t, const Groups& gr, const int* cum,
         at += u;
     }
     __syncthreads();   // (the records of the other threads too)
+    const long long base = quotient(T, workers), rem = T - base * workers;   // (see worker_of)
+#pragma unroll 1
     for (int w = tid; w < t.workers; w += kPrepThreads) {
         WorkerRec r = {};
         r.open = open;
-        r.xs = w < workers ? share_at(T, workers, w) : T;
-        r.xe = w < workers ? share_at(T, workers, w + 1) : T;
+        r.xs = w < workers ? base * w + (w < rem ? w : rem) : T;
+        r.xe = w < workers ? base * (w + 1) + (w + 1 < rem ? w + 1 : rem) : T;
         if (r.xs < r.xe) {
             int b = 0;
             for (int hi = nb - 1; b < hi;) {   // the last block that begins at xs or before
