@@ -30,12 +30,12 @@
 // of the two products, and those are the bound here, not the cache's bytes.  e4m3
 // caches: both to fp16 (2^-11), which the codes need anyway.
 //
-// Measured, the whole call: 8192 tokens, 16 heads of 256 over 4 KV heads, bf16: 363 us,
-// 1515 TFLOP/s (the matrix units at what clock the power limit leaves them).  The same
-// with 128 dimensions over 8 KV heads: 276 us, 995 TFLOP/s, bound by the softmax's
+// Measured, the whole call: 8192 tokens, 16 heads of 256 over 4 KV heads, bf16: 353 us,
+// 1550 TFLOP/s (the matrix units at what clock the power limit leaves them).  The same
+// with 128 dimensions over 8 KV heads: 271 us, 1010 TFLOP/s, bound by the softmax's
 // instructions between two row tiles.  e4m3, two pieces of 1024 tokens behind 15000:
-// 426 us, 1220 TFLOP/s, bound by opening the codes (4 warps) and the softmax together.
-// 64 sequences of up to 3 rows behind 8192 common positions: 57 us, of which this
+// 416 us, 1250 TFLOP/s, bound by opening the codes (4 warps) and the softmax together.
+// 64 sequences of up to 3 rows behind 8192 common positions: 55 us, of which this
 // kernel 42: half of its tiles are the sequences' own, where few of 256 rows count.
 //
 // A result that is not finite is computed again, position by position, by the

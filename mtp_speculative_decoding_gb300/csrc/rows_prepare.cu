@@ -8,7 +8,8 @@
 // work; here they cost their bytes: 12288 rows of 16 heads of 256, 201 MB in and out,
 // take 50 us behind a flushed cache (4 TB/s).  Fewer heads a thread (8, 4), two in
 // flight instead of four, three or four CTAs an SM instead of two measured the same.
-// With few rows the plan's chain of scans and searches is what takes time: 10 us.
+// With few rows the plan's chain of scans and searches is what takes time: run a second
+// time, its parts lengthen a call of 4 sequences behind a prefix by 8 us.
 #include "rows_attn_tc.cuh"
 
 namespace mtp {
