@@ -193,11 +193,16 @@ __device__ __forceinline__ void tma_2d(void* dst, const void* tmap, int x, int y
                  "l"(tmap), "r"(x), "r"(y), "r"(smem_addr(bar))
                  : "memory");
 }
-// 32 bytes (a whole sector) in one store
+// 32 bytes (a whole sector, where p is aligned to as many) in one store
 __device__ __forceinline__ void store_32b(void* p, const uint32_t* w) {
     asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
                  "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
+}
+// the same to 16-byte aligned memory
+__device__ __forceinline__ void store_2x16b(void* p, const uint32_t* w) {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 // two warps (64 threads) at barrier `id`: whether any of them says so
 __device__ __forceinline__ bool pair_vote(int id, bool x) {
@@ -825,6 +830,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
         const uint32_t oat = tmem + lanes + S::O0 + q * S::OC + half * (HD / NH);   // this thread's part of the accumulator
         unsigned tc = 0, ti = 0, g0 = 0;                     // tiles of this row tile, of the CTA; ring slots before this piece
         unsigned used = 0;                                   // bit b: odd uses of score buffer b by this row tile
+        const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // (the caller owes 16 bytes; rows are multiples of 128)
         auto meet = [&](unsigned long long* bar, unsigned parity) {
             wait(bar, parity);
             __syncwarp();
@@ -1136,8 +1142,13 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
                         odd[i >> 1 & 3] = fmaf(x, 0.f, fmaf(y, 0.f, odd[i >> 1 & 3]));
                         w[i >> 1] = pack_bf16(x, y);
                     }
-                    store_32b(dst + c, w);
-                    store_32b(dst + c + 16, w + 8);
+                    if (sectors) {
+                        store_32b(dst + c, w);
+                        store_32b(dst + c + 16, w + 8);
+                    } else {
+                        store_2x16b(dst + c, w);
+                        store_2x16b(dst + c + 16, w + 8);
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) store_32b(part + c + i, v + i);

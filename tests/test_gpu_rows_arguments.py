@@ -1,0 +1,78 @@
+"""Calls of the attention of prompts and of shared prefixes that the header
+allows and few programs make: outputs and queries at any 16-byte address,
+windows without an end, bounds that do not ascend, dirty workspaces."""
+import pytest
+import torch
+
+import paged_common as pc
+import rows_common as rc
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from mtp_speculative_decoding_gb300 import build
+    build.build()
+
+
+def mtp():
+    import mtp_speculative_decoding_gb300 as m
+    return m
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def rand(shape, dtype, seed):
+    return torch.randn(shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)).to(dtype)
+
+
+def at_address(x, byte):
+    """A copy of x whose address is `byte` behind a 256-byte boundary."""
+    n = byte // x.element_size()
+    y = torch.empty(x.numel() + 256, dtype=x.dtype, device="cuda")
+    assert y.data_ptr() % 256 == 0 and byte % x.element_size() == 0
+    y = y[n:n + x.numel()].view(x.shape)
+    y.copy_(x)
+    assert y.data_ptr() % 256 == byte
+    return y
+
+
+def prompt(pool, q, row_start, lens, out=None, ws=None, **kw):
+    m = mtp()
+    h = pool.handle(**kw)
+    T, hq, _ = q.shape
+    ws = m.alloc_workspace(m.prompt_workspace_size(h, len(lens), T, hq)) if ws is None else ws
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda") if out is None else out
+    m.prompt_attention(h, q, i32(row_start), i32(lens), out, ws)
+    return out, m.last_error(ws)
+
+
+@pytest.mark.parametrize("byte", [16, 32, 48, 240])
+@pytest.mark.parametrize("kv,qt,hd", [("bf16", "bf16", 64), ("bf16", "bf16", 128), ("bf16", "bf16", 256), ("e4m3", "bf16", 64), ("e4m3", "bf16", 128),
+                                      ("e4m3", "bf16", 256), ("f32", "f32", 64), ("bf16", "bf16", 512)])
+def test_outputs_and_queries_at_any_16_byte_address(kv, qt, hd, byte):
+    m = mtp()
+    dt = torch.bfloat16 if qt == "bf16" else torch.float32
+    n, lens, hq = [150, 3], [40, 300], 2
+    pool = pc.Pool(2, 24, 16, 1, hd, kv, seed=1)
+    pool.fill([a + c for a, c in zip(lens, n)], seed=2)
+    q = rand((sum(n), hq, hd), dt, 3)
+    want, st = prompt(pool, q, [0, 150, 153], lens, rope_theta=1e4)
+    assert st == m.MTP_OK
+    out, st = prompt(pool, at_address(q, byte), [0, 150, 153], lens, out=at_address(torch.full_like(q, 7.0), byte), rope_theta=1e4)
+    assert st == m.MTP_OK and torch.equal(out, want)
+    # shared prefixes
+    h = pool.handle(rope_theta=1e4)
+    B, M = 2, 3
+    qq = q[:B * M].reshape(B, M, hq, hd).contiguous()
+    ws = m.alloc_workspace(m.prefix_workspace_size(h, B, M, hq))
+    outs = []
+    for b in (0, byte):
+        o = at_address(torch.full_like(qq, 7.0), b)
+        m.prefix_attention(h, at_address(qq, b), i32([40, 300]), i32([0, 2]), i32([37]), o, ws)
+        assert m.last_error(ws) == m.MTP_OK
+        outs.append(o)
+    assert torch.equal(*outs)
