@@ -247,7 +247,8 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
     t.a = a;
     t.workers = p.workers;
     const long long U = (long long)kPosTile * a.G;
-    t.window_units = U * ((a.c.sink + (long long)kPosTile - 1) / kPosTile + (a.c.window + (kRowTile - 1) / a.G) / kPosTile + 2);
+    // (in 64 bits: a window or a sink may be as long as an int goes)
+    t.window_units = U * ((a.c.sink + (long long)kPosTile - 1) / kPosTile + (a.c.window + (long long)(kRowTile - 1) / a.G) / kPosTile + 2);
     t.cta_status = reinterpret_cast<int*>(base + p.status);
     t.note = reinterpret_cast<RowNote*>(base + p.note);
     t.row_parts = reinterpret_cast<RowPart*>(base + p.row_parts);

@@ -76,3 +76,25 @@ def test_outputs_and_queries_at_any_16_byte_address(kv, qt, hd, byte):
         assert m.last_error(ws) == m.MTP_OK
         outs.append(o)
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("kv,qt,hd", [("bf16", "bf16", 64), ("bf16", "bf16", 128), ("bf16", "bf16", 256), ("e4m3", "bf16", 128),
+                                      ("e4m3", "bf16", 256), ("f32", "f32", 64)])
+@pytest.mark.parametrize("G", [1, 4, 16])
+def test_windows_as_long_as_an_int_goes(kv, qt, hd, G):
+    """A window that reaches over everything is no window, up to 2^31 - 1, with any sink."""
+    m = mtp()
+    n, lens = [400, 70, 1], [0, 333, 600]
+    pool = pc.Pool(3, 13, 64, 1, hd, kv, seed=4)
+    pool.fill([a + c for a, c in zip(lens, n)], seed=5)
+    q = rand((471, G, hd), torch.bfloat16 if qt == "bf16" else torch.float32, 6)
+    at = [0, 400, 470, 471]
+    want, st = prompt(pool, q, at, lens, rope_theta=1e4)
+    assert st == m.MTP_OK
+    for b, a in enumerate(lens):
+        r = slice(at[b], at[b + 1])
+        rc.check(want[r], *rc.attend(pool, b, q[r], None, a, 1e4), a + n[b], kv)
+    top = 2 ** 31 - 1
+    for window, sink in ((top, 0), (top, top), (top - 15, 4), (top - 255, 0), (top - 256, 1000), (2 ** 30, top), (671, 0), (601, 9)):
+        out, st = prompt(pool, q, at, lens, rope_theta=1e4, window=window, sink=sink)
+        assert st == m.MTP_OK and torch.equal(out, want), (window, sink)
