@@ -549,7 +549,10 @@ size_t mtp_prefix_workspace_size(const mtp_kv_cache *c, int B, int M, int n_q_he
  * in the cache already.
  *   kv_len [B] int32: positions cached before the rows
  *   row_start [B + 1] int32, ascending, within [0, T]; rows of no sequence (in
- *              front of row_start[0], behind row_start[B]) keep their bytes
+ *              front of row_start[0], behind row_start[B]) keep their bytes.
+ *              Where it does not ascend, a sequence is left out unless all bounds
+ *              in front of its rows are at most row_start[b] and all behind them
+ *              at least row_start[b + 1]: rows that two would claim are no one's
  *   q          rows in dtype (F32 or BF16): row (t, head h) at t*q_stride_m +
  *              h*q_stride_h (elements; 16-byte multiples, 16-byte aligned)
  *   out [T, n_q_heads, head_dim] in dtype; it overlaps no input

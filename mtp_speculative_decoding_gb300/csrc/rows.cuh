@@ -41,8 +41,15 @@ __device__ __forceinline__ int last_at_most(const int32_t* start, int n, int x) 
     }
     return lo;
 }
+// Prompts: sequence b's rows are its alone.  No bound in front of them lies behind their
+// start, none behind them in front of their end; the last bound that is not above one of
+// its rows is then its own.  Of bounds that ascend that holds for every sequence.
+__device__ __forceinline__ bool bound_agrees(const int32_t* row_start, int b, int i) {
+    return i <= b ? row_start[i] <= row_start[b] : row_start[i] >= row_start[b + 1];
+}
 // false: its lengths, rows or group are out of range (s.n is 0 then).  starts,
-// lengths: copies of group_start and prefix_len.
+// lengths: copies of group_start and prefix_len.  (Whether bound_agrees is the caller's
+// to find out.)
 __device__ __forceinline__ bool seq_at(const RowsArgs& a, int b, Seq& s, const int32_t* starts, const int32_t* lengths) {
     s.len = a.kv_len[b];
     s.P = 0;

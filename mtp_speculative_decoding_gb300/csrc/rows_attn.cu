@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_cc_kernel(const __grid_const
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < a.B; b += kRowThreads) {
             Seq s;
-            bad = !seq_at(a, b, s) || bad;
+            bad = !seq_at(a, b, s) || bad;   // (where bounds do not ascend, two neighbours do not)
             if (b < a.n_groups) bad = bad || a.group_start[b] > a.group_start[b + 1];
         }
     const long long row = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
@@ -168,7 +168,12 @@ __global__ void __launch_bounds__(kRowThreads) rows_cc_kernel(const __grid_const
     Seq s;
     if (b < a.B && seq_at(a, b, s)) {
         const int j = (int)(tok - s.row0);
-        if (j >= 0 && j < s.n) bad = !attend_row<QT, KT>(a, s, b, j, h, lane) || bad;
+        bool mine = j >= 0 && j < s.n;
+        if (mine && a.M == 0) {   // (32 bounds at a time: little beside the positions that a row walks)
+            for (int i = lane; i <= a.B; i += 32) mine = mine && bound_agrees(a.row_start, b, i);
+            mine = __all_sync(0xffffffffu, mine);
+        }
+        if (mine) bad = !attend_row<QT, KT>(a, s, b, j, h, lane) || bad;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicCAS(&a.hdr->status, MTP_OK, MTP_ERR_ARG);
 }

@@ -18,8 +18,17 @@ namespace {
 
 constexpr int kPrepThreads = 256;
 
-// group_start and prefix_len, copied to shared memory
-struct Groups { const int32_t *start, *len; };
+// group_start and prefix_len, copied to shared memory; prompts whose row_start does not
+// ascend: whether a sequence's rows are its alone (otherwise null)
+struct Groups { const int32_t *start, *len, *alone; };
+__device__ __forceinline__ bool seq_at(const RowsArgs& a, int b, Seq& s, const Groups& gr) {
+    bool ok = seq_at(a, b, s, gr.start, gr.len);
+    if (gr.alone && !gr.alone[b]) {
+        s.n = 0;
+        ok = false;
+    }
+    return ok;
+}
 
 // The plan's code runs once a call, on one SM, and its instructions come from memory each
 // time: no loop is unrolled and nothing is computed twice (8192 prompt rows: 360 to 352 us;
@@ -60,7 +69,7 @@ __device__ __forceinline__ bool count_tokens(const RowsArgs& a, const Groups& gr
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         Seq s;
-        good = seq_at(a, b, s, gr.start, gr.len) && good;
+        good = seq_at(a, b, s, gr) && good;
         const int tl = own_tiles(s);
         cum[b] = s.n;
         if (cumt) {
@@ -128,7 +137,7 @@ __device__ __forceinline__ BlockRec block_at(const RowsArgs& a, const Groups& gr
     }
     Seq s;
     const int b = blk - 2 * a.n_groups;
-    good = seq_at(a, b, s, gr.start, gr.len) && good;
+    good = seq_at(a, b, s, gr) && good;
     k.table = b;
     if (s.n > 0 && s.group < 0) {
         const StagedAt w = staged_at(a, gr, cum, s, b);
@@ -271,7 +280,7 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
     // the plan's CTA: own tiles before a sequence, cached positions, row tiles before a group and of a block, units before a block
     int *cumt = g_len + a.n_groups, *lens = cumt + a.B + 1, *rt0 = lens + a.B, *nrt = rt0 + a.n_groups + 1;
     long long* pre = reinterpret_cast<long long*>(sm + prep_ints(a.B, a.n_groups));
-    const Groups gr = {g_start, g_len};
+    Groups gr = {g_start, g_len, nullptr};
     const int tid = threadIdx.x;
     const bool planner = blockIdx.x == 0;
     if (a.rope.on && !planner)
@@ -302,8 +311,23 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
         }
     }
     if (a.M > 0) good = count_tokens(a, gr, cum, planner ? cumt : nullptr, planner ? lens : nullptr, tmp);
-    else
-        for (int i = tid; i <= a.B; i += kPrepThreads) cum[i] = a.row_start[i];
+    else {
+        bool ascend = true;
+        for (int i = tid; i <= a.B; i += kPrepThreads) {
+            cum[i] = a.row_start[i];
+            ascend = ascend && (i == 0 || a.row_start[i - 1] <= cum[i]);
+        }
+        // rows of two sequences would be staged over one another (KV head by KV head: over
+        // other tokens' rows too)
+        if (!__syncthreads_and(ascend)) {
+            for (int b = tid; b < a.B; b += kPrepThreads) {
+                bool alone = true;
+                for (int i = 0; i <= a.B; ++i) alone = alone && bound_agrees(cum, b, i);
+                lens[b] = alone;
+            }
+            gr.alone = lens;
+        }
+    }
     __syncthreads();
     if (planner) {
         if (a.M > 0) {
@@ -324,12 +348,19 @@ __global__ void __launch_bounds__(kPrepThreads) rows_prepare_kernel(const __grid
     const int h0 = (int)(x - (long long)tok * groups) * hpt;
     // (whole rows' lanes are out of range together; all lanes go along for the shuffles)
     bool live = tok < toks;
+    const bool there = live;
     if (!live) tok = toks - 1;
     const int b = a.M > 0 ? tok / a.M : last_at_most(cum, a.B, tok);
     Seq s;
-    live = seq_at(a, b, s, gr.start, gr.len) && live;
+    live = seq_at(a, b, s, gr) && live;
     const int j = (int)(tok - s.row0);
     live = live && j >= 0 && j < s.n;
+    // prompts' rows that the attention does not come to: not marked either
+    if (a.M == 0 && there && !live && c == 0)
+        for (int h = h0; h < h0 + hpt && h < a.Hq; ++h) {
+            t.odd[(long long)tok * a.Hq + h] = 0;
+            if (rows_halves(hd) > 1) t.odd[t.odd_plane + (long long)tok * a.Hq + h] = 0;
+        }
     if (!__any_sync(0xffffffffu, live)) return;
     const StagedAt w = live ? staged_at(a, gr, cum, s, b) : StagedAt{0, 0};
     const long long src0 = live ? s.q0 + j * a.sm : 0;

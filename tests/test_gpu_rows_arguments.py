@@ -98,3 +98,43 @@ def test_windows_as_long_as_an_int_goes(kv, qt, hd, G):
     for window, sink in ((top, 0), (top, top), (top - 15, 4), (top - 255, 0), (top - 256, 1000), (2 ** 30, top), (671, 0), (601, 9)):
         out, st = prompt(pool, q, at, lens, rope_theta=1e4, window=window, sink=sink)
         assert st == m.MTP_OK and torch.equal(out, want), (window, sink)
+
+
+def left_in(at, T):
+    """Sequences whose rows are theirs alone and within [0, T]."""
+    return [b for b in range(len(at) - 1) if 0 <= at[b] <= at[b + 1] <= T and max(at[: b + 1]) <= at[b] and min(at[b + 1:]) >= at[b + 1]]
+
+
+@pytest.mark.parametrize("kv,qt,hd", [("bf16", "bf16", 64), ("bf16", "bf16", 128), ("bf16", "bf16", 256), ("e4m3", "bf16", 128),
+                                      ("e4m3", "bf16", 256), ("f32", "f32", 64), ("bf16", "bf16", 512)])
+def test_bounds_that_do_not_ascend(kv, qt, hd):
+    """What two sequences would claim is left out with both of them, for every KV
+    head, and the others are right."""
+    m = mtp()
+    B, T, hkv, G = 5, 150, 2, 2
+    pool = pc.Pool(B, 16, 16, hkv, hd, kv, seed=7)
+    pool.fill([210] * B, seed=8)
+    lens = [60] * B
+    q = rand((T, hkv * G, hd), torch.bfloat16 if qt == "bf16" else torch.float32, 9)
+    h = pool.handle(rope_theta=1e4)
+    ws = m.alloc_workspace(m.prompt_workspace_size(h, B, T, hkv * G))
+    ref = {}
+    g = torch.Generator().manual_seed(10)
+    bounds = [[0, 40, 30, 70, 110, 150], [10, 5, 5, 60, 60, 100], [150, 110, 70, 30, 20, 0], [0, 150, 20, 30, 60, 150], [0, 30, 60, 90, 120, 119],
+              [-5, 20, 10, 60, 90, 151], [0, 2 ** 31 - 1, -2 ** 31, 20, 20, 150]]
+    bounds += [(torch.randint(0, 6, (B + 1,), generator=g).sort().values + torch.randint(0, 2, (B + 1,), generator=g)).mul(25).tolist()
+               for _ in range(8)]
+    for at in bounds:
+        ws.fill_(0xFF)
+        out, st = prompt(pool, q, at, lens, ws=ws, rope_theta=1e4)
+        good = left_in(at, T)
+        assert st == (m.MTP_OK if len(good) == B else m.MTP_ERR_ARG), at
+        used = torch.zeros(T, dtype=torch.bool)
+        for b in good:
+            r0, r1 = at[b], at[b + 1]
+            used[r0:r1] = True
+            if r1 > r0:
+                if (b, r0, r1) not in ref:
+                    ref[b, r0, r1] = rc.attend(pool, b, q[r0:r1], None, 60, 1e4)
+                rc.check(out[r0:r1], *ref[b, r0, r1], 60 + r1 - r0, kv)
+        assert (out[~used] == 7.0).all(), at
