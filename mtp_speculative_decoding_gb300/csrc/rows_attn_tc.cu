@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
         unsigned long long *bf = E4M3 ? rfull : full, *be = E4M3 ? rempty : empty;
         unsigned slot = 0, phase = 0, ti = 0;
         bool ok = true, bad = false;
-        RowNote note = {-1, 0, 0, 0, 0, 0, {0, 0}};
+        RowNote note = {-1, 0, 0, 0, 0, {0, 0, 0}};
         Walk<SHARED> p;
         p.start(first, sq);
         while (ok && p.next(t)) {
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
             }
             if (!SHARED && p.slot == 2 && p.t0 == 0)
                 note = RowNote{worker_of(t.head->T, t.head->workers, p.tiles_at + (long long)(p.it.n - 1) * kPosTile * a.G), p.it.rows, p.it.r0,
-                               p.g, p.k.row0, p.k.table, {0, 0}};
+                               p.g, p.k.row0, {0, 0, 0}};
         }
         if (!SHARED && rank == 0 && lane == 0) t.note[me] = note;
         if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;

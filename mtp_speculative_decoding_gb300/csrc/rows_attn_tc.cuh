@@ -61,8 +61,8 @@ struct __align__(16) WorkerRec {
 struct __align__(16) RowNote {
     int last;                         // worker with its last tile (-1: there is no such item)
     int rows, r0, g;                  // rows [r0, r0 + rows) of the block, KV head
-    int row0, b;                      // the sequence's first token in out, the sequence
-    int pad_[2];
+    int row0;                         // the sequence's first token in out
+    int pad_[3];
 };
 // a part of a row's result with shared prefixes: in `dense`, or in slots of workers
 struct __align__(16) RowPart {
@@ -87,7 +87,7 @@ struct RowsTcArgs {
     int workers;                      // of the launch
     long long window_units;           // most units of a row tile under a window
     PlanHead* head;
-    BlockRec* blocks;                 // [n_groups + B]
+    BlockRec* blocks;                 // [2 n_groups + B]
     WorkerRec* worker;                // [workers]
     int* items;                       // tiles of the groups' own items before each of them
     int *cum, *cumt, *lens;           // shared prefixes: tokens and own tiles before a sequence [B + 1], its cached positions [B]
