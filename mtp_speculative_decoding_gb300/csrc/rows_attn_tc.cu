@@ -591,6 +591,11 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
             }
             __syncwarp();
             ok = wait_all(q_full, seg & 1);
+            if (!ok) {   // gave up: the copy in flight ends before the CTA does
+                const unsigned long long t0 = global_ns();
+                while (!try_wait<CG>(q_full, seg & 1) && global_ns() - t0 < t.timeout_ns) {}
+                __syncwarp();
+            }
             if (CG == 2 && rank == 1 && ok && lane == 0) arrive_lead<CG>(q_peer);
             __syncwarp();
             ++seg;
