@@ -293,6 +293,9 @@ __device__ __forceinline__ void open_codes(const unsigned char* src, unsigned ch
     }
 }
 
+// What a tile of a piece may take at most, some fifty times what it does
+constexpr unsigned long long kTileLimitNs = 100000;
+
 template <bool E4M3, int HD, bool SHARED>
 struct RowShape {
     static constexpr int CG = rows_pair(HD), NQ = 2 / CG;          // CTAs of a worker, row tiles of a CTA
@@ -427,18 +430,19 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
         __syncthreads();
     }
     // bounded wait; after one gave up every other does too
-    auto wait = [&](unsigned long long* bar, unsigned int parity) -> bool {
+    auto wait_for = [&](unsigned long long* bar, unsigned int parity, unsigned long long limit) -> bool {
         if (try_wait<CG>(bar, parity)) return true;
         const unsigned long long t0 = global_ns();
         while (!try_wait<CG>(bar, parity)) {
             if (s_abort) return false;
-            if (global_ns() - t0 > t.timeout_ns) {
+            if (global_ns() - t0 > limit) {
                 s_abort = 1;
                 return false;
             }
         }
         return true;
     };
+    auto wait = [&](unsigned long long* bar, unsigned int parity) { return wait_for(bar, parity, t.timeout_ns); };
     auto wait_all = [&](unsigned long long* bar, unsigned int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     const int ps = 1 << a.c.ps_log2;
     constexpr uint32_t idS = idesc(E4M3 ? 0 : 1, false, 128 * CG, kPosTile), idO = idesc(E4M3 ? 0 : 1, true, 128 * CG, HD);
@@ -576,11 +580,15 @@ __global__ void __launch_bounds__(RowShape<E4M3, HD, SHARED>::THREADS, 1) rows_t
         // ------------------------------------------------------------------
         unsigned seg = 0;
         bool ok = true;
+        unsigned long long limit = t.timeout_ns;
         Walk<SHARED> p;
         p.start(first, sq);
         while (ok && p.next(t)) {
-            ok = wait_all(q_free, (seg & 1) ^ 1);
+            // as long as the piece before takes, the one wait here that is not for a tile's work
+            // (a piece of 10^6 tiles takes longer than any other wait may)
+            ok = __all_sync(0xffffffffu, wait_for(q_free, (seg & 1) ^ 1, limit)) != 0;
             if (!ok) break;
+            limit = t.timeout_ns + (unsigned long long)p.n * kTileLimitNs;
             const int tiles = CG == 1 && p.it.rows <= 128 ? 1 : NQ;
             const long long row = p.k.q_row + (long long)p.g * p.k.q_stride + p.it.r0 + rank * 128;
             if (lane == 0) mbar_arrive_expect_tx(q_full, (unsigned)(tiles * S::QB));
