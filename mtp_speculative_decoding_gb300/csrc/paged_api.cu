@@ -184,7 +184,7 @@ RowsSpace rows_space(const mtp_kv_cache* c, int B, int M, int64_t T, int n_q_hea
         p.worker = take((size_t)p.workers * sizeof(WorkerRec));
         p.blocks = take((M > 0 ? 3 : 1) * (size_t)B * sizeof(BlockRec));
         if (M > 0) {
-            p.items = take(((size_t)B * M * (n_q_heads / c->n_kv_heads) / kRowTile + B + 2) * sizeof(int));
+            p.items = take(((size_t)B * M * (n_q_heads / c->n_kv_heads) / kRowTile + B + 2) * sizeof(long long));
             p.cum = take(((size_t)B + 1) * sizeof(int));
             p.cumt = take(((size_t)B + 1) * sizeof(int));
             p.lens = take((size_t)B * sizeof(int));
@@ -255,7 +255,7 @@ int launch_rows(const mtp_kv_cache* c, const RowsArgs& a, int dtype, int64_t T, 
     t.head = reinterpret_cast<PlanHead*>(base + p.head);
     t.worker = reinterpret_cast<WorkerRec*>(base + p.worker);
     t.blocks = reinterpret_cast<BlockRec*>(base + p.blocks);
-    t.items = reinterpret_cast<int*>(base + p.items);
+    t.items = reinterpret_cast<long long*>(base + p.items);
     t.cum = reinterpret_cast<int*>(base + p.cum);
     t.cumt = reinterpret_cast<int*>(base + p.cumt);
     t.lens = reinterpret_cast<int*>(base + p.lens);

@@ -89,7 +89,8 @@ struct RowsTcArgs {
     PlanHead* head;
     BlockRec* blocks;                 // [2 n_groups + B]
     WorkerRec* worker;                // [workers]
-    int* items;                       // tiles of the groups' own items before each of them
+    long long* items;                 // tiles of the groups' own items before each of them (a sequence's tiles count once an
+                                      // item that its rows reach into: more than 31 bits)
     int *cum, *cumt, *lens;           // shared prefixes: tokens and own tiles before a sequence [B + 1], its cached positions [B]
     uint16_t* staged;                 // [rows][hd]
     float* q_scale;                   // e4m3: [rows] a staged row's power of two times the softmax scale
@@ -125,7 +126,7 @@ __device__ __forceinline__ long long item_units(const RowsTcArgs& t, const Block
 // units of the row tiles before i (without what opening them costs)
 __device__ __forceinline__ long long tile_units(const RowsTcArgs& t, const BlockRec& k, long long i) {
     if (k.kind == kPrefix) return i * item_units(t, k, 0);
-    if (k.kind == kOwn) return (long long)(t.items[k.row0 + i] - t.items[k.row0]) * (kPosTile * t.a.G);
+    if (k.kind == kOwn) return (t.items[k.row0 + i] - t.items[k.row0]) * (kPosTile * t.a.G);
     const long long C = grow_units(t, k);
     long long grow = i;               // row tiles that the window does not bound
     if (t.a.c.window > 0) {

@@ -177,14 +177,14 @@ __device__ void count_items(const RowsTcArgs& t, const Groups& gr, const Sequenc
         const int i = last_at_most(rt0, a.n_groups, x);
         sum += t.items[x] = item_of<true>(a, sq, block_at(a, gr, sq.cum, a.n_groups + i, good), x - rt0[i]).n;
     }
-    at = (int)scan(sum, tmp, all);
+    long long before = scan(sum, tmp, all);
 #pragma unroll 1
     for (int x = x0; x < x1; ++x) {
-        const int n = t.items[x];
-        t.items[x] = at;
-        at += n;
+        const long long n = t.items[x];
+        t.items[x] = before;
+        before += n;
     }
-    if (tid == 0) t.items[items] = (int)all;
+    if (tid == 0) t.items[items] = all;
     __syncthreads();
 }
 
