@@ -556,8 +556,8 @@ size_t mtp_prefix_workspace_size(const mtp_kv_cache *c, int B, int M, int n_q_he
  *   q          rows in dtype (F32 or BF16): row (t, head h) at t*q_stride_m +
  *              h*q_stride_h (elements; 16-byte multiples, 16-byte aligned)
  *   out [T, n_q_heads, head_dim] in dtype; it overlaps no input
- * fp32 queries are computed in fp32 throughout, with any cache, and so are head_dim
- * 32 and 512.  bf16 queries against a bf16 or e4m3 cache with head_dim 64, 128 or
+ * fp32 queries or caches and head_dim 32 and 512 are computed in fp32 throughout,
+ * a row at a time (slower by two orders of magnitude).  bf16 queries against a bf16 or e4m3 cache with head_dim 64, 128 or
  * 256 run on the tensor cores: against bf16, rotated queries and probabilities are
  * then rounded to bf16 (8 bits, half of what mtp_paged_attention keeps); against
  * e4m3 both to fp16: a query's elements to 11 bits down to 2^-21 of their row's
