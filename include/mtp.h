@@ -588,8 +588,7 @@ int mtp_prompt_attention(const mtp_kv_cache *c, int B, int64_t T, int n_q_heads,
  * rows attend few positions of a long prefix, and mtp_paged_attention reads only
  * those).  Types and roundings as for mtp_prompt_attention.
  * A sequence whose kv_len, n_new, prefix_len or group is out of range is left out
- * (group_start that does not ascend: any of them may be),
- * positions on absent pages are masked, and both set the status word to
+ * (all of them are where group_start does not ascend), positions on absent pages are masked, and both set the status word to
  * MTP_ERR_ARG.  1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= M <= MTP_MAX_ATTN_ROWS,
  * 0 <= n_groups <= B, at most 16 query heads per KV head, B * (max_pages *
  * page_size / 128 + 2) < 2^31. */

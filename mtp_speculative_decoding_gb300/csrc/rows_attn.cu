@@ -169,8 +169,11 @@ __global__ void __launch_bounds__(kRowThreads) rows_cc_kernel(const __grid_const
     if (b < a.B && seq_at(a, b, s)) {
         const int j = (int)(tok - s.row0);
         bool mine = j >= 0 && j < s.n;
-        if (mine && a.M == 0) {   // (32 bounds at a time: little beside the positions that a row walks)
-            for (int i = lane; i <= a.B; i += 32) mine = mine && bound_agrees(a.row_start, b, i);
+        if (mine && (a.M == 0 || a.n_groups > 0)) {   // (32 bounds at a time: little beside the positions that a row walks)
+            if (a.M == 0)
+                for (int i = lane; i <= a.B; i += 32) mine = mine && bound_agrees(a.row_start, b, i);
+            else   // groups that do not ascend: all are left out
+                for (int i = lane; i < a.n_groups; i += 32) mine = mine && a.group_start[i] <= a.group_start[i + 1];
             mine = __all_sync(0xffffffffu, mine);
         }
         if (mine) bad = !attend_row<QT, KT>(a, s, b, j, h, lane) || bad;

@@ -138,3 +138,26 @@ def test_bounds_that_do_not_ascend(kv, qt, hd):
                     ref[b, r0, r1] = rc.attend(pool, b, q[r0:r1], None, 60, 1e4)
                 rc.check(out[r0:r1], *ref[b, r0, r1], 60 + r1 - r0, kv)
         assert (out[~used] == 7.0).all(), at
+
+
+@pytest.mark.parametrize("kv,qt,hd", [("bf16", "bf16", 64), ("bf16", "bf16", 256), ("e4m3", "bf16", 128), ("f32", "f32", 64), ("bf16", "bf16", 512),
+                                      ("e4m3", "bf16", 32)])
+def test_groups_that_do_not_ascend(kv, qt, hd):
+    """All sequences are left out, with every type."""
+    m = mtp()
+    B, M, hq = 6, 2, 4
+    pool = pc.Pool(B, 8, 16, 2, hd, kv, seed=11)
+    pool.fill([100] * B, seed=12)
+    q = rand((B, M, hq, hd), torch.bfloat16 if qt == "bf16" else torch.float32, 13)
+    h = pool.handle(rope_theta=1e4)
+    ws = m.alloc_workspace(m.prefix_workspace_size(h, B, M, hq))
+    for start, pre in (([0, 3, 2, 6], [20, 20, 20]), ([6, 0], [20]), ([0, 6, 0, 6], [20, 40, 30]), ([0, 2, 4, 3], [20, 20, 20]), ([3, 2], [0])):
+        ws.fill_(0xFF)
+        out = torch.full_like(q, 7.0)
+        m.prefix_attention(h, q, i32([80] * B), i32(start), i32(pre), out, ws)
+        assert m.last_error(ws) == m.MTP_ERR_ARG and (out == 7.0).all(), start
+    for start, pre, n in (([2, 2, 5], [30, 20], 6), ([-1, 2, 6], [20, 20], 4)):     # bounds that ascend: [-1, 2) alone is out
+        out = torch.full_like(q, 7.0)
+        m.prefix_attention(h, q, i32([80] * B), i32(start), i32(pre), out, ws)
+        assert m.last_error(ws) == (m.MTP_OK if n == 6 else m.MTP_ERR_ARG)
+        assert (out[: B - n] == 7.0).all() and not (out[B - n:] == 7.0).any(), start
