@@ -27,7 +27,7 @@
  *   mtp_prompt_attention  the rows of whole prompts, packed one after another,
  *                      attend that cache.
  *   mtp_prefix_attention  the new rows of sequences that share long prefixes
- *                      attend that cache, a group's prefix once for all.
+ *                      attend that cache, a group's prefix once for its rows.
  *
  * Definitions are those of the pages this library implements:
  *   [G4] "Gemma 4 MTP -- Multi-Token Prediction speculative decoding":
@@ -515,7 +515,9 @@ int mtp_paged_attention(const mtp_kv_cache *c, int B, int M, int n_q_heads, cons
  *       another); otherwise axis(i) = i mod n_axes while i < n_axes *
  *       sections[i mod n_axes], else 0
  * rounded once to dtype.  The rows then go to a cache with rope_theta 0
- * (mtp_kv_append without k_norm) and attend it without q_norm.
+ * (mtp_kv_append without k_norm) and attend it without q_norm.  The drafters
+ * (mtp_draft_block, mtp_nextn_draft) rotate by the slot: behind an image, where a
+ * target's next position is not its next slot, they do not follow these positions.
  *   positions  int32 [n_axes, rows], any sign
  *   sections   HOST pointer, [n_axes] >= 0; P a multiple of 8, 2 P <= head_dim
  *   q, k       rows in dtype (F32 or BF16): row (t, head h) at t*stride_m +
@@ -577,8 +579,15 @@ int mtp_prompt_attention(const mtp_kv_cache *c, int B, int64_t T, int n_q_heads,
  * mtp_paged_attention, but the sequences [group_start[i], group_start[i + 1]) have
  * their positions [0, prefix_len[i]) in common, on the pages of sequence
  * group_start[i]'s row of page_table (the other sequences' entries for whole pages
- * of it are not read).  A group's prefix is read and computed once for all of its
- * rows, and every sequence's own positions [prefix_len[i], kv_len + j] for itself.
+ * of it are not read).  On the tensor cores a group's prefix is read and computed
+ * once for 256 of its rows of a KV head, and every sequence's own positions
+ * [prefix_len[i], kv_len + j] for itself; fp32 queries or caches and head_dim 32
+ * and 512 read the prefix for every row.
+ * It pays where many sequences read a long prefix: measured from 8 sequences on
+ * behind 32768 positions, 16 behind 8192, 32 to 128 behind 2048, none behind 512.
+ * Where it does not, mtp_paged_attention with the prefix's pages in every row of
+ * page_table takes down to half the time, and it keeps more bits of queries and
+ * probabilities over a bf16 cache.
  *   kv_len [B] int32 >= prefix_len of its group: the prefix counts;  n_new [B] or
  *              NULL, q, q_norm, attn_scale, out: as for mtp_paged_attention
  *   group_start [n_groups + 1] int32, ascending, within [0, B]; sequences of no
@@ -588,10 +597,11 @@ int mtp_prompt_attention(const mtp_kv_cache *c, int B, int64_t T, int n_q_heads,
  * rows attend few positions of a long prefix, and mtp_paged_attention reads only
  * those).  Types and roundings as for mtp_prompt_attention.
  * A sequence whose kv_len, n_new, prefix_len or group is out of range is left out
- * (all of them are where group_start does not ascend), positions on absent pages are masked, and both set the status word to
- * MTP_ERR_ARG.  1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= M <= MTP_MAX_ATTN_ROWS,
- * 0 <= n_groups <= B, at most 16 query heads per KV head, B * (max_pages *
- * page_size / 128 + 2) < 2^31. */
+ * (all of them are where group_start does not ascend), positions on absent pages
+ * are masked, and both set the status word to MTP_ERR_ARG.
+ * 1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= M <= MTP_MAX_ATTN_ROWS, 0 <= n_groups <= B,
+ * at most 16 query heads per KV head, B * (max_pages * page_size / 128 + 2) <
+ * 2^31. */
 int mtp_prefix_attention(const mtp_kv_cache *c, int B, int M, int n_q_heads, const int32_t *kv_len, const int32_t *n_new,
                          int n_groups, const int32_t *group_start, const int32_t *prefix_len,
                          const void *q, int dtype, int64_t q_stride_b, int64_t q_stride_m, int64_t q_stride_h,

@@ -4,10 +4,13 @@
 // its axis times theta^(-i / pairs).  A thread takes one unit (8 pairs, or 16
 // elements behind the rotated ones) of `hpt` heads of one row, so that the
 // angles of a row are computed once for those heads.  Long calls are bound by
-// the bytes in and out (8192 rows of 24 heads of 128, bf16: 18.6 us, 5.4 TB/s),
-// in fp32 with a norm also by their instructions at 16 warps an SM (4093 rows of
-// 20 heads of 256: 37.1 us, 4.5 TB/s), short ones by the launch and two dependent
-// loads (4 rows: 9.3 us captured).
+// the bytes in and out (8192 rows of 24 heads of 128, bf16: 18.6 us one call behind
+// another, 5.4 TB/s, and 22.5 us, 4.5 TB/s, in turn with other work; captured, with
+// nothing in L2, 25.7), in fp32 with a norm also by what 16 warps an SM have in flight
+// (4093 rows of 20 heads of 256: 37.1 us, 4.5 TB/s), short ones by the launch and two
+// dependent loads (4 rows: 9.3 us captured).  Four heads are in flight whatever a
+// thread's number of heads is: with one or two (calls of up to some 1600 rows) the others
+// load and turn the same head again.
 #include "rows.cuh"
 
 namespace mtp {
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_axes_kernel(const __grid_c
 cudaError_t launch_rotate_axes(RotateArgs a, int dtype, int sms, cudaStream_t s) {
     // as many heads in one thread as leave 512 threads an SM: an angle costs as much as
     // the rest of four elements (128 to 1024 threads measure alike; with 2048 8192 rows of
-    // bf16 take 20.7 us instead of 18.6), and no more than divide both counts, where that
+    // bf16 take 20.7 us instead of 18.6, one call behind another), and no more than divide both counts, where that
     // leaves four: a group's missing heads cost as much as others
     a.hpt = 1;
     while (a.hpt < 16 && (a.hpt < 4 || (a.heads[0] | a.heads[1]) % (2 * a.hpt) == 0) &&

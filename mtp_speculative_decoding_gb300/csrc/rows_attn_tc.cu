@@ -25,18 +25,26 @@
 // at 256 dimensions e4m3 430 to 448); over e4m3 ones, with fewer registers, a look over
 // the scores first, so that no probability waits for the last one (515 to 496 us).
 //
-// Roundings.  bf16 caches: a rotated query and a probability once to bf16 (2^-8 each);
-// two parts of either, as the attention of a verify step has them, would double one
-// of the two products, and those are the bound here, not the cache's bytes.  e4m3
-// caches: both to fp16 (2^-11), which the codes need anyway.
+// Roundings.  bf16 caches: a rotated query and a probability once to bf16 (2^-8 each),
+// half the bits that the attention of a verify step keeps in two parts of each.  A second
+// part doubles one of the two products: 361 to 448 (probabilities) or 456 us (queries) for
+// 8192 tokens at head dimension 256, where the products are the bound.  Elsewhere they
+// are not (13 packed prompts of 128: 170 to 183 or 219 us, 64 sequences behind a prefix: 57
+// to 60 for either, each without the softmax's share of it), and the one form is kept for
+// its simplicity; against 64 bits results are off by 0.0022 to 0.0029 of their rms, of which
+// their own rounding is 0.0016.  e4m3 caches: both to fp16 (2^-11), which the codes need
+// anyway; the probabilities with their page's value scale, so that they keep their bits
+// down to 2^-25 of the row's largest such product.
 //
-// Measured, the whole call: 8192 tokens, 16 heads of 256 over 4 KV heads, bf16: 353 us,
-// 1550 TFLOP/s (the matrix units at what clock the power limit leaves them).  The same
-// with 128 dimensions over 8 KV heads: 271 us, 1010 TFLOP/s, bound by the softmax's
-// instructions between two row tiles.  e4m3, two pieces of 1024 tokens behind 15000:
-// 416 us, 1250 TFLOP/s, bound by opening the codes (4 warps) and the softmax together.
-// 64 sequences of up to 3 rows behind 8192 common positions: 55 us, of which this
-// kernel 42: half of its tiles are the sequences' own, where few of 256 rows count.
+// Measured, the whole call, one behind another: 8192 tokens, 16 heads of 256 over 4 KV
+// heads, bf16: 361 us, 1520 TFLOP/s (in turn with other work 379; the matrix units at what
+// clock the power limit leaves them).  The same with 128 dimensions over 8 KV heads: 277
+// us, 990 TFLOP/s: matrix units 47 % and issue slots 32 % busy, the two row tiles' chain of
+// product, softmax and hand-over bounds it.  e4m3, two pieces of 1024 tokens behind 15000:
+// 391 us, 1340 TFLOP/s, bound by opening the codes (4 warps) and the softmax, neither at
+// its rate.  64 sequences of up to 3 rows behind 8192 common positions: 54 to 57 us, of
+// which this kernel 42: half of its tiles are the sequences' own, where few of 256 rows
+// count.
 //
 // A result that is not finite is computed again, position by position, by the
 // kernel behind this one (rows_attn.cu): the products here multiply masked
