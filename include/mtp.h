@@ -557,15 +557,16 @@ size_t mtp_prefix_workspace_size(const mtp_kv_cache *c, int B, int M, int n_q_he
  *              at least row_start[b + 1]: rows that two would claim are no one's
  *   q          rows in dtype (F32 or BF16): row (t, head h) at t*q_stride_m +
  *              h*q_stride_h (elements; 16-byte multiples, 16-byte aligned)
- *   out [T, n_q_heads, head_dim] in dtype; it overlaps no input
+ *   out [T, n_q_heads, head_dim] in dtype, 16-byte aligned; it overlaps no input
  * fp32 queries or caches and head_dim 32 and 512 are computed in fp32 throughout,
- * a row at a time (slower by two orders of magnitude).  bf16 queries against a bf16 or e4m3 cache with head_dim 64, 128 or
- * 256 run on the tensor cores: against bf16, rotated queries and probabilities are
- * then rounded to bf16 (8 bits, half of what mtp_paged_attention keeps); against
- * e4m3 both to fp16: a query's elements to 11 bits down to 2^-21 of their row's
- * largest (below, to 2^-32 of it), and of the probabilities each times its page's
- * value scale, to 11 bits down to 2^-25 of the row's largest such product (below,
- * to 2^-36 of it).  Maxima, sums and accumulators are fp32.
+ * a row at a time (slower by two orders of magnitude).  bf16 queries against a bf16
+ * or e4m3 cache with head_dim 64, 128 or 256 run on the tensor cores: against bf16,
+ * rotated queries and probabilities are then rounded to bf16 (8 bits, half of what
+ * mtp_paged_attention keeps); against e4m3 both to fp16: a query's elements to 11
+ * bits down to 2^-21 of their row's largest (below, to 2^-32 of it), and of the
+ * probabilities each times its page's value scale, to 11 bits down to 2^-25 of the
+ * row's largest such product (below, to 2^-36 of it).  Maxima, sums and accumulators
+ * are fp32.
  * A sequence whose kv_len or rows are out of range is left out, positions on
  * absent pages are masked, and both set the status word to MTP_ERR_ARG.
  * 1 <= B <= MTP_MAX_PAGED_BATCH, 1 <= T <= MTP_MAX_PROMPT_ROWS, T * n_q_heads <
