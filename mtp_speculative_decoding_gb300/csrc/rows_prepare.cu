@@ -121,8 +121,8 @@ __device__ __forceinline__ BlockRec block_at(const RowsArgs& a, const Groups& gr
     if (blk < 2 * a.n_groups) {
         const bool own = blk >= a.n_groups;
         const int i = own ? blk - a.n_groups : blk, g0 = gr.start[i], g1 = gr.start[i + 1], P = gr.len[i];
+        // (a group that is out of range is reported by the sequences in it: one without any concerns no one)
         const bool ok = g0 >= 0 && g0 <= g1 && g1 <= a.B && P >= 0 && P <= (long long)a.c.max_pages << a.c.ps_log2;
-        good = good && ok;
         k.kind = own ? kOwn : kPrefix;
         if (ok) {
             k.n = own || P > 0 ? cum[g1] - cum[g0] : 0;

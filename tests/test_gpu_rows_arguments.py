@@ -161,3 +161,22 @@ def test_groups_that_do_not_ascend(kv, qt, hd):
         m.prefix_attention(h, q, i32([80] * B), i32(start), i32(pre), out, ws)
         assert m.last_error(ws) == (m.MTP_OK if n == 6 else m.MTP_ERR_ARG)
         assert (out[: B - n] == 7.0).all() and not (out[B - n:] == 7.0).any(), start
+
+
+@pytest.mark.parametrize("kv,qt,hd", [("bf16", "bf16", 64), ("bf16", "bf16", 256), ("e4m3", "bf16", 128), ("f32", "f32", 64), ("bf16", "bf16", 512)])
+def test_groups_without_a_sequence(kv, qt, hd):
+    """Whatever their prefix is, they concern no one: the same status with every type."""
+    m = mtp()
+    B, M, hq = 3, 2, 4
+    pool = pc.Pool(B, 4, 16, 2, hd, kv, seed=14)
+    pool.fill([42] * B, seed=15)
+    q = rand((B, M, hq, hd), torch.bfloat16 if qt == "bf16" else torch.float32, 16)
+    h = pool.handle(rope_theta=1e4)
+    ws = m.alloc_workspace(m.prefix_workspace_size(h, B, M, hq))
+    for start, pre, shared in (([0, 0], [1000], 0), ([0, 0, 3], [-4, 20], 1), ([0, 3, 3], [20, 2 ** 31 - 1], 1), ([3, 3, 3], [65, -1], 0),
+                               ([-5, -2], [20], 0), ([4, 9], [20], 0)):
+        out = torch.full_like(q, 7.0)
+        m.prefix_attention(h, q, i32([40] * B), i32(start), i32(pre), out, ws)
+        assert m.last_error(ws) == m.MTP_OK, start
+        for b in range(B):
+            rc.check(out[b], *rc.attend(pool, b, q[b], None, 40, 1e4, prefix=20 if shared else 0, first=0), 42, kv)
